@@ -119,11 +119,11 @@ def _tokens(case):
     return sum(t * h * w for t, h, w in _grids(case)) if case.get("grid") else case["tokens"]
 
 
-def _sections(dim):
-    """Pairs turned by time, height and width: about 1/5, 2/5, 2/5 of dim / 2."""
+def _sections(dim, cycled):
+    """Pairs turned by time, height and width: about 1/5, 2/5, 2/5 of dim / 2, or nearly equal shares when they cycle."""
     r = dim // 2
-    t = r - 2 * (2 * r // 5)
-    return t, 2 * r // 5, 2 * r // 5
+    h = 3 * r // 10 if cycled else 2 * r // 5
+    return r - 2 * h, h, h
 
 
 def _axes(sections, cycled):
@@ -149,7 +149,7 @@ def prepare(case, seed):
         s["q"] = normal(T, case["q_heads"], D, scale=2.0)
         s["k"] = normal(T, case["k_heads"], D, scale=2.0)
         s["norm_w"] = normal(2, D, scale=0.2, shift=1.0) if case["norm"] else None
-        s["sections"] = _sections(D)
+        s["sections"] = _sections(D, case["cycled"])
         s["axes"] = torch.tensor(_axes(s["sections"], case["cycled"]), device="cuda")
         j = torch.arange(D // 2, dtype=torch.float64, device="cuda")
         s["inv_freq"] = (THETA ** (-2.0 * j / D)).float()
@@ -429,7 +429,7 @@ def _exact_rotation(case, s):
         pos = torch.tensor(pos, device="cuda")
     else:
         pos = s["pos"].long()
-    t, h, w = _sections(case["dim"])
+    t, h, w = _sections(case["dim"], case["cycled"])
     axis = []
     for m in range(t + h + w):
         if case["cycled"]:
