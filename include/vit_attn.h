@@ -410,6 +410,149 @@ vit_status_t vit_varlen_attn_ex(const void *q, const void *k, const void *v, int
                                 const vit_attn_options_t *opts, void *workspace, size_t workspace_bytes,
                                 int32_t *status_dev, vit_stream_t stream);
 
+/* ---- around a language model's reading of the encoder's states ---------------------------
+ *
+ * The block in which text tokens (or a set of latent queries) read what the vision encoder
+ * wrote, for images and video: rotary positions with three axes on q and k, cross attention
+ * between packed sequences of different lengths, and the gated residual step with the norms on
+ * either side of it; each with its gradient. Conventions as above; in addition:
+ *   - q has Hq heads and k, v have Hk (or Hkv); strides are per tensor.
+ *   - Gradients are written, never accumulated into; sums over tokens are added in a fixed order,
+ *     so every output is the same from run to run.
+ *   - An output may be its input (same pointer and stride) only where that is said.
+ */
+
+/*
+ * Positions of the patches of images and clips with three axes.
+ *
+ *   grid_thw    device int32 [n, 3]: (frames, rows, columns) of each clip in packing order
+ *               (an image has one frame); a clip may be empty.
+ *   n           0 <= n <= VIT_MAX_SEGMENTS.
+ *   T           total tokens; must equal sum(t*h*w) (VIT_ERR_GRID_MISMATCH on the device,
+ *               outputs then untouched).
+ *   pos_thw     device int32 [T, 3] output, or NULL: (frame, row, column) of each token inside its
+ *               clip, column fastest, restarting at 0 for every clip.
+ *   cu_seqlens  device int32 [n + 1] output, or NULL.
+ */
+vit_status_t vit_grid_positions(const int32_t *grid_thw, int n, int64_t T, int32_t *pos_thw, int32_t *cu_seqlens,
+                                int32_t *status_dev, vit_stream_t stream);
+
+/* Which axis a rotary pair follows (vit_qk_norm_mrope). */
+enum {
+    VIT_MROPE_BLOCKED = 0,   /* sections[0] pairs of time, then sections[1] of height, sections[2] of width */
+    VIT_MROPE_CYCLED = 1     /* pair m: height if m % 3 == 1 and m < 3*sections[1], width if m % 3 == 2 and
+                                m < 3*sections[2], else time */
+};
+
+/*
+ * Per-head RMS norm of q and k, then rotary positions with three axes.
+ *
+ *   xn = x * rsqrt(mean(x^2) + eps) * w        (or xn = x without norm_w)
+ *   a_m = pos_thw[t, axis(m)] * inv_freq[m]    for the pairs m < D/2
+ *   y = xn with every pair (m, m + D/2), or (2m, 2m + 1), turned by a_m
+ * in fp32, rounded to bf16 once (vit_qk_norm_rope also rounds the norm's two steps). The angle is
+ * formed and reduced in fp64, so it is as good at position 2^31 - 1 as at 0. Negative positions
+ * are allowed.
+ *
+ *   q_in, q_out   device bf16 [T, Hq, D]; q_out may be q_in (same stride). Both NULL: q is left out.
+ *   k_in, k_out   the same with Hk heads. At least one of q and k is given.
+ *   pos_thw       device int32 [T, 3].
+ *   inv_freq      device fp32 [D/2] (e.g. from vit_rope_freqs(dim = D), or tables of single axes
+ *                 side by side).
+ *   sections      host int [3]: pairs of time, height and width, >= 0, summing to D/2. For
+ *                 VIT_MROPE_CYCLED also 3*sections[1] <= D/2 + 1 and 3*sections[2] <= D/2, so that
+ *                 each axis gets exactly its pairs.
+ *   axis_layout   VIT_MROPE_BLOCKED or VIT_MROPE_CYCLED.
+ *   rope_mode     VIT_ROPE_ROTATE_HALF or VIT_ROPE_INTERLEAVED.
+ *   norm_w        device bf16 [2, D] (row 0 for q, row 1 for k), 16-byte aligned, or NULL.
+ *   eps           >= 0.
+ * D in {32, 64, 80, 96, 128}; 1 <= Hq, Hk <= 65536 for the halves given.
+ */
+vit_status_t vit_qk_norm_mrope(const void *q_in, void *q_out, const void *k_in, void *k_out, int64_t T, int Hq, int Hk,
+                               int D, int64_t q_in_stride, int64_t q_out_stride, int64_t k_in_stride,
+                               int64_t k_out_stride, const int32_t *pos_thw, const float *inv_freq,
+                               const int *sections, int axis_layout, int rope_mode, const void *norm_w, float eps,
+                               vit_stream_t stream);
+
+/* Workspace bytes of vit_qk_norm_mrope_bwd (0 for invalid sizes). */
+size_t vit_qk_norm_mrope_bwd_workspace_size(int D);
+
+/*
+ * Gradient of vit_qk_norm_mrope.
+ *
+ *   dq_out, dk_out   device bf16, gradients of its outputs.
+ *   dq_in, dk_in     device bf16 outputs, gradients of its inputs; may be dq_out / dk_out (same stride).
+ *   q_in, k_in       its inputs; read only with norm_w (else may be NULL).
+ *   dnorm_w          device fp32 [2, D] output: gradient of norm_w (the row of a half that is left
+ *                    out is 0), or NULL. Ignored without norm_w.
+ *   workspace        vit_qk_norm_mrope_bwd_workspace_size(D) bytes, 16-byte aligned; needed only
+ *                    with dnorm_w. Calls sharing one must not overlap.
+ * A half is left out when dq_out and dq_in (or dk_out and dk_in) are both NULL.
+ */
+vit_status_t vit_qk_norm_mrope_bwd(const void *dq_out, void *dq_in, const void *dk_out, void *dk_in, const void *q_in,
+                                   const void *k_in, int64_t T, int Hq, int Hk, int D, int64_t dq_out_stride,
+                                   int64_t dq_in_stride, int64_t dk_out_stride, int64_t dk_in_stride,
+                                   int64_t q_in_stride, int64_t k_in_stride, const int32_t *pos_thw,
+                                   const float *inv_freq, const int *sections, int axis_layout, int rope_mode,
+                                   const void *norm_w, float eps, float *dnorm_w, void *workspace,
+                                   size_t workspace_bytes, vit_stream_t stream);
+
+/* Storage of the residual stream (vit_norm_residual). */
+enum {
+    VIT_RES_BF16 = 0,
+    VIT_RES_FP32 = 1
+};
+
+/*
+ * Residual step with the norms before and after it: the block's output y is normed, gated, scaled
+ * and added to the residual x, and the sum is normed for the next block.
+ *
+ *   u = y * rsqrt(mean(y^2) + eps) * w_post    (or u = y without w_post)
+ *   h = x + scale * gate * u                   (without gate: 1)
+ *   z = h * rsqrt(mean(h^2) + eps) * w_pre     (only with w_pre; from h before it is rounded)
+ *
+ *   x, h_out     device [T, C] in res_type; h_out may be x (same stride).
+ *   y, z_out     device bf16 [T, C]; z_out may be y (same stride). z_out is NULL without w_pre.
+ *   gate         device bf16: [C] for all tokens (gate_stride 0), or [T, C] with gate_stride >= C;
+ *                NULL for none.
+ *   w_post, w_pre  device bf16 [C], or NULL.
+ *   C            a multiple of 8, 8 <= C <= 8192. Row strides in elements, multiples of 8, >= C.
+ *   scale        finite. eps >= 0.
+ */
+vit_status_t vit_norm_residual(const void *x, const void *y, const void *gate, const void *w_post, const void *w_pre,
+                               void *h_out, void *z_out, int64_t T, int C, int res_type, int64_t x_stride,
+                               int64_t y_stride, int64_t gate_stride, int64_t h_stride, int64_t z_stride, float scale,
+                               float eps, vit_stream_t stream);
+
+/* Workspace bytes of vit_norm_residual_bwd (0 for an invalid C). */
+size_t vit_norm_residual_bwd_workspace_size(int C);
+
+/*
+ * Gradient of vit_norm_residual.
+ *
+ *   dz           device bf16 [T, C], gradient of z_out: given exactly when w_pre is.
+ *   dh           device [T, C] in res_type, gradient of h_out (the residual stream's own), or NULL
+ *                for none. At least one of dz and dh is given.
+ *   h            device [T, C] in res_type: h_out as the forward call stored it; read with w_pre.
+ *   y            device bf16 [T, C]; read with w_post or gate (else may be NULL).
+ *   dx           device [T, C] in res_type output; may be dh (same stride).
+ *   dy           device bf16 [T, C] output; may be y or dz (same stride).
+ *   dgate        output, or NULL: fp32 [C] (16-byte aligned) for a gate of all tokens, bf16 [T, C]
+ *                with dgate_stride for a gate per token.
+ *   dw_post, dw_pre  device fp32 [C] outputs, or NULL; need w_post / w_pre.
+ *   workspace    vit_norm_residual_bwd_workspace_size(C) bytes, 16-byte aligned; needed when
+ *                dw_post, dw_pre or a [C] dgate is asked for. Calls sharing one must not overlap.
+ *   status_dev   device int32 [1] or NULL: rows move through shared memory with bulk copies whose
+ *                waits are bounded; one that expires stores VIT_ERR_TIMEOUT (outputs undefined).
+ */
+vit_status_t vit_norm_residual_bwd(const void *dz, const void *dh, const void *h, const void *y, const void *gate,
+                                   const void *w_post, const void *w_pre, void *dx, void *dy, void *dgate,
+                                   float *dw_post, float *dw_pre, int64_t T, int C, int res_type, int64_t dz_stride,
+                                   int64_t dh_stride, int64_t h_stride, int64_t y_stride, int64_t gate_stride,
+                                   int64_t dx_stride, int64_t dy_stride, int64_t dgate_stride, float scale, float eps,
+                                   void *workspace, size_t workspace_bytes, int32_t *status_dev,
+                                   vit_stream_t stream);
+
 /*
  * Synchronise `stream`, then read the status word. Returns VIT_OK, the first
  * device-detected error code stored there, or VIT_ERR_CUDA when the stream or

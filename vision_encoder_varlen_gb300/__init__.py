@@ -28,6 +28,23 @@ _lock = threading.Lock()
 _lib = None
 
 
+def _declare_block(L):
+    vp, i32, i64, f32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+    rope = [vp, vp, vp, i32, i32, vp, f32]      # pos, inv_freq, sections, axis layout, rope mode, norm_w, eps
+    for name, args in (
+            ("vit_grid_positions", [vp, i32, i64, vp, vp, vp, vp]),
+            ("vit_qk_norm_mrope", [vp] * 4 + [i64, i32, i32, i32] + [i64] * 4 + rope + [vp]),
+            ("vit_qk_norm_mrope_bwd", [vp] * 6 + [i64, i32, i32, i32] + [i64] * 6 + rope + [vp, vp, sz, vp]),
+            ("vit_norm_residual", [vp] * 7 + [i64, i32, i32] + [i64] * 5 + [f32, f32, vp]),
+            ("vit_norm_residual_bwd", [vp] * 12 + [i64, i32, i32] + [i64] * 8 + [f32, f32, vp, sz, vp, vp])):
+        fn = getattr(L, name)
+        fn.argtypes, fn.restype = args, i32
+    for name, args in (("vit_qk_norm_mrope_bwd_workspace_size", [i32]),
+                       ("vit_norm_residual_bwd_workspace_size", [i32])):
+        fn = getattr(L, name)
+        fn.argtypes, fn.restype = args, sz
+
+
 class VitError(RuntimeError):
     def __init__(self, code: int, what: str):
         self.code = code
@@ -83,6 +100,7 @@ def lib() -> ctypes.CDLL:
             L.vit_launch_count.restype = i64
             L.vit_kernel_timing.argtypes = [i32]
             L.vit_kernel_timing_read.argtypes = [ctypes.POINTER(_KernelTime), i32]
+            _declare_block(L)
             for fn in ("vit_device_supported", "vit_rope_freqs", "vit_qk_norm_rope", "vit_qk_norm_rope_ex",
                        "vit_varlen_attn", "vit_varlen_attn_lse", "vit_varlen_attn_fused_q", "vit_rope_table",
                        "vit_varlen_attn_padded", "vit_varlen_attn_ex",
@@ -135,8 +153,8 @@ def _ptr(t: torch.Tensor | None):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _tok_stride(t: torch.Tensor, name: str, H: int, D: int) -> int:
-    if t.dim() != 3 or t.shape[1] != H or t.shape[2] != D:
+def _tok_stride(t: torch.Tensor, name: str, H: int, D: int, T: int | None = None) -> int:
+    if t.dim() != 3 or t.shape[1] != H or t.shape[2] != D or (T is not None and t.shape[0] != T):
         raise ValueError(f"{name} must be [T, {H}, {D}], got {tuple(t.shape)}")
     if t.dtype != torch.bfloat16 or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA bfloat16 tensor")
@@ -395,6 +413,278 @@ def encoder_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: 
     q_w = norm_w.reshape(2, -1)[0] if norm_w is not None else None
     return varlen_attn_fused_q(q, kr, v, cu_seqlens, max_seqlen, pos_hw, cos_sin, q_w, eps,
                                interleaved=interleaved, **kw)
+
+
+# ---- around a language model's reading of the encoder's states: three-axis rotary positions, cross
+# ---- attention and the gated residual step with its norms, each with its gradient
+
+@contextlib.contextmanager
+def _on(stream, *tensors):
+    """Checks that the tensors given share one CUDA device, makes it current, and yields its stream handle:
+    the caller's, or the device's current one."""
+    given = [t for t in tensors if t is not None]
+    dev = given[0].device
+    for t in given:
+        if not t.is_cuda:
+            raise ValueError("every tensor must be a CUDA tensor")
+        if t.device != dev:
+            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    with torch.cuda.device(dev):
+        s = torch.cuda.current_stream(dev) if stream is None else stream
+        yield ctypes.c_void_p(s.cuda_stream)
+
+
+def _made(stream, *tensors):
+    """Tells the allocator that tensors allocated by a call are used on the stream the call was given."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _workspace(workspace, need: int, device, stream) -> torch.Tensor:
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        _made(stream, workspace)
+    return workspace
+
+
+def _heads(t: torch.Tensor, name: str, T: int, D: int) -> int:
+    """Head count of [T, H, D], its layout checked as the attention calls do."""
+    if t.dim() != 3 or t.shape[0] != T:
+        raise ValueError(f"{name} must be [{T}, H, {D}], got {tuple(t.shape)}")
+    return t.shape[1]
+
+
+def grid_positions(grid_thw: torch.Tensor, total_tokens: int, *, status: torch.Tensor | None = None, stream=None):
+    """Positions of packed images and clips: ([T, 3] int32 (frame, row, column), cu_seqlens [n + 1] int32) from
+    a device list of (frames, rows, columns)."""
+    if grid_thw.dtype != torch.int32 or not grid_thw.is_contiguous() or grid_thw.dim() != 2 or grid_thw.shape[1] != 3:
+        raise ValueError("grid_thw must be a contiguous CUDA int32 tensor [n, 3]")
+    with _on(stream, grid_thw, status) as s:
+        pos = torch.empty((int(total_tokens), 3), dtype=torch.int32, device=grid_thw.device)
+        cu = torch.empty(grid_thw.shape[0] + 1, dtype=torch.int32, device=grid_thw.device)
+        _made(stream, pos, cu)
+        _check(lib().vit_grid_positions(_ptr(grid_thw), grid_thw.shape[0], int(total_tokens), _ptr(pos), _ptr(cu),
+                                        _ptr(status), s), "vit_grid_positions")
+    return pos, cu
+
+
+def _mrope_args(ref, pos_thw, inv_freq, sections, norm_w, eps, cycled, interleaved):
+    T, _, D = ref.shape
+    if pos_thw.dtype != torch.int32 or tuple(pos_thw.shape) != (T, 3) or not pos_thw.is_contiguous():
+        raise ValueError(f"pos_thw must be a contiguous CUDA int32 tensor [{T}, 3]")
+    if inv_freq.dtype != torch.float32 or tuple(inv_freq.shape) != (D // 2,) or not inv_freq.is_contiguous():
+        raise ValueError(f"inv_freq must be a contiguous CUDA float32 tensor [{D // 2}]")
+    if norm_w is not None and (norm_w.dtype != torch.bfloat16 or tuple(norm_w.shape) != (2, D)
+                               or not norm_w.is_contiguous()):
+        raise ValueError(f"norm_w must be a contiguous CUDA bfloat16 tensor [2, {D}]")
+    if len(sections) != 3:
+        raise ValueError("sections must be three pair counts (time, height, width)")
+    sec = (ctypes.c_int * 3)(*(int(x) for x in sections))
+    return (_ptr(pos_thw), _ptr(inv_freq), sec, MROPE_CYCLED if cycled else MROPE_BLOCKED,
+            ROPE_INTERLEAVED if interleaved else ROPE_ROTATE_HALF, _ptr(norm_w), float(eps))
+
+
+MROPE_BLOCKED = 0   # the sections one after the other
+MROPE_CYCLED = 1    # time, height, width in turn
+
+
+def qk_norm_mrope(q: torch.Tensor | None, k: torch.Tensor | None, pos_thw: torch.Tensor, inv_freq: torch.Tensor,
+                  sections, norm_w: torch.Tensor | None = None, eps: float = 1e-6, *, cycled: bool = False,
+                  interleaved: bool = False, q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+                  inplace: bool = False, stream=None):
+    """QK-RMSNorm (if norm_w [2, D] is given) + rotary positions with three axes. q [T, Hq, D] and k [T, Hk, D]
+    may differ in heads; a half passed as None is skipped and returned as None. ``sections`` are the pairs that
+    follow time, height and width (their sum is D / 2), one after the other or, with ``cycled``, in turn."""
+    ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("at least one of q and k is required")
+    if ref.dim() != 3:
+        raise ValueError(f"q and k must be [T, H, D], got {tuple(ref.shape)}")
+    T, _, D = ref.shape
+    args = _mrope_args(ref, pos_thw, inv_freq, sections, norm_w, eps, cycled, interleaved)
+    if inplace:
+        q_out, k_out = q, k
+    made = []
+
+    def half(x, out, name):
+        if x is None:
+            return None, 0, 0, 0
+        H = _heads(x, name, T, D)
+        xs = _tok_stride(x, name, H, D)
+        if out is None:
+            out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
+            made.append(out)
+        return out, H, xs, _tok_stride(out, name + "_out", H, D, T)
+
+    with _on(stream, q, k, q_out, k_out, pos_thw, inv_freq, norm_w) as s:
+        q_out, Hq, qs, qos = half(q, q_out, "q")
+        k_out, Hk, ks, kos = half(k, k_out, "k")
+        _made(stream, *made)
+        _check(lib().vit_qk_norm_mrope(_ptr(q), _ptr(q_out), _ptr(k), _ptr(k_out), T, Hq, Hk, D, qs, qos, ks, kos,
+                                       *args, s), "vit_qk_norm_mrope")
+    return q_out, k_out
+
+
+def qk_norm_mrope_bwd(dq: torch.Tensor | None, dk: torch.Tensor | None, q: torch.Tensor | None,
+                      k: torch.Tensor | None, pos_thw: torch.Tensor, inv_freq: torch.Tensor, sections,
+                      norm_w: torch.Tensor | None = None, eps: float = 1e-6, *, cycled: bool = False,
+                      interleaved: bool = False, inplace: bool = False, workspace: torch.Tensor | None = None,
+                      stream=None):
+    """Gradient of qk_norm_mrope: from dq, dk (with respect to its outputs; either may be None) and its inputs
+    q, k (needed with norm_w only) returns (dq_in, dk_in, dnorm_w [2, D] fp32 or None). ``inplace`` writes
+    over dq and dk."""
+    ref = dq if dq is not None else dk
+    if ref is None:
+        raise ValueError("at least one of dq and dk is required")
+    if ref.dim() != 3:
+        raise ValueError(f"dq and dk must be [T, H, D], got {tuple(ref.shape)}")
+    T, _, D = ref.shape
+    args = _mrope_args(ref, pos_thw, inv_freq, sections, norm_w, eps, cycled, interleaved)
+    made = []
+
+    def half(d, x, name):
+        if d is None:
+            return None, 0, 0, 0, 0
+        H = _heads(d, "d" + name, T, D)
+        ds = _tok_stride(d, "d" + name, H, D)
+        xs = 0
+        if norm_w is not None:
+            if x is None:
+                raise ValueError(f"{name} is needed for the gradient of its norm")
+            xs = _tok_stride(x, name, H, D, T)
+        if inplace:
+            return d, H, ds, ds, xs
+        out = torch.empty((T, H, D), dtype=d.dtype, device=d.device)
+        made.append(out)
+        return out, H, ds, H * D, xs
+
+    with _on(stream, dq, dk, q, k, pos_thw, inv_freq, norm_w, workspace) as s:
+        dq_in, Hq, dqs, dqis, qs = half(dq, q, "q")
+        dk_in, Hk, dks, dkis, ks = half(dk, k, "k")
+        dw = None
+        if norm_w is not None:
+            dw = torch.empty((2, D), dtype=torch.float32, device=ref.device)
+            made.append(dw)
+            workspace = _workspace(workspace, int(lib().vit_qk_norm_mrope_bwd_workspace_size(D)), ref.device, stream)
+        _made(stream, *made)
+        _check(lib().vit_qk_norm_mrope_bwd(_ptr(dq), _ptr(dq_in), _ptr(dk), _ptr(dk_in), _ptr(q), _ptr(k), T, Hq, Hk,
+                                           D, dqs, dqis, dks, dkis, qs, ks, *args, _ptr(dw), _ptr(workspace),
+                                           _bytes(workspace), s), "vit_qk_norm_mrope_bwd")
+    return dq_in, dk_in, dw
+
+
+def _bytes(t: torch.Tensor | None) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+RES_BF16, RES_FP32 = 0, 1
+
+
+def _rows(t: torch.Tensor, name: str, T: int, C: int, dtype) -> int:
+    if t.dim() != 2 or tuple(t.shape) != (T, C):
+        raise ValueError(f"{name} must be [{T}, {C}], got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.stride(1) != 1:
+        raise ValueError(f"{name} needs unit element stride (got strides {t.stride()})")
+    return t.stride(0) if T > 1 else C
+
+
+def _channel(t: torch.Tensor | None, name: str, C: int):
+    if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != (C,) or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous CUDA bfloat16 tensor [{C}]")
+
+
+def _residual(x: torch.Tensor):
+    if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("the residual must be a CUDA bfloat16 or float32 tensor [T, C]")
+    return x.shape[0], x.shape[1], RES_FP32 if x.dtype == torch.float32 else RES_BF16
+
+
+def _gate_stride(gate, T, C) -> int:
+    if gate is None:
+        return 0
+    if gate.dim() == 1:
+        _channel(gate, "gate", C)
+        return 0
+    return _rows(gate, "gate", T, C, torch.bfloat16)
+
+
+def norm_residual(x: torch.Tensor, y: torch.Tensor, *, gate: torch.Tensor | None = None,
+                  w_post: torch.Tensor | None = None, w_pre: torch.Tensor | None = None, scale: float = 1.0,
+                  eps: float = 1e-6, h_out: torch.Tensor | None = None, z_out: torch.Tensor | None = None,
+                  stream=None):
+    """h = x + scale * gate * RMSNorm(y; w_post); z = RMSNorm(h; w_pre). Returns (h, z), z None without w_pre.
+
+    x [T, C] bf16 or fp32 (h has its type and may be x itself), y [T, C] bf16 (z may be y itself), gate [C] or
+    [T, C] bf16, the weights [C] bf16. Without w_post y is taken as it is."""
+    T, C, res = _residual(x)
+    xs, ys = _rows(x, "x", T, C, x.dtype), _rows(y, "y", T, C, torch.bfloat16)
+    gs = _gate_stride(gate, T, C)
+    _channel(w_post, "w_post", C)
+    _channel(w_pre, "w_pre", C)
+    if w_pre is None and z_out is not None:
+        raise ValueError("z_out needs w_pre")
+    with _on(stream, x, y, gate, w_post, w_pre, h_out, z_out) as s:
+        made = []
+        if h_out is None:
+            h_out = torch.empty((T, C), dtype=x.dtype, device=x.device)
+            made.append(h_out)
+        if w_pre is not None and z_out is None:
+            z_out = torch.empty((T, C), dtype=torch.bfloat16, device=x.device)
+            made.append(z_out)
+        _made(stream, *made)
+        zs = _rows(z_out, "z_out", T, C, torch.bfloat16) if z_out is not None else 0
+        _check(lib().vit_norm_residual(_ptr(x), _ptr(y), _ptr(gate), _ptr(w_post), _ptr(w_pre), _ptr(h_out),
+                                       _ptr(z_out), T, C, res, xs, ys, gs, _rows(h_out, "h_out", T, C, x.dtype), zs,
+                                       float(scale), float(eps), s), "vit_norm_residual")
+    return h_out, z_out
+
+
+def norm_residual_bwd(dz: torch.Tensor | None, dh: torch.Tensor | None, h: torch.Tensor | None, y: torch.Tensor, *,
+                      gate: torch.Tensor | None = None, w_post: torch.Tensor | None = None,
+                      w_pre: torch.Tensor | None = None, scale: float = 1.0, eps: float = 1e-6,
+                      workspace: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
+    """Gradient of norm_residual: from dz (given exactly when w_pre is), dh (the residual stream's own gradient,
+    or None), the stored h (needed with w_pre) and y returns (dx, dy, dgate, dw_post, dw_pre); the last three are
+    None without gate, w_post, w_pre. dgate is fp32 [C] for a [C] gate and bf16 [T, C] for a [T, C] one."""
+    ref = dh if dh is not None else h
+    if ref is None:
+        raise ValueError("dh or h is required")
+    if (dz is None) != (w_pre is None):
+        raise ValueError("dz is given exactly when w_pre is")
+    if w_pre is not None and h is None:
+        raise ValueError("h is needed for the gradient of the norm after the residual")
+    if dz is None and dh is None:
+        raise ValueError("at least one of dz and dh is required")
+    T, C, res = _residual(ref)
+    ds = _rows(dh, "dh", T, C, ref.dtype) if dh is not None else 0
+    zs = _rows(dz, "dz", T, C, torch.bfloat16) if dz is not None else 0
+    hs = _rows(h, "h", T, C, ref.dtype) if h is not None else 0
+    ys = _rows(y, "y", T, C, torch.bfloat16)
+    gs = _gate_stride(gate, T, C)
+    _channel(w_post, "w_post", C)
+    _channel(w_pre, "w_pre", C)
+    with _on(stream, dz, dh, h, y, gate, w_post, w_pre, workspace, status) as s:
+        new = dict(device=ref.device)
+        dx = torch.empty((T, C), dtype=ref.dtype, **new)
+        dy = torch.empty((T, C), dtype=torch.bfloat16, **new)
+        dgate = None
+        if gate is not None:
+            dgate = torch.empty(gate.shape, dtype=torch.float32 if gate.dim() == 1 else torch.bfloat16, **new)
+        dw_post = torch.empty(C, dtype=torch.float32, **new) if w_post is not None else None
+        dw_pre = torch.empty(C, dtype=torch.float32, **new) if w_pre is not None else None
+        _made(stream, dx, dy, dgate, dw_post, dw_pre)
+        workspace = _workspace(workspace, int(lib().vit_norm_residual_bwd_workspace_size(C)), ref.device, stream)
+        _check(lib().vit_norm_residual_bwd(_ptr(dz), _ptr(dh), _ptr(h), _ptr(y), _ptr(gate), _ptr(w_post),
+                                           _ptr(w_pre), _ptr(dx), _ptr(dy), _ptr(dgate), _ptr(dw_post), _ptr(dw_pre),
+                                           T, C, res, zs, ds, hs, ys, gs, C, C, C, float(scale), float(eps),
+                                           _ptr(workspace), _bytes(workspace), _ptr(status), s), "vit_norm_residual_bwd")
+    return dx, dy, dgate, dw_post, dw_pre
 
 
 DEFAULT_SHORT_MAX = 64   # the library's kernel split when a call passes none

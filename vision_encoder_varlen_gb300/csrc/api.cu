@@ -253,6 +253,7 @@ vit_status_t check_varlen_attn_args(const void *q, const void *k, const void *v,
 }
 
 vit_status_t check_device() { return device_info(nullptr); }
+vit_status_t check_device(int *num_sms) { return device_info(num_sms); }
 
 }  // namespace vit
 

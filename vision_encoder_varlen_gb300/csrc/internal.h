@@ -128,6 +128,60 @@ cudaError_t launch_attn_tiny(const AttnArgs &a, int64_t max_items_tiny, int num_
 cudaError_t launch_attn_long(const AttnArgs &a, int64_t max_items_long, int num_sms, int stall_v,
                              cudaStream_t stream);
 
+// ---- the operators around a language model's reading of the encoder's states
+
+// (time, row, column) of every token of n packed clips, and their offsets (either may be NULL)
+cudaError_t launch_grid_positions(const int32_t *grid_thw, int n, int64_t T, int32_t *pos, int32_t *cu_seqlens,
+                                  int32_t *status, cudaStream_t stream);
+
+// Three-axis rotary positions with the per-head norm. A half whose head count is 0 is left out.
+struct MropeArgs {
+    const void *q_in, *k_in;      // bf16 [T, Hq, D], [T, Hk, D] (gradient: the forward call's inputs)
+    void *q_out, *k_out;          // forward: outputs; gradient: dq_in, dk_in
+    const void *dq, *dk;          // gradient: with respect to the outputs
+    int64_t q_in_stride, k_in_stride, q_out_stride, k_out_stride, dq_stride, dk_stride;
+    int64_t T;
+    int Hq, Hk, D;
+    const int32_t *pos;           // [T, 3]
+    const float *inv_freq;        // [D/2]
+    int sections[3];
+    bool cycled, interleaved;
+    const void *norm_w;           // bf16 [2, D] or NULL
+    float eps;
+    float *part;                  // gradient: workspace of kMropeParts rows of 2 D sums
+};
+constexpr int kMropeParts = 608;  // blocks of the gradient kernel at most
+cudaError_t launch_mrope(const MropeArgs &a, int num_sms, cudaStream_t stream);
+cudaError_t launch_mrope_bwd(const MropeArgs &a, float *dnorm_w, int num_sms, cudaStream_t stream);
+
+// Residual step with the norms on either side (x, h, dh, dx in fp32 when res_f32, else bf16).
+struct NormResidualArgs {
+    const void *x, *y, *gate, *w_post, *w_pre;
+    void *h_out, *z_out;
+    int64_t T, x_stride, y_stride, gate_stride, h_stride, z_stride;   // gate_stride 0: one gate row for all tokens
+    int C;
+    bool res_f32;
+    float scale, eps;
+};
+struct NormResidualGrad {
+    const void *dz, *dh, *h, *y, *gate, *w_post, *w_pre;
+    void *dx, *dy, *dgate;        // dgate: bf16 [T, C] for a per-token gate, fp32 [C] otherwise
+    float *dw_post, *dw_pre;      // fp32 [C]
+    float *part;                  // workspace of kNormResidualParts rows of sums
+    int64_t T, dz_stride, dh_stride, h_stride, y_stride, gate_stride, dx_stride, dy_stride, dgate_stride;
+    int C;
+    bool res_f32;
+    float scale, eps;
+    int32_t *status;
+};
+constexpr int kNormResidualParts = 608;   // row groups of the gradient kernel at most
+cudaError_t launch_norm_residual(const NormResidualArgs &a, int num_sms, cudaStream_t stream);
+cudaError_t launch_norm_residual_bwd(const NormResidualGrad &a, int num_sms, cudaStream_t stream);
+
+// out_k[c] = sum over p < n_parts of part[p][k][c], in a fixed order (k < n_sum <= 3)
+cudaError_t launch_column_sum(const float *part, int n_parts, int n_sum, int C, float *out0, float *out1, float *out2,
+                              cudaStream_t stream);
+
 // Every host-side check of the attention calls except those of the workspace (api.cu).
 // *nothing is set when the call has no work at all (no segments, no tokens).
 vit_status_t check_varlen_attn_args(const void *q, const void *k, const void *v, int64_t T, int H, int D,
@@ -145,5 +199,6 @@ bool encode_tiled_map(CUtensorMap *m, const void *ptr, int rank, const uint64_t 
 
 // VIT_OK when the current device is one this library was built for.
 vit_status_t check_device();
+vit_status_t check_device(int *num_sms);
 
 }  // namespace vit

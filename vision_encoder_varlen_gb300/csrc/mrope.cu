@@ -1,0 +1,520 @@
+// Rotary positions with three axes (time, height, width) for images and video, fused with the
+// per-head RMS norm of q and k, and their gradient; plus the positions themselves.
+//
+// Pair m < D/2 of a head turns by a_m = pos[axis(m)] * inv_freq[m], where axis(m) comes from the
+// three section lengths s_t + s_h + s_w = D/2:
+//   blocked   the first s_t pairs follow time, the next s_h height, the last s_w width;
+//   cycled    pair m follows height if m = 1 (mod 3) and m < 3 s_h, width if m = 2 (mod 3) and
+//             m < 3 s_w, else time.
+//   xn = x * rsqrt(mean(x^2) + eps) * w            (or xn = x)
+//   (y1, y2) = (x1 cos a - x2 sin a, x2 cos a + x1 sin a)     over pairs (m, m + D/2) or (2m, 2m + 1)
+// all in fp32, rounded to bf16 once at the end. The gradient turns back and differentiates the norm:
+//   dz = R(-a) dy,  dn = dz w,  dx = r (dn - xh mean(dn xh)),  dw = sum over rows of dz xh,
+//   r = rsqrt(mean(x^2) + eps), xh = x r.
+//
+// The angle: the product of an int32 position and an fp32 frequency needs 55 bits before it is
+// reduced (position 10^6 at frequency 1 leaves an fp32 product with 0.06 rad of error), so it is
+// formed and reduced by 2 pi in fp64 (three operations per pair, shared by all heads of the token;
+// the fp32 remainder in [-pi, pi] then goes through __sincosf, whose absolute error there is 2^-21).
+//
+// HBM bound: 4 T (Hq + Hk) D bytes forward, 6 T (Hq + Hk) D backward. One warp owns a token (or,
+// when there are fewer tokens than warps to fill the GPU, a slice of a token's heads): it builds the
+// token's cos/sin row in its own part of shared memory and then walks the heads, so no barrier
+// wider than a warp is needed. A head row belongs to D/16 lanes, lane c holding the 16-byte chunks
+// c and c + D/16, so every rotated pair lies in one thread; a warp handles 32 / (D/16) rows at a
+// time and keeps several steps' loads in flight. The gradient's weight sums stay in registers (a
+// lane's columns never change), are joined per block in shared memory in a fixed order, and a
+// second kernel adds the blocks' partial sums.
+#include "internal.h"
+#include "rope_math.cuh"
+
+namespace vit {
+namespace {
+
+using rope::unpack8;
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+
+struct Mrope {
+    const __nv_bfloat16 *q_in, *k_in;          // forward input, or (gradient) the normed call's input
+    __nv_bfloat16 *q_out, *k_out;              // forward output, or dx
+    const __nv_bfloat16 *dq, *dk;              // gradient: dy
+    int64_t q_in_stride, k_in_stride, q_out_stride, k_out_stride, dq_stride, dk_stride;
+    int64_t T;
+    int Hq, Hk;
+    const int32_t *pos;
+    const float *inv_freq;
+    int s_t, s_h, s_w;
+    bool cycled;
+    const __nv_bfloat16 *norm_w;
+    float eps;
+    int slices;                                // a token's heads are dealt to this many warps
+    float *part;                               // gradient: [blocks][2][D] sums of dz * xh
+};
+
+__device__ __forceinline__ int axis_of(const Mrope &p, int m) {
+    if (p.cycled) {
+        const int a = m % 3;
+        return a == 1 ? (m < 3 * p.s_h ? 1 : 0) : a == 2 ? (m < 3 * p.s_w ? 2 : 0) : 0;
+    }
+    return m < p.s_t ? 0 : m < p.s_t + p.s_h ? 1 : 2;
+}
+
+// pos * f reduced to [-pi, pi], as an fp32 value
+__device__ __forceinline__ float reduced_angle(int pos, float f) {
+    const double a = (double)pos * (double)f;
+    const double n = rint(a * 0.15915494309189535);                 // 1 / (2 pi)
+    return (float)fma(n, -6.283185307179586, a);
+}
+
+// cos/sin of the token's pairs as {cos m, cos m+1, sin m, sin m+1}, m even
+template <int D> __device__ __forceinline__ void fill_turns(const Mrope &p, int64_t t, int lane, float4 *cs) {
+    int pos[3];
+#pragma unroll
+    for (int a = 0; a < 3; ++a) pos[a] = p.pos[3 * t + a];
+    for (int i = lane; i < D / 4; i += 32) {
+        float c[2], s[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int m = 2 * i + e, a = axis_of(p, m);
+            __sincosf(reduced_angle(a == 0 ? pos[0] : a == 1 ? pos[1] : pos[2], p.inv_freq[m]), &s[e], &c[e]);
+        }
+        cs[i] = make_float4(c[0], c[1], s[0], s[1]);
+    }
+}
+
+// y = R(+-a) x on the 16 elements of a lane; cs: the lane's turns of its two chunks' pairs
+template <bool IL, bool BACK>
+__device__ __forceinline__ void turn(float *xa, float *xb, const float4 *cs_a, const float4 *cs_b) {
+    if constexpr (!IL) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            const float4 t = cs_a[i / 2];
+            const float s0 = BACK ? -t.z : t.z, s1 = BACK ? -t.w : t.w;
+            const float a0 = xa[i], a1 = xa[i + 1], b0 = xb[i], b1 = xb[i + 1];
+            xa[i] = fmaf(a0, t.x, -b0 * s0);
+            xb[i] = fmaf(b0, t.x, a0 * s0);
+            xa[i + 1] = fmaf(a1, t.y, -b1 * s1);
+            xb[i + 1] = fmaf(b1, t.y, a1 * s1);
+        }
+    } else {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float *x = half ? xb : xa;
+            const float4 *cs = half ? cs_b : cs_a;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float4 t = cs[q >> 1];
+                const float c = (q & 1) ? t.y : t.x, s = BACK ? -((q & 1) ? t.w : t.z) : ((q & 1) ? t.w : t.z);
+                const float a = x[2 * q], b = x[2 * q + 1];
+                x[2 * q] = fmaf(a, c, -b * s);
+                x[2 * q + 1] = fmaf(b, c, a * s);
+            }
+        }
+    }
+}
+
+template <int D> struct Shape {
+    static constexpr int CH = D / 16;          // lanes per row
+    static constexpr int ROWS = 32 / CH;       // rows a warp handles at a time
+};
+
+// sum over the CH lanes of a row's group, added in lane order
+template <int D> __device__ __forceinline__ float group_sum(float v, int first) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < Shape<D>::CH; ++i) s += __shfl_sync(0xffffffffu, v, (first + i) & 31);
+    return s;
+}
+
+__device__ __forceinline__ uint4 pack8(const float *x) {
+    return make_uint4(rope::pack2(x[0], x[1]), rope::pack2(x[2], x[3]), rope::pack2(x[4], x[5]),
+                      rope::pack2(x[6], x[7]));
+}
+
+template <int D, bool IL>
+__global__ void __launch_bounds__(kThreads)
+mrope_kernel(const Mrope p)
+{
+    constexpr int CH = Shape<D>::CH, ROWS = Shape<D>::ROWS, BATCH = 4;
+    __shared__ float4 s_cs[kWarps][D / 4];
+    __shared__ uint4 s_w[2][D / 8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane / CH, c = lane % CH;               // row of the step, chunk of the row
+    const bool live = g < ROWS;
+    const int first = g * CH;
+    if (p.norm_w) {
+        for (int i = threadIdx.x; i < D / 4; i += kThreads)
+            s_w[i / (D / 8)][i % (D / 8)] = reinterpret_cast<const uint4 *>(p.norm_w)[i];
+        __syncthreads();
+    }
+    const float4 *cs_a = s_cs[warp] + (IL ? 2 * c : 4 * c), *cs_b = cs_a + D / 8;
+    const int rows = p.Hq + p.Hk, per = (rows + p.slices - 1) / p.slices;
+    const int64_t units = p.T * p.slices;
+    for (int64_t u = (int64_t)blockIdx.x * kWarps + warp; u < units; u += (int64_t)gridDim.x * kWarps) {
+        const int64_t t = p.slices == 1 ? u : u / p.slices;
+        const int lo = p.slices == 1 ? 0 : (int)(u - t * p.slices) * per;
+        const int hi = min(rows, lo + per);
+        bool filled = false;
+        for (int r0 = lo; r0 < hi; r0 += BATCH * ROWS) {
+            uint4 va[BATCH], vb[BATCH];
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) {
+                const int r = r0 + b * ROWS + g;
+                va[b] = vb[b] = make_uint4(0u, 0u, 0u, 0u);
+                if (live && r < hi) {
+                    const __nv_bfloat16 *src = (r < p.Hq ? p.q_in + t * p.q_in_stride + (int64_t)r * D
+                                                         : p.k_in + t * p.k_in_stride + (int64_t)(r - p.Hq) * D) + 8 * c;
+                    va[b] = *reinterpret_cast<const uint4 *>(src);
+                    vb[b] = *reinterpret_cast<const uint4 *>(src + D / 2);
+                }
+            }
+            if (!filled) {                                // while the first rows are on their way
+                __syncwarp();                             // the previous token's turns have been read
+                fill_turns<D>(p, t, lane, s_cs[warp]);
+                __syncwarp();
+                filled = true;
+            }
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) {
+                const int r = r0 + b * ROWS + g;
+                if (r0 + b * ROWS >= hi) break;           // uniform over the warp
+                const bool k_row = r >= p.Hq;
+                float xa[8], xb[8];
+                unpack8(va[b], xa);
+                unpack8(vb[b], xb);
+                if (p.norm_w) {
+                    float ss = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) ss = fmaf(xa[e], xa[e], fmaf(xb[e], xb[e], ss));
+                    const float inv = rsqrtf(group_sum<D>(ss, first) * (1.f / D) + p.eps);
+                    float wa[8], wb[8];
+                    unpack8(s_w[k_row][c], wa);
+                    unpack8(s_w[k_row][CH + c], wb);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        xa[e] *= inv * wa[e];
+                        xb[e] *= inv * wb[e];
+                    }
+                }
+                turn<IL, false>(xa, xb, cs_a, cs_b);
+                if (live && r < hi) {
+                    __nv_bfloat16 *dst = (k_row ? p.k_out + t * p.k_out_stride + (int64_t)(r - p.Hq) * D
+                                                : p.q_out + t * p.q_out_stride + (int64_t)r * D) + 8 * c;
+                    *reinterpret_cast<uint4 *>(dst) = pack8(xa);
+                    *reinterpret_cast<uint4 *>(dst + D / 2) = pack8(xb);
+                }
+            }
+        }
+    }
+}
+
+template <int D, bool IL>
+__global__ void __launch_bounds__(kThreads)
+mrope_bwd_kernel(const Mrope p)
+{
+    constexpr int CH = Shape<D>::CH, ROWS = Shape<D>::ROWS, BATCH = 1;
+    __shared__ float4 s_cs[kWarps][D / 4];
+    __shared__ uint4 s_w[2][D / 8];
+    __shared__ float s_sum[kWarps][2][D];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane / CH, c = lane % CH;
+    const bool live = g < ROWS;
+    const int first = g * CH;
+    const bool norm = p.norm_w != nullptr;
+    if (norm) {
+        for (int i = threadIdx.x; i < D / 4; i += kThreads)
+            s_w[i / (D / 8)][i % (D / 8)] = reinterpret_cast<const uint4 *>(p.norm_w)[i];
+        __syncthreads();
+    }
+    const float4 *cs_a = s_cs[warp] + (IL ? 2 * c : 4 * c), *cs_b = cs_a + D / 8;
+    const int rows = p.Hq + p.Hk, per = (rows + p.slices - 1) / p.slices;
+    const int64_t units = p.T * p.slices;
+    // all q rows, then all k rows: one set of sums in registers at a time (both at once spilled)
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+        const int h0 = which ? p.Hq : 0, h1 = which ? rows : p.Hq;
+        const __nv_bfloat16 *dy0 = which ? p.dk : p.dq, *x0 = which ? p.k_in : p.q_in;
+        __nv_bfloat16 *dx0 = which ? p.k_out : p.q_out;
+        const int64_t dy_s = which ? p.dk_stride : p.dq_stride, x_s = which ? p.k_in_stride : p.q_in_stride;
+        const int64_t dx_s = which ? p.k_out_stride : p.q_out_stride;
+        float acc[16];                                    // this lane's columns of the weight sums
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+        for (int64_t u = (int64_t)blockIdx.x * kWarps + warp; u < units; u += (int64_t)gridDim.x * kWarps) {
+            const int64_t t = p.slices == 1 ? u : u / p.slices;
+            const int lo = p.slices == 1 ? 0 : (int)(u - t * p.slices) * per;
+            const int r_lo = max(lo, h0) - h0, r_hi = min(min(rows, lo + per), h1) - h0;   // heads of this half
+            const __nv_bfloat16 *dy = dy0 + t * dy_s, *x = x0 + t * x_s;
+            __nv_bfloat16 *dx = dx0 + t * dx_s;
+            bool filled = false;
+            for (int r0 = r_lo; r0 < r_hi; r0 += BATCH * ROWS) {
+                uint4 va[BATCH], vb[BATCH], ua[BATCH], ub[BATCH];
+#pragma unroll
+                for (int b = 0; b < BATCH; ++b) {
+                    const int r = r0 + b * ROWS + g;
+                    va[b] = vb[b] = ua[b] = ub[b] = make_uint4(0u, 0u, 0u, 0u);
+                    if (live && r < r_hi) {
+                        const int64_t off = (int64_t)r * D + 8 * c;
+                        va[b] = *reinterpret_cast<const uint4 *>(dy + off);
+                        vb[b] = *reinterpret_cast<const uint4 *>(dy + off + D / 2);
+                        if (norm) {
+                            ua[b] = *reinterpret_cast<const uint4 *>(x + off);
+                            ub[b] = *reinterpret_cast<const uint4 *>(x + off + D / 2);
+                        }
+                    }
+                }
+                if (!filled) {
+                    __syncwarp();
+                    fill_turns<D>(p, t, lane, s_cs[warp]);
+                    __syncwarp();
+                    filled = true;
+                }
+#pragma unroll
+                for (int b = 0; b < BATCH; ++b) {
+                    const int r = r0 + b * ROWS + g;
+                    if (r0 + b * ROWS >= r_hi) break;
+                    const bool row = live && r < r_hi;
+                    float da[8], db[8];
+                    unpack8(va[b], da);
+                    unpack8(vb[b], db);
+                    turn<IL, true>(da, db, cs_a, cs_b);   // dz
+                    if (norm) {
+                        float xa[8], xb[8], dna[8], dnb[8];      // x, dn = dz w
+                        unpack8(ua[b], xa);
+                        unpack8(ub[b], xb);
+                        unpack8(s_w[which][c], dna);
+                        unpack8(s_w[which][CH + c], dnb);
+                        float ss = 0.f, dot = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            dna[e] *= da[e];
+                            dnb[e] *= db[e];
+                            ss = fmaf(xa[e], xa[e], fmaf(xb[e], xb[e], ss));
+                            dot = fmaf(dna[e], xa[e], fmaf(dnb[e], xb[e], dot));
+                        }
+                        // lanes without a row add nothing to the sums, whatever eps is
+                        const float r_rms = rsqrtf(group_sum<D>(ss, first) * (1.f / D) + p.eps);
+                        const float inv = row ? r_rms : 0.f;
+                        const float k = inv * inv * (group_sum<D>(dot, first) * (1.f / D));
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            acc[e] = fmaf(da[e], xa[e] * inv, acc[e]);
+                            acc[8 + e] = fmaf(db[e], xb[e] * inv, acc[8 + e]);
+                            da[e] = inv * fmaf(-xa[e], k, dna[e]);
+                            db[e] = inv * fmaf(-xb[e], k, dnb[e]);
+                        }
+                    }
+                    if (row) {
+                        const int64_t off = (int64_t)r * D + 8 * c;
+                        *reinterpret_cast<uint4 *>(dx + off) = pack8(da);
+                        *reinterpret_cast<uint4 *>(dx + off + D / 2) = pack8(db);
+                    }
+                }
+            }
+        }
+        if (!p.part) continue;
+        // a warp's groups hold the same columns: join them in group order
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) s += __shfl_sync(0xffffffffu, acc[e], (i * CH + c) & 31);
+            if (g == 0) s_sum[warp][which][e < 8 ? 8 * c + e : D / 2 + 8 * c + e - 8] = s;
+        }
+    }
+    if (!p.part) return;
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) s += s_sum[w][i / D][i % D];
+        p.part[(int64_t)blockIdx.x * 2 * D + i] = s;
+    }
+}
+
+// Blocks and slices: one warp per token where tokens alone fill the GPU; otherwise a token's heads
+// are cut into slices of at least one step's rows, up to about 16 warps per SM in all.
+template <int D> void shape(Mrope &p, int num_sms, int64_t max_blocks, unsigned *blocks) {
+    const int rows = p.Hq + p.Hk;
+    const int most = (rows + Shape<D>::ROWS - 1) / Shape<D>::ROWS;
+    int64_t s = (int64_t)num_sms * 16 / (p.T > 0 ? p.T : 1);
+    if (s < 1) s = 1;
+    if (s > most) s = most;
+    p.slices = (int)s;
+    const int64_t want = (p.T * p.slices + kWarps - 1) / kWarps;
+    *blocks = (unsigned)(want < max_blocks ? want : max_blocks);
+}
+
+template <int D> cudaError_t launch_fwd(Mrope p, bool il, int num_sms, cudaStream_t stream) {
+    unsigned blocks;
+    shape<D>(p, num_sms, (int64_t)num_sms * 64, &blocks);
+    LaunchScope scope("qk_norm_mrope", stream);
+    if (il) mrope_kernel<D, true><<<blocks, kThreads, 0, stream>>>(p);
+    else mrope_kernel<D, false><<<blocks, kThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <int D> cudaError_t launch_bwd(Mrope p, bool il, float *dnorm_w, int num_sms, cudaStream_t stream) {
+    unsigned blocks;
+    int64_t most = (int64_t)num_sms * 4;
+    if (most > kMropeParts) most = kMropeParts;
+    shape<D>(p, num_sms, most, &blocks);
+    if (!dnorm_w) p.part = nullptr;
+    if (blocks > 0) {
+        LaunchScope scope("qk_norm_mrope_bwd", stream);
+        if (il) mrope_bwd_kernel<D, true><<<blocks, kThreads, 0, stream>>>(p);
+        else mrope_bwd_kernel<D, false><<<blocks, kThreads, 0, stream>>>(p);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    if (!dnorm_w) return cudaSuccess;
+    return launch_column_sum(p.part, (int)blocks, 1, 2 * D, dnorm_w, nullptr, nullptr, stream);
+}
+
+Mrope params(const MropeArgs &a) {
+    Mrope p{};
+    p.q_in = static_cast<const __nv_bfloat16 *>(a.q_in);
+    p.k_in = static_cast<const __nv_bfloat16 *>(a.k_in);
+    p.q_out = static_cast<__nv_bfloat16 *>(a.q_out);
+    p.k_out = static_cast<__nv_bfloat16 *>(a.k_out);
+    p.dq = static_cast<const __nv_bfloat16 *>(a.dq);
+    p.dk = static_cast<const __nv_bfloat16 *>(a.dk);
+    p.q_in_stride = a.q_in_stride;
+    p.k_in_stride = a.k_in_stride;
+    p.q_out_stride = a.q_out_stride;
+    p.k_out_stride = a.k_out_stride;
+    p.dq_stride = a.dq_stride;
+    p.dk_stride = a.dk_stride;
+    p.T = a.T;
+    p.Hq = a.Hq;
+    p.Hk = a.Hk;
+    p.pos = a.pos;
+    p.inv_freq = a.inv_freq;
+    p.s_t = a.sections[0];
+    p.s_h = a.sections[1];
+    p.s_w = a.sections[2];
+    p.cycled = a.cycled;
+    p.norm_w = static_cast<const __nv_bfloat16 *>(a.norm_w);
+    p.eps = a.eps;
+    p.part = a.part;
+    return p;
+}
+
+constexpr int kPosThreads = 256;
+constexpr int kTokensPerBlock = 2048;
+
+// (time, row, column) of every token of clips packed one after the other, frames row-major one
+// after the other inside a clip, and the clips' offsets: every block scans the grid list in shared
+// memory, so no pass over blocks is needed.
+__global__ void __launch_bounds__(kPosThreads)
+grid_positions_kernel(const int32_t *__restrict__ grid_thw, int n, int64_t T, int32_t *__restrict__ pos,
+                      int32_t *__restrict__ cu_out, int32_t *status)
+{
+    extern __shared__ int64_t s_cu[];          // [n + 1]
+    __shared__ int64_t s_part[kPosThreads];
+    __shared__ int s_bad;
+    const int tid = threadIdx.x;
+    if (tid == 0) s_bad = 0;
+    __syncthreads();
+    // tokens of clip i; a product past any T this call takes is an error, not an overflow
+    auto size = [&](int i) -> int64_t {
+        const int64_t t = grid_thw[3 * i], h = grid_thw[3 * i + 1], w = grid_thw[3 * i + 2];
+        if (t < 0 || h < 0 || w < 0) return -1;
+        const int64_t hw = h * w;
+        if (t == 0 || hw == 0) return 0;
+        return (hw > T || t > T / hw) ? -1 : t * hw;
+    };
+    const int per = (n + kPosThreads - 1) / kPosThreads;
+    const int lo = min(tid * per, n), hi = min(lo + per, n);
+    int64_t local = 0;
+    for (int i = lo; i < hi; ++i) {
+        const int64_t s = size(i);
+        if (s < 0) s_bad = 1;
+        local += s < 0 ? 0 : s;
+    }
+    s_part[tid] = local;
+    __syncthreads();
+    for (int off = 1; off < kPosThreads; off <<= 1) {
+        const int64_t add = tid >= off ? s_part[tid - off] : 0;
+        __syncthreads();
+        s_part[tid] += add;
+        __syncthreads();
+    }
+    int64_t run = s_part[tid] - local;
+    if (tid == 0) s_cu[0] = 0;
+    for (int i = lo; i < hi; ++i) {
+        const int64_t s = size(i);
+        run += s < 0 ? 0 : s;
+        s_cu[i + 1] = run;
+    }
+    __syncthreads();
+    if (s_bad || s_cu[n] != T) {
+        if (blockIdx.x == 0 && tid == 0) report_error(status, VIT_ERR_GRID_MISMATCH);
+        return;
+    }
+    if (blockIdx.x == 0 && cu_out)
+        for (int i = tid; i <= n; i += kPosThreads) cu_out[i] = (int32_t)s_cu[i];
+    if (!pos) return;
+    for (int64_t t = (int64_t)blockIdx.x * kTokensPerBlock + tid;
+         t < T && t < (int64_t)(blockIdx.x + 1) * kTokensPerBlock; t += kPosThreads) {
+        int a = 0, b = n;                      // s_cu[a] <= t < s_cu[b]; ends on the last such a (empty clips skipped)
+        while (b - a > 1) {
+            const int m = (a + b) >> 1;
+            if (s_cu[m] <= t) a = m; else b = m;
+        }
+        const unsigned h = (unsigned)grid_thw[3 * a + 1], w = (unsigned)grid_thw[3 * a + 2];
+        const unsigned off = (unsigned)(t - s_cu[a]), row = off / w;
+        pos[3 * t] = (int32_t)(row / h);
+        pos[3 * t + 1] = (int32_t)(row % h);
+        pos[3 * t + 2] = (int32_t)(off % w);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_grid_positions(const int32_t *grid_thw, int n, int64_t T, int32_t *pos, int32_t *cu_seqlens,
+                                  int32_t *status, cudaStream_t stream)
+{
+    const size_t smem = sizeof(int64_t) * (size_t)(n + 1);
+    static DeviceOnce once;
+    cudaError_t e = once.run([] {
+        return cudaFuncSetAttribute(grid_positions_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)(sizeof(int64_t) * (VIT_MAX_SEGMENTS + 1)));
+    });
+    if (e != cudaSuccess) return e;
+    const int64_t want = pos ? (T + kTokensPerBlock - 1) / kTokensPerBlock : 1;
+    LaunchScope scope("grid_positions", stream);
+    grid_positions_kernel<<<(unsigned)(want > 0 ? want : 1), kPosThreads, smem, stream>>>(grid_thw, n, T, pos,
+                                                                                         cu_seqlens, status);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_mrope(const MropeArgs &a, int num_sms, cudaStream_t stream)
+{
+    const Mrope p = params(a);
+    switch (a.D) {
+        case 32: return launch_fwd<32>(p, a.interleaved, num_sms, stream);
+        case 64: return launch_fwd<64>(p, a.interleaved, num_sms, stream);
+        case 80: return launch_fwd<80>(p, a.interleaved, num_sms, stream);
+        case 96: return launch_fwd<96>(p, a.interleaved, num_sms, stream);
+        case 128: return launch_fwd<128>(p, a.interleaved, num_sms, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t launch_mrope_bwd(const MropeArgs &a, float *dnorm_w, int num_sms, cudaStream_t stream)
+{
+    const Mrope p = params(a);
+    switch (a.D) {
+        case 32: return launch_bwd<32>(p, a.interleaved, dnorm_w, num_sms, stream);
+        case 64: return launch_bwd<64>(p, a.interleaved, dnorm_w, num_sms, stream);
+        case 80: return launch_bwd<80>(p, a.interleaved, dnorm_w, num_sms, stream);
+        case 96: return launch_bwd<96>(p, a.interleaved, dnorm_w, num_sms, stream);
+        case 128: return launch_bwd<128>(p, a.interleaved, dnorm_w, num_sms, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace vit
