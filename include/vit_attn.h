@@ -497,6 +497,48 @@ vit_status_t vit_qk_norm_mrope_bwd(const void *dq_out, void *dq_in, const void *
                                    const void *norm_w, float eps, float *dnorm_w, void *workspace,
                                    size_t workspace_bytes, vit_stream_t stream);
 
+/*
+ * Workspace bytes of vit_cross_attn for these sizes (0 for invalid ones). max_q and max_k as for the
+ * call (0: Tq, Tk).
+ */
+size_t vit_cross_attn_workspace_size(int64_t Tq, int64_t Tk, int Hq, int Hkv, int D, int B, int max_q, int max_k);
+
+/*
+ * Cross attention between packed sequences of different lengths: the queries of sequence b,
+ * rows [cu_q[b], cu_q[b+1]) of q, attend to its keys, rows [cu_k[b], cu_k[b] + n_b) of k and v,
+ * n_b = k_len[b] where k_len is given, else cu_k[b+1] - cu_k[b]:
+ *   out[t, h] = softmax_j(scale * <q[t, h], k[j, h / (Hq/Hkv)]>) v[j, h / (Hq/Hkv)]
+ *   lse[t, h] = ln sum_j exp(scale * <q[t, h], k[j, .]>)
+ * without a causal mask, softmax in fp32, P rounded to bf16 for its product with v, fp32
+ * accumulation. A sequence without keys gets out = 0 and lse = -inf. Prompts, single new tokens and
+ * latent queries alike: with few query rows per key head (max_q * Hq/Hkv <= 64) the keys are split
+ * over the GPU and the parts joined; results do not change from run to run.
+ *
+ *   q, out       device bf16 [Tq, Hq, D]; k, v device bf16 [Tk, Hkv, D]; Hq a multiple of Hkv.
+ *   cu_q, cu_k   device int32 [B + 1], ascending; rows before cu[0] and from cu[B] on belong to no
+ *                sequence: they are not read, and out and lse are left as they were there.
+ *   k_len        device int32 [B], or NULL: how many of a sequence's key rows are real (encoder
+ *                states padded to a common length). The rows behind them are not used, whatever
+ *                they hold.
+ *   B            0 <= B <= VIT_MAX_SEGMENTS.
+ *   max_q, max_k bounds of the query and key counts of a sequence (padded buckets are fine), 0: Tq,
+ *                Tk. They choose how the work is cut, so tight ones are faster.
+ *   scale        <= 0 selects 1/sqrt(D).
+ *   lse          device fp32 [Tq, Hq], or NULL.
+ *   workspace    vit_cross_attn_workspace_size(...) bytes, 16-byte aligned; calls sharing one must
+ *                not overlap.
+ * Device-detected: a sequence whose offsets decrease or leave the tensors, whose k_len does not fit
+ * (VIT_ERR_BAD_SEQLENS) or that is longer than max_q or max_k (VIT_ERR_SEQLEN_EXCEEDS_MAX) is left
+ * untouched; the other sequences of such a call may or may not be computed. Nothing is read or
+ * written out of bounds, and nothing in the call depends on the lengths on the host, so it can be
+ * captured once per bucket and replayed.
+ */
+vit_status_t vit_cross_attn(const void *q, const void *k, const void *v, int64_t Tq, int64_t Tk, int Hq, int Hkv,
+                            int D, int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t *cu_q,
+                            const int32_t *cu_k, const int32_t *k_len, int B, int max_q, int max_k, float scale,
+                            void *out, int64_t out_stride, float *lse, void *workspace, size_t workspace_bytes,
+                            int32_t *status_dev, vit_stream_t stream);
+
 /* Storage of the residual stream (vit_norm_residual). */
 enum {
     VIT_RES_BF16 = 0,

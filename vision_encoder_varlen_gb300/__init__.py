@@ -35,11 +35,14 @@ def _declare_block(L):
             ("vit_grid_positions", [vp, i32, i64, vp, vp, vp, vp]),
             ("vit_qk_norm_mrope", [vp] * 4 + [i64, i32, i32, i32] + [i64] * 4 + rope + [vp]),
             ("vit_qk_norm_mrope_bwd", [vp] * 6 + [i64, i32, i32, i32] + [i64] * 6 + rope + [vp, vp, sz, vp]),
+            ("vit_cross_attn", [vp] * 3 + [i64, i64, i32, i32, i32] + [i64] * 3 + [vp] * 3 + [i32, i32, i32, f32, vp,
+                                                                                              i64, vp, vp, sz, vp, vp]),
             ("vit_norm_residual", [vp] * 7 + [i64, i32, i32] + [i64] * 5 + [f32, f32, vp]),
             ("vit_norm_residual_bwd", [vp] * 12 + [i64, i32, i32] + [i64] * 8 + [f32, f32, vp, sz, vp, vp])):
         fn = getattr(L, name)
         fn.argtypes, fn.restype = args, i32
     for name, args in (("vit_qk_norm_mrope_bwd_workspace_size", [i32]),
+                       ("vit_cross_attn_workspace_size", [i64, i64] + [i32] * 6),
                        ("vit_norm_residual_bwd_workspace_size", [i32])):
         fn = getattr(L, name)
         fn.argtypes, fn.restype = args, sz
@@ -579,6 +582,66 @@ def qk_norm_mrope_bwd(dq: torch.Tensor | None, dk: torch.Tensor | None, q: torch
 
 def _bytes(t: torch.Tensor | None) -> int:
     return 0 if t is None else t.numel() * t.element_size()
+
+
+def cross_attn_workspace_size(Tq: int, Tk: int, Hq: int, Hkv: int, D: int, B: int, max_q: int = 0,
+                              max_k: int = 0) -> int:
+    return int(lib().vit_cross_attn_workspace_size(int(Tq), int(Tk), int(Hq), int(Hkv), int(D), int(B), int(max_q),
+                                                   int(max_k)))
+
+
+def _cross_lists(cu_q, cu_k, k_len) -> int:
+    for name, t in (("cu_q", cu_q), ("cu_k", cu_k), ("k_len", k_len)):
+        if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous CUDA int32 vector")
+    B = cu_q.numel() - 1
+    if B < 0 or cu_k.numel() != B + 1 or (k_len is not None and k_len.numel() != B):
+        raise ValueError("cu_q and cu_k must be [B + 1] and k_len [B]")
+    return B
+
+
+def _lse_ok(lse, T, H):
+    if lse.dtype != torch.float32 or tuple(lse.shape) != (T, H) or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous CUDA float32 tensor [{T}, {H}]")
+
+
+def cross_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor,
+               max_q: int | None = None, max_k: int | None = None, scale: float | None = None, *,
+               k_len: torch.Tensor | None = None, out: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None, status: torch.Tensor | None = None, return_lse: bool = False,
+               lse: torch.Tensor | None = None, stream=None):
+    """Attention of packed queries q [Tq, Hq, D] over packed states k, v [Tk, Hkv, D] of other lengths, sequence
+    by sequence (cu_q, cu_k [B + 1]; k_len [B]: real states per sequence where they are padded), without a causal
+    mask; Hq is a multiple of Hkv. Serves prompts, single new tokens and latent queries. A sequence without
+    states gets zeros and lse = -inf. ``max_q`` and ``max_k`` bound the lengths (None: Tq, Tk); tight bounds are
+    faster. With ``return_lse`` (or an ``lse`` buffer) returns (out, lse [Tq, Hq] fp32)."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q must be [Tq, Hq, D] and k, v [Tk, Hkv, D]")
+    Tq, Hq, D = q.shape
+    Tk, Hkv = k.shape[0], k.shape[1]
+    qs, ks, vs = _tok_stride(q, "q", Hq, D), _tok_stride(k, "k", Hkv, D), _tok_stride(v, "v", Hkv, D, Tk)
+    B = _cross_lists(cu_q, cu_k, k_len)
+    max_q, max_k = _max_seqlen(max_q), _max_seqlen(max_k)
+    with _on(stream, q, k, v, cu_q, cu_k, k_len, out, workspace, status, lse) as s:
+        made = []
+        if out is None:
+            out = torch.empty((Tq, Hq, D), dtype=q.dtype, device=q.device)
+            made.append(out)
+        os_ = _tok_stride(out, "out", Hq, D, Tq)
+        if return_lse and lse is None:
+            lse = torch.empty((Tq, Hq), dtype=torch.float32, device=q.device)
+            made.append(lse)
+        if lse is not None:
+            _lse_ok(lse, Tq, Hq)
+        _made(stream, *made)
+        if workspace is None:
+            workspace = _workspace(None, cross_attn_workspace_size(Tq, Tk, Hq, Hkv, D, B, max_q, max_k), q.device,
+                                   stream)
+        _check(lib().vit_cross_attn(_ptr(q), _ptr(k), _ptr(v), Tq, Tk, Hq, Hkv, D, qs, ks, vs, _ptr(cu_q), _ptr(cu_k),
+                                    _ptr(k_len), B, max_q, max_k, float(scale) if scale is not None else 0.0,
+                                    _ptr(out), os_, _ptr(lse), _ptr(workspace), _bytes(workspace), _ptr(status), s),
+               "vit_cross_attn")
+    return (out, lse) if lse is not None else out
 
 
 RES_BF16, RES_FP32 = 0, 1

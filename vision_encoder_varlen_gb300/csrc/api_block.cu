@@ -2,6 +2,7 @@
 // validation on the host, then kernel launches (as in api.cu).
 #include <math.h>
 
+#include "cross.h"
 #include "internal.h"
 #include "trace.h"
 
@@ -12,7 +13,7 @@ namespace {
 bool head_dim_ok(int D) { return D == 32 || D == 64 || D == 80 || D == 96 || D == 128; }
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 bool stride_ok(int64_t s, int64_t n) { return s >= n && s % 8 == 0; }
-bool heads_ok(int H) { return H >= 1 && H <= 65536; }
+bool heads_ok(int H) { return H >= 1 && H <= 65535; }
 vit_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? VIT_OK : VIT_ERR_CUDA; }
 
 constexpr int64_t kMaxTokens = (int64_t)1 << 31;
@@ -172,6 +173,111 @@ vit_status_t vit_qk_norm_mrope_bwd(const void *dq_out, void *dq_in, const void *
     a.eps = eps;
     a.part = static_cast<float *>(workspace);
     return from_cuda(launch_mrope_bwd(a, dnorm_w, sms, (cudaStream_t)stream));
+}
+
+namespace {
+
+// bounds of the lengths as the kernels take them, and whether the sizes of a cross-attention call fit
+vit_status_t cross_sizes(int64_t Tq, int64_t Tk, int Hq, int Hkv, int D, int B, int *max_q, int *max_k)
+{
+    if (!head_dim_ok(D)) return VIT_ERR_BAD_HEAD_DIM;
+    if (Tq < 0 || Tq >= kMaxTokens || Tk < 0 || Tk >= kMaxTokens || !heads_ok(Hq) || !heads_ok(Hkv) || Hq % Hkv != 0 ||
+        B < 0)
+        return VIT_ERR_BAD_SHAPE;
+    if (B > VIT_MAX_SEGMENTS) return VIT_ERR_TOO_MANY_SEGMENTS;
+    if (*max_q < 0 || *max_k < 0) return VIT_ERR_BAD_ARGUMENT;
+    if (*max_q == 0 || *max_q > Tq) *max_q = (int)Tq;
+    if (*max_k == 0 || *max_k > Tk) *max_k = (int)Tk;
+    return VIT_OK;
+}
+
+bool takes_few(int Hq, int Hkv, int max_q) { return (int64_t)max_q * (Hq / Hkv) <= kFewRows; }
+
+// the checks that the cross-attention calls share (pointers, strides and alignment of q, k, v and the lists)
+vit_status_t check_cross(const void *q, const void *k, const void *v, int64_t Tk, int Hq, int Hkv, int D,
+                         int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t *cu_q,
+                         const int32_t *cu_k, const int32_t *k_len, float scale)
+{
+    if (isnan(scale) || isinf(scale)) return VIT_ERR_BAD_ARGUMENT;
+    if (!q || (Tk > 0 && (!k || !v)) || !cu_q || !cu_k) return VIT_ERR_NULL_POINTER;
+    if (!stride_ok(q_stride, (int64_t)Hq * D) ||
+        (Tk > 0 && (!stride_ok(k_stride, (int64_t)Hkv * D) || !stride_ok(v_stride, (int64_t)Hkv * D))))
+        return VIT_ERR_BAD_STRIDE;
+    if (!aligned16(q) || (Tk > 0 && (!aligned16(k) || !aligned16(v))) || ((uintptr_t)cu_q & 3u) ||
+        ((uintptr_t)cu_k & 3u) || ((uintptr_t)k_len & 3u))
+        return VIT_ERR_MISALIGNED;
+    return VIT_OK;
+}
+
+}  // namespace
+
+size_t vit_cross_attn_workspace_size(int64_t Tq, int64_t Tk, int Hq, int Hkv, int D, int B, int max_q, int max_k)
+{
+    if (cross_sizes(Tq, Tk, Hq, Hkv, D, B, &max_q, &max_k) != VIT_OK) return 0;
+    if (B == 0 || Tq == 0) return 16;
+    if (takes_few(Hq, Hkv, max_q)) {
+        const size_t n = few_plan(B, Hq, Hkv, D, max_q, max_k).partial_bytes;
+        return n > 16 ? n : 16;
+    }
+    const LongPlan p = long_plan(Tq, B, Hq, Hkv, D, max_q, max_k);
+    return p.max_items >= ((int64_t)1 << 31) ? 0 : p.bytes;
+}
+
+vit_status_t vit_cross_attn(const void *q, const void *k, const void *v, int64_t Tq, int64_t Tk, int Hq, int Hkv,
+                            int D, int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t *cu_q,
+                            const int32_t *cu_k, const int32_t *k_len, int B, int max_q, int max_k, float scale,
+                            void *out, int64_t out_stride, float *lse, void *workspace, size_t workspace_bytes,
+                            int32_t *status_dev, vit_stream_t stream)
+{
+    TraceRange trace("vit_cross_attn");
+    vit_status_t st = cross_sizes(Tq, Tk, Hq, Hkv, D, B, &max_q, &max_k);
+    if (st != VIT_OK) return st;
+    if (B == 0 || Tq == 0) return VIT_OK;
+    st = check_cross(q, k, v, Tk, Hq, Hkv, D, q_stride, k_stride, v_stride, cu_q, cu_k, k_len, scale);
+    if (st != VIT_OK) return st;
+    if (!out || !workspace) return VIT_ERR_NULL_POINTER;
+    if (!stride_ok(out_stride, (int64_t)Hq * D)) return VIT_ERR_BAD_STRIDE;
+    if (!aligned16(out) || ((uintptr_t)lse & 3u) || !aligned16(workspace)) return VIT_ERR_MISALIGNED;
+    const size_t need = vit_cross_attn_workspace_size(Tq, Tk, Hq, Hkv, D, B, max_q, max_k);
+    if (need == 0) return VIT_ERR_BAD_SHAPE;
+    if (workspace_bytes < need) return VIT_ERR_WORKSPACE_TOO_SMALL;
+    int sms = 0;
+    st = check_device(&sms);
+    if (st != VIT_OK) return st;
+    CrossArgs a{};
+    a.q = q;
+    a.k = Tk > 0 ? k : q;                       // no keys anywhere: never read, but a map needs an address
+    a.v = Tk > 0 ? v : q;
+    a.k_stride = Tk > 0 ? k_stride : q_stride;
+    a.v_stride = Tk > 0 ? v_stride : q_stride;
+    a.out = out;
+    a.lse = lse;
+    a.Hq = Hq;
+    a.Hk = Hkv;
+    a.D = D;
+    a.q_stride = q_stride;
+    a.out_stride = out_stride;
+    a.scale_log2 = (scale <= 0.f ? 1.0f / sqrtf((float)D) : scale) * 1.4426950408889634f;
+    a.segs = CrossSegs{cu_q, cu_k, k_len, B, Tq, Tk, max_q, max_k};
+    a.workspace = workspace;
+    a.status = status_dev;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (takes_few(Hq, Hkv, max_q)) return from_cuda(launch_cross_few(a, few_plan(B, Hq, Hkv, D, max_q, max_k), s));
+    const LongPlan p = long_plan(Tq, B, Hq, Hkv, D, max_q, max_k);
+    char *ws = static_cast<char *>(workspace);
+    WsHeader *hdr = reinterpret_cast<WsHeader *>(ws);
+    CrossItem *items = reinterpret_cast<CrossItem *>(ws + p.off_items);
+    CrossTile *tiles = reinterpret_cast<CrossTile *>(ws + p.off_tiles);
+    CrossLong cx{};
+    cx.group = Hq / Hkv;
+    cx.lg_pack = p.lg_pack;
+    cx.segs = a.segs;
+    cx.part_s = reinterpret_cast<float *>(ws + p.off_part_s);
+    cx.part_o = reinterpret_cast<float *>(ws + p.off_part_o);
+    cudaError_t e = launch_cross_schedule(a, p, sms, hdr, items, tiles, s);
+    if (e == cudaSuccess) e = launch_cross_long(a, cx, hdr, items, p.max_items, sms, s);
+    if (e == cudaSuccess && p.runs > 1) e = launch_cross_tile_join(a, p, cx, hdr, tiles, s);
+    return from_cuda(e);
 }
 
 static vit_status_t check_norm(int64_t T, int C, int res_type, const void *gate, int64_t gate_stride, float scale,

@@ -56,6 +56,7 @@
 
 #include <type_traits>
 
+#include "cross.h"
 #include "internal.h"
 #include "sm100.cuh"
 
@@ -138,6 +139,19 @@ template <int SW> __device__ __forceinline__ uint64_t kmajor_desc(uint32_t addr)
     return smem_desc(addr, 16, 8 * SW, SW == 128 ? 2 : (SW == 64 ? 4 : 6));
 }
 
+// What an item says, whichever kind it is: the self-attention list's (keys and queries are the same
+// rows) or the cross-attention list's.
+__device__ __forceinline__ int item_k0(const Item &x) { return x.x; }
+__device__ __forceinline__ int item_keys(const Item &x) { return x.y; }
+__device__ __forceinline__ int item_q0(const Item &x) { return x.z; }
+__device__ __forceinline__ int item_q_end(const Item &x) { return x.x + x.y; }
+__device__ __forceinline__ int item_k0(const CrossItem &x) { return x.k0; }
+__device__ __forceinline__ int item_keys(const CrossItem &x) { return x.kn; }
+__device__ __forceinline__ int item_q0(const CrossItem &x) { return x.q0; }
+__device__ __forceinline__ int item_q_end(const CrossItem &x) { return x.q1; }
+
+struct NoCross {};                     // the self-attention kernels carry no cross-attention parameters
+
 struct Bars {
     uint64_t q_full[2], q_empty[2], q_ready[2];
     uint64_t k_full[kMaxStages], v_full[kMaxStages], k_empty[kMaxStages], v_empty[kMaxStages];
@@ -176,15 +190,17 @@ __device__ __forceinline__ void pv_tail(uint32_t tO, uint32_t tP, uint64_t dv, u
     mma_commit(bar_done);
 }
 
-template <int D, bool LSE, bool FQ>
+template <int D, bool LSE, bool FQ, bool X>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qr,
                  const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_kr,
                  const __grid_constant__ CUtensorMap tm_v, __nv_bfloat16 *__restrict__ out, int64_t out_stride,
                  float *__restrict__ lse, int H, float scale_log2, WsHeader *__restrict__ hdr,
-                 const Item *__restrict__ items, int32_t *status, int stall_v, const rope::QRope qr)
+                 const std::conditional_t<X, CrossItem, Item> *__restrict__ items, int32_t *status, int stall_v,
+                 const rope::QRope qr, const std::conditional_t<X, CrossLong, NoCross> cx)
 {
     using C = LongCfg<D>;
+    using Item = std::conditional_t<X, CrossItem, vit::Item>;
     constexpr int BN = C::BN, ST = C::STAGES, NSLAB = C::NSLAB;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *base = reinterpret_cast<unsigned char *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -192,7 +208,7 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     __shared__ float s_m[2][BM], s_l[2][BM];   // split items: each half's running max and row sum per row
-    __shared__ Item s_items[kItemRing];        // the item ring (y < 0: the end of this CTA's list)
+    __shared__ Item s_items[kItemRing];        // the item ring (keys < 0: the end of this CTA's list)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n_items = hdr->n_long;                   // read by the producer; the others take items from it
@@ -260,7 +276,7 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         x = s_items[slot];
         if (warp_wide) __syncwarp();
         if (!warp_wide || lane == 0) mbar_arrive(bar_addr(bars.item_empty[slot]));
-        return x.y >= 0;
+        return item_keys(x) >= 0;
     };
 
     if (warp < 4) regs_dec<FQ ? kCtrlRegsFQ : kCtrlRegs>();
@@ -281,6 +297,14 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 if constexpr (C::REM > 0)
                     tma_load_2d(smem_addr(dst + C::N128 * rows * 128), rem, head * D + 64 * C::N128, row, bar);
             };
+            // cross attention: a tile is 128 / P tokens of P neighbouring heads, rows token-major
+            auto load_q_packed = [&](unsigned char *dst, int head, int tok, uint32_t bar) {
+#pragma unroll
+                for (int s = 0; s < C::N128; ++s)
+                    tma_load_3d(smem_addr(dst + s * BM * 128), &tm_q, 64 * s, head, tok, bar);
+                if constexpr (C::REM > 0)
+                    tma_load_3d(smem_addr(dst + C::N128 * BM * 128), &tm_qr, 64 * C::N128, head, tok, bar);
+            };
             uint32_t g = 0, q_it = 0;
             // parity + 1 of the last load issued on each barrier (0 = none), for the abort drain;
             // two bits per stage, kept in registers
@@ -290,9 +314,13 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             auto load_q = [&](uint32_t qb, uint32_t qn, int q0, int head, bool split) {
                 const int nt = split ? 1 : 2;
                 mbar_arrive_expect_tx(bar_addr(bars.q_full[qb]), nt * C::Q_TILE);
-                for (int i = 0; i < nt; ++i)
-                    load_qk_tile(base + C::OFF_Q + (2 * qb + i) * C::Q_TILE, &tm_q, &tm_qr, BM, head, q0 + BM * i,
-                                 bar_addr(bars.q_full[qb]));
+                for (int i = 0; i < nt; ++i) {
+                    unsigned char *dst = base + C::OFF_Q + (2 * qb + i) * C::Q_TILE;
+                    if constexpr (X)
+                        load_q_packed(dst, head, q0 + (BM >> cx.lg_pack) * i, bar_addr(bars.q_full[qb]));
+                    else
+                        load_qk_tile(dst, &tm_q, &tm_qr, BM, head, q0 + BM * i, bar_addr(bars.q_full[qb]));
+                }
                 q_pend = (q_pend & ~(3u << (2 * qb))) | (((qn & 1) + 1) << (2 * qb));
             };
             // K and V of a tile go into separate halves of a ring slot: a slot's K half is free once
@@ -328,15 +356,23 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 ++k_pub;
                 return true;
             };
-            const Item kEnd = make_int4(0, -1, 0, 0);
+            Item kEnd;
+            if constexpr (X)
+                kEnd = CrossItem{0, -1, 0, 0, 0, 0, -1, 0};
+            else
+                kEnd = make_int4(0, -1, 0, 0);
             int it = blockIdx.x;
             Item item = it < n_items ? items[it] : kEnd;
             for (; ok && it < n_items; ++q_it) {
                 if (!publish(item)) break;
                 const int it_next = (int)gridDim.x + atomicAdd(&hdr->next_long, 1);
                 const Item nx = it_next < n_items ? items[it_next] : kEnd;
-                const int seg0 = item.x, seg_len = item.y, q0 = item.z, head = item_head(item);
+                const int seg0 = item_k0(item), seg_len = item_keys(item), q0 = item_q0(item), head = item_head(item);
                 const int n_kv = (seg_len + BN - 1) / BN;
+                const int kv_head = [&] {
+                    if constexpr (X) return head / cx.group;
+                    else return head;
+                }();
                 // Q pairs alternate between two buffers, so the next item's Q is loaded while
                 // the current item still runs
                 const uint32_t qb = q_it % C::QBUF, qn = q_it / C::QBUF;   // buffer, its use count
@@ -350,7 +386,7 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         if (!q_early && it_next < n_items) {
                             const uint32_t qb1 = (q_it + 1) & 1, qn1 = (q_it + 1) >> 1;
                             if (qn1 == 0 || mbar_test(bar_addr(bars.q_empty[qb1]), (qn1 - 1) & 1)) {
-                                load_q(qb1, qn1, nx.z, item_head(nx), item_split(nx));
+                                load_q(qb1, qn1, item_q0(nx), item_head(nx), item_split(nx));
                                 q_early = true;
                             }
                         }
@@ -359,13 +395,13 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     if (g >= (uint32_t)ST && !(ok = wait(bars.k_empty[st], (g / ST - 1) & 1))) break;
                     const int row = seg0 + j * BN;
                     mbar_arrive_expect_tx(bar_addr(bars.k_full[st]), C::K_TILE);
-                    load_qk_tile(base + C::OFF_K + st * C::K_STRIDE, &tm_k, &tm_kr, BN, head, row,
+                    load_qk_tile(base + C::OFF_K + st * C::K_STRIDE, &tm_k, &tm_kr, BN, kv_head, row,
                                  bar_addr(bars.k_full[st]));
                     k_pend = (k_pend & ~(3u << (2 * st))) | ((((g / ST) & 1) + 1) << (2 * st));
                     if (v_row >= 0 && !load_v()) break;
                     v_g = g;
                     v_row = row;
-                    v_head = head;
+                    v_head = kv_head;
                 }
                 it = it_next;
                 item = nx;
@@ -441,8 +477,8 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             };
 
             for (Item item; take_item(item_cnt, item, false, ok); ++item_cnt) {
-                const int n_kv = (item.y + BN - 1) / BN;
-                const int n_full = item.y / BN;                  // tiles with BN keys of the segment
+                const int n_kv = (item_keys(item) + BN - 1) / BN;
+                const int n_full = item_keys(item) / BN;                  // tiles with BN keys of the segment
                 uint32_t st = t % ST, ph = (t / ST) & 1;
                 const uint32_t qb = item_cnt % C::QBUF;         // Q buffer of this item
                 if (!(ok = wait(FQ ? bars.q_ready[qb] : bars.q_full[qb], (item_cnt / C::QBUF) & 1))) break;
@@ -478,7 +514,7 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         if constexpr (decltype(tail)::value)
                             pv_tail<NSLAB, C::KV_SLAB, D>(tO, tP, dv0 + st * STAGE_STEP,
                                                           base + C::OFF_V + st * C::KV_TILE, j > 0 ? 1u : 0u,
-                                                          item.y - j * BN, a_pvdone);
+                                                          item_keys(item) - j * BN, a_pvdone);
                         else
                             pv(dv0 + st * STAGE_STEP, j > 0 ? 1u : 0u);
                         mma_commit(bar_addr(bars.v_empty[st]));
@@ -512,7 +548,7 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     else
                         pv_tail<NSLAB, C::KV_SLAB, D>(tO, tP, dv0 + prev_st * STAGE_STEP,
                                                       base + C::OFF_V + prev_st * C::KV_TILE, acc,
-                                                      item.y - prev_j * BN, a_pvdone);
+                                                      item_keys(item) - prev_j * BN, a_pvdone);
                     mma_commit(bar_addr(bars.v_empty[prev_st]));
                     first_pv = false;
                     return true;
@@ -584,7 +620,7 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             uint32_t item_cnt = 0;
             bool ok = true;
             for (Item item; take_item(item_cnt, item, true, ok); ++item_cnt) {
-                const int64_t seg_end = (int64_t)item.x + item.y, q0 = item.z;
+                const int64_t seg_end = item_q_end(item), q0 = item_q0(item);
                 const uint32_t qb = item_cnt % C::QBUF;
                 if (!(ok = wait_warp(bars.q_full[qb], (item_cnt / C::QBUF) & 1))) break;
                 unsigned char *qbuf = base + C::OFF_Q + 2 * qb * C::Q_TILE;
@@ -610,11 +646,29 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_addr(bars.q_ready[qb]));
             }
-        } else if (lane == 0) {
-            // nothing to do but free its share of every item ring slot
+        } else {
+            // cross attention: the query rows of sequences without keys, which have no items
+            if constexpr (X) {
+                for (int b = blockIdx.x; b < cx.segs.B; b += gridDim.x) {
+                    CrossSeg seg;
+                    if (!load_seg(cx.segs, b, seg, nullptr, false) || seg.kn > 0) continue;
+                    const int64_t rows = (int64_t)seg.qn * H;
+                    for (int64_t i = lane; i < rows * (D / 8); i += 32) {
+                        const int64_t r = i / (D / 8), t = seg.q0 + r / H;
+                        const int h = (int)(r % H), c = (int)(i % (D / 8));
+                        *reinterpret_cast<uint4 *>(out + t * out_stride + (int64_t)h * D + 8 * c) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                        if (c == 0 && lse) lse[t * H + h] = -INFINITY;
+                    }
+                }
+                __syncwarp();
+            }
+            // nothing (else) to do but free its share of every item ring slot
+            if (lane == 0) {
             bool ok = true;
             Item item;
             for (uint32_t k = 0; take_item(k, item, false, ok); ++k) {
+            }
             }
         }
     } else if (warp >= 4) {
@@ -643,7 +697,7 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             tc_fence_after();
             const float inv_l = 1.f / pend_l;
             // l sums exp2(s * scale*log2(e) - m), so ln(sum exp(scale * s)) = (m + log2 l) ln 2
-            if (LSE && pend_store)
+            if (LSE && pend_store && (!X || lse))
                 lse[(int64_t)pend_row * H + pend_head] = (pend_m + log2f(pend_l)) * 0.6931471805599453f;
             __nv_bfloat16 *dst = out + (int64_t)pend_row * out_stride + (int64_t)pend_head * D;
 #pragma unroll
@@ -668,8 +722,19 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             pend = false;
         };
 
+        // the row of the output (token, head) that tile row `row` of tile `tile` is, and whether it exists
+        auto place = [&](const Item &item, int tile, int &tok, int &h) -> bool {
+            if constexpr (X) {
+                tok = item_q0(item) + (BM >> cx.lg_pack) * tile + (row >> cx.lg_pack);
+                h = item_head(item) + (row & ((1 << cx.lg_pack) - 1));
+            } else {
+                tok = item_q0(item) + tile * BM + row;
+                h = item_head(item);
+            }
+            return tok < item_q_end(item);
+        };
         for (Item item; take_item(item_cnt, item, true, ok); ++item_cnt) {
-            const int seg0 = item.x, seg_len = item.y, q0 = item.z, head = item_head(item);
+            const int seg_len = item_keys(item);
             const int n_kv = (seg_len + BN - 1) / BN;
             // own key tiles: every one, or in a split item every other one starting at this group's
             const int dj = item_split(item) ? 2 : 1;
@@ -768,9 +833,7 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (kDeferOut && dj == 1) {
                 // the output of this item waits for the first P of the next one (or the end)
                 pend = true;
-                pend_row = q0 + grp * BM + row;
-                pend_store = pend_row < seg0 + seg_len;
-                pend_head = head;
+                pend_store = place(item, grp, pend_row, pend_head);
                 pend_m = m_run;
                 pend_l = l_run;
                 continue;
@@ -779,11 +842,11 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 // epilogue: wait for this tile's last P.V, then O / l -> bf16 -> HBM
                 if (!(ok = wait_warp(bars.pv_done[grp], (p_cnt - 1) & 1))) break;
                 tc_fence_after();
-                const int q_row = q0 + grp * BM + row;
-                const bool store = q_row < seg0 + seg_len;
+                int q_row, head;
+                const bool store = place(item, grp, q_row, head);
                 const float inv_l = 1.f / l_run;
                 // l_run sums exp2(s * scale*log2(e) - m_run), so ln(sum exp(scale * s)) = (m_run + log2 l_run) ln 2
-                if (LSE && store) lse[(int64_t)q_row * H + head] = (m_run + log2f(l_run)) * 0.6931471805599453f;
+                if (LSE && store && (!X || lse)) lse[(int64_t)q_row * H + head] = (m_run + log2f(l_run)) * 0.6931471805599453f;
                 __nv_bfloat16 *dst = out + (int64_t)q_row * out_stride + (int64_t)head * D;
 #pragma unroll
                 for (int c = 0; c < D; c += 16) {
@@ -839,9 +902,15 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             const float l_sum = w_own * l_run + w_oth * l_oth;
             const float inv_l = 1.f / l_sum;
             const float c0 = (grp ? w_oth : w_own) * inv_l, c1 = (grp ? w_own : w_oth) * inv_l;
-            const int q_row = q0 + row;
-            const bool store = q_row < seg0 + seg_len;
-            if (LSE && store && grp == 0) lse[(int64_t)q_row * H + head] = (M + log2f(l_sum)) * 0.6931471805599453f;
+            int q_row, head;
+            bool store = place(item, 0, q_row, head);
+            bool part = false;                                 // one of several key runs: leave a partial result
+            if constexpr (X) {
+                part = item.slot >= 0;
+                if (part && store && grp == 0) cx.part_s[(int64_t)item.slot * BM + row] = M + log2f(l_sum);
+            }
+            if (LSE && store && grp == 0 && !part && (!X || lse))
+                lse[(int64_t)q_row * H + head] = (M + log2f(l_sum)) * 0.6931471805599453f;
             constexpr int HALF = D / 2;                        // columns of the head this group writes
             static_assert(HALF % 8 == 0, "each group writes whole 16-byte pieces");
             static_assert(C::TO1 == C::TO0 + D, "O1 follows O0");
@@ -864,8 +933,13 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         x1 = fmaf(__uint_as_float(r1[2 * e + 1]), c1, x1);
                     }
                     o[e] = pack_bf16x2(x0, x1);
+                    if constexpr (X) {
+                        if (part && store)
+                            *reinterpret_cast<float2 *>(cx.part_o + ((int64_t)item.slot * BM + row) * D + grp * HALF + c +
+                                                        2 * e) = make_float2(x0, x1);
+                    }
                 }
-                if (store) *reinterpret_cast<uint4 *>(dst + c) = make_uint4(o[0], o[1], o[2], o[3]);
+                if (store && !part) *reinterpret_cast<uint4 *>(dst + c) = make_uint4(o[0], o[1], o[2], o[3]);
             }
             tc_fence_before();
             __syncwarp();
@@ -897,6 +971,17 @@ bool make_map(CUtensorMap *m, const void *ptr, int64_t T, int H, int D, int64_t 
     return encode_tiled_map(m, ptr, 2, dims, strides, box, cols * 2);
 }
 
+template <typename K> cudaError_t set_up(K kern, int smem)
+{
+    cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (r != cudaSuccess) return r;
+    // the setmaxnreg split assumes exactly this launch budget; refuse anything else rather than wait on it
+    cudaFuncAttributes fa;
+    r = cudaFuncGetAttributes(&fa, kern);
+    if (r != cudaSuccess) return r;
+    return (fa.numRegs != kLaunchRegs || fa.maxThreadsPerBlock < kThreads) ? cudaErrorInvalidConfiguration : cudaSuccess;
+}
+
 template <int D>
 cudaError_t launch_d(const AttnArgs &a, int64_t max_items, int num_sms, int stall_v, cudaStream_t stream)
 {
@@ -911,19 +996,10 @@ cudaError_t launch_d(const AttnArgs &a, int64_t max_items, int num_sms, int stal
         !make_map(&mv, a.v, a.T, a.H, D, a.v_stride, C::BN, 16))
         return cudaErrorInvalidValue;
     // the lse store is compiled in only where it is asked for: the plain kernel keeps its code unchanged
-    auto kern = a.lse ? (a.fuse_q ? attn_long_kernel<D, true, true> : attn_long_kernel<D, true, false>)
-                      : (a.fuse_q ? attn_long_kernel<D, false, true> : attn_long_kernel<D, false, false>);
+    auto kern = a.lse ? (a.fuse_q ? attn_long_kernel<D, true, true, false> : attn_long_kernel<D, true, false, false>)
+                      : (a.fuse_q ? attn_long_kernel<D, false, true, false> : attn_long_kernel<D, false, false, false>);
     static DeviceOnce once[4];                           // per (lse, fused Q) variant
-    cudaError_t e = once[(a.lse ? 2 : 0) + (a.fuse_q ? 1 : 0)].run([&] {
-        cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-        if (r != cudaSuccess) return r;
-        // the setmaxnreg split assumes exactly this launch budget; refuse anything else rather than wait on it
-        cudaFuncAttributes fa;
-        r = cudaFuncGetAttributes(&fa, kern);
-        if (r != cudaSuccess) return r;
-        return (fa.numRegs != kLaunchRegs || fa.maxThreadsPerBlock < kThreads) ? cudaErrorInvalidConfiguration
-                                                                              : cudaSuccess;
-    });
+    cudaError_t e = once[(a.lse ? 2 : 0) + (a.fuse_q ? 1 : 0)].run([&] { return set_up(kern, C::SMEM); });
     if (e != cudaSuccess) return e;
     const unsigned blocks = (unsigned)(max_items < num_sms ? max_items : num_sms);
     if (blocks == 0) return cudaSuccess;
@@ -931,11 +1007,72 @@ cudaError_t launch_d(const AttnArgs &a, int64_t max_items, int num_sms, int stal
     kern<<<blocks, kThreads, C::SMEM, stream>>>(mq, mqr, mk, mkr, mv, static_cast<__nv_bfloat16 *>(a.out),
                                                                a.out_stride, a.lse, a.H, a.scale_log2,
                                                                const_cast<WsHeader *>(a.hdr),
-                                                               a.items, a.status, stall_v, a.qr);
+                                                               a.items, a.status, stall_v, a.qr, NoCross{});
+    return cudaGetLastError();
+}
+
+// [T, H, D] rows as boxes of `cols` columns x P heads x 128 / P tokens: a 128-row tile, token-major.
+bool make_packed_map(CUtensorMap *m, const void *ptr, int64_t T, int H, int D, int64_t stride, int pack, int cols)
+{
+    const uint64_t dims[3] = {(uint64_t)D, (uint64_t)H, (uint64_t)(T > 0 ? T : 1)};
+    const uint64_t strides[2] = {(uint64_t)D * 2, (uint64_t)stride * 2};
+    const uint32_t box[3] = {(uint32_t)cols, (uint32_t)pack, (uint32_t)(BM / pack)};
+    return encode_tiled_map(m, ptr, 3, dims, strides, box, cols * 2);
+}
+
+template <int D>
+cudaError_t launch_cross_d(const CrossArgs &a, const CrossLong &cx, const WsHeader *hdr, const CrossItem *items,
+                           int64_t max_items, int num_sms, cudaStream_t stream)
+{
+    using C = LongCfg<D>;
+    const int rem = C::REM > 0 ? C::REM : 64, wide = D >= 64 ? 64 : rem;   // the wide maps of head_dim 32 go unused
+    const CrossSegs &s = a.segs;
+    const int pack = 1 << cx.lg_pack;
+    CUtensorMap mq, mqr, mk, mkr, mv;
+    if (!make_packed_map(&mq, a.q, s.Tq, a.Hq, D, a.q_stride, pack, wide) ||
+        !make_packed_map(&mqr, a.q, s.Tq, a.Hq, D, a.q_stride, pack, rem) ||
+        !make_map(&mk, a.k, s.Tk, a.Hk, D, a.k_stride, C::BN, wide) ||
+        !make_map(&mkr, a.k, s.Tk, a.Hk, D, a.k_stride, C::BN, rem) ||
+        !make_map(&mv, a.v, s.Tk, a.Hk, D, a.v_stride, C::BN, 16))
+        return cudaErrorInvalidValue;
+    auto kern = attn_long_kernel<D, true, false, true>;
+    static DeviceOnce once;
+    cudaError_t e = once.run([&] { return set_up(kern, C::SMEM); });
+    if (e != cudaSuccess) return e;
+    const unsigned blocks = (unsigned)(max_items < num_sms ? max_items : num_sms);
+    if (blocks == 0) return cudaSuccess;
+    LaunchScope scope("cross_long", stream);
+    kern<<<blocks, kThreads, C::SMEM, stream>>>(mq, mqr, mk, mkr, mv, static_cast<__nv_bfloat16 *>(a.out),
+                                                a.out_stride, a.lse, a.Hq, a.scale_log2, const_cast<WsHeader *>(hdr),
+                                                items, a.status, 0, rope::QRope{}, cx);
     return cudaGetLastError();
 }
 
 }  // namespace
+
+int attn_long_bn(int D)
+{
+    switch (D) {
+        case 32: return LongCfg<32>::BN;
+        case 64: return LongCfg<64>::BN;
+        case 80: return LongCfg<80>::BN;
+        case 96: return LongCfg<96>::BN;
+        default: return LongCfg<128>::BN;
+    }
+}
+
+cudaError_t launch_cross_long(const CrossArgs &a, const CrossLong &cx, const WsHeader *hdr, const CrossItem *items,
+                              int64_t max_items, int num_sms, cudaStream_t stream)
+{
+    switch (a.D) {
+        case 32: return launch_cross_d<32>(a, cx, hdr, items, max_items, num_sms, stream);
+        case 64: return launch_cross_d<64>(a, cx, hdr, items, max_items, num_sms, stream);
+        case 80: return launch_cross_d<80>(a, cx, hdr, items, max_items, num_sms, stream);
+        case 96: return launch_cross_d<96>(a, cx, hdr, items, max_items, num_sms, stream);
+        case 128: return launch_cross_d<128>(a, cx, hdr, items, max_items, num_sms, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
 
 bool encode_tiled_map(CUtensorMap *m, const void *ptr, int rank, const uint64_t *dims, const uint64_t *strides,
                       const uint32_t *box, int swizzle_bytes)

@@ -28,39 +28,13 @@
 //      so concurrently running CTAs share one head's K/V in L2.
 // On invalid offsets it records the error and publishes zero items, so the
 // attention kernels that follow compute nothing.
+#include "block_sort.cuh"
 #include "internal.h"
 
 namespace vit {
 namespace {
 
-constexpr int kThreads = 1024;
-
-__device__ __forceinline__ int64_t block_exclusive_scan(int64_t v, int64_t *s_warp, int64_t *total)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) s_warp[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-        int64_t w = s_warp[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) w += y;
-        }
-        s_warp[lane] = w;                // inclusive over warps
-    }
-    __syncthreads();
-    const int64_t before = (warp > 0 ? s_warp[warp - 1] : 0) + x - v;
-    *total = s_warp[31];
-    __syncthreads();
-    return before;
-}
+constexpr int kThreads = kSortThreads;
 
 __global__ void __launch_bounds__(kThreads)
 schedule_kernel(const int32_t *__restrict__ cu_seqlens, const int32_t *__restrict__ seq_start,
@@ -143,22 +117,7 @@ schedule_kernel(const int32_t *__restrict__ cu_seqlens, const int32_t *__restric
     while (NPL < n_lseg) NPL <<= 1;
     for (int i = n_lseg + tid; i < NPL; i += kThreads) s_key[i] = ~0ull;
     __syncthreads();
-    for (int k = 2; k <= NPL; k <<= 1) {
-        for (int j = k >> 1; j > 0; j >>= 1) {
-            for (int i = tid; i < NPL; i += kThreads) {
-                const int l = i ^ j;
-                if (l > i) {
-                    const unsigned long long x = s_key[i], y = s_key[l];
-                    const bool up = (i & k) == 0;
-                    if ((x > y) == up) {
-                        s_key[i] = y;
-                        s_key[l] = x;
-                    }
-                }
-            }
-            __syncthreads();
-        }
-    }
+    block_sort(s_key, NPL, tid);
     for (int p = tid; p < n_lseg; p += kThreads) s_order[p] = (int32_t)(s_key[p] & 0xffffffffu);
     __syncthreads();
 
