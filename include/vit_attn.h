@@ -539,6 +539,32 @@ vit_status_t vit_cross_attn(const void *q, const void *k, const void *v, int64_t
                             void *out, int64_t out_stride, float *lse, void *workspace, size_t workspace_bytes,
                             int32_t *status_dev, vit_stream_t stream);
 
+/* Workspace bytes of vit_cross_attn_bwd for these sizes (0 for invalid ones). */
+size_t vit_cross_attn_bwd_workspace_size(int64_t Tq, int64_t Tk, int Hq, int Hkv, int D, int B, int max_q, int max_k);
+
+/*
+ * Gradient of vit_cross_attn.
+ *
+ *   dout         device bf16 [Tq, Hq, D]: gradient of out.
+ *   out, lse     as the forward call wrote them for the same q, k, v, lists and scale.
+ *   dq, dk, dv   device bf16 outputs [Tq, Hq, D], [Tk, Hkv, D], [Tk, Hkv, D]; dk and dv are summed
+ *                over the query heads that share a key head. They must not overlap an input. Rows
+ *                of no sequence (and key rows behind k_len) are left as they were; the gradients of
+ *                a sequence without keys, or without queries, are 0.
+ *   workspace    vit_cross_attn_bwd_workspace_size(...) bytes, 16-byte aligned; calls sharing one
+ *                must not overlap.
+ * S and dP are recomputed once for dq and once for dk and dv, P and dS rounded to bf16 for their
+ * products; nothing is added up in memory, so results do not change from run to run. Errors as for
+ * vit_cross_attn (key offsets that decrease also leave the whole call uncomputed).
+ */
+vit_status_t vit_cross_attn_bwd(const void *dout, const void *q, const void *k, const void *v, const void *out,
+                                const float *lse, int64_t Tq, int64_t Tk, int Hq, int Hkv, int D, int64_t dout_stride,
+                                int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t out_stride,
+                                const int32_t *cu_q, const int32_t *cu_k, const int32_t *k_len, int B, int max_q,
+                                int max_k, float scale, void *dq, void *dk, void *dv, int64_t dq_stride,
+                                int64_t dk_stride, int64_t dv_stride, void *workspace, size_t workspace_bytes,
+                                int32_t *status_dev, vit_stream_t stream);
+
 /* Storage of the residual stream (vit_norm_residual). */
 enum {
     VIT_RES_BF16 = 0,

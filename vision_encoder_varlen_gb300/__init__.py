@@ -37,12 +37,15 @@ def _declare_block(L):
             ("vit_qk_norm_mrope_bwd", [vp] * 6 + [i64, i32, i32, i32] + [i64] * 6 + rope + [vp, vp, sz, vp]),
             ("vit_cross_attn", [vp] * 3 + [i64, i64, i32, i32, i32] + [i64] * 3 + [vp] * 3 + [i32, i32, i32, f32, vp,
                                                                                               i64, vp, vp, sz, vp, vp]),
+            ("vit_cross_attn_bwd", [vp] * 6 + [i64, i64, i32, i32, i32] + [i64] * 5 + [vp] * 3 + [i32, i32, i32, f32] +
+             [vp] * 3 + [i64] * 3 + [vp, sz, vp, vp]),
             ("vit_norm_residual", [vp] * 7 + [i64, i32, i32] + [i64] * 5 + [f32, f32, vp]),
             ("vit_norm_residual_bwd", [vp] * 12 + [i64, i32, i32] + [i64] * 8 + [f32, f32, vp, sz, vp, vp])):
         fn = getattr(L, name)
         fn.argtypes, fn.restype = args, i32
     for name, args in (("vit_qk_norm_mrope_bwd_workspace_size", [i32]),
                        ("vit_cross_attn_workspace_size", [i64, i64] + [i32] * 6),
+                       ("vit_cross_attn_bwd_workspace_size", [i64, i64] + [i32] * 6),
                        ("vit_norm_residual_bwd_workspace_size", [i32])):
         fn = getattr(L, name)
         fn.argtypes, fn.restype = args, sz
@@ -642,6 +645,52 @@ def cross_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Te
                                     _ptr(out), os_, _ptr(lse), _ptr(workspace), _bytes(workspace), _ptr(status), s),
                "vit_cross_attn")
     return (out, lse) if lse is not None else out
+
+
+def cross_attn_bwd_workspace_size(Tq: int, Tk: int, Hq: int, Hkv: int, D: int, B: int, max_q: int = 0,
+                                  max_k: int = 0) -> int:
+    return int(lib().vit_cross_attn_bwd_workspace_size(int(Tq), int(Tk), int(Hq), int(Hkv), int(D), int(B),
+                                                       int(max_q), int(max_k)))
+
+
+def cross_attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                   lse: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor, max_q: int | None = None,
+                   max_k: int | None = None, scale: float | None = None, *, k_len: torch.Tensor | None = None,
+                   dq: torch.Tensor | None = None, dk: torch.Tensor | None = None, dv: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
+    """Gradient of cross_attn: from dout and the forward call's inputs and results returns (dq, dk, dv), dk and dv
+    summed over the query heads that share a key head. Rows of no sequence are 0 in the tensors the call
+    allocates and left as they were in dq, dk, dv buffers it is given."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q must be [Tq, Hq, D] and k, v [Tk, Hkv, D]")
+    Tq, Hq, D = q.shape
+    Tk, Hkv = k.shape[0], k.shape[1]
+    qs, ks, vs = _tok_stride(q, "q", Hq, D), _tok_stride(k, "k", Hkv, D), _tok_stride(v, "v", Hkv, D, Tk)
+    dos, os_ = _tok_stride(dout, "dout", Hq, D, Tq), _tok_stride(out, "out", Hq, D, Tq)
+    _lse_ok(lse, Tq, Hq)
+    B = _cross_lists(cu_q, cu_k, k_len)
+    max_q, max_k = _max_seqlen(max_q), _max_seqlen(max_k)
+    with _on(stream, dout, q, k, v, out, lse, cu_q, cu_k, k_len, dq, dk, dv, workspace, status) as s:
+        nq, nk = Tq * Hq * D, Tk * Hkv * D
+        sizes = [n for n, t in ((nq, dq), (nk, dk), (nk, dv)) if t is None]
+        if sizes:      # one zeroed block for all of them
+            with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+                made = torch.zeros(sum(sizes), dtype=q.dtype, device=q.device).split(sizes)
+            made = list(made)
+            dq = made.pop(0).view(Tq, Hq, D) if dq is None else dq
+            dk = made.pop(0).view(Tk, Hkv, D) if dk is None else dk
+            dv = made.pop(0).view(Tk, Hkv, D) if dv is None else dv
+        dqs, dks, dvs = (_tok_stride(dq, "dq", Hq, D, Tq), _tok_stride(dk, "dk", Hkv, D, Tk),
+                         _tok_stride(dv, "dv", Hkv, D, Tk))
+        if workspace is None:
+            workspace = _workspace(None, cross_attn_bwd_workspace_size(Tq, Tk, Hq, Hkv, D, B, max_q, max_k), q.device,
+                                   stream)
+        _check(lib().vit_cross_attn_bwd(_ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), Tq, Tk, Hq, Hkv,
+                                        D, dos, qs, ks, vs, os_, _ptr(cu_q), _ptr(cu_k), _ptr(k_len), B, max_q, max_k,
+                                        float(scale) if scale is not None else 0.0, _ptr(dq), _ptr(dk), _ptr(dv), dqs,
+                                        dks, dvs, _ptr(workspace), _bytes(workspace), _ptr(status), s),
+               "vit_cross_attn_bwd")
+    return dq, dk, dv
 
 
 RES_BF16, RES_FP32 = 0, 1

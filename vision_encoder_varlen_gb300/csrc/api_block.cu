@@ -280,6 +280,74 @@ vit_status_t vit_cross_attn(const void *q, const void *k, const void *v, int64_t
     return from_cuda(e);
 }
 
+size_t vit_cross_attn_bwd_workspace_size(int64_t Tq, int64_t Tk, int Hq, int Hkv, int D, int B, int max_q, int max_k)
+{
+    if (cross_sizes(Tq, Tk, Hq, Hkv, D, B, &max_q, &max_k) != VIT_OK) return 0;
+    const GradPlan p = grad_plan(Tq, Tk, B, Hq, Hkv, D, max_q, max_k);
+    return p.max_dq >= ((int64_t)1 << 31) || p.max_dkv >= ((int64_t)1 << 31) ? 0 : p.bytes;
+}
+
+vit_status_t vit_cross_attn_bwd(const void *dout, const void *q, const void *k, const void *v, const void *out,
+                                const float *lse, int64_t Tq, int64_t Tk, int Hq, int Hkv, int D, int64_t dout_stride,
+                                int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t out_stride,
+                                const int32_t *cu_q, const int32_t *cu_k, const int32_t *k_len, int B, int max_q,
+                                int max_k, float scale, void *dq, void *dk, void *dv, int64_t dq_stride,
+                                int64_t dk_stride, int64_t dv_stride, void *workspace, size_t workspace_bytes,
+                                int32_t *status_dev, vit_stream_t stream)
+{
+    TraceRange trace("vit_cross_attn_bwd");
+    vit_status_t st = cross_sizes(Tq, Tk, Hq, Hkv, D, B, &max_q, &max_k);
+    if (st != VIT_OK) return st;
+    if (B == 0 || (Tq == 0 && Tk == 0)) return VIT_OK;
+    // with no rows on one side nothing of it is read: the other side's address stands in for the maps
+    if (Tq == 0) {
+        q = dout = out = k;
+        q_stride = dout_stride = out_stride = (int64_t)Hq * D;
+    }
+    st = check_cross(q, k, v, Tk, Hq, Hkv, D, q_stride, k_stride, v_stride, cu_q, cu_k, k_len, scale);
+    if (st != VIT_OK) return st;
+    if (!workspace || (Tq > 0 && (!dout || !out || !lse || !dq)) || (Tk > 0 && (!dk || !dv))) return VIT_ERR_NULL_POINTER;
+    const int64_t nq = (int64_t)Hq * D, nk = (int64_t)Hkv * D;
+    if (!stride_ok(dout_stride, nq) || !stride_ok(out_stride, nq) || (Tq > 0 && !stride_ok(dq_stride, nq)) ||
+        (Tk > 0 && (!stride_ok(dk_stride, nk) || !stride_ok(dv_stride, nk))))
+        return VIT_ERR_BAD_STRIDE;
+    if (!aligned16(dout) || !aligned16(out) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv) ||
+        ((uintptr_t)lse & 3u) || !aligned16(workspace))
+        return VIT_ERR_MISALIGNED;
+    const size_t need = vit_cross_attn_bwd_workspace_size(Tq, Tk, Hq, Hkv, D, B, max_q, max_k);
+    if (need == 0) return VIT_ERR_BAD_SHAPE;
+    if (workspace_bytes < need) return VIT_ERR_WORKSPACE_TOO_SMALL;
+    int sms = 0;
+    st = check_device(&sms);
+    if (st != VIT_OK) return st;
+    CrossGradArgs a{};
+    a.f.q = q;
+    a.f.k = Tk > 0 ? k : q;
+    a.f.v = Tk > 0 ? v : q;
+    a.f.k_stride = Tk > 0 ? k_stride : nk;
+    a.f.v_stride = Tk > 0 ? v_stride : nk;
+    a.f.out = const_cast<void *>(out);
+    a.f.lse = const_cast<float *>(lse);
+    a.f.Hq = Hq;
+    a.f.Hk = Hkv;
+    a.f.D = D;
+    a.f.q_stride = q_stride;
+    a.f.out_stride = out_stride;
+    a.f.scale_log2 = (scale <= 0.f ? 1.0f / sqrtf((float)D) : scale) * 1.4426950408889634f;
+    a.f.segs = CrossSegs{cu_q, cu_k, k_len, B, Tq, Tk, max_q, max_k};
+    a.f.workspace = workspace;
+    a.f.status = status_dev;
+    a.dout = dout;
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    a.dout_stride = dout_stride;
+    a.dq_stride = dq_stride;
+    a.dk_stride = dk_stride;
+    a.dv_stride = dv_stride;
+    return from_cuda(launch_cross_grad(a, grad_plan(Tq, Tk, B, Hq, Hkv, D, max_q, max_k), sms, (cudaStream_t)stream));
+}
+
 static vit_status_t check_norm(int64_t T, int C, int res_type, const void *gate, int64_t gate_stride, float scale,
                                float eps)
 {

@@ -107,4 +107,32 @@ cudaError_t launch_cross_long(const CrossArgs &a, const CrossLong &cx, const WsH
 cudaError_t launch_cross_tile_join(const CrossArgs &a, const LongPlan &p, const CrossLong &cx, const WsHeader *hdr,
                                    const CrossTile *tiles, cudaStream_t stream);
 
+// ---- gradient
+
+// Work item of a gradient pass. dk, dv: the 128 keys from r0 on (below r1) of key head `head`, over
+// the queries [l0, l0 + ln) of all its heads; dq: the 128 / P tokens from r0 on of P heads, over the
+// keys [l0, l0 + ln). The loop's tiles [j0, j1) are this item's; j0 = j1: nothing to add up.
+struct GradItem {
+    int r0, r1, l0, ln;
+    int head, j0, j1;
+    int slot;                     // place of the partial sums when the loop was cut, or -1
+};
+static_assert(sizeof(GradItem) == 32, "two 16-byte words");
+
+struct GradPlan {
+    int lg_pack;
+    int64_t max_dq, max_dkv;      // bounds of the two item lists
+    size_t off_dq, off_dkv, off_stats, bytes;   // workspace layout; the two item counts are at 0
+};
+struct CrossGradArgs {
+    CrossArgs f;                  // the forward call: its inputs, out and lse (read), workspace of this call
+    const void *dout;             // bf16 [Tq, Hq, D]
+    void *dq, *dk, *dv;
+    int64_t dout_stride, dq_stride, dk_stride, dv_stride;
+};
+GradPlan grad_plan(int64_t Tq, int64_t Tk, int B, int Hq, int Hk, int D, int max_q, int max_k);
+int cross_grad_bn(int D);
+cudaError_t launch_grad_schedule(const CrossGradArgs &a, const GradPlan &p, cudaStream_t stream);
+cudaError_t launch_cross_grad(const CrossGradArgs &a, const GradPlan &p, int num_sms, cudaStream_t stream);
+
 }  // namespace vit

@@ -1,0 +1,580 @@
+// Gradient of cross attention on the 5th-generation tensor cores (tcgen05 + TMEM + TMA).
+//
+//   p_ij  = exp(scale q_i k_j - lse_i)                 delta_i = sum_d do_i o_i
+//   dv_j  = sum_i p_ij do_i                            ds_ij = p_ij (do_i v_j - delta_i)
+//   dq_i  = scale sum_j ds_ij k_j                      dk_j = scale sum_i ds_ij q_i
+// summed over the query heads that share a key head for dk and dv. P and dS are rounded to bf16 for
+// their products (as P is in the forward pass), everything else is fp32.
+//
+// dq sums over keys and dk, dv sum over queries, so one pass over the tiles would have to add one of
+// them up in memory with fp32 atomics, whose order changes the result. Instead there are two passes,
+// each keeping its own sums in TMEM and recomputing S and dP (7 products instead of 5):
+//   dk, dv   a tile of 128 keys stays, the queries of its heads stream by:
+//            S^T = K Q^T, dP^T = V dO^T (SS MMAs), dV += P^T dO, dK += dS^T Q (TS MMAs: P and dS in TMEM)
+//   dq       a tile of 128 query rows stays, the keys stream by:
+//            S = Q K^T, dP = dO V^T, dQ += dS K
+// which is the same kernel: two resident tiles X1, X2, two streamed ones Y1, Y2, S = X1 Y1^T,
+// dP = X2 Y2^T, A1 += dS Y1 and (dk, dv only) A2 += P Y2. Statistics go by the streamed side in the
+// first pass (read from shared memory) and by the row in the second.
+//
+// Roles of a block (384 threads, one per SM, persistent over the item list):
+//   warp 0       TMA producer: X tiles (two buffers) and a ring of Y tiles of BN rows
+//   warp 1       TMEM owner and MMA issuer: acc(j) as soon as P, dS of tile j are stored, then S, dP of
+//                tile j + 2 into the TMEM stage that tile j leaves (MMAs of one thread run in order)
+//   warps 4-7, 8-11  the two softmax groups take alternate tiles: S, dP -> registers -> P, dS -> TMEM
+//                over their own S and dP columns; at an item's end they write dk and dv (or half of dq each)
+// TMEM (512 columns): A1 | A2 | two stages of S and dP (BN columns each). BN is 64 at head_dim 128 and 80
+// below: 2 D + 4 BN <= 512, and both S and dP of a tile fit a thread's registers.
+// All tiles use slabs of W columns with a 2 W-byte swizzle, so that the same bytes serve as a K-major
+// operand (of S and dP, reduced over D) and as an MN-major one (of the sums, reduced over rows).
+// Streamed rows past the sequence's end enter the sums with P = dS = 0 and are zeroed in shared memory
+// first (0 * NaN is NaN), the last 16-row step included.
+#include <type_traits>
+
+#include "cross.h"
+#include "sm100.cuh"
+
+namespace vit {
+namespace {
+
+using namespace sm100;
+
+constexpr int kThreads = 384;
+constexpr int kLaunchRegs = 168;
+constexpr int kCtrlRegs = 88;
+constexpr int kSoftmaxRegs = 208;
+static_assert(128 * kCtrlRegs + 256 * kSoftmaxRegs <= kThreads * kLaunchRegs, "register split exceeds the launch pool");
+constexpr int BM = 128;
+constexpr long long kWaitBudget = 4000000000ll;
+constexpr int kMaxY = 4;
+
+template <int D> struct GradCfg {
+    static constexpr int BN = D == 128 ? 64 : 80;          // streamed rows per tile
+    static constexpr int W = D % 64 == 0 ? 64 : D % 32 == 0 ? 32 : 16;   // columns of a slab
+    static constexpr int SW = 2 * W;                       // its swizzle in bytes
+    static constexpr int NS = D / W;                       // slabs
+    static constexpr int X_SLAB = BM * SW, Y_SLAB = BN * SW;
+    static constexpr int X_TILE = NS * X_SLAB, Y_TILE = NS * Y_SLAB;
+    static constexpr int Y_PAIR = (2 * Y_TILE + 1023) / 1024 * 1024;
+    static constexpr int NY = D == 128 ? 3 : 4;            // Y ring slots
+    static constexpr int OFF_Y = 4 * X_TILE;               // two X buffers of two tiles
+    static constexpr int DATA = OFF_Y + NY * Y_PAIR;
+    static constexpr int SMEM = DATA + 1024 > 118 * 1024 ? DATA + 1024 : 118 * 1024;   // one block per SM
+    static constexpr int LAYOUT = SW == 128 ? 2 : SW == 64 ? 4 : 6;
+    static constexpr int TA1 = 0, TA2 = D, TSTAGE = 2 * D; // TMEM columns; stage s: S at TSTAGE + 2 BN s, dP BN further
+    static_assert(TSTAGE + 4 * BN <= 512, "TMEM budget");
+    static_assert(SMEM + 1280 <= 227 * 1024, "shared memory per block, with the statistics and barriers");
+    static_assert(X_TILE % 1024 == 0 && Y_SLAB % (8 * SW) == 0 && Y_TILE % (8 * SW) == 0, "slabs start on swizzle atoms");
+    static_assert(NY <= kMaxY && BN % 16 == 0, "tile shapes");
+};
+
+struct Bars {
+    uint64_t x_full[2], x_empty[2], y_full[kMaxY], y_empty[kMaxY];
+    uint64_t s_full[2], p_full[2], stat[2], acc_done, acc_free, drain;
+};
+
+__device__ __forceinline__ uint32_t bar_addr(const uint64_t &b) { return smem_addr(&b); }
+
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.ftz.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+struct Grad {
+    const GradItem *items;
+    const int32_t *n_items;
+    const float2 *stats;          // [Tq, Hq] {-lse log2(e), -delta}
+    __nv_bfloat16 *out1, *out2;   // dk, dv; or dq
+    int64_t out1_stride, out2_stride;
+    int Hq, group, lg_pack;
+    float scale, scale_log2;
+    float *part;                  // partial sums of items whose loop was cut
+    int32_t *status;
+};
+
+template <int D, bool DKV>
+__global__ void __launch_bounds__(kThreads, 1)
+cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_constant__ CUtensorMap tm_x2,
+                  const __grid_constant__ CUtensorMap tm_y1, const __grid_constant__ CUtensorMap tm_y2, const Grad p)
+{
+    using C = GradCfg<D>;
+    constexpr int BN = C::BN, NY = C::NY, W = C::W;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *base = reinterpret_cast<unsigned char *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    __shared__ Bars bars;
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_abort;
+    __shared__ __align__(16) float s_stat[2][2][BN];       // [group][-lse2 | -delta][column]
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n_items = *p.n_items;
+    if (threadIdx.x == 0) {
+        s_abort = 0;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar_addr(bars.x_full[i]), 1);
+            mbar_init(bar_addr(bars.x_empty[i]), 1);
+            mbar_init(bar_addr(bars.s_full[i]), 1);
+            mbar_init(bar_addr(bars.p_full[i]), 4);
+            mbar_init(bar_addr(bars.stat[i]), 4);        // the four warps of a group
+        }
+        for (int i = 0; i < NY; ++i) {
+            mbar_init(bar_addr(bars.y_full[i]), 1);
+            mbar_init(bar_addr(bars.y_empty[i]), 1);
+        }
+        mbar_init(bar_addr(bars.acc_done), 1);
+        mbar_init(bar_addr(bars.acc_free), 8);
+        mbar_init(bar_addr(bars.drain), 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_addr(&s_tmem), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+
+    auto wait = [&](const uint64_t &b, uint32_t parity) -> bool {
+        if (mbar_wait(bar_addr(b), parity, (const volatile int *)&s_abort, kWaitBudget)) return true;
+        if (!s_abort) {
+            s_abort = 1;
+            report_error(p.status, VIT_ERR_TIMEOUT);
+        }
+        return false;
+    };
+    auto wait_warp = [&](const uint64_t &b, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, wait(b, parity)) != 0;
+    };
+    // tokens of a streamed tile; tiles of an item; streamed rows of tile j inside the sequence
+    const int y_tok = DKV ? BN >> p.lg_pack : BN;
+    auto valid_rows = [&](const GradItem &it, int j) -> int {
+        if constexpr (DKV) {
+            const int nt = (it.ln + y_tok - 1) / y_tok;
+            return min(y_tok, it.ln - j % nt * y_tok) << p.lg_pack;
+        } else {
+            return min(BN, it.ln - j * BN);
+        }
+    };
+
+    if (warp < 4) regs_dec<kCtrlRegs>();
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            tma_prefetch_desc(&tm_x1);
+            tma_prefetch_desc(&tm_x2);
+            tma_prefetch_desc(&tm_y1);
+            tma_prefetch_desc(&tm_y2);
+            uint32_t xc = 0, yc = 0;
+            bool ok = true;
+            for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
+                const GradItem it = p.items[i];
+                if (it.j1 <= it.j0) continue;
+                const uint32_t xb = xc & 1;
+                if (xc >= 2 && !(ok = wait(bars.x_empty[xb], (xc / 2 - 1) & 1))) break;
+                mbar_arrive_expect_tx(bar_addr(bars.x_full[xb]), 2 * C::X_TILE);
+#pragma unroll
+                for (int s = 0; s < C::NS; ++s) {
+                    unsigned char *x = base + xb * 2 * C::X_TILE + s * C::X_SLAB;
+                    tma_load_3d(smem_addr(x), &tm_x1, W * s, it.head, it.r0, bar_addr(bars.x_full[xb]));
+                    tma_load_3d(smem_addr(x + C::X_TILE), &tm_x2, W * s, it.head, it.r0, bar_addr(bars.x_full[xb]));
+                }
+                ++xc;
+                const int nt = DKV ? (it.ln + y_tok - 1) / y_tok : 0;
+                for (int j = it.j0; j < it.j1; ++j, ++yc) {
+                    const int s = yc % NY;
+                    if (yc >= (uint32_t)NY && !(ok = wait(bars.y_empty[s], (yc / NY - 1) & 1))) break;
+                    int head, row;
+                    if constexpr (DKV) {
+                        head = it.head * p.group + ((j / nt) << p.lg_pack);
+                        row = it.l0 + j % nt * y_tok;
+                    } else {
+                        head = it.head / p.group;
+                        row = it.l0 + j * BN;
+                    }
+                    mbar_arrive_expect_tx(bar_addr(bars.y_full[s]), 2 * C::Y_TILE);
+#pragma unroll
+                    for (int c = 0; c < C::NS; ++c) {
+                        unsigned char *y = base + C::OFF_Y + s * C::Y_PAIR + c * C::Y_SLAB;
+                        tma_load_3d(smem_addr(y), &tm_y1, W * c, head, row, bar_addr(bars.y_full[s]));
+                        tma_load_3d(smem_addr(y + C::Y_TILE), &tm_y2, W * c, head, row, bar_addr(bars.y_full[s]));
+                    }
+                }
+            }
+            if (!ok) {
+                // let every copy already issued land before this block's shared memory is released
+                const int never = 0;
+                for (uint32_t k = xc > 2 ? xc - 2 : 0; k < xc; ++k)
+                    mbar_wait(bar_addr(bars.x_full[k & 1]), (k / 2) & 1, &never, 20000000ll);
+                for (uint32_t k = yc > (uint32_t)NY ? yc - NY : 0; k < yc; ++k)
+                    mbar_wait(bar_addr(bars.y_full[k % NY]), (k / NY) & 1, &never, 20000000ll);
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer (lane 0; all lanes zero tails)
+        constexpr uint32_t ID_S = idesc_bf16(128, BN, 0, 0), ID_ACC = idesc_bf16(128, D, 0, 1);
+        const uint32_t a_x = smem_addr(base), a_y = smem_addr(base + C::OFF_Y);
+        const uint64_t dx0 = smem_desc(a_x, 16, 8 * C::SW, C::LAYOUT), dy0 = smem_desc(a_y, 16, 8 * C::SW, C::LAYOUT);
+        const uint64_t dm0 = smem_desc(a_y, C::Y_SLAB, 8 * C::SW, C::LAYOUT);      // the same tile, MN-major
+        uint32_t xc = 0, u0 = 0;                             // items and tiles before this item
+        bool ok = true;
+        // S and dP of tile j (global count u0 + j - j0) into its stage
+        auto products = [&](const GradItem &it, int j, uint32_t xb) -> bool {
+            const uint32_t u = u0 + (j - it.j0), s = u % NY, st = u & 1;
+            if (!(ok = wait_warp(bars.y_full[s], (u / NY) & 1))) return false;
+            const int valid = valid_rows(it, j);
+            if (valid & 15) {                                // rows past the end, up to the 16-row step's end
+                unsigned char *y = base + C::OFF_Y + s * C::Y_PAIR;
+                const int n = 16 - (valid & 15);
+                for (int x = lane; x < n * C::NS * (W / 8) * (DKV ? 2 : 1); x += 32) {
+                    const int r = valid + x % n, c = x / n % (W / 8), sl = x / n / (W / 8);   // every 16 bytes of the row
+                    *reinterpret_cast<uint4 *>(y + (sl / C::NS) * C::Y_TILE + (sl % C::NS) * C::Y_SLAB + r * C::SW +
+                                               16 * c) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            tc_fence_after();
+            if (lane == 0) {
+                const uint32_t tS = tmem + C::TSTAGE + st * 2 * BN;
+                const uint64_t dx = dx0 + ((xb * 2 * C::X_TILE) >> 4), dy = dy0 + ((s * C::Y_PAIR) >> 4);
+#pragma unroll
+                for (int w = 0; w < 2; ++w)
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        constexpr int PER = W / 16;
+                        const uint32_t ox = w * C::X_TILE + (kk / PER) * C::X_SLAB + (kk % PER) * 32;
+                        const uint32_t oy = w * C::Y_TILE + (kk / PER) * C::Y_SLAB + (kk % PER) * 32;
+                        mma_ss(tS + w * BN, dx + (ox >> 4), dy + (oy >> 4), ID_S, kk > 0 ? 1u : 0u);
+                    }
+                mma_commit(bar_addr(bars.s_full[st]));
+                if (j + 1 == it.j1) mma_commit(bar_addr(bars.x_empty[xb]));
+            }
+            __syncwarp();
+            return true;
+        };
+        for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
+            const GradItem it = p.items[i];
+            const int n = it.j1 - it.j0;
+            if (n <= 0) continue;
+            const uint32_t xb = xc & 1;
+            if (!(ok = wait_warp(bars.x_full[xb], (xc / 2) & 1))) break;
+            if (!products(it, it.j0, xb)) break;
+            if (n > 1 && !products(it, it.j0 + 1, xb)) break;
+            for (int j = it.j0; j < it.j1; ++j) {
+                const uint32_t u = u0 + (j - it.j0), s = u % NY, st = u & 1;
+                if (j == it.j0 && xc > 0 && !(ok = wait_warp(bars.acc_free, (xc - 1) & 1))) break;
+                if (!(ok = wait_warp(bars.p_full[st], (u / 2) & 1))) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t tP = tmem + C::TSTAGE + st * 2 * BN, tDS = tP + BN;
+                    const uint64_t dm = dm0 + ((s * C::Y_PAIR) >> 4);
+                    const int steps = (valid_rows(it, j) + 15) >> 4;
+                    const uint32_t acc = j > it.j0 ? 1u : 0u;
+                    if constexpr (DKV)
+                        for (int kk = 0; kk < steps; ++kk)
+                            mma_ts(tmem + C::TA2, tP + kk * 8, dm + ((C::Y_TILE + kk * 16 * C::SW) >> 4), ID_ACC,
+                                   kk > 0 ? 1u : acc);
+                    for (int kk = 0; kk < steps; ++kk)
+                        mma_ts(tmem + C::TA1, tDS + kk * 8, dm + ((kk * 16 * C::SW) >> 4), ID_ACC, kk > 0 ? 1u : acc);
+                    mma_commit(bar_addr(bars.y_empty[s]));
+                    if (j + 1 == it.j1) mma_commit(bar_addr(bars.acc_done));
+                }
+                __syncwarp();
+                // the stage is free: its softmax group has read it, and the MMAs above run first
+                if (j + 2 < it.j1 && !products(it, j + 2, xb)) break;
+            }
+            u0 += n;
+            ++xc;
+        }
+        if (lane == 0) {
+            // nothing this thread issued may still be running when TMEM is freed
+            mma_commit(bar_addr(bars.drain));
+            mbar_wait(bar_addr(bars.drain), 0, (const volatile int *)&s_abort, ok ? kWaitBudget : 200000000ll);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ softmax groups
+        regs_inc<kSoftmaxRegs>();
+        const int grp = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane, gt = threadIdx.x - 128 - 128 * grp;
+        const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
+        uint32_t u0 = 0, xc = 0;                              // tiles and items with tiles before this item
+        bool ok = true;
+        for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
+            const GradItem it = p.items[i];
+            const int n = max(0, it.j1 - it.j0);
+            // the row of the output that this lane holds
+            int o_row, o_head;
+            if constexpr (DKV) {
+                o_row = it.r0 + row;
+                o_head = it.head;
+            } else {
+                o_row = it.r0 + (row >> p.lg_pack);
+                o_head = it.head + (row & ((1 << p.lg_pack) - 1));
+            }
+            const bool exists = o_row < it.r1;
+            float2 st_row = make_float2(0.f, 0.f);
+            if constexpr (!DKV) {
+                if (exists && n > 0) st_row = p.stats[(int64_t)o_row * p.Hq + o_head];
+            }
+            const int nt = DKV ? (it.ln + y_tok - 1) / y_tok : 0;
+            for (int j = it.j0 + (int)((u0 ^ (uint32_t)grp) & 1); j < it.j1; j += 2) {
+                const uint32_t u = u0 + (j - it.j0), st = u & 1;
+                const int valid = valid_rows(it, j);
+                const float *nl = s_stat[grp][0], *nd = s_stat[grp][1];
+                if constexpr (DKV) {
+                    // the statistics of the tile's columns, fetched while S is still being computed and stored once
+                    // every warp of the group has finished its previous tile (the group's tiles share a stage)
+                    float2 v = make_float2(0.f, 0.f);
+                    if (gt < BN) {
+                        if (gt < valid) {
+                            const int64_t tok = it.l0 + j % nt * y_tok + (gt >> p.lg_pack);
+                            const int head = it.head * p.group + ((j / nt) << p.lg_pack) + (gt & ((1 << p.lg_pack) - 1));
+                            v = p.stats[tok * p.Hq + head];
+                        }
+                    }
+                    if (u >= 2 && !(ok = wait_warp(bars.p_full[st], (u / 2 - 1) & 1))) break;
+                    if (gt < BN) {
+                        s_stat[grp][0][gt] = v.x;
+                        s_stat[grp][1][gt] = v.y;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_addr(bars.stat[grp]));
+                    if (!(ok = wait_warp(bars.stat[grp], (u / 2) & 1))) break;
+                }
+                if (!(ok = wait_warp(bars.s_full[st], (u / 2) & 1))) break;
+                tc_fence_after();
+                const uint32_t tS = t_lane + C::TSTAGE + st * 2 * BN, tD = tS + BN;
+                uint32_t sr[BN], dr[BN];
+#pragma unroll
+                for (int c = 0; c < BN; c += 16) tmem_ld16(tS + c, *reinterpret_cast<uint32_t(*)[16]>(sr + c));
+#pragma unroll
+                for (int c = 0; c < BN; c += 16) tmem_ld16(tD + c, *reinterpret_cast<uint32_t(*)[16]>(dr + c));
+                tmem_wait_ld();
+                reg_fence(sr);
+                reg_fence(dr);
+                const uint64_t sc2 = f2_splat(p.scale_log2);
+                const uint64_t nl_row = f2_splat(st_row.x), nd_row = f2_splat(st_row.y);
+#pragma unroll
+                for (int c = 0; c < BN; c += 2) {
+                    uint64_t l2 = nl_row, d2 = nd_row;
+                    if constexpr (DKV) {
+                        l2 = *reinterpret_cast<const uint64_t *>(nl + c);
+                        d2 = *reinterpret_cast<const uint64_t *>(nd + c);
+                    }
+                    float x0, x1;
+                    f2_split(f2_fma(f2_from_u32(sr[c], sr[c + 1]), sc2, l2), x0, x1);
+                    float p0 = ex2(x0), p1 = ex2(x1);
+                    uint64_t pp;
+                    asm("mov.b64 %0, {%1, %2};\n" : "=l"(pp) : "f"(p0), "f"(p1));
+                    float g0, g1;
+                    f2_split(f2_mul(f2_add(f2_from_u32(dr[c], dr[c + 1]), d2), pp), g0, g1);
+                    sr[c / 2] = pack_bf16x2(p0, p1);
+                    dr[c / 2] = pack_bf16x2(g0, g1);
+                }
+                if (valid < BN) {                             // columns past the end: exactly 0, whatever was there
+#pragma unroll
+                    for (int c = 0; c < BN; c += 2) {
+                        const uint32_t keep = c + 1 < valid ? 0xffffffffu : c < valid ? 0x0000ffffu : 0u;
+                        sr[c / 2] &= keep;
+                        dr[c / 2] &= keep;
+                    }
+                }
+                if constexpr (DKV) {
+#pragma unroll
+                    for (int c = 0; c < BN / 2; c += 8) tmem_st8(tS + c, *reinterpret_cast<const uint32_t(*)[8]>(sr + c));
+                }
+#pragma unroll
+                for (int c = 0; c < BN / 2; c += 8) tmem_st8(tD + c, *reinterpret_cast<const uint32_t(*)[8]>(dr + c));
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_addr(bars.p_full[st]));
+            }
+            if (!ok) break;
+            u0 += n;
+            // ---- the item's sums: group 0 writes dk, group 1 dv; of dq each writes half of the columns
+            constexpr int COLS = DKV ? D : D / 2;
+            const int col0 = DKV ? 0 : grp * COLS;
+            const uint32_t tA = t_lane + (DKV && grp ? C::TA2 : C::TA1) + col0;
+            __nv_bfloat16 *dst = DKV && grp ? p.out2 + (int64_t)o_row * p.out2_stride
+                                            : p.out1 + (int64_t)o_row * p.out1_stride;
+            dst += (int64_t)o_head * D + col0;
+            const float f = DKV && grp ? 1.f : p.scale;
+            if (n > 0) {
+                if (!(ok = wait_warp(bars.acc_done, xc & 1))) break;
+                ++xc;
+                tc_fence_after();
+            }
+            float *part = p.part + ((int64_t)it.slot * 2 + (DKV ? grp : 0)) * (BM * D) + row * D + col0;
+#pragma unroll
+            for (int c = 0; c < COLS; c += 8) {
+                uint32_t r[8];
+                if (n > 0) {
+                    tmem_ld8(tA + c, r);
+                    tmem_wait_ld();
+                    reg_fence(r);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) r[e] = 0u;
+                }
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(r[e]) * f;
+                if (exists) {
+                    if (it.slot < 0) {
+                        *reinterpret_cast<uint4 *>(dst + c) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                                         pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+                    } else {
+                        *reinterpret_cast<float4 *>(part + c) = make_float4(v[0], v[1], v[2], v[3]);
+                        *reinterpret_cast<float4 *>(part + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
+                    }
+                }
+            }
+            if (n > 0) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_addr(bars.acc_free));
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// {-lse log2(e), -delta} of every (token, head): D / 8 lanes per row, 16 bytes of o and do each.
+template <int D>
+__global__ void __launch_bounds__(256)
+cross_stats_kernel(const __nv_bfloat16 *__restrict__ out, const __nv_bfloat16 *__restrict__ dout,
+                   const float *__restrict__ lse, float2 *__restrict__ stats, int64_t rows, int Hq, int64_t out_stride,
+                   int64_t dout_stride)
+{
+    constexpr int CH = D / 8, R = 32 / CH;
+    const int lane = threadIdx.x & 31, g = lane / CH, c = lane % CH;
+    const int64_t warp = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5, n_warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
+    for (int64_t r0 = warp * R; r0 < rows; r0 += n_warps * R) {
+        const int64_t r = r0 + g;
+        const bool live = g < R && r < rows;
+        float s = 0.f;
+        if (live) {
+            const int64_t t = r / Hq;
+            const int h = (int)(r - t * Hq);
+            float a[8], b[8];
+            rope::unpack8(*reinterpret_cast<const uint4 *>(out + t * out_stride + (int64_t)h * D + 8 * c), a);
+            rope::unpack8(*reinterpret_cast<const uint4 *>(dout + t * dout_stride + (int64_t)h * D + 8 * c), b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s = fmaf(a[e], b[e], s);
+        }
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) sum += __shfl_sync(0xffffffffu, s, (g * CH + i) & 31);
+        if (live && c == 0) stats[r] = make_float2(-lse[r] * 1.4426950408889634f, -sum);
+    }
+}
+
+// ------------------------------------------------------------------ host side
+
+bool tile_map(CUtensorMap *m, const void *ptr, int64_t T, int H, int D, int64_t stride, int w, int pack, int rows)
+{
+    const uint64_t dims[3] = {(uint64_t)D, (uint64_t)H, (uint64_t)(T > 0 ? T : 1)};
+    const uint64_t strides[2] = {(uint64_t)D * 2, (uint64_t)stride * 2};
+    const uint32_t box[3] = {(uint32_t)w, (uint32_t)pack, (uint32_t)(rows / pack)};
+    return encode_tiled_map(m, ptr, 3, dims, strides, box, 2 * w);
+}
+
+template <int D, bool DKV>
+cudaError_t launch_pass(const CrossGradArgs &a, const GradPlan &pl, int num_sms, cudaStream_t stream)
+{
+    using C = GradCfg<D>;
+    const CrossSegs &s = a.f.segs;
+    const int pack = 1 << pl.lg_pack;
+    CUtensorMap q, dq, k, v;              // q and do, then k and v, as the resident or the streamed side
+    const int qr = DKV ? C::BN : BM, kr = DKV ? BM : C::BN;
+    if (!tile_map(&q, a.f.q, s.Tq, a.f.Hq, D, a.f.q_stride, C::W, pack, qr) ||
+        !tile_map(&dq, a.dout, s.Tq, a.f.Hq, D, a.dout_stride, C::W, pack, qr) ||
+        !tile_map(&k, a.f.k, s.Tk, a.f.Hk, D, a.f.k_stride, C::W, 1, kr) ||
+        !tile_map(&v, a.f.v, s.Tk, a.f.Hk, D, a.f.v_stride, C::W, 1, kr))
+        return cudaErrorInvalidValue;
+    auto kern = cross_grad_kernel<D, DKV>;
+    static DeviceOnce once;
+    cudaError_t e = once.run([&] {
+        cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (r != cudaSuccess) return r;
+        // the setmaxnreg split assumes exactly this launch budget
+        cudaFuncAttributes fa;
+        r = cudaFuncGetAttributes(&fa, kern);
+        if (r != cudaSuccess) return r;
+        return (fa.numRegs != kLaunchRegs || fa.maxThreadsPerBlock < kThreads) ? cudaErrorInvalidConfiguration
+                                                                              : cudaSuccess;
+    });
+    if (e != cudaSuccess) return e;
+    char *ws = static_cast<char *>(a.f.workspace);
+    Grad p;
+    p.items = reinterpret_cast<const GradItem *>(ws + (DKV ? pl.off_dkv : pl.off_dq));
+    p.n_items = reinterpret_cast<const int32_t *>(ws) + (DKV ? 1 : 0);
+    p.stats = reinterpret_cast<const float2 *>(ws + pl.off_stats);
+    p.out1 = static_cast<__nv_bfloat16 *>(DKV ? a.dk : a.dq);
+    p.out2 = static_cast<__nv_bfloat16 *>(a.dv);
+    p.out1_stride = DKV ? a.dk_stride : a.dq_stride;
+    p.out2_stride = a.dv_stride;
+    p.Hq = a.f.Hq;
+    p.group = a.f.Hq / a.f.Hk;
+    p.lg_pack = pl.lg_pack;
+    p.scale = a.f.scale_log2 * 0.6931471805599453f;
+    p.scale_log2 = a.f.scale_log2;
+    p.part = nullptr;
+    p.status = a.f.status;
+    const int64_t most = DKV ? pl.max_dkv : pl.max_dq;
+    const unsigned blocks = (unsigned)(most < num_sms ? most : num_sms);
+    if (blocks == 0) return cudaSuccess;
+    LaunchScope scope(DKV ? "cross_grad_dkv" : "cross_grad_dq", stream);
+    if (DKV)
+        kern<<<blocks, kThreads, C::SMEM, stream>>>(k, v, q, dq, p);
+    else
+        kern<<<blocks, kThreads, C::SMEM, stream>>>(q, dq, k, v, p);
+    return cudaGetLastError();
+}
+
+template <int D> cudaError_t launch_d(const CrossGradArgs &a, const GradPlan &pl, int num_sms, cudaStream_t stream)
+{
+    const int64_t rows = a.f.segs.Tq * a.f.Hq;
+    if (rows > 0) {
+        constexpr int per = 8 * (32 / (D / 8));
+        const int64_t want = (rows + per - 1) / per, cap = (int64_t)num_sms * 32;
+        LaunchScope scope("cross_stats", stream);
+        cross_stats_kernel<D><<<(unsigned)(want < cap ? want : cap), 256, 0, stream>>>(
+            static_cast<const __nv_bfloat16 *>(a.f.out), static_cast<const __nv_bfloat16 *>(a.dout), a.f.lse,
+            reinterpret_cast<float2 *>(static_cast<char *>(a.f.workspace) + pl.off_stats), rows, a.f.Hq,
+            a.f.out_stride, a.dout_stride);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    cudaError_t e = launch_pass<D, true>(a, pl, num_sms, stream);
+    if (e != cudaSuccess) return e;
+    return launch_pass<D, false>(a, pl, num_sms, stream);
+}
+
+}  // namespace
+
+int cross_grad_bn(int D) { return D == 128 ? GradCfg<128>::BN : GradCfg<80>::BN; }
+
+cudaError_t launch_cross_grad(const CrossGradArgs &a, const GradPlan &p, int num_sms, cudaStream_t stream)
+{
+    cudaError_t e = launch_grad_schedule(a, p, stream);
+    if (e != cudaSuccess) return e;
+    switch (a.f.D) {
+        case 32: return launch_d<32>(a, p, num_sms, stream);
+        case 64: return launch_d<64>(a, p, num_sms, stream);
+        case 80: return launch_d<80>(a, p, num_sms, stream);
+        case 96: return launch_d<96>(a, p, num_sms, stream);
+        case 128: return launch_d<128>(a, p, num_sms, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace vit
