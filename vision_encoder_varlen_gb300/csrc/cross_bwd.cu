@@ -219,11 +219,12 @@ cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_consta
         const uint64_t dm0 = smem_desc(a_y, C::Y_SLAB, 8 * C::SW, C::LAYOUT);      // the same tile, MN-major
         uint32_t xc = 0, u0 = 0;                             // items and tiles before this item
         bool ok = true;
-        // S and dP of tile j (global count u0 + j - j0) into its stage
-        auto products = [&](const GradItem &it, int j, uint32_t xb) -> bool {
-            const uint32_t u = u0 + (j - it.j0), s = u % NY, st = u & 1;
+        const bool leader = elect_one();
+        auto uni = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+        // S and dP of a tile (global count u, `valid` rows of the sequence) into its stage
+        auto products = [&](uint32_t u, int valid, uint32_t xb, bool last) -> bool {
+            const uint32_t s = u % NY, st = u & 1;
             if (!(ok = wait_warp(bars.y_full[s], (u / NY) & 1))) return false;
-            const int valid = valid_rows(it, j);
             if (valid & 15) {                                // rows past the end, up to the 16-row step's end
                 unsigned char *y = base + C::OFF_Y + s * C::Y_PAIR;
                 const int n = 16 - (valid & 15);
@@ -236,59 +237,75 @@ cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_consta
                 __syncwarp();
             }
             tc_fence_after();
-            if (lane == 0) {
-                const uint32_t tS = tmem + C::TSTAGE + st * 2 * BN;
-                const uint64_t dx = dx0 + ((xb * 2 * C::X_TILE) >> 4), dy = dy0 + ((s * C::Y_PAIR) >> 4);
+            const uint32_t tS = tmem + C::TSTAGE + st * 2 * BN;
+            const uint64_t dx = dx0 + ((xb * 2 * C::X_TILE) >> 4), dy = dy0 + ((s * C::Y_PAIR) >> 4);
+            const uint32_t full = bar_addr(bars.s_full[st]), empty = bar_addr(bars.x_empty[xb]);
+            if (leader) {
 #pragma unroll
-                for (int w = 0; w < 2; ++w)
+                for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
+                    for (int w = 0; w < 2; ++w) {
                         constexpr int PER = W / 16;
                         const uint32_t ox = w * C::X_TILE + (kk / PER) * C::X_SLAB + (kk % PER) * 32;
                         const uint32_t oy = w * C::Y_TILE + (kk / PER) * C::Y_SLAB + (kk % PER) * 32;
                         mma_ss(tS + w * BN, dx + (ox >> 4), dy + (oy >> 4), ID_S, kk > 0 ? 1u : 0u);
                     }
-                mma_commit(bar_addr(bars.s_full[st]));
-                if (j + 1 == it.j1) mma_commit(bar_addr(bars.x_empty[xb]));
+                mma_commit(full);
+                if (last) mma_commit(empty);
             }
             __syncwarp();
             return true;
         };
         for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
             const GradItem it = p.items[i];
-            const int n = it.j1 - it.j0;
+            const int n = uni(it.j1 - it.j0);
             if (n <= 0) continue;
+            // tiles follow one another inside a head pack; the last one of a pack holds `tail` rows
+            const int nt = DKV ? uni((it.ln + y_tok - 1) / y_tok) : (it.ln + BN - 1) / BN;
+            const int tail = uni(valid_rows(it, nt - 1));
+            int pj = uni(it.j0 % nt), aj = pj;               // place in its pack of the next tile to start, to add up
+            auto next = [&](int &x) {
+                const int v = x + 1 == nt ? tail : BN;
+                x = x + 1 == nt ? 0 : x + 1;
+                return v;
+            };
             const uint32_t xb = xc & 1;
             if (!(ok = wait_warp(bars.x_full[xb], (xc / 2) & 1))) break;
-            if (!products(it, it.j0, xb)) break;
-            if (n > 1 && !products(it, it.j0 + 1, xb)) break;
-            for (int j = it.j0; j < it.j1; ++j) {
-                const uint32_t u = u0 + (j - it.j0), s = u % NY, st = u & 1;
-                if (j == it.j0 && xc > 0 && !(ok = wait_warp(bars.acc_free, (xc - 1) & 1))) break;
+            if (!products(u0, next(pj), xb, n == 1)) break;
+            if (n > 1 && !products(u0 + 1, next(pj), xb, n == 2)) break;
+            for (int j = 0; j < n; ++j) {
+                const uint32_t u = u0 + j, s = u % NY, st = u & 1;
+                if (j == 0 && xc > 0 && !(ok = wait_warp(bars.acc_free, (xc - 1) & 1))) break;
+                const int steps = (next(aj) + 15) >> 4;
                 if (!(ok = wait_warp(bars.p_full[st], (u / 2) & 1))) break;
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t tP = tmem + C::TSTAGE + st * 2 * BN, tDS = tP + BN;
-                    const uint64_t dm = dm0 + ((s * C::Y_PAIR) >> 4);
-                    const int steps = (valid_rows(it, j) + 15) >> 4;
-                    const uint32_t acc = j > it.j0 ? 1u : 0u;
-                    if constexpr (DKV)
-                        for (int kk = 0; kk < steps; ++kk)
+                const uint32_t tP = tmem + C::TSTAGE + st * 2 * BN, tDS = tP + BN;
+                const uint64_t dm = dm0 + ((s * C::Y_PAIR) >> 4);
+                const uint32_t acc = j > 0 ? 1u : 0u, empty = bar_addr(bars.y_empty[s]);
+                if (leader) {
+                    auto sums = [&](int kk) {
+                        if constexpr (DKV)
                             mma_ts(tmem + C::TA2, tP + kk * 8, dm + ((C::Y_TILE + kk * 16 * C::SW) >> 4), ID_ACC,
                                    kk > 0 ? 1u : acc);
-                    for (int kk = 0; kk < steps; ++kk)
                         mma_ts(tmem + C::TA1, tDS + kk * 8, dm + ((kk * 16 * C::SW) >> 4), ID_ACC, kk > 0 ? 1u : acc);
-                    mma_commit(bar_addr(bars.y_empty[s]));
-                    if (j + 1 == it.j1) mma_commit(bar_addr(bars.acc_done));
+                    };
+                    if (steps == BN / 16) {
+#pragma unroll
+                        for (int kk = 0; kk < BN / 16; ++kk) sums(kk);
+                    } else {
+                        for (int kk = 0; kk < steps; ++kk) sums(kk);
+                    }
+                    mma_commit(empty);
+                    if (j + 1 == n) mma_commit(bar_addr(bars.acc_done));
                 }
                 __syncwarp();
                 // the stage is free: its softmax group has read it, and the MMAs above run first
-                if (j + 2 < it.j1 && !products(it, j + 2, xb)) break;
+                if (j + 2 < n && !products(u + 2, next(pj), xb, j + 3 == n)) break;
             }
             u0 += n;
             ++xc;
         }
-        if (lane == 0) {
+        if (leader) {
             // nothing this thread issued may still be running when TMEM is freed
             mma_commit(bar_addr(bars.drain));
             mbar_wait(bar_addr(bars.drain), 0, (const volatile int *)&s_abort, ok ? kWaitBudget : 200000000ll);

@@ -115,6 +115,15 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+// One thread of a converged warp, chosen by the hardware: unlike a test of the lane index it tells the
+// compiler that the branch is taken by a single thread, which keeps the operands of the tensor-core
+// instructions below in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+
 // ------------------------------------------------------------------ register reallocation
 
 // Warpgroup-wide (all 4 warps) change of the per-thread register budget.
