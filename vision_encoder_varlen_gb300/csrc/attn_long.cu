@@ -435,7 +435,7 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         // from one global key-tile counter. The two issuers share nothing but the K/V stage
         // barriers (two-arrival k_empty / v_empty / q_empty); each softmax group rewrites its tile's P
         // region only after that tile's previous P.V has completed.
-        if (lane == 0) {
+        if (elect_one()) {
             const int ti = warp - 1;                              // Q tile of this issuer
             constexpr uint32_t ID_QK = idesc_bf16(128, BN, 0, 0);
             constexpr uint32_t ID_PV = idesc_bf16(128, D, 0, 1);
