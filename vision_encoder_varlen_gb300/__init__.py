@@ -73,6 +73,8 @@ class _KernelTime(ctypes.Structure):
 def lib() -> ctypes.CDLL:
     """The loaded libvitattn (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -159,8 +161,8 @@ def _ptr(t: torch.Tensor | None):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _tok_stride(t: torch.Tensor, name: str, H: int, D: int, T: int | None = None) -> int:
-    if t.dim() != 3 or t.shape[1] != H or t.shape[2] != D or (T is not None and t.shape[0] != T):
+def _tok_stride(t: torch.Tensor, name: str, H: int, D: int) -> int:
+    if t.dim() != 3 or t.shape[1] != H or t.shape[2] != D:
         raise ValueError(f"{name} must be [T, {H}, {D}], got {tuple(t.shape)}")
     if t.dtype != torch.bfloat16 or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA bfloat16 tensor")
@@ -424,22 +426,42 @@ def encoder_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: 
 # ---- around a language model's reading of the encoder's states: three-axis rotary positions, cross
 # ---- attention and the gated residual step with its norms, each with its gradient
 
-@contextlib.contextmanager
-def _on(stream, *tensors):
-    """Checks that the tensors given share one CUDA device, makes it current, and yields its stream handle:
-    the caller's, or the device's current one."""
-    given = [t for t in tensors if t is not None]
-    dev = given[0].device
-    for t in given:
-        if not t.is_cuda:
-            raise ValueError("every tensor must be a CUDA tensor")
-        if t.device != dev:
-            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-    with torch.cuda.device(dev):
-        s = torch.cuda.current_stream(dev) if stream is None else stream
-        yield ctypes.c_void_p(s.cuda_stream)
+def _device(*tensors) -> int:
+    """The index of the one CUDA device that every tensor given is on."""
+    dev = -1
+    for t in tensors:
+        if t is not None:
+            i = t.get_device()
+            if dev < 0:
+                dev = i
+            if i < 0:
+                raise ValueError("every tensor must be a CUDA tensor")
+            if i != dev:
+                raise ValueError(f"tensors on different devices: {dev} and {i}")
+    return dev
+
+
+def _call(fn: str, dev: int, stream, *args):
+    """Calls a library function on device `dev`, on the caller's stream or the device's current one (the last
+    argument of every function), and raises on an error."""
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        if stream.device_index != dev:
+            raise ValueError(f"the stream is on device {stream.device_index}, the tensors on {dev}")
+        handle = stream.cuda_stream
+    f = getattr(lib(), fn)
+    if torch.cuda.current_device() == dev:
+        code = f(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            code = f(*args, handle)
+    if code:
+        raise VitError(code, fn)
+
+
+def _addr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
 
 
 def _made(stream, *tensors):
@@ -450,52 +472,63 @@ def _made(stream, *tensors):
                 t.record_stream(stream)
 
 
-def _workspace(workspace, need: int, device, stream) -> torch.Tensor:
-    if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-        _made(stream, workspace)
-    return workspace
+def _scratch(need: int, like: torch.Tensor, stream) -> torch.Tensor:
+    ws = like.new_empty(max(need, 16), dtype=torch.uint8)
+    _made(stream, ws)
+    return ws
 
 
-def _heads(t: torch.Tensor, name: str, T: int, D: int) -> int:
-    """Head count of [T, H, D], its layout checked as the attention calls do."""
-    if t.dim() != 3 or t.shape[0] != T:
-        raise ValueError(f"{name} must be [{T}, H, {D}], got {tuple(t.shape)}")
-    return t.shape[1]
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def _rows3(t: torch.Tensor, name: str, T: int, H: int, D: int) -> int:
+    """Token stride of bf16 [T, H, D] with head stride D."""
+    if tuple(t.shape) != (T, H, D):
+        raise ValueError(f"{name} must be [{T}, {H}, {D}], got {tuple(t.shape)}")
+    if t.dtype is not _BF16:
+        raise ValueError(f"{name} must be a CUDA bfloat16 tensor")
+    st = t.stride()
+    if st[2] != 1 or (st[1] != D and H > 1):
+        raise ValueError(f"{name} needs head stride D and unit element stride (got strides {st})")
+    return st[0] if T > 1 else H * D
+
+
+def _shape3(t: torch.Tensor, name: str):
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [T, H, D], got {tuple(t.shape)}")
+    return t.shape
 
 
 def grid_positions(grid_thw: torch.Tensor, total_tokens: int, *, status: torch.Tensor | None = None, stream=None):
     """Positions of packed images and clips: ([T, 3] int32 (frame, row, column), cu_seqlens [n + 1] int32) from
     a device list of (frames, rows, columns)."""
-    if grid_thw.dtype != torch.int32 or not grid_thw.is_contiguous() or grid_thw.dim() != 2 or grid_thw.shape[1] != 3:
+    if grid_thw.dtype is not _I32 or not grid_thw.is_contiguous() or grid_thw.dim() != 2 or grid_thw.shape[1] != 3:
         raise ValueError("grid_thw must be a contiguous CUDA int32 tensor [n, 3]")
-    with _on(stream, grid_thw, status) as s:
-        pos = torch.empty((int(total_tokens), 3), dtype=torch.int32, device=grid_thw.device)
-        cu = torch.empty(grid_thw.shape[0] + 1, dtype=torch.int32, device=grid_thw.device)
-        _made(stream, pos, cu)
-        _check(lib().vit_grid_positions(_ptr(grid_thw), grid_thw.shape[0], int(total_tokens), _ptr(pos), _ptr(cu),
-                                        _ptr(status), s), "vit_grid_positions")
+    dev, n, T = _device(grid_thw, status), grid_thw.shape[0], int(total_tokens)
+    if T < 0:
+        raise ValueError("total_tokens must not be negative")
+    pos, cu = grid_thw.new_empty((T, 3)), grid_thw.new_empty(n + 1)
+    _made(stream, pos, cu)
+    _call("vit_grid_positions", dev, stream, _addr(grid_thw), n, T, _addr(pos), _addr(cu), _addr(status))
     return pos, cu
-
-
-def _mrope_args(ref, pos_thw, inv_freq, sections, norm_w, eps, cycled, interleaved):
-    T, _, D = ref.shape
-    if pos_thw.dtype != torch.int32 or tuple(pos_thw.shape) != (T, 3) or not pos_thw.is_contiguous():
-        raise ValueError(f"pos_thw must be a contiguous CUDA int32 tensor [{T}, 3]")
-    if inv_freq.dtype != torch.float32 or tuple(inv_freq.shape) != (D // 2,) or not inv_freq.is_contiguous():
-        raise ValueError(f"inv_freq must be a contiguous CUDA float32 tensor [{D // 2}]")
-    if norm_w is not None and (norm_w.dtype != torch.bfloat16 or tuple(norm_w.shape) != (2, D)
-                               or not norm_w.is_contiguous()):
-        raise ValueError(f"norm_w must be a contiguous CUDA bfloat16 tensor [2, {D}]")
-    if len(sections) != 3:
-        raise ValueError("sections must be three pair counts (time, height, width)")
-    sec = (ctypes.c_int * 3)(*(int(x) for x in sections))
-    return (_ptr(pos_thw), _ptr(inv_freq), sec, MROPE_CYCLED if cycled else MROPE_BLOCKED,
-            ROPE_INTERLEAVED if interleaved else ROPE_ROTATE_HALF, _ptr(norm_w), float(eps))
 
 
 MROPE_BLOCKED = 0   # the sections one after the other
 MROPE_CYCLED = 1    # time, height, width in turn
+
+
+def _mrope_args(T, D, pos_thw, inv_freq, sections, norm_w, eps, cycled, interleaved):
+    if pos_thw.dtype is not _I32 or tuple(pos_thw.shape) != (T, 3) or not pos_thw.is_contiguous():
+        raise ValueError(f"pos_thw must be a contiguous CUDA int32 tensor [{T}, 3]")
+    if inv_freq.dtype is not _F32 or tuple(inv_freq.shape) != (D // 2,) or not inv_freq.is_contiguous():
+        raise ValueError(f"inv_freq must be a contiguous CUDA float32 tensor [{D // 2}]")
+    if norm_w is not None and (norm_w.dtype is not _BF16 or tuple(norm_w.shape) != (2, D)
+                               or not norm_w.is_contiguous()):
+        raise ValueError(f"norm_w must be a contiguous CUDA bfloat16 tensor [2, {D}]")
+    if len(sections) != 3:
+        raise ValueError("sections must be three pair counts (time, height, width)")
+    return (_addr(pos_thw), _addr(inv_freq), (ctypes.c_int * 3)(*sections), MROPE_CYCLED if cycled else MROPE_BLOCKED,
+            ROPE_INTERLEAVED if interleaved else ROPE_ROTATE_HALF, _addr(norm_w), float(eps))
 
 
 def qk_norm_mrope(q: torch.Tensor | None, k: torch.Tensor | None, pos_thw: torch.Tensor, inv_freq: torch.Tensor,
@@ -508,30 +541,27 @@ def qk_norm_mrope(q: torch.Tensor | None, k: torch.Tensor | None, pos_thw: torch
     ref = q if q is not None else k
     if ref is None:
         raise ValueError("at least one of q and k is required")
-    if ref.dim() != 3:
-        raise ValueError(f"q and k must be [T, H, D], got {tuple(ref.shape)}")
-    T, _, D = ref.shape
-    args = _mrope_args(ref, pos_thw, inv_freq, sections, norm_w, eps, cycled, interleaved)
+    T, _, D = _shape3(ref, "q and k")
     if inplace:
         q_out, k_out = q, k
-    made = []
+    dev = _device(q, k, q_out, k_out, pos_thw, inv_freq, norm_w)
+    args = _mrope_args(T, D, pos_thw, inv_freq, sections, norm_w, eps, cycled, interleaved)
 
     def half(x, out, name):
         if x is None:
             return None, 0, 0, 0
-        H = _heads(x, name, T, D)
-        xs = _tok_stride(x, name, H, D)
+        H = _shape3(x, name)[1]
+        xs = _rows3(x, name, T, H, D)
         if out is None:
-            out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
-            made.append(out)
-        return out, H, xs, _tok_stride(out, name + "_out", H, D, T)
+            out = x.new_empty((T, H, D))
+            _made(stream, out)
+            return out, H, xs, H * D
+        return out, H, xs, _rows3(out, name + "_out", T, H, D)
 
-    with _on(stream, q, k, q_out, k_out, pos_thw, inv_freq, norm_w) as s:
-        q_out, Hq, qs, qos = half(q, q_out, "q")
-        k_out, Hk, ks, kos = half(k, k_out, "k")
-        _made(stream, *made)
-        _check(lib().vit_qk_norm_mrope(_ptr(q), _ptr(q_out), _ptr(k), _ptr(k_out), T, Hq, Hk, D, qs, qos, ks, kos,
-                                       *args, s), "vit_qk_norm_mrope")
+    q_out, Hq, qs, qos = half(q, q_out, "q")
+    k_out, Hk, ks, kos = half(k, k_out, "k")
+    _call("vit_qk_norm_mrope", dev, stream, _addr(q), _addr(q_out), _addr(k), _addr(k_out), T, Hq, Hk, D, qs, qos, ks,
+          kos, *args)
     return q_out, k_out
 
 
@@ -546,40 +576,37 @@ def qk_norm_mrope_bwd(dq: torch.Tensor | None, dk: torch.Tensor | None, q: torch
     ref = dq if dq is not None else dk
     if ref is None:
         raise ValueError("at least one of dq and dk is required")
-    if ref.dim() != 3:
-        raise ValueError(f"dq and dk must be [T, H, D], got {tuple(ref.shape)}")
-    T, _, D = ref.shape
-    args = _mrope_args(ref, pos_thw, inv_freq, sections, norm_w, eps, cycled, interleaved)
-    made = []
+    T, _, D = _shape3(ref, "dq and dk")
+    dev = _device(dq, dk, q, k, pos_thw, inv_freq, norm_w, workspace)
+    args = _mrope_args(T, D, pos_thw, inv_freq, sections, norm_w, eps, cycled, interleaved)
 
     def half(d, x, name):
         if d is None:
-            return None, 0, 0, 0, 0
-        H = _heads(d, "d" + name, T, D)
-        ds = _tok_stride(d, "d" + name, H, D)
-        xs = 0
+            return None, 0, 0, 0, 0, None
+        H = _shape3(d, "d" + name)[1]
+        ds, xs = _rows3(d, "d" + name, T, H, D), 0
         if norm_w is not None:
             if x is None:
                 raise ValueError(f"{name} is needed for the gradient of its norm")
-            xs = _tok_stride(x, name, H, D, T)
+            xs = _rows3(x, name, T, H, D)
+        else:
+            x = None
         if inplace:
-            return d, H, ds, ds, xs
-        out = torch.empty((T, H, D), dtype=d.dtype, device=d.device)
-        made.append(out)
-        return out, H, ds, H * D, xs
+            return d, H, ds, ds, xs, x
+        out = d.new_empty((T, H, D))
+        _made(stream, out)
+        return out, H, ds, H * D, xs, x
 
-    with _on(stream, dq, dk, q, k, pos_thw, inv_freq, norm_w, workspace) as s:
-        dq_in, Hq, dqs, dqis, qs = half(dq, q, "q")
-        dk_in, Hk, dks, dkis, ks = half(dk, k, "k")
-        dw = None
-        if norm_w is not None:
-            dw = torch.empty((2, D), dtype=torch.float32, device=ref.device)
-            made.append(dw)
-            workspace = _workspace(workspace, int(lib().vit_qk_norm_mrope_bwd_workspace_size(D)), ref.device, stream)
-        _made(stream, *made)
-        _check(lib().vit_qk_norm_mrope_bwd(_ptr(dq), _ptr(dq_in), _ptr(dk), _ptr(dk_in), _ptr(q), _ptr(k), T, Hq, Hk,
-                                           D, dqs, dqis, dks, dkis, qs, ks, *args, _ptr(dw), _ptr(workspace),
-                                           _bytes(workspace), s), "vit_qk_norm_mrope_bwd")
+    dq_in, Hq, dqs, dqis, qs, q = half(dq, q, "q")
+    dk_in, Hk, dks, dkis, ks, k = half(dk, k, "k")
+    dw = None
+    if norm_w is not None:
+        dw = inv_freq.new_empty((2, D))
+        _made(stream, dw)
+        if workspace is None:
+            workspace = _scratch(lib().vit_qk_norm_mrope_bwd_workspace_size(D), ref, stream)
+    _call("vit_qk_norm_mrope_bwd", dev, stream, _addr(dq), _addr(dq_in), _addr(dk), _addr(dk_in), _addr(q), _addr(k),
+          T, Hq, Hk, D, dqs, dqis, dks, dkis, qs, ks, *args, _addr(dw), _addr(workspace), _bytes(workspace))
     return dq_in, dk_in, dw
 
 
@@ -593,9 +620,15 @@ def cross_attn_workspace_size(Tq: int, Tk: int, Hq: int, Hkv: int, D: int, B: in
                                                    int(max_k)))
 
 
+def cross_attn_bwd_workspace_size(Tq: int, Tk: int, Hq: int, Hkv: int, D: int, B: int, max_q: int = 0,
+                                  max_k: int = 0) -> int:
+    return int(lib().vit_cross_attn_bwd_workspace_size(int(Tq), int(Tk), int(Hq), int(Hkv), int(D), int(B),
+                                                       int(max_q), int(max_k)))
+
+
 def _cross_lists(cu_q, cu_k, k_len) -> int:
     for name, t in (("cu_q", cu_q), ("cu_k", cu_k), ("k_len", k_len)):
-        if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous()):
+        if t is not None and (t.dtype is not _I32 or t.dim() != 1 or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous CUDA int32 vector")
     B = cu_q.numel() - 1
     if B < 0 or cu_k.numel() != B + 1 or (k_len is not None and k_len.numel() != B):
@@ -604,7 +637,7 @@ def _cross_lists(cu_q, cu_k, k_len) -> int:
 
 
 def _lse_ok(lse, T, H):
-    if lse.dtype != torch.float32 or tuple(lse.shape) != (T, H) or not lse.is_contiguous():
+    if lse.dtype is not _F32 or tuple(lse.shape) != (T, H) or not lse.is_contiguous():
         raise ValueError(f"lse must be a contiguous CUDA float32 tensor [{T}, {H}]")
 
 
@@ -618,39 +651,29 @@ def cross_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Te
     mask; Hq is a multiple of Hkv. Serves prompts, single new tokens and latent queries. A sequence without
     states gets zeros and lse = -inf. ``max_q`` and ``max_k`` bound the lengths (None: Tq, Tk); tight bounds are
     faster. With ``return_lse`` (or an ``lse`` buffer) returns (out, lse [Tq, Hq] fp32)."""
-    if q.dim() != 3 or k.dim() != 3:
-        raise ValueError("q must be [Tq, Hq, D] and k, v [Tk, Hkv, D]")
-    Tq, Hq, D = q.shape
-    Tk, Hkv = k.shape[0], k.shape[1]
-    qs, ks, vs = _tok_stride(q, "q", Hq, D), _tok_stride(k, "k", Hkv, D), _tok_stride(v, "v", Hkv, D, Tk)
+    Tq, Hq, D = _shape3(q, "q")
+    Tk, Hkv, _ = _shape3(k, "k")
+    dev = _device(q, k, v, cu_q, cu_k, k_len, out, workspace, status, lse)
+    qs, ks, vs = _rows3(q, "q", Tq, Hq, D), _rows3(k, "k", Tk, Hkv, D), _rows3(v, "v", Tk, Hkv, D)
     B = _cross_lists(cu_q, cu_k, k_len)
     max_q, max_k = _max_seqlen(max_q), _max_seqlen(max_k)
-    with _on(stream, q, k, v, cu_q, cu_k, k_len, out, workspace, status, lse) as s:
-        made = []
-        if out is None:
-            out = torch.empty((Tq, Hq, D), dtype=q.dtype, device=q.device)
-            made.append(out)
-        os_ = _tok_stride(out, "out", Hq, D, Tq)
-        if return_lse and lse is None:
-            lse = torch.empty((Tq, Hq), dtype=torch.float32, device=q.device)
-            made.append(lse)
-        if lse is not None:
-            _lse_ok(lse, Tq, Hq)
-        _made(stream, *made)
-        if workspace is None:
-            workspace = _workspace(None, cross_attn_workspace_size(Tq, Tk, Hq, Hkv, D, B, max_q, max_k), q.device,
-                                   stream)
-        _check(lib().vit_cross_attn(_ptr(q), _ptr(k), _ptr(v), Tq, Tk, Hq, Hkv, D, qs, ks, vs, _ptr(cu_q), _ptr(cu_k),
-                                    _ptr(k_len), B, max_q, max_k, float(scale) if scale is not None else 0.0,
-                                    _ptr(out), os_, _ptr(lse), _ptr(workspace), _bytes(workspace), _ptr(status), s),
-               "vit_cross_attn")
+    if out is None:
+        out = q.new_empty((Tq, Hq, D))
+        _made(stream, out)
+        os_ = Hq * D
+    else:
+        os_ = _rows3(out, "out", Tq, Hq, D)
+    if lse is not None:
+        _lse_ok(lse, Tq, Hq)
+    elif return_lse:
+        lse = q.new_empty((Tq, Hq), dtype=_F32)
+        _made(stream, lse)
+    if workspace is None:
+        workspace = _scratch(lib().vit_cross_attn_workspace_size(Tq, Tk, Hq, Hkv, D, B, max_q, max_k), q, stream)
+    _call("vit_cross_attn", dev, stream, _addr(q), _addr(k), _addr(v), Tq, Tk, Hq, Hkv, D, qs, ks, vs, _addr(cu_q),
+          _addr(cu_k), _addr(k_len), B, max_q, max_k, 0.0 if scale is None else float(scale), _addr(out), os_,
+          _addr(lse), _addr(workspace), _bytes(workspace), _addr(status))
     return (out, lse) if lse is not None else out
-
-
-def cross_attn_bwd_workspace_size(Tq: int, Tk: int, Hq: int, Hkv: int, D: int, B: int, max_q: int = 0,
-                                  max_k: int = 0) -> int:
-    return int(lib().vit_cross_attn_bwd_workspace_size(int(Tq), int(Tk), int(Hq), int(Hkv), int(D), int(B),
-                                                       int(max_q), int(max_k)))
 
 
 def cross_attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
@@ -661,60 +684,61 @@ def cross_attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
     """Gradient of cross_attn: from dout and the forward call's inputs and results returns (dq, dk, dv), dk and dv
     summed over the query heads that share a key head. Rows of no sequence are 0 in the tensors the call
     allocates and left as they were in dq, dk, dv buffers it is given."""
-    if q.dim() != 3 or k.dim() != 3:
-        raise ValueError("q must be [Tq, Hq, D] and k, v [Tk, Hkv, D]")
-    Tq, Hq, D = q.shape
-    Tk, Hkv = k.shape[0], k.shape[1]
-    qs, ks, vs = _tok_stride(q, "q", Hq, D), _tok_stride(k, "k", Hkv, D), _tok_stride(v, "v", Hkv, D, Tk)
-    dos, os_ = _tok_stride(dout, "dout", Hq, D, Tq), _tok_stride(out, "out", Hq, D, Tq)
+    Tq, Hq, D = _shape3(q, "q")
+    Tk, Hkv, _ = _shape3(k, "k")
+    dev = _device(dout, q, k, v, out, lse, cu_q, cu_k, k_len, dq, dk, dv, workspace, status)
+    qs, ks, vs = _rows3(q, "q", Tq, Hq, D), _rows3(k, "k", Tk, Hkv, D), _rows3(v, "v", Tk, Hkv, D)
+    dos, os_ = _rows3(dout, "dout", Tq, Hq, D), _rows3(out, "out", Tq, Hq, D)
     _lse_ok(lse, Tq, Hq)
     B = _cross_lists(cu_q, cu_k, k_len)
     max_q, max_k = _max_seqlen(max_q), _max_seqlen(max_k)
-    with _on(stream, dout, q, k, v, out, lse, cu_q, cu_k, k_len, dq, dk, dv, workspace, status) as s:
-        nq, nk = Tq * Hq * D, Tk * Hkv * D
-        sizes = [n for n, t in ((nq, dq), (nk, dk), (nk, dv)) if t is None]
-        if sizes:      # one zeroed block for all of them
-            with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
-                made = torch.zeros(sum(sizes), dtype=q.dtype, device=q.device).split(sizes)
-            made = list(made)
-            dq = made.pop(0).view(Tq, Hq, D) if dq is None else dq
-            dk = made.pop(0).view(Tk, Hkv, D) if dk is None else dk
-            dv = made.pop(0).view(Tk, Hkv, D) if dv is None else dv
-        dqs, dks, dvs = (_tok_stride(dq, "dq", Hq, D, Tq), _tok_stride(dk, "dk", Hkv, D, Tk),
-                         _tok_stride(dv, "dv", Hkv, D, Tk))
-        if workspace is None:
-            workspace = _workspace(None, cross_attn_bwd_workspace_size(Tq, Tk, Hq, Hkv, D, B, max_q, max_k), q.device,
-                                   stream)
-        _check(lib().vit_cross_attn_bwd(_ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), Tq, Tk, Hq, Hkv,
-                                        D, dos, qs, ks, vs, os_, _ptr(cu_q), _ptr(cu_k), _ptr(k_len), B, max_q, max_k,
-                                        float(scale) if scale is not None else 0.0, _ptr(dq), _ptr(dk), _ptr(dv), dqs,
-                                        dks, dvs, _ptr(workspace), _bytes(workspace), _ptr(status), s),
-               "vit_cross_attn_bwd")
+    nq, nk = Tq * Hq * D, Tk * Hkv * D
+    sizes = [n for n, t in ((nq, dq), (nk, dk), (nk, dv)) if t is None]
+    if sizes:      # one zeroed block for all of them
+        if stream is None:
+            made = q.new_zeros(sum(sizes))
+        else:
+            with torch.cuda.stream(stream):
+                made = q.new_zeros(sum(sizes))
+        made = list(made.split(sizes))
+        dq = made.pop(0).view(Tq, Hq, D) if dq is None else dq
+        dk = made.pop(0).view(Tk, Hkv, D) if dk is None else dk
+        dv = made.pop(0).view(Tk, Hkv, D) if dv is None else dv
+    dqs, dks, dvs = _rows3(dq, "dq", Tq, Hq, D), _rows3(dk, "dk", Tk, Hkv, D), _rows3(dv, "dv", Tk, Hkv, D)
+    if workspace is None:
+        workspace = _scratch(lib().vit_cross_attn_bwd_workspace_size(Tq, Tk, Hq, Hkv, D, B, max_q, max_k), q, stream)
+    _call("vit_cross_attn_bwd", dev, stream, _addr(dout), _addr(q), _addr(k), _addr(v), _addr(out), _addr(lse), Tq,
+          Tk, Hq, Hkv, D, dos, qs, ks, vs, os_, _addr(cu_q), _addr(cu_k), _addr(k_len), B, max_q, max_k,
+          0.0 if scale is None else float(scale), _addr(dq), _addr(dk), _addr(dv), dqs, dks, dvs, _addr(workspace),
+          _bytes(workspace), _addr(status))
     return dq, dk, dv
 
 
 RES_BF16, RES_FP32 = 0, 1
 
 
-def _rows(t: torch.Tensor, name: str, T: int, C: int, dtype) -> int:
-    if t.dim() != 2 or tuple(t.shape) != (T, C):
+def _rows2(t: torch.Tensor, name: str, T: int, C: int, dtype) -> int:
+    """Row stride of [T, C] with unit element stride."""
+    if tuple(t.shape) != (T, C):
         raise ValueError(f"{name} must be [{T}, {C}], got {tuple(t.shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.stride(1) != 1:
-        raise ValueError(f"{name} needs unit element stride (got strides {t.stride()})")
-    return t.stride(0) if T > 1 else C
+    st = t.stride()
+    if st[1] != 1 and C > 1:
+        raise ValueError(f"{name} needs unit element stride (got strides {st})")
+    return st[0] if T > 1 else C
 
 
 def _channel(t: torch.Tensor | None, name: str, C: int):
-    if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != (C,) or not t.is_contiguous()):
+    if t is not None and (t.dtype is not _BF16 or tuple(t.shape) != (C,) or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous CUDA bfloat16 tensor [{C}]")
 
 
 def _residual(x: torch.Tensor):
-    if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float32):
+    if x.dim() != 2 or x.dtype not in (_BF16, _F32):
         raise ValueError("the residual must be a CUDA bfloat16 or float32 tensor [T, C]")
-    return x.shape[0], x.shape[1], RES_FP32 if x.dtype == torch.float32 else RES_BF16
+    T, C = x.shape
+    return T, C, RES_FP32 if x.dtype is _F32 else RES_BF16
 
 
 def _gate_stride(gate, T, C) -> int:
@@ -723,7 +747,7 @@ def _gate_stride(gate, T, C) -> int:
     if gate.dim() == 1:
         _channel(gate, "gate", C)
         return 0
-    return _rows(gate, "gate", T, C, torch.bfloat16)
+    return _rows2(gate, "gate", T, C, _BF16)
 
 
 def norm_residual(x: torch.Tensor, y: torch.Tensor, *, gate: torch.Tensor | None = None,
@@ -735,35 +759,38 @@ def norm_residual(x: torch.Tensor, y: torch.Tensor, *, gate: torch.Tensor | None
     x [T, C] bf16 or fp32 (h has its type and may be x itself), y [T, C] bf16 (z may be y itself), gate [C] or
     [T, C] bf16, the weights [C] bf16. Without w_post y is taken as it is."""
     T, C, res = _residual(x)
-    xs, ys = _rows(x, "x", T, C, x.dtype), _rows(y, "y", T, C, torch.bfloat16)
+    dev = _device(x, y, gate, w_post, w_pre, h_out, z_out)
+    xs, ys = _rows2(x, "x", T, C, x.dtype), _rows2(y, "y", T, C, _BF16)
     gs = _gate_stride(gate, T, C)
     _channel(w_post, "w_post", C)
     _channel(w_pre, "w_pre", C)
     if w_pre is None and z_out is not None:
         raise ValueError("z_out needs w_pre")
-    with _on(stream, x, y, gate, w_post, w_pre, h_out, z_out) as s:
-        made = []
-        if h_out is None:
-            h_out = torch.empty((T, C), dtype=x.dtype, device=x.device)
-            made.append(h_out)
-        if w_pre is not None and z_out is None:
-            z_out = torch.empty((T, C), dtype=torch.bfloat16, device=x.device)
-            made.append(z_out)
-        _made(stream, *made)
-        zs = _rows(z_out, "z_out", T, C, torch.bfloat16) if z_out is not None else 0
-        _check(lib().vit_norm_residual(_ptr(x), _ptr(y), _ptr(gate), _ptr(w_post), _ptr(w_pre), _ptr(h_out),
-                                       _ptr(z_out), T, C, res, xs, ys, gs, _rows(h_out, "h_out", T, C, x.dtype), zs,
-                                       float(scale), float(eps), s), "vit_norm_residual")
+    hs = zs = C
+    if h_out is None:
+        h_out = x.new_empty((T, C))
+        _made(stream, h_out)
+    else:
+        hs = _rows2(h_out, "h_out", T, C, x.dtype)
+    if z_out is not None:
+        zs = _rows2(z_out, "z_out", T, C, _BF16)
+    elif w_pre is not None:
+        z_out = y.new_empty((T, C))
+        _made(stream, z_out)
+    _call("vit_norm_residual", dev, stream, _addr(x), _addr(y), _addr(gate), _addr(w_post), _addr(w_pre),
+          _addr(h_out), _addr(z_out), T, C, res, xs, ys, gs, hs, zs, float(scale), float(eps))
     return h_out, z_out
 
 
-def norm_residual_bwd(dz: torch.Tensor | None, dh: torch.Tensor | None, h: torch.Tensor | None, y: torch.Tensor, *,
-                      gate: torch.Tensor | None = None, w_post: torch.Tensor | None = None,
-                      w_pre: torch.Tensor | None = None, scale: float = 1.0, eps: float = 1e-6,
-                      workspace: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
+def norm_residual_bwd(dz: torch.Tensor | None, dh: torch.Tensor | None, h: torch.Tensor | None,
+                      y: torch.Tensor | None, *, gate: torch.Tensor | None = None,
+                      w_post: torch.Tensor | None = None, w_pre: torch.Tensor | None = None, scale: float = 1.0,
+                      eps: float = 1e-6, workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                      stream=None):
     """Gradient of norm_residual: from dz (given exactly when w_pre is), dh (the residual stream's own gradient,
-    or None), the stored h (needed with w_pre) and y returns (dx, dy, dgate, dw_post, dw_pre); the last three are
-    None without gate, w_post, w_pre. dgate is fp32 [C] for a [C] gate and bf16 [T, C] for a [T, C] one."""
+    or None), the stored h (needed with w_pre) and y (needed with w_post or gate) returns (dx, dy, dgate, dw_post,
+    dw_pre); the last three are None without gate, w_post, w_pre. dgate is fp32 [C] for a [C] gate and bf16 [T, C]
+    for a [T, C] one."""
     ref = dh if dh is not None else h
     if ref is None:
         raise ValueError("dh or h is required")
@@ -773,29 +800,35 @@ def norm_residual_bwd(dz: torch.Tensor | None, dh: torch.Tensor | None, h: torch
         raise ValueError("h is needed for the gradient of the norm after the residual")
     if dz is None and dh is None:
         raise ValueError("at least one of dz and dh is required")
+    if y is None and (w_post is not None or gate is not None):
+        raise ValueError("y is needed for the gradient of its norm or gate")
     T, C, res = _residual(ref)
-    ds = _rows(dh, "dh", T, C, ref.dtype) if dh is not None else 0
-    zs = _rows(dz, "dz", T, C, torch.bfloat16) if dz is not None else 0
-    hs = _rows(h, "h", T, C, ref.dtype) if h is not None else 0
-    ys = _rows(y, "y", T, C, torch.bfloat16)
+    dev = _device(dz, dh, h, y, gate, w_post, w_pre, workspace, status)
+    ds = _rows2(dh, "dh", T, C, ref.dtype) if dh is not None else 0
+    zs = _rows2(dz, "dz", T, C, _BF16) if dz is not None else 0
+    hs = _rows2(h, "h", T, C, ref.dtype) if h is not None else 0
+    ys = _rows2(y, "y", T, C, _BF16) if y is not None else 0
     gs = _gate_stride(gate, T, C)
     _channel(w_post, "w_post", C)
     _channel(w_pre, "w_pre", C)
-    with _on(stream, dz, dh, h, y, gate, w_post, w_pre, workspace, status) as s:
-        new = dict(device=ref.device)
-        dx = torch.empty((T, C), dtype=ref.dtype, **new)
-        dy = torch.empty((T, C), dtype=torch.bfloat16, **new)
-        dgate = None
-        if gate is not None:
-            dgate = torch.empty(gate.shape, dtype=torch.float32 if gate.dim() == 1 else torch.bfloat16, **new)
-        dw_post = torch.empty(C, dtype=torch.float32, **new) if w_post is not None else None
-        dw_pre = torch.empty(C, dtype=torch.float32, **new) if w_pre is not None else None
-        _made(stream, dx, dy, dgate, dw_post, dw_pre)
-        workspace = _workspace(workspace, int(lib().vit_norm_residual_bwd_workspace_size(C)), ref.device, stream)
-        _check(lib().vit_norm_residual_bwd(_ptr(dz), _ptr(dh), _ptr(h), _ptr(y), _ptr(gate), _ptr(w_post),
-                                           _ptr(w_pre), _ptr(dx), _ptr(dy), _ptr(dgate), _ptr(dw_post), _ptr(dw_pre),
-                                           T, C, res, zs, ds, hs, ys, gs, C, C, C, float(scale), float(eps),
-                                           _ptr(workspace), _bytes(workspace), _ptr(status), s), "vit_norm_residual_bwd")
+    dx, dy = ref.new_empty((T, C)), ref.new_empty((T, C), dtype=_BF16)
+    sums = (gate is not None and gate.dim() == 1) + (w_post is not None) + (w_pre is not None)
+    vec = list(ref.new_empty((sums, C), dtype=_F32).unbind(0)) if sums else []
+    _made(stream, dx, dy, *vec)
+    dgate = None
+    if gate is not None:
+        if gate.dim() == 1:
+            dgate = vec.pop()
+        else:
+            dgate = gate.new_empty((T, C))
+            _made(stream, dgate)
+    dw_post = vec.pop() if w_post is not None else None
+    dw_pre = vec.pop() if w_pre is not None else None
+    if workspace is None:
+        workspace = _scratch(lib().vit_norm_residual_bwd_workspace_size(C) if sums else 0, ref, stream)
+    _call("vit_norm_residual_bwd", dev, stream, _addr(dz), _addr(dh), _addr(h), _addr(y), _addr(gate), _addr(w_post),
+          _addr(w_pre), _addr(dx), _addr(dy), _addr(dgate), _addr(dw_post), _addr(dw_pre), T, C, res, zs, ds, hs, ys,
+          gs, C, C, C, float(scale), float(eps), _addr(workspace), _bytes(workspace), _addr(status))
     return dx, dy, dgate, dw_post, dw_pre
 
 

@@ -14,15 +14,18 @@
 //
 // The angle: the product of an int32 position and an fp32 frequency needs 55 bits before it is
 // reduced (position 10^6 at frequency 1 leaves an fp32 product with 0.06 rad of error), so it is
-// formed and reduced by 2 pi in fp64 (three operations per pair, shared by all heads of the token;
-// the fp32 remainder in [-pi, pi] then goes through __sincosf, whose absolute error there is 2^-21).
+// formed and reduced by 2 pi exactly enough: as a product and its rounding error in fp32 where the
+// position fits 22 bits, in fp64 beyond (GB300's fp64 rate is low). The remainder in about [-pi, pi]
+// then goes through __sincosf, whose absolute error there is 2^-21. All heads of a token share it.
 //
 // HBM bound: 4 T (Hq + Hk) D bytes forward, 6 T (Hq + Hk) D backward. One warp owns a token (or,
 // when there are fewer tokens than warps to fill the GPU, a slice of a token's heads): it builds the
 // token's cos/sin row in its own part of shared memory and then walks the heads, so no barrier
 // wider than a warp is needed. A head row belongs to D/16 lanes, lane c holding the 16-byte chunks
-// c and c + D/16, so every rotated pair lies in one thread; a warp handles 32 / (D/16) rows at a
-// time and keeps several steps' loads in flight. The gradient's weight sums stay in registers (a
+// c and c + D/16, so every rotated pair lies in one thread; a warp handles 32 / (D/16) rows per
+// step. Rows arrive through asynchronous copies a fixed number of steps ahead (across tokens), each
+// lane copying into shared memory exactly the bytes that it will read itself, so the loads in flight
+// need neither registers nor a barrier. The gradient's weight sums stay in registers (a
 // lane's columns never change), are joined per block in shared memory in a fixed order, and a
 // second kernel adds the blocks' partial sums.
 #include "internal.h"
@@ -61,28 +64,81 @@ __device__ __forceinline__ int axis_of(const Mrope &p, int m) {
     return m < p.s_t ? 0 : m < p.s_t + p.s_h ? 1 : 2;
 }
 
-// pos * f reduced to [-pi, pi], as an fp32 value
+// pos * f reduced to about [-pi, pi], as an fp32 value
 __device__ __forceinline__ float reduced_angle(int pos, float f) {
+    if (abs(pos) < (1 << 22) && fabsf(f) <= 1.f) {
+        // pos is exact in fp32 and p + e is the exact product; the multiple n of 2 pi (|n| < 2^20) is
+        // taken off in two parts, 2 pi = C1 + C2 to 2^-50 (Cody and Waite): the error stays below 2^-21
+        const float x = (float)pos, p = x * f, e = fmaf(x, f, -p);
+        const float n = rintf(p * 0.159154943f);
+        constexpr float C1 = 6.28318548f, C2 = -1.74845553e-7f;
+        return fmaf(-n, C2, fmaf(-n, C1, p)) + e;
+    }
     const double a = (double)pos * (double)f;
     const double n = rint(a * 0.15915494309189535);                 // 1 / (2 pi)
     return (float)fma(n, -6.283185307179586, a);
 }
 
-// cos/sin of the token's pairs as {cos m, cos m+1, sin m, sin m+1}, m even
-template <int D> __device__ __forceinline__ void fill_turns(const Mrope &p, int64_t t, int lane, float4 *cs) {
-    int pos[3];
-#pragma unroll
-    for (int a = 0; a < 3; ++a) pos[a] = p.pos[3 * t + a];
-    for (int i = lane; i < D / 4; i += 32) {
-        float c[2], s[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int m = 2 * i + e, a = axis_of(p, m);
-            __sincosf(reduced_angle(a == 0 ? pos[0] : a == 1 ? pos[1] : pos[2], p.inv_freq[m]), &s[e], &c[e]);
-        }
-        cs[i] = make_float4(c[0], c[1], s[0], s[1]);
+// The pairs whose cos/sin a lane makes for every token: 2 lane and 2 lane + 1 (D/4 lanes have some).
+struct LanePairs {
+    float f0, f1;
+    int a0, a1;
+};
+template <int D> __device__ __forceinline__ LanePairs lane_pairs(const Mrope &p, int lane) {
+    LanePairs x{0.f, 0.f, 0, 0};
+    if (lane < D / 4) {
+        x.f0 = p.inv_freq[2 * lane];
+        x.f1 = p.inv_freq[2 * lane + 1];
+        x.a0 = axis_of(p, 2 * lane);
+        x.a1 = axis_of(p, 2 * lane + 1);
+    }
+    return x;
+}
+// cos/sin of a token's pairs as {cos m, cos m+1, sin m, sin m+1}, m even
+template <int D> __device__ __forceinline__ void fill_turns(const LanePairs &x, const int *pos, int lane, float4 *cs) {
+    if (lane < D / 4) {
+        float c0, s0, c1, s1;
+        __sincosf(reduced_angle(pos[x.a0], x.f0), &s0, &c0);
+        __sincosf(reduced_angle(pos[x.a1], x.f1), &s1, &c1);
+        cs[lane] = make_float4(c0, c1, s0, s1);
     }
 }
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+
+// A warp's way over its units (token, slice of heads), `rows` head rows at a time, among the rows
+// [h0, h1) of a token's Hq + Hk.
+struct Walk {
+    int64_t u, t;
+    int r, hi;
+    __device__ __forceinline__ bool done(int64_t units) const { return u >= units; }
+    __device__ __forceinline__ void enter(const Mrope &p, int64_t units, int64_t stride, int per, int h0, int h1) {
+        for (; u < units; u += stride) {
+            t = p.slices == 1 ? u : u / p.slices;
+            const int lo = p.slices == 1 ? 0 : (int)(u - t * p.slices) * per;
+            r = max(lo, h0);
+            hi = min(lo + per, h1);
+            if (r < hi) return;
+        }
+    }
+    __device__ __forceinline__ void step(const Mrope &p, int64_t units, int64_t stride, int per, int h0, int h1,
+                                         int rows) {
+        r += rows;
+        if (r >= hi) {
+            u += stride;
+            enter(p, units, stride, per, h0, h1);
+        }
+    }
+};
 
 // y = R(+-a) x on the 16 elements of a lane; cs: the lane's turns of its two chunks' pairs
 template <bool IL, bool BACK>
@@ -133,11 +189,15 @@ __device__ __forceinline__ uint4 pack8(const float *x) {
                       rope::pack2(x[6], x[7]));
 }
 
+constexpr int kAheadFwd = 6, kAheadBwd = 4;        // steps in flight: 48 and 64 KB of a block
+
 template <int D, bool IL>
 __global__ void __launch_bounds__(kThreads)
 mrope_kernel(const Mrope p)
 {
-    constexpr int CH = Shape<D>::CH, ROWS = Shape<D>::ROWS, BATCH = 4;
+    constexpr int CH = Shape<D>::CH, ROWS = Shape<D>::ROWS, AHEAD = kAheadFwd;
+    extern __shared__ uint4 s_rows[];                      // [warp][step][chunk a, b][lane]
+    __shared__ int s_pos[kWarps][AHEAD][4];               // the steps' positions, copied with their rows
     __shared__ float4 s_cs[kWarps][D / 4];
     __shared__ uint4 s_w[2][D / 8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -150,63 +210,76 @@ mrope_kernel(const Mrope p)
         __syncthreads();
     }
     const float4 *cs_a = s_cs[warp] + (IL ? 2 * c : 4 * c), *cs_b = cs_a + D / 8;
+    uint4 *mine = s_rows + warp * (AHEAD * 64) + lane;
+    const uint32_t mine_a = (uint32_t)__cvta_generic_to_shared(mine);
     const int rows = p.Hq + p.Hk, per = (rows + p.slices - 1) / p.slices;
-    const int64_t units = p.T * p.slices;
-    for (int64_t u = (int64_t)blockIdx.x * kWarps + warp; u < units; u += (int64_t)gridDim.x * kWarps) {
-        const int64_t t = p.slices == 1 ? u : u / p.slices;
-        const int lo = p.slices == 1 ? 0 : (int)(u - t * p.slices) * per;
-        const int hi = min(rows, lo + per);
-        bool filled = false;
-        for (int r0 = lo; r0 < hi; r0 += BATCH * ROWS) {
-            uint4 va[BATCH], vb[BATCH];
-#pragma unroll
-            for (int b = 0; b < BATCH; ++b) {
-                const int r = r0 + b * ROWS + g;
-                va[b] = vb[b] = make_uint4(0u, 0u, 0u, 0u);
-                if (live && r < hi) {
-                    const __nv_bfloat16 *src = (r < p.Hq ? p.q_in + t * p.q_in_stride + (int64_t)r * D
-                                                         : p.k_in + t * p.k_in_stride + (int64_t)(r - p.Hq) * D) + 8 * c;
-                    va[b] = *reinterpret_cast<const uint4 *>(src);
-                    vb[b] = *reinterpret_cast<const uint4 *>(src + D / 2);
-                }
+    const int64_t units = p.T * p.slices, stride = (int64_t)gridDim.x * kWarps;
+    const LanePairs pairs = lane_pairs<D>(p, lane);
+
+    Walk fetch;
+    fetch.u = (int64_t)blockIdx.x * kWarps + warp;
+    fetch.enter(p, units, stride, per, 0, rows);
+    auto request = [&](int slot) {                         // this lane's chunks of the fetch step's rows
+        if (!fetch.done(units)) {
+            const int r = fetch.r + g;
+            if (lane < 3) copy4((uint32_t)__cvta_generic_to_shared(&s_pos[warp][slot][lane]), p.pos + 3 * fetch.t + lane);
+            if (live && r < fetch.hi) {
+                const __nv_bfloat16 *src = (r < p.Hq ? p.q_in + fetch.t * p.q_in_stride + (int64_t)r * D
+                                                     : p.k_in + fetch.t * p.k_in_stride + (int64_t)(r - p.Hq) * D) + 8 * c;
+                copy16(mine_a + slot * 1024, src);
+                copy16(mine_a + slot * 1024 + 512, src + D / 2);
             }
-            if (!filled) {                                // while the first rows are on their way
-                __syncwarp();                             // the previous token's turns have been read
-                fill_turns<D>(p, t, lane, s_cs[warp]);
-                __syncwarp();
-                filled = true;
-            }
+            fetch.step(p, units, stride, per, 0, rows, ROWS);
+        }
+        copies_commit();
+    };
+    Walk at = fetch;
 #pragma unroll
-            for (int b = 0; b < BATCH; ++b) {
-                const int r = r0 + b * ROWS + g;
-                if (r0 + b * ROWS >= hi) break;           // uniform over the warp
-                const bool k_row = r >= p.Hq;
-                float xa[8], xb[8];
-                unpack8(va[b], xa);
-                unpack8(vb[b], xb);
-                if (p.norm_w) {
-                    float ss = 0.f;
+    for (int i = 0; i < AHEAD; ++i) request(i);
+    int64_t turned = -1;                                   // the unit whose turns are in s_cs
+    int slot = 0;
+    while (!at.done(units)) {
+        copies_wait<AHEAD - 1>();
+        if (at.u != turned) {
+            __syncwarp();                                  // the copied position is there, the last turns were read
+            fill_turns<D>(pairs, s_pos[warp][slot], lane, s_cs[warp]);
+            turned = at.u;
+            __syncwarp();
+        }
+        const int r = at.r + g;
+        const bool row = live && r < at.hi, k_row = r >= p.Hq;
+        uint4 va = make_uint4(0u, 0u, 0u, 0u), vb = va;
+        if (row) {
+            va = mine[slot * 64];
+            vb = mine[slot * 64 + 32];
+        }
+        float xa[8], xb[8];
+        unpack8(va, xa);
+        unpack8(vb, xb);
+        if (p.norm_w) {
+            float ss = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) ss = fmaf(xa[e], xa[e], fmaf(xb[e], xb[e], ss));
-                    const float inv = rsqrtf(group_sum<D>(ss, first) * (1.f / D) + p.eps);
-                    float wa[8], wb[8];
-                    unpack8(s_w[k_row][c], wa);
-                    unpack8(s_w[k_row][CH + c], wb);
+            for (int e = 0; e < 8; ++e) ss = fmaf(xa[e], xa[e], fmaf(xb[e], xb[e], ss));
+            const float inv = rsqrtf(group_sum<D>(ss, first) * (1.f / D) + p.eps);
+            float wa[8], wb[8];
+            unpack8(s_w[k_row][c], wa);
+            unpack8(s_w[k_row][CH + c], wb);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        xa[e] *= inv * wa[e];
-                        xb[e] *= inv * wb[e];
-                    }
-                }
-                turn<IL, false>(xa, xb, cs_a, cs_b);
-                if (live && r < hi) {
-                    __nv_bfloat16 *dst = (k_row ? p.k_out + t * p.k_out_stride + (int64_t)(r - p.Hq) * D
-                                                : p.q_out + t * p.q_out_stride + (int64_t)r * D) + 8 * c;
-                    *reinterpret_cast<uint4 *>(dst) = pack8(xa);
-                    *reinterpret_cast<uint4 *>(dst + D / 2) = pack8(xb);
-                }
+            for (int e = 0; e < 8; ++e) {
+                xa[e] *= inv * wa[e];
+                xb[e] *= inv * wb[e];
             }
         }
+        turn<IL, false>(xa, xb, cs_a, cs_b);
+        if (row) {
+            __nv_bfloat16 *dst = (k_row ? p.k_out + at.t * p.k_out_stride + (int64_t)(r - p.Hq) * D
+                                        : p.q_out + at.t * p.q_out_stride + (int64_t)r * D) + 8 * c;
+            *reinterpret_cast<uint4 *>(dst) = pack8(xa);
+            *reinterpret_cast<uint4 *>(dst + D / 2) = pack8(xb);
+        }
+        request(slot);                                     // read above: the slot is free
+        if (++slot == AHEAD) slot = 0;
+        at.step(p, units, stride, per, 0, rows, ROWS);
     }
 }
 
@@ -214,7 +287,9 @@ template <int D, bool IL>
 __global__ void __launch_bounds__(kThreads)
 mrope_bwd_kernel(const Mrope p)
 {
-    constexpr int CH = Shape<D>::CH, ROWS = Shape<D>::ROWS, BATCH = 1;
+    constexpr int CH = Shape<D>::CH, ROWS = Shape<D>::ROWS, AHEAD = kAheadBwd;
+    extern __shared__ uint4 s_rows[];                      // [warp][step][dy a, dy b, x a, x b][lane]
+    __shared__ int s_pos[kWarps][AHEAD][4];               // the steps' positions, copied with their rows
     __shared__ float4 s_cs[kWarps][D / 4];
     __shared__ uint4 s_w[2][D / 8];
     __shared__ float s_sum[kWarps][2][D];
@@ -229,8 +304,11 @@ mrope_bwd_kernel(const Mrope p)
         __syncthreads();
     }
     const float4 *cs_a = s_cs[warp] + (IL ? 2 * c : 4 * c), *cs_b = cs_a + D / 8;
+    uint4 *mine = s_rows + warp * (AHEAD * 128) + lane;
+    const uint32_t mine_a = (uint32_t)__cvta_generic_to_shared(mine);
     const int rows = p.Hq + p.Hk, per = (rows + p.slices - 1) / p.slices;
-    const int64_t units = p.T * p.slices;
+    const int64_t units = p.T * p.slices, stride = (int64_t)gridDim.x * kWarps;
+    const LanePairs pairs = lane_pairs<D>(p, lane);
     // all q rows, then all k rows: one set of sums in registers at a time (both at once spilled)
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
@@ -242,84 +320,98 @@ mrope_bwd_kernel(const Mrope p)
         float acc[16];                                    // this lane's columns of the weight sums
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-        for (int64_t u = (int64_t)blockIdx.x * kWarps + warp; u < units; u += (int64_t)gridDim.x * kWarps) {
-            const int64_t t = p.slices == 1 ? u : u / p.slices;
-            const int lo = p.slices == 1 ? 0 : (int)(u - t * p.slices) * per;
-            const int r_lo = max(lo, h0) - h0, r_hi = min(min(rows, lo + per), h1) - h0;   // heads of this half
-            const __nv_bfloat16 *dy = dy0 + t * dy_s, *x = x0 + t * x_s;
-            __nv_bfloat16 *dx = dx0 + t * dx_s;
-            bool filled = false;
-            for (int r0 = r_lo; r0 < r_hi; r0 += BATCH * ROWS) {
-                uint4 va[BATCH], vb[BATCH], ua[BATCH], ub[BATCH];
-#pragma unroll
-                for (int b = 0; b < BATCH; ++b) {
-                    const int r = r0 + b * ROWS + g;
-                    va[b] = vb[b] = ua[b] = ub[b] = make_uint4(0u, 0u, 0u, 0u);
-                    if (live && r < r_hi) {
-                        const int64_t off = (int64_t)r * D + 8 * c;
-                        va[b] = *reinterpret_cast<const uint4 *>(dy + off);
-                        vb[b] = *reinterpret_cast<const uint4 *>(dy + off + D / 2);
-                        if (norm) {
-                            ua[b] = *reinterpret_cast<const uint4 *>(x + off);
-                            ub[b] = *reinterpret_cast<const uint4 *>(x + off + D / 2);
-                        }
-                    }
-                }
-                if (!filled) {
-                    __syncwarp();
-                    fill_turns<D>(p, t, lane, s_cs[warp]);
-                    __syncwarp();
-                    filled = true;
-                }
-#pragma unroll
-                for (int b = 0; b < BATCH; ++b) {
-                    const int r = r0 + b * ROWS + g;
-                    if (r0 + b * ROWS >= r_hi) break;
-                    const bool row = live && r < r_hi;
-                    float da[8], db[8];
-                    unpack8(va[b], da);
-                    unpack8(vb[b], db);
-                    turn<IL, true>(da, db, cs_a, cs_b);   // dz
+        Walk fetch;
+        fetch.u = (int64_t)blockIdx.x * kWarps + warp;
+        fetch.enter(p, units, stride, per, h0, h1);
+        auto request = [&](int slot) {
+            if (!fetch.done(units)) {
+                const int r = fetch.r + g;
+                if (lane < 3) copy4((uint32_t)__cvta_generic_to_shared(&s_pos[warp][slot][lane]), p.pos + 3 * fetch.t + lane);
+                if (live && r < fetch.hi) {
+                    const int64_t off = (int64_t)(r - h0) * D + 8 * c;
+                    const __nv_bfloat16 *dy = dy0 + fetch.t * dy_s + off;
+                    copy16(mine_a + slot * 2048, dy);
+                    copy16(mine_a + slot * 2048 + 512, dy + D / 2);
                     if (norm) {
-                        float xa[8], xb[8], dna[8], dnb[8];      // x, dn = dz w
-                        unpack8(ua[b], xa);
-                        unpack8(ub[b], xb);
-                        unpack8(s_w[which][c], dna);
-                        unpack8(s_w[which][CH + c], dnb);
-                        float ss = 0.f, dot = 0.f;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            dna[e] *= da[e];
-                            dnb[e] *= db[e];
-                            ss = fmaf(xa[e], xa[e], fmaf(xb[e], xb[e], ss));
-                            dot = fmaf(dna[e], xa[e], fmaf(dnb[e], xb[e], dot));
-                        }
-                        // lanes without a row add nothing to the sums, whatever eps is
-                        const float r_rms = rsqrtf(group_sum<D>(ss, first) * (1.f / D) + p.eps);
-                        const float inv = row ? r_rms : 0.f;
-                        const float k = inv * inv * (group_sum<D>(dot, first) * (1.f / D));
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            acc[e] = fmaf(da[e], xa[e] * inv, acc[e]);
-                            acc[8 + e] = fmaf(db[e], xb[e] * inv, acc[8 + e]);
-                            da[e] = inv * fmaf(-xa[e], k, dna[e]);
-                            db[e] = inv * fmaf(-xb[e], k, dnb[e]);
-                        }
+                        const __nv_bfloat16 *x = x0 + fetch.t * x_s + off;
+                        copy16(mine_a + slot * 2048 + 1024, x);
+                        copy16(mine_a + slot * 2048 + 1536, x + D / 2);
                     }
-                    if (row) {
-                        const int64_t off = (int64_t)r * D + 8 * c;
-                        *reinterpret_cast<uint4 *>(dx + off) = pack8(da);
-                        *reinterpret_cast<uint4 *>(dx + off + D / 2) = pack8(db);
-                    }
+                }
+                fetch.step(p, units, stride, per, h0, h1, ROWS);
+            }
+            copies_commit();
+        };
+        Walk at = fetch;
+    #pragma unroll
+        for (int i = 0; i < AHEAD; ++i) request(i);
+        int64_t turned = -1;
+        int slot = 0;
+        while (!at.done(units)) {
+            copies_wait<AHEAD - 1>();
+            if (at.u != turned) {
+                __syncwarp();
+                fill_turns<D>(pairs, s_pos[warp][slot], lane, s_cs[warp]);
+                turned = at.u;
+                __syncwarp();
+            }
+            const int r = at.r + g;
+            const bool row = live && r < at.hi;
+            uint4 va = make_uint4(0u, 0u, 0u, 0u), vb = va, ua = va, ub = va;
+            if (row) {
+                va = mine[slot * 128];
+                vb = mine[slot * 128 + 32];
+                if (norm) {
+                    ua = mine[slot * 128 + 64];
+                    ub = mine[slot * 128 + 96];
                 }
             }
+            float da[8], db[8];
+            unpack8(va, da);
+            unpack8(vb, db);
+            turn<IL, true>(da, db, cs_a, cs_b);           // dz
+            if (norm) {
+                float xa[8], xb[8], dna[8], dnb[8];       // x, dn = dz w
+                unpack8(ua, xa);
+                unpack8(ub, xb);
+                unpack8(s_w[which][c], dna);
+                unpack8(s_w[which][CH + c], dnb);
+                float ss = 0.f, dot = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    dna[e] *= da[e];
+                    dnb[e] *= db[e];
+                    ss = fmaf(xa[e], xa[e], fmaf(xb[e], xb[e], ss));
+                    dot = fmaf(dna[e], xa[e], fmaf(dnb[e], xb[e], dot));
+                }
+                // lanes without a row add nothing to the sums, whatever eps is
+                const float r_rms = rsqrtf(group_sum<D>(ss, first) * (1.f / D) + p.eps);
+                const float inv = row ? r_rms : 0.f;
+                const float k = inv * inv * (group_sum<D>(dot, first) * (1.f / D));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    acc[e] = fmaf(da[e], xa[e] * inv, acc[e]);
+                    acc[8 + e] = fmaf(db[e], xb[e] * inv, acc[8 + e]);
+                    da[e] = inv * fmaf(-xa[e], k, dna[e]);
+                    db[e] = inv * fmaf(-xb[e], k, dnb[e]);
+                }
+            }
+            if (row) {
+                __nv_bfloat16 *dx = dx0 + at.t * dx_s + (int64_t)(r - h0) * D + 8 * c;
+                *reinterpret_cast<uint4 *>(dx) = pack8(da);
+                *reinterpret_cast<uint4 *>(dx + D / 2) = pack8(db);
+            }
+            request(slot);
+            if (++slot == AHEAD) slot = 0;
+            at.step(p, units, stride, per, h0, h1, ROWS);
         }
+        copies_wait<0>();
         if (!p.part) continue;
         // a warp's groups hold the same columns: join them in group order
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
             float s = 0.f;
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < ROWS; ++i) s += __shfl_sync(0xffffffffu, acc[e], (i * CH + c) & 31);
             if (g == 0) s_sum[warp][which][e < 8 ? 8 * c + e : D / 2 + 8 * c + e - 8] = s;
         }
@@ -349,24 +441,32 @@ template <int D> void shape(Mrope &p, int num_sms, int64_t max_blocks, unsigned 
 
 template <int D> cudaError_t launch_fwd(Mrope p, bool il, int num_sms, cudaStream_t stream) {
     unsigned blocks;
-    shape<D>(p, num_sms, (int64_t)num_sms * 64, &blocks);
+    shape<D>(p, num_sms, (int64_t)num_sms * 4, &blocks);   // resident blocks: 64 registers, 53 KB each
+    constexpr int smem = kWarps * kAheadFwd * 1024;
+    auto kern = il ? mrope_kernel<D, true> : mrope_kernel<D, false>;
+    static DeviceOnce once[2];
+    cudaError_t e = once[il].run([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
+    if (e != cudaSuccess) return e;
     LaunchScope scope("qk_norm_mrope", stream);
-    if (il) mrope_kernel<D, true><<<blocks, kThreads, 0, stream>>>(p);
-    else mrope_kernel<D, false><<<blocks, kThreads, 0, stream>>>(p);
+    kern<<<blocks, kThreads, smem, stream>>>(p);
     return cudaGetLastError();
 }
 
 template <int D> cudaError_t launch_bwd(Mrope p, bool il, float *dnorm_w, int num_sms, cudaStream_t stream) {
     unsigned blocks;
-    int64_t most = (int64_t)num_sms * 4;
+    int64_t most = (int64_t)num_sms * 2;                 // resident blocks: 128 registers, 77 KB each
     if (most > kMropeParts) most = kMropeParts;
     shape<D>(p, num_sms, most, &blocks);
     if (!dnorm_w) p.part = nullptr;
     if (blocks > 0) {
+        constexpr int smem = kWarps * kAheadBwd * 2048;
+        auto kern = il ? mrope_bwd_kernel<D, true> : mrope_bwd_kernel<D, false>;
+        static DeviceOnce once[2];
+        cudaError_t e = once[il].run([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
+        if (e != cudaSuccess) return e;
         LaunchScope scope("qk_norm_mrope_bwd", stream);
-        if (il) mrope_bwd_kernel<D, true><<<blocks, kThreads, 0, stream>>>(p);
-        else mrope_bwd_kernel<D, false><<<blocks, kThreads, 0, stream>>>(p);
-        const cudaError_t e = cudaGetLastError();
+        kern<<<blocks, kThreads, smem, stream>>>(p);
+        e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     if (!dnorm_w) return cudaSuccess;

@@ -352,17 +352,20 @@ struct Ring {
 constexpr int kMaxStages = 4;
 constexpr long long kWaitBudget = 4000000000ll;   // clock cycles before a wait gives up (~2 s)
 
+__device__ __forceinline__ void unpack4(const uint2 &a, float *x) {
+    x[0] = __uint_as_float(a.x << 16);
+    x[1] = __uint_as_float(a.x & 0xffff0000u);
+    x[2] = __uint_as_float(a.y << 16);
+    x[3] = __uint_as_float(a.y & 0xffff0000u);
+}
+
 // 4 consecutive values in bf16 or fp32
 template <bool F32> __device__ __forceinline__ void get4(const void *p, int64_t i, float *x) {
     if constexpr (F32) {
         const float4 a = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
         x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
     } else {
-        const uint2 a = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p) + i);
-        x[0] = __uint_as_float(a.x << 16);
-        x[1] = __uint_as_float(a.x & 0xffff0000u);
-        x[2] = __uint_as_float(a.y << 16);
-        x[3] = __uint_as_float(a.y & 0xffff0000u);
+        unpack4(*reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p) + i), x);
     }
 }
 template <bool F32> __device__ __forceinline__ void put4(void *p, int64_t i, const float *x) {
@@ -377,8 +380,11 @@ template <bool F32> __device__ __forceinline__ void put4(void *p, int64_t i, con
 // apart: mixed, or with pieces of 8, the widest variant spills
 __device__ __forceinline__ void one_piece() { asm volatile("" ::: "memory"); }
 
-template <int NP, bool F32>
-__global__ void __launch_bounds__(512)
+// WR: the lane's columns of the two weights and of a gate of all tokens stay in registers (from
+// memory they come through an L1 that the ring leaves almost nothing of: 9001 x 5120 took 340 us).
+// Only the widest rows (above 6144 columns: 512 threads of 128 registers) have no room for them.
+template <int NP, bool F32, bool WR>
+__global__ void __launch_bounds__(NP == 4 && WR ? 384 : 512)
 norm_residual_bwd_ring_kernel(const Bwd p, const Ring ring)
 {
     extern __shared__ __align__(128) unsigned char s_ring[];
@@ -423,6 +429,26 @@ norm_residual_bwd_ring_kernel(const Bwd p, const Ring ring)
 #pragma unroll
         for (int e = 0; e < 4; ++e) a_pre[i][e] = a_post[i][e] = a_gate[i][e] = 0.f;
 
+    uint2 r_pre[WR ? NP : 1], r_post[WR ? NP : 1], r_gate[WR ? NP : 1];
+    if constexpr (WR) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int v = i * group + threadIdx.x;
+            const auto take = [&](const __nv_bfloat16 *w) {
+                return w && v < nvec ? *reinterpret_cast<const uint2 *>(w + 4 * v) : make_uint2(0u, 0u);
+            };
+            r_pre[i] = take(p.w_pre);
+            r_post[i] = take(p.w_post);
+            r_gate[i] = take(gate_tok ? nullptr : p.gate);
+        }
+    }
+    auto weight4 = [&](const __nv_bfloat16 *w, const uint2 *reg, int i, int v, float *x) {
+        if constexpr (WR)
+            unpack4(reg[i], x);
+        else
+            get4<false>(w, 4 * v, x);
+    };
+
     bool ok = true;
     int s_at = 0;
     uint32_t phase = 0;
@@ -431,8 +457,7 @@ norm_residual_bwd_ring_kernel(const Bwd p, const Ring ring)
         const unsigned char *slot = s_ring + s_at * ring.slot;
         const __nv_bfloat16 *dz_r = reinterpret_cast<const __nv_bfloat16 *>(slot + ring.at_dz);
         const __nv_bfloat16 *y_r = reinterpret_cast<const __nv_bfloat16 *>(slot + ring.at_y);
-        const __nv_bfloat16 *g_r =
-            gate_tok ? reinterpret_cast<const __nv_bfloat16 *>(slot + ring.at_gate) : p.gate;
+        const __nv_bfloat16 *g_r = reinterpret_cast<const __nv_bfloat16 *>(slot + ring.at_gate);
         ok = __all_sync(0xffffffffu, sm100::mbar_wait(sm100::smem_addr(&s_full[s_at]), phase, &never, kWaitBudget));
         if (++s_at == ring.stages) {
             s_at = 0;
@@ -444,12 +469,12 @@ norm_residual_bwd_ring_kernel(const Bwd p, const Ring ring)
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
                 const int v = i * group + threadIdx.x;
-                one_piece();
+                if constexpr (!WR) one_piece();
                 if (v >= nvec) continue;
                 float h[4], dz[4], w[4];
                 get4<F32>(slot, 4 * v, h);
                 get4<false>(dz_r, 4 * v, dz);
-                get4<false>(p.w_pre, 4 * v, w);
+                weight4(p.w_pre, r_pre, i, v, w);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     ss = fmaf(h[e], h[e], ss);
@@ -480,7 +505,7 @@ norm_residual_bwd_ring_kernel(const Bwd p, const Ring ring)
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int v = i * group + threadIdx.x;
-            one_piece();
+            if constexpr (!WR) one_piece();
 #pragma unroll
             for (int e = 0; e < 4; ++e) dH[i][e] = 0.f;
             if (v >= nvec) continue;
@@ -489,7 +514,7 @@ norm_residual_bwd_ring_kernel(const Bwd p, const Ring ring)
                 float h[4], dz[4], w[4];
                 get4<F32>(slot, 4 * v, h);
                 get4<false>(dz_r, 4 * v, dz);
-                get4<false>(p.w_pre, 4 * v, w);
+                weight4(p.w_pre, r_pre, i, v, w);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     dH[i][e] = fmaf(r2, fmaf(dz[e], w[e], -h[e] * c2), dH[i][e]);
@@ -501,8 +526,9 @@ norm_residual_bwd_ring_kernel(const Bwd p, const Ring ring)
                 // second reduction: sum y^2 and sum du w_post y
                 float y[4], w[4], g[4];
                 get4<false>(y_r, 4 * v, y);
-                get4<false>(p.w_post, 4 * v, w);
-                if (p.gate) get4<false>(g_r, 4 * v, g);
+                weight4(p.w_post, r_post, i, v, w);
+                if (gate_tok) get4<false>(g_r, 4 * v, g);
+                else if (p.gate) weight4(p.gate, r_gate, i, v, g);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float du = p.scale * dH[i][e] * (p.gate ? g[e] : 1.f);
@@ -520,12 +546,13 @@ norm_residual_bwd_ring_kernel(const Bwd p, const Ring ring)
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int v = i * group + threadIdx.x;
-            one_piece();
+            if constexpr (!WR) one_piece();
             if (v >= nvec) continue;
             float y[4], w[4], g[4], dy[4], dg[4];
             if (p.y) get4<false>(y_r, 4 * v, y);
-            if (p.gate) get4<false>(g_r, 4 * v, g);
-            if (p.w_post) get4<false>(p.w_post, 4 * v, w);
+            if (gate_tok) get4<false>(g_r, 4 * v, g);
+                else if (p.gate) weight4(p.gate, r_gate, i, v, g);
+            if (p.w_post) weight4(p.w_post, r_post, i, v, w);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float d = p.scale * dH[i][e];
@@ -635,7 +662,7 @@ template <bool F32> cudaError_t launch_fwd(const Fwd &p, int num_sms, cudaStream
 
 constexpr int kRingBytes = 224 * 1024;     // shared memory of an SM that the rings share
 
-template <int NP, bool F32>
+template <int NP, bool F32, bool WR>
 cudaError_t launch_ring(const Bwd &p, int32_t *status, int num_sms, unsigned *blocks, cudaStream_t stream)
 {
     const int res_b = (F32 ? 4 : 2) * p.C, row_b = 2 * p.C;
@@ -663,7 +690,7 @@ cudaError_t launch_ring(const Bwd &p, int32_t *status, int num_sms, unsigned *bl
     if (most > kNormResidualParts) most = kNormResidualParts;
     *blocks = (unsigned)(p.T < most ? p.T : most);
     if (*blocks == 0) return cudaSuccess;
-    auto kern = norm_residual_bwd_ring_kernel<NP, F32>;
+    auto kern = norm_residual_bwd_ring_kernel<NP, F32, WR>;
     static DeviceOnce once;
     cudaError_t e = once.run([&] {
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
@@ -692,9 +719,11 @@ cudaError_t launch_bwd(const Bwd &p, const SumOut &o, int32_t *status, int num_s
             e = cudaGetLastError();
         }
     } else if (p.C <= 4096) {
-        e = launch_ring<2, F32>(p, status, num_sms, &blocks, stream);
+        e = launch_ring<2, F32, true>(p, status, num_sms, &blocks, stream);
+    } else if (p.C <= 6144) {
+        e = launch_ring<4, F32, true>(p, status, num_sms, &blocks, stream);
     } else {
-        e = launch_ring<4, F32>(p, status, num_sms, &blocks, stream);
+        e = launch_ring<4, F32, false>(p, status, num_sms, &blocks, stream);
     }
     if (e != cudaSuccess || p.n_sum == 0) return e;
     return launch_column_sum(p.part, (int)blocks * rows, p.n_sum, p.C, o.out[0], o.out[1], o.out[2], stream);
