@@ -18,9 +18,10 @@
 // first pass (read from shared memory) and by the row in the second.
 //
 // Roles of a block (384 threads, one per SM, persistent over the item list):
-//   warp 0       TMA producer: X tiles (two buffers) and a ring of Y tiles of BN rows
+//   warp 0       TMA producer: the X tiles and a ring of Y tiles of BN rows
 //   warp 1       TMEM owner and MMA issuer: acc(j) as soon as P, dS of tile j are stored, then S, dP of
 //                tile j + 2 into the TMEM stage that tile j leaves (MMAs of one thread run in order)
+//   warps 2, 3   dk, dv: the statistics of each softmax group's next tile into shared memory
 //   warps 4-7, 8-11  the two softmax groups take alternate tiles: S, dP -> registers -> P, dS -> TMEM
 //                over their own S and dP columns; at an item's end they write dk and dv (or half of dq each)
 // TMEM (512 columns): A1 | A2 | two stages of S and dP (BN columns each). BN is 64 at head_dim 128 and 80
@@ -46,7 +47,7 @@ constexpr int kSoftmaxRegs = 208;
 static_assert(128 * kCtrlRegs + 256 * kSoftmaxRegs <= kThreads * kLaunchRegs, "register split exceeds the launch pool");
 constexpr int BM = 128;
 constexpr long long kWaitBudget = 4000000000ll;
-constexpr int kMaxY = 4;
+constexpr int kMaxY = 6;
 
 template <int D> struct GradCfg {
     static constexpr int BN = D == 128 ? 64 : 80;          // streamed rows per tile
@@ -56,8 +57,11 @@ template <int D> struct GradCfg {
     static constexpr int X_SLAB = BM * SW, Y_SLAB = BN * SW;
     static constexpr int X_TILE = NS * X_SLAB, Y_TILE = NS * Y_SLAB;
     static constexpr int Y_PAIR = (2 * Y_TILE + 1023) / 1024 * 1024;
-    static constexpr int NY = D == 128 ? 3 : 4;            // Y ring slots
-    static constexpr int OFF_Y = 4 * X_TILE;               // two X buffers of two tiles
+    static constexpr int BUDGET = 227 * 1024 - 1024 - 1280;   // without the alignment, the statistics and barriers
+    // two X buffers, so that an item's tiles arrive while the one before it runs (with one, its Y loads wait as
+    // well: 4 x 2048 x 4096 at head_dim 80 took 275 instead of 235 us for dq), and as many Y slots as fit, up to 6
+    static constexpr int NY = (BUDGET - 4 * X_TILE) / Y_PAIR > 6 ? 6 : (BUDGET - 4 * X_TILE) / Y_PAIR;
+    static constexpr int OFF_Y = 4 * X_TILE;
     static constexpr int DATA = OFF_Y + NY * Y_PAIR;
     static constexpr int SMEM = DATA + 1024 > 118 * 1024 ? DATA + 1024 : 118 * 1024;   // one block per SM
     static constexpr int LAYOUT = SW == 128 ? 2 : SW == 64 ? 4 : 6;
@@ -116,7 +120,7 @@ cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_consta
             mbar_init(bar_addr(bars.x_empty[i]), 1);
             mbar_init(bar_addr(bars.s_full[i]), 1);
             mbar_init(bar_addr(bars.p_full[i]), 4);
-            mbar_init(bar_addr(bars.stat[i]), 4);        // the four warps of a group
+            mbar_init(bar_addr(bars.stat[i]), 1);
         }
         for (int i = 0; i < NY; ++i) {
             mbar_init(bar_addr(bars.y_full[i]), 1);
@@ -217,43 +221,74 @@ cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_consta
         const uint32_t a_x = smem_addr(base), a_y = smem_addr(base + C::OFF_Y);
         const uint64_t dx0 = smem_desc(a_x, 16, 8 * C::SW, C::LAYOUT), dy0 = smem_desc(a_y, 16, 8 * C::SW, C::LAYOUT);
         const uint64_t dm0 = smem_desc(a_y, C::Y_SLAB, 8 * C::SW, C::LAYOUT);      // the same tile, MN-major
-        uint32_t xc = 0, u0 = 0;                             // items and tiles before this item
+        uint32_t xc = 0;                                     // items before this item
         bool ok = true;
         const bool leader = elect_one();
         auto uni = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
-        // S and dP of a tile (global count u, `valid` rows of the sequence) into its stage
-        auto products = [&](uint32_t u, int valid, uint32_t xb, bool last) -> bool {
-            const uint32_t s = u % NY, st = u & 1;
-            if (!(ok = wait_warp(bars.y_full[s], (u / NY) & 1))) return false;
-            if (valid & 15) {                                // rows past the end, up to the 16-row step's end
-                unsigned char *y = base + C::OFF_Y + s * C::Y_PAIR;
-                const int n = 16 - (valid & 15);
-                for (int x = lane; x < n * C::NS * (W / 8) * (DKV ? 2 : 1); x += 32) {
-                    const int r = valid + x % n, c = x / n % (W / 8), sl = x / n / (W / 8);   // every 16 bytes of the row
-                    *reinterpret_cast<uint4 *>(y + (sl / C::NS) * C::Y_TILE + (sl % C::NS) * C::Y_SLAB + r * C::SW +
-                                               16 * c) = make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
+        // the 16-row step in which a tile's `valid` rows end: its rows past them are zeroed
+        auto zero_tail = [&](uint32_t slot, int valid) {
+            if (!(valid & 15)) return;
+            unsigned char *y = base + C::OFF_Y + slot * C::Y_PAIR;
+            const int n = 16 - (valid & 15);
+            for (int x = lane; x < n * C::NS * (W / 8) * (DKV ? 2 : 1); x += 32) {
+                const int r = valid + x % n, c = x / n % (W / 8), sl = x / n / (W / 8);   // every 16 bytes of the row
+                *reinterpret_cast<uint4 *>(y + (sl / C::NS) * C::Y_TILE + (sl % C::NS) * C::Y_SLAB + r * C::SW + 16 * c) =
+                    make_uint4(0u, 0u, 0u, 0u);
             }
-            tc_fence_after();
-            const uint32_t tS = tmem + C::TSTAGE + st * 2 * BN;
-            const uint64_t dx = dx0 + ((xb * 2 * C::X_TILE) >> 4), dy = dy0 + ((s * C::Y_PAIR) >> 4);
-            const uint32_t full = bar_addr(bars.s_full[st]), empty = bar_addr(bars.x_empty[xb]);
-            if (leader) {
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        constexpr int PER = W / 16;
-                        const uint32_t ox = w * C::X_TILE + (kk / PER) * C::X_SLAB + (kk % PER) * 32;
-                        const uint32_t oy = w * C::Y_TILE + (kk / PER) * C::Y_SLAB + (kk % PER) * 32;
-                        mma_ss(tS + w * BN, dx + (ox >> 4), dy + (oy >> 4), ID_S, kk > 0 ? 1u : 0u);
-                    }
-                mma_commit(full);
-                if (last) mma_commit(empty);
-            }
+            fence_proxy_async_smem();
             __syncwarp();
+        };
+        // leader: S and dP of a tile into its stage, in turn. The operands' places are worked out by the whole warp:
+        // inside the elected thread's branch the compiler no longer knows them to be uniform, and every MMA waits
+        // for its operands to be made so. Between the two groups of MMAs of a tile, and before the next tile's,
+        // there is little arithmetic: the tensor pipe holds only about four MMAs while the issuer does other things.
+        auto products = [&](uint32_t tS, uint64_t dx, uint64_t dy, uint32_t full) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    constexpr int PER = W / 16;
+                    const uint32_t ox = w * C::X_TILE + (kk / PER) * C::X_SLAB + (kk % PER) * 32;
+                    const uint32_t oy = w * C::Y_TILE + (kk / PER) * C::Y_SLAB + (kk % PER) * 32;
+                    mma_ss(tS + w * BN, dx + (ox >> 4), dy + (oy >> 4), ID_S, kk > 0 ? 1u : 0u);
+                }
+            mma_commit(full);
+        };
+        // leader: the tile's part of the sums
+        auto sums = [&](uint32_t tS, uint64_t dm, int steps, uint32_t acc, uint32_t empty) {
+            auto step = [&](int kk) {
+                if constexpr (DKV)
+                    mma_ts(tmem + C::TA2, tS + kk * 8, dm + ((C::Y_TILE + kk * 16 * C::SW) >> 4), ID_ACC, kk > 0 ? 1u : acc);
+                mma_ts(tmem + C::TA1, tS + BN + kk * 8, dm + ((kk * 16 * C::SW) >> 4), ID_ACC, kk > 0 ? 1u : acc);
+            };
+            if (steps == BN / 16) {
+#pragma unroll
+                for (int kk = 0; kk < BN / 16; ++kk) step(kk);
+            } else {
+                for (int kk = 0; kk < steps; ++kk) step(kk);
+            }
+            mma_commit(empty);
+        };
+        // the next tile to start: its ring slot and phase, and its operand; the next to add up; the stage of both
+        constexpr uint32_t Y_STEP = C::Y_PAIR >> 4;
+        uint32_t s_p = 0, ph_p = 0, s_a = 0, st = 0, ph_s = 0;
+        uint64_t dy = dy0, dm = dm0;
+        uint32_t tS = tmem + C::TSTAGE;
+        constexpr uint32_t TS_SUM = 2 * C::TSTAGE + 2 * BN;   // of the two stages' columns
+        const uint32_t a_sfull = bar_addr(bars.s_full[0]), a_yempty = bar_addr(bars.y_empty[0]);
+        auto start = [&](uint64_t dx, uint32_t x_empty, int valid, bool last, uint32_t stage, uint32_t t) -> bool {
+            if (!(ok = wait_warp(bars.y_full[s_p], ph_p))) return false;
+            zero_tail(s_p, valid);
+            tc_fence_after();
+            if (leader) products(t, dx, dy, a_sfull + 8 * stage);
+            if (last && leader) mma_commit(x_empty);
+            __syncwarp();
+            dy += Y_STEP;
+            if (++s_p == (uint32_t)NY) {
+                s_p = 0;
+                dy = dy0;
+                ph_p ^= 1u;
+            }
             return true;
         };
         for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
@@ -261,48 +296,41 @@ cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_consta
             const int n = uni(it.j1 - it.j0);
             if (n <= 0) continue;
             // tiles follow one another inside a head pack; the last one of a pack holds `tail` rows
-            const int nt = DKV ? uni((it.ln + y_tok - 1) / y_tok) : (it.ln + BN - 1) / BN;
-            const int tail = uni(valid_rows(it, nt - 1));
+            const int nt = DKV ? uni((it.ln + y_tok - 1) / y_tok) : uni((it.ln + BN - 1) / BN);
+            const int tail = uni(valid_rows(it, nt - 1)), tail_steps = (tail + 15) >> 4;
             int pj = uni(it.j0 % nt), aj = pj;               // place in its pack of the next tile to start, to add up
-            auto next = [&](int &x) {
-                const int v = x + 1 == nt ? tail : BN;
-                x = x + 1 == nt ? 0 : x + 1;
-                return v;
+            auto next_valid = [&]() {
+                const bool end = ++pj == nt;
+                pj = end ? 0 : pj;
+                return end ? tail : BN;
             };
-            const uint32_t xb = xc & 1;
+            const uint32_t xb = xc & 1, x_empty = bar_addr(bars.x_empty[0]) + 8 * xb;
+            const uint64_t dx = dx0 + xb * (2 * C::X_TILE >> 4);
             if (!(ok = wait_warp(bars.x_full[xb], (xc / 2) & 1))) break;
-            if (!products(u0, next(pj), xb, n == 1)) break;
-            if (n > 1 && !products(u0 + 1, next(pj), xb, n == 2)) break;
+            if (!start(dx, x_empty, next_valid(), n == 1, st, tS)) break;
+            if (n > 1 && !start(dx, x_empty, next_valid(), n == 2, st ^ 1u, tmem + (TS_SUM - (tS - tmem)))) break;
+            if (xc > 0 && !(ok = wait_warp(bars.acc_free, (xc - 1) & 1))) break;
+            uint32_t acc = 0;
             for (int j = 0; j < n; ++j) {
-                const uint32_t u = u0 + j, s = u % NY, st = u & 1;
-                if (j == 0 && xc > 0 && !(ok = wait_warp(bars.acc_free, (xc - 1) & 1))) break;
-                const int steps = (next(aj) + 15) >> 4;
-                if (!(ok = wait_warp(bars.p_full[st], (u / 2) & 1))) break;
+                const bool end = ++aj == nt;
+                aj = end ? 0 : aj;
+                if (!(ok = wait_warp(bars.p_full[st], ph_s))) break;
                 tc_fence_after();
-                const uint32_t tP = tmem + C::TSTAGE + st * 2 * BN, tDS = tP + BN;
-                const uint64_t dm = dm0 + ((s * C::Y_PAIR) >> 4);
-                const uint32_t acc = j > 0 ? 1u : 0u, empty = bar_addr(bars.y_empty[s]);
-                if (leader) {
-                    auto sums = [&](int kk) {
-                        if constexpr (DKV)
-                            mma_ts(tmem + C::TA2, tP + kk * 8, dm + ((C::Y_TILE + kk * 16 * C::SW) >> 4), ID_ACC,
-                                   kk > 0 ? 1u : acc);
-                        mma_ts(tmem + C::TA1, tDS + kk * 8, dm + ((kk * 16 * C::SW) >> 4), ID_ACC, kk > 0 ? 1u : acc);
-                    };
-                    if (steps == BN / 16) {
-#pragma unroll
-                        for (int kk = 0; kk < BN / 16; ++kk) sums(kk);
-                    } else {
-                        for (int kk = 0; kk < steps; ++kk) sums(kk);
-                    }
-                    mma_commit(empty);
-                    if (j + 1 == n) mma_commit(bar_addr(bars.acc_done));
-                }
+                if (leader) sums(tS, dm, end ? tail_steps : BN / 16, acc, a_yempty + 8 * s_a);
+                if (j + 1 == n && leader) mma_commit(bar_addr(bars.acc_done));
                 __syncwarp();
+                acc = 1;
+                dm += Y_STEP;
+                if (++s_a == (uint32_t)NY) {
+                    s_a = 0;
+                    dm = dm0;
+                }
                 // the stage is free: its softmax group has read it, and the MMAs above run first
-                if (j + 2 < n && !products(u + 2, next(pj), xb, j + 3 == n)) break;
+                if (j + 2 < n && !start(dx, x_empty, next_valid(), j + 3 == n, st, tS)) break;
+                tS = tmem + (TS_SUM - (tS - tmem));
+                ph_s ^= st;                                  // both stages share a phase: it turns after stage 1
+                st ^= 1u;
             }
-            u0 += n;
             ++xc;
         }
         if (leader) {
@@ -311,10 +339,55 @@ cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_consta
             mbar_wait(bar_addr(bars.drain), 0, (const volatile int *)&s_abort, ok ? kWaitBudget : 200000000ll);
         }
         __syncwarp();
+    } else if (DKV && warp < 4) {
+        // ------------------------------------------------------------ statistics of the streamed columns
+        // Warp 2 + g stores those of group g's next tile as soon as every warp of the group has finished the one
+        // before (the group's tiles share a TMEM stage, and p_full is their last arrival), read a tile ahead.
+        const int grp = warp - 2;
+        constexpr int PER = (BN + 31) / 32;
+        uint32_t u0 = 0;
+        bool ok = true;
+        for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
+            const GradItem it = p.items[i];
+            const int n = max(0, it.j1 - it.j0);
+            if (n == 0) continue;
+            const int nt = (it.ln + y_tok - 1) / y_tok;
+            float2 v[PER];
+            auto fetch = [&](int j) {
+                if (j >= it.j1) return;
+                const int valid = valid_rows(it, j), tok0 = it.l0 + j % nt * y_tok;
+                const int head0 = it.head * p.group + ((j / nt) << p.lg_pack);
+#pragma unroll
+                for (int e = 0; e < PER; ++e) {
+                    const int c = lane + 32 * e;
+                    v[e] = make_float2(0.f, 0.f);
+                    if (c < valid)
+                        v[e] = p.stats[(int64_t)(tok0 + (c >> p.lg_pack)) * p.Hq + head0 + (c & ((1 << p.lg_pack) - 1))];
+                }
+            };
+            int j = it.j0 + (int)((u0 ^ (uint32_t)grp) & 1);
+            fetch(j);
+            for (; j < it.j1; j += 2) {
+                const uint32_t u = u0 + (j - it.j0);
+                if (u >= 2 && !(ok = wait_warp(bars.p_full[grp], (u / 2 - 1) & 1))) break;
+#pragma unroll
+                for (int e = 0; e < PER; ++e) {
+                    const int c = lane + 32 * e;
+                    if (c < BN) {
+                        s_stat[grp][0][c] = v[e].x;
+                        s_stat[grp][1][c] = v[e].y;
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_addr(bars.stat[grp]));
+                fetch(j + 2);
+            }
+            u0 += n;
+        }
     } else if (warp >= 4) {
         // ------------------------------------------------------------ softmax groups
         regs_inc<kSoftmaxRegs>();
-        const int grp = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane, gt = threadIdx.x - 128 - 128 * grp;
+        const int grp = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
         uint32_t u0 = 0, xc = 0;                              // tiles and items with tiles before this item
         bool ok = true;
@@ -335,29 +408,12 @@ cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_consta
             if constexpr (!DKV) {
                 if (exists && n > 0) st_row = p.stats[(int64_t)o_row * p.Hq + o_head];
             }
-            const int nt = DKV ? (it.ln + y_tok - 1) / y_tok : 0;
-            for (int j = it.j0 + (int)((u0 ^ (uint32_t)grp) & 1); j < it.j1; j += 2) {
+            const float *nl = s_stat[grp][0], *nd = s_stat[grp][1];
+            const int j_first = it.j0 + (int)((u0 ^ (uint32_t)grp) & 1);
+            for (int j = j_first; j < it.j1; j += 2) {
                 const uint32_t u = u0 + (j - it.j0), st = u & 1;
                 const int valid = valid_rows(it, j);
-                const float *nl = s_stat[grp][0], *nd = s_stat[grp][1];
                 if constexpr (DKV) {
-                    // the statistics of the tile's columns, fetched while S is still being computed and stored once
-                    // every warp of the group has finished its previous tile (the group's tiles share a stage)
-                    float2 v = make_float2(0.f, 0.f);
-                    if (gt < BN) {
-                        if (gt < valid) {
-                            const int64_t tok = it.l0 + j % nt * y_tok + (gt >> p.lg_pack);
-                            const int head = it.head * p.group + ((j / nt) << p.lg_pack) + (gt & ((1 << p.lg_pack) - 1));
-                            v = p.stats[tok * p.Hq + head];
-                        }
-                    }
-                    if (u >= 2 && !(ok = wait_warp(bars.p_full[st], (u / 2 - 1) & 1))) break;
-                    if (gt < BN) {
-                        s_stat[grp][0][gt] = v.x;
-                        s_stat[grp][1][gt] = v.y;
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar_addr(bars.stat[grp]));
                     if (!(ok = wait_warp(bars.stat[grp], (u / 2) & 1))) break;
                 }
                 if (!(ok = wait_warp(bars.s_full[st], (u / 2) & 1))) break;
@@ -373,12 +429,17 @@ cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_consta
                 reg_fence(dr);
                 const uint64_t sc2 = f2_splat(p.scale_log2);
                 const uint64_t nl_row = f2_splat(st_row.x), nd_row = f2_splat(st_row.y);
+                ulonglong2 l4, d4;
 #pragma unroll
                 for (int c = 0; c < BN; c += 2) {
                     uint64_t l2 = nl_row, d2 = nd_row;
                     if constexpr (DKV) {
-                        l2 = *reinterpret_cast<const uint64_t *>(nl + c);
-                        d2 = *reinterpret_cast<const uint64_t *>(nd + c);
+                        if (c % 4 == 0) {
+                            l4 = *reinterpret_cast<const ulonglong2 *>(nl + c);
+                            d4 = *reinterpret_cast<const ulonglong2 *>(nd + c);
+                        }
+                        l2 = c % 4 == 0 ? l4.x : l4.y;
+                        d2 = c % 4 == 0 ? d4.x : d4.y;
                     }
                     float x0, x1;
                     f2_split(f2_fma(f2_from_u32(sr[c], sr[c + 1]), sc2, l2), x0, x1);
