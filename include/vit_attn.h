@@ -548,9 +548,10 @@ size_t vit_cross_attn_bwd_workspace_size(int64_t Tq, int64_t Tk, int Hq, int Hkv
  *   dout         device bf16 [Tq, Hq, D]: gradient of out.
  *   out, lse     as the forward call wrote them for the same q, k, v, lists and scale.
  *   dq, dk, dv   device bf16 outputs [Tq, Hq, D], [Tk, Hkv, D], [Tk, Hkv, D]; dk and dv are summed
- *                over the query heads that share a key head. They must not overlap an input. Rows
- *                of no sequence (and key rows behind k_len) are left as they were; the gradients of
- *                a sequence without keys, or without queries, are 0.
+ *                over the query heads that share a key head. They must not overlap an input. The
+ *                gradients of a sequence without keys, or without queries, are 0.
+ *   zero_rest    0: rows of no sequence (and key rows behind k_len) are left as they were; else
+ *                they are set to 0.
  *   workspace    vit_cross_attn_bwd_workspace_size(...) bytes, 16-byte aligned; calls sharing one
  *                must not overlap.
  * S and dP are recomputed once for dq and once for dk and dv, P and dS rounded to bf16 for their
@@ -562,7 +563,8 @@ vit_status_t vit_cross_attn_bwd(const void *dout, const void *q, const void *k, 
                                 int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t out_stride,
                                 const int32_t *cu_q, const int32_t *cu_k, const int32_t *k_len, int B, int max_q,
                                 int max_k, float scale, void *dq, void *dk, void *dv, int64_t dq_stride,
-                                int64_t dk_stride, int64_t dv_stride, void *workspace, size_t workspace_bytes,
+                                int64_t dk_stride, int64_t dv_stride, int zero_rest, void *workspace,
+                                size_t workspace_bytes,
                                 int32_t *status_dev, vit_stream_t stream);
 
 /* Storage of the residual stream (vit_norm_residual). */

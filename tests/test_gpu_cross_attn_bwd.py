@@ -163,7 +163,7 @@ def test_one_side_empty():
     assert (dq == 0).all() and dk.shape == dv.shape == (0, 2, 64)
     buf = torch.full_like(k, 3.0), torch.full_like(k, 3.0)
     vit.cross_attn_bwd(none_q, none_q, k, k, none_q, torch.empty(0, 4, device="cuda"), cu(0, 0), cu(0, 150),
-                       dk=buf[0], dv=buf[1])
+                       dq=torch.empty_like(none_q), dk=buf[0], dv=buf[1])
     assert (buf[0] == 0).all() and (buf[1] == 0).all()
 
 

@@ -38,7 +38,7 @@ def _declare_block(L):
             ("vit_cross_attn", [vp] * 3 + [i64, i64, i32, i32, i32] + [i64] * 3 + [vp] * 3 + [i32, i32, i32, f32, vp,
                                                                                               i64, vp, vp, sz, vp, vp]),
             ("vit_cross_attn_bwd", [vp] * 6 + [i64, i64, i32, i32, i32] + [i64] * 5 + [vp] * 3 + [i32, i32, i32, f32] +
-             [vp] * 3 + [i64] * 3 + [vp, sz, vp, vp]),
+             [vp] * 3 + [i64] * 3 + [i32, vp, sz, vp, vp]),
             ("vit_norm_residual", [vp] * 7 + [i64, i32, i32] + [i64] * 5 + [f32, f32, vp]),
             ("vit_norm_residual_bwd", [vp] * 12 + [i64, i32, i32] + [i64] * 8 + [f32, f32, vp, sz, vp, vp])):
         fn = getattr(L, name)
@@ -692,25 +692,19 @@ def cross_attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
     _lse_ok(lse, Tq, Hq)
     B = _cross_lists(cu_q, cu_k, k_len)
     max_q, max_k = _max_seqlen(max_q), _max_seqlen(max_k)
-    nq, nk = Tq * Hq * D, Tk * Hkv * D
-    sizes = [n for n, t in ((nq, dq), (nk, dk), (nk, dv)) if t is None]
-    if sizes:      # one zeroed block for all of them
-        if stream is None:
-            made = q.new_zeros(sum(sizes))
-        else:
-            with torch.cuda.stream(stream):
-                made = q.new_zeros(sum(sizes))
-        made = list(made.split(sizes))
-        dq = made.pop(0).view(Tq, Hq, D) if dq is None else dq
-        dk = made.pop(0).view(Tk, Hkv, D) if dk is None else dk
-        dv = made.pop(0).view(Tk, Hkv, D) if dv is None else dv
+    given = [t is not None for t in (dq, dk, dv)]
+    if any(given) and not all(given):
+        raise ValueError("give all of dq, dk and dv, or none")
+    if not any(given):
+        dq, dk, dv = q.new_empty((Tq, Hq, D)), k.new_empty((Tk, Hkv, D)), k.new_empty((Tk, Hkv, D))
+        _made(stream, dq, dk, dv)
     dqs, dks, dvs = _rows3(dq, "dq", Tq, Hq, D), _rows3(dk, "dk", Tk, Hkv, D), _rows3(dv, "dv", Tk, Hkv, D)
     if workspace is None:
         workspace = _scratch(lib().vit_cross_attn_bwd_workspace_size(Tq, Tk, Hq, Hkv, D, B, max_q, max_k), q, stream)
     _call("vit_cross_attn_bwd", dev, stream, _addr(dout), _addr(q), _addr(k), _addr(v), _addr(out), _addr(lse), Tq,
           Tk, Hq, Hkv, D, dos, qs, ks, vs, os_, _addr(cu_q), _addr(cu_k), _addr(k_len), B, max_q, max_k,
-          0.0 if scale is None else float(scale), _addr(dq), _addr(dk), _addr(dv), dqs, dks, dvs, _addr(workspace),
-          _bytes(workspace), _addr(status))
+          0.0 if scale is None else float(scale), _addr(dq), _addr(dk), _addr(dv), dqs, dks, dvs,
+          0 if given[0] else 1, _addr(workspace), _bytes(workspace), _addr(status))
     return dq, dk, dv
 
 

@@ -292,7 +292,8 @@ vit_status_t vit_cross_attn_bwd(const void *dout, const void *q, const void *k, 
                                 int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t out_stride,
                                 const int32_t *cu_q, const int32_t *cu_k, const int32_t *k_len, int B, int max_q,
                                 int max_k, float scale, void *dq, void *dk, void *dv, int64_t dq_stride,
-                                int64_t dk_stride, int64_t dv_stride, void *workspace, size_t workspace_bytes,
+                                int64_t dk_stride, int64_t dv_stride, int zero_rest, void *workspace,
+                                size_t workspace_bytes,
                                 int32_t *status_dev, vit_stream_t stream)
 {
     TraceRange trace("vit_cross_attn_bwd");
@@ -345,6 +346,7 @@ vit_status_t vit_cross_attn_bwd(const void *dout, const void *q, const void *k, 
     a.dq_stride = dq_stride;
     a.dk_stride = dk_stride;
     a.dv_stride = dv_stride;
+    a.zero_rest = zero_rest != 0;
     return from_cuda(launch_cross_grad(a, grad_plan(Tq, Tk, B, Hq, Hkv, D, max_q, max_k), sms, (cudaStream_t)stream));
 }
 

@@ -99,6 +99,7 @@ struct LongPlan {
 };
 constexpr int kDesignSms = 152;
 LongPlan long_plan(int64_t Tq, int B, int Hq, int Hk, int D, int max_q, int max_k);
+int cross_pack(int group);     // log2 of P
 int attn_long_bn(int D);
 cudaError_t launch_cross_schedule(const CrossArgs &a, const LongPlan &p, int num_sms, WsHeader *hdr, CrossItem *items,
                                   CrossTile *tiles, cudaStream_t stream);
@@ -115,24 +116,23 @@ cudaError_t launch_cross_tile_join(const CrossArgs &a, const LongPlan &p, const 
 struct GradItem {
     int r0, r1, l0, ln;
     int head, j0, j1;
-    int slot;                     // place of the partial sums when the loop was cut, or -1
+    int pad;
 };
 static_assert(sizeof(GradItem) == 32, "two 16-byte words");
 
 struct GradPlan {
     int lg_pack;
     int64_t max_dq, max_dkv;      // bounds of the two item lists
-    size_t off_dq, off_dkv, off_stats, bytes;   // workspace layout; the two item counts are at 0
+    size_t off_dq, off_dkv, off_stats, bytes;   // workspace layout; at 0: the two lists' lengths
 };
 struct CrossGradArgs {
     CrossArgs f;                  // the forward call: its inputs, out and lse (read), workspace of this call
     const void *dout;             // bf16 [Tq, Hq, D]
     void *dq, *dk, *dv;
     int64_t dout_stride, dq_stride, dk_stride, dv_stride;
+    bool zero_rest;               // rows of no sequence get 0
 };
 GradPlan grad_plan(int64_t Tq, int64_t Tk, int B, int Hq, int Hk, int D, int max_q, int max_k);
-int cross_grad_bn(int D);
-cudaError_t launch_grad_schedule(const CrossGradArgs &a, const GradPlan &p, cudaStream_t stream);
 cudaError_t launch_cross_grad(const CrossGradArgs &a, const GradPlan &p, int num_sms, cudaStream_t stream);
 
 }  // namespace vit

@@ -15,13 +15,20 @@
 //            S = Q K^T, dP = dO V^T, dQ += dS K
 // which is the same kernel: two resident tiles X1, X2, two streamed ones Y1, Y2, S = X1 Y1^T,
 // dP = X2 Y2^T, A1 += dS Y1 and (dk, dv only) A2 += P Y2. Statistics go by the streamed side in the
-// first pass (read from shared memory) and by the row in the second.
+// first pass (read from shared memory) and by the row in the second. The passes do not depend on one
+// another: the second may start on SMs that the first has left (programmatic launch). One kernel for
+// both kinds of items was 10 % slower at large sizes (616 against 564 us at 4 x 2048 x 4096, 16 heads
+// of 80: the issuer's loop compiles worse).
+//
+// Before them, one launch makes the two item lists (a block each) and the statistics -lse log2(e) and
+// -delta of every (token, head) (the other blocks).
 //
 // Roles of a block (384 threads, one per SM, persistent over the item list):
 //   warp 0       TMA producer: the X tiles and a ring of Y tiles of BN rows
 //   warp 1       TMEM owner and MMA issuer: acc(j) as soon as P, dS of tile j are stored, then S, dP of
 //                tile j + 2 into the TMEM stage that tile j leaves (MMAs of one thread run in order)
-//   warps 2, 3   dk, dv: the statistics of each softmax group's next tile into shared memory
+//   warps 2, 3   dk, dv: the statistics of each softmax group's next tile into shared memory; before that, where
+//                asked for, zeros into the rows that belong to no sequence
 //   warps 4-7, 8-11  the two softmax groups take alternate tiles: S, dP -> registers -> P, dS -> TMEM
 //                over their own S and dP columns; at an item's end they write dk and dv (or half of dq each)
 // TMEM (512 columns): A1 | A2 | two stages of S and dP (BN columns each). BN is 64 at head_dim 128 and 80
@@ -30,8 +37,11 @@
 // operand (of S and dP, reduced over D) and as an MN-major one (of the sums, reduced over rows).
 // Streamed rows past the sequence's end enter the sums with P = dS = 0 and are zeroed in shared memory
 // first (0 * NaN is NaN), the last 16-row step included.
+#include <limits.h>
+
 #include <type_traits>
 
+#include "block_sort.cuh"
 #include "cross.h"
 #include "sm100.cuh"
 
@@ -42,8 +52,8 @@ using namespace sm100;
 
 constexpr int kThreads = 384;
 constexpr int kLaunchRegs = 168;
-constexpr int kCtrlRegs = 88;
-constexpr int kSoftmaxRegs = 208;
+constexpr int kCtrlRegs = 96;
+constexpr int kSoftmaxRegs = 200;
 static_assert(128 * kCtrlRegs + 256 * kSoftmaxRegs <= kThreads * kLaunchRegs, "register split exceeds the launch pool");
 constexpr int BM = 128;
 constexpr long long kWaitBudget = 4000000000ll;
@@ -67,7 +77,7 @@ template <int D> struct GradCfg {
     static constexpr int LAYOUT = SW == 128 ? 2 : SW == 64 ? 4 : 6;
     static constexpr int TA1 = 0, TA2 = D, TSTAGE = 2 * D; // TMEM columns; stage s: S at TSTAGE + 2 BN s, dP BN further
     static_assert(TSTAGE + 4 * BN <= 512, "TMEM budget");
-    static_assert(SMEM + 1280 <= 227 * 1024, "shared memory per block, with the statistics and barriers");
+    static_assert(SMEM + (D == 128 ? 1280 : 1536) <= 227 * 1024, "shared memory per block, with the statistics and barriers");
     static_assert(X_TILE % 1024 == 0 && Y_SLAB % (8 * SW) == 0 && Y_TILE % (8 * SW) == 0, "slabs start on swizzle atoms");
     static_assert(NY <= kMaxY && BN % 16 == 0, "tile shapes");
 };
@@ -88,12 +98,13 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
 struct Grad {
     const GradItem *items;
     const int32_t *n_items;
+    CrossSegs segs;
+    bool zero_rest;               // rows of no sequence get 0
     const float2 *stats;          // [Tq, Hq] {-lse log2(e), -delta}
     __nv_bfloat16 *out1, *out2;   // dk, dv; or dq
     int64_t out1_stride, out2_stride;
-    int Hq, group, lg_pack;
+    int Hq, Hk, group, lg_pack;
     float scale, scale_log2;
-    float *part;                  // partial sums of items whose loop was cut
     int32_t *status;
 };
 
@@ -112,7 +123,6 @@ cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_consta
     __shared__ __align__(16) float s_stat[2][2][BN];       // [group][-lse2 | -delta][column]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n_items = *p.n_items;
     if (threadIdx.x == 0) {
         s_abort = 0;
         for (int i = 0; i < 2; ++i) {
@@ -139,6 +149,11 @@ cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
+    // dk, dv: the lists and statistics are there when the launch before this one is done. dq is launched behind
+    // dk, dv, which has waited for them, and waits for that pass only before it ends.
+    if constexpr (DKV) grid_wait();
+    grid_release();
+    const int n_items = *p.n_items;
 
     auto wait = [&](const uint64_t &b, uint32_t parity) -> bool {
         if (mbar_wait(bar_addr(b), parity, (const volatile int *)&s_abort, kWaitBudget)) return true;
@@ -339,7 +354,37 @@ cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_consta
             mbar_wait(bar_addr(bars.drain), 0, (const volatile int *)&s_abort, ok ? kWaitBudget : 200000000ll);
         }
         __syncwarp();
-    } else if (DKV && warp < 4) {
+    } else if (warp < 4) {
+        if (p.zero_rest) {
+            // the rows between and around the sequences, dealt to both warps of all blocks; gap b lies before sequence
+            // b, and only k_len leaves gaps between sequences
+            const CrossSegs &s = p.segs;
+            const int64_t T = DKV ? s.Tk : s.Tq;
+            const int32_t *cu = DKV ? s.cu_k : s.cu_q, *len = DKV ? s.k_len : nullptr;
+            const int H = DKV ? p.Hk : p.Hq, gaps = len ? s.B + 1 : 2;
+            for (int g0 = 0; g0 < gaps; g0 += 32) {
+                const int b = len ? g0 + lane : lane * s.B;   // without k_len: gaps 0 and B
+                int lo = 0, hi = 0;
+                if (g0 + lane < gaps) {
+                    hi = b < s.B ? cu[b] : (int)T;
+                    if (b > 0) lo = len ? (int)min((int64_t)cu[b - 1] + len[b - 1], (int64_t)INT_MAX) : cu[b];
+                    if (lo < 0 || hi > T) hi = lo;
+                }
+                for (unsigned todo = __ballot_sync(0xffffffffu, lo < hi); todo; todo &= todo - 1) {
+                    const int src = __ffs(todo) - 1;
+                    const int end = __shfl_sync(0xffffffffu, hi, src);
+                    for (int64_t r = __shfl_sync(0xffffffffu, lo, src) + (int64_t)(2 * blockIdx.x + warp - 2); r < end;
+                         r += 2 * gridDim.x)
+                        for (int c = lane; c < H * (D / 8); c += 32) {
+                            const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+                            *reinterpret_cast<uint4 *>(p.out1 + r * p.out1_stride + 8 * c) = z;
+                            if constexpr (DKV) *reinterpret_cast<uint4 *>(p.out2 + r * p.out2_stride + 8 * c) = z;
+                        }
+                }
+            }
+            __syncwarp();
+        }
+        if constexpr (DKV) {
         // ------------------------------------------------------------ statistics of the streamed columns
         // Warp 2 + g stores those of group g's next tile as soon as every warp of the group has finished the one
         // before (the group's tiles share a TMEM stage, and p_full is their last arrival), read a tile ahead.
@@ -383,6 +428,7 @@ cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_consta
                 fetch(j + 2);
             }
             u0 += n;
+        }
         }
     } else if (warp >= 4) {
         // ------------------------------------------------------------ softmax groups
@@ -485,7 +531,6 @@ cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_consta
                 ++xc;
                 tc_fence_after();
             }
-            float *part = p.part + ((int64_t)it.slot * 2 + (DKV ? grp : 0)) * (BM * D) + row * D + col0;
 #pragma unroll
             for (int c = 0; c < COLS; c += 8) {
                 uint32_t r[8];
@@ -497,18 +542,11 @@ cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_consta
 #pragma unroll
                     for (int e = 0; e < 8; ++e) r[e] = 0u;
                 }
-                float v[8];
+                uint32_t o[4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(r[e]) * f;
-                if (exists) {
-                    if (it.slot < 0) {
-                        *reinterpret_cast<uint4 *>(dst + c) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                                         pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-                    } else {
-                        *reinterpret_cast<float4 *>(part + c) = make_float4(v[0], v[1], v[2], v[3]);
-                        *reinterpret_cast<float4 *>(part + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
-                    }
-                }
+                for (int e = 0; e < 4; ++e)
+                    o[e] = pack_bf16x2(__uint_as_float(r[2 * e]) * f, __uint_as_float(r[2 * e + 1]) * f);
+                if (exists) *reinterpret_cast<uint4 *>(dst + c) = make_uint4(o[0], o[1], o[2], o[3]);
             }
             if (n > 0) {
                 tc_fence_before();
@@ -523,35 +561,129 @@ cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_consta
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    if constexpr (!DKV) grid_wait();       // what follows in the stream waits for this pass, and so for both
 }
 
-// {-lse log2(e), -delta} of every (token, head): D / 8 lanes per row, 16 bytes of o and do each.
-template <int D>
-__global__ void __launch_bounds__(256)
-cross_stats_kernel(const __nv_bfloat16 *__restrict__ out, const __nv_bfloat16 *__restrict__ dout,
-                   const float *__restrict__ lse, float2 *__restrict__ stats, int64_t rows, int Hq, int64_t out_stride,
-                   int64_t dout_stride)
+// ------------------------------------------------------------------ lists and statistics
+
+// One list of work items by one block of 1024 threads: the dk, dv tiles (`keys`, ordered by query
+// count) or the dq tiles (ordered by key count), longest loop first. Tiles without a loop are listed
+// too: their gradients are 0.
+__device__ void make_list(bool keys, const CrossSegs &segs, int Hq, int Hk, int lg_pack, int bn, int32_t *counts,
+                          GradItem *items, int32_t *status)
 {
+    constexpr int kThreads = kSortThreads;
+    extern __shared__ unsigned long long s_key[];
+    __shared__ int64_t s_warp[32];
+    __shared__ int s_bad;
+    const int tid = threadIdx.x, B = segs.B;
+    int NP = 1;
+    while (NP < B) NP <<= 1;
+    if (tid == 0) s_bad = 0;
+    __syncthreads();
+    for (int i = tid; i < NP; i += kThreads) {
+        CrossSeg x;
+        const bool fine = i < B && load_seg(segs, i, x, status, !keys);
+        if (i < B && (segs.cu_q[i + 1] < segs.cu_q[i] || segs.cu_k[i + 1] < segs.cu_k[i])) s_bad = 1;
+        const bool use = fine && (keys ? x.kn : x.qn) > 0;
+        s_key[i] = use ? ((unsigned long long)(0x7fffffffu - (uint32_t)(keys ? x.qn : x.kn)) << 32) | (uint32_t)i : ~0ull;
+    }
+    __syncthreads();
+    if (s_bad) {
+        if (tid == 0) counts[keys] = 0;
+        return;
+    }
+    block_sort(s_key, NP, tid);
+    const int lg_tile = keys ? 7 : 7 - lg_pack;        // rows (tokens) of a tile, log2
+    const int heads = keys ? Hk : Hq >> lg_pack;       // tiles side by side
+    const int per = (B + kThreads - 1) / kThreads, lo = min(tid * per, B), hi = min(lo + per, B);
+    auto seg_at = [&](int p, CrossSeg &x) -> bool {
+        if (s_key[p] == ~0ull) return false;
+        load_seg(segs, (int)(s_key[p] & 0xffffffffu), x, nullptr, false);
+        return true;
+    };
+    auto tiles_of = [&](const CrossSeg &x) { return ((keys ? x.kn : x.qn) + (1 << lg_tile) - 1) >> lg_tile; };
+    int64_t n = 0, total;
+    for (int p = lo; p < hi; ++p) {
+        CrossSeg x;
+        if (seg_at(p, x)) n += (int64_t)heads * tiles_of(x);
+    }
+    int64_t at = block_exclusive_scan(n, s_warp, &total);
+    for (int p = lo; p < hi; ++p) {
+        CrossSeg x;
+        if (!seg_at(p, x)) continue;
+        s_key[p] = ((unsigned long long)at << 32) | (uint32_t)(s_key[p] & 0xffffffffu);
+        at += (int64_t)heads * tiles_of(x);
+    }
+    __syncthreads();
+    const int lane = tid & 31, warp = tid >> 5;
+    for (int p = warp; p < B; p += kThreads / 32) {
+        if (s_key[p] == ~0ull) break;
+        CrossSeg x;
+        load_seg(segs, (int)(s_key[p] & 0xffffffffu), x, nullptr, false);
+        const int first = (int)(s_key[p] >> 32), nr = tiles_of(x);
+        GradItem it;
+        it.l0 = keys ? x.q0 : x.k0;
+        it.ln = keys ? x.qn : x.kn;
+        it.r1 = keys ? x.k0 + x.kn : x.q0 + x.qn;
+        it.j0 = 0;
+        const int step = keys ? bn >> lg_pack : bn;
+        it.j1 = (it.ln + step - 1) / step * (keys ? Hq / Hk >> lg_pack : 1);
+        it.pad = 0;
+        for (int i = lane; i < heads * nr; i += 32) {
+            const int h = i / nr, r = i - h * nr;
+            it.r0 = (keys ? x.k0 : x.q0) + (r << lg_tile);
+            it.head = keys ? h : h << lg_pack;
+            items[first + i] = it;
+        }
+    }
+    if (tid == 0) counts[keys] = (int32_t)total;
+}
+
+struct Prepare {
+    const __nv_bfloat16 *out, *dout;
+    const float *lse;
+    float2 *stats;                // {-lse log2(e), -delta} of every (token, head)
+    int64_t rows, out_stride, dout_stride;
+    CrossSegs segs;
+    int Hq, Hk, lg_pack;
+    int32_t *counts;
+    GradItem *dq, *dkv;
+    int32_t *status;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kSortThreads)
+cross_grad_prepare_kernel(const Prepare p)
+{
+    grid_release();
+    if (blockIdx.x < 2) {
+        make_list(blockIdx.x == 1, p.segs, p.Hq, p.Hk, p.lg_pack, GradCfg<D>::BN, p.counts,
+                  blockIdx.x == 1 ? p.dkv : p.dq, p.status);
+        return;
+    }
+    // D / 8 lanes per row, 16 bytes of o and do each
     constexpr int CH = D / 8, R = 32 / CH;
     const int lane = threadIdx.x & 31, g = lane / CH, c = lane % CH;
-    const int64_t warp = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5, n_warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-    for (int64_t r0 = warp * R; r0 < rows; r0 += n_warps * R) {
+    const int64_t warp = ((int64_t)(blockIdx.x - 2) * blockDim.x + threadIdx.x) >> 5;
+    const int64_t n_warps = ((int64_t)(gridDim.x - 2) * blockDim.x) >> 5;
+    for (int64_t r0 = warp * R; r0 < p.rows; r0 += n_warps * R) {
         const int64_t r = r0 + g;
-        const bool live = g < R && r < rows;
+        const bool live = g < R && r < p.rows;
         float s = 0.f;
         if (live) {
-            const int64_t t = r / Hq;
-            const int h = (int)(r - t * Hq);
+            const int64_t t = r / p.Hq;
+            const int h = (int)(r - t * p.Hq);
             float a[8], b[8];
-            rope::unpack8(*reinterpret_cast<const uint4 *>(out + t * out_stride + (int64_t)h * D + 8 * c), a);
-            rope::unpack8(*reinterpret_cast<const uint4 *>(dout + t * dout_stride + (int64_t)h * D + 8 * c), b);
+            rope::unpack8(*reinterpret_cast<const uint4 *>(p.out + t * p.out_stride + (int64_t)h * D + 8 * c), a);
+            rope::unpack8(*reinterpret_cast<const uint4 *>(p.dout + t * p.dout_stride + (int64_t)h * D + 8 * c), b);
 #pragma unroll
             for (int e = 0; e < 8; ++e) s = fmaf(a[e], b[e], s);
         }
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < CH; ++i) sum += __shfl_sync(0xffffffffu, s, (g * CH + i) & 31);
-        if (live && c == 0) stats[r] = make_float2(-lse[r] * 1.4426950408889634f, -sum);
+        if (live && c == 0) p.stats[r] = make_float2(-p.lse[r] * 1.4426950408889634f, -sum);
     }
 }
 
@@ -605,46 +737,85 @@ cudaError_t launch_pass(const CrossGradArgs &a, const GradPlan &pl, int num_sms,
     p.lg_pack = pl.lg_pack;
     p.scale = a.f.scale_log2 * 0.6931471805599453f;
     p.scale_log2 = a.f.scale_log2;
-    p.part = nullptr;
+    p.Hk = a.f.Hk;
+    p.segs = s;
+    p.zero_rest = a.zero_rest;
     p.status = a.f.status;
-    const int64_t most = DKV ? pl.max_dkv : pl.max_dq;
+    // zeros are dealt to every SM; an empty pass is launched all the same, for its place in the chain of launches
+    const int64_t list = DKV ? pl.max_dkv : pl.max_dq, most = a.zero_rest ? num_sms : list > 0 ? list : 1;
     const unsigned blocks = (unsigned)(most < num_sms ? most : num_sms);
-    if (blocks == 0) return cudaSuccess;
     LaunchScope scope(DKV ? "cross_grad_dkv" : "cross_grad_dq", stream);
-    if (DKV)
-        kern<<<blocks, kThreads, C::SMEM, stream>>>(k, v, q, dq, p);
-    else
-        kern<<<blocks, kThreads, C::SMEM, stream>>>(q, dq, k, v, p);
-    return cudaGetLastError();
+    return DKV ? launch_chained(kern, blocks, kThreads, C::SMEM, stream, k, v, q, dq, p)
+               : launch_chained(kern, blocks, kThreads, C::SMEM, stream, q, dq, k, v, p);
 }
 
 template <int D> cudaError_t launch_d(const CrossGradArgs &a, const GradPlan &pl, int num_sms, cudaStream_t stream)
 {
-    const int64_t rows = a.f.segs.Tq * a.f.Hq;
-    if (rows > 0) {
-        constexpr int per = 8 * (32 / (D / 8));
-        const int64_t want = (rows + per - 1) / per, cap = (int64_t)num_sms * 32;
-        LaunchScope scope("cross_stats", stream);
-        cross_stats_kernel<D><<<(unsigned)(want < cap ? want : cap), 256, 0, stream>>>(
-            static_cast<const __nv_bfloat16 *>(a.f.out), static_cast<const __nv_bfloat16 *>(a.dout), a.f.lse,
-            reinterpret_cast<float2 *>(static_cast<char *>(a.f.workspace) + pl.off_stats), rows, a.f.Hq,
-            a.f.out_stride, a.dout_stride);
-        const cudaError_t e = cudaGetLastError();
+    const CrossSegs &s = a.f.segs;
+    char *ws = static_cast<char *>(a.f.workspace);
+
+    Prepare r;
+    r.out = static_cast<const __nv_bfloat16 *>(a.f.out);
+    r.dout = static_cast<const __nv_bfloat16 *>(a.dout);
+    r.lse = a.f.lse;
+    r.stats = reinterpret_cast<float2 *>(ws + pl.off_stats);
+    r.rows = s.Tq * a.f.Hq;
+    r.out_stride = a.f.out_stride;
+    r.dout_stride = a.dout_stride;
+    r.segs = s;
+    r.Hq = a.f.Hq;
+    r.Hk = a.f.Hk;
+    r.lg_pack = pl.lg_pack;
+    r.counts = reinterpret_cast<int32_t *>(ws);
+    r.dq = reinterpret_cast<GradItem *>(ws + pl.off_dq);
+    r.dkv = reinterpret_cast<GradItem *>(ws + pl.off_dkv);
+    r.status = a.f.status;
+    int np = 1;
+    while (np < s.B) np <<= 1;
+    static DeviceOnce once_prepare;
+    cudaError_t e = once_prepare.run([] {
+        return cudaFuncSetAttribute(cross_grad_prepare_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)sizeof(unsigned long long) * VIT_MAX_SEGMENTS);
+    });
+    if (e != cudaSuccess) return e;
+    {
+        constexpr int per = 32 * (32 / (D / 8));             // rows of a block at a time
+        const int64_t want = (r.rows + per - 1) / per, cap = (int64_t)num_sms * 8;
+        LaunchScope scope("cross_grad_prepare", stream);
+        cross_grad_prepare_kernel<D><<<2 + (unsigned)(want < cap ? want : cap), kSortThreads,
+                                       sizeof(unsigned long long) * (size_t)np, stream>>>(r);
+        e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    cudaError_t e = launch_pass<D, true>(a, pl, num_sms, stream);
-    if (e != cudaSuccess) return e;
-    return launch_pass<D, false>(a, pl, num_sms, stream);
+
+    e = launch_pass<D, true>(a, pl, num_sms, stream);
+    return e != cudaSuccess ? e : launch_pass<D, false>(a, pl, num_sms, stream);
 }
+
+size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
-int cross_grad_bn(int D) { return D == 128 ? GradCfg<128>::BN : GradCfg<80>::BN; }
+GradPlan grad_plan(int64_t Tq, int64_t Tk, int B, int Hq, int Hk, int D, int max_q, int max_k)
+{
+    GradPlan p;
+    p.lg_pack = cross_pack(Hq / Hk);
+    const int64_t tok = 128 >> p.lg_pack;
+    auto tiles = [&](int64_t T, int64_t rows, int most) {
+        const int64_t a = T / rows + B, b = (int64_t)B * ((most + rows - 1) / rows);
+        return a < b ? a : b;
+    };
+    p.max_dq = tiles(Tq, tok, max_q) * (Hq >> p.lg_pack);
+    p.max_dkv = tiles(Tk, 128, max_k) * Hk;
+    p.off_dq = 256;
+    p.off_dkv = up(p.off_dq + sizeof(GradItem) * (size_t)p.max_dq);
+    p.off_stats = up(p.off_dkv + sizeof(GradItem) * (size_t)p.max_dkv);
+    p.bytes = p.off_stats + sizeof(float2) * (size_t)Tq * Hq;
+    return p;
+}
 
 cudaError_t launch_cross_grad(const CrossGradArgs &a, const GradPlan &p, int num_sms, cudaStream_t stream)
 {
-    cudaError_t e = launch_grad_schedule(a, p, stream);
-    if (e != cudaSuccess) return e;
     switch (a.f.D) {
         case 32: return launch_d<32>(a, p, num_sms, stream);
         case 64: return launch_d<64>(a, p, num_sms, stream);

@@ -172,94 +172,18 @@ cross_tile_join_kernel(const WsHeader *__restrict__ hdr, const CrossTile *__rest
     }
 }
 
-// Work lists of the two gradient passes, one block each: block 0 the dq tiles (ordered by key count),
-// block 1 the dk, dv tiles (ordered by query count), longest loop first. Tiles without a loop are
-// listed too: their gradients are 0.
-__global__ void __launch_bounds__(kThreads)
-grad_schedule_kernel(const CrossSegs segs, int Hq, int Hk, int lg_pack, int bn, int32_t *counts, GradItem *dq,
-                     GradItem *dkv, int32_t *status)
-{
-    extern __shared__ unsigned long long s_key[];
-    __shared__ int64_t s_warp[32];
-    __shared__ int s_bad;
-    const int tid = threadIdx.x, B = segs.B;
-    const bool keys = blockIdx.x == 1;                 // the tiles are of keys
-    int NP = 1;
-    while (NP < B) NP <<= 1;
-    if (tid == 0) s_bad = 0;
-    __syncthreads();
-    for (int i = tid; i < NP; i += kThreads) {
-        CrossSeg x;
-        const bool fine = i < B && load_seg(segs, i, x, status, !keys);
-        if (i < B && (segs.cu_q[i + 1] < segs.cu_q[i] || segs.cu_k[i + 1] < segs.cu_k[i])) s_bad = 1;
-        const bool use = fine && (keys ? x.kn : x.qn) > 0;
-        s_key[i] = use ? ((unsigned long long)(0x7fffffffu - (uint32_t)(keys ? x.qn : x.kn)) << 32) | (uint32_t)i : ~0ull;
-    }
-    __syncthreads();
-    if (s_bad) {
-        if (tid == 0) counts[blockIdx.x] = 0;
-        return;
-    }
-    block_sort(s_key, NP, tid);
-    const int lg_tile = keys ? 7 : 7 - lg_pack;        // rows (tokens) of a tile, log2
-    const int heads = keys ? Hk : Hq >> lg_pack;       // tiles side by side
-    const int per = (B + kThreads - 1) / kThreads, lo = min(tid * per, B), hi = min(lo + per, B);
-    auto seg_at = [&](int p, CrossSeg &x) -> bool {
-        if (s_key[p] == ~0ull) return false;
-        load_seg(segs, (int)(s_key[p] & 0xffffffffu), x, nullptr, false);
-        return true;
-    };
-    auto tiles_of = [&](const CrossSeg &x) { return ((keys ? x.kn : x.qn) + (1 << lg_tile) - 1) >> lg_tile; };
-    int64_t n = 0, total;
-    for (int p = lo; p < hi; ++p) {
-        CrossSeg x;
-        if (seg_at(p, x)) n += (int64_t)heads * tiles_of(x);
-    }
-    int64_t at = block_exclusive_scan(n, s_warp, &total);
-    for (int p = lo; p < hi; ++p) {
-        CrossSeg x;
-        if (!seg_at(p, x)) continue;
-        s_key[p] = ((unsigned long long)at << 32) | (uint32_t)(s_key[p] & 0xffffffffu);
-        at += (int64_t)heads * tiles_of(x);
-    }
-    __syncthreads();
-    GradItem *items = keys ? dkv : dq;
-    const int lane = tid & 31, warp = tid >> 5;
-    for (int p = warp; p < B; p += kThreads / 32) {
-        if (s_key[p] == ~0ull) break;
-        CrossSeg x;
-        load_seg(segs, (int)(s_key[p] & 0xffffffffu), x, nullptr, false);
-        const int first = (int)(s_key[p] >> 32), nr = tiles_of(x);
-        GradItem it;
-        it.l0 = keys ? x.q0 : x.k0;
-        it.ln = keys ? x.qn : x.kn;
-        it.r1 = keys ? x.k0 + x.kn : x.q0 + x.qn;
-        it.j0 = 0;
-        const int step = keys ? bn >> lg_pack : bn;
-        it.j1 = (it.ln + step - 1) / step * (keys ? Hq / Hk >> lg_pack : 1);
-        it.slot = -1;
-        for (int i = lane; i < heads * nr; i += 32) {
-            const int h = i / nr, r = i - h * nr;
-            it.r0 = (keys ? x.k0 : x.q0) + (r << lg_tile);
-            it.head = keys ? h : h << lg_pack;
-            items[first + i] = it;
-        }
-    }
-    if (tid == 0) counts[blockIdx.x] = (int32_t)total;
-}
-
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
 // as many heads side by side as divide the group, up to 8 (a tile keeps 16 tokens at least)
-static int pack_of(int group) { return group % 8 == 0 ? 3 : group % 4 == 0 ? 2 : group % 2 == 0 ? 1 : 0; }
+int cross_pack(int group) { return group % 8 == 0 ? 3 : group % 4 == 0 ? 2 : group % 2 == 0 ? 1 : 0; }
 
 LongPlan long_plan(int64_t Tq, int B, int Hq, int Hk, int D, int max_q, int max_k)
 {
     LongPlan p;
     const int group = Hq / Hk;
-    p.lg_pack = pack_of(group);
+    p.lg_pack = cross_pack(group);
     const int64_t tok = 128 >> p.lg_pack, packs = Hq >> p.lg_pack;
     int64_t tiles = Tq / tok + B;
     const int64_t by_seq = (int64_t)B * ((max_q + tok - 1) / tok);
@@ -308,42 +232,6 @@ cudaError_t launch_cross_schedule(const CrossArgs &a, const LongPlan &p, int num
     LaunchScope scope("cross_schedule", stream);
     cross_schedule_kernel<<<1, kThreads, sizeof(unsigned long long) * (size_t)np, stream>>>(
         a.segs, a.Hq, p.lg_pack, p.chunk, num_sms, hdr, items, tiles, a.status);
-    return cudaGetLastError();
-}
-
-GradPlan grad_plan(int64_t Tq, int64_t Tk, int B, int Hq, int Hk, int D, int max_q, int max_k)
-{
-    GradPlan p;
-    p.lg_pack = pack_of(Hq / Hk);
-    const int64_t tok = 128 >> p.lg_pack;
-    auto tiles = [&](int64_t T, int64_t rows, int most) {
-        const int64_t a = T / rows + B, b = (int64_t)B * ((most + rows - 1) / rows);
-        return a < b ? a : b;
-    };
-    p.max_dq = tiles(Tq, tok, max_q) * (Hq >> p.lg_pack);
-    p.max_dkv = tiles(Tk, 128, max_k) * Hk;
-    p.off_dq = 256;
-    p.off_dkv = up(p.off_dq + sizeof(GradItem) * (size_t)p.max_dq);
-    p.off_stats = up(p.off_dkv + sizeof(GradItem) * (size_t)p.max_dkv);
-    p.bytes = p.off_stats + sizeof(float2) * (size_t)Tq * Hq;
-    return p;
-}
-
-cudaError_t launch_grad_schedule(const CrossGradArgs &a, const GradPlan &p, cudaStream_t stream)
-{
-    int np = 1;
-    while (np < a.f.segs.B) np <<= 1;
-    static DeviceOnce once;
-    cudaError_t e = once.run([] {
-        return cudaFuncSetAttribute(grad_schedule_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)sizeof(unsigned long long) * VIT_MAX_SEGMENTS);
-    });
-    if (e != cudaSuccess) return e;
-    char *ws = static_cast<char *>(a.f.workspace);
-    LaunchScope scope("grad_schedule", stream);
-    grad_schedule_kernel<<<2, kThreads, sizeof(unsigned long long) * (size_t)np, stream>>>(
-        a.f.segs, a.f.Hq, a.f.Hk, p.lg_pack, cross_grad_bn(a.f.D), reinterpret_cast<int32_t *>(ws),
-        reinterpret_cast<GradItem *>(ws + p.off_dq), reinterpret_cast<GradItem *>(ws + p.off_dkv), a.f.status);
     return cudaGetLastError();
 }
 

@@ -76,6 +76,29 @@ struct DeviceOnce {
     }
 };
 
+// Chained launches: a kernel started by launch_chained may begin while the launch before it in the
+// stream still runs (as soon as every block of that one has called grid_release or ended), and must
+// call grid_wait before it touches anything that launch writes, or before it ends. Both are nothing in
+// an ordinary launch. Waiting here is the hardware's, and ends when the launch before has ended.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A &&...args)
+{
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+
 // ---- launch bookkeeping (instrument.cpp) ----
 struct LaunchScope {
     LaunchScope(const char *name, cudaStream_t stream);
