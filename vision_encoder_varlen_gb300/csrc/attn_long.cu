@@ -211,7 +211,8 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     __shared__ Item s_items[kItemRing];        // the item ring (keys < 0: the end of this CTA's list)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n_items = hdr->n_long;                   // read by the producer; the others take items from it
+    int n_items = 0;                                   // read by the producer; the others take items from it
+    if constexpr (!X) n_items = hdr->n_long;
 
     if (threadIdx.x == 0) {
         s_abort = 0;
@@ -250,6 +251,11 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
+    if constexpr (X) {                                 // launched behind its scheduler: the list is there now
+        grid_wait();
+        grid_release();
+        n_items = hdr->n_long;
+    }
 
     auto fail = [&]() {
         if (!s_abort) {
@@ -1042,10 +1048,9 @@ cudaError_t launch_cross_d(const CrossArgs &a, const CrossLong &cx, const WsHead
     const unsigned blocks = (unsigned)(max_items < num_sms ? max_items : num_sms);
     if (blocks == 0) return cudaSuccess;
     LaunchScope scope("cross_long", stream);
-    kern<<<blocks, kThreads, C::SMEM, stream>>>(mq, mqr, mk, mkr, mv, static_cast<__nv_bfloat16 *>(a.out),
-                                                a.out_stride, a.lse, a.Hq, a.scale_log2, const_cast<WsHeader *>(hdr),
-                                                items, a.status, 0, rope::QRope{}, cx);
-    return cudaGetLastError();
+    return launch_chained(kern, blocks, kThreads, C::SMEM, stream, mq, mqr, mk, mkr, mv,
+                          static_cast<__nv_bfloat16 *>(a.out), a.out_stride, a.lse, a.Hq, a.scale_log2,
+                          const_cast<WsHeader *>(hdr), items, a.status, 0, rope::QRope{}, cx);
 }
 
 }  // namespace

@@ -75,6 +75,7 @@ cross_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     __shared__ volatile int s_abort;
     __shared__ float s_m[NW][16], s_l[NW][16];
 
+    grid_release();                                           // the join may take its place already
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
     CrossSeg seg;
@@ -338,7 +339,9 @@ cross_join_kernel(const Few p)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.y;
     CrossSeg seg;
-    if (!load_seg(p.segs, b, seg, nullptr, false)) return;
+    const bool fine = load_seg(p.segs, b, seg, nullptr, false);
+    grid_wait();                                              // the runs' results
+    if (!fine) return;
     const int n_rows = seg.qn * p.Hq;                         // (token, head) rows of the sequence
     const int runs = (seg.kn + p.chunk - 1) / p.chunk;
     for (int x = blockIdx.x * 8 + warp; x < n_rows; x += gridDim.x * 8) {
@@ -409,8 +412,7 @@ cudaError_t launch_mt(const CrossArgs &a, const FewPlan &pl, const Few &p, cudaS
     if (e != cudaSuccess || pl.n_split == 1) return e;
     LaunchScope scope("cross_join", stream);
     const int rows = s.max_q * a.Hq;
-    cross_join_kernel<D><<<dim3((rows + 7) / 8, s.B), 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_chained(cross_join_kernel<D>, dim3((rows + 7) / 8, s.B), 256, 0, stream, p);
 }
 
 template <int D> cudaError_t launch_d(const CrossArgs &a, const FewPlan &pl, cudaStream_t stream)

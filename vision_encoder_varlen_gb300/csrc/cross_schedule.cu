@@ -26,6 +26,7 @@ cross_schedule_kernel(const CrossSegs segs, int Hq, int lg_pack, int chunk, int 
     extern __shared__ unsigned long long s_key[];      // [NP]: key count descending, then index
     __shared__ int64_t s_warp[32];
     __shared__ int s_bad;
+    grid_release();
     const int tid = threadIdx.x, B = segs.B;
     int NP = 1;
     while (NP < B) NP <<= 1;
@@ -137,6 +138,7 @@ __global__ void __launch_bounds__(256)
 cross_tile_join_kernel(const WsHeader *__restrict__ hdr, const CrossTile *__restrict__ tiles, const CrossLong cx,
                        __nv_bfloat16 *__restrict__ out, int64_t out_stride, float *__restrict__ lse, int Hq)
 {
+    grid_wait();
     const int n_tiles = hdr->reserved, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n_rows = 16;                             // rows per block: a tile is dealt to 8 blocks
     for (int w = blockIdx.x; w < n_tiles * 8; w += gridDim.x) {
@@ -241,8 +243,8 @@ cudaError_t launch_cross_tile_join(const CrossArgs &a, const LongPlan &p, const 
     const unsigned blocks = (unsigned)(p.max_tiles * 8);
     LaunchScope scope("cross_tile_join", stream);
     auto run = [&](auto kern) {
-        kern<<<blocks, 256, 0, stream>>>(hdr, tiles, cx, static_cast<__nv_bfloat16 *>(a.out), a.out_stride, a.lse, a.Hq);
-        return cudaGetLastError();
+        return launch_chained(kern, blocks, 256, 0, stream, hdr, tiles, cx, static_cast<__nv_bfloat16 *>(a.out),
+                              a.out_stride, a.lse, a.Hq);
     };
     switch (a.D) {
         case 32: return run(cross_tile_join_kernel<32>);

@@ -293,6 +293,7 @@ mrope_bwd_kernel(const Mrope p)
     __shared__ float4 s_cs[kWarps][D / 4];
     __shared__ uint4 s_w[2][D / 8];
     __shared__ float s_sum[kWarps][2][D];
+    grid_release();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane / CH, c = lane % CH;
     const bool live = g < ROWS;

@@ -213,6 +213,7 @@ template <int VPT, bool F32>
 __global__ void __launch_bounds__(256)
 norm_residual_bwd_kernel(const Bwd p, int rows_per_block)
 {
+    grid_release();
     constexpr int wpr = 1;
     __shared__ float2 s_red2[2 * kMaxWarps];
     const int lane_in_row = threadIdx.x & 31, row_in_block = (int)(threadIdx.x >> 5);
@@ -391,6 +392,7 @@ norm_residual_bwd_ring_kernel(const Bwd p, const Ring ring)
     __shared__ float2 s_red2[2 * kMaxWarps];
     __shared__ uint64_t s_full[kMaxStages];
     const int never = 0;                       // no abort flag: every thread waits for itself
+    grid_release();
     const int nvec = p.C >> 2, group = blockDim.x, wpr = blockDim.x >> 5;
     const float inv_c = 1.f / (float)p.C;
     const bool gate_tok = p.gate && p.gate_stride != 0;
@@ -600,6 +602,7 @@ struct SumOut {
 __global__ void __launch_bounds__(1024)
 column_sum_kernel(const float *__restrict__ part, int n_parts, int n_sum, int C, const SumOut o)
 {
+    grid_wait();                               // the partial sums of the launch before
     __shared__ float s[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t cols = (int64_t)n_sum * C;
@@ -736,8 +739,8 @@ cudaError_t launch_column_sum(const float *part, int n_parts, int n_sum, int C, 
 {
     const SumOut o{{out0, out1, out2}};
     LaunchScope scope("column_sum", stream);
-    column_sum_kernel<<<(unsigned)(((int64_t)n_sum * C + 31) / 32), 1024, 0, stream>>>(part, n_parts, n_sum, C, o);
-    return cudaGetLastError();
+    return launch_chained(column_sum_kernel, (unsigned)(((int64_t)n_sum * C + 31) / 32), 1024, 0, stream, part, n_parts,
+                          n_sum, C, o);
 }
 
 cudaError_t launch_norm_residual(const NormResidualArgs &a, int num_sms, cudaStream_t stream)
