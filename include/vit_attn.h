@@ -511,8 +511,8 @@ size_t vit_cross_attn_workspace_size(int64_t Tq, int64_t Tk, int Hq, int Hkv, in
  *   lse[t, h] = ln sum_j exp(scale * <q[t, h], k[j, .]>)
  * without a causal mask, softmax in fp32, P rounded to bf16 for its product with v, fp32
  * accumulation. A sequence without keys gets out = 0 and lse = -inf. Prompts, single new tokens and
- * latent queries alike: with few query rows per key head (max_q * Hq/Hkv <= 64) the keys are split
- * over the GPU and the parts joined; results do not change from run to run.
+ * latent queries alike: where there are few query rows the keys are split over the GPU and the parts
+ * joined; results do not change from run to run.
  *
  *   q, out       device bf16 [Tq, Hq, D]; k, v device bf16 [Tk, Hkv, D]; Hq a multiple of Hkv.
  *   cu_q, cu_k   device int32 [B + 1], ascending; rows before cu[0] and from cu[B] on belong to no

@@ -191,8 +191,6 @@ vit_status_t cross_sizes(int64_t Tq, int64_t Tk, int Hq, int Hkv, int D, int B, 
     return VIT_OK;
 }
 
-bool takes_few(int Hq, int Hkv, int max_q) { return (int64_t)max_q * (Hq / Hkv) <= kFewRows; }
-
 // the checks that the cross-attention calls share (pointers, strides and alignment of q, k, v and the lists)
 vit_status_t check_cross(const void *q, const void *k, const void *v, int64_t Tk, int Hq, int Hkv, int D,
                          int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t *cu_q,
@@ -215,7 +213,7 @@ size_t vit_cross_attn_workspace_size(int64_t Tq, int64_t Tk, int Hq, int Hkv, in
 {
     if (cross_sizes(Tq, Tk, Hq, Hkv, D, B, &max_q, &max_k) != VIT_OK) return 0;
     if (B == 0 || Tq == 0) return 16;
-    if (takes_few(Hq, Hkv, max_q)) {
+    if (takes_few(B, Hq, Hkv, D, max_q, max_k)) {
         const size_t n = few_plan(B, Hq, Hkv, D, max_q, max_k).partial_bytes;
         return n > 16 ? n : 16;
     }
@@ -262,7 +260,8 @@ vit_status_t vit_cross_attn(const void *q, const void *k, const void *v, int64_t
     a.workspace = workspace;
     a.status = status_dev;
     cudaStream_t s = (cudaStream_t)stream;
-    if (takes_few(Hq, Hkv, max_q)) return from_cuda(launch_cross_few(a, few_plan(B, Hq, Hkv, D, max_q, max_k), s));
+    if (takes_few(B, Hq, Hkv, D, max_q, max_k))
+        return from_cuda(launch_cross_few(a, few_plan(B, Hq, Hkv, D, max_q, max_k), s));
     const LongPlan p = long_plan(Tq, B, Hq, Hkv, D, max_q, max_k);
     char *ws = static_cast<char *>(workspace);
     WsHeader *hdr = reinterpret_cast<WsHeader *>(ws);

@@ -53,12 +53,13 @@ struct CrossArgs {
 // that the workspace size is one too).
 struct FewPlan {
     int rows;                     // max_q * group: query rows that share one key head
-    int row_tiles;                // 16-row tiles of a block: 1, 2 or 4
+    int row_tiles;                // 16-row tiles of a block: 1 or 2
     int chunk;                    // keys per split
     int n_split;                  // splits of the longest sequence
     size_t partial_bytes;         // workspace of the partial results (0 with one split)
 };
-constexpr int kFewRows = 64;      // above it the tcgen05 kernel takes the call
+constexpr int kDesignSms = 152;   // the plans count on this many SMs
+bool takes_few(int B, int Hq, int Hk, int D, int max_q, int max_k);   // else the tcgen05 kernel takes the call
 FewPlan few_plan(int B, int Hq, int Hk, int D, int max_q, int max_k);
 cudaError_t launch_cross_few(const CrossArgs &a, const FewPlan &p, cudaStream_t stream);
 
@@ -97,7 +98,6 @@ struct LongPlan {
     int runs;                     // runs of the longest sequence
     size_t off_items, off_tiles, off_part_s, off_part_o, bytes;   // workspace layout
 };
-constexpr int kDesignSms = 152;
 LongPlan long_plan(int64_t Tq, int B, int Hq, int Hk, int D, int max_q, int max_k);
 int cross_pack(int group);     // log2 of P
 int attn_long_bn(int D);

@@ -1,18 +1,17 @@
 // Cross attention with few query rows: single new tokens, short continuations, small sets of latent
-// queries (at most 64 rows of max_q * (Hq / Hk) that share one key head).
+// queries (at most 32 rows of max_q * (Hq / Hk) that share one key head).
 //
 //   o = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),  s_j = scale q k_j,  m = max_j s_j,
 // over one sequence's keys. With so few rows the cost is reading k and v once (4 D bytes per key and
 // key head against 4 D rows flops), so the work is laid out for loads: a block takes one (sequence,
 // key head, run of `chunk` keys), all query rows of the group at once so that k and v are read only
-// once, and a producer warp keeps whole 64-key tiles in flight (TMA into a ring of two slots; blocks
-// are small enough that two or three share an SM). The keys of a sequence are split over blocks so
+// once, and a producer warp keeps whole 64-key tiles in flight (TMA into a ring of three slots; two or
+// more blocks share an SM). The keys of a sequence are split over blocks so
 // that a few long sequences still fill the GPU; each block leaves (m, l, O) of its run and a second
 // kernel joins a row's runs in order (results do not depend on timing). With one run per sequence the
 // block writes the result itself.
 //
-// Inside a block a warp takes one 16-row tile and a group of 16 (or, with four row tiles, 2 x 16) keys
-// of every 64-key tile: S = Q K^T and O += P V by m16n8k16 MMAs (the rows are far too few for 128-row tcgen05 tiles to pay:
+// Inside a block a warp takes one 16-row tile and a group of 16 keys of every 64-key tile: S = Q K^T and O += P V by m16n8k16 MMAs (the rows are far too few for 128-row tcgen05 tiles to pay:
 // the tensor pipe is idle either way), softmax statistics in fp32 registers, P rounded to bf16 as in
 // the other attention kernels, O rescaled only when a row's maximum grows by more than 2^8. The key
 // groups are joined through shared memory at the end.
@@ -27,7 +26,7 @@ namespace vit {
 namespace {
 
 constexpr int kTile = 64;                     // keys per ring slot
-constexpr int kStages = 2;
+constexpr int kStages = 3;                    // 96 KB at head_dim 128: two blocks of an SM keep 192 KB in flight
 constexpr long long kWaitBudget = 4000000000ll;
 
 // A tile of `kTile` rows of D columns as TMA leaves it: 64-column slabs with 128-byte swizzle, then one
@@ -57,10 +56,9 @@ struct Few {
     float *part_o, *part_s;                   // [B][Hk][n_split][rows][D] and [..][rows] (log2 of the run's sum)
 };
 
-// Warps of a block: MT row tiles x KQ key groups. Four row tiles take two key groups (each 2 x 16 keys
-// of a tile): with four there would be 16 warps of too few registers for Q and O.
-template <int MT> constexpr int kGroups = MT == 4 ? 2 : 4;
-template <int MT> constexpr int kMmaWarps = MT * kGroups<MT>;
+// Warps of a block: MT row tiles x 4 key groups.
+constexpr int kGroups = 4;
+template <int MT> constexpr int kMmaWarps = MT * kGroups;
 
 template <int D, int MT>
 __global__ void __launch_bounds__(32 * kMmaWarps<MT> + 32)
@@ -68,7 +66,7 @@ cross_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_vr, const Few p)
 {
     using T = Tile<D>;
-    constexpr int NK = D / 16, KQ = kGroups<MT>, NW = kMmaWarps<MT>;
+    constexpr int NK = D / 16, KQ = kGroups, NW = kMmaWarps<MT>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *ring = reinterpret_cast<unsigned char *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     __shared__ uint64_t s_full[kStages], s_empty[kStages];
@@ -77,7 +75,7 @@ cross_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 
     grid_release();                                           // the join may take its place already
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int split = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
+    const int split = blockIdx.z, hk = blockIdx.x, b = blockIdx.y;   // later runs last: ragged lengths leave them empty
     CrossSeg seg;
     // a sequence without keys is left to the join, or to split 0 where there is none
     if (!load_seg(p.segs, b, seg, p.status, threadIdx.x == 0 && split == 0 && hk == 0)) return;
@@ -164,81 +162,77 @@ cross_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             ok = __all_sync(0xffffffffu, wait(s_full[s], (i / kStages) & 1));
             if (!ok) break;
             unsigned char *kt = ring + s * 2 * T::BYTES, *vt = kt + T::BYTES;
+            const int key0 = 16 * quarter;
+            const int live = n_keys - i * kTile - key0;       // of this warp's 16 keys
+            if (live > 0) {
+                const uint32_t ka = sm100::smem_addr(kt), va = sm100::smem_addr(vt);
+                float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                // ldmatrix: lane l gives the row address of matrix l / 8: keys (l & 7) + 8 (l / 16), chunk (l / 8) & 1
+                const int kr = key0 + (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
 #pragma unroll
-            for (int sub = 0; sub < 4 / KQ; ++sub) {
-                const int key0 = 16 * (quarter + KQ * sub);
-                const int live = n_keys - i * kTile - key0;       // of this warp's 16 keys
-                if (live <= 0) break;
-                {
-                    const uint32_t ka = sm100::smem_addr(kt), va = sm100::smem_addr(vt);
-                    float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-                    // ldmatrix: lane l gives the row address of matrix l / 8: keys (l & 7) + 8 (l / 16), chunk (l / 8) & 1
-                    const int kr = key0 + (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
+                for (int kk = 0; kk < NK; ++kk) {
+                    uint32_t b0, b1, b2, b3;
+                    wmma16::ldsm_x4(ka + T::at(kr, 2 * kk + kc), b0, b1, b2, b3);
+                    wmma16::mma16816(sc[0], qa[kk], b0, b1);
+                    wmma16::mma16816(sc[1], qa[kk], b2, b3);
+                }
+                if (live < 16) {
 #pragma unroll
-                    for (int kk = 0; kk < NK; ++kk) {
-                        uint32_t b0, b1, b2, b3;
-                        wmma16::ldsm_x4(ka + T::at(kr, 2 * kk + kc), b0, b1, b2, b3);
-                        wmma16::mma16816(sc[0], qa[kk], b0, b1);
-                        wmma16::mma16816(sc[1], qa[kk], b2, b3);
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (8 * n + 2 * c + (e & 1) >= live) sc[n][e] = -INFINITY;
+                    // V rows past the end: zero them (this warp alone reads its 16 keys)
+                    for (int x = lane; x < (16 - live) * (D / 8); x += 32)
+                        *reinterpret_cast<uint4 *>(vt + T::at(key0 + live + x / (D / 8), x % (D / 8))) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                    __syncwarp();
+                }
+                float pr[2][4];
+                bool grew = false;
+                float alpha[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {                 // rows g and g + 8
+                    float mx = fmaxf(fmaxf(sc[0][2 * h], sc[0][2 * h + 1]), fmaxf(sc[1][2 * h], sc[1][2 * h + 1]));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    mx *= p.scale_log2;
+                    alpha[h] = 1.f;
+                    if (mx > m_run[h] + 8.f) {
+                        alpha[h] = wmma16::ex2(m_run[h] - mx);
+                        m_run[h] = mx;
+                        grew = true;
                     }
-                    if (live < 16) {
+                    float sum = 0.f;
 #pragma unroll
-                        for (int n = 0; n < 2; ++n)
+                    for (int n = 0; n < 2; ++n)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (8 * n + 2 * c + (e & 1) >= live) sc[n][e] = -INFINITY;
-                        // V rows past the end: zero them (this warp alone reads its 16 keys)
-                        for (int x = lane; x < (16 - live) * (D / 8); x += 32)
-                            *reinterpret_cast<uint4 *>(vt + T::at(key0 + live + x / (D / 8), x % (D / 8))) =
-                                make_uint4(0u, 0u, 0u, 0u);
-                        __syncwarp();
-                    }
-                    float pr[2][4];
-                    bool grew = false;
-                    float alpha[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {                 // rows g and g + 8
-                        float mx = fmaxf(fmaxf(sc[0][2 * h], sc[0][2 * h + 1]), fmaxf(sc[1][2 * h], sc[1][2 * h + 1]));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                        mx *= p.scale_log2;
-                        alpha[h] = 1.f;
-                        if (mx > m_run[h] + 8.f) {
-                            alpha[h] = wmma16::ex2(m_run[h] - mx);
-                            m_run[h] = mx;
-                            grew = true;
+                        for (int e = 0; e < 2; ++e) {
+                            const float v = wmma16::ex2(fmaf(sc[n][2 * h + e], p.scale_log2, -m_run[h]));
+                            pr[n][2 * h + e] = v;
+                            sum += v;
                         }
-                        float sum = 0.f;
+                    l_run[h] = l_run[h] * alpha[h] + sum;     // per lane: joined over the quad at the end
+                }
+                if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-                        for (int n = 0; n < 2; ++n)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const float v = wmma16::ex2(fmaf(sc[n][2 * h + e], p.scale_log2, -m_run[h]));
-                                pr[n][2 * h + e] = v;
-                                sum += v;
-                            }
-                        l_run[h] = l_run[h] * alpha[h] + sum;     // per lane: joined over the quad at the end
+                    for (int j = 0; j < 2 * NK; ++j) {
+                        o[j][0] *= alpha[0];
+                        o[j][1] *= alpha[0];
+                        o[j][2] *= alpha[1];
+                        o[j][3] *= alpha[1];
                     }
-                    if (__any_sync(0xffffffffu, grew)) {
+                }
+                const uint32_t pa[4] = {wmma16::pack_bf16(pr[0][0], pr[0][1]), wmma16::pack_bf16(pr[0][2], pr[0][3]),
+                                        wmma16::pack_bf16(pr[1][0], pr[1][1]), wmma16::pack_bf16(pr[1][2], pr[1][3])};
+                // transposed: matrices (keys 0-7, chunk 2j), (keys 8-15, 2j), (keys 0-7, 2j + 1), (keys 8-15, 2j + 1)
+                const int vr = key0 + (lane & 15), vc = lane >> 4;
 #pragma unroll
-                        for (int j = 0; j < 2 * NK; ++j) {
-                            o[j][0] *= alpha[0];
-                            o[j][1] *= alpha[0];
-                            o[j][2] *= alpha[1];
-                            o[j][3] *= alpha[1];
-                        }
-                    }
-                    const uint32_t pa[4] = {wmma16::pack_bf16(pr[0][0], pr[0][1]), wmma16::pack_bf16(pr[0][2], pr[0][3]),
-                                            wmma16::pack_bf16(pr[1][0], pr[1][1]), wmma16::pack_bf16(pr[1][2], pr[1][3])};
-                    // transposed: matrices (keys 0-7, chunk 2j), (keys 8-15, 2j), (keys 0-7, 2j + 1), (keys 8-15, 2j + 1)
-                    const int vr = key0 + (lane & 15), vc = lane >> 4;
-#pragma unroll
-                    for (int j = 0; j < NK; ++j) {
-                        uint32_t b0, b1, b2, b3;
-                        wmma16::ldsm_x4_t(va + T::at(vr, 2 * j + vc), b0, b1, b2, b3);
-                        wmma16::mma16816(o[2 * j], pa, b0, b1);
-                        wmma16::mma16816(o[2 * j + 1], pa, b2, b3);
-                    }
+                for (int j = 0; j < NK; ++j) {
+                    uint32_t b0, b1, b2, b3;
+                    wmma16::ldsm_x4_t(va + T::at(vr, 2 * j + vc), b0, b1, b2, b3);
+                    wmma16::mma16816(o[2 * j], pa, b0, b1);
+                    wmma16::mma16816(o[2 * j + 1], pa, b2, b3);
                 }
             }
             __syncwarp();
@@ -331,11 +325,13 @@ cross_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     }
 }
 
-// One warp per query row: out = sum_s 2^(e_s - E) O_s / sum_s 2^(e_s - E), e_s the log2 of run s's sum.
-template <int D>
+// out = sum_s 2^(e_s - E) O_s / sum_s 2^(e_s - E), e_s the log2 of run s's sum: a row by one warp, or
+// (WIDE, many runs) by the eight warps of a block, each every eighth run, added up in warp order.
+template <int D, bool WIDE>
 __global__ void __launch_bounds__(256)
 cross_join_kernel(const Few p)
 {
+    __shared__ float s_acc[WIDE ? 8 : 1][WIDE ? D : 1], s_sum[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.y;
     CrossSeg seg;
@@ -344,41 +340,48 @@ cross_join_kernel(const Few p)
     if (!fine) return;
     const int n_rows = seg.qn * p.Hq;                         // (token, head) rows of the sequence
     const int runs = (seg.kn + p.chunk - 1) / p.chunk;
-    for (int x = blockIdx.x * 8 + warp; x < n_rows; x += gridDim.x * 8) {
-        const int tok = x / p.Hq, head = x - tok * p.Hq, hk = head / p.group;
-        const int r = tok * p.group + head - hk * p.group;
-        const int64_t row0 = ((int64_t)b * p.Hk + hk) * p.n_split * p.rows + r;
-        float E = -INFINITY;
-        for (int s = lane; s < runs; s += 32) E = fmaxf(E, p.part_s[row0 + (int64_t)s * p.rows]);
+    const int x = WIDE ? (int)blockIdx.x : (int)blockIdx.x * 8 + warp;
+    if (x >= n_rows) return;
+    const int tok = x / p.Hq, head = x - tok * p.Hq, hk = head / p.group;
+    const int r = tok * p.group + head - hk * p.group;
+    const int64_t row0 = ((int64_t)b * p.Hk + hk) * p.n_split * p.rows + r;
+    float E = -INFINITY;
+    for (int s = lane; s < runs; s += 32) E = fmaxf(E, p.part_s[row0 + (int64_t)s * p.rows]);
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) E = fmaxf(E, __shfl_xor_sync(0xffffffffu, E, d));
-        const float base = E == -INFINITY ? 0.f : E;
-        float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-        const bool col = lane < D / 4;
-        for (int s0 = 0; s0 < runs; s0 += 32) {
-            const float w_lane = s0 + lane < runs ? wmma16::ex2(p.part_s[row0 + (int64_t)(s0 + lane) * p.rows] - base) : 0.f;
-            const int n = min(32, runs - s0);
+    for (int d = 16; d > 0; d >>= 1) E = fmaxf(E, __shfl_xor_sync(0xffffffffu, E, d));
+    const float base = E == -INFINITY ? 0.f : E;
+    float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    const bool col = lane < D / 4;
 #pragma unroll 4
-            for (int s = 0; s < n; ++s) {
-                const float w = __shfl_sync(0xffffffffu, w_lane, s);
-                sum += w;
-                if (col) {
-                    const float4 v = *reinterpret_cast<const float4 *>(p.part_o + (row0 + (int64_t)(s0 + s) * p.rows) * D +
-                                                                       4 * lane);
-                    acc[0] = fmaf(w, v.x, acc[0]);
-                    acc[1] = fmaf(w, v.y, acc[1]);
-                    acc[2] = fmaf(w, v.z, acc[2]);
-                    acc[3] = fmaf(w, v.w, acc[3]);
-                }
-            }
+    for (int s = WIDE ? warp : 0; s < runs; s += WIDE ? 8 : 1) {
+        const int64_t row = row0 + (int64_t)s * p.rows;
+        const float w = wmma16::ex2(p.part_s[row] - base);
+        sum += w;
+        if (col) {
+            const float4 v = *reinterpret_cast<const float4 *>(p.part_o + row * D + 4 * lane);
+            acc[0] = fmaf(w, v.x, acc[0]);
+            acc[1] = fmaf(w, v.y, acc[1]);
+            acc[2] = fmaf(w, v.z, acc[2]);
+            acc[3] = fmaf(w, v.w, acc[3]);
         }
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
-        const int64_t t = seg.q0 + tok;
-        if (col)
-            *reinterpret_cast<uint2 *>(p.out + t * p.out_stride + (int64_t)head * D + 4 * lane) =
-                make_uint2(wmma16::pack_bf16(acc[0] * inv, acc[1] * inv), wmma16::pack_bf16(acc[2] * inv, acc[3] * inv));
-        if (p.lse && lane == 0) p.lse[t * p.Hq + head] = (E + log2f(sum)) * 0.6931471805599453f;
     }
+    if constexpr (WIDE) {
+        if (col) *reinterpret_cast<float4 *>(&s_acc[warp][4 * lane]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        if (lane == 0) s_sum[warp] = sum;
+        __syncthreads();
+        if (warp > 0) return;
+        for (int w = 1; w < 8; ++w) {
+            sum += s_sum[w];
+            if (col)
+                for (int e = 0; e < 4; ++e) acc[e] += s_acc[w][4 * lane + e];
+        }
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const int64_t t = seg.q0 + tok;
+    if (col)
+        *reinterpret_cast<uint2 *>(p.out + t * p.out_stride + (int64_t)head * D + 4 * lane) =
+            make_uint2(wmma16::pack_bf16(acc[0] * inv, acc[1] * inv), wmma16::pack_bf16(acc[2] * inv, acc[3] * inv));
+    if (p.lse && lane == 0) p.lse[t * p.Hq + head] = (E + log2f(sum)) * 0.6931471805599453f;
 }
 
 bool kv_map(CUtensorMap *m, const void *ptr, int64_t T, int H, int D, int64_t stride, int cols)
@@ -406,13 +409,15 @@ cudaError_t launch_mt(const CrossArgs &a, const FewPlan &pl, const Few &p, cudaS
     if (e != cudaSuccess) return e;
     {
         LaunchScope scope("cross_few", stream);
-        kern<<<dim3(pl.n_split, a.Hk, s.B), 32 * kMmaWarps<MT> + 32, smem, stream>>>(mk, mkr, mv, mvr, p);
+        kern<<<dim3(a.Hk, s.B, pl.n_split), 32 * kMmaWarps<MT> + 32, smem, stream>>>(mk, mkr, mv, mvr, p);
         e = cudaGetLastError();
     }
     if (e != cudaSuccess || pl.n_split == 1) return e;
     LaunchScope scope("cross_join", stream);
     const int rows = s.max_q * a.Hq;
-    return launch_chained(cross_join_kernel<D>, dim3((rows + 7) / 8, s.B), 256, 0, stream, p);
+    // with more than 16 runs a warp per row is too few loads in flight (147 runs: 37 us)
+    return pl.n_split > 16 ? launch_chained(cross_join_kernel<D, true>, dim3(rows, s.B), 256, 0, stream, p)
+                           : launch_chained(cross_join_kernel<D, false>, dim3((rows + 7) / 8, s.B), 256, 0, stream, p);
 }
 
 template <int D> cudaError_t launch_d(const CrossArgs &a, const FewPlan &pl, cudaStream_t stream)
@@ -437,32 +442,46 @@ template <int D> cudaError_t launch_d(const CrossArgs &a, const FewPlan &pl, cud
     p.part_s = p.part_o + n * D;
     switch (pl.row_tiles) {
         case 1: return launch_mt<D, 1>(a, pl, p, stream);
-        case 2: return launch_mt<D, 2>(a, pl, p, stream);
-        default: return launch_mt<D, 4>(a, pl, p, stream);
+        default: return launch_mt<D, 2>(a, pl, p, stream);
     }
 }
 
 }  // namespace
 
-// Keys per split. Enough blocks to fill the GPU about eight times over where the sequences are long
-// enough (ragged lengths then even out), but at least 128 keys (two tiles) and, since a split leaves
+// Keys per split: enough blocks to fill the GPU about eight times over where the sequences are long
+// enough (ragged lengths then even out; 4, 16 and 32 times were slower on 48 single tokens over up to
+// 8191 keys: 72, 64, 68 against 62 us), but at least 128 keys (two tiles) and, since a split leaves
 // rows * D fp32 values that are written and read again, at least 16 keys per row (at most 1/8 of the
-// traffic). A whole number of tiles.
+// traffic). Runs of equal length, in whole tiles.
 FewPlan few_plan(int B, int Hq, int Hk, int D, int max_q, int max_k)
 {
     FewPlan p;
     p.rows = max_q * (Hq / Hk);
-    p.row_tiles = p.rows <= 16 ? 1 : p.rows <= 32 ? 2 : 4;
-    const int64_t pairs = (int64_t)B * Hk, want = 152 * 8;
-    int64_t chunk = (pairs * (int64_t)max_k + want - 1) / want;
+    p.row_tiles = p.rows <= 16 ? 1 : 2;
+    const int64_t pairs = (int64_t)B * Hk, want = kDesignSms * 8;
     const int64_t least = 16 * p.rows > 128 ? 16 * p.rows : 128;
-    if (chunk < least) chunk = least;
+    int64_t n = (want + pairs / 2) / pairs;
+    const int64_t most = ((int64_t)max_k + least - 1) / least;
+    if (n > most) n = most;
+    if (n < 1) n = 1;
+    int64_t chunk = ((int64_t)max_k + n - 1) / n;
     chunk = (chunk + kTile - 1) / kTile * kTile;
-    int64_t n = max_k > 0 ? ((int64_t)max_k + chunk - 1) / chunk : 1;
+    if (chunk < kTile) chunk = kTile;
+    n = max_k > 0 ? ((int64_t)max_k + chunk - 1) / chunk : 1;
     p.chunk = (int)(chunk < (1 << 30) ? chunk : (1 << 30));
     p.n_split = (int)n;
     p.partial_bytes = n > 1 ? sizeof(float) * (size_t)pairs * n * p.rows * (D + 1) : 0;
     return p;
+}
+
+// Few rows take this kernel. Up to 16 rows always; up to 32 where all the keys are at most 32 MiB, and
+// launches dominate (8 rows x 4 heads over 4096 keys of 8 heads of 128: 22 us here, 28 us by the tcgen05
+// kernel; over 8 such sequences 61 and 53 us, over 32 of 16 heads of 80 118 and 92 us; with four row
+// tiles, 64 rows over 16 sequences of 256 to 4097 keys, 87 and 58 us).
+bool takes_few(int B, int Hq, int Hk, int D, int max_q, int max_k)
+{
+    const int64_t rows = (int64_t)max_q * (Hq / Hk);
+    return rows <= 16 || (rows <= 32 && (int64_t)B * max_k * Hk * D * 4 <= ((int64_t)32 << 20));
 }
 
 cudaError_t launch_cross_few(const CrossArgs &a, const FewPlan &p, cudaStream_t stream)
