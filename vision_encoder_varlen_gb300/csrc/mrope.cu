@@ -28,13 +28,13 @@
 // need neither registers nor a barrier. The gradient's weight sums stay in registers (a
 // lane's columns never change), are joined per block in shared memory in a fixed order, and a
 // second kernel adds the blocks' partial sums.
+#include <limits.h>
+
 #include "internal.h"
 #include "rope_math.cuh"
 
 namespace vit {
 namespace {
-
-using rope::unpack8;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
@@ -115,9 +115,215 @@ template <int N> __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
 
-// A warp's way over its units (token, slice of heads), `rows` head rows at a time, among the rows
-// [h0, h1) of a token's Hq + Hk.
-struct Walk {
+// A lane's way over its warp's rows, `ROWS` head rows per step: unit after unit (a token, or a slice
+// of its heads), and in each the q rows and then the k rows. `at` is the
+// lane's own place in the current row of one tensor; only a change of part computes an address anew.
+template <int D> struct Walk {
+    int64_t u, t;                              // unit and its token
+    char *at;                                  // this lane's chunk c of row (first row of the step + g)
+    int left;                                  // rows of the part from the step's first on
+    int part;                                  // 0: q, 1: k
+};
+struct Side {                                  // one tensor pair (q, k) that a walk goes over
+    char *q, *k;
+    int64_t q_stride, k_stride;                // token strides, bytes
+};
+template <int D> struct Way {
+    int64_t units, stride;
+    int slices, per, Hq, rows;
+    int off;                                   // the lane's bytes from a row's start: row g, chunk c
+
+    // the first rows at or after (unit w.u, part w.part)
+    __device__ __forceinline__ void enter(Walk<D> &w, const Side &s) const {
+        for (; w.u < units; w.u += stride, w.part = 0) {
+            w.t = slices == 1 ? w.u : w.u / slices;
+            const int lo = slices == 1 ? 0 : (int)(w.u - w.t * slices) * per, hi = min(rows, lo + per);
+            for (; w.part < 2; ++w.part) {
+                const int first = w.part ? max(lo, Hq) - Hq : lo, last = w.part ? hi - Hq : min(hi, Hq);
+                w.left = last - first;
+                if (w.left > 0) {
+                    w.at = (w.part ? s.k + w.t * s.k_stride : s.q + w.t * s.q_stride) + (int64_t)first * (2 * D) + off;
+                    return;
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ bool done(const Walk<D> &w) const { return w.u >= units; }
+    __device__ __forceinline__ void step(Walk<D> &w, const Side &s, int n) const {
+        w.left -= n;
+        w.at += n * (2 * D);
+        if (w.left <= 0) {
+            ++w.part;
+            enter(w, s);
+        }
+    }
+};
+
+// A lane's 16 elements as eight pairs, for the packed fp32 instructions: pairs 0..3 are the chunk of
+// the first half, 4..7 that of the second.
+__device__ __forceinline__ void unpack16(const uint4 &a, const uint4 &b, uint64_t *x) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = rope::f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t pack_pair(uint64_t x) {
+    float lo, hi;
+    rope::f2_split(x, lo, hi);
+    return rope::pack2(lo, hi);
+}
+__device__ __forceinline__ void pack16(const uint64_t *x, uint4 &a, uint4 &b) {
+    a = make_uint4(pack_pair(x[0]), pack_pair(x[1]), pack_pair(x[2]), pack_pair(x[3]));
+    b = make_uint4(pack_pair(x[4]), pack_pair(x[5]), pack_pair(x[6]), pack_pair(x[7]));
+}
+__device__ __forceinline__ float pair_sum(uint64_t x) {
+    float lo, hi;
+    rope::f2_split(x, lo, hi);
+    return lo + hi;
+}
+
+// y = R(a) x on the 16 elements of a lane; cs: the lane's turns of its two chunks' pairs
+// (rotate-half: the four entries of chunk c in cs[0..3]; interleaved: two of each chunk)
+template <bool IL>
+__device__ __forceinline__ void turn(uint64_t *x, const float4 *cs) {
+    using rope::f2;
+    using rope::f2_fma;
+    using rope::f2_mul;
+    if constexpr (!IL) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {                          // elements 2i, 2i + 1 of both chunks
+            const float4 t = cs[i];
+            const uint64_t c = f2(t.x, t.y), s = f2(t.z, t.w);
+            const uint64_t n = f2(-t.z, -t.w);
+            const uint64_t a = x[i], b = x[4 + i];
+            x[i] = f2_fma(b, n, f2_mul(a, c));
+            x[4 + i] = f2_fma(a, s, f2_mul(b, c));
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {                          // one rotated pair each
+            const float4 t = cs[q >> 1];
+            const float c = (q & 1) ? t.y : t.x, s = (q & 1) ? t.w : t.z;
+            float a, b;
+            rope::f2_split(x[q], a, b);
+            x[q] = f2_fma(f2(b, a), f2(-s, s), f2_mul(x[q], f2(c, c)));
+        }
+    }
+}
+
+template <int D> struct Shape {
+    static constexpr int CH = D / 16;          // lanes per row
+    static constexpr int ROWS = 32 / CH;       // rows a warp handles at a time
+};
+
+// sum over the CH lanes of a row's group, added in lane order
+template <int D> __device__ __forceinline__ float group_sum(float v, int first) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < Shape<D>::CH; ++i) s += __shfl_sync(0xffffffffu, v, (first + i) & 31);
+    return s;
+}
+
+constexpr int kAheadFwd = 6, kAheadBwd = 4;        // steps in flight: 48 and 64 KB of a block
+
+template <int D, bool IL>
+__global__ void __launch_bounds__(kThreads, 3)
+mrope_kernel(const Mrope p)
+{
+    constexpr int CH = Shape<D>::CH, ROWS = Shape<D>::ROWS, AHEAD = kAheadFwd;
+    extern __shared__ uint4 s_rows[];                      // [warp][step][chunk a, b][lane]
+    __shared__ int s_pos[kWarps][AHEAD][4];               // the steps' positions, copied with their rows
+    __shared__ float4 s_cs[kWarps][D / 4];
+    __shared__ uint4 s_w[2][D / 8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane / CH, c = lane % CH;               // row of the step, chunk of the row
+    const int my_row = g < ROWS ? g : INT_MAX;             // lanes past the last group have none
+    const int first = g * CH;
+    if (p.norm_w) {
+        for (int i = threadIdx.x; i < D / 4; i += kThreads)
+            s_w[i / (D / 8)][i % (D / 8)] = reinterpret_cast<const uint4 *>(p.norm_w)[i];
+        __syncthreads();
+    }
+    const float4 *cs_a = s_cs[warp] + (IL ? 2 * c : 4 * c), *cs_b = cs_a + D / 8;
+    uint4 *mine = s_rows + warp * (AHEAD * 64) + lane;
+    const uint32_t mine_a = (uint32_t)__cvta_generic_to_shared(mine);
+    const uint32_t pos_a = (uint32_t)__cvta_generic_to_shared(&s_pos[warp][0][lane & 3]);
+    const int rows = p.Hq + p.Hk;
+    const Way<D> way{p.T * p.slices, (int64_t)gridDim.x * kWarps, p.slices, (rows + p.slices - 1) / p.slices, p.Hq, rows,
+                     2 * (g * D + 8 * c)};
+    const Side in{(char *)p.q_in, (char *)p.k_in, 2 * p.q_in_stride, 2 * p.k_in_stride};
+    const Side out{(char *)p.q_out, (char *)p.k_out, 2 * p.q_out_stride, 2 * p.k_out_stride};
+    const LanePairs pairs = lane_pairs<D>(p, lane);
+
+    Walk<D> fetch;
+    fetch.u = (int64_t)blockIdx.x * kWarps + warp;
+    fetch.part = 0;
+    Walk<D> at = fetch;
+    way.enter(fetch, in);
+    way.enter(at, out);
+    auto request = [&](int slot) {                         // this lane's chunks of the fetch step's rows
+        if (!way.done(fetch)) {
+            if (lane < 3) copy4(pos_a + slot * 16, p.pos + 3 * fetch.t + lane);
+            if (my_row < fetch.left) {
+                copy16(mine_a + slot * 1024, fetch.at);
+                copy16(mine_a + slot * 1024 + 512, fetch.at + D);
+            }
+            way.step(fetch, in, ROWS);
+        }
+        copies_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) request(i);
+    int64_t turned = -1;                                   // the unit whose turns are in cs
+    float4 cs[4];
+    int slot = 0;
+    while (!way.done(at)) {
+        copies_wait<AHEAD - 1>();
+        if (at.u != turned) {
+            __syncwarp();                                  // the copied position is there, the last turns were read
+            fill_turns<D>(pairs, s_pos[warp][slot], lane, s_cs[warp]);
+            turned = at.u;
+            __syncwarp();
+            cs[0] = cs_a[0];                               // the lane's turns, for all rows of the token
+            cs[1] = cs_a[1];
+            cs[2] = IL ? cs_b[0] : cs_a[2];
+            cs[3] = IL ? cs_b[1] : cs_a[3];
+        }
+        const bool row = my_row < at.left;
+        uint4 va = make_uint4(0u, 0u, 0u, 0u), vb = va;
+        if (row) {
+            va = mine[slot * 64];
+            vb = mine[slot * 64 + 32];
+        }
+        uint64_t x[8];
+        unpack16(va, vb, x);
+        if (p.norm_w) {
+            uint64_t sq = rope::f2_mul(x[0], x[0]);
+#pragma unroll
+            for (int e = 1; e < 8; ++e) sq = rope::f2_fma(x[e], x[e], sq);
+            const float inv = rsqrtf(group_sum<D>(pair_sum(sq), first) * (1.f / D) + p.eps);
+            uint64_t w[8];
+            unpack16(s_w[at.part][c], s_w[at.part][CH + c], w);
+            const uint64_t inv2 = rope::f2(inv, inv);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = rope::f2_mul(x[e], rope::f2_mul(inv2, w[e]));
+        }
+        turn<IL>(x, cs);
+        if (row) {
+            uint4 ya, yb;
+            pack16(x, ya, yb);
+            *reinterpret_cast<uint4 *>(at.at) = ya;
+            *reinterpret_cast<uint4 *>(at.at + D) = yb;
+        }
+        request(slot);                                     // read above: the slot is free
+        if (++slot == AHEAD) slot = 0;
+        way.step(at, out, ROWS);
+    }
+}
+
+// The gradient's way over its units, `rows` head rows at a time, among the rows [h0, h1) of a token's
+// Hq + Hk. (It goes over three tensors: row numbers and unpacked arithmetic, 128 us for 40013 tokens of
+// 16 + 4 heads of 128, were faster here than the forward kernel's places and pairs, 137 us.)
+struct RowWalk {
     int64_t u, t;
     int r, hi;
     __device__ __forceinline__ bool done(int64_t units) const { return u >= units; }
@@ -140,14 +346,14 @@ struct Walk {
     }
 };
 
-// y = R(+-a) x on the 16 elements of a lane; cs: the lane's turns of its two chunks' pairs
-template <bool IL, bool BACK>
-__device__ __forceinline__ void turn(float *xa, float *xb, const float4 *cs_a, const float4 *cs_b) {
+// dz = R(-a) dy on the 16 elements of a lane; cs: the lane's turns of its two chunks' pairs
+template <bool IL>
+__device__ __forceinline__ void turn_back(float *xa, float *xb, const float4 *cs_a, const float4 *cs_b) {
     if constexpr (!IL) {
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
             const float4 t = cs_a[i / 2];
-            const float s0 = BACK ? -t.z : t.z, s1 = BACK ? -t.w : t.w;
+            const float s0 = -t.z, s1 = -t.w;
             const float a0 = xa[i], a1 = xa[i + 1], b0 = xb[i], b1 = xb[i + 1];
             xa[i] = fmaf(a0, t.x, -b0 * s0);
             xb[i] = fmaf(b0, t.x, a0 * s0);
@@ -162,7 +368,7 @@ __device__ __forceinline__ void turn(float *xa, float *xb, const float4 *cs_a, c
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const float4 t = cs[q >> 1];
-                const float c = (q & 1) ? t.y : t.x, s = BACK ? -((q & 1) ? t.w : t.z) : ((q & 1) ? t.w : t.z);
+                const float c = (q & 1) ? t.y : t.x, s = -((q & 1) ? t.w : t.z);
                 const float a = x[2 * q], b = x[2 * q + 1];
                 x[2 * q] = fmaf(a, c, -b * s);
                 x[2 * q + 1] = fmaf(b, c, a * s);
@@ -171,116 +377,9 @@ __device__ __forceinline__ void turn(float *xa, float *xb, const float4 *cs_a, c
     }
 }
 
-template <int D> struct Shape {
-    static constexpr int CH = D / 16;          // lanes per row
-    static constexpr int ROWS = 32 / CH;       // rows a warp handles at a time
-};
-
-// sum over the CH lanes of a row's group, added in lane order
-template <int D> __device__ __forceinline__ float group_sum(float v, int first) {
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < Shape<D>::CH; ++i) s += __shfl_sync(0xffffffffu, v, (first + i) & 31);
-    return s;
-}
-
 __device__ __forceinline__ uint4 pack8(const float *x) {
     return make_uint4(rope::pack2(x[0], x[1]), rope::pack2(x[2], x[3]), rope::pack2(x[4], x[5]),
                       rope::pack2(x[6], x[7]));
-}
-
-constexpr int kAheadFwd = 6, kAheadBwd = 4;        // steps in flight: 48 and 64 KB of a block
-
-template <int D, bool IL>
-__global__ void __launch_bounds__(kThreads)
-mrope_kernel(const Mrope p)
-{
-    constexpr int CH = Shape<D>::CH, ROWS = Shape<D>::ROWS, AHEAD = kAheadFwd;
-    extern __shared__ uint4 s_rows[];                      // [warp][step][chunk a, b][lane]
-    __shared__ int s_pos[kWarps][AHEAD][4];               // the steps' positions, copied with their rows
-    __shared__ float4 s_cs[kWarps][D / 4];
-    __shared__ uint4 s_w[2][D / 8];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int g = lane / CH, c = lane % CH;               // row of the step, chunk of the row
-    const bool live = g < ROWS;
-    const int first = g * CH;
-    if (p.norm_w) {
-        for (int i = threadIdx.x; i < D / 4; i += kThreads)
-            s_w[i / (D / 8)][i % (D / 8)] = reinterpret_cast<const uint4 *>(p.norm_w)[i];
-        __syncthreads();
-    }
-    const float4 *cs_a = s_cs[warp] + (IL ? 2 * c : 4 * c), *cs_b = cs_a + D / 8;
-    uint4 *mine = s_rows + warp * (AHEAD * 64) + lane;
-    const uint32_t mine_a = (uint32_t)__cvta_generic_to_shared(mine);
-    const int rows = p.Hq + p.Hk, per = (rows + p.slices - 1) / p.slices;
-    const int64_t units = p.T * p.slices, stride = (int64_t)gridDim.x * kWarps;
-    const LanePairs pairs = lane_pairs<D>(p, lane);
-
-    Walk fetch;
-    fetch.u = (int64_t)blockIdx.x * kWarps + warp;
-    fetch.enter(p, units, stride, per, 0, rows);
-    auto request = [&](int slot) {                         // this lane's chunks of the fetch step's rows
-        if (!fetch.done(units)) {
-            const int r = fetch.r + g;
-            if (lane < 3) copy4((uint32_t)__cvta_generic_to_shared(&s_pos[warp][slot][lane]), p.pos + 3 * fetch.t + lane);
-            if (live && r < fetch.hi) {
-                const __nv_bfloat16 *src = (r < p.Hq ? p.q_in + fetch.t * p.q_in_stride + (int64_t)r * D
-                                                     : p.k_in + fetch.t * p.k_in_stride + (int64_t)(r - p.Hq) * D) + 8 * c;
-                copy16(mine_a + slot * 1024, src);
-                copy16(mine_a + slot * 1024 + 512, src + D / 2);
-            }
-            fetch.step(p, units, stride, per, 0, rows, ROWS);
-        }
-        copies_commit();
-    };
-    Walk at = fetch;
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) request(i);
-    int64_t turned = -1;                                   // the unit whose turns are in s_cs
-    int slot = 0;
-    while (!at.done(units)) {
-        copies_wait<AHEAD - 1>();
-        if (at.u != turned) {
-            __syncwarp();                                  // the copied position is there, the last turns were read
-            fill_turns<D>(pairs, s_pos[warp][slot], lane, s_cs[warp]);
-            turned = at.u;
-            __syncwarp();
-        }
-        const int r = at.r + g;
-        const bool row = live && r < at.hi, k_row = r >= p.Hq;
-        uint4 va = make_uint4(0u, 0u, 0u, 0u), vb = va;
-        if (row) {
-            va = mine[slot * 64];
-            vb = mine[slot * 64 + 32];
-        }
-        float xa[8], xb[8];
-        unpack8(va, xa);
-        unpack8(vb, xb);
-        if (p.norm_w) {
-            float ss = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(xa[e], xa[e], fmaf(xb[e], xb[e], ss));
-            const float inv = rsqrtf(group_sum<D>(ss, first) * (1.f / D) + p.eps);
-            float wa[8], wb[8];
-            unpack8(s_w[k_row][c], wa);
-            unpack8(s_w[k_row][CH + c], wb);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                xa[e] *= inv * wa[e];
-                xb[e] *= inv * wb[e];
-            }
-        }
-        turn<IL, false>(xa, xb, cs_a, cs_b);
-        if (row) {
-            __nv_bfloat16 *dst = (k_row ? p.k_out + at.t * p.k_out_stride + (int64_t)(r - p.Hq) * D
-                                        : p.q_out + at.t * p.q_out_stride + (int64_t)r * D) + 8 * c;
-            *reinterpret_cast<uint4 *>(dst) = pack8(xa);
-            *reinterpret_cast<uint4 *>(dst + D / 2) = pack8(xb);
-        }
-        request(slot);                                     // read above: the slot is free
-        if (++slot == AHEAD) slot = 0;
-        at.step(p, units, stride, per, 0, rows, ROWS);
-    }
 }
 
 template <int D, bool IL>
@@ -321,7 +420,7 @@ mrope_bwd_kernel(const Mrope p)
         float acc[16];                                    // this lane's columns of the weight sums
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-        Walk fetch;
+        RowWalk fetch;
         fetch.u = (int64_t)blockIdx.x * kWarps + warp;
         fetch.enter(p, units, stride, per, h0, h1);
         auto request = [&](int slot) {
@@ -343,7 +442,7 @@ mrope_bwd_kernel(const Mrope p)
             }
             copies_commit();
         };
-        Walk at = fetch;
+        RowWalk at = fetch;
     #pragma unroll
         for (int i = 0; i < AHEAD; ++i) request(i);
         int64_t turned = -1;
@@ -368,15 +467,15 @@ mrope_bwd_kernel(const Mrope p)
                 }
             }
             float da[8], db[8];
-            unpack8(va, da);
-            unpack8(vb, db);
-            turn<IL, true>(da, db, cs_a, cs_b);           // dz
+            rope::unpack8(va, da);
+            rope::unpack8(vb, db);
+            turn_back<IL>(da, db, cs_a, cs_b);           // dz
             if (norm) {
                 float xa[8], xb[8], dna[8], dnb[8];       // x, dn = dz w
-                unpack8(ua, xa);
-                unpack8(ub, xb);
-                unpack8(s_w[which][c], dna);
-                unpack8(s_w[which][CH + c], dnb);
+                rope::unpack8(ua, xa);
+                rope::unpack8(ub, xb);
+                rope::unpack8(s_w[which][c], dna);
+                rope::unpack8(s_w[which][CH + c], dnb);
                 float ss = 0.f, dot = 0.f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -442,7 +541,7 @@ template <int D> void shape(Mrope &p, int num_sms, int64_t max_blocks, unsigned 
 
 template <int D> cudaError_t launch_fwd(Mrope p, bool il, int num_sms, cudaStream_t stream) {
     unsigned blocks;
-    shape<D>(p, num_sms, (int64_t)num_sms * 4, &blocks);   // resident blocks: 64 registers, 53 KB each
+    shape<D>(p, num_sms, (int64_t)num_sms * 3, &blocks);   // resident blocks: 80 registers, 53 KB each
     constexpr int smem = kWarps * kAheadFwd * 1024;
     auto kern = il ? mrope_kernel<D, true> : mrope_kernel<D, false>;
     static DeviceOnce once[2];

@@ -341,10 +341,14 @@ norm_residual_bwd_kernel(const Bwd p, int rows_per_block)
     }
 }
 
-// Rows above 512 columns: a block per row, fed by a ring of whole rows in shared memory. Registers
-// then hold only the sums and the row's dH, and the loads in flight are the ring's, not the
-// occupancy's: thread 0 keeps bulk copies of the block's next rows running while this one is
-// reduced. A slot is refilled after the first barrier of the next row, when every thread has left it.
+// Rows above 512 columns: a block per row, fed by a ring of whole rows in shared memory, so that the
+// loads in flight are the ring's and not the occupancy's: thread 0 keeps bulk copies of the block's
+// next rows running while this one is reduced.
+//
+// One reduction (and one barrier) per row: dy needs sum_c A dH with A = scale gate w_post y, and
+// dH = dh + r2 (a - h c2), a = dz w_pre, is linear in what the first reduction gives, so
+//   sum A dH = sum A dh + r2 (sum A a - c2 sum A h)
+// and six sums (h^2, a h, y^2, A dh, A a, A h) are taken at once.
 struct Ring {
     int stages, slot;                          // slots, bytes of one
     int at_dz, at_dh, at_y, at_gate;           // byte offsets in a slot (h is at 0)
@@ -360,15 +364,16 @@ __device__ __forceinline__ void unpack4(const uint2 &a, float *x) {
     x[3] = __uint_as_float(a.y & 0xffff0000u);
 }
 
-// 4 consecutive values in bf16 or fp32
-template <bool F32> __device__ __forceinline__ void get4(const void *p, int64_t i, float *x) {
+// piece v (4 values) of a row in shared memory, or 0
+template <bool F32> __device__ __forceinline__ void get4(bool there, const unsigned char *row, int v, float *x) {
     if constexpr (F32) {
-        const float4 a = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+        const float4 a = there ? *reinterpret_cast<const float4 *>(row + 16 * v) : make_float4(0.f, 0.f, 0.f, 0.f);
         x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
     } else {
-        unpack4(*reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p) + i), x);
+        unpack4(there ? *reinterpret_cast<const uint2 *>(row + 8 * v) : make_uint2(0u, 0u), x);
     }
 }
+// 4 consecutive values in bf16 or fp32
 template <bool F32> __device__ __forceinline__ void put4(void *p, int64_t i, const float *x) {
     if constexpr (F32)
         *reinterpret_cast<float4 *>(static_cast<float *>(p) + i) = make_float4(x[0], x[1], x[2], x[3]);
@@ -377,19 +382,22 @@ template <bool F32> __device__ __forceinline__ void put4(void *p, int64_t i, con
             make_uint2(rope::pack2(x[0], x[1]), rope::pack2(x[2], x[3]));
 }
 
-// keeps the loads of a lane's pieces (4 columns each, so that few values are live beside the sums)
-// apart: mixed, or with pieces of 8, the widest variant spills
+constexpr int kSums = 6;
+
+// keeps the loads of a lane's pieces (4 columns each, so that few values are live beside the sums) apart
 __device__ __forceinline__ void one_piece() { asm volatile("" ::: "memory"); }
 
-// WR: the lane's columns of the two weights and of a gate of all tokens stay in registers (from
-// memory they come through an L1 that the ring leaves almost nothing of: 9001 x 5120 took 340 us).
-// Only the widest rows (above 6144 columns: 512 threads of 128 registers) have no room for them.
+// WR: the lane's columns of the weights and of a gate of all tokens stay in registers (from memory
+// they come through an L1 that the ring leaves almost nothing of: 9001 x 5120 took 340 us that way).
+// Rows above 5120 columns, six pieces per lane, have no room for them. Measured at 9001 x 5120 with an
+// fp32 residual and a gate per token: 176 us (5.76 TB/s); with two reductions per row 225 us; with the
+// row's values kept in registers as well 275 us; with two pieces per lane and 640 threads 180 us.
 template <int NP, bool F32, bool WR>
-__global__ void __launch_bounds__(NP == 4 && WR ? 384 : 512)
+__global__ void __launch_bounds__(NP == 2 ? 512 : NP == 4 ? 320 : 352)
 norm_residual_bwd_ring_kernel(const Bwd p, const Ring ring)
 {
     extern __shared__ __align__(128) unsigned char s_ring[];
-    __shared__ float2 s_red2[2 * kMaxWarps];
+    __shared__ __align__(16) float s_red[2][kMaxWarps][8];
     __shared__ uint64_t s_full[kMaxStages];
     const int never = 0;                       // no abort flag: every thread waits for itself
     grid_release();
@@ -424,14 +432,13 @@ norm_residual_bwd_ring_kernel(const Bwd p, const Ring ring)
     if (threadIdx.x == 0)
         for (; fetched < n_rows && fetched < ring.stages; ++fetched) fetch(fetched);
 
-    int buf = 0;
     float a_pre[NP][4], a_post[NP][4], a_gate[NP][4];
 #pragma unroll
     for (int i = 0; i < NP; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) a_pre[i][e] = a_post[i][e] = a_gate[i][e] = 0.f;
-
-    uint2 r_pre[WR ? NP : 1], r_post[WR ? NP : 1], r_gate[WR ? NP : 1];
+    constexpr int NH = WR ? NP : 1;
+    uint2 r_pre[NH], r_post[NH], r_gate[NH];
     if constexpr (WR) {
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
@@ -444,132 +451,123 @@ norm_residual_bwd_ring_kernel(const Bwd p, const Ring ring)
             r_gate[i] = take(gate_tok ? nullptr : p.gate);
         }
     }
-    auto weight4 = [&](const __nv_bfloat16 *w, const uint2 *reg, int i, int v, float *x) {
-        if constexpr (WR)
-            unpack4(reg[i], x);
-        else
-            get4<false>(w, 4 * v, x);
+    // one piece of a row: 0 where an input is not there, 1 for a missing gate or post-norm weight
+    struct Piece {
+        float h[4], dh[4], dz[4], y[4], g[4], wr[4], wo[4];
+    };
+    auto values = [&](const unsigned char *slot, int i, Piece &x) {
+        const int v = i * group + threadIdx.x, k = WR ? i : 0;
+        const bool in = v < nvec;
+        auto word = [&](bool there, int at) {
+            return there && in ? *reinterpret_cast<const uint2 *>(slot + at + 8 * v) : make_uint2(0u, 0u);
+        };
+        get4<F32>(p.w_pre && in, slot, v, x.h);
+        get4<F32>(p.dh && in, slot + ring.at_dh, v, x.dh);
+        unpack4(word(p.w_pre, ring.at_dz), x.dz);
+        unpack4(word(p.y, ring.at_y), x.y);
+        auto weight = [&](const __nv_bfloat16 *w, const uint2 &reg, float *o) {
+            if constexpr (WR)
+                unpack4(reg, o);
+            else
+                unpack4(w && in ? *reinterpret_cast<const uint2 *>(w + 4 * v) : make_uint2(0u, 0u), o);
+        };
+        weight(p.w_pre, r_pre[k], x.wr);
+        if (gate_tok)
+            unpack4(word(true, ring.at_gate), x.g);
+        else if (p.gate)
+            weight(p.gate, r_gate[k], x.g);
+        if (p.w_post) weight(p.w_post, r_post[k], x.wo);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (!p.gate) x.g[e] = 1.f;
+            if (!p.w_post) x.wo[e] = 1.f;
+        }
     };
 
     bool ok = true;
-    int s_at = 0;
+    int s_at = 0, buf = 0;
     uint32_t phase = 0;
     for (int k = 0; k < n_rows; ++k) {
         const int64_t t = blockIdx.x + (int64_t)k * gridDim.x;
         const unsigned char *slot = s_ring + s_at * ring.slot;
-        const __nv_bfloat16 *dz_r = reinterpret_cast<const __nv_bfloat16 *>(slot + ring.at_dz);
-        const __nv_bfloat16 *y_r = reinterpret_cast<const __nv_bfloat16 *>(slot + ring.at_y);
-        const __nv_bfloat16 *g_r = reinterpret_cast<const __nv_bfloat16 *>(slot + ring.at_gate);
         ok = __all_sync(0xffffffffu, sm100::mbar_wait(sm100::smem_addr(&s_full[s_at]), phase, &never, kWaitBudget));
         if (++s_at == ring.stages) {
             s_at = 0;
             phase ^= 1u;
         }
-        // first reduction: sum h^2 and sum dz w_pre h; its barrier also agrees that the row has landed
-        float ss = 0.f, dot = 0.f;
-        if (p.w_pre && ok) {
+        float sum[kSums] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (ok) {
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
-                const int v = i * group + threadIdx.x;
                 if constexpr (!WR) one_piece();
-                if (v >= nvec) continue;
-                float h[4], dz[4], w[4];
-                get4<F32>(slot, 4 * v, h);
-                get4<false>(dz_r, 4 * v, dz);
-                weight4(p.w_pre, r_pre, i, v, w);
+                Piece x;
+                values(slot, i, x);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    ss = fmaf(h[e], h[e], ss);
-                    dot = fmaf(dz[e] * w[e], h[e], dot);
+                    const float a = x.dz[e] * x.wr[e], A = x.g[e] * x.wo[e] * x.y[e];
+                    sum[0] = fmaf(x.h[e], x.h[e], sum[0]);
+                    sum[1] = fmaf(a, x.h[e], sum[1]);
+                    sum[2] = fmaf(x.y[e], x.y[e], sum[2]);
+                    sum[3] = fmaf(A, x.dh[e], sum[3]);
+                    sum[4] = fmaf(A, a, sum[4]);
+                    sum[5] = fmaf(A, x.h[e], sum[5]);
                 }
             }
-            ss = warp_sum(ss);
-            dot = warp_sum(dot);
+#pragma unroll
+            for (int j = 0; j < kSums; ++j) sum[j] = warp_sum(sum[j]);
         }
-        float2 *red = s_red2 + buf * kMaxWarps;
+        float(*red)[8] = s_red[buf];
         buf ^= 1;
-        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(ss, dot);
-        ok = __syncthreads_and(ok);
+        if ((threadIdx.x & 31) == 0) {
+            *reinterpret_cast<float4 *>(red[threadIdx.x >> 5]) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+            *reinterpret_cast<float2 *>(red[threadIdx.x >> 5] + 4) = make_float2(sum[4], sum[5]);
+        }
+        ok = __syncthreads_and(ok);            // also agrees that the row has landed
         if (!ok) break;
-        if (threadIdx.x == 0 && k > 0 && fetched < n_rows) fetch(fetched++);   // the slot of row k - 1
-        float r2 = 0.f, c2 = 0.f;
+        // every thread has left the row before
+        if (threadIdx.x == 0 && k > 0 && fetched < n_rows) fetch(fetched++);
+#pragma unroll
+        for (int j = 0; j < kSums; ++j) sum[j] = 0.f;
+        for (int w = 0; w < wpr; ++w) {
+            const float4 x = *reinterpret_cast<const float4 *>(red[w]);
+            const float2 z = *reinterpret_cast<const float2 *>(red[w] + 4);
+            sum[0] += x.x;
+            sum[1] += x.y;
+            sum[2] += x.z;
+            sum[3] += x.w;
+            sum[4] += z.x;
+            sum[5] += z.y;
+        }
+        float r2 = 0.f, c2 = 0.f, r1 = 1.f, c1 = 0.f;
         if (p.w_pre) {
-            float2 s = make_float2(0.f, 0.f);
-            for (int w = 0; w < wpr; ++w) {
-                s.x += red[w].x;
-                s.y += red[w].y;
-            }
-            r2 = rsqrtf(s.x * inv_c + p.eps);
-            c2 = r2 * r2 * (s.y * inv_c);             // dH = dh + r2 (dz w - h c2)
+            r2 = rsqrtf(sum[0] * inv_c + p.eps);
+            c2 = r2 * r2 * (sum[1] * inv_c);          // dH = dh + r2 (a - h c2)
         }
-        float dH[NP][4];
-        float ssy = 0.f, doty = 0.f;
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const int v = i * group + threadIdx.x;
-            if constexpr (!WR) one_piece();
-#pragma unroll
-            for (int e = 0; e < 4; ++e) dH[i][e] = 0.f;
-            if (v >= nvec) continue;
-            if (p.dh) get4<F32>(slot + ring.at_dh, 4 * v, dH[i]);
-            if (p.w_pre) {
-                float h[4], dz[4], w[4];
-                get4<F32>(slot, 4 * v, h);
-                get4<false>(dz_r, 4 * v, dz);
-                weight4(p.w_pre, r_pre, i, v, w);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    dH[i][e] = fmaf(r2, fmaf(dz[e], w[e], -h[e] * c2), dH[i][e]);
-                    a_pre[i][e] = fmaf(dz[e], h[e] * r2, a_pre[i][e]);
-                }
-            }
-            put4<F32>(p.dx, t * p.dx_stride + 4 * v, dH[i]);
-            if (p.w_post) {
-                // second reduction: sum y^2 and sum du w_post y
-                float y[4], w[4], g[4];
-                get4<false>(y_r, 4 * v, y);
-                weight4(p.w_post, r_post, i, v, w);
-                if (gate_tok) get4<false>(g_r, 4 * v, g);
-                else if (p.gate) weight4(p.gate, r_gate, i, v, g);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float du = p.scale * dH[i][e] * (p.gate ? g[e] : 1.f);
-                    ssy = fmaf(y[e], y[e], ssy);
-                    doty = fmaf(du * w[e], y[e], doty);
-                }
-            }
-        }
-        float r1 = 1.f, c1 = 0.f;
         if (p.w_post) {
-            const float2 s = row_sum2(ssy, doty, wpr, s_red2, buf);
-            r1 = rsqrtf(s.x * inv_c + p.eps);
-            c1 = r1 * r1 * (s.y * inv_c);             // dy = r1 (du w - y c1)
+            r1 = rsqrtf(sum[2] * inv_c + p.eps);
+            c1 = r1 * r1 * (p.scale * fmaf(r2, fmaf(-c2, sum[5], sum[4]), sum[3]) * inv_c);   // dy = r1 (du w - y c1)
         }
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int v = i * group + threadIdx.x;
             if constexpr (!WR) one_piece();
             if (v >= nvec) continue;
-            float y[4], w[4], g[4], dy[4], dg[4];
-            if (p.y) get4<false>(y_r, 4 * v, y);
-            if (gate_tok) get4<false>(g_r, 4 * v, g);
-                else if (p.gate) weight4(p.gate, r_gate, i, v, g);
-            if (p.w_post) weight4(p.w_post, r_post, i, v, w);
+            Piece x;
+            values(slot, i, x);
+            float dx[4], dy[4], dg[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float d = p.scale * dH[i][e];
-                const float du = p.gate ? d * g[e] : d;
-                if (p.y) {
-                    const float yh = y[e] * r1;
-                    dg[e] = d * (p.w_post ? yh * w[e] : y[e]);
-                    a_gate[i][e] += dg[e];
-                    a_post[i][e] = fmaf(du, yh, a_post[i][e]);
-                }
-                dy[e] = p.w_post ? r1 * fmaf(du, w[e], -y[e] * c1) : du;
+                dx[e] = fmaf(r2, fmaf(x.dz[e], x.wr[e], -x.h[e] * c2), x.dh[e]);
+                a_pre[i][e] = fmaf(x.dz[e], x.h[e] * r2, a_pre[i][e]);
+                const float d = p.scale * dx[e], du = d * x.g[e], yh = x.y[e] * r1;
+                dg[e] = d * yh * x.wo[e];
+                a_gate[i][e] += dg[e];
+                a_post[i][e] = fmaf(du, yh, a_post[i][e]);
+                dy[e] = p.w_post ? r1 * fmaf(du, x.wo[e], -x.y[e] * c1) : du;
             }
+            put4<F32>(p.dx, t * p.dx_stride + 4 * v, dx);
             put4<false>(p.dy, t * p.dy_stride + 4 * v, dy);
-            if (gate_tok && p.dgate)
-                put4<false>(p.dgate, t * p.dgate_stride + 4 * v, dg);
+            if (gate_tok && p.dgate) put4<false>(p.dgate, t * p.dgate_stride + 4 * v, dg);
         }
     }
     if (!ok) {
@@ -723,10 +721,10 @@ cudaError_t launch_bwd(const Bwd &p, const SumOut &o, int32_t *status, int num_s
         }
     } else if (p.C <= 4096) {
         e = launch_ring<2, F32, true>(p, status, num_sms, &blocks, stream);
-    } else if (p.C <= 6144) {
+    } else if (p.C <= 5120) {
         e = launch_ring<4, F32, true>(p, status, num_sms, &blocks, stream);
     } else {
-        e = launch_ring<4, F32, false>(p, status, num_sms, &blocks, stream);
+        e = launch_ring<6, F32, false>(p, status, num_sms, &blocks, stream);
     }
     if (e != cudaSuccess || p.n_sum == 0) return e;
     return launch_column_sum(p.part, (int)blocks * rows, p.n_sum, p.C, o.out[0], o.out[1], o.out[2], stream);
