@@ -451,8 +451,8 @@ enum {
  *   a_m = pos_thw[t, axis(m)] * inv_freq[m]    for the pairs m < D/2
  *   y = xn with every pair (m, m + D/2), or (2m, 2m + 1), turned by a_m
  * in fp32, rounded to bf16 once (vit_qk_norm_rope also rounds the norm's two steps). The angle is
- * formed and reduced in fp64, so it is as good at position 2^31 - 1 as at 0. Negative positions
- * are allowed.
+ * formed without rounding and reduced by 2 pi before it becomes fp32 (error below 2^-20), so it is
+ * as good at position 2^31 - 1 as at 0. Negative positions are allowed.
  *
  *   q_in, q_out   device bf16 [T, Hq, D]; q_out may be q_in (same stride). Both NULL: q is left out.
  *   k_in, k_out   the same with Hk heads. At least one of q and k is given.
@@ -514,7 +514,8 @@ size_t vit_cross_attn_workspace_size(int64_t Tq, int64_t Tk, int Hq, int Hkv, in
  * latent queries alike: where there are few query rows the keys are split over the GPU and the parts
  * joined; results do not change from run to run.
  *
- *   q, out       device bf16 [Tq, Hq, D]; k, v device bf16 [Tk, Hkv, D]; Hq a multiple of Hkv.
+ *   q, out       device bf16 [Tq, Hq, D]; k, v device bf16 [Tk, Hkv, D]; Hq a multiple of Hkv;
+ *                Tq, Tk <= 2^31 - 2^16. out must not overlap an input.
  *   cu_q, cu_k   device int32 [B + 1], ascending; rows before cu[0] and from cu[B] on belong to no
  *                sequence: they are not read, and out and lse are left as they were there.
  *   k_len        device int32 [B], or NULL: how many of a sequence's key rows are real (encoder
@@ -564,8 +565,7 @@ vit_status_t vit_cross_attn_bwd(const void *dout, const void *q, const void *k, 
                                 const int32_t *cu_q, const int32_t *cu_k, const int32_t *k_len, int B, int max_q,
                                 int max_k, float scale, void *dq, void *dk, void *dv, int64_t dq_stride,
                                 int64_t dk_stride, int64_t dv_stride, int zero_rest, void *workspace,
-                                size_t workspace_bytes,
-                                int32_t *status_dev, vit_stream_t stream);
+                                size_t workspace_bytes, int32_t *status_dev, vit_stream_t stream);
 
 /* Storage of the residual stream (vit_norm_residual). */
 enum {

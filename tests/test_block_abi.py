@@ -103,7 +103,7 @@ def both(L, **kw):
 
 def test_cross_attention_and_gradient(L):
     assert both(L, D=72) == -2
-    assert both(L, Hq=9) == -3 and both(L, Hk=0) == -3 and both(L, Tq=-1) == -3 and both(L, Tk=1 << 31) == -3
+    assert both(L, Hq=9) == -3 and both(L, Hk=0) == -3 and both(L, Tq=-1) == -3 and both(L, Tk=(1 << 31) - (1 << 16) + 1) == -3
     assert both(L, B=-1) == -3 and both(L, B=8193) == -7
     assert both(L, mq=-1) == -14 and both(L, scale=float("inf")) == -14
     assert both(L, q=None) == -1 and both(L, v=None) == -1 and both(L, cuk=None) == -1 and both(L, ws=None) == -1
@@ -126,8 +126,10 @@ def test_cross_workspace_sizes(L):
     # one new token each, long states: a split's partial rows; bounds above the totals are the totals
     assert f(4, 40000, 8, 2, 64, 4, 1, 40000) == f(4, 40000, 8, 2, 64, 4, 1, 1 << 30) > 0
     assert f(5000, 9000, 16, 16, 80, 3) > 0 and g(5000, 9000, 16, 16, 80, 3) >= 5000 * 16 * 8
-    # offsets of a long cache pass 32 bits
-    assert f(64, 2 ** 31 - 1, 64, 8, 128, 64, 1, 2 ** 31 - 1) > 0
+    # a long cache: element offsets pass 32 bits; rows up to 2^31 - 2^16
+    most = 2 ** 31 - 2 ** 16
+    assert f(64, most, 64, 8, 128, 64, 1, most) > 0 and f(64, most + 1, 64, 8, 128, 64, 1, most) == 0
+    assert f(1, most, 1, 1, 32, 8192, 1, most) > 0 and g(1, most, 1, 1, 32, 8192, 1, most) > 0
 
 
 NORM = "x y gate wo wr h z T C res xs ys gs hs zs scale eps stream".split()

@@ -17,6 +17,7 @@ bool heads_ok(int H) { return H >= 1 && H <= 65535; }
 vit_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? VIT_OK : VIT_ERR_CUDA; }
 
 constexpr int64_t kMaxTokens = (int64_t)1 << 31;
+constexpr int64_t kMaxRows = kMaxTokens - (1 << 16);   // of a cross-attention side: a tile past the end still fits an int
 constexpr int kMaxWidth = 8192;
 
 // the checks that the three-axis rotary calls share
@@ -181,7 +182,7 @@ namespace {
 vit_status_t cross_sizes(int64_t Tq, int64_t Tk, int Hq, int Hkv, int D, int B, int *max_q, int *max_k)
 {
     if (!head_dim_ok(D)) return VIT_ERR_BAD_HEAD_DIM;
-    if (Tq < 0 || Tq >= kMaxTokens || Tk < 0 || Tk >= kMaxTokens || !heads_ok(Hq) || !heads_ok(Hkv) || Hq % Hkv != 0 ||
+    if (Tq < 0 || Tq > kMaxRows || Tk < 0 || Tk > kMaxRows || !heads_ok(Hq) || !heads_ok(Hkv) || Hq % Hkv != 0 ||
         B < 0)
         return VIT_ERR_BAD_SHAPE;
     if (B > VIT_MAX_SEGMENTS) return VIT_ERR_TOO_MANY_SEGMENTS;
@@ -292,8 +293,7 @@ vit_status_t vit_cross_attn_bwd(const void *dout, const void *q, const void *k, 
                                 const int32_t *cu_q, const int32_t *cu_k, const int32_t *k_len, int B, int max_q,
                                 int max_k, float scale, void *dq, void *dk, void *dv, int64_t dq_stride,
                                 int64_t dk_stride, int64_t dv_stride, int zero_rest, void *workspace,
-                                size_t workspace_bytes,
-                                int32_t *status_dev, vit_stream_t stream)
+                                size_t workspace_bytes, int32_t *status_dev, vit_stream_t stream)
 {
     TraceRange trace("vit_cross_attn_bwd");
     vit_status_t st = cross_sizes(Tq, Tk, Hq, Hkv, D, B, &max_q, &max_k);

@@ -37,6 +37,11 @@ __device__ __forceinline__ bool load_seg(const CrossSegs &s, int b, CrossSeg &x,
     return err == 0;
 }
 
+// runs of `chunk` keys that n keys make (the sum may pass 31 bits)
+__host__ __device__ inline int key_runs(int n, int chunk) {
+    return (int)(((unsigned)n + (unsigned)chunk - 1u) / (unsigned)chunk);
+}
+
 struct CrossArgs {
     const void *q, *k, *v;        // bf16 [Tq, Hq, D], [Tk, Hk, D], [Tk, Hk, D]
     void *out;                    // bf16 [Tq, Hq, D]

@@ -339,7 +339,7 @@ cross_join_kernel(const Few p)
     grid_wait();                                              // the runs' results
     if (!fine) return;
     const int n_rows = seg.qn * p.Hq;                         // (token, head) rows of the sequence
-    const int runs = (seg.kn + p.chunk - 1) / p.chunk;
+    const int runs = key_runs(seg.kn, p.chunk);
     const int x = WIDE ? (int)blockIdx.x : (int)blockIdx.x * 8 + warp;
     if (x >= n_rows) return;
     const int tok = x / p.Hq, head = x - tok * p.Hq, hk = head / p.group;
@@ -468,7 +468,7 @@ FewPlan few_plan(int B, int Hq, int Hk, int D, int max_q, int max_k)
     chunk = (chunk + kTile - 1) / kTile * kTile;
     if (chunk < kTile) chunk = kTile;
     n = max_k > 0 ? ((int64_t)max_k + chunk - 1) / chunk : 1;
-    p.chunk = (int)(chunk < (1 << 30) ? chunk : (1 << 30));
+    p.chunk = (int)chunk;
     p.n_split = (int)n;
     p.partial_bytes = n > 1 ? sizeof(float) * (size_t)pairs * n * p.rows * (D + 1) : 0;
     return p;

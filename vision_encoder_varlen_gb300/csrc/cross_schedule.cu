@@ -72,7 +72,7 @@ cross_schedule_kernel(const CrossSegs segs, int Hq, int lg_pack, int chunk, int 
         CrossSeg x;
         if (!seg_at(p, x)) continue;
         const int64_t n = (int64_t)packs * ((x.qn + (1 << lg_block) - 1) >> lg_block);
-        const int runs = chunk > 0 ? (x.kn + chunk - 1) / chunk : 1;
+        const int runs = chunk > 0 ? key_runs(x.kn, chunk) : 1;
         n_items += n * runs;
         if (runs > 1) n_tiles += n;
     }
@@ -83,7 +83,7 @@ cross_schedule_kernel(const CrossSegs segs, int Hq, int lg_pack, int chunk, int 
         CrossSeg x;
         if (!seg_at(p, x)) continue;
         const int nq = (x.qn + (1 << lg_block) - 1) >> lg_block;
-        const int runs = chunk > 0 ? (x.kn + chunk - 1) / chunk : 1;
+        const int runs = chunk > 0 ? key_runs(x.kn, chunk) : 1;
         s_key[p] = ((unsigned long long)at << 32) | (uint32_t)(s_key[p] & 0xffffffffu);   // first item | sequence
         if (runs > 1) {
             for (int i = 0; i < packs * nq; ++i) {
@@ -103,7 +103,7 @@ cross_schedule_kernel(const CrossSegs segs, int Hq, int lg_pack, int chunk, int 
         load_seg(segs, (int)(s_key[p] & 0xffffffffu), x, nullptr, false);
         const int first = (int)(s_key[p] >> 32);
         const int nq = (x.qn + (1 << lg_block) - 1) >> lg_block;
-        const int runs = chunk > 0 ? (x.kn + chunk - 1) / chunk : 1;
+        const int runs = chunk > 0 ? key_runs(x.kn, chunk) : 1;
         const int n = packs * nq * runs;
         for (int i = lane; i < n; i += 32) {
             const int run = i % runs, j = i / runs, h = j / nq, qb = j - h * nq;
