@@ -197,7 +197,7 @@ struct NormResidualGrad {
     float scale, eps;
     int32_t *status;
 };
-constexpr int kNormResidualParts = 608;   // row groups of the gradient kernel at most
+constexpr int kNormResidualParts = 608;   // blocks of the gradient kernel at most
 cudaError_t launch_norm_residual(const NormResidualArgs &a, int num_sms, cudaStream_t stream);
 cudaError_t launch_norm_residual_bwd(const NormResidualGrad &a, int num_sms, cudaStream_t stream);
 

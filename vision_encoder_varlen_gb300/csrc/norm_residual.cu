@@ -88,21 +88,6 @@ __device__ __forceinline__ float row_sum(float v, int wpr, float *red, int &buf)
     for (int w = 0; w < wpr; ++w) s += r[w];
     return s;
 }
-__device__ __forceinline__ float2 row_sum2(float a, float b, int wpr, float2 *red, int &buf) {
-    a = warp_sum(a);
-    b = warp_sum(b);
-    if (wpr == 1) return make_float2(a, b);
-    float2 *r = red + buf * kMaxWarps;
-    buf ^= 1;
-    if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = make_float2(a, b);
-    __syncthreads();
-    float2 s = make_float2(0.f, 0.f);
-    for (int w = 0; w < wpr; ++w) {
-        s.x += r[w].x;
-        s.y += r[w].y;
-    }
-    return s;
-}
 
 struct Fwd {
     const void *x;
@@ -214,13 +199,11 @@ __global__ void __launch_bounds__(256)
 norm_residual_bwd_kernel(const Bwd p, int rows_per_block)
 {
     grid_release();
-    constexpr int wpr = 1;
-    __shared__ float2 s_red2[2 * kMaxWarps];
+    __shared__ float3 s_sum[256 * VPT];
     const int lane_in_row = threadIdx.x & 31, row_in_block = (int)(threadIdx.x >> 5);
     const int nvec = p.C >> 3, group = 32;
     const float inv_c = 1.f / (float)p.C;
     const bool gate_tok = p.gate && p.gate_stride != 0;
-    int buf = 0;
     float a_pre[VPT][8], a_post[VPT][8], a_gate[VPT][8];
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
@@ -263,7 +246,7 @@ norm_residual_bwd_kernel(const Bwd p, int rows_per_block)
                     dot = fmaf(dz[e] * w[e], h[e], dot);
                 }
             }
-            const float2 s = row_sum2(ss, dot, wpr, s_red2, buf);
+            const float2 s = make_float2(warp_sum(ss), warp_sum(dot));
             r2 = rsqrtf(s.x * inv_c + p.eps);
             c2 = r2 * r2 * (s.y * inv_c);             // dH = dh + r2 (dz w - h c2)
         }
@@ -302,7 +285,7 @@ norm_residual_bwd_kernel(const Bwd p, int rows_per_block)
         }
         float r1 = 1.f, c1 = 0.f;
         if (p.w_post) {
-            const float2 s = row_sum2(ssy, doty, wpr, s_red2, buf);
+            const float2 s = make_float2(warp_sum(ssy), warp_sum(doty));
             r1 = rsqrtf(s.x * inv_c + p.eps);
             c1 = r1 * r1 * (s.y * inv_c);             // dy = r1 (du w - y c1)
         }
@@ -330,14 +313,28 @@ norm_residual_bwd_kernel(const Bwd p, int rows_per_block)
         }
     }
     if (p.n_sum == 0) return;
-    float *dst = p.part + ((int64_t)blockIdx.x * rows_per_block + row_in_block) * p.n_sum * p.C;
+    // the block's sums: its warps add theirs one after the other
+    for (int w = 0; w < rows_per_block; ++w) {
+        if (row_in_block == w) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int v = i * group + lane_in_row;
-        if (v >= nvec) continue;
-        if (p.at_pre >= 0) Vec8<true>::store(dst, (int64_t)p.at_pre * p.C + 8 * v, a_pre[i]);
-        if (p.at_post >= 0) Vec8<true>::store(dst, (int64_t)p.at_post * p.C + 8 * v, a_post[i]);
-        if (p.at_gate >= 0) Vec8<true>::store(dst, (int64_t)p.at_gate * p.C + 8 * v, a_gate[i]);
+            for (int i = 0; i < VPT; ++i) {
+                const int v = i * group + lane_in_row;
+                if (v >= nvec) continue;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float3 t = w > 0 ? s_sum[8 * v + e] : make_float3(0.f, 0.f, 0.f);
+                    s_sum[8 * v + e] = make_float3(t.x + a_pre[i][e], t.y + a_post[i][e], t.z + a_gate[i][e]);
+                }
+            }
+        }
+        __syncthreads();
+    }
+    float *dst = p.part + (int64_t)blockIdx.x * p.n_sum * p.C;
+    for (int c = threadIdx.x; c < p.C; c += blockDim.x) {
+        const float3 t = s_sum[c];
+        if (p.at_pre >= 0) dst[(int64_t)p.at_pre * p.C + c] = t.x;
+        if (p.at_post >= 0) dst[(int64_t)p.at_post * p.C + c] = t.y;
+        if (p.at_gate >= 0) dst[(int64_t)p.at_gate * p.C + c] = t.z;
     }
 }
 
@@ -706,12 +703,11 @@ template <bool F32>
 cudaError_t launch_bwd(const Bwd &p, const SumOut &o, int32_t *status, int num_sms, cudaStream_t stream)
 {
     unsigned blocks = 0;
-    int rows = 1;
     cudaError_t e = cudaSuccess;
     if (p.C <= 512) {
-        rows = 8;
+        const int rows = 8;
         const int64_t want = (p.T + rows - 1) / rows;
-        int64_t cap = kNormResidualParts / rows;
+        const int64_t most = (int64_t)num_sms * 4, cap = most < kNormResidualParts ? most : kNormResidualParts;
         blocks = (unsigned)(want < cap ? want : cap);
         if (blocks > 0) {
             LaunchScope scope("norm_residual_bwd", stream);
@@ -727,7 +723,7 @@ cudaError_t launch_bwd(const Bwd &p, const SumOut &o, int32_t *status, int num_s
         e = launch_ring<6, F32, false>(p, status, num_sms, &blocks, stream);
     }
     if (e != cudaSuccess || p.n_sum == 0) return e;
-    return launch_column_sum(p.part, (int)blocks * rows, p.n_sum, p.C, o.out[0], o.out[1], o.out[2], stream);
+    return launch_column_sum(p.part, (int)blocks, p.n_sum, p.C, o.out[0], o.out[1], o.out[2], stream);
 }
 
 }  // namespace
