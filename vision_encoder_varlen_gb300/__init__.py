@@ -464,18 +464,19 @@ def _addr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
 
-def _made(stream, *tensors):
-    """Tells the allocator that tensors allocated by a call are used on the stream the call was given."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
+    """A tensor on like's device that a call will write: from the pool of the stream the call is given (memory
+    that the current stream has let go of may still be in use there), and marked as used on the current one."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        t = like.new_empty(shape, dtype=dtype)
+    t.record_stream(torch.cuda.current_stream(like.device))
+    return t
 
 
 def _scratch(need: int, like: torch.Tensor, stream) -> torch.Tensor:
-    ws = like.new_empty(max(need, 16), dtype=torch.uint8)
-    _made(stream, ws)
-    return ws
+    return _new(like, max(need, 16), torch.uint8, stream)
 
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
@@ -507,9 +508,8 @@ def grid_positions(grid_thw: torch.Tensor, total_tokens: int, *, status: torch.T
     dev, n, T = _device(grid_thw, status), grid_thw.shape[0], int(total_tokens)
     if T < 0:
         raise ValueError("total_tokens must not be negative")
-    pos, cu = grid_thw.new_empty((T, 3)), grid_thw.new_empty(n + 1)
-    _made(stream, pos, cu)
-    _call("vit_grid_positions", dev, stream, _addr(grid_thw), n, T, _addr(pos), _addr(cu), _addr(status))
+    pos, cu = _new(grid_thw, (T, 3), _I32, stream), _new(grid_thw, n + 1, _I32, stream)
+    _call("vit_grid_positions", dev, stream, _addr(grid_thw), n, T, _addr(pos), _addr(cu), _word(status))
     return pos, cu
 
 
@@ -553,9 +553,7 @@ def qk_norm_mrope(q: torch.Tensor | None, k: torch.Tensor | None, pos_thw: torch
         H = _shape3(x, name)[1]
         xs = _rows3(x, name, T, H, D)
         if out is None:
-            out = x.new_empty((T, H, D))
-            _made(stream, out)
-            return out, H, xs, H * D
+            return _new(x, (T, H, D), _BF16, stream), H, xs, H * D
         return out, H, xs, _rows3(out, name + "_out", T, H, D)
 
     q_out, Hq, qs, qos = half(q, q_out, "q")
@@ -593,16 +591,13 @@ def qk_norm_mrope_bwd(dq: torch.Tensor | None, dk: torch.Tensor | None, q: torch
             x = None
         if inplace:
             return d, H, ds, ds, xs, x
-        out = d.new_empty((T, H, D))
-        _made(stream, out)
-        return out, H, ds, H * D, xs, x
+        return _new(d, (T, H, D), _BF16, stream), H, ds, H * D, xs, x
 
     dq_in, Hq, dqs, dqis, qs, q = half(dq, q, "q")
     dk_in, Hk, dks, dkis, ks, k = half(dk, k, "k")
     dw = None
     if norm_w is not None:
-        dw = inv_freq.new_empty((2, D))
-        _made(stream, dw)
+        dw = _new(inv_freq, (2, D), _F32, stream)
         if workspace is None:
             workspace = _scratch(lib().vit_qk_norm_mrope_bwd_workspace_size(D), ref, stream)
     _call("vit_qk_norm_mrope_bwd", dev, stream, _addr(dq), _addr(dq_in), _addr(dk), _addr(dk_in), _addr(q), _addr(k),
@@ -611,7 +606,20 @@ def qk_norm_mrope_bwd(dq: torch.Tensor | None, dk: torch.Tensor | None, q: torch
 
 
 def _bytes(t: torch.Tensor | None) -> int:
-    return 0 if t is None else t.numel() * t.element_size()
+    if t is None:
+        return 0
+    if not t.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    return t.numel() * t.element_size()
+
+
+def _word(status: torch.Tensor | None):
+    """Address of a status word."""
+    if status is None:
+        return None
+    if status.dtype is not _I32 or status.numel() < 1:
+        raise ValueError("status must be a CUDA int32 tensor (new_status)")
+    return status.data_ptr()
 
 
 def cross_attn_workspace_size(Tq: int, Tk: int, Hq: int, Hkv: int, D: int, B: int, max_q: int = 0,
@@ -658,21 +666,19 @@ def cross_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Te
     B = _cross_lists(cu_q, cu_k, k_len)
     max_q, max_k = _max_seqlen(max_q), _max_seqlen(max_k)
     if out is None:
-        out = q.new_empty((Tq, Hq, D))
-        _made(stream, out)
+        out = _new(q, (Tq, Hq, D), _BF16, stream)
         os_ = Hq * D
     else:
         os_ = _rows3(out, "out", Tq, Hq, D)
     if lse is not None:
         _lse_ok(lse, Tq, Hq)
     elif return_lse:
-        lse = q.new_empty((Tq, Hq), dtype=_F32)
-        _made(stream, lse)
+        lse = _new(q, (Tq, Hq), _F32, stream)
     if workspace is None:
         workspace = _scratch(lib().vit_cross_attn_workspace_size(Tq, Tk, Hq, Hkv, D, B, max_q, max_k), q, stream)
     _call("vit_cross_attn", dev, stream, _addr(q), _addr(k), _addr(v), Tq, Tk, Hq, Hkv, D, qs, ks, vs, _addr(cu_q),
           _addr(cu_k), _addr(k_len), B, max_q, max_k, 0.0 if scale is None else float(scale), _addr(out), os_,
-          _addr(lse), _addr(workspace), _bytes(workspace), _addr(status))
+          _addr(lse), _addr(workspace), _bytes(workspace), _word(status))
     return (out, lse) if lse is not None else out
 
 
@@ -696,15 +702,14 @@ def cross_attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
     if any(given) and not all(given):
         raise ValueError("give all of dq, dk and dv, or none")
     if not any(given):
-        dq, dk, dv = q.new_empty((Tq, Hq, D)), k.new_empty((Tk, Hkv, D)), k.new_empty((Tk, Hkv, D))
-        _made(stream, dq, dk, dv)
+        dq, dk, dv = (_new(q, n, _BF16, stream) for n in ((Tq, Hq, D), (Tk, Hkv, D), (Tk, Hkv, D)))
     dqs, dks, dvs = _rows3(dq, "dq", Tq, Hq, D), _rows3(dk, "dk", Tk, Hkv, D), _rows3(dv, "dv", Tk, Hkv, D)
     if workspace is None:
         workspace = _scratch(lib().vit_cross_attn_bwd_workspace_size(Tq, Tk, Hq, Hkv, D, B, max_q, max_k), q, stream)
     _call("vit_cross_attn_bwd", dev, stream, _addr(dout), _addr(q), _addr(k), _addr(v), _addr(out), _addr(lse), Tq,
           Tk, Hq, Hkv, D, dos, qs, ks, vs, os_, _addr(cu_q), _addr(cu_k), _addr(k_len), B, max_q, max_k,
           0.0 if scale is None else float(scale), _addr(dq), _addr(dk), _addr(dv), dqs, dks, dvs,
-          0 if given[0] else 1, _addr(workspace), _bytes(workspace), _addr(status))
+          0 if given[0] else 1, _addr(workspace), _bytes(workspace), _word(status))
     return dq, dk, dv
 
 
@@ -762,15 +767,13 @@ def norm_residual(x: torch.Tensor, y: torch.Tensor, *, gate: torch.Tensor | None
         raise ValueError("z_out needs w_pre")
     hs = zs = C
     if h_out is None:
-        h_out = x.new_empty((T, C))
-        _made(stream, h_out)
+        h_out = _new(x, (T, C), x.dtype, stream)
     else:
         hs = _rows2(h_out, "h_out", T, C, x.dtype)
     if z_out is not None:
         zs = _rows2(z_out, "z_out", T, C, _BF16)
     elif w_pre is not None:
-        z_out = y.new_empty((T, C))
-        _made(stream, z_out)
+        z_out = _new(y, (T, C), _BF16, stream)
     _call("vit_norm_residual", dev, stream, _addr(x), _addr(y), _addr(gate), _addr(w_post), _addr(w_pre),
           _addr(h_out), _addr(z_out), T, C, res, xs, ys, gs, hs, zs, float(scale), float(eps))
     return h_out, z_out
@@ -805,24 +808,22 @@ def norm_residual_bwd(dz: torch.Tensor | None, dh: torch.Tensor | None, h: torch
     gs = _gate_stride(gate, T, C)
     _channel(w_post, "w_post", C)
     _channel(w_pre, "w_pre", C)
-    dx, dy = ref.new_empty((T, C)), ref.new_empty((T, C), dtype=_BF16)
+    dx, dy = _new(ref, (T, C), ref.dtype, stream), _new(ref, (T, C), _BF16, stream)
     sums = (gate is not None and gate.dim() == 1) + (w_post is not None) + (w_pre is not None)
-    vec = list(ref.new_empty((sums, C), dtype=_F32).unbind(0)) if sums else []
-    _made(stream, dx, dy, *vec)
+    vec = list(_new(ref, (sums, C), _F32, stream).unbind(0)) if sums else []
     dgate = None
     if gate is not None:
         if gate.dim() == 1:
             dgate = vec.pop()
         else:
-            dgate = gate.new_empty((T, C))
-            _made(stream, dgate)
+            dgate = _new(gate, (T, C), _BF16, stream)
     dw_post = vec.pop() if w_post is not None else None
     dw_pre = vec.pop() if w_pre is not None else None
     if workspace is None:
         workspace = _scratch(lib().vit_norm_residual_bwd_workspace_size(C) if sums else 0, ref, stream)
     _call("vit_norm_residual_bwd", dev, stream, _addr(dz), _addr(dh), _addr(h), _addr(y), _addr(gate), _addr(w_post),
           _addr(w_pre), _addr(dx), _addr(dy), _addr(dgate), _addr(dw_post), _addr(dw_pre), T, C, res, zs, ds, hs, ys,
-          gs, C, C, C, float(scale), float(eps), _addr(workspace), _bytes(workspace), _addr(status))
+          gs, C, C, C, float(scale), float(eps), _addr(workspace), _bytes(workspace), _word(status))
     return dx, dy, dgate, dw_post, dw_pre
 
 
