@@ -404,7 +404,7 @@ vit_status_t vit_norm_residual(const void *x, const void *y, const void *gate, c
 size_t vit_norm_residual_bwd_workspace_size(int C)
 {
     if (C < 8 || C > kMaxWidth || C % 8 != 0) return 0;
-    return sizeof(float) * 3 * (size_t)C * kNormResidualParts;
+    return sizeof(float) * 3 * (size_t)C * norm_residual_parts(C);
 }
 
 vit_status_t vit_norm_residual_bwd(const void *dz, const void *dh, const void *h, const void *y, const void *gate,

@@ -63,7 +63,6 @@ struct FewPlan {
     int n_split;                  // splits of the longest sequence
     size_t partial_bytes;         // workspace of the partial results (0 with one split)
 };
-constexpr int kDesignSms = 152;   // the plans count on this many SMs
 bool takes_few(int B, int Hq, int Hk, int D, int max_q, int max_k);   // else the tcgen05 kernel takes the call
 FewPlan few_plan(int B, int Hq, int Hk, int D, int max_q, int max_k);
 cudaError_t launch_cross_few(const CrossArgs &a, const FewPlan &p, cudaStream_t stream);

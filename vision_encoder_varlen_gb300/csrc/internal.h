@@ -178,6 +178,7 @@ cudaError_t launch_mrope(const MropeArgs &a, int num_sms, cudaStream_t stream);
 cudaError_t launch_mrope_bwd(const MropeArgs &a, float *dnorm_w, int num_sms, cudaStream_t stream);
 
 // Residual step with the norms on either side (x, h, dh, dx in fp32 when res_f32, else bf16).
+constexpr int kDesignSms = 152;   // the sizes of workspaces count on this many SMs
 struct NormResidualArgs {
     const void *x, *y, *gate, *w_post, *w_pre;
     void *h_out, *z_out;
@@ -190,14 +191,14 @@ struct NormResidualGrad {
     const void *dz, *dh, *h, *y, *gate, *w_post, *w_pre;
     void *dx, *dy, *dgate;        // dgate: bf16 [T, C] for a per-token gate, fp32 [C] otherwise
     float *dw_post, *dw_pre;      // fp32 [C]
-    float *part;                  // workspace of kNormResidualParts rows of sums
+    float *part;                  // workspace of norm_residual_parts(C) rows of sums
     int64_t T, dz_stride, dh_stride, h_stride, y_stride, gate_stride, dx_stride, dy_stride, dgate_stride;
     int C;
     bool res_f32;
     float scale, eps;
     int32_t *status;
 };
-constexpr int kNormResidualParts = 608;   // blocks of the gradient kernel at most
+int norm_residual_parts(int C);            // row groups of the gradient kernel at most
 cudaError_t launch_norm_residual(const NormResidualArgs &a, int num_sms, cudaStream_t stream);
 cudaError_t launch_norm_residual_bwd(const NormResidualGrad &a, int num_sms, cudaStream_t stream);
 

@@ -11,11 +11,12 @@
 //   dy = r1 (du w_post - yh mean(du w_post yh))           (or dy = du)
 //   dw_pre = sum_t dz hh,  dw_post = sum_t du yh,  dg (per channel) = sum_t scale u dH
 //
-// Everything is HBM bound: a row is read once into registers, both reductions run on it there in
-// fp32, and it is written once. A row belongs to a group of `wpr` warps, each lane holding VPT
-// pieces of 8 columns; a group of one warp needs shuffles only, larger ones (a whole block) meet
-// in shared memory. h is normalised before it is rounded to its storage type; the gradient
-// recomputes r2 from the stored h it is given.
+// Everything is HBM bound: a row is read once, the reductions run on it in fp32 and it is written
+// once. Forward, a row belongs to a group of `wpr` warps, each lane holding VPT pieces of 8 columns in
+// registers; a group of one warp needs shuffles only, larger ones (a whole block) meet in shared memory.
+// 37007 x 1280 in bf16 takes 72 us (5.3 TB/s; a plain copy of as many bytes 63 us; rows through a ring in
+// shared memory, as the gradient has them, 107 us). h is normalised before it is rounded to its storage type;
+// the gradient recomputes r2 from the stored h it is given.
 //
 // The sums over tokens are accumulated in registers by persistent groups (a lane keeps its columns
 // from row to row), written once per group as a partial row of the workspace and added up by a
@@ -27,7 +28,7 @@
 namespace vit {
 namespace {
 
-constexpr int kMaxWarps = 16;             // per row: rows of up to 8192 columns with two pieces per lane
+constexpr int kMaxWarps = 16;             // per row: up to 8192 columns, two pieces of 8 per lane
 
 using rope::unpack8;
 
@@ -346,55 +347,69 @@ norm_residual_bwd_kernel(const Bwd p, int rows_per_block)
 // dH = dh + r2 (a - h c2), a = dz w_pre, is linear in what the first reduction gives, so
 //   sum A dH = sum A dh + r2 (sum A a - c2 sum A h)
 // and six sums (h^2, a h, y^2, A dh, A a, A h) are taken at once.
+// An input that a call does not have reads as zeros (or, for a gate, ones) from a part of shared memory
+// filled once, and rows are padded with zeros to whole pieces of all lanes, so that the loops have no conditions.
 struct Ring {
     int stages, slot;                          // slots, bytes of one
-    int at_dz, at_dh, at_y, at_gate;           // byte offsets in a slot (h is at 0)
+    int at_h, at_dz, at_dh, at_y, at_gate;     // byte offsets in slot 0
+    int st_h, st_dz, st_dh, st_y, st_gate;     // and from slot to slot: `slot`, or 0 for what is filled once
+    int fill, gate_fill;                       // the zeros' place, and that of a gate for all tokens (-1: none)
     int32_t *status;
 };
 constexpr int kMaxStages = 4;
 constexpr long long kWaitBudget = 4000000000ll;   // clock cycles before a wait gives up (~2 s)
 
-__device__ __forceinline__ void unpack4(const uint2 &a, float *x) {
-    x[0] = __uint_as_float(a.x << 16);
-    x[1] = __uint_as_float(a.x & 0xffff0000u);
-    x[2] = __uint_as_float(a.y << 16);
-    x[3] = __uint_as_float(a.y & 0xffff0000u);
+// Four consecutive values as two pairs for the packed fp32 instructions.
+struct Quad {
+    uint64_t a, b;
+};
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Quad unpack4(const uint2 &a) {
+    return {rope::f2(__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xffff0000u)),
+            rope::f2(__uint_as_float(a.y << 16), __uint_as_float(a.y & 0xffff0000u))};
 }
 
-// piece v (4 values) of a row in shared memory, or 0
-template <bool F32> __device__ __forceinline__ void get4(bool there, const unsigned char *row, int v, float *x) {
+// a piece (4 values) of a row in shared memory
+template <bool F32> __device__ __forceinline__ Quad get4(const unsigned char *at) {
     if constexpr (F32) {
-        const float4 a = there ? *reinterpret_cast<const float4 *>(row + 16 * v) : make_float4(0.f, 0.f, 0.f, 0.f);
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(at);
+        return {a.x, a.y};
     } else {
-        unpack4(there ? *reinterpret_cast<const uint2 *>(row + 8 * v) : make_uint2(0u, 0u), x);
+        return unpack4(*reinterpret_cast<const uint2 *>(at));
     }
 }
 // 4 consecutive values in bf16 or fp32
-template <bool F32> __device__ __forceinline__ void put4(void *p, int64_t i, const float *x) {
+template <bool F32> __device__ __forceinline__ void put4(void *p, int64_t i, const Quad &x) {
+    float v[4];
+    rope::f2_split(x.a, v[0], v[1]);
+    rope::f2_split(x.b, v[2], v[3]);
     if constexpr (F32)
-        *reinterpret_cast<float4 *>(static_cast<float *>(p) + i) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4 *>(static_cast<float *>(p) + i) = make_float4(v[0], v[1], v[2], v[3]);
     else
         *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p) + i) =
-            make_uint2(rope::pack2(x[0], x[1]), rope::pack2(x[2], x[3]));
+            make_uint2(rope::pack2(v[0], v[1]), rope::pack2(v[2], v[3]));
 }
 
 constexpr int kSums = 6;
 
-// keeps the loads of a lane's pieces (4 columns each, so that few values are live beside the sums) apart
-__device__ __forceinline__ void one_piece() { asm volatile("" ::: "memory"); }
-
-// WR: the lane's columns of the weights and of a gate of all tokens stay in registers (from memory
-// they come through an L1 that the ring leaves almost nothing of: 9001 x 5120 took 340 us that way).
-// Rows above 5120 columns, six pieces per lane, have no room for them. Measured at 9001 x 5120 with an
-// fp32 residual and a gate per token: 176 us (5.76 TB/s); with two reductions per row 225 us; with the
-// row's values kept in registers as well 275 us; with two pieces per lane and 640 threads 180 us.
-template <int NP, bool F32, bool WR>
-__global__ void __launch_bounds__(NP == 2 ? 512 : NP == 4 ? 320 : 352)
+// A lane holds NP pieces of 4 columns; its columns of the two weights stay in registers (from memory they
+// come through an L1 that the ring leaves almost nothing of: 9001 x 5120 took 340 us that way). Measured at
+// 9001 x 5120 with an fp32 residual and a gate per token: 168 us (6.0 TB/s); with two reductions per row
+// 225 us. With conditions on what is there in the loops, 66 instead of about 30 instructions per column,
+// 9001 x 5120 in bf16 took 162 instead of 144 us.
+template <int NP, bool F32, int THREADS>
+__global__ void __launch_bounds__(THREADS)
 norm_residual_bwd_ring_kernel(const Bwd p, const Ring ring)
 {
+    using rope::f2_fma;
+    using rope::f2_mul;
+    constexpr int WARPS = THREADS / 32, RB = F32 ? 16 : 8;   // bytes of a piece of the residual stream
     extern __shared__ __align__(128) unsigned char s_ring[];
-    __shared__ __align__(16) float s_red[2][kMaxWarps][8];
+    __shared__ __align__(16) float s_red[2][WARPS][8];
     __shared__ uint64_t s_full[kMaxStages];
     const int never = 0;                       // no abort flag: every thread waits for itself
     grid_release();
@@ -408,17 +423,32 @@ norm_residual_bwd_ring_kernel(const Bwd p, const Ring ring)
         for (int i = 0; i < ring.stages; ++i) sm100::mbar_init(sm100::smem_addr(&s_full[i]), 1);
         sm100::fence_mbar_init();
     }
+    // zeros everywhere that no copy writes
+    for (int i = threadIdx.x; i < ring.stages * ring.slot / 16; i += blockDim.x)
+        reinterpret_cast<uint4 *>(s_ring)[i] = make_uint4(0u, 0u, 0u, 0u);
+    const int padded = NP * group;             // pieces of a row
+    for (int i = threadIdx.x; ring.fill >= 0 && i < padded; i += blockDim.x) {
+        *reinterpret_cast<uint2 *>(s_ring + ring.fill + RB * i) = make_uint2(0u, 0u);
+        if constexpr (F32) *reinterpret_cast<uint2 *>(s_ring + ring.fill + RB * i + 8) = make_uint2(0u, 0u);
+    }
+    constexpr uint32_t ONES = 0x3f803f80u;     // two bf16 1.0
+    const auto weight_at = [&](const __nv_bfloat16 *w, int v, uint32_t none) {
+        return !w || v >= nvec ? make_uint2(none, none) : *reinterpret_cast<const uint2 *>(w + 4 * v);
+    };
+    for (int i = threadIdx.x; ring.gate_fill >= 0 && i < padded; i += blockDim.x)
+        *reinterpret_cast<uint2 *>(s_ring + ring.gate_fill + 8 * i) = weight_at(p.gate, i, ONES);
+    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");   // the copies come after these stores
     __syncthreads();
     const int n_rows = blockIdx.x < p.T ? (int)((p.T - 1 - blockIdx.x) / gridDim.x + 1) : 0;   // of this block
     auto fetch = [&](int k) {                  // thread 0: the block's k-th row into its slot
         const int64_t t = blockIdx.x + (int64_t)k * gridDim.x;
         const int s = k % ring.stages;
         const uint32_t bar = sm100::smem_addr(&s_full[s]);
-        const uint32_t dst = sm100::smem_addr(s_ring) + s * ring.slot;
+        const uint32_t dst = sm100::smem_addr(s_ring) + s * ring.slot;   // (of what is copied, all go from slot to slot)
         sm100::mbar_arrive_expect_tx(bar, slot_b);
         const char *h = static_cast<const char *>(p.h), *dh = static_cast<const char *>(p.dh);
         if (p.w_pre) {
-            sm100::bulk_load(dst, h + t * p.h_stride * (F32 ? 4 : 2), res_b, bar);
+            sm100::bulk_load(dst + ring.at_h, h + t * p.h_stride * (F32 ? 4 : 2), res_b, bar);
             sm100::bulk_load(dst + ring.at_dz, p.dz + t * p.dz_stride, row_b, bar);
         }
         if (p.dh) sm100::bulk_load(dst + ring.at_dh, dh + t * p.dh_stride * (F32 ? 4 : 2), res_b, bar);
@@ -429,102 +459,79 @@ norm_residual_bwd_ring_kernel(const Bwd p, const Ring ring)
     if (threadIdx.x == 0)
         for (; fetched < n_rows && fetched < ring.stages; ++fetched) fetch(fetched);
 
-    float a_pre[NP][4], a_post[NP][4], a_gate[NP][4];
+    Quad a_pre[NP], a_post[NP], a_gate[NP];
 #pragma unroll
-    for (int i = 0; i < NP; ++i)
+    for (int i = 0; i < NP; ++i) a_pre[i] = a_post[i] = a_gate[i] = Quad{0ull, 0ull};
+    Quad w_pre[NP], w_post[NP];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) a_pre[i][e] = a_post[i][e] = a_gate[i][e] = 0.f;
-    constexpr int NH = WR ? NP : 1;
-    uint2 r_pre[NH], r_post[NH], r_gate[NH];
-    if constexpr (WR) {
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const int v = i * group + threadIdx.x;
-            const auto take = [&](const __nv_bfloat16 *w) {
-                return w && v < nvec ? *reinterpret_cast<const uint2 *>(w + 4 * v) : make_uint2(0u, 0u);
-            };
-            r_pre[i] = take(p.w_pre);
-            r_post[i] = take(p.w_post);
-            r_gate[i] = take(gate_tok ? nullptr : p.gate);
-        }
+    for (int i = 0; i < NP; ++i) {
+        const int v = i * group + threadIdx.x;
+        w_pre[i] = unpack4(weight_at(p.w_pre, v, 0u));
+        w_post[i] = unpack4(weight_at(p.w_post, v, ONES));
     }
-    // one piece of a row: 0 where an input is not there, 1 for a missing gate or post-norm weight
     struct Piece {
-        float h[4], dh[4], dz[4], y[4], g[4], wr[4], wo[4];
+        Quad h, dh, dz, y, g;
     };
-    auto values = [&](const unsigned char *slot, int i, Piece &x) {
-        const int v = i * group + threadIdx.x, k = WR ? i : 0;
-        const bool in = v < nvec;
-        auto word = [&](bool there, int at) {
-            return there && in ? *reinterpret_cast<const uint2 *>(slot + at + 8 * v) : make_uint2(0u, 0u);
-        };
-        get4<F32>(p.w_pre && in, slot, v, x.h);
-        get4<F32>(p.dh && in, slot + ring.at_dh, v, x.dh);
-        unpack4(word(p.w_pre, ring.at_dz), x.dz);
-        unpack4(word(p.y, ring.at_y), x.y);
-        auto weight = [&](const __nv_bfloat16 *w, const uint2 &reg, float *o) {
-            if constexpr (WR)
-                unpack4(reg, o);
-            else
-                unpack4(w && in ? *reinterpret_cast<const uint2 *>(w + 4 * v) : make_uint2(0u, 0u), o);
-        };
-        weight(p.w_pre, r_pre[k], x.wr);
-        if (gate_tok)
-            unpack4(word(true, ring.at_gate), x.g);
-        else if (p.gate)
-            weight(p.gate, r_gate[k], x.g);
-        if (p.w_post) weight(p.w_post, r_post[k], x.wo);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (!p.gate) x.g[e] = 1.f;
-            if (!p.w_post) x.wo[e] = 1.f;
-        }
+    const unsigned char *m_h = s_ring + ring.at_h + RB * threadIdx.x, *m_dh = s_ring + ring.at_dh + RB * threadIdx.x;
+    const unsigned char *m_dz = s_ring + ring.at_dz + 8 * threadIdx.x, *m_y = s_ring + ring.at_y + 8 * threadIdx.x;
+    const unsigned char *m_g = s_ring + ring.at_gate + 8 * threadIdx.x;
+    auto values = [&](int s, int i, Piece &x) {
+        x.h = get4<F32>(m_h + s * ring.st_h + i * RB * group);
+        x.dh = get4<F32>(m_dh + s * ring.st_dh + i * RB * group);
+        x.dz = get4<false>(m_dz + s * ring.st_dz + i * 8 * group);
+        x.y = get4<false>(m_y + s * ring.st_y + i * 8 * group);
+        x.g = get4<false>(m_g + s * ring.st_gate + i * 8 * group);
     };
 
     bool ok = true;
-    int s_at = 0, buf = 0;
+    int buf = 0, s_at = 0;
     uint32_t phase = 0;
     for (int k = 0; k < n_rows; ++k) {
-        const int64_t t = blockIdx.x + (int64_t)k * gridDim.x;
-        const unsigned char *slot = s_ring + s_at * ring.slot;
-        ok = __all_sync(0xffffffffu, sm100::mbar_wait(sm100::smem_addr(&s_full[s_at]), phase, &never, kWaitBudget));
+        const int s = s_at;
+        ok = __all_sync(0xffffffffu, sm100::mbar_wait(sm100::smem_addr(&s_full[s]), phase, &never, kWaitBudget));
         if (++s_at == ring.stages) {
             s_at = 0;
             phase ^= 1u;
         }
-        float sum[kSums] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (ok) {
+            uint64_t sum[kSums] = {0ull, 0ull, 0ull, 0ull, 0ull, 0ull};
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
-                if constexpr (!WR) one_piece();
                 Piece x;
-                values(slot, i, x);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float a = x.dz[e] * x.wr[e], A = x.g[e] * x.wo[e] * x.y[e];
-                    sum[0] = fmaf(x.h[e], x.h[e], sum[0]);
-                    sum[1] = fmaf(a, x.h[e], sum[1]);
-                    sum[2] = fmaf(x.y[e], x.y[e], sum[2]);
-                    sum[3] = fmaf(A, x.dh[e], sum[3]);
-                    sum[4] = fmaf(A, a, sum[4]);
-                    sum[5] = fmaf(A, x.h[e], sum[5]);
-                }
+                values(s, i, x);
+                auto add = [&](uint64_t h, uint64_t dh, uint64_t dz, uint64_t y, uint64_t g, uint64_t wr, uint64_t wo) {
+                    const uint64_t a = f2_mul(dz, wr), A = f2_mul(f2_mul(g, wo), y);
+                    sum[0] = f2_fma(h, h, sum[0]);
+                    sum[1] = f2_fma(a, h, sum[1]);
+                    sum[2] = f2_fma(y, y, sum[2]);
+                    sum[3] = f2_fma(A, dh, sum[3]);
+                    sum[4] = f2_fma(A, a, sum[4]);
+                    sum[5] = f2_fma(A, h, sum[5]);
+                };
+                add(x.h.a, x.dh.a, x.dz.a, x.y.a, x.g.a, w_pre[i].a, w_post[i].a);
+                add(x.h.b, x.dh.b, x.dz.b, x.y.b, x.g.b, w_pre[i].b, w_post[i].b);
             }
+            float t[kSums];
 #pragma unroll
-            for (int j = 0; j < kSums; ++j) sum[j] = warp_sum(sum[j]);
+            for (int j = 0; j < kSums; ++j) {
+                float lo, hi;
+                rope::f2_split(sum[j], lo, hi);
+                t[j] = warp_sum(lo + hi);
+            }
+            if ((threadIdx.x & 31) == 0) {
+                float *red = s_red[buf][threadIdx.x >> 5];
+                *reinterpret_cast<float4 *>(red) = make_float4(t[0], t[1], t[2], t[3]);
+                *reinterpret_cast<float2 *>(red + 4) = make_float2(t[4], t[5]);
+            }
         }
-        float(*red)[8] = s_red[buf];
+        const auto *red = s_red[buf];
         buf ^= 1;
-        if ((threadIdx.x & 31) == 0) {
-            *reinterpret_cast<float4 *>(red[threadIdx.x >> 5]) = make_float4(sum[0], sum[1], sum[2], sum[3]);
-            *reinterpret_cast<float2 *>(red[threadIdx.x >> 5] + 4) = make_float2(sum[4], sum[5]);
-        }
         ok = __syncthreads_and(ok);            // also agrees that the row has landed
         if (!ok) break;
         // every thread has left the row before
         if (threadIdx.x == 0 && k > 0 && fetched < n_rows) fetch(fetched++);
-#pragma unroll
-        for (int j = 0; j < kSums; ++j) sum[j] = 0.f;
+        const int64_t t = blockIdx.x + (int64_t)k * gridDim.x;
+        float sum[kSums] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         for (int w = 0; w < wpr; ++w) {
             const float4 x = *reinterpret_cast<const float4 *>(red[w]);
             const float2 z = *reinterpret_cast<const float2 *>(red[w] + 4);
@@ -544,24 +551,30 @@ norm_residual_bwd_ring_kernel(const Bwd p, const Ring ring)
             r1 = rsqrtf(sum[2] * inv_c + p.eps);
             c1 = r1 * r1 * (p.scale * fmaf(r2, fmaf(-c2, sum[5], sum[4]), sum[3]) * inv_c);   // dy = r1 (du w - y c1)
         }
+        const uint64_t r2_2 = rope::f2(r2, r2), nc2 = rope::f2(-c2, -c2), r1_2 = rope::f2(r1, r1);
+        const uint64_t nc1 = rope::f2(-c1, -c1), scale = rope::f2(p.scale, p.scale);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int v = i * group + threadIdx.x;
-            if constexpr (!WR) one_piece();
-            if (v >= nvec) continue;
             Piece x;
-            values(slot, i, x);
-            float dx[4], dy[4], dg[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                dx[e] = fmaf(r2, fmaf(x.dz[e], x.wr[e], -x.h[e] * c2), x.dh[e]);
-                a_pre[i][e] = fmaf(x.dz[e], x.h[e] * r2, a_pre[i][e]);
-                const float d = p.scale * dx[e], du = d * x.g[e], yh = x.y[e] * r1;
-                dg[e] = d * yh * x.wo[e];
-                a_gate[i][e] += dg[e];
-                a_post[i][e] = fmaf(du, yh, a_post[i][e]);
-                dy[e] = p.w_post ? r1 * fmaf(du, x.wo[e], -x.y[e] * c1) : du;
-            }
+            values(s, i, x);
+            Quad dx, dy, dg;
+            auto back = [&](uint64_t h, uint64_t dh, uint64_t dz, uint64_t y, uint64_t g, uint64_t wr, uint64_t wo,
+                            uint64_t &s_pre, uint64_t &s_post, uint64_t &s_gate, uint64_t &ox, uint64_t &oy,
+                            uint64_t &og) {
+                ox = f2_fma(r2_2, f2_fma(dz, wr, f2_mul(h, nc2)), dh);
+                s_pre = f2_fma(dz, f2_mul(h, r2_2), s_pre);
+                const uint64_t d = f2_mul(scale, ox), du = f2_mul(d, g), yh = f2_mul(y, r1_2);
+                og = f2_mul(f2_mul(d, yh), wo);
+                s_gate = f2_add(s_gate, og);
+                s_post = f2_fma(du, yh, s_post);
+                oy = p.w_post ? f2_mul(r1_2, f2_fma(du, wo, f2_mul(y, nc1))) : du;   // (0 y is not 0 for every y)
+            };
+            back(x.h.a, x.dh.a, x.dz.a, x.y.a, x.g.a, w_pre[i].a, w_post[i].a, a_pre[i].a, a_post[i].a, a_gate[i].a,
+                 dx.a, dy.a, dg.a);
+            back(x.h.b, x.dh.b, x.dz.b, x.y.b, x.g.b, w_pre[i].b, w_post[i].b, a_pre[i].b, a_post[i].b, a_gate[i].b,
+                 dx.b, dy.b, dg.b);
+            if (v >= nvec) continue;
             put4<F32>(p.dx, t * p.dx_stride + 4 * v, dx);
             put4<false>(p.dy, t * p.dy_stride + 4 * v, dy);
             if (gate_tok && p.dgate) put4<false>(p.dgate, t * p.dgate_stride + 4 * v, dg);
@@ -615,32 +628,22 @@ column_sum_kernel(const float *__restrict__ part, int n_parts, int n_sum, int C,
     }
 }
 
-// Columns per lane and warps per row: the fewest pieces per lane with which a row fits `max_warps`
-// warps; a row of one warp is preferred up to `solo` pieces per lane (no barriers).
-void row_shape(int C, int solo, int max_vpt, int max_warps, int *vpt, int *wpr)
+// Pieces of 8 columns per lane and warps per row. A row of one warp has no barriers; wider rows have as few
+// warps as the registers allow. In bf16 that is one warp up to 6 pieces, then 4 pieces each (15000 x 4096: 82 us,
+// 2 pieces 90, 1 piece 110; 6000 x 8192: 70, 82, 82). Pieces of an fp32 residual are twice as large: one warp
+// up to 3 pieces, then 2 pieces each (60000 x 1024: 135 us, 4 pieces 164; 15000 x 4096: 141, 4 pieces 170, 1 piece
+// 147).
+void row_shape(int C, bool f32, int *vpt, int *wpr)
 {
-    const int nvec = C / 8;
-    if (nvec <= 32 * solo) {
-        *wpr = 1;
-        *vpt = (nvec + 31) / 32;
-        return;
-    }
-    for (int v = 1; v <= max_vpt; ++v) {
-        const int w = (nvec + 32 * v - 1) / (32 * v);
-        if (w <= max_warps) {
-            *vpt = v;
-            *wpr = w;
-            return;
-        }
-    }
-    *vpt = max_vpt;
-    *wpr = (nvec + 32 * max_vpt - 1) / (32 * max_vpt);
+    const int nvec = C / 8, solo = f32 ? 3 : 6, each = f32 ? 2 : 4;
+    *vpt = nvec <= 32 * solo ? (nvec + 31) / 32 : each;
+    *wpr = (nvec + 32 * *vpt - 1) / (32 * *vpt);
 }
 
 template <bool F32> cudaError_t launch_fwd(const Fwd &p, int num_sms, cudaStream_t stream)
 {
     int vpt, wpr;
-    row_shape(p.C, 6, 4, 16, &vpt, &wpr);
+    row_shape(p.C, F32, &vpt, &wpr);
     const int rows = wpr == 1 ? 4 : 1;
     const int64_t want = (p.T + rows - 1) / rows, cap = (int64_t)num_sms * 64;
     const unsigned blocks = (unsigned)(want < cap ? want : cap);
@@ -650,52 +653,72 @@ template <bool F32> cudaError_t launch_fwd(const Fwd &p, int num_sms, cudaStream
         case 1: norm_residual_kernel<1, F32><<<blocks, threads, 0, stream>>>(p, wpr, rows); break;
         case 2: norm_residual_kernel<2, F32><<<blocks, threads, 0, stream>>>(p, wpr, rows); break;
         case 3: norm_residual_kernel<3, F32><<<blocks, threads, 0, stream>>>(p, wpr, rows); break;
-        case 4: norm_residual_kernel<4, F32><<<blocks, threads, 0, stream>>>(p, wpr, rows); break;
-        case 5: norm_residual_kernel<5, F32><<<blocks, threads, 0, stream>>>(p, wpr, rows); break;
-        case 6: norm_residual_kernel<6, F32><<<blocks, threads, 0, stream>>>(p, wpr, rows); break;
-        default: return cudaErrorInvalidValue;
+        default:
+            if constexpr (!F32) {
+                if (vpt == 4) norm_residual_kernel<4, F32><<<blocks, threads, 0, stream>>>(p, wpr, rows);
+                else if (vpt == 5) norm_residual_kernel<5, F32><<<blocks, threads, 0, stream>>>(p, wpr, rows);
+                else norm_residual_kernel<6, F32><<<blocks, threads, 0, stream>>>(p, wpr, rows);
+            }
     }
     return cudaGetLastError();
 }
 
 constexpr int kRingBytes = 224 * 1024;     // shared memory of an SM that the rings share
+constexpr int kNarrow = 6144;              // widest row that 384 threads hold at four pieces each
 
-template <int NP, bool F32, bool WR>
+// Pieces per lane and threads of a row's block. Fewer threads with more pieces each cost fewer shuffles and
+// barriers per column (15000 x 4096 bf16: 225 us with two pieces and 512 threads, 185 with four and 256;
+// 6000 x 8192: 220 us with six and 352, 132 with eight and 256). Eight below 6144 columns as well help where
+// they fill the lanes (4096: 152 us) and not elsewhere (1280: 169 instead of 144 us, 520 with an fp32 residual
+// 285 instead of 207). Threads of an SM: 384 (480, which the registers allow, leave each block too few slots:
+// 37007 x 1280 with an fp32 residual 232 instead of 173 us; 320: 176).
+int ring_pieces(int C) { return C <= kNarrow ? 4 : 8; }
+int ring_threads(int C) { return (C / 4 + 32 * ring_pieces(C) - 1) / (32 * ring_pieces(C)) * 32; }
+int ring_blocks(int C) { return C <= kNarrow ? 384 / ring_threads(C) : 1; }
+
+template <int NP, bool F32, int THREADS>
 cudaError_t launch_ring(const Bwd &p, int32_t *status, int num_sms, unsigned *blocks, cudaStream_t stream)
 {
-    const int res_b = (F32 ? 4 : 2) * p.C, row_b = 2 * p.C;
+    const int threads = ring_threads(p.C), cols = 4 * NP * threads;      // of a padded row
+    const bool gate_tok = p.gate && p.gate_stride != 0;
+    const int res_b = (F32 ? 4 : 2) * cols, row_b = 2 * cols;
     Ring r;
-    int at = p.w_pre ? res_b : 0;
-    auto place = [&](bool there, int bytes) {
-        const int here = at;
-        if (there) at += bytes;
-        return here;
-    };
-    r.at_dz = place(p.w_pre != nullptr, row_b);
-    r.at_dh = place(p.dh != nullptr, res_b);
-    r.at_y = place(p.y != nullptr, row_b);
-    r.at_gate = place(p.gate && p.gate_stride != 0, row_b);
-    r.slot = (at + 127) / 128 * 128;
     r.status = status;
-    const int threads = (p.C / 4 + 32 * NP - 1) / (32 * NP) * 32;
+    r.slot = (p.w_pre ? res_b + row_b : 0) + (p.dh ? res_b : 0) + (p.y ? row_b : 0) + (gate_tok ? row_b : 0);
+    const bool absent = !p.w_pre || !p.dh || !p.y;
+    const int fixed = (absent ? res_b : 0) + (gate_tok ? 0 : row_b);
     // as many blocks per SM as its registers hold, each with two slots at least
-    int ctas = 512 / threads;
-    while (ctas > 1 && kRingBytes / ctas < 2 * r.slot) --ctas;
-    r.stages = kRingBytes / ctas / r.slot;
+    int ctas = ring_blocks(p.C);
+    while (ctas > 1 && kRingBytes / ctas < 2 * r.slot + fixed) --ctas;
+    r.stages = (kRingBytes / ctas - fixed) / r.slot;
     if (r.stages > kMaxStages) r.stages = kMaxStages;
     if (r.stages < 2) return cudaErrorInvalidValue;
+    r.fill = absent ? r.stages * r.slot : -1;
+    r.gate_fill = gate_tok ? -1 : r.stages * r.slot + (absent ? res_b : 0);
+    int at = 0;
+    auto place = [&](bool there, int bytes, int &where, int &step) {
+        where = there ? at : r.fill;
+        step = there ? r.slot : 0;
+        if (there) at += bytes;
+    };
+    place(p.w_pre != nullptr, res_b, r.at_h, r.st_h);
+    place(p.w_pre != nullptr, row_b, r.at_dz, r.st_dz);
+    place(p.dh != nullptr, res_b, r.at_dh, r.st_dh);
+    place(p.y != nullptr, row_b, r.at_y, r.st_y);
+    place(gate_tok, row_b, r.at_gate, r.st_gate);
+    if (!gate_tok) r.at_gate = r.gate_fill;
     int64_t most = (int64_t)num_sms * ctas;
-    if (most > kNormResidualParts) most = kNormResidualParts;
+    if (most > norm_residual_parts(p.C)) most = norm_residual_parts(p.C);
     *blocks = (unsigned)(p.T < most ? p.T : most);
     if (*blocks == 0) return cudaSuccess;
-    auto kern = norm_residual_bwd_ring_kernel<NP, F32, WR>;
+    auto kern = norm_residual_bwd_ring_kernel<NP, F32, THREADS>;
     static DeviceOnce once;
     cudaError_t e = once.run([&] {
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
     });
     if (e != cudaSuccess) return e;
     LaunchScope scope("norm_residual_bwd", stream);
-    kern<<<*blocks, threads, (size_t)r.stages * r.slot, stream>>>(p, r);
+    kern<<<*blocks, threads, (size_t)r.stages * r.slot + fixed, stream>>>(p, r);
     return cudaGetLastError();
 }
 
@@ -707,7 +730,7 @@ cudaError_t launch_bwd(const Bwd &p, const SumOut &o, int32_t *status, int num_s
     if (p.C <= 512) {
         const int rows = 8;
         const int64_t want = (p.T + rows - 1) / rows;
-        const int64_t most = (int64_t)num_sms * 4, cap = most < kNormResidualParts ? most : kNormResidualParts;
+        const int64_t most = (int64_t)num_sms * 4, parts = norm_residual_parts(p.C), cap = most < parts ? most : parts;
         blocks = (unsigned)(want < cap ? want : cap);
         if (blocks > 0) {
             LaunchScope scope("norm_residual_bwd", stream);
@@ -715,18 +738,19 @@ cudaError_t launch_bwd(const Bwd &p, const SumOut &o, int32_t *status, int num_s
             else norm_residual_bwd_kernel<2, F32><<<blocks, 32 * rows, 0, stream>>>(p, rows);
             e = cudaGetLastError();
         }
-    } else if (p.C <= 4096) {
-        e = launch_ring<2, F32, true>(p, status, num_sms, &blocks, stream);
-    } else if (p.C <= 5120) {
-        e = launch_ring<4, F32, true>(p, status, num_sms, &blocks, stream);
+    } else if (p.C <= kNarrow) {
+        e = launch_ring<4, F32, 384>(p, status, num_sms, &blocks, stream);
     } else {
-        e = launch_ring<6, F32, false>(p, status, num_sms, &blocks, stream);
+        e = launch_ring<8, F32, 256>(p, status, num_sms, &blocks, stream);
     }
     if (e != cudaSuccess || p.n_sum == 0) return e;
     return launch_column_sum(p.part, (int)blocks, p.n_sum, p.C, o.out[0], o.out[1], o.out[2], stream);
 }
 
 }  // namespace
+
+// Blocks of the gradient kernel at most, each of which leaves a row of sums.
+int norm_residual_parts(int C) { return kDesignSms * (C <= 512 ? 4 : ring_blocks(C)); }
 
 cudaError_t launch_column_sum(const float *part, int n_parts, int n_sum, int C, float *out0, float *out1, float *out2,
                               cudaStream_t stream)
