@@ -486,7 +486,7 @@ _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 def _rows3(t: torch.Tensor, name: str, T: int, H: int, D: int) -> int:
     """Token stride of bf16 [T, H, D] with head stride D."""
-    if tuple(t.shape) != (T, H, D):
+    if t.shape != (T, H, D):
         raise ValueError(f"{name} must be [{T}, {H}, {D}], got {tuple(t.shape)}")
     if t.dtype is not _BF16:
         raise ValueError(f"{name} must be a CUDA bfloat16 tensor")
@@ -525,11 +525,11 @@ def _three(sections: tuple):
 
 
 def _mrope_args(T, D, pos_thw, inv_freq, sections, norm_w, eps, cycled, interleaved):
-    if pos_thw.dtype is not _I32 or tuple(pos_thw.shape) != (T, 3) or not pos_thw.is_contiguous():
+    if pos_thw.dtype is not _I32 or pos_thw.shape != (T, 3) or not pos_thw.is_contiguous():
         raise ValueError(f"pos_thw must be a contiguous CUDA int32 tensor [{T}, 3]")
-    if inv_freq.dtype is not _F32 or tuple(inv_freq.shape) != (D // 2,) or not inv_freq.is_contiguous():
+    if inv_freq.dtype is not _F32 or inv_freq.shape != (D // 2,) or not inv_freq.is_contiguous():
         raise ValueError(f"inv_freq must be a contiguous CUDA float32 tensor [{D // 2}]")
-    if norm_w is not None and (norm_w.dtype is not _BF16 or tuple(norm_w.shape) != (2, D)
+    if norm_w is not None and (norm_w.dtype is not _BF16 or norm_w.shape != (2, D)
                                or not norm_w.is_contiguous()):
         raise ValueError(f"norm_w must be a contiguous CUDA bfloat16 tensor [2, {D}]")
     if len(sections) != 3:
@@ -731,7 +731,7 @@ RES_BF16, RES_FP32 = 0, 1
 
 def _rows2(t: torch.Tensor, name: str, T: int, C: int, dtype) -> int:
     """Row stride of [T, C] with unit element stride."""
-    if tuple(t.shape) != (T, C):
+    if t.shape != (T, C):
         raise ValueError(f"{name} must be [{T}, {C}], got {tuple(t.shape)}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
@@ -742,7 +742,7 @@ def _rows2(t: torch.Tensor, name: str, T: int, C: int, dtype) -> int:
 
 
 def _channel(t: torch.Tensor | None, name: str, C: int):
-    if t is not None and (t.dtype is not _BF16 or tuple(t.shape) != (C,) or not t.is_contiguous()):
+    if t is not None and (t.dtype is not _BF16 or t.shape != (C,) or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous CUDA bfloat16 tensor [{C}]")
 
 
