@@ -1,4 +1,4 @@
-// Scan and sort of one 1024-thread block, shared by the work schedulers.
+// Scan and sort of one 1024-thread block, and of one warp, shared by the work schedulers.
 #pragma once
 
 #include <stdint.h>
@@ -53,6 +53,35 @@ __device__ __forceinline__ void block_sort(unsigned long long *s_key, int NPL, i
             __syncthreads();
         }
     }
+}
+
+// For up to 32 keys, one per lane (all different): the lane's place in ascending order, and the sums of n0 and n1
+// over the lanes placed before it.
+__device__ __forceinline__ void warp_place(unsigned long long key, int n0, int n1, int &rank, int &at0, int &at1)
+{
+    rank = at0 = at1 = 0;
+#pragma unroll 4
+    for (int j = 0; j < 32; ++j) {
+        const unsigned long long other = __shfl_sync(0xffffffffu, key, j);
+        const int m0 = __shfl_sync(0xffffffffu, n0, j), m1 = __shfl_sync(0xffffffffu, n1, j);
+        if (other < key) {
+            ++rank;
+            at0 += m0;
+            at1 += m1;
+        }
+    }
+}
+
+// The last p < n with first(p) <= i, for items whose list is sorted by first = s_key >> 32.
+__device__ __forceinline__ int place_of(const unsigned long long *s_key, int n, int i)
+{
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int m = (lo + hi) >> 1;
+        if ((int)(s_key[m] >> 32) <= i) lo = m;
+        else hi = m;
+    }
+    return lo;
 }
 
 }  // namespace vit

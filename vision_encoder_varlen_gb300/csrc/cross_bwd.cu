@@ -20,6 +20,14 @@
 // both kinds of items was 10 % slower at large sizes (616 against 564 us at 4 x 2048 x 4096, 16 heads
 // of 80: the issuer's loop compiles worse).
 //
+// Measured at 4 sequences of 1500 to 2311 queries over 3000 to 5117 keys, 16 heads of 80: dk, dv 316 us and dq
+// 239 us (1.08 PFLOP/s of the products they make; the forward and backward pass together 0.79 PFLOP/s of the five
+// products of the gradient and two of the forward pass), the tensor pipe 43 % busy: bound by the exchange
+// between the softmax groups and the issuer, whose products of one tile and sums of the one before take turns
+// in one pipe. delta comes from the stored bf16 out, as the interface has no other: where few keys carry a row,
+// dP - delta cancels, and dq and dk are off by 1.6 times what their own rounding is (0.27 against 0.17 % in the
+// 2-norm), in longer rows by 1.4 times, for the rounding of P and dS.
+//
 // Before them, one launch makes the two item lists (a block each) and the statistics -lse log2(e) and
 // -delta of every (token, head) (the other blocks).
 //
@@ -573,71 +581,87 @@ __device__ void make_list(bool keys, const CrossSegs &segs, int Hq, int Hk, int 
                           GradItem *items, int32_t *status)
 {
     constexpr int kThreads = kSortThreads;
-    extern __shared__ unsigned long long s_key[];
+    extern __shared__ unsigned long long s_key[];      // [NP] loop length descending, then index; later first item | index
     __shared__ int64_t s_warp[32];
-    __shared__ int s_bad;
+    __shared__ int s_bad, s_used, s_total;
     const int tid = threadIdx.x, B = segs.B;
-    int NP = 1;
-    while (NP < B) NP <<= 1;
-    if (tid == 0) s_bad = 0;
-    __syncthreads();
-    for (int i = tid; i < NP; i += kThreads) {
-        CrossSeg x;
-        const bool fine = i < B && load_seg(segs, i, x, status, !keys);
-        if (i < B && (segs.cu_q[i + 1] < segs.cu_q[i] || segs.cu_k[i + 1] < segs.cu_k[i])) s_bad = 1;
-        const bool use = fine && (keys ? x.kn : x.qn) > 0;
-        s_key[i] = use ? ((unsigned long long)(0x7fffffffu - (uint32_t)(keys ? x.qn : x.kn)) << 32) | (uint32_t)i : ~0ull;
-    }
-    __syncthreads();
-    if (s_bad) {
-        if (tid == 0) counts[keys] = 0;
-        return;
-    }
-    block_sort(s_key, NP, tid);
     const int lg_tile = keys ? 7 : 7 - lg_pack;        // rows (tokens) of a tile, log2
     const int heads = keys ? Hk : Hq >> lg_pack;       // tiles side by side
-    const int per = (B + kThreads - 1) / kThreads, lo = min(tid * per, B), hi = min(lo + per, B);
-    auto seg_at = [&](int p, CrossSeg &x) -> bool {
-        if (s_key[p] == ~0ull) return false;
-        load_seg(segs, (int)(s_key[p] & 0xffffffffu), x, nullptr, false);
-        return true;
+    auto rows_of = [&](const CrossSeg &x) { return keys ? x.kn : x.qn; };
+    auto key_of = [&](bool use, const CrossSeg &x, int i) {
+        return ((unsigned long long)(use ? 0x7fffffffu - (uint32_t)(keys ? x.qn : x.kn) : 0xffffffffu) << 32) | (uint32_t)i;
     };
-    auto tiles_of = [&](const CrossSeg &x) { return ((keys ? x.kn : x.qn) + (1 << lg_tile) - 1) >> lg_tile; };
-    int64_t n = 0, total;
-    for (int p = lo; p < hi; ++p) {
-        CrossSeg x;
-        if (seg_at(p, x)) n += (int64_t)heads * tiles_of(x);
+    auto items_of = [&](const CrossSeg &x) { return heads * ((rows_of(x) + (1 << lg_tile) - 1) >> lg_tile); };
+    auto decreases = [&](int i) { return segs.cu_q[i + 1] < segs.cu_q[i] || segs.cu_k[i + 1] < segs.cu_k[i]; };
+    if (B <= 32) {
+        // a warp: one sequence per lane
+        if (tid < 32) {
+            CrossSeg x;
+            const bool fine = tid < B && load_seg(segs, tid, x, status, !keys);
+            const bool bad = tid < B && decreases(tid), use = fine && rows_of(x) > 0;
+            const int n = use ? items_of(x) : 0;
+            int rank, at, none;
+            warp_place(key_of(use, x, tid), n, 0, rank, at, none);
+            s_key[rank] = ((unsigned long long)at << 32) | (uint32_t)tid;
+            const unsigned used = __ballot_sync(0xffffffffu, use), any_bad = __ballot_sync(0xffffffffu, bad);
+            if (rank == 31) {
+                s_total = at + n;
+                s_used = __popc(used);
+                s_bad = any_bad != 0;
+            }
+        }
+        __syncthreads();
+    } else {
+        int NP = 32;
+        while (NP < B) NP <<= 1;
+        if (tid == 0) s_bad = s_used = 0;
+        __syncthreads();
+        for (int i = tid; i < NP; i += kThreads) {
+            CrossSeg x;
+            const bool fine = i < B && load_seg(segs, i, x, status, !keys);
+            if (i < B && decreases(i)) s_bad = 1;
+            const bool use = fine && rows_of(x) > 0;
+            s_key[i] = key_of(use, x, i);
+            if (use) atomicAdd(&s_used, 1);
+        }
+        __syncthreads();
+        block_sort(s_key, NP, tid);
+        const int per = (B + kThreads - 1) / kThreads, lo = min(tid * per, s_used), hi = min(lo + per, s_used);
+        auto seg_at = [&](int p) {
+            CrossSeg x;
+            load_seg(segs, (int)(s_key[p] & 0xffffffffu), x, nullptr, false);
+            return x;
+        };
+        int64_t n = 0, total;
+        for (int p = lo; p < hi; ++p) n += items_of(seg_at(p));
+        int64_t at = block_exclusive_scan(n, s_warp, &total);
+        for (int p = lo; p < hi; ++p) {
+            const int k = items_of(seg_at(p));
+            s_key[p] = ((unsigned long long)at << 32) | (uint32_t)(s_key[p] & 0xffffffffu);
+            at += k;
+        }
+        if (tid == 0) s_total = (int)total;
+        __syncthreads();
     }
-    int64_t at = block_exclusive_scan(n, s_warp, &total);
-    for (int p = lo; p < hi; ++p) {
-        CrossSeg x;
-        if (!seg_at(p, x)) continue;
-        s_key[p] = ((unsigned long long)at << 32) | (uint32_t)(s_key[p] & 0xffffffffu);
-        at += (int64_t)heads * tiles_of(x);
-    }
-    __syncthreads();
-    const int lane = tid & 31, warp = tid >> 5;
-    for (int p = warp; p < B; p += kThreads / 32) {
-        if (s_key[p] == ~0ull) break;
+    const int total = s_bad ? 0 : s_total;
+    if (tid == 0) counts[keys] = total;
+    for (int i = tid; i < total; i += kThreads) {
+        const int p = place_of(s_key, s_used, i), n = i - (int)(s_key[p] >> 32);
         CrossSeg x;
         load_seg(segs, (int)(s_key[p] & 0xffffffffu), x, nullptr, false);
-        const int first = (int)(s_key[p] >> 32), nr = tiles_of(x);
+        const int nr = (rows_of(x) + (1 << lg_tile) - 1) >> lg_tile, h = n / nr, r = n - h * nr;
+        const int step = keys ? bn >> lg_pack : bn;
         GradItem it;
+        it.r0 = (keys ? x.k0 : x.q0) + (r << lg_tile);
+        it.r1 = keys ? x.k0 + x.kn : x.q0 + x.qn;
         it.l0 = keys ? x.q0 : x.k0;
         it.ln = keys ? x.qn : x.kn;
-        it.r1 = keys ? x.k0 + x.kn : x.q0 + x.qn;
+        it.head = keys ? h : h << lg_pack;
         it.j0 = 0;
-        const int step = keys ? bn >> lg_pack : bn;
         it.j1 = (it.ln + step - 1) / step * (keys ? Hq / Hk >> lg_pack : 1);
         it.pad = 0;
-        for (int i = lane; i < heads * nr; i += 32) {
-            const int h = i / nr, r = i - h * nr;
-            it.r0 = (keys ? x.k0 : x.q0) + (r << lg_tile);
-            it.head = keys ? h : h << lg_pack;
-            items[first + i] = it;
-        }
+        items[i] = it;
     }
-    if (tid == 0) counts[keys] = (int32_t)total;
 }
 
 struct Prepare {
@@ -770,7 +794,7 @@ template <int D> cudaError_t launch_d(const CrossGradArgs &a, const GradPlan &pl
     r.dq = reinterpret_cast<GradItem *>(ws + pl.off_dq);
     r.dkv = reinterpret_cast<GradItem *>(ws + pl.off_dkv);
     r.status = a.f.status;
-    int np = 1;
+    int np = 32;
     while (np < s.B) np <<= 1;
     static DeviceOnce once_prepare;
     cudaError_t e = once_prepare.run([] {

@@ -2,14 +2,17 @@
 //
 // One block reads the two offset lists on the device (nothing returns to the host, so a call can be
 // captured in a graph): each sequence is checked by itself and left out when it is malformed (all of
-// them when the query offsets decrease somewhere); the others are ordered by key count, longest first (an item's time goes by its keys, and the
-// persistent kernel takes items in list order), and cut into items:
+// them when the query offsets decrease somewhere); the others are ordered by key count, longest first (an
+// item's time goes by its keys, and the persistent kernel takes items in list order), and cut into items:
 //   - 256 query rows (two tiles) per item, a last block of at most 128 rows, or every block of a
 //     batch too small to occupy half the GPU otherwise, as a split item of one tile;
 //   - where the sizes bound the batch to at most half as many 128-row tiles as SMs, split items of
 //     one tile and at most `chunk` keys each, whose partial results cross_tile_join adds up.
 // Rows are packed: P query heads that share a key head lie side by side in a tile, so that short
 // query sequences under grouped heads fill it and k and v are read once for all P.
+//
+// It is one block's latency, before the tcgen05 kernel can start: up to 32 sequences are ordered and counted by
+// one warp in registers, more by the block; items are written by all threads, each finding its sequence.
 #include "block_sort.cuh"
 #include "cross.h"
 #include "warp_mma.cuh"
@@ -23,112 +26,127 @@ __global__ void __launch_bounds__(kThreads)
 cross_schedule_kernel(const CrossSegs segs, int Hq, int lg_pack, int chunk, int num_sms, WsHeader *hdr,
                       CrossItem *items, CrossTile *tiles, int32_t *status)
 {
-    extern __shared__ unsigned long long s_key[];      // [NP]: key count descending, then index
+    extern __shared__ unsigned long long s_key[];      // [NP]: key count descending, then index; later first item | index
     __shared__ int64_t s_warp[32];
-    __shared__ int s_bad;
+    __shared__ int s_bad, s_used, s_total, s_tiles, s_all_split;
     grid_release();
     const int tid = threadIdx.x, B = segs.B;
-    int NP = 1;
+    int NP = 32;
     while (NP < B) NP <<= 1;
-    if (tid == 0) s_bad = 0;
-    __syncthreads();
-    for (int i = tid; i < NP; i += kThreads) {
-        CrossSeg x;
-        const bool fine = i < B && load_seg(segs, i, x, status, true);
-        // offsets that decrease somewhere could claim more rows than there are: no items at all then
-        if (i < B && segs.cu_q[i + 1] < segs.cu_q[i]) s_bad = 1;
-        const bool use = fine && x.qn > 0 && x.kn > 0;
-        s_key[i] = use ? ((unsigned long long)(0x7fffffffu - (uint32_t)x.kn) << 32) | (uint32_t)i : ~0ull;
-    }
-    __syncthreads();
-    if (s_bad) {
-        if (tid == 0) {
-            hdr->n_long = hdr->reserved = hdr->n_tiny = hdr->next_long = 0;
-            hdr->error = VIT_ERR_BAD_SEQLENS;
-        }
-        return;
-    }
-    block_sort(s_key, NP, tid);
-
+    int *s_tile = reinterpret_cast<int *>(s_key + NP); // [NP] first tile
     const int lg_tile = 7 - lg_pack;                   // tokens of a 128-row tile, log2
     const int packs = Hq >> lg_pack;
-    const int per = (B + kThreads - 1) / kThreads, lo = min(tid * per, B), hi = min(lo + per, B);
-    auto seg_at = [&](int p, CrossSeg &x) -> bool {
-        if (s_key[p] == ~0ull) return false;
-        load_seg(segs, (int)(s_key[p] & 0xffffffffu), x, nullptr, false);
-        return true;
+    // an unusable sequence sorts behind all others
+    auto key_of = [&](bool use, const CrossSeg &x, int i) {
+        return ((unsigned long long)(use ? 0x7fffffffu - (uint32_t)x.kn : 0xffffffffu) << 32) | (uint32_t)i;
     };
+    auto blocks_of = [&](const CrossSeg &x, int lg) { return packs * ((x.qn + (1 << lg) - 1) >> lg); };
+    auto runs_of = [&](const CrossSeg &x) { return chunk > 0 ? key_runs(x.kn, chunk) : 1; };
     // two-tile blocks of the batch: few of them means split items throughout
-    int64_t mine = 0, total_full;
-    for (int p = lo; p < hi; ++p) {
-        CrossSeg x;
-        if (seg_at(p, x)) mine += (int64_t)packs * ((x.qn + (2 << lg_tile) - 1) >> (lg_tile + 1));
-    }
-    block_exclusive_scan(mine, s_warp, &total_full);
-    const bool all_split = chunk > 0 || 2 * total_full <= (int64_t)num_sms;
-    const int lg_block = all_split ? lg_tile : lg_tile + 1;
-    int64_t n_items = 0, n_tiles = 0, total, total_tiles;
-    for (int p = lo; p < hi; ++p) {
-        CrossSeg x;
-        if (!seg_at(p, x)) continue;
-        const int64_t n = (int64_t)packs * ((x.qn + (1 << lg_block) - 1) >> lg_block);
-        const int runs = chunk > 0 ? key_runs(x.kn, chunk) : 1;
-        n_items += n * runs;
-        if (runs > 1) n_tiles += n;
-    }
-    int64_t at = block_exclusive_scan(n_items, s_warp, &total);
-    int64_t tile_at = block_exclusive_scan(n_tiles, s_warp, &total_tiles);
-    // a sequence's items by the thread that holds it when they are few, else by all threads in turn
-    for (int p = lo; p < hi; ++p) {
-        CrossSeg x;
-        if (!seg_at(p, x)) continue;
-        const int nq = (x.qn + (1 << lg_block) - 1) >> lg_block;
-        const int runs = chunk > 0 ? key_runs(x.kn, chunk) : 1;
-        s_key[p] = ((unsigned long long)at << 32) | (uint32_t)(s_key[p] & 0xffffffffu);   // first item | sequence
-        if (runs > 1) {
-            for (int i = 0; i < packs * nq; ++i) {
-                const int h = i / nq, qb = i - h * nq;
-                tiles[tile_at + i] = CrossTile{x.q0 + (qb << lg_block), x.q0 + x.qn, h << lg_pack,
-                                               (int)(at + (int64_t)i * runs), runs, {0, 0, 0}};
+    auto split_all = [&](int64_t full) { return chunk > 0 || 2 * full <= (int64_t)num_sms; };
+    if (B <= 32) {
+        // a warp: one sequence per lane
+        if (tid < 32) {
+            CrossSeg x;
+            const bool fine = tid < B && load_seg(segs, tid, x, status, true);
+            // offsets that decrease somewhere could claim more rows than there are: no items at all then
+            const bool bad = tid < B && segs.cu_q[tid + 1] < segs.cu_q[tid];
+            const bool use = fine && x.qn > 0 && x.kn > 0;
+            int64_t full = use ? blocks_of(x, lg_tile + 1) : 0;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) full += __shfl_xor_sync(0xffffffffu, full, o);
+            const bool all_split = split_all(full);
+            const int n = use ? blocks_of(x, all_split ? lg_tile : lg_tile + 1) : 0, runs = use ? runs_of(x) : 1;
+            int rank, at, tile_at;
+            warp_place(key_of(use, x, tid), n * runs, runs > 1 ? n : 0, rank, at, tile_at);
+            s_key[rank] = ((unsigned long long)at << 32) | (uint32_t)tid;
+            s_tile[rank] = tile_at;
+            const unsigned used = __ballot_sync(0xffffffffu, use), any_bad = __ballot_sync(0xffffffffu, bad);
+            if (rank == 31) {                          // the last: its sums are all but its own
+                s_total = at + n * runs;
+                s_tiles = tile_at + (runs > 1 ? n : 0);
+                s_used = __popc(used);
+                s_all_split = all_split;
+                s_bad = any_bad != 0;
             }
-            tile_at += (int64_t)packs * nq;
         }
-        at += (int64_t)packs * nq * runs;
-    }
-    __syncthreads();
-    const int lane = tid & 31, warp = tid >> 5;
-    for (int p = warp; p < B; p += kThreads / 32) {
-        if (s_key[p] == ~0ull) break;                  // the unused sequences are last
-        CrossSeg x;
-        load_seg(segs, (int)(s_key[p] & 0xffffffffu), x, nullptr, false);
-        const int first = (int)(s_key[p] >> 32);
-        const int nq = (x.qn + (1 << lg_block) - 1) >> lg_block;
-        const int runs = chunk > 0 ? key_runs(x.kn, chunk) : 1;
-        const int n = packs * nq * runs;
-        for (int i = lane; i < n; i += 32) {
-            const int run = i % runs, j = i / runs, h = j / nq, qb = j - h * nq;
-            const int q0 = x.q0 + (qb << lg_block), left = x.qn - (qb << lg_block);
-            CrossItem it;
-            it.k0 = x.k0 + run * chunk;
-            it.kn = runs > 1 ? min(chunk, x.kn - run * chunk) : x.kn;
-            it.q0 = q0;
-            it.q1 = x.q0 + x.qn;
-            it.head = h << lg_pack;
-            it.split = all_split || left <= (1 << lg_tile);
-            it.slot = runs > 1 ? first + i : -1;
-            it.pad = 0;
-            items[first + i] = it;
+        __syncthreads();
+    } else {
+        if (tid == 0) s_bad = s_used = 0;
+        __syncthreads();
+        for (int i = tid; i < NP; i += kThreads) {
+            CrossSeg x;
+            const bool fine = i < B && load_seg(segs, i, x, status, true);
+            if (i < B && segs.cu_q[i + 1] < segs.cu_q[i]) s_bad = 1;
+            const bool use = fine && x.qn > 0 && x.kn > 0;
+            s_key[i] = key_of(use, x, i);
+            if (use) atomicAdd(&s_used, 1);
         }
+        __syncthreads();
+        block_sort(s_key, NP, tid);
+        const int per = (B + kThreads - 1) / kThreads, lo = min(tid * per, s_used), hi = min(lo + per, s_used);
+        auto seg_at = [&](int p) {
+            CrossSeg x;
+            load_seg(segs, (int)(s_key[p] & 0xffffffffu), x, nullptr, false);
+            return x;
+        };
+        int64_t mine = 0, total_full, n_items = 0, n_tiles = 0, total, total_tiles;
+        for (int p = lo; p < hi; ++p) mine += blocks_of(seg_at(p), lg_tile + 1);
+        block_exclusive_scan(mine, s_warp, &total_full);
+        const bool all_split = split_all(total_full);
+        const int lg_block = all_split ? lg_tile : lg_tile + 1;
+        for (int p = lo; p < hi; ++p) {
+            const CrossSeg x = seg_at(p);
+            const int n = blocks_of(x, lg_block), runs = runs_of(x);
+            n_items += (int64_t)n * runs;
+            if (runs > 1) n_tiles += n;
+        }
+        int64_t at = block_exclusive_scan(n_items, s_warp, &total);
+        int64_t tile_at = block_exclusive_scan(n_tiles, s_warp, &total_tiles);
+        for (int p = lo; p < hi; ++p) {
+            const CrossSeg x = seg_at(p);
+            const int n = blocks_of(x, lg_block), runs = runs_of(x);
+            s_key[p] = ((unsigned long long)at << 32) | (uint32_t)(s_key[p] & 0xffffffffu);
+            s_tile[p] = (int)tile_at;
+            at += (int64_t)n * runs;
+            if (runs > 1) tile_at += n;
+        }
+        if (tid == 0) {
+            s_total = (int)total;
+            s_tiles = (int)total_tiles;
+            s_all_split = all_split;
+        }
+        __syncthreads();
     }
+    const bool bad = s_bad != 0, all_split = s_all_split != 0;
+    const int total = bad ? 0 : s_total, lg_block = all_split ? lg_tile : lg_tile + 1;
     if (tid == 0) {
-        hdr->n_long = (int32_t)total;
-        hdr->reserved = (int32_t)total_tiles;
+        hdr->n_long = total;
+        hdr->reserved = bad ? 0 : s_tiles;
         hdr->n_tiny = 0;
         hdr->bm_long = 1 << lg_block;
         hdr->tiny_max = 0;
-        hdr->error = 0;
+        hdr->error = bad ? VIT_ERR_BAD_SEQLENS : 0;
         hdr->long_all_split = all_split ? 1 : 0;
         hdr->next_long = 0;
+    }
+    for (int i = tid; i < total; i += kThreads) {
+        const int p = place_of(s_key, s_used, i), n = i - (int)(s_key[p] >> 32);
+        CrossSeg x;
+        load_seg(segs, (int)(s_key[p] & 0xffffffffu), x, nullptr, false);
+        const int nq = (x.qn + (1 << lg_block) - 1) >> lg_block, runs = runs_of(x);
+        const int j = n / runs, run = n - j * runs, h = j / nq, qb = j - h * nq;
+        CrossItem it;
+        it.k0 = x.k0 + run * chunk;
+        it.kn = runs > 1 ? min(chunk, x.kn - run * chunk) : x.kn;
+        it.q0 = x.q0 + (qb << lg_block);
+        it.q1 = x.q0 + x.qn;
+        it.head = h << lg_pack;
+        it.split = all_split || x.qn - (qb << lg_block) <= (1 << lg_tile);
+        it.slot = runs > 1 ? i : -1;
+        it.pad = 0;
+        items[i] = it;
+        if (runs > 1 && run == 0) tiles[s_tile[p] + j] = CrossTile{it.q0, it.q1, it.head, i, runs, {0, 0, 0}};
     }
 }
 
@@ -223,16 +241,17 @@ LongPlan long_plan(int64_t Tq, int B, int Hq, int Hk, int D, int max_q, int max_
 cudaError_t launch_cross_schedule(const CrossArgs &a, const LongPlan &p, int num_sms, WsHeader *hdr, CrossItem *items,
                                   CrossTile *tiles, cudaStream_t stream)
 {
-    int np = 1;
+    int np = 32;
     while (np < a.segs.B) np <<= 1;
+    constexpr size_t each = sizeof(unsigned long long) + sizeof(int);
     static DeviceOnce once;
     cudaError_t e = once.run([] {
         return cudaFuncSetAttribute(cross_schedule_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)sizeof(unsigned long long) * VIT_MAX_SEGMENTS);
+                                    (int)each * VIT_MAX_SEGMENTS);
     });
     if (e != cudaSuccess) return e;
     LaunchScope scope("cross_schedule", stream);
-    cross_schedule_kernel<<<1, kThreads, sizeof(unsigned long long) * (size_t)np, stream>>>(
+    cross_schedule_kernel<<<1, kThreads, each * np, stream>>>(
         a.segs, a.Hq, p.lg_pack, p.chunk, num_sms, hdr, items, tiles, a.status);
     return cudaGetLastError();
 }

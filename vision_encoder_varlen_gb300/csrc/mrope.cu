@@ -18,7 +18,10 @@
 // position fits 22 bits, in fp64 beyond (GB300's fp64 rate is low). The remainder in about [-pi, pi]
 // then goes through __sincosf, whose absolute error there is 2^-21. All heads of a token share it.
 //
-// HBM bound: 4 T (Hq + Hk) D bytes forward, 6 T (Hq + Hk) D backward. One warp owns a token (or,
+// HBM bound: 4 T (Hq + Hk) D bytes forward, 6 T (Hq + Hk) D backward. Measured: 36771 tokens of 16 + 16
+// heads of 80, 82 us forward (4.6 TB/s; a plain copy of as many bytes 63 us); 40013 tokens of 16 + 4 heads
+// of 128, 127 us backward (4.8 TB/s); what is above the copy is issue slots (66 and 60 % busy). Rows of one
+// warp's loads straight into registers took 108 and 176 us. One warp owns a token (or,
 // when there are fewer tokens than warps to fill the GPU, a slice of a token's heads): it builds the
 // token's cos/sin row in its own part of shared memory and then walks the heads, so no barrier
 // wider than a warp is needed. A head row belongs to D/16 lanes, lane c holding the 16-byte chunks
