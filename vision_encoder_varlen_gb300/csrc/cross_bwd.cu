@@ -20,13 +20,12 @@
 // both kinds of items was 10 % slower at large sizes (616 against 564 us at 4 x 2048 x 4096, 16 heads
 // of 80: the issuer's loop compiles worse).
 //
-// Measured at 4 sequences of 1500 to 2311 queries over 3000 to 5117 keys, 16 heads of 80: dk, dv 316 us and dq
-// 239 us (1.08 PFLOP/s of the products they make; the forward and backward pass together 0.79 PFLOP/s of the five
-// products of the gradient and two of the forward pass), the tensor pipe 43 % busy: bound by the exchange
-// between the softmax groups and the issuer, whose products of one tile and sums of the one before take turns
-// in one pipe. delta comes from the stored bf16 out, as the interface has no other: where few keys carry a row,
-// dP - delta cancels, and dq and dk are off by 1.6 times what their own rounding is (0.27 against 0.17 % in the
-// 2-norm), in longer rows by 1.4 times, for the rounding of P and dS.
+// Measured at 4 x 2048 queries over 4096 keys, 16 heads of 80: dk, dv 317 us, dq 211 us (1.08 and 1.22 PFLOP/s of
+// the products they make), the tensor pipe 43 to 50 % busy: bound by the exchange between the softmax groups and
+// the issuer, whose products of one tile and sums of the one before take turns in one pipe, at 1.3 to 1.5 times
+// the time that the MMAs need alone. delta comes from the stored bf16 out, as the interface has no other: where few
+// keys carry a row, dP - delta cancels, and dq and dk are off by 1.6 times what their own rounding is (0.27
+// against 0.17 % in the 2-norm), in longer rows by 1.4 times, for the rounding of P and dS.
 //
 // Before them, one launch makes the two item lists (a block each) and the statistics -lse log2(e) and
 // -delta of every (token, head) (the other blocks).
@@ -39,8 +38,7 @@
 //                asked for, zeros into the rows that belong to no sequence
 //   warps 4-7, 8-11  the two softmax groups take alternate tiles: S, dP -> registers -> P, dS -> TMEM
 //                over their own S and dP columns; at an item's end they write dk and dv (or half of dq each)
-// TMEM (512 columns): A1 | A2 | two stages of S and dP (BN columns each). BN is 64 at head_dim 128 and 80
-// below: 2 D + 4 BN <= 512, and both S and dP of a tile fit a thread's registers.
+// TMEM (512 columns): A1 | A2 (dk, dv only) | two stages of S and dP (BN columns each).
 // All tiles use slabs of W columns with a 2 W-byte swizzle, so that the same bytes serve as a K-major
 // operand (of S and dP, reduced over D) and as an MN-major one (of the sums, reduced over rows).
 // Streamed rows past the sequence's end enter the sums with P = dS = 0 and are zeroed in shared memory
@@ -67,8 +65,17 @@ constexpr int BM = 128;
 constexpr long long kWaitBudget = 4000000000ll;
 constexpr int kMaxY = 6;
 
-template <int D> struct GradCfg {
-    static constexpr int BN = D == 128 ? 64 : 80;          // streamed rows per tile
+template <int D, bool DKV> struct GradCfg {
+    // Streamed rows per tile: what an MMA of 128 rows costs in shared memory (its A operand) and what a tile costs
+    // in hand-overs go down with more of them, so as many as TMEM has room for beside the sums, (512 - sums) / 4,
+    // and shared memory for four ring slots (64 at head_dim 128, with three). 4 x 2048 x 4096, 16 heads: dq at
+    // head_dim 80 with 96 rows 211 us, 80 rows 240, 64 rows and three TMEM stages 275; at 64 with 112 rows 173,
+    // 80 rows 209; at 96 with 80 rows and four slots 250, 96 rows and three 268; at 128 with 64 rows and three slots
+    // 375, 80 rows and two 598. dk, dv at 80 with 80 rows 317, 48 rows and three stages 394.
+    static constexpr int BN = DKV ? (D == 32 ? 112 : D == 64 ? 96 : D == 128 ? 64 : 80)
+                                  : (D <= 64 ? 112 : D == 80 ? 96 : D == 96 ? 80 : 64);
+    // columns of S and dP that a softmax thread has in registers at a time (tiles of more than 80 come in two parts)
+    static constexpr int PART = BN <= 80 ? BN : (BN / 2 + 15) / 16 * 16;
     static constexpr int W = D % 64 == 0 ? 64 : D % 32 == 0 ? 32 : 16;   // columns of a slab
     static constexpr int SW = 2 * W;                       // its swizzle in bytes
     static constexpr int NS = D / W;                       // slabs
@@ -83,7 +90,7 @@ template <int D> struct GradCfg {
     static constexpr int DATA = OFF_Y + NY * Y_PAIR;
     static constexpr int SMEM = DATA + 1024 > 118 * 1024 ? DATA + 1024 : 118 * 1024;   // one block per SM
     static constexpr int LAYOUT = SW == 128 ? 2 : SW == 64 ? 4 : 6;
-    static constexpr int TA1 = 0, TA2 = D, TSTAGE = 2 * D; // TMEM columns; stage s: S at TSTAGE + 2 BN s, dP BN further
+    static constexpr int TA1 = 0, TA2 = D, TSTAGE = DKV ? 2 * D : D; // TMEM columns; stage s: S at TSTAGE + 2 BN s, dP BN further
     static_assert(TSTAGE + 4 * BN <= 512, "TMEM budget");
     static_assert(SMEM + (D == 128 ? 1280 : 1536) <= 227 * 1024, "shared memory per block, with the statistics and barriers");
     static_assert(X_TILE % 1024 == 0 && Y_SLAB % (8 * SW) == 0 && Y_TILE % (8 * SW) == 0, "slabs start on swizzle atoms");
@@ -121,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_constant__ CUtensorMap tm_x2,
                   const __grid_constant__ CUtensorMap tm_y1, const __grid_constant__ CUtensorMap tm_y2, const Grad p)
 {
-    using C = GradCfg<D>;
+    using C = GradCfg<D, DKV>;
     constexpr int BN = C::BN, NY = C::NY, W = C::W;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *base = reinterpret_cast<unsigned char *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -473,52 +480,63 @@ cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_consta
                 if (!(ok = wait_warp(bars.s_full[st], (u / 2) & 1))) break;
                 tc_fence_after();
                 const uint32_t tS = t_lane + C::TSTAGE + st * 2 * BN, tD = tS + BN;
-                uint32_t sr[BN], dr[BN];
-#pragma unroll
-                for (int c = 0; c < BN; c += 16) tmem_ld16(tS + c, *reinterpret_cast<uint32_t(*)[16]>(sr + c));
-#pragma unroll
-                for (int c = 0; c < BN; c += 16) tmem_ld16(tD + c, *reinterpret_cast<uint32_t(*)[16]>(dr + c));
-                tmem_wait_ld();
-                reg_fence(sr);
-                reg_fence(dr);
                 const uint64_t sc2 = f2_splat(p.scale_log2);
                 const uint64_t nl_row = f2_splat(st_row.x), nd_row = f2_splat(st_row.y);
-                ulonglong2 l4, d4;
+                // columns [C0, C0 + CN): P and dS go where columns already read were
+                auto part = [&](auto c0, auto cn) {
+                    constexpr int C0 = decltype(c0)::value, CN = decltype(cn)::value;
+                    uint32_t sr[CN], dr[CN];
 #pragma unroll
-                for (int c = 0; c < BN; c += 2) {
-                    uint64_t l2 = nl_row, d2 = nd_row;
-                    if constexpr (DKV) {
-                        if (c % 4 == 0) {
-                            l4 = *reinterpret_cast<const ulonglong2 *>(nl + c);
-                            d4 = *reinterpret_cast<const ulonglong2 *>(nd + c);
+                    for (int c = 0; c < CN; c += 16) tmem_ld16(tS + C0 + c, *reinterpret_cast<uint32_t(*)[16]>(sr + c));
+#pragma unroll
+                    for (int c = 0; c < CN; c += 16) tmem_ld16(tD + C0 + c, *reinterpret_cast<uint32_t(*)[16]>(dr + c));
+                    tmem_wait_ld();
+                    reg_fence(sr);
+                    reg_fence(dr);
+                    [[maybe_unused]] ulonglong2 l4, d4;
+#pragma unroll
+                    for (int c = 0; c < CN; c += 2) {
+                        uint64_t l2 = nl_row, d2 = nd_row;
+                        if constexpr (DKV) {
+                            if (c % 4 == 0) {
+                                l4 = *reinterpret_cast<const ulonglong2 *>(nl + C0 + c);
+                                d4 = *reinterpret_cast<const ulonglong2 *>(nd + C0 + c);
+                            }
+                            l2 = c % 4 == 0 ? l4.x : l4.y;
+                            d2 = c % 4 == 0 ? d4.x : d4.y;
                         }
-                        l2 = c % 4 == 0 ? l4.x : l4.y;
-                        d2 = c % 4 == 0 ? d4.x : d4.y;
+                        float x0, x1;
+                        f2_split(f2_fma(f2_from_u32(sr[c], sr[c + 1]), sc2, l2), x0, x1);
+                        float p0 = ex2(x0), p1 = ex2(x1);
+                        uint64_t pp;
+                        asm("mov.b64 %0, {%1, %2};\n" : "=l"(pp) : "f"(p0), "f"(p1));
+                        float g0, g1;
+                        f2_split(f2_mul(f2_add(f2_from_u32(dr[c], dr[c + 1]), d2), pp), g0, g1);
+                        sr[c / 2] = pack_bf16x2(p0, p1);
+                        dr[c / 2] = pack_bf16x2(g0, g1);
                     }
-                    float x0, x1;
-                    f2_split(f2_fma(f2_from_u32(sr[c], sr[c + 1]), sc2, l2), x0, x1);
-                    float p0 = ex2(x0), p1 = ex2(x1);
-                    uint64_t pp;
-                    asm("mov.b64 %0, {%1, %2};\n" : "=l"(pp) : "f"(p0), "f"(p1));
-                    float g0, g1;
-                    f2_split(f2_mul(f2_add(f2_from_u32(dr[c], dr[c + 1]), d2), pp), g0, g1);
-                    sr[c / 2] = pack_bf16x2(p0, p1);
-                    dr[c / 2] = pack_bf16x2(g0, g1);
-                }
-                if (valid < BN) {                             // columns past the end: exactly 0, whatever was there
+                    if (valid < C0 + CN) {                    // columns past the end: exactly 0, whatever was there
 #pragma unroll
-                    for (int c = 0; c < BN; c += 2) {
-                        const uint32_t keep = c + 1 < valid ? 0xffffffffu : c < valid ? 0x0000ffffu : 0u;
-                        sr[c / 2] &= keep;
-                        dr[c / 2] &= keep;
+                        for (int c = 0; c < CN; c += 2) {
+                            const int x = C0 + c;
+                            const uint32_t keep = x + 1 < valid ? 0xffffffffu : x < valid ? 0x0000ffffu : 0u;
+                            sr[c / 2] &= keep;
+                            dr[c / 2] &= keep;
+                        }
                     }
-                }
-                if constexpr (DKV) {
+                    if constexpr (DKV) {
 #pragma unroll
-                    for (int c = 0; c < BN / 2; c += 8) tmem_st8(tS + c, *reinterpret_cast<const uint32_t(*)[8]>(sr + c));
-                }
+                        for (int c = 0; c < CN / 2; c += 8)
+                            tmem_st8(tS + C0 / 2 + c, *reinterpret_cast<const uint32_t(*)[8]>(sr + c));
+                    }
 #pragma unroll
-                for (int c = 0; c < BN / 2; c += 8) tmem_st8(tD + c, *reinterpret_cast<const uint32_t(*)[8]>(dr + c));
+                    for (int c = 0; c < CN / 2; c += 8)
+                        tmem_st8(tD + C0 / 2 + c, *reinterpret_cast<const uint32_t(*)[8]>(dr + c));
+                };
+                using std::integral_constant;
+                part(integral_constant<int, 0>(), integral_constant<int, C::PART>());
+                if constexpr (C::PART < BN)
+                    part(integral_constant<int, C::PART>(), integral_constant<int, BN - C::PART>());
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -682,8 +700,9 @@ cross_grad_prepare_kernel(const Prepare p)
 {
     grid_release();
     if (blockIdx.x < 2) {
-        make_list(blockIdx.x == 1, p.segs, p.Hq, p.Hk, p.lg_pack, GradCfg<D>::BN, p.counts,
-                  blockIdx.x == 1 ? p.dkv : p.dq, p.status);
+        const bool keys = blockIdx.x == 1;
+        make_list(keys, p.segs, p.Hq, p.Hk, p.lg_pack, keys ? GradCfg<D, true>::BN : GradCfg<D, false>::BN, p.counts,
+                  keys ? p.dkv : p.dq, p.status);
         return;
     }
     // D / 8 lanes per row, 16 bytes of o and do each
@@ -724,7 +743,7 @@ bool tile_map(CUtensorMap *m, const void *ptr, int64_t T, int H, int D, int64_t 
 template <int D, bool DKV>
 cudaError_t launch_pass(const CrossGradArgs &a, const GradPlan &pl, int num_sms, cudaStream_t stream)
 {
-    using C = GradCfg<D>;
+    using C = GradCfg<D, DKV>;
     const CrossSegs &s = a.f.segs;
     const int pack = 1 << pl.lg_pack;
     CUtensorMap q, dq, k, v;              // q and do, then k and v, as the resident or the streamed side
