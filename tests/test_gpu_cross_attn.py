@@ -208,3 +208,66 @@ def test_side_stream():
     got = [vit.cross_attn(q, k, v, cq, ck, 1, 900, stream=side) for _ in range(8)]
     side.synchronize()
     assert all(torch.equal(want, x) for x in got)
+
+
+def many(B, lo_q, hi_q, lo_k, hi_k, seed):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda lo, hi: torch.randint(lo, hi + 1, (B,), generator=g).tolist()
+    return r(lo_q, hi_q), r(lo_k, hi_k)
+
+
+# up to 32 sequences are ordered by one warp, more by the block; lists that end in a wave for few SMs are cut there
+# (20 x 8 heads of 300 rows: 320 items; 5 x 4 x 8 of 1000: 160); chunked keys (few tiles, long keys) with many sequences
+MANY = [
+    (31, 17, 60, 0, 200, 4, 1, 64),
+    (32, 17, 60, 0, 200, 4, 4, 80),
+    (33, 17, 60, 0, 200, 4, 1, 64),
+    (700, 0, 40, 0, 50, 2, 1, 32),
+    (20, 300, 300, 128, 300, 8, 8, 64),
+    (5, 1000, 1000, 100, 500, 8, 2, 96),
+    (36, 20, 50, 1, 3000, 2, 2, 128),
+    (6, 100, 140, 1, 5000, 4, 2, 128),
+    (40, 1, 16, 0, 300, 2, 2, 80),
+]
+
+
+@pytest.mark.parametrize("B,lo_q,hi_q,lo_k,hi_k,Hq,Hk,D", MANY)
+def test_many_sequences(B, lo_q, hi_q, lo_k, hi_k, Hq, Hk, D):
+    ql, kl = many(B, lo_q, hi_q, lo_k, hi_k, B)
+    q, k, v, cq, ck = make(ql, kl, Hq, Hk, D)
+    status = vit.new_status()
+    out, lse = vit.cross_attn(q, k, v, cq, ck, max(ql), max(kl), return_lse=True, status=status)
+    assert vit.read_status(status) == 0
+    check(out, lse, reference(q, k, v, cq, ck))
+    assert torch.equal(out, vit.cross_attn(q, k, v, cq, ck, max(ql), max(kl)))
+
+
+@pytest.mark.parametrize("B", [20, 50])
+def test_one_bad_sequence_among_many(B):
+    ql, kl = many(B, 20, 60, 30, 100, 7)
+    q, k, v, cq, ck = make(ql, kl, 4, 2, 64)
+    ref = reference(q, k, v, cq, ck)
+    # a key count past its bound: only that sequence is left alone
+    k_len = torch.tensor(kl, dtype=torch.int32, device="cuda")
+    k_len[11] += 1
+    out, status = torch.full_like(q, 3.0), vit.new_status()
+    vit.cross_attn(q, k, v, cq, ck, 60, 200, k_len=k_len, out=out, status=status)
+    assert vit.read_status(status) == -10
+    a, b = int(cq[11]), int(cq[12])
+    assert (out[a:b] == 3).all()
+    check(out, None, ref, torch.cat((torch.arange(a), torch.arange(b, q.shape[0]))).cuda())
+    # query offsets that decrease: nothing past the tensors, and the error is told
+    cq[11] = cq[12] + 1
+    status = vit.new_status()
+    vit.cross_attn(q, k, v, cq, ck, 200, 200, out=out, status=status)
+    assert vit.read_status(status) == -10
+
+
+@pytest.mark.parametrize("rows", [15, 16, 17, 32, 33])
+def test_where_the_kernels_change(rows):
+    """Query rows per key head around the sizes at which another kernel takes the call; keys around 32 MiB, and more
+    than 16 runs of a sequence."""
+    for keys, D in ((400, 64), (65000, 128)):
+        q, k, v, cq, ck = make([rows, 1], [keys, 700], 2, 2, D)
+        out, lse = vit.cross_attn(q, k, v, cq, ck, rows, max(keys, 700), return_lse=True)
+        check(out, lse, reference(q, k, v, cq, ck))

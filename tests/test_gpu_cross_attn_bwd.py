@@ -14,7 +14,7 @@ import pytest
 import torch
 
 import vision_encoder_varlen_gb300 as vit
-from test_gpu_cross_attn import make
+from test_gpu_cross_attn import make, many
 
 pytestmark = pytest.mark.gpu
 BF = 2.0 ** -8
@@ -208,3 +208,28 @@ def test_graph_replays_other_lengths():
         graph.replay()
         torch.cuda.synchronize()
         check(g, reference(q, k, v, do, cq, ck), f"{n}: ")
+
+
+@pytest.mark.parametrize("B,Hq,Hk,D", [(31, 4, 1, 64), (32, 2, 2, 80), (33, 4, 2, 96), (700, 2, 1, 32), (40, 8, 8, 128)])
+def test_many_sequences(B, Hq, Hk, D):
+    ql, kl = many(B, 0, 60, 0, 150, B)
+    q, k, v, cq, ck = make(ql, kl, Hq, Hk, D)
+    g = torch.Generator(device="cuda").manual_seed(B)
+    do = torch.randn(q.shape, generator=g, device="cuda").bfloat16()
+    out, lse = vit.cross_attn(q, k, v, cq, ck, max(ql), max(kl), return_lse=True)
+    status = vit.new_status()
+    got = vit.cross_attn_bwd(do, q, k, v, out, lse, cq, ck, max(ql), max(kl), status=status)
+    assert vit.read_status(status) == 0
+    check(got, reference(q, k, v, do, cq, ck))
+
+
+@pytest.mark.parametrize("D", [32, 64, 80, 96, 128])
+def test_every_tail(D):
+    """Streamed lengths that end in each 16-row step of a tile, and in each half of the widest."""
+    kl = [112 * 2 + n for n in (0, 1, 15, 16, 17, 47, 48, 49, 63, 64, 65, 79, 80, 81, 95, 96, 97, 111)]
+    ql = kl[::-1]
+    q, k, v, cq, ck = make(ql, kl, 2, 2, D)
+    g = torch.Generator(device="cuda").manual_seed(D)
+    do = torch.randn(q.shape, generator=g, device="cuda").bfloat16()
+    out, lse = vit.cross_attn(q, k, v, cq, ck, return_lse=True)
+    check(vit.cross_attn_bwd(do, q, k, v, out, lse, cq, ck), reference(q, k, v, do, cq, ck))
