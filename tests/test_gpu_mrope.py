@@ -235,3 +235,20 @@ def test_agrees_with_the_two_axis_call():
     # both round once; cos and sin differ by at most 2^-20
     assert ((two.double() - three.double()).abs() <= 2 * BF * two.double().abs() + 2.0 ** -17).all()
     assert math.isclose(float((two == three).double().mean()), 1.0, abs_tol=0.02)
+
+
+def test_extreme_positions():
+    """The largest and smallest positions of an int32, and those around the change to 64-bit angles."""
+    D, H = 64, 3
+    ends = [2 ** 31 - 1, -2 ** 31, -2 ** 31 + 1, 2 ** 22 - 1, 2 ** 22, -2 ** 22, -2 ** 22 + 1, 0]
+    pos = torch.tensor([[a, b, c] for a in ends for b, c in ((0, 7), (a, -a - 1))], dtype=torch.int32, device="cuda")
+    T = pos.shape[0]
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(T, H, D, generator=g, device="cuda").bfloat16()
+    freq = torch.cat((torch.ones(3), torch.rand(28), torch.tensor([-0.7]))).float().cuda()
+    sec = (12, 10, 10)
+    y, _ = vit.qk_norm_mrope(x, None, pos, freq, sec)
+    close(y, *reference(x, None, angles(pos, freq, sec, False), False), "y")
+    dx, _, _ = vit.qk_norm_mrope_bwd(x, None, None, None, pos, freq, sec)
+    ref, mag, _, _ = reference_grad(x, None, None, angles(pos, freq, sec, False), False)
+    close(dx, ref, mag, "dx")

@@ -6,6 +6,8 @@ lane, 5 shuffle steps and 16 warps; rsqrtf to 2 units) is good to 64 * 2^-24 = 2
 magnitudes that enter an element. Weight sums over n rows add (n + 64) 2^-24 of the sum of
 magnitudes.
 """
+import math
+
 import pytest
 import torch
 
@@ -54,6 +56,17 @@ CASES = [
     (31, 8192, "channel", True, True, True, 1.0),
     (2, 8192, "token", False, True, False, 1.0),
     (9, 504, None, False, False, False, 1.0),
+    # many rows per block (the ring goes round), and widths where the layout changes
+    (3001, 5120, "token", True, True, True, 1.0),
+    (5003, 640, "channel", True, True, False, 1.0),
+    (6001, 512, "token", True, True, True, 1.0),
+    (1501, 4096, "channel", True, True, False, 0.5),
+    (903, 6144, "channel", True, True, True, 1.0),
+    (701, 6152, "token", True, True, True, 1.0),
+    (1103, 8192, "token", True, True, True, 1.0),
+    (611, 7000, None, False, True, False, 1.0),
+    (1200, 2056, "channel", True, False, True, 1.0),
+    (1301, 776, "token", False, False, False, 1.0),
 ]
 
 
@@ -178,3 +191,21 @@ def test_empty_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_expanded_gate_is_refused():
+    # an expanded row is a gate for all tokens, whose gradient is a [C] sum: it is given as [C]
+    x, y, _, wo, wr, dz, dh = make(5, 64, None, True, True, False)
+    g = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: vit.norm_residual(x, y, gate=g.expand(5, 64), w_post=wo, w_pre=wr),
+                 lambda: vit.norm_residual_bwd(dz.bfloat16(), None, x, y, gate=g.expand(5, 64), w_post=wo, w_pre=wr)):
+        with pytest.raises(ValueError, match=r"given as \[C\]"):
+            call()
+
+
+def test_infinity_in_y_without_its_norm():
+    # dy is the gradient times the gate where y has no norm: finite whatever y holds
+    h, y, g, _, wr, dz, dh = make(300, 1280, "channel", False, True, False)
+    y[7, 5], y[200, 1279] = math.inf, math.nan
+    dx, dy, *_ = vit.norm_residual_bwd(dz.bfloat16(), dh.bfloat16(), h, y, gate=g, w_pre=wr)
+    assert torch.isfinite(dx).all() and torch.isfinite(dy).all()

@@ -293,3 +293,42 @@ def test_offsets_past_32_bits():
     # the sum is exact in fp32 (two bf16 values, a power of two) up to its rounding and one more to bf16
     want = (tail[0].double() + 2 * want.double()).view(600, -1)
     close(h[-600:], want, (2.0 ** -8 + 2.0 ** -22) * want.abs() + 1e-30, "h")
+
+
+@pytest.mark.parametrize("Lq", [1, 33])
+def test_most_sequences(Lq):
+    """As many sequences as a call takes: 1 or 33 queries each, 0 to 7 states; one more is refused."""
+    B, Hq, Hk, D, most = 8192, 2, 1, 64, 7
+    g = torch.Generator(device="cuda").manual_seed(5)
+    n = torch.randint(0, most + 1, (B,), generator=g, device="cuda")
+    cu_k = torch.cat((n.new_zeros(1), n.cumsum(0))).int()
+    cu_q = torch.arange(B + 1, device="cuda", dtype=torch.int32) * Lq
+    r = lambda T, H: torch.randn(T, H, D, generator=g, device="cuda").bfloat16()
+    q, k, v, do = r(B * Lq, Hq), r(int(cu_k[-1]), Hk), r(int(cu_k[-1]), Hk), r(B * Lq, Hq)
+    status = vit.new_status()
+    out, lse = vit.cross_attn(q, k, v, cu_q, cu_k, Lq, most, return_lse=True, status=status)
+    dq, dk, dv = vit.cross_attn_bwd(do, q, k, v, out, lse, cu_q, cu_k, Lq, most, status=status)
+    assert vit.read_status(status) == 0
+    # padded to 7 states in 64 bits
+    at = (cu_k[:-1, None] + torch.arange(most, device="cuda")).clamp(max=int(cu_k[-1]) - 1).long()
+    there = (torch.arange(most, device="cuda") < n[:, None])[:, None, None]
+    K, V = (t[at, 0].double().masked_fill(~there[:, 0, 0, :, None], 0.0) for t in (k, v))
+    Q, DO = (t.view(B, Lq, Hq, D).double() for t in (q, do))
+    s = (torch.einsum("bqhd,bkd->bqhk", Q, K) / 8).masked_fill(~there, -math.inf)
+    p = torch.softmax(s, -1).nan_to_num(0.0)
+    o = torch.einsum("bqhk,bkd->bqhd", p, V)
+    mag = torch.einsum("bqhk,bkd->bqhd", p, V.abs())
+    close(out.view(B, Lq, Hq, D), o, E * o.abs() + 1.01 * E * mag, "out")
+    dP = torch.einsum("bqhd,bkd->bqhk", DO, V)
+    dl, dm = (DO * o).sum(-1, keepdim=True), (DO.abs() * (o.abs() + mag)).sum(-1, keepdim=True)
+    ds = p * (dP - dl)
+    DS = 1.01 * (E * ds.abs() + p * E * dm) + F * p * (dP.abs() + dl.abs())
+    want = torch.einsum("bqhk,bkd->bqhd", ds, K) / 8
+    close(dq.view(B, Lq, Hq, D), want, torch.einsum("bqhk,bkd->bqhd", DS, K.abs()) / 8 + E * want.abs(), "dq")
+    rows = there[:, 0, 0]
+    want = torch.einsum("bqhk,bqhd->bkd", ds, Q)[rows] / 8
+    close(dk[:, 0], want, (torch.einsum("bqhk,bqhd->bkd", DS, Q.abs()) / 8)[rows] + E * want.abs(), "dk")
+    want = torch.einsum("bqhk,bqhd->bkd", p, DO)[rows]
+    close(dv[:, 0], want, 1.01 * E * torch.einsum("bqhk,bqhd->bkd", p, DO.abs())[rows] + E * want.abs(), "dv")
+    with pytest.raises(vit.VitError, match="-7"):
+        vit.cross_attn(q, k, v, torch.cat((cu_q, cu_q[-1:])), torch.cat((cu_k, cu_k[-1:])), Lq, most)

@@ -759,7 +759,10 @@ def _gate_stride(gate, T, C) -> int:
     if gate.dim() == 1:
         _channel(gate, "gate", C)
         return 0
-    return _rows2(gate, "gate", T, C, _BF16)
+    stride = _rows2(gate, "gate", T, C, _BF16)
+    if stride == 0:                                    # an expanded row: its gradient would be a [C] one
+        raise ValueError("a gate for all tokens is given as [C]")
+    return stride
 
 
 def norm_residual(x: torch.Tensor, y: torch.Tensor, *, gate: torch.Tensor | None = None,

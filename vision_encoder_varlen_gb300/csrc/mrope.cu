@@ -69,7 +69,7 @@ __device__ __forceinline__ int axis_of(const Mrope &p, int m) {
 
 // pos * f reduced to about [-pi, pi], as an fp32 value
 __device__ __forceinline__ float reduced_angle(int pos, float f) {
-    if (abs(pos) < (1 << 22) && fabsf(f) <= 1.f) {
+    if ((unsigned)pos + (1u << 22) < (1u << 23) && fabsf(f) <= 1.f) {      // (abs(-2^31) is negative)
         // pos is exact in fp32 and p + e is the exact product; the multiple n of 2 pi (|n| < 2^20) is
         // taken off in two parts, 2 pi = C1 + C2 to 2^-50 (Cody and Waite): the error stays below 2^-21
         const float x = (float)pos, p = x * f, e = fmaf(x, f, -p);
