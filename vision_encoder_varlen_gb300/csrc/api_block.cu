@@ -55,9 +55,10 @@ vit_status_t vit_grid_positions(const int32_t *grid_thw, int n, int64_t T, int32
     if (((uintptr_t)grid_thw & 3u) || ((uintptr_t)pos_thw & 3u) || ((uintptr_t)cu_seqlens & 3u))
         return VIT_ERR_MISALIGNED;
     if (!pos_thw && !cu_seqlens) return VIT_OK;
-    vit_status_t st = check_device();
+    int sms = 0;
+    vit_status_t st = check_device(&sms);
     if (st != VIT_OK) return st;
-    return from_cuda(launch_grid_positions(grid_thw, n, T, pos_thw, cu_seqlens, status_dev, (cudaStream_t)stream));
+    return from_cuda(launch_grid_positions(grid_thw, n, T, pos_thw, cu_seqlens, status_dev, sms, (cudaStream_t)stream));
 }
 
 vit_status_t vit_qk_norm_mrope(const void *q_in, void *q_out, const void *k_in, void *k_out, int64_t T, int Hq, int Hk,

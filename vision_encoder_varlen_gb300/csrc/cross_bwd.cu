@@ -698,6 +698,7 @@ template <int D>
 __global__ void __launch_bounds__(kSortThreads)
 cross_grad_prepare_kernel(const Prepare p)
 {
+    grid_wait();
     grid_release();
     if (blockIdx.x < 2) {
         const bool keys = blockIdx.x == 1;
@@ -825,9 +826,8 @@ template <int D> cudaError_t launch_d(const CrossGradArgs &a, const GradPlan &pl
         constexpr int per = 32 * (32 / (D / 8));             // rows of a block at a time
         const int64_t want = (r.rows + per - 1) / per, cap = (int64_t)num_sms * 8;
         LaunchScope scope("cross_grad_prepare", stream);
-        cross_grad_prepare_kernel<D><<<2 + (unsigned)(want < cap ? want : cap), kSortThreads,
-                                       sizeof(unsigned long long) * (size_t)np, stream>>>(r);
-        e = cudaGetLastError();
+        e = launch_chained(cross_grad_prepare_kernel<D>, 2 + (unsigned)(want < cap ? want : cap), kSortThreads,
+                           sizeof(unsigned long long) * (size_t)np, stream, r);
         if (e != cudaSuccess) return e;
     }
 

@@ -78,6 +78,7 @@ cross_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     __shared__ volatile int s_abort;
     __shared__ float s_m[NW][16], s_l[NW][16];
 
+    grid_wait();
     grid_release();                                           // the join may take its place already
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = blockIdx.z, hk = blockIdx.x, b = blockIdx.y;   // later runs last: ragged lengths leave them empty
@@ -340,9 +341,8 @@ cross_join_kernel(const Few p)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.y;
     CrossSeg seg;
-    const bool fine = load_seg(p.segs, b, seg, nullptr, false);
     grid_wait();                                              // the runs' results
-    if (!fine) return;
+    if (!load_seg(p.segs, b, seg, nullptr, false)) return;
     const int n_rows = seg.qn * p.Hq;                         // (token, head) rows of the sequence
     const int runs = key_runs(seg.kn, p.chunk);
     const int x = WIDE ? (int)blockIdx.x : (int)blockIdx.x * 8 + warp;
@@ -414,8 +414,7 @@ cudaError_t launch_mt(const CrossArgs &a, const FewPlan &pl, const Few &p, cudaS
     if (e != cudaSuccess) return e;
     {
         LaunchScope scope("cross_few", stream);
-        kern<<<dim3(a.Hk, s.B, pl.n_split), 32 * kMmaWarps<MT> + 32, smem, stream>>>(mk, mkr, mv, mvr, p);
-        e = cudaGetLastError();
+        e = launch_chained(kern, dim3(a.Hk, s.B, pl.n_split), 32 * kMmaWarps<MT> + 32, smem, stream, mk, mkr, mv, mvr, p);
     }
     if (e != cudaSuccess || pl.n_split == 1) return e;
     LaunchScope scope("cross_join", stream);

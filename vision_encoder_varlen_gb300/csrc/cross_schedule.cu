@@ -31,6 +31,7 @@ cross_schedule_kernel(const CrossSegs segs, int Hq, int lg_pack, int chunk, int 
     extern __shared__ unsigned long long s_key[];      // [NP]: key count descending, then index; later first item | index
     __shared__ int64_t s_warp[32];
     __shared__ int s_bad, s_used, s_total, s_tiles, s_all_split, s_more;
+    grid_wait();
     grid_release();
     const int tid = threadIdx.x, B = segs.B;
     int NP = 32;
@@ -168,8 +169,8 @@ cross_schedule_kernel(const CrossSegs segs, int Hq, int lg_pack, int chunk, int 
 // out = sum_s 2^(e_s - E) O_s / sum_s 2^(e_s - E) over a tile's key runs, one warp per row.
 template <int D>
 __global__ void __launch_bounds__(256)
-cross_tile_join_kernel(const WsHeader *__restrict__ hdr, const CrossTile *__restrict__ tiles, const CrossLong cx,
-                       __nv_bfloat16 *__restrict__ out, int64_t out_stride, float *__restrict__ lse, int Hq)
+cross_tile_join_kernel(const WsHeader *hdr, const CrossTile *tiles, const CrossLong cx, __nv_bfloat16 *out,
+                       int64_t out_stride, float *lse, int Hq)
 {
     grid_wait();
     const int n_tiles = hdr->reserved, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -266,9 +267,8 @@ cudaError_t launch_cross_schedule(const CrossArgs &a, const LongPlan &p, int num
     });
     if (e != cudaSuccess) return e;
     LaunchScope scope("cross_schedule", stream);
-    cross_schedule_kernel<<<1, kThreads, each * np, stream>>>(
-        a.segs, a.Hq, p.lg_pack, p.chunk, num_sms, hdr, items, tiles, a.status);
-    return cudaGetLastError();
+    return launch_chained(cross_schedule_kernel, 1, kThreads, each * np, stream, a.segs, a.Hq, p.lg_pack, p.chunk,
+                          num_sms, hdr, items, tiles, a.status);
 }
 
 cudaError_t launch_cross_tile_join(const CrossArgs &a, const LongPlan &p, const CrossLong &cx, const WsHeader *hdr,

@@ -79,7 +79,10 @@ struct DeviceOnce {
 // Chained launches: a kernel started by launch_chained may begin while the launch before it in the
 // stream still runs (as soon as every block of that one has called grid_release or ended), and must
 // call grid_wait before it touches anything that launch writes, or before it ends. Both are nothing in
-// an ordinary launch. Waiting here is the hardware's, and ends when the launch before has ended.
+// an ordinary launch. Waiting here is the hardware's, and ends when the launch before has ended. The launch
+// before may be another call's or another library's: a kernel that starts a call waits before it reads anything,
+// and hides only its own start. Pointers of such kernels are not `const __restrict__`: a load through those could
+// be moved before the wait.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 
@@ -155,7 +158,7 @@ cudaError_t launch_attn_long(const AttnArgs &a, int64_t max_items_long, int num_
 
 // (time, row, column) of every token of n packed clips, and their offsets (either may be NULL)
 cudaError_t launch_grid_positions(const int32_t *grid_thw, int n, int64_t T, int32_t *pos, int32_t *cu_seqlens,
-                                  int32_t *status, cudaStream_t stream);
+                                  int32_t *status, int num_sms, cudaStream_t stream);
 
 // Three-axis rotary positions with the per-head norm. A half whose head count is 0 is left out.
 struct MropeArgs {

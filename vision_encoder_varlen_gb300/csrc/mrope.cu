@@ -19,9 +19,10 @@
 // then goes through __sincosf, whose absolute error there is 2^-21. All heads of a token share it.
 //
 // HBM bound: 4 T (Hq + Hk) D bytes forward, 6 T (Hq + Hk) D backward. Measured: 36771 tokens of 16 + 16
-// heads of 80, 82 us forward (4.6 TB/s; a plain copy of as many bytes 63 us); 40013 tokens of 16 + 4 heads
-// of 128, 127 us backward (4.8 TB/s); what is above the copy is issue slots (66 and 60 % busy). Rows of one
-// warp's loads straight into registers took 108 and 176 us. One warp owns a token (or,
+// heads of 80, 77 us forward with their positions (4.9 TB/s; a plain copy of as many bytes 63 us); 40013 tokens
+// of 16 + 4 heads of 128, 126 us backward (4.9 TB/s). Issue slots are 66 and 60 % busy, but fewer instructions
+// (the weights unpacked once in shared memory) changed nothing forward and cost 7 % backward (bank conflicts).
+// Rows of one warp's loads straight into registers took 108 and 176 us. One warp owns a token (or,
 // when there are fewer tokens than warps to fill the GPU, a slice of a token's heads): it builds the
 // token's cos/sin row in its own part of shared memory and then walks the heads, so no barrier
 // wider than a warp is needed. A head row belongs to D/16 lanes, lane c holding the 16-byte chunks
@@ -237,6 +238,8 @@ mrope_kernel(const Mrope p)
     __shared__ int s_pos[kWarps][AHEAD][4];               // the steps' positions, copied with their rows
     __shared__ float4 s_cs[kWarps][D / 4];
     __shared__ uint4 s_w[2][D / 8];
+    grid_wait();
+    grid_release();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane / CH, c = lane % CH;               // row of the step, chunk of the row
     const int my_row = g < ROWS ? g : INT_MAX;             // lanes past the last group have none
@@ -395,6 +398,7 @@ mrope_bwd_kernel(const Mrope p)
     __shared__ float4 s_cs[kWarps][D / 4];
     __shared__ uint4 s_w[2][D / 8];
     __shared__ float s_sum[kWarps][2][D];
+    grid_wait();
     grid_release();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane / CH, c = lane % CH;
@@ -551,8 +555,7 @@ template <int D> cudaError_t launch_fwd(Mrope p, bool il, int num_sms, cudaStrea
     cudaError_t e = once[il].run([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
     if (e != cudaSuccess) return e;
     LaunchScope scope("qk_norm_mrope", stream);
-    kern<<<blocks, kThreads, smem, stream>>>(p);
-    return cudaGetLastError();
+    return launch_chained(kern, blocks, kThreads, smem, stream, p);
 }
 
 template <int D> cudaError_t launch_bwd(Mrope p, bool il, float *dnorm_w, int num_sms, cudaStream_t stream) {
@@ -568,8 +571,7 @@ template <int D> cudaError_t launch_bwd(Mrope p, bool il, float *dnorm_w, int nu
         cudaError_t e = once[il].run([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
         if (e != cudaSuccess) return e;
         LaunchScope scope("qk_norm_mrope_bwd", stream);
-        kern<<<blocks, kThreads, smem, stream>>>(p);
-        e = cudaGetLastError();
+        e = launch_chained(kern, blocks, kThreads, smem, stream, p);
         if (e != cudaSuccess) return e;
     }
     if (!dnorm_w) return cudaSuccess;
@@ -606,21 +608,19 @@ Mrope params(const MropeArgs &a) {
 }
 
 constexpr int kPosThreads = 256;
-constexpr int kTokensPerBlock = 2048;
 
 // (time, row, column) of every token of clips packed one after the other, frames row-major one
 // after the other inside a clip, and the clips' offsets: every block scans the grid list in shared
-// memory, so no pass over blocks is needed.
+// memory, so no pass over blocks is needed. Latency bound at a batch's sizes: a thread's tokens are few, and
+// the scan takes two barriers.
 __global__ void __launch_bounds__(kPosThreads)
-grid_positions_kernel(const int32_t *__restrict__ grid_thw, int n, int64_t T, int32_t *__restrict__ pos,
-                      int32_t *__restrict__ cu_out, int32_t *status)
+grid_positions_kernel(const int32_t *grid_thw, int n, int64_t T, int32_t *pos, int32_t *cu_out, int32_t *status)
 {
     extern __shared__ int64_t s_cu[];          // [n + 1]
-    __shared__ int64_t s_part[kPosThreads];
-    __shared__ int s_bad;
-    const int tid = threadIdx.x;
-    if (tid == 0) s_bad = 0;
-    __syncthreads();
+    __shared__ int64_t s_part[kPosThreads / 32];
+    grid_wait();
+    grid_release();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // tokens of clip i; a product past any T this call takes is an error, not an overflow
     auto size = [&](int i) -> int64_t {
         const int64_t t = grid_thw[3 * i], h = grid_thw[3 * i + 1], w = grid_thw[3 * i + 2];
@@ -632,20 +632,22 @@ grid_positions_kernel(const int32_t *__restrict__ grid_thw, int n, int64_t T, in
     const int per = (n + kPosThreads - 1) / kPosThreads;
     const int lo = min(tid * per, n), hi = min(lo + per, n);
     int64_t local = 0;
+    int bad = 0;
     for (int i = lo; i < hi; ++i) {
         const int64_t s = size(i);
-        if (s < 0) s_bad = 1;
+        bad |= s < 0;
         local += s < 0 ? 0 : s;
     }
-    s_part[tid] = local;
-    __syncthreads();
-    for (int off = 1; off < kPosThreads; off <<= 1) {
-        const int64_t add = tid >= off ? s_part[tid - off] : 0;
-        __syncthreads();
-        s_part[tid] += add;
-        __syncthreads();
+    int64_t run = local;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += y;
     }
-    int64_t run = s_part[tid] - local;
+    if (lane == 31) s_part[warp] = run;
+    bad = __syncthreads_or(bad);
+    run -= local;
+    for (int w = 0; w < warp; ++w) run += s_part[w];
     if (tid == 0) s_cu[0] = 0;
     for (int i = lo; i < hi; ++i) {
         const int64_t s = size(i);
@@ -653,15 +655,14 @@ grid_positions_kernel(const int32_t *__restrict__ grid_thw, int n, int64_t T, in
         s_cu[i + 1] = run;
     }
     __syncthreads();
-    if (s_bad || s_cu[n] != T) {
+    if (bad || s_cu[n] != T) {
         if (blockIdx.x == 0 && tid == 0) report_error(status, VIT_ERR_GRID_MISMATCH);
         return;
     }
     if (blockIdx.x == 0 && cu_out)
         for (int i = tid; i <= n; i += kPosThreads) cu_out[i] = (int32_t)s_cu[i];
     if (!pos) return;
-    for (int64_t t = (int64_t)blockIdx.x * kTokensPerBlock + tid;
-         t < T && t < (int64_t)(blockIdx.x + 1) * kTokensPerBlock; t += kPosThreads) {
+    for (int64_t t = (int64_t)blockIdx.x * kPosThreads + tid; t < T; t += (int64_t)gridDim.x * kPosThreads) {
         int a = 0, b = n;                      // s_cu[a] <= t < s_cu[b]; ends on the last such a (empty clips skipped)
         while (b - a > 1) {
             const int m = (a + b) >> 1;
@@ -678,7 +679,7 @@ grid_positions_kernel(const int32_t *__restrict__ grid_thw, int n, int64_t T, in
 }  // namespace
 
 cudaError_t launch_grid_positions(const int32_t *grid_thw, int n, int64_t T, int32_t *pos, int32_t *cu_seqlens,
-                                  int32_t *status, cudaStream_t stream)
+                                  int32_t *status, int num_sms, cudaStream_t stream)
 {
     const size_t smem = sizeof(int64_t) * (size_t)(n + 1);
     static DeviceOnce once;
@@ -687,11 +688,12 @@ cudaError_t launch_grid_positions(const int32_t *grid_thw, int n, int64_t T, int
                                     (int)(sizeof(int64_t) * (VIT_MAX_SEGMENTS + 1)));
     });
     if (e != cudaSuccess) return e;
-    const int64_t want = pos ? (T + kTokensPerBlock - 1) / kTokensPerBlock : 1;
+    // a token per thread up to four blocks an SM; a long list, which every block scans, is worth fewer blocks
+    const int64_t want = pos ? (T + kPosThreads - 1) / kPosThreads : 1, most = (int64_t)num_sms * (n <= 1024 ? 4 : 1);
+    const unsigned blocks = (unsigned)(want < 1 ? 1 : want < most ? want : most);
     LaunchScope scope("grid_positions", stream);
-    grid_positions_kernel<<<(unsigned)(want > 0 ? want : 1), kPosThreads, smem, stream>>>(grid_thw, n, T, pos,
-                                                                                         cu_seqlens, status);
-    return cudaGetLastError();
+    return launch_chained(grid_positions_kernel, blocks, kPosThreads, smem, stream, grid_thw, n, T, pos, cu_seqlens,
+                          status);
 }
 
 cudaError_t launch_mrope(const MropeArgs &a, int num_sms, cudaStream_t stream)

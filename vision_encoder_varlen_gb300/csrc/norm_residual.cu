@@ -105,6 +105,8 @@ __global__ void __launch_bounds__(512)
 norm_residual_kernel(const Fwd p, int wpr, int rows_per_block)
 {
     __shared__ float s_red[2 * kMaxWarps];
+    grid_wait();
+    grid_release();
     const int lane_in_row = wpr == 1 ? (threadIdx.x & 31) : (int)threadIdx.x;
     const int row_in_block = wpr == 1 ? (int)(threadIdx.x >> 5) : 0;
     const int nvec = p.C >> 3, group = wpr * 32;
@@ -199,6 +201,7 @@ template <int VPT, bool F32>
 __global__ void __launch_bounds__(256)
 norm_residual_bwd_kernel(const Bwd p, int rows_per_block)
 {
+    grid_wait();
     grid_release();
     __shared__ float3 s_sum[256 * VPT];
     const int lane_in_row = threadIdx.x & 31, row_in_block = (int)(threadIdx.x >> 5);
@@ -412,6 +415,7 @@ norm_residual_bwd_ring_kernel(const Bwd p, const Ring ring)
     __shared__ __align__(16) float s_red[2][WARPS][8];
     __shared__ uint64_t s_full[kMaxStages];
     const int never = 0;                       // no abort flag: every thread waits for itself
+    grid_wait();
     grid_release();
     const int nvec = p.C >> 2, group = blockDim.x, wpr = blockDim.x >> 5;
     const float inv_c = 1.f / (float)p.C;
@@ -608,7 +612,7 @@ struct SumOut {
     float *out[3];
 };
 __global__ void __launch_bounds__(1024)
-column_sum_kernel(const float *__restrict__ part, int n_parts, int n_sum, int C, const SumOut o)
+column_sum_kernel(const float *part, int n_parts, int n_sum, int C, const SumOut o)
 {
     grid_wait();                               // the partial sums of the launch before
     __shared__ float s[32][33];
@@ -649,18 +653,19 @@ template <bool F32> cudaError_t launch_fwd(const Fwd &p, int num_sms, cudaStream
     const unsigned blocks = (unsigned)(want < cap ? want : cap);
     const int threads = 32 * wpr * rows;
     LaunchScope scope("norm_residual", stream);
+    auto run = [&](auto kern) { return launch_chained(kern, blocks, threads, 0, stream, p, wpr, rows); };
     switch (vpt) {
-        case 1: norm_residual_kernel<1, F32><<<blocks, threads, 0, stream>>>(p, wpr, rows); break;
-        case 2: norm_residual_kernel<2, F32><<<blocks, threads, 0, stream>>>(p, wpr, rows); break;
-        case 3: norm_residual_kernel<3, F32><<<blocks, threads, 0, stream>>>(p, wpr, rows); break;
+        case 1: return run(norm_residual_kernel<1, F32>);
+        case 2: return run(norm_residual_kernel<2, F32>);
+        case 3: return run(norm_residual_kernel<3, F32>);
         default:
             if constexpr (!F32) {
-                if (vpt == 4) norm_residual_kernel<4, F32><<<blocks, threads, 0, stream>>>(p, wpr, rows);
-                else if (vpt == 5) norm_residual_kernel<5, F32><<<blocks, threads, 0, stream>>>(p, wpr, rows);
-                else norm_residual_kernel<6, F32><<<blocks, threads, 0, stream>>>(p, wpr, rows);
+                if (vpt == 4) return run(norm_residual_kernel<4, F32>);
+                if (vpt == 5) return run(norm_residual_kernel<5, F32>);
+                return run(norm_residual_kernel<6, F32>);
             }
+            return cudaErrorInvalidValue;
     }
-    return cudaGetLastError();
 }
 
 constexpr int kRingBytes = 224 * 1024;     // shared memory of an SM that the rings share
@@ -718,8 +723,7 @@ cudaError_t launch_ring(const Bwd &p, int32_t *status, int num_sms, unsigned *bl
     });
     if (e != cudaSuccess) return e;
     LaunchScope scope("norm_residual_bwd", stream);
-    kern<<<*blocks, threads, (size_t)r.stages * r.slot + fixed, stream>>>(p, r);
-    return cudaGetLastError();
+    return launch_chained(kern, *blocks, threads, (size_t)r.stages * r.slot + fixed, stream, p, r);
 }
 
 template <bool F32>
@@ -734,9 +738,8 @@ cudaError_t launch_bwd(const Bwd &p, const SumOut &o, int32_t *status, int num_s
         blocks = (unsigned)(want < cap ? want : cap);
         if (blocks > 0) {
             LaunchScope scope("norm_residual_bwd", stream);
-            if (p.C <= 256) norm_residual_bwd_kernel<1, F32><<<blocks, 32 * rows, 0, stream>>>(p, rows);
-            else norm_residual_bwd_kernel<2, F32><<<blocks, 32 * rows, 0, stream>>>(p, rows);
-            e = cudaGetLastError();
+            e = launch_chained(p.C <= 256 ? norm_residual_bwd_kernel<1, F32> : norm_residual_bwd_kernel<2, F32>, blocks,
+                               32 * rows, 0, stream, p, rows);
         }
     } else if (p.C <= kNarrow) {
         e = launch_ring<4, F32, 384>(p, status, num_sms, &blocks, stream);
