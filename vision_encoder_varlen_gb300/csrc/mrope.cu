@@ -627,7 +627,7 @@ grid_positions_kernel(const int32_t *grid_thw, int n, int64_t T, int32_t *pos, i
         if (t < 0 || h < 0 || w < 0) return -1;
         const int64_t hw = h * w;
         if (t == 0 || hw == 0) return 0;
-        return (hw > T || t > T / hw) ? -1 : t * hw;
+        return (hw > T || t > T || t * hw > T) ? -1 : t * hw;
     };
     const int per = (n + kPosThreads - 1) / kPosThreads;
     const int lo = min(tid * per, n), hi = min(lo + per, n);

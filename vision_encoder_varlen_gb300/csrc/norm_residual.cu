@@ -417,7 +417,8 @@ norm_residual_bwd_ring_kernel(const Bwd p, const Ring ring)
     const int never = 0;                       // no abort flag: every thread waits for itself
     grid_wait();
     grid_release();
-    const int nvec = p.C >> 2, group = blockDim.x, wpr = blockDim.x >> 5;
+    // with eight pieces always all threads: a lane's places are constants then, and take no registers
+    const int nvec = p.C >> 2, group = NP == 8 ? THREADS : (int)blockDim.x, wpr = group >> 5;
     const float inv_c = 1.f / (float)p.C;
     const bool gate_tok = p.gate && p.gate_stride != 0;
     const uint32_t row_b = 2u * (uint32_t)p.C, res_b = (F32 ? 4u : 2u) * (uint32_t)p.C;
@@ -503,6 +504,7 @@ norm_residual_bwd_ring_kernel(const Bwd p, const Ring ring)
             for (int i = 0; i < NP; ++i) {
                 Piece x;
                 values(s, i, x);
+                const Quad wr = w_pre[i], wo = w_post[i];
                 auto add = [&](uint64_t h, uint64_t dh, uint64_t dz, uint64_t y, uint64_t g, uint64_t wr, uint64_t wo) {
                     const uint64_t a = f2_mul(dz, wr), A = f2_mul(f2_mul(g, wo), y);
                     sum[0] = f2_fma(h, h, sum[0]);
@@ -512,8 +514,8 @@ norm_residual_bwd_ring_kernel(const Bwd p, const Ring ring)
                     sum[4] = f2_fma(A, a, sum[4]);
                     sum[5] = f2_fma(A, h, sum[5]);
                 };
-                add(x.h.a, x.dh.a, x.dz.a, x.y.a, x.g.a, w_pre[i].a, w_post[i].a);
-                add(x.h.b, x.dh.b, x.dz.b, x.y.b, x.g.b, w_pre[i].b, w_post[i].b);
+                add(x.h.a, x.dh.a, x.dz.a, x.y.a, x.g.a, wr.a, wo.a);
+                add(x.h.b, x.dh.b, x.dz.b, x.y.b, x.g.b, wr.b, wo.b);
             }
             float t[kSums];
 #pragma unroll
@@ -562,6 +564,7 @@ norm_residual_bwd_ring_kernel(const Bwd p, const Ring ring)
             const int v = i * group + threadIdx.x;
             Piece x;
             values(s, i, x);
+            const Quad wr = w_pre[i], wo = w_post[i];
             Quad dx, dy, dg;
             auto back = [&](uint64_t h, uint64_t dh, uint64_t dz, uint64_t y, uint64_t g, uint64_t wr, uint64_t wo,
                             uint64_t &s_pre, uint64_t &s_post, uint64_t &s_gate, uint64_t &ox, uint64_t &oy,
@@ -574,10 +577,10 @@ norm_residual_bwd_ring_kernel(const Bwd p, const Ring ring)
                 s_post = f2_fma(du, yh, s_post);
                 oy = p.w_post ? f2_mul(r1_2, f2_fma(du, wo, f2_mul(y, nc1))) : du;   // (0 y is not 0 for every y)
             };
-            back(x.h.a, x.dh.a, x.dz.a, x.y.a, x.g.a, w_pre[i].a, w_post[i].a, a_pre[i].a, a_post[i].a, a_gate[i].a,
-                 dx.a, dy.a, dg.a);
-            back(x.h.b, x.dh.b, x.dz.b, x.y.b, x.g.b, w_pre[i].b, w_post[i].b, a_pre[i].b, a_post[i].b, a_gate[i].b,
-                 dx.b, dy.b, dg.b);
+            back(x.h.a, x.dh.a, x.dz.a, x.y.a, x.g.a, wr.a, wo.a, a_pre[i].a, a_post[i].a, a_gate[i].a, dx.a, dy.a,
+                 dg.a);
+            back(x.h.b, x.dh.b, x.dz.b, x.y.b, x.g.b, wr.b, wo.b, a_pre[i].b, a_post[i].b, a_gate[i].b, dx.b, dy.b,
+                 dg.b);
             if (v >= nvec) continue;
             put4<F32>(p.dx, t * p.dx_stride + 4 * v, dx);
             put4<false>(p.dy, t * p.dy_stride + 4 * v, dy);
@@ -673,12 +676,11 @@ constexpr int kNarrow = 6144;              // widest row that 384 threads hold a
 
 // Pieces per lane and threads of a row's block. Fewer threads with more pieces each cost fewer shuffles and
 // barriers per column (15000 x 4096 bf16: 225 us with two pieces and 512 threads, 185 with four and 256;
-// 6000 x 8192: 220 us with six and 352, 132 with eight and 256). Eight below 6144 columns as well help where
+// 6000 x 8192: 220 us with six and 352, 109 with eight and 256). Eight below 6144 columns as well help where
 // they fill the lanes (4096: 152 us) and not elsewhere (1280: 169 instead of 144 us, 520 with an fp32 residual
 // 285 instead of 207). Threads of an SM: 384 (480, which the registers allow, leave each block too few slots:
 // 37007 x 1280 with an fp32 residual 232 instead of 173 us; 320: 176).
-int ring_pieces(int C) { return C <= kNarrow ? 4 : 8; }
-int ring_threads(int C) { return (C / 4 + 32 * ring_pieces(C) - 1) / (32 * ring_pieces(C)) * 32; }
+int ring_threads(int C) { return C <= kNarrow ? (C / 4 + 127) / 128 * 32 : 256; }
 int ring_blocks(int C) { return C <= kNarrow ? 384 / ring_threads(C) : 1; }
 
 template <int NP, bool F32, int THREADS>
