@@ -403,8 +403,9 @@ constexpr int kSums = 6;
 // come through an L1 that the ring leaves almost nothing of: 9001 x 5120 took 340 us that way). Measured at
 // 9001 x 5120 with an fp32 residual and a gate per token: 168 us (6.0 TB/s); with two reductions per row
 // 225 us. With conditions on what is there in the loops, 66 instead of about 30 instructions per column,
-// 9001 x 5120 in bf16 took 162 instead of 144 us.
-template <int NP, bool F32, int THREADS>
+// 9001 x 5120 in bf16 took 162 instead of 144 us (125 with a constant number of threads).
+// GROUP: the block's threads where they are a constant, and a lane's places with them (0: taken from the launch).
+template <int NP, bool F32, int THREADS, int GROUP>
 __global__ void __launch_bounds__(THREADS)
 norm_residual_bwd_ring_kernel(const Bwd p, const Ring ring)
 {
@@ -417,8 +418,7 @@ norm_residual_bwd_ring_kernel(const Bwd p, const Ring ring)
     const int never = 0;                       // no abort flag: every thread waits for itself
     grid_wait();
     grid_release();
-    // with eight pieces always all threads: a lane's places are constants then, and take no registers
-    const int nvec = p.C >> 2, group = NP == 8 ? THREADS : (int)blockDim.x, wpr = group >> 5;
+    const int nvec = p.C >> 2, group = GROUP ? GROUP : (int)blockDim.x, wpr = group >> 5;
     const float inv_c = 1.f / (float)p.C;
     const bool gate_tok = p.gate && p.gate_stride != 0;
     const uint32_t row_b = 2u * (uint32_t)p.C, res_b = (F32 ? 4u : 2u) * (uint32_t)p.C;
@@ -675,18 +675,26 @@ constexpr int kRingBytes = 224 * 1024;     // shared memory of an SM that the ri
 constexpr int kNarrow = 6144;              // widest row that 384 threads hold at four pieces each
 
 // Pieces per lane and threads of a row's block. Fewer threads with more pieces each cost fewer shuffles and
-// barriers per column (15000 x 4096 bf16: 225 us with two pieces and 512 threads, 185 with four and 256;
+// barriers per column (15000 x 4096 bf16: 225 us with two pieces and 512 threads, 185 with four and 256, before their number was a constant;
 // 6000 x 8192: 220 us with six and 352, 109 with eight and 256). Eight below 6144 columns as well help where
 // they fill the lanes (4096: 152 us) and not elsewhere (1280: 169 instead of 144 us, 520 with an fp32 residual
 // 285 instead of 207). Threads of an SM: 384 (480, which the registers allow, leave each block too few slots:
 // 37007 x 1280 with an fp32 residual 232 instead of 173 us; 320: 176).
 int ring_threads(int C) { return C <= kNarrow ? (C / 4 + 127) / 128 * 32 : 256; }
+// A constant number of threads is worth 10 to 14 % with a bf16 residual (15000 x 4096: 185 -> 160 us, 37007 x 1280: 143
+// -> 127), where the loops are bound by their instructions, and nothing with an fp32 one; above 6144 columns
+// the constants also keep eight pieces from spilling. A few numbers serve all widths.
+int ring_threads_bf16(int C)
+{
+    const int t = ring_threads(C);
+    return t <= 192 ? t : (t + 63) / 64 * 64;
+}
 int ring_blocks(int C) { return C <= kNarrow ? 384 / ring_threads(C) : 1; }
 
-template <int NP, bool F32, int THREADS>
+template <int NP, bool F32, int THREADS, int GROUP>
 cudaError_t launch_ring(const Bwd &p, int32_t *status, int num_sms, unsigned *blocks, cudaStream_t stream)
 {
-    const int threads = ring_threads(p.C), cols = 4 * NP * threads;      // of a padded row
+    const int threads = GROUP ? GROUP : ring_threads(p.C), cols = 4 * NP * threads;      // of a padded row
     const bool gate_tok = p.gate && p.gate_stride != 0;
     const int res_b = (F32 ? 4 : 2) * cols, row_b = 2 * cols;
     Ring r;
@@ -695,7 +703,7 @@ cudaError_t launch_ring(const Bwd &p, int32_t *status, int num_sms, unsigned *bl
     const bool absent = !p.w_pre || !p.dh || !p.y;
     const int fixed = (absent ? res_b : 0) + (gate_tok ? 0 : row_b);
     // as many blocks per SM as its registers hold, each with two slots at least
-    int ctas = ring_blocks(p.C);
+    int ctas = THREADS / threads;
     while (ctas > 1 && kRingBytes / ctas < 2 * r.slot + fixed) --ctas;
     r.stages = (kRingBytes / ctas - fixed) / r.slot;
     if (r.stages > kMaxStages) r.stages = kMaxStages;
@@ -718,7 +726,7 @@ cudaError_t launch_ring(const Bwd &p, int32_t *status, int num_sms, unsigned *bl
     if (most > norm_residual_parts(p.C)) most = norm_residual_parts(p.C);
     *blocks = (unsigned)(p.T < most ? p.T : most);
     if (*blocks == 0) return cudaSuccess;
-    auto kern = norm_residual_bwd_ring_kernel<NP, F32, THREADS>;
+    auto kern = norm_residual_bwd_ring_kernel<NP, F32, THREADS, GROUP>;
     static DeviceOnce once;
     cudaError_t e = once.run([&] {
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
@@ -743,10 +751,21 @@ cudaError_t launch_bwd(const Bwd &p, const SumOut &o, int32_t *status, int num_s
             e = launch_chained(p.C <= 256 ? norm_residual_bwd_kernel<1, F32> : norm_residual_bwd_kernel<2, F32>, blocks,
                                32 * rows, 0, stream, p, rows);
         }
-    } else if (p.C <= kNarrow) {
-        e = launch_ring<4, F32, 384>(p, status, num_sms, &blocks, stream);
+    } else if (p.C > kNarrow) {
+        e = launch_ring<8, F32, 256, 256>(p, status, num_sms, &blocks, stream);
+    } else if constexpr (F32) {
+        e = launch_ring<4, F32, 384, 0>(p, status, num_sms, &blocks, stream);
     } else {
-        e = launch_ring<8, F32, 256>(p, status, num_sms, &blocks, stream);
+        switch (ring_threads_bf16(p.C)) {
+            case 64: e = launch_ring<4, F32, 384, 64>(p, status, num_sms, &blocks, stream); break;
+            case 96: e = launch_ring<4, F32, 384, 96>(p, status, num_sms, &blocks, stream); break;
+            case 128: e = launch_ring<4, F32, 384, 128>(p, status, num_sms, &blocks, stream); break;
+            case 160: e = launch_ring<4, F32, 384, 160>(p, status, num_sms, &blocks, stream); break;
+            case 192: e = launch_ring<4, F32, 384, 192>(p, status, num_sms, &blocks, stream); break;
+            case 256: e = launch_ring<4, F32, 384, 256>(p, status, num_sms, &blocks, stream); break;
+            case 320: e = launch_ring<4, F32, 384, 320>(p, status, num_sms, &blocks, stream); break;
+            default: e = launch_ring<4, F32, 384, 384>(p, status, num_sms, &blocks, stream); break;
+        }
     }
     if (e != cudaSuccess || p.n_sum == 0) return e;
     return launch_column_sum(p.part, (int)blocks, p.n_sum, p.C, o.out[0], o.out[1], o.out[2], stream);
