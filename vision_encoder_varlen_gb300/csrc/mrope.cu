@@ -21,7 +21,8 @@
 // HBM bound: 4 T (Hq + Hk) D bytes forward, 6 T (Hq + Hk) D backward. Measured: 36771 tokens of 16 + 16
 // heads of 80, 77 us forward with their positions (4.9 TB/s; a plain copy of as many bytes 63 us); 40013 tokens
 // of 16 + 4 heads of 128, 126 us backward (4.9 TB/s). Issue slots are 66 and 60 % busy, but fewer instructions
-// (the weights unpacked once in shared memory) changed nothing forward and cost 7 % backward (bank conflicts).
+// (the weights unpacked once in shared memory; a variant for whole tokens) changed nothing forward, and cost 7 %
+// backward (bank conflicts).
 // Rows of one warp's loads straight into registers took 108 and 176 us. One warp owns a token (or,
 // when there are fewer tokens than warps to fill the GPU, a slice of a token's heads): it builds the
 // token's cos/sin row in its own part of shared memory and then walks the heads, so no barrier

@@ -14,13 +14,15 @@
 // Everything is HBM bound: a row is read once, the reductions run on it in fp32 and it is written
 // once. Forward, a row belongs to a group of `wpr` warps, each lane holding VPT pieces of 8 columns in
 // registers; a group of one warp needs shuffles only, larger ones (a whole block) meet in shared memory.
-// 37007 x 1280 in bf16 takes 72 us (5.3 TB/s; a plain copy of as many bytes 63 us; rows through a ring in
-// shared memory, as the gradient has them, 107 us). h is normalised before it is rounded to its storage type;
+// 37007 x 1280 in bf16 takes 63 us (6.0 TB/s), what a plain copy of as many bytes takes (rows through a ring in
+// shared memory, as the gradient has them, took 107 us). h is normalised before it is rounded to its storage type;
 // the gradient recomputes r2 from the stored h it is given.
 //
 // The sums over tokens are accumulated in registers by persistent groups (a lane keeps its columns
 // from row to row), written once per group as a partial row of the workspace and added up by a
 // second small kernel in a fixed order, so results do not change from run to run.
+#include <type_traits>
+
 #include "internal.h"
 #include "rope_math.cuh"
 #include "sm100.cuh"
@@ -100,10 +102,13 @@ struct Fwd {
     float scale, eps;
 };
 
-template <int VPT, bool F32>
-__global__ void __launch_bounds__(512)
-norm_residual_kernel(const Fwd p, int wpr, int rows_per_block)
+// ONE: a warp per row, whose lanes' places are constants (37007 x 1280: 63 us, 71 with the row's warps taken from
+// the launch).
+template <int VPT, bool F32, bool ONE>
+__global__ void __launch_bounds__(ONE ? 128 : 512)
+norm_residual_kernel(const Fwd p, int warps, int rows_per_block)
 {
+    const int wpr = ONE ? 1 : warps;
     __shared__ float s_red[2 * kMaxWarps];
     grid_wait();
     grid_release();
@@ -449,7 +454,7 @@ norm_residual_bwd_ring_kernel(const Bwd p, const Ring ring)
         const int64_t t = blockIdx.x + (int64_t)k * gridDim.x;
         const int s = k % ring.stages;
         const uint32_t bar = sm100::smem_addr(&s_full[s]);
-        const uint32_t dst = sm100::smem_addr(s_ring) + s * ring.slot;   // (of what is copied, all go from slot to slot)
+        const uint32_t dst = sm100::smem_addr(s_ring) + s * ring.slot;   // (all that is copied is there per slot)
         sm100::mbar_arrive_expect_tx(bar, slot_b);
         const char *h = static_cast<const char *>(p.h), *dh = static_cast<const char *>(p.dh);
         if (p.w_pre) {
@@ -647,6 +652,8 @@ void row_shape(int C, bool f32, int *vpt, int *wpr)
     *wpr = (nvec + 32 * *vpt - 1) / (32 * *vpt);
 }
 
+template <int V> using Pieces = std::integral_constant<int, V>;
+
 template <bool F32> cudaError_t launch_fwd(const Fwd &p, int num_sms, cudaStream_t stream)
 {
     int vpt, wpr;
@@ -656,16 +663,20 @@ template <bool F32> cudaError_t launch_fwd(const Fwd &p, int num_sms, cudaStream
     const unsigned blocks = (unsigned)(want < cap ? want : cap);
     const int threads = 32 * wpr * rows;
     LaunchScope scope("norm_residual", stream);
-    auto run = [&](auto kern) { return launch_chained(kern, blocks, threads, 0, stream, p, wpr, rows); };
+    auto run = [&](auto v) {
+        constexpr int V = decltype(v)::value;
+        return launch_chained(wpr == 1 ? norm_residual_kernel<V, F32, true> : norm_residual_kernel<V, F32, false>, blocks,
+                              threads, 0, stream, p, wpr, rows);
+    };
     switch (vpt) {
-        case 1: return run(norm_residual_kernel<1, F32>);
-        case 2: return run(norm_residual_kernel<2, F32>);
-        case 3: return run(norm_residual_kernel<3, F32>);
+        case 1: return run(Pieces<1>());
+        case 2: return run(Pieces<2>());
+        case 3: return run(Pieces<3>());
         default:
             if constexpr (!F32) {
-                if (vpt == 4) return run(norm_residual_kernel<4, F32>);
-                if (vpt == 5) return run(norm_residual_kernel<5, F32>);
-                return run(norm_residual_kernel<6, F32>);
+                if (vpt == 4) return run(Pieces<4>());
+                if (vpt == 5) return run(Pieces<5>());
+                return run(Pieces<6>());
             }
             return cudaErrorInvalidValue;
     }
@@ -675,8 +686,8 @@ constexpr int kRingBytes = 224 * 1024;     // shared memory of an SM that the ri
 constexpr int kNarrow = 6144;              // widest row that 384 threads hold at four pieces each
 
 // Pieces per lane and threads of a row's block. Fewer threads with more pieces each cost fewer shuffles and
-// barriers per column (15000 x 4096 bf16: 225 us with two pieces and 512 threads, 185 with four and 256, before their number was a constant;
-// 6000 x 8192: 220 us with six and 352, 109 with eight and 256). Eight below 6144 columns as well help where
+// barriers per column (15000 x 4096 bf16: 225 us with two pieces and 512 threads, 185 with four and 256, before
+// their number was a constant; 6000 x 8192: 220 us with six and 352, 109 with eight and 256). Eight below 6144 columns as well help where
 // they fill the lanes (4096: 152 us) and not elsewhere (1280: 169 instead of 144 us, 520 with an fp32 residual
 // 285 instead of 207). Threads of an SM: 384 (480, which the registers allow, leave each block too few slots:
 // 37007 x 1280 with an fp32 residual 232 instead of 173 us; 320: 176).
