@@ -825,16 +825,11 @@ def norm_residual_bwd(dz: torch.Tensor | None, dh: torch.Tensor | None, h: torch
     _channel(w_post, "w_post", C)
     _channel(w_pre, "w_pre", C)
     dx, dy = _new(ref, (T, C), ref.dtype, stream), _new(ref, (T, C), _BF16, stream)
-    sums = (gate is not None and gate.dim() == 1) + (w_post is not None) + (w_pre is not None)
-    vec = list(_new(ref, (sums, C), _F32, stream).unbind(0)) if sums else []
-    dgate = None
-    if gate is not None:
-        if gate.dim() == 1:
-            dgate = vec.pop()
-        else:
-            dgate = _new(gate, (T, C), _BF16, stream)
-    dw_post = vec.pop() if w_post is not None else None
-    dw_pre = vec.pop() if w_pre is not None else None
+    whole = gate is not None and gate.dim() == 1       # one gate for all tokens
+    dgate = None if gate is None else _new(ref, (C,), _F32, stream) if whole else _new(ref, (T, C), _BF16, stream)
+    dw_post = None if w_post is None else _new(ref, (C,), _F32, stream)
+    dw_pre = None if w_pre is None else _new(ref, (C,), _F32, stream)
+    sums = whole or w_post is not None or w_pre is not None
     if workspace is None:
         workspace = _scratch(_size("vit_norm_residual_bwd_workspace_size", C) if sums else 0, ref, stream)
     _call("vit_norm_residual_bwd", dev, stream, _addr(dz), _addr(dh), _addr(h), _addr(y), _addr(gate), _addr(w_post),
