@@ -403,8 +403,12 @@ cudaError_t launch_mt(const CrossArgs &a, const FewPlan &pl, const Few &p, cudaS
     constexpr int rem = Tile<D>::REM > 0 ? Tile<D>::REM : 64, wide = D >= 64 ? 64 : rem;
     CUtensorMap mk, mkr, mv, mvr;
     const CrossSegs &s = a.segs;
-    if (!kv_map(&mk, a.k, s.Tk, a.Hk, D, a.k_stride, wide) || !kv_map(&mkr, a.k, s.Tk, a.Hk, D, a.k_stride, rem) ||
-        !kv_map(&mv, a.v, s.Tk, a.Hk, D, a.v_stride, wide) || !kv_map(&mvr, a.v, s.Tk, a.Hk, D, a.v_stride, rem))
+    if (!kv_map(&mk, a.k, s.Tk, a.Hk, D, a.k_stride, wide) || !kv_map(&mv, a.v, s.Tk, a.Hk, D, a.v_stride, wide))
+        return cudaErrorInvalidValue;
+    mkr = mk;
+    mvr = mv;
+    if (rem != wide &&
+        (!kv_map(&mkr, a.k, s.Tk, a.Hk, D, a.k_stride, rem) || !kv_map(&mvr, a.v, s.Tk, a.Hk, D, a.v_stride, rem)))
         return cudaErrorInvalidValue;
     constexpr int smem = kStages * 2 * Tile<D>::BYTES + 1024;
     static_assert(kStages * 2 * Tile<D>::BYTES >= 2 * MT * 16 * D * 4, "the joins reuse the ring");
