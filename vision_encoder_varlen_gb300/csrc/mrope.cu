@@ -19,10 +19,10 @@
 // then goes through __sincosf, whose absolute error there is 2^-21. All heads of a token share it.
 //
 // HBM bound: 4 T (Hq + Hk) D bytes forward, 6 T (Hq + Hk) D backward. Measured: 36771 tokens of 16 + 16
-// heads of 80, 77 us forward with their positions (4.9 TB/s; a plain copy of as many bytes 63 us); 40013 tokens
+// heads of 80, 75 us forward with their positions (5.0 TB/s; a plain copy of as many bytes 63 us); 40013 tokens
 // of 16 + 4 heads of 128, 126 us backward (4.9 TB/s). Issue slots are 66 and 60 % busy, but fewer instructions
 // (the weights unpacked once in shared memory; a variant for whole tokens) changed nothing forward, and cost 7 %
-// backward (bank conflicts).
+// backward (bank conflicts); blocks of one token per warp instead of resident ones 82 us forward.
 // Rows of one warp's loads straight into registers took 108 and 176 us. One warp owns a token (or,
 // when there are fewer tokens than warps to fill the GPU, a slice of a token's heads): it builds the
 // token's cos/sin row in its own part of shared memory and then walks the heads, so no barrier
@@ -228,7 +228,8 @@ template <int D> __device__ __forceinline__ float group_sum(float v, int first) 
     return s;
 }
 
-constexpr int kAheadFwd = 6, kAheadBwd = 4;        // steps in flight: 48 and 64 KB of a block
+// steps in flight: 40 and 64 KB of a block (forward: 4 steps 78 us, 5 75, 6 77, 8, of which fewer blocks fit, 97)
+constexpr int kAheadFwd = 5, kAheadBwd = 4;
 
 template <int D, bool IL>
 __global__ void __launch_bounds__(kThreads, 3)
