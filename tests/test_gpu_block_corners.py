@@ -1,0 +1,35 @@
+"""Corner calls of the operators around a language model's reading of the encoder's states: no rows, no sequences,
+sequences without states beside others, lists that are wrong in one place, infinities.
+
+Expected values are exact (zeros, untouched rows, the same bits as another call) or from the formulas in 64 bits with
+the bounds that stand beside them.
+"""
+import pytest
+import torch
+
+import vision_encoder_varlen_gb300 as vit
+
+pytestmark = pytest.mark.gpu
+
+BF16 = dict(dtype=torch.bfloat16, device="cuda")
+
+
+# ------------------------------------------------------------------ residual step
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("C", [256, 520, 1280, 6144, 8192])
+@pytest.mark.parametrize("post,pre,gate", [(True, False, False), (False, False, True), (True, True, True),
+                                           (True, False, True), (False, True, False)])
+def test_residual_gradient_of_no_rows(C, post, pre, gate, wide):
+    """The sums over no tokens are 0, whichever of the inputs are there."""
+    w = torch.ones(C, **BF16)
+    dh = torch.empty(0, C, device="cuda", dtype=torch.float32 if wide else torch.bfloat16)
+    none = torch.empty(0, C, **BF16)
+    dx, dy, dgate, dw_post, dw_pre = vit.norm_residual_bwd(
+        none if pre else None, dh, dh if pre else None, none, gate=w if gate else None, w_post=w if post else None,
+        w_pre=w if pre else None)
+    assert dx.shape == dy.shape == (0, C)
+    for asked, s in ((gate, dgate), (post, dw_post), (pre, dw_pre)):
+        assert (s is not None) == asked
+        if asked:
+            assert s.shape == (C,) and not s.any()

@@ -705,6 +705,8 @@ int ring_blocks(int C) { return C <= kNarrow ? 384 / ring_threads(C) : 1; }
 template <int NP, bool F32, int THREADS, int GROUP>
 cudaError_t launch_ring(const Bwd &p, int32_t *status, int num_sms, unsigned *blocks, cudaStream_t stream)
 {
+    *blocks = 0;
+    if (p.T == 0) return cudaSuccess;          // its tensors may be absent, all of them, and then a slot has no size
     const int threads = GROUP ? GROUP : ring_threads(p.C), cols = 4 * NP * threads;      // of a padded row
     const bool gate_tok = p.gate && p.gate_stride != 0;
     const int res_b = (F32 ? 4 : 2) * cols, row_b = 2 * cols;
@@ -736,7 +738,6 @@ cudaError_t launch_ring(const Bwd &p, int32_t *status, int num_sms, unsigned *bl
     int64_t most = (int64_t)num_sms * ctas;
     if (most > norm_residual_parts(p.C)) most = norm_residual_parts(p.C);
     *blocks = (unsigned)(p.T < most ? p.T : most);
-    if (*blocks == 0) return cudaSuccess;
     auto kern = norm_residual_bwd_ring_kernel<NP, F32, THREADS, GROUP>;
     static DeviceOnce once;
     cudaError_t e = once.run([&] {
