@@ -521,7 +521,7 @@ size_t vit_cross_attn_workspace_size(int64_t Tq, int64_t Tk, int Hq, int Hkv, in
  *   k_len        device int32 [B], or NULL: how many of a sequence's key rows are real (encoder
  *                states padded to a common length). The rows behind them are not used, whatever
  *                they hold.
- *   B            0 <= B <= VIT_MAX_SEGMENTS.
+ *   B            0 <= B <= VIT_MAX_SEGMENTS (0: nothing to do).
  *   max_q, max_k bounds of the query and key counts of a sequence (padded buckets are fine), 0: Tq,
  *                Tk. They choose how the work is cut, so tight ones are faster.
  *   scale        <= 0 selects 1/sqrt(D).
@@ -552,7 +552,8 @@ size_t vit_cross_attn_bwd_workspace_size(int64_t Tq, int64_t Tk, int Hq, int Hkv
  *                over the query heads that share a key head. They must not overlap an input. The
  *                gradients of a sequence without keys, or without queries, are 0.
  *   zero_rest    0: rows of no sequence (and key rows behind k_len) are left as they were; else
- *                they are set to 0.
+ *                they are set to 0. With B = 0 nothing is launched, whatever zero_rest is: dq, dk and
+ *                dv are left as they were.
  *   workspace    vit_cross_attn_bwd_workspace_size(...) bytes, 16-byte aligned; calls sharing one
  *                must not overlap.
  * S and dP are recomputed once for dq and once for dk and dv, P and dS rounded to bf16 for their

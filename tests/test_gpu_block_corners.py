@@ -33,3 +33,27 @@ def test_residual_gradient_of_no_rows(C, post, pre, gate, wide):
         assert (s is not None) == asked
         if asked:
             assert s.shape == (C,) and not s.any()
+
+
+# ------------------------------------------------------------------ cross attention
+
+@pytest.mark.parametrize("side", [False, True])
+@pytest.mark.parametrize("Tq,Tk", [(37, 210), (37, 0), (0, 210)])
+def test_gradient_of_no_sequences(Tq, Tk, side):
+    """All rows are rows of no sequence: 0 in new tensors, as they were in given ones."""
+    q, k = torch.randn(Tq, 4, 64, device="cuda").bfloat16(), torch.randn(Tk, 2, 64, device="cuda").bfloat16()
+    lse = torch.zeros(Tq, 4, device="cuda")
+    cu = torch.zeros(1, dtype=torch.int32, device="cuda")
+    stream = torch.cuda.Stream() if side else None
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        for t in [torch.full_like(x, float("nan")) for x in (q, k, k) for _ in range(4)]:
+            del t                                             # what the allocator hands out next is not 0
+    got = vit.cross_attn_bwd(q, q, k, k, q, lse, cu, cu, stream=stream)
+    torch.cuda.synchronize()
+    for t, like in zip(got, (q, k, k)):
+        assert t.shape == like.shape and not t.any()
+    given = [torch.full_like(x, 7) for x in (q, k, k)]
+    vit.cross_attn_bwd(q, q, k, k, q, lse, cu, cu, dq=given[0], dk=given[1], dv=given[2], stream=stream)
+    torch.cuda.synchronize()
+    assert all((t == 7).all() for t in given)

@@ -670,8 +670,9 @@ def cross_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Te
     """Attention of packed queries q [Tq, Hq, D] over packed states k, v [Tk, Hkv, D] of other lengths, sequence
     by sequence (cu_q, cu_k [B + 1]; k_len [B]: real states per sequence where they are padded), without a causal
     mask; Hq is a multiple of Hkv. Serves prompts, single new tokens and latent queries. A sequence without
-    states gets zeros and lse = -inf. ``max_q`` and ``max_k`` bound the lengths (None: Tq, Tk); tight bounds are
-    faster. With ``return_lse`` (or an ``lse`` buffer) returns (out, lse [Tq, Hq] fp32)."""
+    states gets zeros and lse = -inf; rows of no sequence are left as they were (in tensors the call allocates: with
+    any values). ``max_q`` and ``max_k`` bound the lengths (None: Tq, Tk); tight bounds are faster. With
+    ``return_lse`` (or an ``lse`` buffer) returns (out, lse [Tq, Hq] fp32)."""
     Tq, Hq, D = _shape3(q, "q")
     Tk, Hkv, _ = _shape3(k, "k")
     dev = _device(q, k, v, cu_q, cu_k, k_len, out, workspace, status, lse)
@@ -723,6 +724,10 @@ def cross_attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
           Tk, Hq, Hkv, D, dos, qs, ks, vs, os_, _addr(cu_q), _addr(cu_k), _addr(k_len), B, max_q, max_k,
           0.0 if scale is None else float(scale), _addr(dq), _addr(dk), _addr(dv), dqs, dks, dvs,
           0 if given[0] else 1, _addr(workspace), _bytes(workspace), _word(status))
+    if B == 0 and not given[0]:                        # the library does nothing at all without sequences
+        with torch.cuda.stream(stream):
+            for t in (dq, dk, dv):
+                t.zero_()
     return dq, dk, dv
 
 
