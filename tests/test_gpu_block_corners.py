@@ -57,3 +57,45 @@ def test_gradient_of_no_sequences(Tq, Tk, side):
     vit.cross_attn_bwd(q, q, k, k, q, lse, cu, cu, dq=given[0], dk=given[1], dv=given[2], stream=stream)
     torch.cuda.synchronize()
     assert all((t == 7).all() for t in given)
+
+
+def _lists(lengths):
+    return torch.tensor([0] + list(torch.tensor(lengths).cumsum(0)), dtype=torch.int32, device="cuda")
+
+
+def test_gradients_back_to_back_on_one_workspace():
+    """Calls of different lengths that follow one another on one workspace, captured in one graph and replayed
+    without a pause, give the bits of separate calls: none reads the lists or statistics of another."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    Hq, Hk, D = 8, 2, 64
+    calls = []
+    for ql, kl in (([300, 1, 77], [900, 40, 333]), ([5, 200], [64, 1500]), ([1] * 40, [1] * 40), ([513], [2049])):
+        n = lambda T, H: torch.randn(T, H, D, generator=g, device="cuda").bfloat16()
+        q, do, k, v = n(sum(ql), Hq), n(sum(ql), Hq), n(sum(kl), Hk), n(sum(kl), Hk)
+        cq, ck = _lists(ql), _lists(kl)
+        out, lse = vit.cross_attn(q, k, v, cq, ck, max(ql), max(kl), return_lse=True)
+        ref = vit.cross_attn_bwd(do, q, k, v, out, lse, cq, ck, max(ql), max(kl))
+        got = [torch.empty_like(t) for t in (q, k, v)]
+        calls.append(((do, q, k, v, out, lse, cq, ck, max(ql), max(kl)), ref, got))
+    size = max(vit.cross_attn_bwd_workspace_size(a[1].shape[0], a[2].shape[0], Hq, Hk, D, a[6].numel() - 1, a[8], a[9])
+               for a, _, _ in calls)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+
+    def run():
+        for a, _, (dq, dk, dv) in calls:
+            vit.cross_attn_bwd(*a, dq=dq, dk=dk, dv=dv, workspace=ws)
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(30):
+        for _, _, got in calls:
+            for t in got:
+                t.zero_()
+        for _ in range(4):
+            graph.replay()
+        for _, ref, got in calls:
+            for x, y in zip(got, ref):
+                assert torch.equal(x, y)

@@ -16,12 +16,14 @@
 // which is the same kernel: two resident tiles X1, X2, two streamed ones Y1, Y2, S = X1 Y1^T,
 // dP = X2 Y2^T, A1 += dS Y1 and (dk, dv only) A2 += P Y2. Statistics go by the streamed side in the
 // first pass (read from shared memory) and by the row in the second. The passes do not depend on one
-// another: the second may start on SMs that the first has left (programmatic launch). One kernel for
-// both kinds of items was 10 % slower at large sizes (616 against 564 us at 4 x 2048 x 4096, 16 heads
-// of 80: the issuer's loop compiles worse).
+// another and are the two halves of one launch's blocks: those of dq come to SMs as those of dk, dv
+// leave, and all of them wait for the launch that made the lists. (As two launches, the second released
+// early, 532 instead of 541 us at 4 x 2048 x 4096, 16 heads of 80, and 796 of 800 at 128; but there only the
+// first has waited for the lists, and what one launch has waited for is not visible to the next. Both
+// kinds of items in one list, taken by the same blocks, was 10 % slower: the issuer's loop compiles worse.)
 //
-// Measured at 4 x 2048 queries over 4096 keys, 16 heads of 80: dk, dv 317 us, dq 211 us (1.08 and 1.22 PFLOP/s of
-// the products they make), the tensor pipe 43 to 50 % busy: bound by the exchange between the softmax groups and
+// Measured at 4 x 2048 queries over 4096 keys, 16 heads of 80: 541 us (1.11 PFLOP/s of the seven products; in
+// launches of their own dk, dv 317 us, dq 211), the tensor pipe 43 to 50 % busy: bound by the exchange between the softmax groups and
 // the issuer, whose products of one tile and sums of the one before take turns in one pipe, at 1.3 to 1.5 times
 // the time that the MMAs need alone. delta comes from the stored bf16 out, as the interface has no other: where few
 // keys carry a row, dP - delta cancels, and dq and dk are off by 1.6 times what their own rounding is (0.27
@@ -58,8 +60,8 @@ using namespace sm100;
 
 constexpr int kThreads = 384;
 constexpr int kLaunchRegs = 168;
-constexpr int kCtrlRegs = 96;
-constexpr int kSoftmaxRegs = 200;
+constexpr int kCtrlRegs = 88;
+constexpr int kSoftmaxRegs = 208;
 static_assert(128 * kCtrlRegs + 256 * kSoftmaxRegs <= kThreads * kLaunchRegs, "register split exceeds the launch pool");
 constexpr int BM = 128;
 constexpr long long kWaitBudget = 4000000000ll;
@@ -68,7 +70,7 @@ constexpr int kMaxY = 6;
 template <int D, bool DKV> struct GradCfg {
     // Streamed rows per tile: what an MMA of 128 rows costs in shared memory (its A operand) and what a tile costs
     // in hand-overs go down with more of them, so as many as TMEM has room for beside the sums, (512 - sums) / 4,
-    // and shared memory for four ring slots (64 at head_dim 128, with three). 4 x 2048 x 4096, 16 heads: dq at
+    // and shared memory for four ring slots (64 at head_dim 128, with three). A pass alone, 4 x 2048 x 4096, 16 heads: dq at
     // head_dim 80 with 96 rows 211 us, 80 rows 240, 64 rows and three TMEM stages 275; at 64 with 112 rows 173,
     // 80 rows 209; at 96 with 80 rows and four slots 250, 96 rows and three 268; at 128 with 64 rows and three slots
     // 375, 80 rows and two 598. dk, dv at 80 with 80 rows 317, 48 rows and three stages 394.
@@ -110,6 +112,7 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
     return d;
 }
 
+// One pass over its list, by the blocks of a launch that take it.
 struct Grad {
     const GradItem *items;
     const int32_t *n_items;
@@ -120,22 +123,31 @@ struct Grad {
     int64_t out1_stride, out2_stride;
     int Hq, Hk, group, lg_pack;
     float scale, scale_log2;
+    int first_block, n_blocks;
     int32_t *status;
+};
+struct GradMaps {
+    CUtensorMap x1, x2, y1, y2;
+};
+
+template <int D> struct GradShared {
+    Bars bars;
+    uint32_t tmem;
+    volatile int abort;
+    float stat[2][2][GradCfg<D, true>::BN];                // dk, dv: [group][-lse2 | -delta][column]
 };
 
 template <int D, bool DKV>
-__global__ void __launch_bounds__(kThreads, 1)
-cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_constant__ CUtensorMap tm_x2,
-                  const __grid_constant__ CUtensorMap tm_y1, const __grid_constant__ CUtensorMap tm_y2, const Grad p)
+__device__ __forceinline__ void grad_pass(const GradMaps &tm, const Grad &p, GradShared<D> &sh)
 {
     using C = GradCfg<D, DKV>;
     constexpr int BN = C::BN, NY = C::NY, W = C::W;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *base = reinterpret_cast<unsigned char *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    __shared__ Bars bars;
-    __shared__ uint32_t s_tmem;
-    __shared__ volatile int s_abort;
-    __shared__ __align__(16) float s_stat[2][2][BN];       // [group][-lse2 | -delta][column]
+    Bars &bars = sh.bars;
+    uint32_t &s_tmem = sh.tmem;
+    volatile int &s_abort = sh.abort;
+    auto &s_stat = sh.stat;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -164,11 +176,15 @@ cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    // dk, dv: the lists and statistics are there when the launch before this one is done. dq is launched behind
-    // dk, dv, which has waited for them, and waits for that pass only before it ends.
-    if constexpr (DKV) grid_wait();
+    grid_wait();                           // the lists and statistics of the launch before
     grid_release();
-    const int n_items = *p.n_items;
+    // Each role reads the block's place and the list's length for itself: kept from here on, either of them spills.
+    auto block = [&] {
+        uint32_t b;
+        asm volatile("mov.u32 %0, %%ctaid.x;\n" : "=r"(b));
+        return (int)b - p.first_block;
+    };
+    auto list_length = [&] { return *static_cast<const volatile int32_t *>(p.n_items); };
 
     auto wait = [&](const uint64_t &b, uint32_t parity) -> bool {
         if (mbar_wait(bar_addr(b), parity, (const volatile int *)&s_abort, kWaitBudget)) return true;
@@ -196,13 +212,13 @@ cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_consta
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
         if (lane == 0) {
-            tma_prefetch_desc(&tm_x1);
-            tma_prefetch_desc(&tm_x2);
-            tma_prefetch_desc(&tm_y1);
-            tma_prefetch_desc(&tm_y2);
+            tma_prefetch_desc(&tm.x1);
+            tma_prefetch_desc(&tm.x2);
+            tma_prefetch_desc(&tm.y1);
+            tma_prefetch_desc(&tm.y2);
             uint32_t xc = 0, yc = 0;
             bool ok = true;
-            for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
+            for (int i = block(), n_items = list_length(); ok && i < n_items; i += p.n_blocks) {
                 const GradItem it = p.items[i];
                 if (it.j1 <= it.j0) continue;
                 const uint32_t xb = xc & 1;
@@ -211,8 +227,8 @@ cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_consta
 #pragma unroll
                 for (int s = 0; s < C::NS; ++s) {
                     unsigned char *x = base + xb * 2 * C::X_TILE + s * C::X_SLAB;
-                    tma_load_3d(smem_addr(x), &tm_x1, W * s, it.head, it.r0, bar_addr(bars.x_full[xb]));
-                    tma_load_3d(smem_addr(x + C::X_TILE), &tm_x2, W * s, it.head, it.r0, bar_addr(bars.x_full[xb]));
+                    tma_load_3d(smem_addr(x), &tm.x1, W * s, it.head, it.r0, bar_addr(bars.x_full[xb]));
+                    tma_load_3d(smem_addr(x + C::X_TILE), &tm.x2, W * s, it.head, it.r0, bar_addr(bars.x_full[xb]));
                 }
                 ++xc;
                 const int nt = DKV ? (it.ln + y_tok - 1) / y_tok : 0;
@@ -231,8 +247,8 @@ cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_consta
 #pragma unroll
                     for (int c = 0; c < C::NS; ++c) {
                         unsigned char *y = base + C::OFF_Y + s * C::Y_PAIR + c * C::Y_SLAB;
-                        tma_load_3d(smem_addr(y), &tm_y1, W * c, head, row, bar_addr(bars.y_full[s]));
-                        tma_load_3d(smem_addr(y + C::Y_TILE), &tm_y2, W * c, head, row, bar_addr(bars.y_full[s]));
+                        tma_load_3d(smem_addr(y), &tm.y1, W * c, head, row, bar_addr(bars.y_full[s]));
+                        tma_load_3d(smem_addr(y + C::Y_TILE), &tm.y2, W * c, head, row, bar_addr(bars.y_full[s]));
                     }
                 }
             }
@@ -321,7 +337,7 @@ cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_consta
             }
             return true;
         };
-        for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
+        for (int i = block(), n_items = list_length(); ok && i < n_items; i += p.n_blocks) {
             const GradItem it = p.items[i];
             const int n = uni(it.j1 - it.j0);
             if (n <= 0) continue;
@@ -388,8 +404,8 @@ cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_consta
                 for (unsigned todo = __ballot_sync(0xffffffffu, lo < hi); todo; todo &= todo - 1) {
                     const int src = __ffs(todo) - 1;
                     const int end = __shfl_sync(0xffffffffu, hi, src);
-                    for (int64_t r = __shfl_sync(0xffffffffu, lo, src) + (int64_t)(2 * blockIdx.x + warp - 2); r < end;
-                         r += 2 * gridDim.x)
+                    for (int64_t r = __shfl_sync(0xffffffffu, lo, src) + (int64_t)(2 * block() + warp - 2); r < end;
+                         r += 2 * p.n_blocks)
                         for (int c = lane; c < H * (D / 8); c += 32) {
                             const uint4 z = make_uint4(0u, 0u, 0u, 0u);
                             *reinterpret_cast<uint4 *>(p.out1 + r * p.out1_stride + 8 * c) = z;
@@ -407,7 +423,7 @@ cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_consta
         constexpr int PER = (BN + 31) / 32;
         uint32_t u0 = 0;
         bool ok = true;
-        for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
+        for (int i = block(), n_items = list_length(); ok && i < n_items; i += p.n_blocks) {
             const GradItem it = p.items[i];
             const int n = max(0, it.j1 - it.j0);
             if (n == 0) continue;
@@ -452,7 +468,7 @@ cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_consta
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
         uint32_t u0 = 0, xc = 0;                              // tiles and items with tiles before this item
         bool ok = true;
-        for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
+        for (int i = block(), n_items = list_length(); ok && i < n_items; i += p.n_blocks) {
             const GradItem it = p.items[i];
             const int n = max(0, it.j1 - it.j0);
             // the row of the output that this lane holds
@@ -587,7 +603,20 @@ cross_grad_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_consta
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
-    if constexpr (!DKV) grid_wait();       // what follows in the stream waits for this pass, and so for both
+}
+
+// Both passes: the first blocks take dk, dv, the rest dq. They do not depend on one another, and the blocks of the
+// second come to SMs as those of the first leave.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+cross_grad_kernel(const __grid_constant__ GradMaps tm_dkv, const __grid_constant__ GradMaps tm_dq,
+                  const __grid_constant__ Grad dkv, const __grid_constant__ Grad dq)
+{
+    __shared__ __align__(16) GradShared<D> sh;
+    if ((int)blockIdx.x < dkv.n_blocks)
+        grad_pass<D, true>(tm_dkv, dkv, sh);
+    else
+        grad_pass<D, false>(tm_dq, dq, sh);
 }
 
 // ------------------------------------------------------------------ lists and statistics
@@ -741,34 +770,22 @@ bool tile_map(CUtensorMap *m, const void *ptr, int64_t T, int H, int D, int64_t 
     return encode_tiled_map(m, ptr, 3, dims, strides, box, 2 * w);
 }
 
+// A pass's tensor maps and parameters; its blocks are as many as its items at most.
 template <int D, bool DKV>
-cudaError_t launch_pass(const CrossGradArgs &a, const GradPlan &pl, int num_sms, cudaStream_t stream)
+bool make_pass(const CrossGradArgs &a, const GradPlan &pl, int num_sms, GradMaps &m, Grad &p)
 {
     using C = GradCfg<D, DKV>;
     const CrossSegs &s = a.f.segs;
     const int pack = 1 << pl.lg_pack;
-    CUtensorMap q, dq, k, v;              // q and do, then k and v, as the resident or the streamed side
+    // q and do, then k and v, as the resident or the streamed side
     const int qr = DKV ? C::BN : BM, kr = DKV ? BM : C::BN;
+    CUtensorMap &q = DKV ? m.y1 : m.x1, &dout = DKV ? m.y2 : m.x2, &k = DKV ? m.x1 : m.y1, &v = DKV ? m.x2 : m.y2;
     if (!tile_map(&q, a.f.q, s.Tq, a.f.Hq, D, a.f.q_stride, C::W, pack, qr) ||
-        !tile_map(&dq, a.dout, s.Tq, a.f.Hq, D, a.dout_stride, C::W, pack, qr) ||
+        !tile_map(&dout, a.dout, s.Tq, a.f.Hq, D, a.dout_stride, C::W, pack, qr) ||
         !tile_map(&k, a.f.k, s.Tk, a.f.Hk, D, a.f.k_stride, C::W, 1, kr) ||
         !tile_map(&v, a.f.v, s.Tk, a.f.Hk, D, a.f.v_stride, C::W, 1, kr))
-        return cudaErrorInvalidValue;
-    auto kern = cross_grad_kernel<D, DKV>;
-    static DeviceOnce once;
-    cudaError_t e = once.run([&] {
-        cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-        if (r != cudaSuccess) return r;
-        // the setmaxnreg split assumes exactly this launch budget
-        cudaFuncAttributes fa;
-        r = cudaFuncGetAttributes(&fa, kern);
-        if (r != cudaSuccess) return r;
-        return (fa.numRegs != kLaunchRegs || fa.maxThreadsPerBlock < kThreads) ? cudaErrorInvalidConfiguration
-                                                                              : cudaSuccess;
-    });
-    if (e != cudaSuccess) return e;
+        return false;
     char *ws = static_cast<char *>(a.f.workspace);
-    Grad p;
     p.items = reinterpret_cast<const GradItem *>(ws + (DKV ? pl.off_dkv : pl.off_dq));
     p.n_items = reinterpret_cast<const int32_t *>(ws) + (DKV ? 1 : 0);
     p.stats = reinterpret_cast<const float2 *>(ws + pl.off_stats);
@@ -785,12 +802,9 @@ cudaError_t launch_pass(const CrossGradArgs &a, const GradPlan &pl, int num_sms,
     p.segs = s;
     p.zero_rest = a.zero_rest;
     p.status = a.f.status;
-    // zeros are dealt to every SM; an empty pass is launched all the same, for its place in the chain of launches
-    const int64_t list = DKV ? pl.max_dkv : pl.max_dq, most = a.zero_rest ? num_sms : list > 0 ? list : 1;
-    const unsigned blocks = (unsigned)(most < num_sms ? most : num_sms);
-    LaunchScope scope(DKV ? "cross_grad_dkv" : "cross_grad_dq", stream);
-    return DKV ? launch_chained(kern, blocks, kThreads, C::SMEM, stream, k, v, q, dq, p)
-               : launch_chained(kern, blocks, kThreads, C::SMEM, stream, q, dq, k, v, p);
+    const int64_t list = DKV ? pl.max_dkv : pl.max_dq, most = a.zero_rest ? num_sms : list;   // zeros: by every SM
+    p.n_blocks = (int)(most < num_sms ? most : num_sms);
+    return true;
 }
 
 template <int D> cudaError_t launch_d(const CrossGradArgs &a, const GradPlan &pl, int num_sms, cudaStream_t stream)
@@ -831,8 +845,30 @@ template <int D> cudaError_t launch_d(const CrossGradArgs &a, const GradPlan &pl
         if (e != cudaSuccess) return e;
     }
 
-    e = launch_pass<D, true>(a, pl, num_sms, stream);
-    return e != cudaSuccess ? e : launch_pass<D, false>(a, pl, num_sms, stream);
+    GradMaps m_dkv, m_dq;
+    Grad dkv, dq;
+    if (!make_pass<D, true>(a, pl, num_sms, m_dkv, dkv) || !make_pass<D, false>(a, pl, num_sms, m_dq, dq))
+        return cudaErrorInvalidValue;
+    dkv.first_block = 0;
+    dq.first_block = dkv.n_blocks;
+    const int blocks = dkv.n_blocks + dq.n_blocks;
+    if (blocks == 0) return cudaSuccess;
+    constexpr int a1 = GradCfg<D, true>::SMEM, a2 = GradCfg<D, false>::SMEM, smem = a1 > a2 ? a1 : a2;
+    auto kern = cross_grad_kernel<D>;
+    static DeviceOnce once;
+    e = once.run([&] {
+        cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (r != cudaSuccess) return r;
+        // the setmaxnreg split assumes exactly this launch budget
+        cudaFuncAttributes fa;
+        r = cudaFuncGetAttributes(&fa, kern);
+        if (r != cudaSuccess) return r;
+        return (fa.numRegs != kLaunchRegs || fa.maxThreadsPerBlock < kThreads) ? cudaErrorInvalidConfiguration
+                                                                              : cudaSuccess;
+    });
+    if (e != cudaSuccess) return e;
+    LaunchScope scope("cross_grad", stream);
+    return launch_chained(kern, (unsigned)blocks, kThreads, smem, stream, m_dkv, m_dq, dkv, dq);
 }
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }

@@ -77,11 +77,12 @@ struct DeviceOnce {
 };
 
 // Chained launches: a kernel started by launch_chained may begin while the launch before it in the
-// stream still runs (as soon as every block of that one has called grid_release or ended), and must
-// call grid_wait before it touches anything that launch writes, or before it ends. Both are nothing in
-// an ordinary launch. Waiting here is the hardware's, and ends when the launch before has ended. The launch
-// before may be another call's or another library's: a kernel that starts a call waits before it reads anything,
-// and hides only its own start. Pointers of such kernels are not `const __restrict__`: a load through those could
+// stream still runs (as soon as every block of that one has called grid_release or ended). Every such kernel
+// calls grid_wait, in all of its threads, before it reads or writes any memory but its own, and grid_release after
+// that: the wait makes the writes of the launch before visible to the grid that waits and to no other, so a kernel
+// cannot rely on what the launch before it has waited for. Both are nothing in an ordinary launch. Waiting here
+// is the hardware's, and ends when the launch before has ended (and so all launches before that, which it has
+// waited for); that may be another call's or another library's, and what is hidden is a kernel's own start. Pointers of such kernels are not `const __restrict__`: a load through those could
 // be moved before the wait.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
