@@ -37,3 +37,14 @@ def test_each_kernel_waits_before_it_releases(path):
     for i, x in enumerate(lines):
         if "grid_release()" in x:
             assert x == "grid_release();" and i - 1 in waits, lines[i - 1:i + 1]
+
+
+@pytest.mark.parametrize("path", SOURCES, ids=os.path.basename)
+def test_their_pointers_may_change_under_them(path):
+    """A parameter declared __restrict__ lets the compiler load through it before the wait, and through a cache that
+    does not see the writes of the launch before."""
+    kernels = re.split(r"\b__global__\b", "\n".join(code(path)))[1:]
+    for k in kernels:
+        signature, body = k.split("\n{\n", 1)
+        if "grid_wait();" in body:
+            assert "__restrict__" not in signature, signature

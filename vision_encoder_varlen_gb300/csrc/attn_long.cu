@@ -166,6 +166,10 @@ __device__ __forceinline__ int item_q_end(const CrossItem &x) { return x.q1; }
 
 struct NoCross {};                     // the self-attention kernels carry no cross-attention parameters
 
+// A pointer parameter: nothing else writes through the self-attention kernels' pointers while they run; the launch
+// that writes a chained kernel's list may still run when that kernel starts.
+template <bool X, typename T> using Param = std::conditional_t<X, T *, T *__restrict__>;
+
 struct Bars {
     uint64_t q_full[2], q_empty[2], q_ready[2];
     uint64_t k_full[kMaxStages], v_full[kMaxStages], k_empty[kMaxStages], v_empty[kMaxStages];
@@ -208,9 +212,9 @@ template <int D, bool LSE, bool FQ, bool X>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qr,
                  const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_kr,
-                 const __grid_constant__ CUtensorMap tm_v, __nv_bfloat16 *__restrict__ out, int64_t out_stride,
-                 float *__restrict__ lse, int H, float scale_log2, WsHeader *__restrict__ hdr,
-                 const std::conditional_t<X, CrossItem, Item> *__restrict__ items, int32_t *status, int stall_v,
+                 const __grid_constant__ CUtensorMap tm_v, Param<X, __nv_bfloat16> out, int64_t out_stride,
+                 Param<X, float> lse, int H, float scale_log2, Param<X, WsHeader> hdr,
+                 Param<X, const std::conditional_t<X, CrossItem, Item>> items, int32_t *status, int stall_v,
                  const rope::QRope qr, const std::conditional_t<X, CrossLong, NoCross> cx)
 {
     using C = LongCfg<D>;
