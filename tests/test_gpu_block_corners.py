@@ -99,3 +99,83 @@ def test_gradients_back_to_back_on_one_workspace():
         for _, ref, got in calls:
             for x, y in zip(got, ref):
                 assert torch.equal(x, y)
+
+
+def _cross(ql, kl, Hq, Hk, D, seed=0):
+    """q, k, v with rows of no sequence before, behind and around them, and the two lists."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    n = lambda T, H: torch.randn(T, H, D, generator=g, device="cuda").bfloat16()
+    return n(sum(ql) + 9, Hq), n(sum(kl) + 5, Hk), n(sum(kl) + 5, Hk), _lists(ql) + 4, _lists(kl) + 2
+
+
+def _check_rows_without_states(ql, kl, Hq, Hk, D, lse=True):
+    """Zeros and -inf for the sequences without states, the bits of the call without them for the others, and the
+    rows of no sequence as they were."""
+    q, k, v, cq, ck = _cross(ql, kl, Hq, Hk, D)
+    out = torch.full_like(q, 3)
+    l = torch.full(q.shape[:2], 5.0, device="cuda") if lse else None
+    status = vit.new_status()
+    vit.cross_attn(q, k, v, cq, ck, max(ql), max(max(kl), 1), out=out, lse=l, status=status)
+    assert vit.read_status(status) == 0
+    at = [4]
+    for n in ql:
+        at.append(at[-1] + n)
+    inside = torch.zeros(q.shape[0], dtype=torch.bool, device="cuda")
+    inside[at[0]:at[-1]] = True
+    assert (out[~inside] == 3).all() and (not lse or (l[~inside] == 5).all())
+    keep = [i for i, n in enumerate(kl) if n]
+    for i, n in enumerate(kl):
+        if n == 0:
+            rows = slice(at[i], at[i + 1])
+            assert (out[rows] == 0).all() and (not lse or torch.isneginf(l[rows]).all()), i
+    if not keep:
+        return
+    qs = torch.cat([q[at[i]:at[i + 1]] for i in keep])
+    ref, ref_l = vit.cross_attn(qs, k, v, _lists([ql[i] for i in keep]), _lists([kl[i] for i in keep]) + 2,
+                                max(ql), max(kl), return_lse=True)
+    # The other call may cut the keys differently. Each side then rounds P and its result to bf16 (2^-8 of them), so
+    # they are 2 x 2^-8 (max |v| + |out|) apart at most; sums of n <= 2048 exponentials in another order n 2^-24.
+    got = torch.cat([out[at[i]:at[i + 1]] for i in keep])
+    assert ((got.float() - ref.float()).abs() <= 2.0 ** -7 * (v.float().abs().max() + ref.float().abs())).all()
+    if lse:
+        got_l = torch.cat([l[at[i]:at[i + 1]] for i in keep])
+        assert ((got_l - ref_l).abs() <= 2.0 ** -12 + 2.0 ** -22 * ref_l.abs()).all()
+
+
+@pytest.mark.parametrize("lse", [True, False])
+@pytest.mark.parametrize("ql,kl,Hq,Hk,D", [
+    ([300, 257, 64, 500], [700, 0, 1300, 0], 8, 2, 128),          # between and behind others
+    ([40, 1, 333], [0, 0, 900], 4, 4, 80),                        # before them
+    ([1000], [0], 16, 16, 64),                                    # alone
+    ([200, 5, 77], [0, 0, 0], 6, 2, 32),                          # all of them
+    ([64] * 18, [500] * 16 + [0, 0], 16, 16, 80),                 # latents
+    ([70] * 20 + [3] * 20 + [90] * 60, ([300] * 10 + [0] * 10) * 5, 8, 8, 96),   # more than a warp lists
+    ([0, 50, 0, 60], [0, 0, 10, 20], 4, 2, 64),                   # without queries either
+])
+def test_sequences_without_states(ql, kl, Hq, Hk, D, lse):
+    _check_rows_without_states(ql, kl, Hq, Hk, D, lse)
+
+
+@pytest.mark.parametrize("other", [0, 600])
+def test_a_long_sequence_without_states(other):
+    """200 000 rows, behind a prompt and alone."""
+    _check_rows_without_states([200000, 300], [0, other], 8, 2, 64)
+
+
+def test_a_text_only_request_costs_no_more_than_its_zeros():
+    """A prompt without states beside three others: its rows (17 MB of zeros, some microseconds) are written by all
+    SMs beside the others' work, not by one warp at ten times the whole call's time."""
+    def time(ql, kl):
+        q, k, v, cq, ck = _cross(ql, kl, 32, 8, 128)
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+        ms = []
+        for i in range(8):
+            s, e = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            s.record()
+            vit.cross_attn(q, k, v, cq, ck, max(ql), max(kl), out=out, lse=lse)
+            e.record()
+            torch.cuda.synchronize()
+            ms.append(s.elapsed_time(e))
+        return min(ms[2:])
+
+    assert time([2047] * 4, [8000] * 3 + [0]) < 1.5 * time([2047] * 3, [8000] * 3)

@@ -269,13 +269,14 @@ vit_status_t vit_cross_attn(const void *q, const void *k, const void *v, int64_t
     WsHeader *hdr = reinterpret_cast<WsHeader *>(ws);
     CrossItem *items = reinterpret_cast<CrossItem *>(ws + p.off_items);
     CrossTile *tiles = reinterpret_cast<CrossTile *>(ws + p.off_tiles);
+    CrossEmpty *empty = reinterpret_cast<CrossEmpty *>(ws + p.off_empty);
     CrossLong cx{};
     cx.group = Hq / Hkv;
     cx.lg_pack = p.lg_pack;
-    cx.segs = a.segs;
+    cx.empty = empty;
     cx.part_s = reinterpret_cast<float *>(ws + p.off_part_s);
     cx.part_o = reinterpret_cast<float *>(ws + p.off_part_o);
-    cudaError_t e = launch_cross_schedule(a, p, sms, hdr, items, tiles, s);
+    cudaError_t e = launch_cross_schedule(a, p, sms, hdr, items, tiles, empty, s);
     if (e == cudaSuccess) e = launch_cross_long(a, cx, hdr, items, p.max_items, sms, s);
     if (e == cudaSuccess && p.runs > 1) e = launch_cross_tile_join(a, p, cx, hdr, tiles, s);
     return from_cuda(e);

@@ -61,8 +61,8 @@
 // Cross attention (X): queries and keys are rows of different tensors, the items are CrossItem, and a 128-row
 // Q tile holds 128 / P tokens of P query heads that share a key head (one 3-D TMA box per slab), so that
 // grouped heads read K and V once and short query sequences fill the tile. An item may be one of several
-// runs of its keys (fp32 partial results and log2 sums, added up by cross_tile_join_kernel). Warp 3 writes
-// the rows of sequences without keys. Prompts of 700 to 2047 tokens, 32 heads over 8 of 128, over 6404 to
+// runs of its keys (fp32 partial results and log2 sums, added up by cross_tile_join_kernel). The warps 3 of all
+// blocks write the rows of sequences without keys. Prompts of 700 to 2047 tokens, 32 heads over 8 of 128, over 6404 to
 // 16389 states: 0.76 to 0.81 ms, 1.40 to 1.50 PFLOP/s; bound by the exchange between softmax and tensor pipe
 // like the self-attention. 64 latents of 16 images over 256 to 4097 states, 16 heads of 80 (half-filled tiles):
 // 50 to 58 us, 2.8 to 3.3 TB/s; there one item is the longest image's and the list is 1.7 items an SM.
@@ -257,7 +257,7 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         mbar_init(bar_addr(bars.merge), 8);
         for (int r = 0; r < kItemRing; ++r) {
             mbar_init(bar_addr(bars.item_full[r]), 1);
-            mbar_init(bar_addr(bars.item_empty[r]), kItemReaders);
+            mbar_init(bar_addr(bars.item_empty[r]), X ? kItemReaders - 1 : kItemReaders);   // X: not warp 3
         }
         fence_mbar_init();
     }
@@ -670,29 +670,32 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_addr(bars.q_ready[qb]));
             }
-        } else {
-            // cross attention: the query rows of sequences without keys, which have no items
-            if constexpr (X) {
-                for (int b = blockIdx.x; b < cx.segs.B; b += gridDim.x) {
-                    CrossSeg seg;
-                    if (!load_seg(cx.segs, b, seg, nullptr, false) || seg.kn > 0) continue;
-                    const int64_t rows = (int64_t)seg.qn * H;
-                    for (int64_t i = lane; i < rows * (D / 8); i += 32) {
-                        const int64_t r = i / (D / 8), t = seg.q0 + r / H;
-                        const int h = (int)(r % H), c = (int)(i % (D / 8));
-                        *reinterpret_cast<uint4 *>(out + t * out_stride + (int64_t)h * D + 8 * c) =
-                            make_uint4(0u, 0u, 0u, 0u);
-                        if (c == 0 && lse) lse[t * H + h] = -INFINITY;
+        } else if constexpr (X) {
+            // the query rows of sequences without keys, dealt token by token to this warp of every block. It takes no
+            // part in the item ring, so that they hold no item up. (Three prompts of 2047 tokens over 8000 states and
+            // 20000 tokens without: 551 us, 548 without those; by one warp, ring and all, 52 ms.)
+            const int n_empty = hdr->n_empty;
+            int64_t at = blockIdx.x;                     // the block's next row, from the current sequence's first on
+            for (int e0 = 0; e0 < n_empty; e0 += 32) {
+                CrossEmpty mine{0, 0};
+                if (e0 + lane < n_empty) mine = cx.empty[e0 + lane];
+                for (int e = 0; e < min(32, n_empty - e0); ++e) {
+                    const int q0 = __shfl_sync(0xffffffffu, mine.q0, e), qn = __shfl_sync(0xffffffffu, mine.qn, e);
+                    for (; at < qn; at += gridDim.x) {
+                        const int64_t t = q0 + at;
+                        for (int c = lane; c < H * (D / 8); c += 32)
+                            *reinterpret_cast<uint4 *>(out + t * out_stride + 8 * c) = make_uint4(0u, 0u, 0u, 0u);
+                        for (int h = lane; lse && h < H; h += 32) lse[t * H + h] = -INFINITY;
                     }
+                    at -= qn;
                 }
-                __syncwarp();
             }
-            // nothing (else) to do but free its share of every item ring slot
-            if (lane == 0) {
+            __syncwarp();
+        } else if (lane == 0) {
+            // nothing to do but free its share of every item ring slot
             bool ok = true;
             Item item;
             for (uint32_t k = 0; take_item(k, item, false, ok); ++k) {
-            }
             }
         }
     } else if (warp >= 4) {

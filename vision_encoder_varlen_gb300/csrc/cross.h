@@ -87,10 +87,15 @@ struct CrossTile {
     int runs, pad[3];
 };
 
+// The query rows of a sequence without keys, which has no items.
+struct CrossEmpty {
+    int q0, qn;
+};
+
 // What the tcgen05 kernel needs besides the self-attention kernels' parameters.
 struct CrossLong {
     int group, lg_pack;           // query heads per key head; log2 of P
-    CrossSegs segs;
+    const CrossEmpty *empty;      // hdr->n_empty of them
     float *part_o, *part_s;       // [slots][128][D], [slots][128] (log2 of the run's sum)
 };
 
@@ -100,13 +105,13 @@ struct LongPlan {
     int chunk;                    // keys per run (0: keys are not cut)
     int64_t max_items, max_tiles; // bounds of the item list and of the tiles with several runs
     int runs;                     // runs of the longest sequence
-    size_t off_items, off_tiles, off_part_s, off_part_o, bytes;   // workspace layout
+    size_t off_items, off_tiles, off_empty, off_part_s, off_part_o, bytes;   // workspace layout
 };
 LongPlan long_plan(int64_t Tq, int B, int Hq, int Hk, int D, int max_q, int max_k);
 int cross_pack(int group);     // log2 of P
 int attn_long_bn(int D);
 cudaError_t launch_cross_schedule(const CrossArgs &a, const LongPlan &p, int num_sms, WsHeader *hdr, CrossItem *items,
-                                  CrossTile *tiles, cudaStream_t stream);
+                                  CrossTile *tiles, CrossEmpty *empty, cudaStream_t stream);
 cudaError_t launch_cross_long(const CrossArgs &a, const CrossLong &cx, const WsHeader *hdr, const CrossItem *items,
                               int64_t max_items, int num_sms, cudaStream_t stream);
 cudaError_t launch_cross_tile_join(const CrossArgs &a, const LongPlan &p, const CrossLong &cx, const WsHeader *hdr,

@@ -10,6 +10,8 @@
 //     queries over 4096 keys, 16 heads of 80: 169 -> 157 us; ragged batches of several waves gain 0 to 3 %);
 //   - where the sizes bound the batch to at most half as many 128-row tiles as SMs, split items of
 //     one tile and at most `chunk` keys each, whose partial results cross_tile_join adds up.
+// A sequence with queries and no keys has no items; its rows go to a list of their own, from which the tcgen05
+// kernel's idle warps write the zeros.
 // Rows are packed: P query heads that share a key head lie side by side in a tile, so that short
 // query sequences under grouped heads fill it and k and v are read once for all P.
 //
@@ -26,11 +28,11 @@ constexpr int kThreads = kSortThreads;
 
 __global__ void __launch_bounds__(kThreads)
 cross_schedule_kernel(const CrossSegs segs, int Hq, int lg_pack, int chunk, int num_sms, WsHeader *hdr,
-                      CrossItem *items, CrossTile *tiles, int32_t *status)
+                      CrossItem *items, CrossTile *tiles, CrossEmpty *empty, int32_t *status)
 {
     extern __shared__ unsigned long long s_key[];      // [NP]: key count descending, then index; later first item | index
     __shared__ int64_t s_warp[32];
-    __shared__ int s_bad, s_used, s_total, s_tiles, s_all_split, s_more;
+    __shared__ int s_bad, s_used, s_total, s_tiles, s_all_split, s_more, s_empty;
     grid_wait();
     grid_release();
     const int tid = threadIdx.x, B = segs.B;
@@ -54,7 +56,7 @@ cross_schedule_kernel(const CrossSegs segs, int Hq, int lg_pack, int chunk, int 
             const bool fine = tid < B && load_seg(segs, tid, x, status, true);
             // offsets that decrease somewhere could claim more rows than there are: no items at all then
             const bool bad = tid < B && segs.cu_q[tid + 1] < segs.cu_q[tid];
-            const bool use = fine && x.qn > 0 && x.kn > 0;
+            const bool use = fine && x.qn > 0 && x.kn > 0, none = fine && x.qn > 0 && x.kn == 0;
             int64_t full = use ? blocks_of(x, lg_tile + 1) : 0;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) full += __shfl_xor_sync(0xffffffffu, full, o);
@@ -65,17 +67,20 @@ cross_schedule_kernel(const CrossSegs segs, int Hq, int lg_pack, int chunk, int 
             s_key[rank] = ((unsigned long long)at << 32) | (uint32_t)tid;
             s_tile[rank] = tile_at;
             const unsigned used = __ballot_sync(0xffffffffu, use), any_bad = __ballot_sync(0xffffffffu, bad);
+            const unsigned nones = __ballot_sync(0xffffffffu, none);
+            if (none) empty[__popc(nones & ((1u << tid) - 1u))] = CrossEmpty{x.q0, x.qn};
             if (rank == 31) {                          // the last: its sums are all but its own
                 s_total = at + n * runs;
                 s_tiles = tile_at + (runs > 1 ? n : 0);
                 s_used = __popc(used);
+                s_empty = __popc(nones);
                 s_all_split = all_split;
                 s_bad = any_bad != 0;
             }
         }
         __syncthreads();
     } else {
-        if (tid == 0) s_bad = s_used = 0;
+        if (tid == 0) s_bad = s_used = s_empty = 0;
         __syncthreads();
         for (int i = tid; i < NP; i += kThreads) {
             CrossSeg x;
@@ -84,6 +89,7 @@ cross_schedule_kernel(const CrossSegs segs, int Hq, int lg_pack, int chunk, int 
             const bool use = fine && x.qn > 0 && x.kn > 0;
             s_key[i] = key_of(use, x, i);
             if (use) atomicAdd(&s_used, 1);
+            if (fine && x.qn > 0 && x.kn == 0) empty[atomicAdd(&s_empty, 1)] = CrossEmpty{x.q0, x.qn};   // (in any order)
         }
         __syncthreads();
         block_sort(s_key, NP, tid);
@@ -156,7 +162,8 @@ cross_schedule_kernel(const CrossSegs segs, int Hq, int lg_pack, int chunk, int 
     __syncthreads();
     if (tid == 0) {
         hdr->n_long = whole + s_more;
-        hdr->reserved = bad ? 0 : s_tiles;
+        hdr->n_joins = bad ? 0 : s_tiles;
+        hdr->n_empty = bad ? 0 : s_empty;
         hdr->n_tiny = 0;
         hdr->bm_long = 1 << lg_block;
         hdr->tiny_max = 0;
@@ -173,7 +180,7 @@ cross_tile_join_kernel(const WsHeader *hdr, const CrossTile *tiles, const CrossL
                        int64_t out_stride, float *lse, int Hq)
 {
     grid_wait();
-    const int n_tiles = hdr->reserved, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int n_tiles = hdr->n_joins, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n_rows = 16;                             // rows per block: a tile is dealt to 8 blocks
     for (int w = blockIdx.x; w < n_tiles * 8; w += gridDim.x) {
         const CrossTile t = tiles[w >> 3];
@@ -247,7 +254,8 @@ LongPlan long_plan(int64_t Tq, int B, int Hq, int Hk, int D, int max_q, int max_
     }
     p.off_items = sizeof(WsHeader);
     p.off_tiles = up(p.off_items + sizeof(CrossItem) * (size_t)p.max_items);
-    p.off_part_s = up(p.off_tiles + sizeof(CrossTile) * (size_t)p.max_tiles);
+    p.off_empty = up(p.off_tiles + sizeof(CrossTile) * (size_t)p.max_tiles);
+    p.off_part_s = up(p.off_empty + sizeof(CrossEmpty) * (size_t)B);
     const size_t slots = p.runs > 1 ? (size_t)p.max_items : 0;
     p.off_part_o = up(p.off_part_s + slots * 128 * sizeof(float));
     p.bytes = p.off_part_o + slots * 128 * (size_t)D * sizeof(float);
@@ -255,7 +263,7 @@ LongPlan long_plan(int64_t Tq, int B, int Hq, int Hk, int D, int max_q, int max_
 }
 
 cudaError_t launch_cross_schedule(const CrossArgs &a, const LongPlan &p, int num_sms, WsHeader *hdr, CrossItem *items,
-                                  CrossTile *tiles, cudaStream_t stream)
+                                  CrossTile *tiles, CrossEmpty *empty, cudaStream_t stream)
 {
     int np = 32;
     while (np < a.segs.B) np <<= 1;
@@ -268,7 +276,7 @@ cudaError_t launch_cross_schedule(const CrossArgs &a, const LongPlan &p, int num
     if (e != cudaSuccess) return e;
     LaunchScope scope("cross_schedule", stream);
     return launch_chained(cross_schedule_kernel, 1, kThreads, each * np, stream, a.segs, a.Hq, p.lg_pack, p.chunk,
-                          num_sms, hdr, items, tiles, a.status);
+                          num_sms, hdr, items, tiles, empty, a.status);
 }
 
 cudaError_t launch_cross_tile_join(const CrossArgs &a, const LongPlan &p, const CrossLong &cx, const WsHeader *hdr,

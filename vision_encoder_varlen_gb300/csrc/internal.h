@@ -29,14 +29,15 @@ __host__ __device__ inline bool item_split(const Item &it) { return (it.w & kIte
 // Header at the start of the attention workspace, written by the scheduler.
 struct WsHeader {
     int32_t n_long;      // items [0, n_long) go to the long-segment kernel
-    int32_t reserved;    // 0
+    int32_t n_joins;     // cross attention: tiles whose keys were cut into runs
     int32_t bm_long;     // query rows per long item
     int32_t tiny_max;    // segments of at most this many tokens are tiny (one item per head)
     int32_t error;       // device-detected error of the last scheduling pass (0 = none)
     int32_t n_tiny;      // items [n_long, n_long + n_tiny) go to the tiny-segment kernel
     int32_t long_all_split;   // 1 when every long item is a split item of bm_long / 2 rows
     int32_t next_long;   // long items handed out so far beyond each CTA's first (zeroed by the scheduler)
-    int32_t pad[8];
+    int32_t n_empty;     // cross attention: sequences with queries and no keys
+    int32_t pad[7];
 };
 static_assert(sizeof(WsHeader) == 64, "header is 64 bytes");
 

@@ -85,7 +85,7 @@ schedule_kernel(const int32_t *__restrict__ cu_seqlens, const int32_t *__restric
     if (s_err) {
         if (tid == 0) {
             hdr->n_long = 0;
-            hdr->reserved = 0;
+            hdr->n_joins = 0;
             hdr->n_tiny = 0;
             hdr->long_all_split = 0;
             hdr->next_long = 0;
@@ -181,7 +181,7 @@ schedule_kernel(const int32_t *__restrict__ cu_seqlens, const int32_t *__restric
     }
     if (tid == 0) {
         hdr->n_long = (int32_t)total_long;
-        hdr->reserved = 0;
+        hdr->n_joins = 0;
         hdr->n_tiny = (int32_t)(total - total_long);
         hdr->bm_long = 1 << lg_long;
         hdr->tiny_max = sp.tiny_max;
