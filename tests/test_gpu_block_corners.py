@@ -179,3 +179,67 @@ def test_a_text_only_request_costs_no_more_than_its_zeros():
         return min(ms[2:])
 
     assert time([2047] * 4, [8000] * 3 + [0]) < 1.5 * time([2047] * 3, [8000] * 3)
+
+
+def _gradient_into(q, k, v, do, cq, ck, k_len, max_q, max_k, zero_rest, fill=7.0):
+    """The C call on buffers full of `fill`: (status code of the device, dq, dk, dv)."""
+    (Tq, Hq, D), (Tk, Hk, _) = q.shape, k.shape
+    out, lse = vit.cross_attn(q, k, v, cq, ck, max_q, max_k, k_len=k_len, status=vit.new_status(), return_lse=True)
+    g = [torch.full_like(t, fill) for t in (q, k, v)]
+    status = vit.new_status()
+    n = vit.cross_attn_bwd_workspace_size(Tq, Tk, Hq, Hk, D, cq.numel() - 1, max_q, max_k)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    p = lambda t: None if t is None else t.data_ptr()
+    code = vit.lib().vit_cross_attn_bwd(
+        p(do), p(q), p(k), p(v), p(out), p(lse), Tq, Tk, Hq, Hk, D, *[t.stride(0) for t in (do, q, k, v, out)], p(cq),
+        p(ck), p(k_len), cq.numel() - 1, max_q, max_k, 0.0, *[p(t) for t in g], *[t.stride(0) for t in g], zero_rest,
+        p(ws), n, p(status), torch.cuda.current_stream().cuda_stream)
+    assert code == 0
+    torch.cuda.synchronize()
+    return vit.read_status(status), *g
+
+
+@pytest.mark.parametrize("zero_rest", [0, 1])
+@pytest.mark.parametrize("bad,code", [(-5, -10), (130, -10), (101, -11)])
+@pytest.mark.parametrize("at", [0, 1, 2])
+def test_gradient_beside_a_malformed_length(at, bad, code, zero_rest):
+    """Real states per sequence: one wrong entry leaves that sequence's rows as they were, whether or not the rest is
+    cleared, and nobody else's are touched by it. (101 of 120 rows is sound but above the bound of 100.)"""
+    g = torch.Generator(device="cuda").manual_seed(at)
+    n = lambda T, H: torch.randn(T, H, 64, generator=g, device="cuda").bfloat16()
+    q, do, k, v = n(150, 4), n(150, 4), n(400, 2), n(400, 2)
+    cq, ck = _lists([50, 50, 50]), _lists([120, 120, 120]) + 11
+    lens = [100, 33, 77]
+    fine = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    _, *ref = _gradient_into(q, k, v, do, cq, ck, fine, 50, 100, 1, 0.0)
+    lens[at] = bad
+    status, *got = _gradient_into(q, k, v, do, cq, ck, torch.tensor(lens, dtype=torch.int32, device="cuda"), 50, 100,
+                                  zero_rest)
+    assert status == code
+    rest = 0.0 if zero_rest else 7.0
+    for x, y, lo, per in ((got[0], ref[0], 0, 50), (got[1], ref[1], 11, 120), (got[2], ref[2], 11, 120)):
+        want = torch.full_like(x, rest)
+        for b in range(3):
+            rows = slice(lo + b * per, lo + (b + 1) * per)
+            if b == at:
+                want[rows] = 7.0
+            else:
+                real = slice(rows.start, rows.start + (per if per == 50 else lens[b]))
+                want[real] = y[real]
+        # the sound sequences may be left out of such a call; where they are computed they are right
+        for b in range(3):
+            rows = slice(lo + b * per, lo + (b + 1) * per)
+            assert torch.equal(x[rows], want[rows]) or (b != at and (x[rows] == 7.0).all()), (b, per)
+        assert (x[:lo] == rest).all() and (x[lo + 3 * per:] == rest).all()
+
+
+@pytest.mark.parametrize("which", ["q", "k"])
+def test_gradient_with_offsets_that_decrease(which):
+    """Nothing at all is written, the rest included."""
+    q, k = torch.randn(90, 4, 64, device="cuda").bfloat16(), torch.randn(90, 2, 64, device="cuda").bfloat16()
+    good = _lists([30, 20, 10]) + 5
+    wrong = torch.tensor([5, 35, 25, 65], dtype=torch.int32, device="cuda")
+    k_len = torch.tensor([10, 0, 10], dtype=torch.int32, device="cuda")
+    status, *got = _gradient_into(q, k, k, q, wrong if which == "q" else good, wrong if which == "k" else good, k_len,
+                                  90, 90, 1)
+    assert status == -10 and all((t == 7).all() for t in got)

@@ -45,8 +45,6 @@
 // operand (of S and dP, reduced over D) and as an MN-major one (of the sums, reduced over rows).
 // Streamed rows past the sequence's end enter the sums with P = dS = 0 and are zeroed in shared memory
 // first (0 * NaN is NaN), the last 16-row step included.
-#include <limits.h>
-
 #include <type_traits>
 
 #include "block_sort.cuh"
@@ -386,9 +384,9 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const Grad &p, Gra
         }
         __syncwarp();
     } else if (warp < 4) {
-        if (p.zero_rest) {
+        if (p.zero_rest && list_length() >= 0) {
             // the rows between and around the sequences, dealt to both warps of all blocks; gap b lies before sequence
-            // b, and only k_len leaves gaps between sequences
+            // b, and only k_len leaves gaps between sequences (none behind one that is malformed: all its rows stay)
             const CrossSegs &s = p.segs;
             const int64_t T = DKV ? s.Tk : s.Tq;
             const int32_t *cu = DKV ? s.cu_k : s.cu_q, *len = DKV ? s.k_len : nullptr;
@@ -398,7 +396,10 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const Grad &p, Gra
                 int lo = 0, hi = 0;
                 if (g0 + lane < gaps) {
                     hi = b < s.B ? cu[b] : (int)T;
-                    if (b > 0) lo = len ? (int)min((int64_t)cu[b - 1] + len[b - 1], (int64_t)INT_MAX) : cu[b];
+                    if (b > 0) {
+                        CrossSeg x;
+                        lo = len && load_seg(s, b - 1, x, nullptr, false) ? x.k0 + x.kn : cu[b];
+                    }
                     if (lo < 0 || hi > T) hi = lo;
                 }
                 for (unsigned todo = __ballot_sync(0xffffffffu, lo < hi); todo; todo &= todo - 1) {
@@ -691,7 +692,7 @@ __device__ void make_list(bool keys, const CrossSegs &segs, int Hq, int Hk, int 
         __syncthreads();
     }
     const int total = s_bad ? 0 : s_total;
-    if (tid == 0) counts[keys] = total;
+    if (tid == 0) counts[keys] = s_bad ? -1 : total;   // -1: the call is left alone altogether
     for (int i = tid; i < total; i += kThreads) {
         const int p = place_of(s_key, s_used, i), n = i - (int)(s_key[p] >> 32);
         CrossSeg x;
