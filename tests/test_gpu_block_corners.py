@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import vision_encoder_varlen_gb300 as vit
+from test_gpu_cross_attn import check, make, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -243,3 +244,67 @@ def test_gradient_with_offsets_that_decrease(which):
     status, *got = _gradient_into(q, k, k, q, wrong if which == "q" else good, wrong if which == "k" else good, k_len,
                                   90, 90, 1)
     assert status == -10 and all((t == 7).all() for t in got)
+
+
+# keys that take no part because their scores are -inf (an infinite component against a positive one of the queries):
+# the first ones, up to whole tiles and runs; all but the last; every other group of 16
+MINUS = {
+    "first_16": lambda n: slice(0, min(16, n - 1)), "first_64": lambda n: slice(0, min(64, n - 1)),
+    "first_half": lambda n: slice(0, n // 2), "all_but_the_last": lambda n: slice(0, n - 1),
+    "last_half": lambda n: slice((n + 1) // 2, n),
+    "every_other_16": lambda n: [i for i in range(n) if (i // 16) % 2 == 0 and i < n - 1],
+}
+SCORES = [
+    # query lengths, key lengths, Hq, Hkv, D
+    ([1, 2], [37, 3000], 8, 2, 128),          # few rows, keys split and joined
+    ([1], [100000], 2, 1, 64),                # in many runs
+    ([1] * 200, [70] * 200, 8, 8, 80),        # in one
+    ([64], [6000], 2, 2, 80),                 # one tile, keys cut into runs
+    ([300, 130], [900, 113], 4, 2, 96),       # split items
+    ([700] * 6, [500] * 6, 16, 4, 128),       # whole items
+    ([700] * 6, [300] * 6, 16, 16, 64),
+]
+
+
+@pytest.mark.parametrize("ql,kl,Hq,Hk,D", SCORES)
+@pytest.mark.parametrize("where", sorted(MINUS))
+def test_scores_of_minus_infinity(where, ql, kl, Hq, Hk, D):
+    """Such keys have weight 0, wherever they lie: the result is that of the other keys."""
+    q, k, v, cq, ck = make(ql, kl, Hq, Hk, D)
+    q[..., 0] = q[..., 0].abs() + 0.125
+    keep = torch.ones(k.shape[0], dtype=torch.bool, device="cuda")
+    for b, n in enumerate(kl):
+        keep[int(ck[b]):int(ck[b]) + n][MINUS[where](n)] = False
+    k[~keep, :, 0] = -float("inf")
+    kept = torch.cat([torch.zeros(1, dtype=torch.long, device="cuda"), keep.long().cumsum(0)])
+    out, lse = vit.cross_attn(q, k, v, cq, ck, max(ql), max(kl), return_lse=True)
+    check(out, lse, reference(q, k[keep], v[keep], cq, kept[ck.long()].int()))
+
+
+@pytest.mark.parametrize("ql,kl,Hq,Hk,D", SCORES)
+def test_all_scores_minus_infinity(ql, kl, Hq, Hk, D):
+    """0 / 0 and ln 0 by the formulas, in one row; the other rows are as always."""
+    q, k, v, cq, ck = make(ql, kl, Hq, Hk, D)
+    q[..., 0] = 0
+    ref = reference(q, k, v, cq, ck)
+    t = q.shape[0] // 2
+    q[t, 1, 0] = -float("inf")
+    k[..., 0] = 1
+    out, lse = vit.cross_attn(q, k, v, cq, ck, max(ql), max(kl), return_lse=True)
+    assert torch.isnan(out[t, 1]).all() and torch.isneginf(lse[t, 1])
+    rows = torch.ones(out.shape[:2], dtype=torch.bool, device="cuda")
+    rows[t, 1] = False
+    check(out, lse, ref, rows)
+
+
+@pytest.mark.parametrize("ql,kl,Hq,Hk,D", SCORES)
+def test_a_key_of_nan(ql, kl, Hq, Hk, D):
+    """A NaN among the first sequence's keys makes all of its rows NaN, the log-sum-exp too, and no other's."""
+    q, k, v, cq, ck = make(ql, kl, Hq, Hk, D)
+    ref = reference(q, k, v, cq, ck)
+    k[int(ck[0]), :, 3] = float("nan")
+    out, lse = vit.cross_attn(q, k, v, cq, ck, max(ql), max(kl), return_lse=True)
+    n = ql[0]
+    assert torch.isnan(out[:n]).all() and torch.isnan(lse[:n]).all()
+    if len(ql) > 1:
+        check(out, lse, ref, slice(n, None))

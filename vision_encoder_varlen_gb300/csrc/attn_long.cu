@@ -67,6 +67,7 @@
 // like the self-attention. 64 latents of 16 images over 256 to 4097 states, 16 heads of 80 (half-filled tiles):
 // 50 to 58 us, 2.8 to 3.3 TB/s; there one item is the longest image's and the list is 1.7 items an SM.
 #include <cudaTypedefs.h>
+#include <float.h>
 
 #include <type_traits>
 
@@ -765,7 +766,9 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             const int n_kv = (seg_len + BN - 1) / BN;
             // own key tiles: every one, or in a split item every other one starting at this group's
             const int dj = item_split(item) ? 2 : 1;
-            float m_run = -INFINITY, l_run = 0.f;
+            // cross attention begins with a finite maximum, so that scores of -inf have weight 0 also where no other has
+            // come yet (-inf less -inf is NaN; a test of it in each tile cost 3 % at head_dim 80)
+            float m_run = X ? -FLT_MAX : -INFINITY, l_run = 0.f;
 
             for (int j = dj == 2 ? grp : 0; j < n_kv && ok; j += dj) {
                 if (!(ok = wait_warp(bars.s_full[grp], p_cnt & 1))) break;
@@ -927,13 +930,16 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             const float M = oth_has ? fmaxf(m_run, m_oth) : m_run;
             const float w_own = mine ? ex2(m_run - M) : 0.f, w_oth = oth_has ? ex2(m_oth - M) : 0.f;
             const float l_sum = w_own * l_run + w_oth * l_oth;
-            const float inv_l = 1.f / l_sum;
-            const float c0 = (grp ? w_oth : w_own) * inv_l, c1 = (grp ? w_own : w_oth) * inv_l;
-            int q_row, head;
-            bool store = place(item, 0, q_row, head);
+            float inv_l = 1.f / l_sum;
             bool part = false;                                 // one of several key runs: leave a partial result
             if constexpr (X) {
                 part = item.slot >= 0;
+                if (part && l_sum == 0.f) inv_l = 0.f;         // a run of weight 0
+            }
+            const float c0 = (grp ? w_oth : w_own) * inv_l, c1 = (grp ? w_own : w_oth) * inv_l;
+            int q_row, head;
+            bool store = place(item, 0, q_row, head);
+            if constexpr (X) {
                 if (part && store && grp == 0) cx.part_s[(int64_t)item.slot * BM + row] = M + log2f(l_sum);
             }
             if (LSE && store && grp == 0 && !part && (!X || lse))

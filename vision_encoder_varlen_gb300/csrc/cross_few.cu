@@ -210,11 +210,12 @@ cross_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                         grew = true;
                     }
                     float sum = 0.f;
+                    const float base = m_run[h] == -INFINITY ? 0.f : m_run[h];   // scores of -inf: weight 0
 #pragma unroll
                     for (int n = 0; n < 2; ++n)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const float v = wmma16::ex2(fmaf(sc[n][2 * h + e], p.scale_log2, -m_run[h]));
+                            const float v = wmma16::ex2(fmaf(sc[n][2 * h + e], p.scale_log2, -base));
                             pr[n][2 * h + e] = v;
                             sum += v;
                         }
@@ -267,13 +268,11 @@ cross_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 #pragma unroll
             for (int x = 1; x < KQ; ++x) M[h] = fmaxf(M[h], s_m[w0 + x][r]);
             L[h] = 0.f;
-            // a group without keys has m = -inf and l = 0: no weight (also where every group is empty)
+            // a group without keys, or whose scores are all -inf, has m = -inf and l = 0: weight 0
+            const float base = M[h] == -INFINITY ? 0.f : M[h];
 #pragma unroll
-            for (int x = 0; x < KQ; ++x) {
-                const float mx = s_m[w0 + x][r];
-                L[h] += mx == -INFINITY ? 0.f : s_l[w0 + x][r] * wmma16::ex2(mx - M[h]);
-            }
-            const float f = m_run[h] == -INFINITY ? 0.f : wmma16::ex2(m_run[h] - M[h]);
+            for (int x = 0; x < KQ; ++x) L[h] += s_l[w0 + x][r] * wmma16::ex2(s_m[w0 + x][r] - base);
+            const float f = wmma16::ex2(m_run[h] - base);
 #pragma unroll
             for (int j = 0; j < 2 * NK; ++j) {
                 o[j][2 * h] *= f;
@@ -313,7 +312,7 @@ cross_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         if (only) {
             const int64_t tok = seg.q0 + r / p.group;
             const int head = hk * p.group + r % p.group;
-            const float inv = L[h] > 0.f ? 1.f / L[h] : 0.f;  // no key at all: 0, and lse = -inf
+            const float inv = seg.kn > 0 ? 1.f / L[h] : 0.f;  // no key at all: 0, and lse = -inf
             __nv_bfloat16 *dst = p.out + tok * p.out_stride + (int64_t)head * D + 2 * c;
 #pragma unroll
             for (int j = 0; j < 2 * NK; ++j)
@@ -322,7 +321,7 @@ cross_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         } else {
             const int64_t row = (((int64_t)b * p.Hk + hk) * p.n_split + split) * p.rows + r;
             float *dst = p.part_o + row * D + 2 * c;
-            const float inv = 1.f / L[h];                     // a run has at least one key
+            const float inv = L[h] == 0.f ? 0.f : 1.f / L[h];   // every score -inf: a run of weight 0
 #pragma unroll
             for (int j = 0; j < 2 * NK; ++j)
                 *reinterpret_cast<float2 *>(dst + 8 * j) = make_float2(o[j][2 * h] * inv, o[j][2 * h + 1] * inv);
@@ -355,7 +354,8 @@ cross_join_kernel(const Few p)
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) E = fmaxf(E, __shfl_xor_sync(0xffffffffu, E, d));
     const float base = E == -INFINITY ? 0.f : E;
-    float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    const float first = E == -INFINITY && runs > 0 ? NAN : 0.f;   // keys, but no weight: 0 / 0; no keys: 0
+    float sum = 0.f, acc[4] = {first, first, first, first};
     const bool col = lane < D / 4;
 #pragma unroll 4
     for (int s = WIDE ? warp : 0; s < runs; s += WIDE ? 8 : 1) {

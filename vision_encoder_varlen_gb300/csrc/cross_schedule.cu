@@ -192,10 +192,11 @@ cross_tile_join_kernel(const WsHeader *hdr, const CrossTile *tiles, const CrossL
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) E = fmaxf(E, __shfl_xor_sync(0xffffffffu, E, d));
             float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+            const float base = E == -INFINITY ? 0.f : E;
 #pragma unroll 4
             for (int s = 0; s < t.runs; ++s) {
                 const int64_t row = (int64_t)(t.slot + s) * 128 + r;
-                const float x = wmma16::ex2(cx.part_s[row] - E);
+                const float x = wmma16::ex2(cx.part_s[row] - base);
                 sum += x;
                 if (lane < D / 4) {
                     const float4 v = *reinterpret_cast<const float4 *>(cx.part_o + row * D + 4 * lane);
@@ -205,7 +206,7 @@ cross_tile_join_kernel(const WsHeader *hdr, const CrossTile *tiles, const CrossL
                     acc[3] = fmaf(x, v.w, acc[3]);
                 }
             }
-            const float inv = 1.f / sum;
+            const float inv = 1.f / sum;               // (no weight in any run: 0 / 0)
             if (lane < D / 4)
                 *reinterpret_cast<uint2 *>(out + (int64_t)tok * out_stride + (int64_t)head * D + 4 * lane) =
                     make_uint2(wmma16::pack_bf16(acc[0] * inv, acc[1] * inv),
