@@ -514,8 +514,8 @@ size_t vit_cross_attn_workspace_size(int64_t Tq, int64_t Tk, int Hq, int Hkv, in
  * latent queries alike: where there are few query rows the keys are split over the GPU and the parts
  * joined; results do not change from run to run.
  *
- *   q, out       device bf16 [Tq, Hq, D]; k, v device bf16 [Tk, Hkv, D]; Hq a multiple of Hkv;
- *                Tq, Tk <= 2^31 - 2^16. out must not overlap an input.
+ *   q, out       device bf16 [Tq, Hq, D]; k, v device bf16 [Tk, Hkv, D]; Hq a multiple of Hkv, at
+ *                most 65536; Tq, Tk <= 2^31 - 2^16. out must not overlap an input.
  *   cu_q, cu_k   device int32 [B + 1], ascending; rows before cu[0] and from cu[B] on belong to no
  *                sequence: they are not read, and out and lse are left as they were there.
  *   k_len        device int32 [B], or NULL: how many of a sequence's key rows are real (encoder

@@ -308,3 +308,31 @@ def test_a_key_of_nan(ql, kl, Hq, Hk, D):
     assert torch.isnan(out[:n]).all() and torch.isnan(lse[:n]).all()
     if len(ql) > 1:
         check(out, lse, ref, slice(n, None))
+
+
+# ------------------------------------------------------------------ as many heads as a call takes
+
+def test_most_heads():
+    """65536 heads: the bits of calls on a few of them, first and last."""
+    H, D = 65536, 32
+    g = torch.Generator(device="cuda").manual_seed(3)
+    n = lambda T: torch.randn(T, H, D, generator=g, device="cuda").bfloat16()
+    q, do, k, v = n(2), n(2), n(5), n(5)
+    pos = torch.tensor([[1, 7, 3], [0, 2, 100000]], dtype=torch.int32, device="cuda")
+    freq = torch.logspace(0, -4, D // 2, device="cuda")
+    w = torch.ones(2, D, **BF16)
+    cq, ck = _lists([2]), _lists([5])
+    y, _ = vit.qk_norm_mrope(q, None, pos, freq, (6, 5, 5), w)
+    _, yk = vit.qk_norm_mrope(None, q, pos, freq, (6, 5, 5), w)
+    back, _, _ = vit.qk_norm_mrope_bwd(do, None, q, None, pos, freq, (6, 5, 5), w)
+    out, lse = vit.cross_attn(q, k, v, cq, ck, return_lse=True)
+    grad = vit.cross_attn_bwd(do, q, k, v, out, lse, cq, ck)
+    for few in (slice(0, 64), slice(H - 64, H)):
+        a, b, c, d = (t[:, few].contiguous() for t in (q, do, k, v))
+        assert torch.equal(y[:, few], vit.qk_norm_mrope(a, None, pos, freq, (6, 5, 5), w)[0])
+        assert torch.equal(yk[:, few], vit.qk_norm_mrope(None, a, pos, freq, (6, 5, 5), w)[1])
+        assert torch.equal(back[:, few], vit.qk_norm_mrope_bwd(b, None, a, None, pos, freq, (6, 5, 5), w)[0])
+        o, l = vit.cross_attn(a, c, d, cq, ck, return_lse=True)
+        assert torch.equal(out[:, few], o) and torch.equal(lse[:, few], l)
+        for x, ref in zip(grad, vit.cross_attn_bwd(b, a, c, d, o, l, cq, ck)):
+            assert torch.equal(x[:, few], ref)

@@ -13,7 +13,7 @@ namespace {
 bool head_dim_ok(int D) { return D == 32 || D == 64 || D == 80 || D == 96 || D == 128; }
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 bool stride_ok(int64_t s, int64_t n) { return s >= n && s % 8 == 0; }
-bool heads_ok(int H) { return H >= 1 && H <= 65535; }
+bool heads_ok(int H) { return H >= 1 && H <= 65536; }
 vit_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? VIT_OK : VIT_ERR_CUDA; }
 
 constexpr int64_t kMaxTokens = (int64_t)1 << 31;
