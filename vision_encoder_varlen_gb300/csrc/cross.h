@@ -121,11 +121,11 @@ cudaError_t launch_cross_tile_join(const CrossArgs &a, const LongPlan &p, const 
 
 // Work item of a gradient pass. dk, dv: the 128 keys from r0 on (below r1) of key head `head`, over
 // the queries [l0, l0 + ln) of all its heads; dq: the 128 / P tokens from r0 on of P heads, over the
-// keys [l0, l0 + ln). The loop's tiles [j0, j1) are this item's; j0 = j1: nothing to add up.
+// keys [l0, l0 + ln), which are `tiles` steps of the loop (0: nothing to add up).
 struct GradItem {
     int r0, r1, l0, ln;
-    int head, j0, j1;
-    int pad;
+    int head, tiles;
+    int pad[2];
 };
 static_assert(sizeof(GradItem) == 32, "two 16-byte words");
 

@@ -23,9 +23,9 @@
 // kinds of items in one list, taken by the same blocks, was 10 % slower: the issuer's loop compiles worse.)
 //
 // Measured at 4 x 2048 queries over 4096 keys, 16 heads of 80: 541 us (1.11 PFLOP/s of the seven products; in
-// launches of their own dk, dv 317 us, dq 211), the tensor pipe 43 to 50 % busy: bound by the exchange between the softmax groups and
-// the issuer, whose products of one tile and sums of the one before take turns in one pipe, at 1.3 to 1.5 times
-// the time that the MMAs need alone. delta comes from the stored bf16 out, as the interface has no other: where few
+// launches of their own dk, dv 317 us, dq 211), the tensor pipe 43 to 50 % busy: bound by the exchange between the
+// softmax groups and the issuer, whose products of one tile and sums of the one before take turns in one pipe, at
+// 1.3 to 1.5 times the time that the MMAs need alone. delta comes from the stored bf16 out, as the interface has no other: where few
 // keys carry a row, dP - delta cancels, and dq and dk are off by 1.6 times what their own rounding is (0.27
 // against 0.17 % in the 2-norm), in longer rows by 1.4 times, for the rounding of P and dS.
 //
@@ -218,7 +218,7 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const Grad &p, Gra
             bool ok = true;
             for (int i = block(), n_items = list_length(); ok && i < n_items; i += p.n_blocks) {
                 const GradItem it = p.items[i];
-                if (it.j1 <= it.j0) continue;
+                if (it.tiles == 0) continue;
                 const uint32_t xb = xc & 1;
                 if (xc >= 2 && !(ok = wait(bars.x_empty[xb], (xc / 2 - 1) & 1))) break;
                 mbar_arrive_expect_tx(bar_addr(bars.x_full[xb]), 2 * C::X_TILE);
@@ -230,7 +230,7 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const Grad &p, Gra
                 }
                 ++xc;
                 const int nt = DKV ? (it.ln + y_tok - 1) / y_tok : 0;
-                for (int j = it.j0; j < it.j1; ++j, ++yc) {
+                for (int j = 0; j < it.tiles; ++j, ++yc) {
                     const int s = yc % NY;
                     if (yc >= (uint32_t)NY && !(ok = wait(bars.y_empty[s], (yc / NY - 1) & 1))) break;
                     int head, row;
@@ -337,12 +337,12 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const Grad &p, Gra
         };
         for (int i = block(), n_items = list_length(); ok && i < n_items; i += p.n_blocks) {
             const GradItem it = p.items[i];
-            const int n = uni(it.j1 - it.j0);
-            if (n <= 0) continue;
+            const int n = uni(it.tiles);
+            if (n == 0) continue;
             // tiles follow one another inside a head pack; the last one of a pack holds `tail` rows
             const int nt = DKV ? uni((it.ln + y_tok - 1) / y_tok) : uni((it.ln + BN - 1) / BN);
             const int tail = uni(valid_rows(it, nt - 1)), tail_steps = (tail + 15) >> 4;
-            int pj = uni(it.j0 % nt), aj = pj;               // place in its pack of the next tile to start, to add up
+            int pj = 0, aj = 0;                              // place in its pack of the next tile to start, to add up
             auto next_valid = [&]() {
                 const bool end = ++pj == nt;
                 pj = end ? 0 : pj;
@@ -417,50 +417,51 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const Grad &p, Gra
             __syncwarp();
         }
         if constexpr (DKV) {
-        // ------------------------------------------------------------ statistics of the streamed columns
-        // Warp 2 + g stores those of group g's next tile as soon as every warp of the group has finished the one
-        // before (the group's tiles share a TMEM stage, and p_full is their last arrival), read a tile ahead.
-        const int grp = warp - 2;
-        constexpr int PER = (BN + 31) / 32;
-        uint32_t u0 = 0;
-        bool ok = true;
-        for (int i = block(), n_items = list_length(); ok && i < n_items; i += p.n_blocks) {
-            const GradItem it = p.items[i];
-            const int n = max(0, it.j1 - it.j0);
-            if (n == 0) continue;
-            const int nt = (it.ln + y_tok - 1) / y_tok;
-            float2 v[PER];
-            auto fetch = [&](int j) {
-                if (j >= it.j1) return;
-                const int valid = valid_rows(it, j), tok0 = it.l0 + j % nt * y_tok;
-                const int head0 = it.head * p.group + ((j / nt) << p.lg_pack);
+            // ------------------------------------------------------------ statistics of the streamed columns
+            // Warp 2 + g stores those of group g's next tile as soon as every warp of the group has finished the one
+            // before (the group's tiles share a TMEM stage, and p_full is their last arrival), read a tile ahead.
+            const int grp = warp - 2;
+            constexpr int PER = (BN + 31) / 32;
+            uint32_t u0 = 0;
+            bool ok = true;
+            for (int i = block(), n_items = list_length(); ok && i < n_items; i += p.n_blocks) {
+                const GradItem it = p.items[i];
+                const int n = it.tiles;
+                if (n == 0) continue;
+                const int nt = (it.ln + y_tok - 1) / y_tok;
+                float2 v[PER];
+                auto fetch = [&](int j) {
+                    if (j >= n) return;
+                    const int valid = valid_rows(it, j), tok0 = it.l0 + j % nt * y_tok;
+                    const int head0 = it.head * p.group + ((j / nt) << p.lg_pack);
 #pragma unroll
-                for (int e = 0; e < PER; ++e) {
-                    const int c = lane + 32 * e;
-                    v[e] = make_float2(0.f, 0.f);
-                    if (c < valid)
-                        v[e] = p.stats[(int64_t)(tok0 + (c >> p.lg_pack)) * p.Hq + head0 + (c & ((1 << p.lg_pack) - 1))];
-                }
-            };
-            int j = it.j0 + (int)((u0 ^ (uint32_t)grp) & 1);
-            fetch(j);
-            for (; j < it.j1; j += 2) {
-                const uint32_t u = u0 + (j - it.j0);
-                if (u >= 2 && !(ok = wait_warp(bars.p_full[grp], (u / 2 - 1) & 1))) break;
-#pragma unroll
-                for (int e = 0; e < PER; ++e) {
-                    const int c = lane + 32 * e;
-                    if (c < BN) {
-                        s_stat[grp][0][c] = v[e].x;
-                        s_stat[grp][1][c] = v[e].y;
+                    for (int e = 0; e < PER; ++e) {
+                        const int c = lane + 32 * e;
+                        v[e] = make_float2(0.f, 0.f);
+                        if (c < valid)
+                            v[e] = p.stats[(int64_t)(tok0 + (c >> p.lg_pack)) * p.Hq + head0 +
+                                           (c & ((1 << p.lg_pack) - 1))];
                     }
+                };
+                int j = (int)((u0 ^ (uint32_t)grp) & 1);
+                fetch(j);
+                for (; j < n; j += 2) {
+                    const uint32_t u = u0 + j;
+                    if (u >= 2 && !(ok = wait_warp(bars.p_full[grp], (u / 2 - 1) & 1))) break;
+#pragma unroll
+                    for (int e = 0; e < PER; ++e) {
+                        const int c = lane + 32 * e;
+                        if (c < BN) {
+                            s_stat[grp][0][c] = v[e].x;
+                            s_stat[grp][1][c] = v[e].y;
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_addr(bars.stat[grp]));
+                    fetch(j + 2);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_addr(bars.stat[grp]));
-                fetch(j + 2);
+                u0 += n;
             }
-            u0 += n;
-        }
         }
     } else if (warp >= 4) {
         // ------------------------------------------------------------ softmax groups
@@ -471,7 +472,7 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const Grad &p, Gra
         bool ok = true;
         for (int i = block(), n_items = list_length(); ok && i < n_items; i += p.n_blocks) {
             const GradItem it = p.items[i];
-            const int n = max(0, it.j1 - it.j0);
+            const int n = it.tiles;
             // the row of the output that this lane holds
             int o_row, o_head;
             if constexpr (DKV) {
@@ -487,9 +488,8 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const Grad &p, Gra
                 if (exists && n > 0) st_row = p.stats[(int64_t)o_row * p.Hq + o_head];
             }
             const float *nl = s_stat[grp][0], *nd = s_stat[grp][1];
-            const int j_first = it.j0 + (int)((u0 ^ (uint32_t)grp) & 1);
-            for (int j = j_first; j < it.j1; j += 2) {
-                const uint32_t u = u0 + (j - it.j0), st = u & 1;
+            for (int j = (int)((u0 ^ (uint32_t)grp) & 1); j < n; j += 2) {
+                const uint32_t u = u0 + j, st = u & 1;
                 const int valid = valid_rows(it, j);
                 if constexpr (DKV) {
                     if (!(ok = wait_warp(bars.stat[grp], (u / 2) & 1))) break;
@@ -705,9 +705,8 @@ __device__ void make_list(bool keys, const CrossSegs &segs, int Hq, int Hk, int 
         it.l0 = keys ? x.q0 : x.k0;
         it.ln = keys ? x.qn : x.kn;
         it.head = keys ? h : h << lg_pack;
-        it.j0 = 0;
-        it.j1 = (it.ln + step - 1) / step * (keys ? Hq / Hk >> lg_pack : 1);
-        it.pad = 0;
+        it.tiles = (it.ln + step - 1) / step * (keys ? Hq / Hk >> lg_pack : 1);
+        it.pad[0] = it.pad[1] = 0;
         items[i] = it;
     }
 }

@@ -83,8 +83,8 @@ struct DeviceOnce {
 // that: the wait makes the writes of the launch before visible to the grid that waits and to no other, so a kernel
 // cannot rely on what the launch before it has waited for. Both are nothing in an ordinary launch. Waiting here
 // is the hardware's, and ends when the launch before has ended (and so all launches before that, which it has
-// waited for); that may be another call's or another library's, and what is hidden is a kernel's own start. Pointers of such kernels are not `const __restrict__`: a load through those could
-// be moved before the wait.
+// waited for); that may be another call's or another library's, and what is hidden is a kernel's own start. Pointers
+// of such kernels are not `__restrict__`: a load through those could be moved before the wait.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 

@@ -452,7 +452,7 @@ mrope_bwd_kernel(const Mrope p)
             copies_commit();
         };
         RowWalk at = fetch;
-    #pragma unroll
+#pragma unroll
         for (int i = 0; i < AHEAD; ++i) request(i);
         int64_t turned = -1;
         int slot = 0;
