@@ -336,3 +336,59 @@ def test_most_heads():
         assert torch.equal(out[:, few], o) and torch.equal(lse[:, few], l)
         for x, ref in zip(grad, vit.cross_attn_bwd(b, a, c, d, o, l, cq, ck)):
             assert torch.equal(x[:, few], ref)
+
+
+# ------------------------------------------------------------------ the residual gradient's other forms
+
+def _norm_bwd(dz, dh, h, y, gate, w_post, w_pre, dx, dy, dgate, dw_post, dw_pre, scale=0.75, eps=1e-6):
+    """The C call; strides are the tensors' own."""
+    ref = dh if dh is not None else h
+    T, C = ref.shape
+    p = lambda t: None if t is None else t.data_ptr()
+    s = lambda t: 0 if t is None else t.stride(0)
+    n = vit.lib().vit_norm_residual_bwd_workspace_size(C)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    status = vit.new_status()
+    token = gate is not None and gate.dim() == 2
+    code = vit.lib().vit_norm_residual_bwd(
+        p(dz), p(dh), p(h), p(y), p(gate), p(w_post), p(w_pre), p(dx), p(dy), p(dgate), p(dw_post), p(dw_pre), T, C,
+        vit.RES_FP32 if ref.dtype == torch.float32 else vit.RES_BF16, s(dz), s(dh), s(h), s(y),
+        gate.stride(0) if token else 0, s(dx), s(dy), dgate.stride(0) if token and dgate is not None else 0, scale, eps,
+        p(ws), n, p(status), torch.cuda.current_stream().cuda_stream)
+    assert code == 0 and vit.read_status(status) == 0
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("T,C", [(1, 8), (37, 256), (333, 512), (700, 520), (3001, 1280), (450, 4096), (333, 6144), (170, 8192)])
+def test_residual_gradient_in_place_and_in_part(T, C, wide):
+    """dx over dh, dy over y or dz, and any of the sums left out: the bits of the call with tensors of its own."""
+    g = torch.Generator(device="cuda").manual_seed(C + T)
+    n = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    res = (lambda t: t) if wide else (lambda t: t.bfloat16())
+    rows = lambda t: torch.cat([t, torch.full_like(t[:, :16], 9)], 1)[:, :C]      # a stride above the width
+    h, dh, y, dz = rows(res(n(T, C))), rows(res(n(T, C))), rows(n(T, C).bfloat16()), rows(n(T, C).bfloat16())
+    w1, w2 = (1 + 0.2 * n(C)).bfloat16(), (1 + 0.2 * n(C)).bfloat16()
+    for gate in (None, n(C).bfloat16(), rows(n(T, C).bfloat16())):
+        for post, pre, stream in ((w1, w2, True), (w1, None, True), (None, w2, False), (None, None, True), (w1, w2, False)):
+            if pre is None and not stream:
+                continue
+            z, d = dz if pre is not None else None, dh if stream else None
+            dx, dy, dgate, dw_post, dw_pre = vit.norm_residual_bwd(z, d, h, y, gate=gate, w_post=post, w_pre=pre, scale=0.75)
+            same = lambda t: t if t is None else rows(t.clone())
+            # dx over dh; dy over y; the sums one at a time
+            for keep in range(4):
+                d2, y2, z2 = same(d), same(y), same(z)
+                if keep % 2 and z is not None:                # dy over dz
+                    over = z2
+                else:
+                    over = y2
+                out = [None if t is None or i != keep else torch.empty_like(t)
+                       for i, t in enumerate((dgate, dw_post, dw_pre))]
+                x2 = d2 if d2 is not None else torch.empty_like(dx)
+                _norm_bwd(z2, d2, h, y2, gate, post, pre, x2, over, *out)
+                assert torch.equal(x2, dx) and torch.equal(over, dy), (post is None, pre is None, keep)
+                for got, ref in zip(out, (dgate, dw_post, dw_pre)):
+                    assert got is None or torch.equal(got, ref)
+                for t in (x2, over):                          # what lies between the rows
+                    if t.stride(0) > C:
+                        assert (t.as_strided((T - 1, 16), (t.stride(0), 1), t.storage_offset() + C) == 9).all()
