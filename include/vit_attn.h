@@ -557,9 +557,10 @@ size_t vit_cross_attn_bwd_workspace_size(int64_t Tq, int64_t Tk, int Hq, int Hkv
  *   workspace    vit_cross_attn_bwd_workspace_size(...) bytes, 16-byte aligned; calls sharing one
  *                must not overlap.
  * S and dP are recomputed once for dq and once for dk and dv, P and dS rounded to bf16 for their
- * products, sum_d do o formed from the stored out; nothing is added up in memory, so results do not
- * change from run to run. Errors as for vit_cross_attn: all rows of a malformed sequence are left
- * untouched, also with zero_rest, and offsets of either list that decrease leave the whole call uncomputed.
+ * products, sum_d do o formed from the stored out (from the scores in sequences of 2 to 16 keys);
+ * nothing is added up in memory, so results do not change from run to run. Errors as for
+ * vit_cross_attn: all rows of a malformed sequence are left untouched, also with zero_rest, and
+ * offsets of either list that decrease leave the whole call uncomputed.
  */
 vit_status_t vit_cross_attn_bwd(const void *dout, const void *q, const void *k, const void *v, const void *out,
                                 const float *lse, int64_t Tq, int64_t Tk, int Hq, int Hkv, int D, int64_t dout_stride,

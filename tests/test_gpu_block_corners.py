@@ -392,3 +392,56 @@ def test_residual_gradient_in_place_and_in_part(T, C, wide):
                 for t in (x2, over):                          # what lies between the rows
                     if t.stride(0) > C:
                         assert (t.as_strided((T - 1, 16), (t.stride(0), 1), t.storage_offset() + C) == 9).all()
+
+
+# ------------------------------------------------------------------ the gradient over few keys
+
+@pytest.mark.parametrize("ql,kl,Hq,Hk,D", [
+    ([50, 7, 131, 1], [2, 3, 5, 1], 4, 4, 64),
+    ([64] * 6, [1, 2, 4, 8, 15, 16], 8, 1, 128),
+    ([33, 200, 3, 90], [13, 16, 17, 900], 6, 2, 80),              # beside longer ones
+    ([17, 1, 0, 40], [9, 14, 5, 0], 12, 4, 96),
+    ([5] * 100, [1 + i % 16 for i in range(100)], 2, 2, 32),
+    ([1000], [3], 16, 4, 64),
+])
+@pytest.mark.parametrize("padded", [False, True])
+def test_gradient_over_few_keys(ql, kl, Hq, Hk, D, padded):
+    """Over few keys delta nearly cancels dP, so it is taken from the scores and not from the rounded output: dS is off
+    by its own rounding and the fp32 arithmetic alone. With e = 2 (D 2^-24 max sum |q k| scale) + 2^-19 the relative
+    error of every p, and 2 m, m = D 2^-24 sum |do v|, that of dP and delta,
+      |dS err| <= 2^-8 |dS| + (1 + 2^-8) p (2 m + e (|dP| + sum p |dP|)) =: w
+      |dq err| <= 2^-8 |dq| + scale sum_j w |k|, likewise dk."""
+    q, k, v, cq, ck = make(ql, kl, Hq, Hk, D)
+    k_len = None
+    if padded:                                                    # twice the rows, the second half not there
+        wide = [torch.full((2 * t.shape[0], *t.shape[1:]), float("nan"), **BF16) for t in (k, v)]
+        lists = ck.tolist()
+        for a, b in zip(lists[:-1], lists[1:]):
+            for t, w in zip((k, v), wide):
+                w[2 * a:a + b] = t[a:b]
+        k, v = wide
+        k_len, ck = torch.tensor(kl, dtype=torch.int32, device="cuda"), 2 * ck
+    g = torch.Generator(device="cuda").manual_seed(1)
+    do = torch.randn(q.shape, generator=g, device="cuda").bfloat16()
+    out, lse = vit.cross_attn(q, k, v, cq, ck, max(ql), max(kl), k_len=k_len, return_lse=True)
+    dq, dk, _ = vit.cross_attn_bwd(do, q, k, v, out, lse, cq, ck, max(ql), max(kl), k_len=k_len)
+    half, G, scale = 2.0 ** -8, Hq // Hk, D ** -0.5
+    at, of, T = cq.tolist(), ck.tolist(), lambda t: t.transpose(1, 2)
+    for b, n in enumerate(kl):
+        if n == 0 or n > 16 or ql[b] == 0:
+            continue
+        rq, rk = slice(at[b], at[b + 1]), slice(of[b], of[b] + n)
+        Q, DO = (t[rq].double().transpose(0, 1) for t in (q, do))
+        K, V = (t[rk].double().transpose(0, 1).repeat_interleave(G, 0) for t in (k, v))
+        p = torch.softmax(Q @ T(K) * scale, -1)
+        dp = DO @ T(V)
+        ds = p * (dp - (p * dp).sum(-1, keepdim=True))
+        e = 2 * (Q.abs() @ T(K.abs())).amax() * scale * D * 2.0 ** -24 + 2.0 ** -19
+        m = D * 2.0 ** -24 * (DO.abs() @ T(V.abs()))
+        m = m + (p * m).sum(-1, keepdim=True)
+        w = half * ds.abs() + (1 + half) * p * (2 * m + e * (dp.abs() + (p * dp.abs()).sum(-1, keepdim=True)))
+        heads = lambda t: t.reshape(Hk, G, *t.shape[1:]).sum(1).transpose(0, 1)
+        for name, x, y, t in (("dq", dq[rq], scale * (ds @ K).transpose(0, 1), scale * (w @ K.abs()).transpose(0, 1)),
+                              ("dk", dk[rk], heads(scale * T(ds) @ Q), heads(scale * T(w) @ Q.abs()))):
+            err = (x.double() - y).abs() - (half * y.abs() + (1 + half) * t + 2.0 ** -130)
+            assert (err <= 0).all(), f"{name} over {n} keys: {float(err.max()):.3e} past its bound"

@@ -125,7 +125,8 @@ cudaError_t launch_cross_tile_join(const CrossArgs &a, const LongPlan &p, const 
 struct GradItem {
     int r0, r1, l0, ln;
     int head, tiles;
-    int pad[2];
+    int exact;                    // delta from the scores (few keys), else from the stored out
+    int pad;
 };
 static_assert(sizeof(GradItem) == 32, "two 16-byte words");
 

@@ -25,9 +25,14 @@
 // Measured at 4 x 2048 queries over 4096 keys, 16 heads of 80: 541 us (1.11 PFLOP/s of the seven products; in
 // launches of their own dk, dv 317 us, dq 211), the tensor pipe 43 to 50 % busy: bound by the exchange between the
 // softmax groups and the issuer, whose products of one tile and sums of the one before take turns in one pipe, at
-// 1.3 to 1.5 times the time that the MMAs need alone. delta comes from the stored bf16 out, as the interface has no other: where few
-// keys carry a row, dP - delta cancels, and dq and dk are off by 1.6 times what their own rounding is (0.27
-// against 0.17 % in the 2-norm), in longer rows by 1.4 times, for the rounding of P and dS.
+// 1.3 to 1.5 times the time that the MMAs need alone.
+//
+// delta comes from the stored bf16 out, as the interface has no other, except in sequences of 2 to 16 keys: where
+// few keys carry a row, dP - delta cancels and leaves out's rounding. In the 2-norm dq is off by 0.35 % over 2
+// keys, 0.28 over 4, 0.25 over 16 and 0.24 over 32 with delta from out, and by 0.24 % (its own rounding 0.17, that
+// of dS the rest) over any number with delta from the scores. So few keys are one tile of the loop for dq, and one
+// warp's lanes for dk, dv: S and dP are all there. (2000 sequences of 64 queries over 16 keys, 16 heads of 64: 1.31
+// instead of 1.16 ms; over 32 keys, up to which it would go, 1.35 instead of 1.16.)
 //
 // Before them, one launch makes the two item lists (a block each) and the statistics -lse log2(e) and
 // -delta of every (token, head) (the other blocks).
@@ -64,6 +69,7 @@ static_assert(128 * kCtrlRegs + 256 * kSoftmaxRegs <= kThreads * kLaunchRegs, "r
 constexpr int BM = 128;
 constexpr long long kWaitBudget = 4000000000ll;
 constexpr int kMaxY = 6;
+constexpr int kExactKeys = 16;         // sequences of 2 to so many keys have delta from the scores
 
 template <int D, bool DKV> struct GradCfg {
     // Streamed rows per tile: what an MMA of 128 rows costs in shared memory (its A operand) and what a tile costs
@@ -488,77 +494,135 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const Grad &p, Gra
                 if (exists && n > 0) st_row = p.stats[(int64_t)o_row * p.Hq + o_head];
             }
             const float *nl = s_stat[grp][0], *nd = s_stat[grp][1];
-            for (int j = (int)((u0 ^ (uint32_t)grp) & 1); j < n; j += 2) {
-                const uint32_t u = u0 + j, st = u & 1;
-                const int valid = valid_rows(it, j);
-                if constexpr (DKV) {
-                    if (!(ok = wait_warp(bars.stat[grp], (u / 2) & 1))) break;
-                }
-                if (!(ok = wait_warp(bars.s_full[st], (u / 2) & 1))) break;
-                tc_fence_after();
-                const uint32_t tS = t_lane + C::TSTAGE + st * 2 * BN, tD = tS + BN;
-                const uint64_t sc2 = f2_splat(p.scale_log2);
-                const uint64_t nl_row = f2_splat(st_row.x), nd_row = f2_splat(st_row.y);
-                // columns [C0, C0 + CN): P and dS go where columns already read were
-                auto part = [&](auto c0, auto cn) {
-                    constexpr int C0 = decltype(c0)::value, CN = decltype(cn)::value;
-                    uint32_t sr[CN], dr[CN];
-#pragma unroll
-                    for (int c = 0; c < CN; c += 16) tmem_ld16(tS + C0 + c, *reinterpret_cast<uint32_t(*)[16]>(sr + c));
-#pragma unroll
-                    for (int c = 0; c < CN; c += 16) tmem_ld16(tD + C0 + c, *reinterpret_cast<uint32_t(*)[16]>(dr + c));
-                    tmem_wait_ld();
-                    reg_fence(sr);
-                    reg_fence(dr);
-                    [[maybe_unused]] ulonglong2 l4, d4;
-#pragma unroll
-                    for (int c = 0; c < CN; c += 2) {
-                        uint64_t l2 = nl_row, d2 = nd_row;
-                        if constexpr (DKV) {
-                            if (c % 4 == 0) {
-                                l4 = *reinterpret_cast<const ulonglong2 *>(nl + C0 + c);
-                                d4 = *reinterpret_cast<const ulonglong2 *>(nd + C0 + c);
-                            }
-                            l2 = c % 4 == 0 ? l4.x : l4.y;
-                            d2 = c % 4 == 0 ? d4.x : d4.y;
-                        }
-                        float x0, x1;
-                        f2_split(f2_fma(f2_from_u32(sr[c], sr[c + 1]), sc2, l2), x0, x1);
-                        float p0 = ex2(x0), p1 = ex2(x1);
-                        uint64_t pp;
-                        asm("mov.b64 %0, {%1, %2};\n" : "=l"(pp) : "f"(p0), "f"(p1));
-                        float g0, g1;
-                        f2_split(f2_mul(f2_add(f2_from_u32(dr[c], dr[c + 1]), d2), pp), g0, g1);
-                        sr[c / 2] = pack_bf16x2(p0, p1);
-                        dr[c / 2] = pack_bf16x2(g0, g1);
+            // the item's tiles, as it has delta from the scores or not
+            auto tiles = [&](auto exact) {
+                for (int j = (int)((u0 ^ (uint32_t)grp) & 1); j < n; j += 2) {
+                    const uint32_t u = u0 + j, st = u & 1;
+                    const int valid = valid_rows(it, j);
+                    if constexpr (DKV) {
+                        if (!(ok = wait_warp(bars.stat[grp], (u / 2) & 1))) break;
                     }
-                    if (valid < C0 + CN) {                    // columns past the end: exactly 0, whatever was there
+                    if (!(ok = wait_warp(bars.s_full[st], (u / 2) & 1))) break;
+                    tc_fence_after();
+                    const uint32_t tS = t_lane + C::TSTAGE + st * 2 * BN, tD = tS + BN;
+                    if constexpr (decltype(exact)::value) {
+                        // few keys, all of them in this tile: delta = sum_j p_ij dP_ij, in dq over this lane's
+                        // columns, in dk, dv for each column over the lanes of the one warp that has keys (what the
+                        // others make of a delta that is half written goes to rows that do not exist)
+                        auto products = [&](int c0, float row_nl, auto keep, float (&x)[16]) {
+                            uint32_t s[16], d[16];
+                            tmem_ld16(tS + c0, s);
+                            tmem_ld16(tD + c0, d);
+                            tmem_wait_ld();
+                            reg_fence(s);
+                            reg_fence(d);
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) {
+                                const float l = DKV ? nl[c0 + c] : row_nl;
+                                const float pr = ex2(fmaf(__uint_as_float(s[c]), p.scale_log2, l));
+                                const float y = pr * __uint_as_float(d[c]);
+                                x[c] = keep(c0 + c) ? y : 0.f;
+                            }
+                        };
+                        float x[16];
+                        if constexpr (DKV) {
+                            if (quarter == 0) {
+#pragma unroll 1
+                                for (int c0 = 0; c0 < valid; c0 += 16) {
+                                    products(c0, 0.f, [&](int) { return exists; }, x);
+                                    // sums over the lanes by halving: lane l ends with column l / 2
+#pragma unroll
+                                    for (int h = 0; h < 4; ++h)
+#pragma unroll
+                                        for (int i = 0; i < 8 >> h; ++i) {
+                                            const bool up = (lane & (16 >> h)) != 0;
+                                            const float a = x[i], b = x[i + (8 >> h)];
+                                            x[i] = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, 16 >> h);
+                                        }
+                                    x[0] += __shfl_xor_sync(0xffffffffu, x[0], 1);
+                                    if ((lane & 1) == 0) s_stat[grp][1][c0 + (lane >> 1)] = -x[0];
+                                }
+                                __syncwarp();
+                            }
+                        } else {
+                            float sum = 0.f;
+#pragma unroll 1
+                            for (int c0 = 0; c0 < valid; c0 += 16) {
+                                products(c0, st_row.x, [&](int c) { return c < valid; }, x);
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) sum += x[c];
+                            }
+                            st_row.y = -sum;
+                        }
+                    }
+                    const uint64_t sc2 = f2_splat(p.scale_log2);
+                    const uint64_t nl_row = f2_splat(st_row.x), nd_row = f2_splat(st_row.y);
+                    // columns [C0, C0 + CN): P and dS go where columns already read were
+                    auto part = [&](auto c0, auto cn) {
+                        constexpr int C0 = decltype(c0)::value, CN = decltype(cn)::value;
+                        uint32_t sr[CN], dr[CN];
+#pragma unroll
+                        for (int c = 0; c < CN; c += 16)
+                            tmem_ld16(tS + C0 + c, *reinterpret_cast<uint32_t(*)[16]>(sr + c));
+#pragma unroll
+                        for (int c = 0; c < CN; c += 16)
+                            tmem_ld16(tD + C0 + c, *reinterpret_cast<uint32_t(*)[16]>(dr + c));
+                        tmem_wait_ld();
+                        reg_fence(sr);
+                        reg_fence(dr);
+                        [[maybe_unused]] ulonglong2 l4, d4;
 #pragma unroll
                         for (int c = 0; c < CN; c += 2) {
-                            const int x = C0 + c;
-                            const uint32_t keep = x + 1 < valid ? 0xffffffffu : x < valid ? 0x0000ffffu : 0u;
-                            sr[c / 2] &= keep;
-                            dr[c / 2] &= keep;
+                            uint64_t l2 = nl_row, d2 = nd_row;
+                            if constexpr (DKV) {
+                                if (c % 4 == 0) {
+                                    l4 = *reinterpret_cast<const ulonglong2 *>(nl + C0 + c);
+                                    d4 = *reinterpret_cast<const ulonglong2 *>(nd + C0 + c);
+                                }
+                                l2 = c % 4 == 0 ? l4.x : l4.y;
+                                d2 = c % 4 == 0 ? d4.x : d4.y;
+                            }
+                            float x0, x1;
+                            f2_split(f2_fma(f2_from_u32(sr[c], sr[c + 1]), sc2, l2), x0, x1);
+                            float p0 = ex2(x0), p1 = ex2(x1);
+                            uint64_t pp;
+                            asm("mov.b64 %0, {%1, %2};\n" : "=l"(pp) : "f"(p0), "f"(p1));
+                            float g0, g1;
+                            f2_split(f2_mul(f2_add(f2_from_u32(dr[c], dr[c + 1]), d2), pp), g0, g1);
+                            sr[c / 2] = pack_bf16x2(p0, p1);
+                            dr[c / 2] = pack_bf16x2(g0, g1);
                         }
-                    }
-                    if constexpr (DKV) {
+                        if (valid < C0 + CN) {                    // columns past the end: exactly 0, whatever was there
+#pragma unroll
+                            for (int c = 0; c < CN; c += 2) {
+                                const int x = C0 + c;
+                                const uint32_t keep = x + 1 < valid ? 0xffffffffu : x < valid ? 0x0000ffffu : 0u;
+                                sr[c / 2] &= keep;
+                                dr[c / 2] &= keep;
+                            }
+                        }
+                        if constexpr (DKV) {
+#pragma unroll
+                            for (int c = 0; c < CN / 2; c += 8)
+                                tmem_st8(tS + C0 / 2 + c, *reinterpret_cast<const uint32_t(*)[8]>(sr + c));
+                        }
 #pragma unroll
                         for (int c = 0; c < CN / 2; c += 8)
-                            tmem_st8(tS + C0 / 2 + c, *reinterpret_cast<const uint32_t(*)[8]>(sr + c));
-                    }
-#pragma unroll
-                    for (int c = 0; c < CN / 2; c += 8)
-                        tmem_st8(tD + C0 / 2 + c, *reinterpret_cast<const uint32_t(*)[8]>(dr + c));
-                };
-                using std::integral_constant;
-                part(integral_constant<int, 0>(), integral_constant<int, C::PART>());
-                if constexpr (C::PART < BN)
-                    part(integral_constant<int, C::PART>(), integral_constant<int, BN - C::PART>());
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_addr(bars.p_full[st]));
-            }
+                            tmem_st8(tD + C0 / 2 + c, *reinterpret_cast<const uint32_t(*)[8]>(dr + c));
+                    };
+                    using std::integral_constant;
+                    part(integral_constant<int, 0>(), integral_constant<int, C::PART>());
+                    if constexpr (C::PART < BN)
+                        part(integral_constant<int, C::PART>(), integral_constant<int, BN - C::PART>());
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_addr(bars.p_full[st]));
+                }
+            };
+            using std::bool_constant;
+            if (it.exact) tiles(bool_constant<true>());
+            else tiles(bool_constant<false>());
             if (!ok) break;
             u0 += n;
             // ---- the item's sums: group 0 writes dk, group 1 dv; of dq each writes half of the columns
@@ -706,7 +770,8 @@ __device__ void make_list(bool keys, const CrossSegs &segs, int Hq, int Hk, int 
         it.ln = keys ? x.qn : x.kn;
         it.head = keys ? h : h << lg_pack;
         it.tiles = (it.ln + step - 1) / step * (keys ? Hq / Hk >> lg_pack : 1);
-        it.pad[0] = it.pad[1] = 0;
+        it.exact = x.kn > 1 && x.kn <= kExactKeys;     // (one key: out is v, and nothing is lost)
+        it.pad = 0;
         items[i] = it;
     }
 }
