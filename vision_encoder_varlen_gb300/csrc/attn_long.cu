@@ -63,9 +63,9 @@
 // grouped heads read K and V once and short query sequences fill the tile. An item may be one of several
 // runs of its keys (fp32 partial results and log2 sums, added up by cross_tile_join_kernel). The warps 3 of all
 // blocks write the rows of sequences without keys. Prompts of 700 to 2047 tokens, 32 heads over 8 of 128, over 6404 to
-// 16389 states: 0.76 to 0.81 ms, 1.40 to 1.50 PFLOP/s; bound by the exchange between softmax and tensor pipe
+// 16389 states: 0.755 to 0.82 ms, 1.39 to 1.51 PFLOP/s; bound by the exchange between softmax and tensor pipe
 // like the self-attention. 64 latents of 16 images over 256 to 4097 states, 16 heads of 80 (half-filled tiles):
-// 50 to 58 us, 2.8 to 3.3 TB/s; there one item is the longest image's and the list is 1.7 items an SM.
+// 45 to 55 us, 3.0 to 3.6 TB/s; there one item is the longest image's and the list is 1.7 items an SM.
 #include <cudaTypedefs.h>
 #include <float.h>
 
