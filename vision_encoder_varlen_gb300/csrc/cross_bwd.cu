@@ -18,7 +18,7 @@
 // first pass (read from shared memory) and by the row in the second. The passes do not depend on one
 // another and are the two halves of one launch's blocks: those of dq come to SMs as those of dk, dv
 // leave, and all of them wait for the launch that made the lists. (As two launches, the second released
-// early, 532 instead of 541 us at 4 x 2048 x 4096, 16 heads of 80, and 796 of 800 at 128; but there only the
+// early, 532 instead of 541 us at 4 x 2048 x 4096, 16 heads of 80, and 792 instead of 795 at 128; but there only the
 // first has waited for the lists, and what one launch has waited for is not visible to the next. Both
 // kinds of items in one list, taken by the same blocks, was 10 % slower: the issuer's loop compiles worse.)
 //
@@ -74,7 +74,7 @@ constexpr int kExactKeys = 16;         // sequences of 2 to so many keys have de
 template <int D, bool DKV> struct GradCfg {
     // Streamed rows per tile: what an MMA of 128 rows costs in shared memory (its A operand) and what a tile costs
     // in hand-overs go down with more of them, so as many as TMEM has room for beside the sums, (512 - sums) / 4,
-    // and shared memory for four ring slots (64 at head_dim 128, with three). A pass alone, 4 x 2048 x 4096, 16 heads: dq at
+    // and shared memory for four ring slots (64 at head_dim 128, with three). A pass alone, 16 heads, 4 x 2048 x 4096: dq at
     // head_dim 80 with 96 rows 211 us, 80 rows 240, 64 rows and three TMEM stages 275; at 64 with 112 rows 173,
     // 80 rows 209; at 96 with 80 rows and four slots 250, 96 rows and three 268; at 128 with 64 rows and three slots
     // 375, 80 rows and two 598. dk, dv at 80 with 80 rows 317, 48 rows and three stages 394.
@@ -98,7 +98,6 @@ template <int D, bool DKV> struct GradCfg {
     static constexpr int LAYOUT = SW == 128 ? 2 : SW == 64 ? 4 : 6;
     static constexpr int TA1 = 0, TA2 = D, TSTAGE = DKV ? 2 * D : D; // TMEM columns; stage s: S at TSTAGE + 2 BN s, dP BN further
     static_assert(TSTAGE + 4 * BN <= 512, "TMEM budget");
-    static_assert(SMEM + (D == 128 ? 1280 : 1536) <= 227 * 1024, "shared memory per block, with the statistics and barriers");
     static_assert(X_TILE % 1024 == 0 && Y_SLAB % (8 * SW) == 0 && Y_TILE % (8 * SW) == 0, "slabs start on swizzle atoms");
     static_assert(NY <= kMaxY && BN % 16 == 0, "tile shapes");
 };
@@ -138,7 +137,7 @@ template <int D> struct GradShared {
     Bars bars;
     uint32_t tmem;
     volatile int abort;
-    float stat[2][2][GradCfg<D, true>::BN];                // dk, dv: [group][-lse2 | -delta][column]
+    alignas(16) float stat[2][2][GradCfg<D, true>::BN];    // dk, dv: [group][-lse2 | -delta][column]
 };
 
 template <int D, bool DKV>
@@ -677,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 cross_grad_kernel(const __grid_constant__ GradMaps tm_dkv, const __grid_constant__ GradMaps tm_dq,
                   const __grid_constant__ Grad dkv, const __grid_constant__ Grad dq)
 {
-    __shared__ __align__(16) GradShared<D> sh;
+    __shared__ GradShared<D> sh;
     if ((int)blockIdx.x < dkv.n_blocks)
         grad_pass<D, true>(tm_dkv, dkv, sh);
     else
@@ -919,6 +918,7 @@ template <int D> cudaError_t launch_d(const CrossGradArgs &a, const GradPlan &pl
     const int blocks = dkv.n_blocks + dq.n_blocks;
     if (blocks == 0) return cudaSuccess;
     constexpr int a1 = GradCfg<D, true>::SMEM, a2 = GradCfg<D, false>::SMEM, smem = a1 > a2 ? a1 : a2;
+    static_assert(smem + sizeof(GradShared<D>) <= 227 * 1024, "shared memory per block");
     auto kern = cross_grad_kernel<D>;
     static DeviceOnce once;
     e = once.run([&] {
