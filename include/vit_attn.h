@@ -570,6 +570,72 @@ vit_status_t vit_cross_attn_bwd(const void *dout, const void *q, const void *k, 
                                 int64_t dk_stride, int64_t dv_stride, int zero_rest, void *workspace,
                                 size_t workspace_bytes, int32_t *status_dev, vit_stream_t stream);
 
+/* ---- a language model's attention over its own tokens --------------------------------------
+ *
+ * The other half of such a decoder layer: packed sequences over their own keys, those of earlier
+ * tokens (a cache) and of the new ones, under a causal mask that a window may narrow; its gradient;
+ * and sequences that share a long prefix (questions about one image, answers to one document).
+ * Conventions as above.
+ */
+
+/*
+ * Workspace bytes of vit_window_attn for these sizes (0 for invalid ones). max_q, max_k, window and
+ * sinks as for the call.
+ */
+size_t vit_window_attn_workspace_size(int64_t Tq, int64_t Tk, int Hq, int Hkv, int D, int B, int max_q, int max_k,
+                                      int window, int sinks);
+
+/*
+ * Causal attention with a sliding window and the first tokens kept visible. The queries of sequence
+ * b are its last tokens: with n_b keys (k_len[b], or cu_k[b+1] - cu_k[b]) and m_b queries
+ * (cu_q[b+1] - cu_q[b]), query i has position p = n_b - m_b + i and sees the keys j <= p of its
+ * sequence with
+ *   p - j < window   or   j < sinks          (all j <= p where window is 0)
+ *   out[t, h] = softmax_j(scale * <q[t, h], k[j, h / (Hq/Hkv)]>) v[j, h / (Hq/Hkv)]
+ *   lse[t, h] = ln sum_j exp(scale * <q[t, h], k[j, .]>)                 over the keys that it sees
+ * softmax in fp32, P rounded to bf16 for its product with v, fp32 accumulation. A query that sees no
+ * key (fewer keys than queries: its position is negative) gets out = 0 and lse = -inf. Prompts, single
+ * new tokens over a cache and continuations alike; only keys that some query of a tile sees are read.
+ *
+ *   window       >= 0: how many keys a query sees at most, itself included; 0: no window.
+ *   sinks        >= 0: how many first tokens of a sequence every query sees; ignored without a window.
+ *   The other arguments, limits and errors are those of vit_cross_attn; max_k bounds the keys of a
+ *   sequence, seen or not. A value that is not finite in a row of v reaches the queries that see the
+ *   row, and may reach others of its sequence that are computed in one tile with those (128 rows).
+ */
+vit_status_t vit_window_attn(const void *q, const void *k, const void *v, int64_t Tq, int64_t Tk, int Hq, int Hkv,
+                             int D, int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t *cu_q,
+                             const int32_t *cu_k, const int32_t *k_len, int B, int max_q, int max_k, int window,
+                             int sinks, float scale, void *out, int64_t out_stride, float *lse, void *workspace,
+                             size_t workspace_bytes, int32_t *status_dev, vit_stream_t stream);
+
+/* Workspace bytes of vit_prefix_attn for these sizes (0 for invalid ones). */
+size_t vit_prefix_attn_workspace_size(int64_t Tq, int64_t Tp, int64_t Tk, int Hq, int Hkv, int D, int B, int G,
+                                      int max_q, int max_p, int max_k);
+
+/*
+ * Attention of sequences that share prefixes: the sequences [cu_g[g], cu_g[g+1]) of group g see all
+ * of the group's prefix, rows [cu_p[g], cu_p[g+1]) of k_prefix and v_prefix, and behind it their own
+ * keys causally (as vit_window_attn without a window), in one softmax. Where sequences are short the
+ * prefix is read once for the tokens of the whole group; the parts are joined in fp32. A query that
+ * sees no key at all gets out = 0 and lse = -inf.
+ *
+ *   k_prefix, v_prefix  device bf16 [Tp, Hkv, D] (they may be rows of k's and v's storage).
+ *   cu_g         device int32 [G + 1], ascending from 0 to B; NULL with G = 1: all sequences.
+ *   cu_p         device int32 [G + 1], ascending; rows of no group are not read.
+ *   G            1 <= G <= VIT_MAX_SEGMENTS (0 only with B = 0).
+ *   max_p        bound of the prefixes' lengths, 0: Tp.
+ *   The other arguments and errors are those of vit_cross_attn, but where any sequence, group or
+ *   prefix is malformed nothing is computed and the outputs are left untouched.
+ */
+vit_status_t vit_prefix_attn(const void *q, const void *k_prefix, const void *v_prefix, const void *k, const void *v,
+                             int64_t Tq, int64_t Tp, int64_t Tk, int Hq, int Hkv, int D, int64_t q_stride,
+                             int64_t kp_stride, int64_t vp_stride, int64_t k_stride, int64_t v_stride,
+                             const int32_t *cu_q, const int32_t *cu_g, const int32_t *cu_p, const int32_t *cu_k,
+                             const int32_t *k_len, int B, int G, int max_q, int max_p, int max_k, float scale,
+                             void *out, int64_t out_stride, float *lse, void *workspace, size_t workspace_bytes,
+                             int32_t *status_dev, vit_stream_t stream);
+
 /* Storage of the residual stream (vit_norm_residual). */
 enum {
     VIT_RES_BF16 = 0,

@@ -40,6 +40,10 @@ def _declare_block(L):
                                                                                               i64, vp, vp, sz, vp, vp]),
             ("vit_cross_attn_bwd", [vp] * 6 + [i64, i64, i32, i32, i32] + [i64] * 5 + [vp] * 3 + [i32, i32, i32, f32] +
              [vp] * 3 + [i64] * 3 + [i32, vp, sz, vp, vp]),
+            ("vit_window_attn", [vp] * 3 + [i64, i64, i32, i32, i32] + [i64] * 3 + [vp] * 3 + [i32] * 5 +
+             [f32, vp, i64, vp, vp, sz, vp, vp]),
+            ("vit_prefix_attn", [vp] * 5 + [i64] * 3 + [i32] * 3 + [i64] * 5 + [vp] * 5 + [i32] * 5 +
+             [f32, vp, i64, vp, vp, sz, vp, vp]),
             ("vit_norm_residual", [vp] * 7 + [i64, i32, i32] + [i64] * 5 + [f32, f32, vp]),
             ("vit_norm_residual_bwd", [vp] * 12 + [i64, i32, i32] + [i64] * 8 + [f32, f32, vp, sz, vp, vp])):
         fn = getattr(L, name)
@@ -47,6 +51,8 @@ def _declare_block(L):
     for name, args in (("vit_qk_norm_mrope_bwd_workspace_size", [i32]),
                        ("vit_cross_attn_workspace_size", [i64, i64] + [i32] * 6),
                        ("vit_cross_attn_bwd_workspace_size", [i64, i64] + [i32] * 6),
+                       ("vit_window_attn_workspace_size", [i64, i64] + [i32] * 8),
+                       ("vit_prefix_attn_workspace_size", [i64] * 3 + [i32] * 8),
                        ("vit_norm_residual_bwd_workspace_size", [i32])):
         fn = getattr(L, name)
         fn.argtypes, fn.restype = args, sz
@@ -729,6 +735,104 @@ def cross_attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
             for t in (dq, dk, dv):
                 t.zero_()
     return dq, dk, dv
+
+
+def window_attn_workspace_size(Tq: int, Tk: int, Hq: int, Hkv: int, D: int, B: int, max_q: int = 0, max_k: int = 0,
+                               window: int = 0, sinks: int = 0) -> int:
+    return int(lib().vit_window_attn_workspace_size(int(Tq), int(Tk), int(Hq), int(Hkv), int(D), int(B), int(max_q),
+                                                    int(max_k), int(window), int(sinks)))
+
+
+def prefix_attn_workspace_size(Tq: int, Tp: int, Tk: int, Hq: int, Hkv: int, D: int, B: int, G: int, max_q: int = 0,
+                               max_p: int = 0, max_k: int = 0) -> int:
+    return int(lib().vit_prefix_attn_workspace_size(int(Tq), int(Tp), int(Tk), int(Hq), int(Hkv), int(D), int(B),
+                                                    int(G), int(max_q), int(max_p), int(max_k)))
+
+
+def _window(window, sinks):
+    """The C convention: 0 = no window."""
+    if window is not None and window < 1:
+        raise ValueError("window must be at least 1, or None")
+    return 0 if window is None else int(window), int(sinks)
+
+
+def window_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor,
+                max_q: int | None = None, max_k: int | None = None, window: int | None = None, sinks: int = 0,
+                scale: float | None = None, *, k_len: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None, status: torch.Tensor | None = None, return_lse: bool = False,
+                lse: torch.Tensor | None = None, stream=None):
+    """Causal attention of packed sequences over their own tokens: the queries of a sequence, q [Tq, Hq, D], are the
+    last ones of its keys k, v [Tk, Hkv, D] (cu_q, cu_k [B + 1]; k_len [B]: real rows per sequence where a cache is
+    padded). A query at position p sees the keys j <= p with p - j < ``window`` (None: all of them) or j < ``sinks``.
+    Serves prompts, continuations and single tokens over a cache. A query without a key to see (fewer keys than
+    queries) gets zeros and lse = -inf; the rest is as for cross_attn."""
+    Tq, Hq, D = _shape3(q, "q")
+    Tk, Hkv, _ = _shape3(k, "k")
+    dev = _device(q, k, v, cu_q, cu_k, k_len, out, workspace, status, lse)
+    qs, ks, vs = _rows3(q, "q", Tq, Hq, D), _rows3(k, "k", Tk, Hkv, D), _rows3(v, "v", Tk, Hkv, D)
+    B = _cross_lists(cu_q, cu_k, k_len)
+    max_q, max_k = _max_seqlen(max_q), _max_seqlen(max_k)
+    window, sinks = _window(window, sinks)
+    if out is None:
+        out = _new(q, (Tq, Hq, D), _BF16, stream)
+        os_ = Hq * D
+    else:
+        os_ = _rows3(out, "out", Tq, Hq, D)
+    if lse is not None:
+        _lse_ok(lse, Tq, Hq)
+    elif return_lse:
+        lse = _new(q, (Tq, Hq), _F32, stream)
+    if workspace is None:
+        workspace = _scratch(_size("vit_window_attn_workspace_size", Tq, Tk, Hq, Hkv, D, B, max_q, max_k, window,
+                                   sinks), q, stream)
+    _call("vit_window_attn", dev, stream, _addr(q), _addr(k), _addr(v), Tq, Tk, Hq, Hkv, D, qs, ks, vs, _addr(cu_q),
+          _addr(cu_k), _addr(k_len), B, max_q, max_k, window, sinks, 0.0 if scale is None else float(scale),
+          _addr(out), os_, _addr(lse), _addr(workspace), _bytes(workspace), _word(status))
+    return (out, lse) if lse is not None else out
+
+
+def prefix_attn(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                cu_q: torch.Tensor, cu_prefix: torch.Tensor, cu_k: torch.Tensor, cu_group: torch.Tensor | None = None,
+                max_q: int | None = None, max_prefix: int | None = None, max_k: int | None = None,
+                scale: float | None = None, *, k_len: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None, status: torch.Tensor | None = None, return_lse: bool = False,
+                lse: torch.Tensor | None = None, stream=None):
+    """Attention of sequences that share prefixes: the sequences cu_group[g] .. cu_group[g + 1] (None: all of them)
+    see the rows cu_prefix[g] .. cu_prefix[g + 1] of k_prefix, v_prefix [Tp, Hkv, D] and behind them their own keys
+    k, v [Tk, Hkv, D] causally, as in window_attn without a window. The prefix is read once for all of a group's
+    short sequences. ``max_q``, ``max_prefix`` and ``max_k`` bound the lengths (None: Tq, Tp, Tk). A malformed list
+    leaves the whole call uncomputed; the rest is as for window_attn."""
+    Tq, Hq, D = _shape3(q, "q")
+    Tk, Hkv, _ = _shape3(k, "k")
+    Tp = _shape3(k_prefix, "k_prefix")[0]
+    dev = _device(q, k_prefix, v_prefix, k, v, cu_q, cu_prefix, cu_k, cu_group, k_len, out, workspace, status, lse)
+    qs, ks, vs = _rows3(q, "q", Tq, Hq, D), _rows3(k, "k", Tk, Hkv, D), _rows3(v, "v", Tk, Hkv, D)
+    kps, vps = _rows3(k_prefix, "k_prefix", Tp, Hkv, D), _rows3(v_prefix, "v_prefix", Tp, Hkv, D)
+    B = _cross_lists(cu_q, cu_k, k_len)
+    for name, t in (("cu_prefix", cu_prefix), ("cu_group", cu_group)):
+        if t is not None and (t.dtype is not _I32 or t.dim() != 1 or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous CUDA int32 vector")
+    G = cu_prefix.numel() - 1
+    if G < 0 or (cu_group is None and G != 1) or (cu_group is not None and cu_group.numel() != G + 1):
+        raise ValueError("cu_prefix and cu_group must be [G + 1], G = 1 without cu_group")
+    max_q, max_p, max_k = _max_seqlen(max_q), _max_seqlen(max_prefix), _max_seqlen(max_k)
+    if out is None:
+        out = _new(q, (Tq, Hq, D), _BF16, stream)
+        os_ = Hq * D
+    else:
+        os_ = _rows3(out, "out", Tq, Hq, D)
+    if lse is not None:
+        _lse_ok(lse, Tq, Hq)
+    elif return_lse:
+        lse = _new(q, (Tq, Hq), _F32, stream)
+    if workspace is None:
+        workspace = _scratch(_size("vit_prefix_attn_workspace_size", Tq, Tp, Tk, Hq, Hkv, D, B, G, max_q, max_p,
+                                   max_k), q, stream)
+    _call("vit_prefix_attn", dev, stream, _addr(q), _addr(k_prefix), _addr(v_prefix), _addr(k), _addr(v), Tq, Tp, Tk,
+          Hq, Hkv, D, qs, kps, vps, ks, vs, _addr(cu_q), _addr(cu_group), _addr(cu_prefix), _addr(cu_k), _addr(k_len),
+          B, G, max_q, max_p, max_k, 0.0 if scale is None else float(scale), _addr(out), os_, _addr(lse),
+          _addr(workspace), _bytes(workspace), _word(status))
+    return (out, lse) if lse is not None else out
 
 
 RES_BF16, RES_FP32 = 0, 1

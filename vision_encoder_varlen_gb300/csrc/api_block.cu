@@ -5,6 +5,7 @@
 #include "cross.h"
 #include "internal.h"
 #include "trace.h"
+#include "window.h"
 
 using namespace vit;
 
@@ -349,6 +350,161 @@ vit_status_t vit_cross_attn_bwd(const void *dout, const void *q, const void *k, 
     a.dv_stride = dv_stride;
     a.zero_rest = zero_rest != 0;
     return from_cuda(launch_cross_grad(a, grad_plan(Tq, Tk, B, Hq, Hkv, D, max_q, max_k), sms, (cudaStream_t)stream));
+}
+
+// ---- a language model's attention over its own tokens
+
+namespace {
+
+CrossArgs forward_args(const void *q, const void *k, const void *v, int64_t Tq, int64_t Tk, int Hq, int Hkv, int D,
+                       int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t *cu_q, const int32_t *cu_k,
+                       const int32_t *k_len, int B, int max_q, int max_k, float scale, void *out, int64_t out_stride,
+                       float *lse, void *workspace, int32_t *status)
+{
+    CrossArgs a{};
+    a.q = q;
+    a.k = Tk > 0 ? k : q;                       // no keys anywhere: never read, but a map needs an address
+    a.v = Tk > 0 ? v : q;
+    a.k_stride = Tk > 0 ? k_stride : (int64_t)Hkv * D;
+    a.v_stride = Tk > 0 ? v_stride : (int64_t)Hkv * D;
+    a.out = out;
+    a.lse = lse;
+    a.Hq = Hq;
+    a.Hk = Hkv;
+    a.D = D;
+    a.q_stride = q_stride;
+    a.out_stride = out_stride;
+    a.scale_log2 = (scale <= 0.f ? 1.0f / sqrtf((float)D) : scale) * 1.4426950408889634f;
+    a.segs = CrossSegs{cu_q, cu_k, k_len, B, Tq, Tk, max_q, max_k};
+    a.workspace = workspace;
+    a.status = status;
+    return a;
+}
+
+vit_status_t window_sizes(int64_t Tq, int64_t Tk, int Hq, int Hkv, int D, int B, int *max_q, int *max_k, int window,
+                          int *sinks)
+{
+    const vit_status_t st = cross_sizes(Tq, Tk, Hq, Hkv, D, B, max_q, max_k);
+    if (st != VIT_OK) return st;
+    if (window < 0 || *sinks < 0) return VIT_ERR_BAD_ARGUMENT;
+    if (window == 0) *sinks = 0;
+    return VIT_OK;
+}
+
+constexpr int64_t kMaxItems = (int64_t)1 << 31;
+
+}  // namespace
+
+size_t vit_window_attn_workspace_size(int64_t Tq, int64_t Tk, int Hq, int Hkv, int D, int B, int max_q, int max_k,
+                                      int window, int sinks)
+{
+    if (window_sizes(Tq, Tk, Hq, Hkv, D, B, &max_q, &max_k, window, &sinks) != VIT_OK) return 0;
+    if (B == 0 || Tq == 0) return 16;
+    if (window_takes_few(B, Hq, Hkv, D, max_q, max_k, window, sinks)) {
+        const size_t n = window_few_plan(B, Hq, Hkv, D, max_q, max_k, window, sinks).partial_bytes;
+        return n > 16 ? n : 16;
+    }
+    const WinPlan p = win_plan(Tq, B, Hq, Hkv, D, max_q, max_k, window, sinks, 0, 0, 0);
+    return p.max_items >= kMaxItems ? 0 : p.bytes;
+}
+
+vit_status_t vit_window_attn(const void *q, const void *k, const void *v, int64_t Tq, int64_t Tk, int Hq, int Hkv,
+                             int D, int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t *cu_q,
+                             const int32_t *cu_k, const int32_t *k_len, int B, int max_q, int max_k, int window,
+                             int sinks, float scale, void *out, int64_t out_stride, float *lse, void *workspace,
+                             size_t workspace_bytes, int32_t *status_dev, vit_stream_t stream)
+{
+    TraceRange trace("vit_window_attn");
+    vit_status_t st = window_sizes(Tq, Tk, Hq, Hkv, D, B, &max_q, &max_k, window, &sinks);
+    if (st != VIT_OK) return st;
+    if (B == 0 || Tq == 0) return VIT_OK;
+    st = check_cross(q, k, v, Tk, Hq, Hkv, D, q_stride, k_stride, v_stride, cu_q, cu_k, k_len, scale);
+    if (st != VIT_OK) return st;
+    if (!out || !workspace) return VIT_ERR_NULL_POINTER;
+    if (!stride_ok(out_stride, (int64_t)Hq * D)) return VIT_ERR_BAD_STRIDE;
+    if (!aligned16(out) || ((uintptr_t)lse & 3u) || !aligned16(workspace)) return VIT_ERR_MISALIGNED;
+    const size_t need = vit_window_attn_workspace_size(Tq, Tk, Hq, Hkv, D, B, max_q, max_k, window, sinks);
+    if (need == 0) return VIT_ERR_BAD_SHAPE;
+    if (workspace_bytes < need) return VIT_ERR_WORKSPACE_TOO_SMALL;
+    int sms = 0;
+    st = check_device(&sms);
+    if (st != VIT_OK) return st;
+    WinArgs a{};
+    a.f = forward_args(q, k, v, Tq, Tk, Hq, Hkv, D, q_stride, k_stride, v_stride, cu_q, cu_k, k_len, B, max_q, max_k,
+                       scale, out, out_stride, lse, workspace, status_dev);
+    a.window = window;
+    a.sinks = sinks;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (window_takes_few(B, Hq, Hkv, D, max_q, max_k, window, sinks))
+        return from_cuda(launch_window_few(a, window_few_plan(B, Hq, Hkv, D, max_q, max_k, window, sinks), s));
+    return from_cuda(launch_window_tiles(a, win_plan(Tq, B, Hq, Hkv, D, max_q, max_k, window, sinks, 0, 0, 0), sms, s));
+}
+
+// the sizes of a call with prefixes
+static vit_status_t prefix_sizes(int64_t Tq, int64_t Tp, int64_t Tk, int Hq, int Hkv, int D, int B, int G, int *max_q,
+                                 int *max_p, int *max_k)
+{
+    const vit_status_t st = cross_sizes(Tq, Tk, Hq, Hkv, D, B, max_q, max_k);
+    if (st != VIT_OK) return st;
+    if (Tp < 0 || Tp > kMaxRows || G < 0 || (G == 0 && B > 0)) return VIT_ERR_BAD_SHAPE;
+    if (G > VIT_MAX_SEGMENTS) return VIT_ERR_TOO_MANY_SEGMENTS;
+    if (*max_p < 0) return VIT_ERR_BAD_ARGUMENT;
+    if (*max_p == 0 || *max_p > Tp) *max_p = (int)Tp;
+    return VIT_OK;
+}
+
+size_t vit_prefix_attn_workspace_size(int64_t Tq, int64_t Tp, int64_t Tk, int Hq, int Hkv, int D, int B, int G,
+                                      int max_q, int max_p, int max_k)
+{
+    if (prefix_sizes(Tq, Tp, Tk, Hq, Hkv, D, B, G, &max_q, &max_p, &max_k) != VIT_OK) return 0;
+    if (B == 0 || Tq == 0) return 16;
+    const WinPlan p = win_plan(Tq, B, Hq, Hkv, D, max_q, max_k, 0, 0, G, Tp, max_p);
+    return p.max_items >= kMaxItems ? 0 : p.bytes;
+}
+
+vit_status_t vit_prefix_attn(const void *q, const void *k_prefix, const void *v_prefix, const void *k, const void *v,
+                             int64_t Tq, int64_t Tp, int64_t Tk, int Hq, int Hkv, int D, int64_t q_stride,
+                             int64_t kp_stride, int64_t vp_stride, int64_t k_stride, int64_t v_stride,
+                             const int32_t *cu_q, const int32_t *cu_g, const int32_t *cu_p, const int32_t *cu_k,
+                             const int32_t *k_len, int B, int G, int max_q, int max_p, int max_k, float scale,
+                             void *out, int64_t out_stride, float *lse, void *workspace, size_t workspace_bytes,
+                             int32_t *status_dev, vit_stream_t stream)
+{
+    TraceRange trace("vit_prefix_attn");
+    vit_status_t st = prefix_sizes(Tq, Tp, Tk, Hq, Hkv, D, B, G, &max_q, &max_p, &max_k);
+    if (st != VIT_OK) return st;
+    if (B == 0 || Tq == 0) return VIT_OK;
+    st = check_cross(q, k, v, Tk, Hq, Hkv, D, q_stride, k_stride, v_stride, cu_q, cu_k, k_len, scale);
+    if (st != VIT_OK) return st;
+    if (!out || !workspace || !cu_p || (!cu_g && G > 1) || (Tp > 0 && (!k_prefix || !v_prefix)))
+        return VIT_ERR_NULL_POINTER;
+    if (!stride_ok(out_stride, (int64_t)Hq * D) ||
+        (Tp > 0 && (!stride_ok(kp_stride, (int64_t)Hkv * D) || !stride_ok(vp_stride, (int64_t)Hkv * D))))
+        return VIT_ERR_BAD_STRIDE;
+    if (!aligned16(out) || ((uintptr_t)lse & 3u) || !aligned16(workspace) || ((uintptr_t)cu_g & 3u) ||
+        ((uintptr_t)cu_p & 3u) || (Tp > 0 && (!aligned16(k_prefix) || !aligned16(v_prefix))))
+        return VIT_ERR_MISALIGNED;
+    const size_t need = vit_prefix_attn_workspace_size(Tq, Tp, Tk, Hq, Hkv, D, B, G, max_q, max_p, max_k);
+    if (need == 0) return VIT_ERR_BAD_SHAPE;
+    if (workspace_bytes < need) return VIT_ERR_WORKSPACE_TOO_SMALL;
+    int sms = 0;
+    st = check_device(&sms);
+    if (st != VIT_OK) return st;
+    WinArgs a{};
+    a.f = forward_args(q, k, v, Tq, Tk, Hq, Hkv, D, q_stride, k_stride, v_stride, cu_q, cu_k, k_len, B, max_q, max_k,
+                       scale, out, out_stride, lse, workspace, status_dev);
+    a.prefix = true;
+    a.kp = Tp > 0 ? k_prefix : q;
+    a.vp = Tp > 0 ? v_prefix : q;
+    a.kp_stride = Tp > 0 ? kp_stride : (int64_t)Hkv * D;
+    a.vp_stride = Tp > 0 ? vp_stride : (int64_t)Hkv * D;
+    a.Tp = Tp;
+    a.cu_g = cu_g;
+    a.cu_p = cu_p;
+    a.G = G;
+    a.max_p = max_p;
+    return from_cuda(launch_window_tiles(a, win_plan(Tq, B, Hq, Hkv, D, max_q, max_k, 0, 0, G, Tp, max_p), sms,
+                                         (cudaStream_t)stream));
 }
 
 static vit_status_t check_norm(int64_t T, int C, int res_type, const void *gate, int64_t gate_stride, float scale,

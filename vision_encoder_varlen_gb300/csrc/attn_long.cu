@@ -74,6 +74,7 @@
 #include "cross.h"
 #include "internal.h"
 #include "sm100.cuh"
+#include "window.h"
 
 namespace vit {
 namespace {
@@ -164,8 +165,17 @@ __device__ __forceinline__ int item_k0(const CrossItem &x) { return x.k0; }
 __device__ __forceinline__ int item_keys(const CrossItem &x) { return x.kn; }
 __device__ __forceinline__ int item_q0(const CrossItem &x) { return x.q0; }
 __device__ __forceinline__ int item_q_end(const CrossItem &x) { return x.q1; }
+__device__ __forceinline__ int item_k0(const WinItem &x) { return x.k0; }
+__device__ __forceinline__ int item_keys(const WinItem &x) { return x.kn; }
+__device__ __forceinline__ int item_q0(const WinItem &x) { return x.q0; }
+__device__ __forceinline__ int item_q_end(const WinItem &x) { return x.q1; }
 
 struct NoCross {};                     // the self-attention kernels carry no cross-attention parameters
+
+// The tensors of the keys that a windowed item reads first (its sequence's first tokens, or a prefix).
+struct FirstMaps {
+    CUtensorMap k, kr, v;
+};
 
 // A pointer parameter: nothing else writes through the self-attention kernels' pointers while they run; the launch
 // that writes a chained kernel's list may still run when that kernel starts.
@@ -209,17 +219,19 @@ __device__ __forceinline__ void pv_tail(uint32_t tO, uint32_t tP, uint64_t dv, u
     mma_commit(bar_done);
 }
 
-template <int D, bool LSE, bool FQ, bool X>
-__global__ void __launch_bounds__(kThreads, 1)
-attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qr,
-                 const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_kr,
-                 const __grid_constant__ CUtensorMap tm_v, Param<X, __nv_bfloat16> out, int64_t out_stride,
-                 Param<X, float> lse, int H, float scale_log2, Param<X, WsHeader> hdr,
-                 Param<X, const std::conditional_t<X, CrossItem, Item>> items, int32_t *status, int stall_v,
-                 const rope::QRope qr, const std::conditional_t<X, CrossLong, NoCross> cx)
+// The kernel: X for cross attention, and with it W where a query sees part of its sequence.
+template <int D, bool LSE, bool FQ, bool X, bool W>
+__device__ __forceinline__ void
+long_body(const CUtensorMap &tm_q, const CUtensorMap &tm_qr, const CUtensorMap &tm_k, const CUtensorMap &tm_kr,
+          const CUtensorMap &tm_v, Param<X, __nv_bfloat16> out, int64_t out_stride, Param<X, float> lse, int H,
+          float scale_log2, Param<X, WsHeader> hdr,
+          Param<X, const std::conditional_t<W, WinItem, std::conditional_t<X, CrossItem, Item>>> items,
+          int32_t *status, int stall_v, const rope::QRope &qr,
+          const std::conditional_t<W, WinLong, std::conditional_t<X, CrossLong, NoCross>> &cx,
+          const std::conditional_t<W, FirstMaps, NoCross> &tm_f)
 {
     using C = LongCfg<D>;
-    using Item = std::conditional_t<X, CrossItem, vit::Item>;
+    using Item = std::conditional_t<W, WinItem, std::conditional_t<X, CrossItem, vit::Item>>;
     constexpr int BN = C::BN, ST = C::STAGES, NSLAB = C::NSLAB;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *base = reinterpret_cast<unsigned char *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -303,6 +315,21 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         if (!warp_wide || lane == 0) mbar_arrive(bar_addr(bars.item_empty[slot]));
         return item_keys(x) >= 0;
     };
+    // a windowed item's tiles: those of the keys that it reads first, then those of its own range
+    auto first_tiles = [&](const Item &x) -> int {
+        if constexpr (W) return (x.fn + BN - 1) / BN;
+        else return 0;
+    };
+    auto n_tiles = [&](const Item &x) -> int { return first_tiles(x) + (item_keys(x) + BN - 1) / BN; };
+    // keys from tile j's first one to its range's end
+    auto tile_keys = [&](const Item &x, int j) -> int {
+        if constexpr (W) {
+            const int nf = first_tiles(x);
+            return j < nf ? x.fn - j * BN : x.kn - (j - nf) * BN;
+        } else {
+            return item_keys(x) - j * BN;
+        }
+    };
 
     if (warp < 4) regs_dec<FQ ? kCtrlRegsFQ : kCtrlRegs>();
     if (warp == 0) {
@@ -354,13 +381,14 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             // and the K of the tile after next reaches shared memory well before its QK.
             uint32_t v_g = 0;                                // pending V: ring index, first row, head
             int v_row = -1, v_head = 0;
+            const CUtensorMap *v_map = &tm_v;
             auto load_v = [&]() -> bool {
                 const int st = v_g % ST;
                 if (v_g >= (uint32_t)ST && !(ok = wait(bars.v_empty[st], (v_g / ST - 1) & 1))) return false;
                 if (stall_v) return true;       // test hook: V never arrives, the MMA wait expires
                 mbar_arrive_expect_tx(bar_addr(bars.v_full[st]), C::KV_TILE);
                 for (int s = 0; s < NSLAB; ++s)
-                    tma_load_2d(smem_addr(base + C::OFF_V + st * C::KV_TILE + s * C::KV_SLAB), &tm_v,
+                    tma_load_2d(smem_addr(base + C::OFF_V + st * C::KV_TILE + s * C::KV_SLAB), W ? v_map : &tm_v,
                                 v_head * D + 16 * s, v_row, bar_addr(bars.v_full[st]));
                 v_pend = (v_pend & ~(3u << (2 * st))) | ((((v_g / ST) & 1) + 1) << (2 * st));
                 return true;
@@ -382,7 +410,9 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 return true;
             };
             Item kEnd;
-            if constexpr (X)
+            if constexpr (W)
+                kEnd = WinItem{0, 0, 0, -1, 0, 0, 0, 0, -1, 0, 0, 0};
+            else if constexpr (X)
                 kEnd = CrossItem{0, -1, 0, 0, 0, 0, -1, 0};
             else
                 kEnd = make_int4(0, -1, 0, 0);
@@ -392,8 +422,8 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 if (!publish(item)) break;
                 const int it_next = (int)gridDim.x + atomicAdd(&hdr->next_long, 1);
                 const Item nx = it_next < n_items ? items[it_next] : kEnd;
-                const int seg0 = item_k0(item), seg_len = item_keys(item), q0 = item_q0(item), head = item_head(item);
-                const int n_kv = (seg_len + BN - 1) / BN;
+                const int seg0 = item_k0(item), q0 = item_q0(item), head = item_head(item);
+                const int n_kv = n_tiles(item), nf = first_tiles(item);
                 const int kv_head = [&] {
                     if constexpr (X) return head / cx.group;
                     else return head;
@@ -418,15 +448,25 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     }
                     const int st = g % ST;
                     if (g >= (uint32_t)ST && !(ok = wait(bars.k_empty[st], (g / ST - 1) & 1))) break;
-                    const int row = seg0 + j * BN;
+                    int row = seg0 + (j - nf) * BN;
+                    const CUtensorMap *mk = &tm_k, *mkr = &tm_kr, *mv = &tm_v;
+                    if constexpr (W) {
+                        if (j < nf) {
+                            row = item.f0 + j * BN;
+                            mk = &tm_f.k;
+                            mkr = &tm_f.kr;
+                            mv = &tm_f.v;
+                        }
+                    }
                     mbar_arrive_expect_tx(bar_addr(bars.k_full[st]), C::K_TILE);
-                    load_qk_tile(base + C::OFF_K + st * C::K_STRIDE, &tm_k, &tm_kr, BN, kv_head, row,
+                    load_qk_tile(base + C::OFF_K + st * C::K_STRIDE, mk, mkr, BN, kv_head, row,
                                  bar_addr(bars.k_full[st]));
                     k_pend = (k_pend & ~(3u << (2 * st))) | ((((g / ST) & 1) + 1) << (2 * st));
                     if (v_row >= 0 && !load_v()) break;
                     v_g = g;
                     v_row = row;
                     v_head = kv_head;
+                    v_map = mv;
                 }
                 it = it_next;
                 item = nx;
@@ -502,7 +542,7 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             };
 
             for (Item item; take_item(item_cnt, item, false, ok); ++item_cnt) {
-                const int n_kv = (item_keys(item) + BN - 1) / BN;
+                const int n_kv = n_tiles(item);
                 const int n_full = item_keys(item) / BN;                  // tiles with BN keys of the segment
                 uint32_t st = t % ST, ph = (t / ST) & 1;
                 const uint32_t qb = item_cnt % C::QBUF;         // Q buffer of this item
@@ -539,7 +579,7 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         if constexpr (decltype(tail)::value)
                             pv_tail<NSLAB, C::KV_SLAB, D>(tO, tP, dv0 + st * STAGE_STEP,
                                                           base + C::OFF_V + st * C::KV_TILE, j > 0 ? 1u : 0u,
-                                                          item_keys(item) - j * BN, a_pvdone);
+                                                          tile_keys(item, j), a_pvdone);
                         else
                             pv(dv0 + st * STAGE_STEP, j > 0 ? 1u : 0u);
                         mma_commit(bar_addr(bars.v_empty[st]));
@@ -547,9 +587,15 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         ph = ph1;
                         return true;
                     };
-                    for (int j = 0; j < n_full; ++j)
-                        if (!step(j, std::false_type{})) break;
-                    if (ok && n_full < n_kv) step(n_full, std::true_type{});
+                    if constexpr (W) {                             // either range may end inside a tile
+                        for (int j = 0; j < n_kv; ++j)
+                            if (!(tile_keys(item, j) >= BN ? step(j, std::false_type{}) : step(j, std::true_type{})))
+                                break;
+                    } else {
+                        for (int j = 0; j < n_full; ++j)
+                            if (!step(j, std::false_type{})) break;
+                        if (ok && n_full < n_kv) step(n_full, std::true_type{});
+                    }
                     t += n_kv;
                     c += n_kv;
                     continue;
@@ -568,12 +614,12 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     if (!(ok = wait(b_pfull, prev_c & 1))) return false;
                     tc_fence_after();
                     const uint32_t acc = first_pv ? 0u : 1u;
-                    if (prev_j < n_full)
+                    if (W ? tile_keys(item, prev_j) >= BN : prev_j < n_full)
                         pv(dv0 + prev_st * STAGE_STEP, acc);
                     else
                         pv_tail<NSLAB, C::KV_SLAB, D>(tO, tP, dv0 + prev_st * STAGE_STEP,
                                                       base + C::OFF_V + prev_st * C::KV_TILE, acc,
-                                                      item_keys(item) - prev_j * BN, a_pvdone);
+                                                      tile_keys(item, prev_j), a_pvdone);
                     mma_commit(bar_addr(bars.v_empty[prev_st]));
                     first_pv = false;
                     return true;
@@ -762,8 +808,7 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             return tok < item_q_end(item);
         };
         for (Item item; take_item(item_cnt, item, true, ok); ++item_cnt) {
-            const int seg_len = item_keys(item);
-            const int n_kv = (seg_len + BN - 1) / BN;
+            const int n_kv = n_tiles(item);
             // own key tiles: every one, or in a split item every other one starting at this group's
             const int dj = item_split(item) ? 2 : 1;
             // cross attention begins with a finite maximum, so that scores of -inf have weight 0 also where no other has
@@ -786,8 +831,26 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 // the previous P.V of this tile has almost always finished by now: probe it
                 // without blocking, so its barrier latency overlaps the arithmetic below
                 const bool pv_probe = p_cnt == 0 || mbar_test(bar_addr(bars.pv_done[grp]), (p_cnt - 1) & 1);
-                const int kv_valid = seg_len - j * BN;         // keys of this tile inside the segment
-                if (kv_valid < BN) {
+                const int kv_valid = tile_keys(item, j);       // keys of this tile inside the segment
+                if constexpr (W) {
+                    // what this row sees of the tile: columns up to `hi`, from `lo` on or before `sk`
+                    int hi = min(kv_valid, BN) - 1, lo = 0, sk = 0;
+                    const int nf = first_tiles(item);
+                    if (j >= nf) {
+                        const int kp = item.kp + (j - nf) * BN;
+                        const int d = item.p0 - kp + (dj == 1 ? grp * (BM >> cx.lg_pack) : 0) + (row >> cx.lg_pack);
+                        hi = min(hi, d);
+                        if (cx.window > 0) {
+                            lo = d - cx.window + 1;
+                            sk = cx.sinks - kp;
+                        }
+                    }
+                    if (__any_sync(0xffffffffu, hi < BN - 1 || lo > 0)) {
+#pragma unroll
+                        for (int c = 0; c < BN; ++c)
+                            if (c > hi || (c < lo && c >= sk)) sr[c] = __float_as_uint(-INFINITY);
+                    }
+                } else if (kv_valid < BN) {
 #pragma unroll
                     for (int c = 0; c < BN; ++c)
                         if (c >= kv_valid) sr[c] = __float_as_uint(-INFINITY);
@@ -992,6 +1055,31 @@ attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
 }
 
+template <int D, bool LSE, bool FQ, bool X>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qr,
+                 const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_kr,
+                 const __grid_constant__ CUtensorMap tm_v, Param<X, __nv_bfloat16> out, int64_t out_stride,
+                 Param<X, float> lse, int H, float scale_log2, Param<X, WsHeader> hdr,
+                 Param<X, const std::conditional_t<X, CrossItem, Item>> items, int32_t *status, int stall_v,
+                 const rope::QRope qr, const std::conditional_t<X, CrossLong, NoCross> cx)
+{
+    long_body<D, LSE, FQ, X, false>(tm_q, tm_qr, tm_k, tm_kr, tm_v, out, out_stride, lse, H, scale_log2, hdr, items,
+                                    status, stall_v, qr, cx, NoCross{});
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+window_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qr,
+                   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_kr,
+                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ FirstMaps tm_f,
+                   __nv_bfloat16 *out, int64_t out_stride, float *lse, int H, float scale_log2, WsHeader *hdr,
+                   const WinItem *items, int32_t *status, const __grid_constant__ WinLong cx)
+{
+    long_body<D, true, false, true, true>(tm_q, tm_qr, tm_k, tm_kr, tm_v, out, out_stride, lse, H, scale_log2, hdr,
+                                          items, status, 0, rope::QRope{}, cx, tm_f);
+}
+
 // ------------------------------------------------------------------ host side
 
 // [T, H*D] bf16 rows with a token stride, read as boxes of `cols` columns x `rows` rows with the
@@ -1080,7 +1168,57 @@ cudaError_t launch_cross_d(const CrossArgs &a, const CrossLong &cx, const WsHead
                           const_cast<WsHeader *>(hdr), items, a.status, 0, rope::QRope{}, cx);
 }
 
+template <int D>
+cudaError_t launch_window_d(const WinArgs &a, const WinLong &cx, const WsHeader *hdr, const WinItem *items,
+                            int64_t max_items, int num_sms, cudaStream_t stream)
+{
+    using C = LongCfg<D>;
+    const int rem = C::REM > 0 ? C::REM : 64, wide = D >= 64 ? 64 : rem;   // the wide maps of head_dim 32 go unused
+    const CrossArgs &f = a.f;
+    const CrossSegs &s = f.segs;
+    const int pack = 1 << cx.lg_pack;
+    CUtensorMap mq, mqr, mk, mkr, mv;
+    FirstMaps first;
+    if (!make_packed_map(&mq, f.q, s.Tq, f.Hq, D, f.q_stride, pack, wide) ||
+        !make_packed_map(&mqr, f.q, s.Tq, f.Hq, D, f.q_stride, pack, rem) ||
+        !make_map(&mk, f.k, s.Tk, f.Hk, D, f.k_stride, C::BN, wide) ||
+        !make_map(&mkr, f.k, s.Tk, f.Hk, D, f.k_stride, C::BN, rem) ||
+        !make_map(&mv, f.v, s.Tk, f.Hk, D, f.v_stride, C::BN, 16))
+        return cudaErrorInvalidValue;
+    if (a.prefix) {
+        if (!make_map(&first.k, a.kp, a.Tp, f.Hk, D, a.kp_stride, C::BN, wide) ||
+            !make_map(&first.kr, a.kp, a.Tp, f.Hk, D, a.kp_stride, C::BN, rem) ||
+            !make_map(&first.v, a.vp, a.Tp, f.Hk, D, a.vp_stride, C::BN, 16))
+            return cudaErrorInvalidValue;
+    } else {
+        first = FirstMaps{mk, mkr, mv};
+    }
+    auto kern = window_long_kernel<D>;
+    static DeviceOnce once;
+    cudaError_t e = once.run([&] { return set_up(kern, C::SMEM); });
+    if (e != cudaSuccess) return e;
+    const unsigned blocks = (unsigned)(max_items < num_sms ? max_items : num_sms);
+    if (blocks == 0) return cudaSuccess;
+    LaunchScope scope("window_long", stream);
+    return launch_chained(kern, blocks, kThreads, C::SMEM, stream, mq, mqr, mk, mkr, mv, first,
+                          static_cast<__nv_bfloat16 *>(f.out), f.out_stride, f.lse, f.Hq, f.scale_log2,
+                          const_cast<WsHeader *>(hdr), items, f.status, cx);
+}
+
 }  // namespace
+
+cudaError_t launch_window_long(const WinArgs &a, const WinLong &cx, const WsHeader *hdr, const WinItem *items,
+                               int64_t max_items, int num_sms, cudaStream_t stream)
+{
+    switch (a.f.D) {
+        case 32: return launch_window_d<32>(a, cx, hdr, items, max_items, num_sms, stream);
+        case 64: return launch_window_d<64>(a, cx, hdr, items, max_items, num_sms, stream);
+        case 80: return launch_window_d<80>(a, cx, hdr, items, max_items, num_sms, stream);
+        case 96: return launch_window_d<96>(a, cx, hdr, items, max_items, num_sms, stream);
+        case 128: return launch_window_d<128>(a, cx, hdr, items, max_items, num_sms, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
 
 int attn_long_bn(int D)
 {

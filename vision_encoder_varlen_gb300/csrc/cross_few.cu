@@ -23,9 +23,14 @@
 //
 // Keys past the run's end score -inf, and their V rows are zeroed in shared memory before use: what
 // lies there (the next sequence, padding, Inf or NaN) enters nothing.
+//
+// A causal window (W): the keys that a sequence's queries see between them are its first `sn` tokens, in tiles of
+// their own, and the run of positions from `lo` on; a run of `chunk` keys counts along both. Keys outside are not
+// loaded, and where there is more than one query each masks for itself what another one sees.
 #include "cross.h"
 #include "sm100.cuh"
 #include "warp_mma.cuh"
+#include "window.h"
 
 namespace vit {
 namespace {
@@ -59,13 +64,26 @@ struct Few {
     int32_t *status;
     int chunk, n_split, rows;                 // rows: max_q * group, the partial rows of a split
     float *part_o, *part_s;                   // [B][Hk][n_split][rows][D] and [..][rows] (log2 of the run's sum)
+    int window, sinks;                        // W: as in WinLong
 };
+
+// The keys of a sequence as the runs count them: [0, head) are its first sn tokens padded to whole tiles, and
+// head + i is position lo + i; n in all. Without a window: its keys.
+struct Keys {
+    int sn, head, lo, n;
+};
+__device__ __forceinline__ Keys window_keys(const Few &p, const WinSeg &w)
+{
+    const WinRange r = win_range(w.p0, p.window, p.sinks);
+    const int head = (r.first + kTile - 1) / kTile * kTile;
+    return Keys{r.first, head, r.lo, w.qn > 0 ? head + w.kn - r.lo : 0};
+}
 
 // Warps of a block: MT row tiles x 4 key groups.
 constexpr int kGroups = 4;
 template <int MT> constexpr int kMmaWarps = MT * kGroups;
 
-template <int D, int MT>
+template <int D, int MT, bool W>
 __global__ void __launch_bounds__(32 * kMmaWarps<MT> + 32)
 cross_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_kr,
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_vr, const Few p)
@@ -88,8 +106,27 @@ cross_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     if (seg.qn == 0) return;
     const int first = split * p.chunk;
     const bool only = p.n_split == 1;
-    if (first >= seg.kn && !(only && seg.kn == 0)) return;
-    const int n_keys = min(p.chunk, seg.kn - first);          // of this run
+    Keys keys{0, 0, 0, 0};
+    int p0 = 0;                                               // position of the first query
+    if constexpr (W) {
+        const WinSeg w = win_seg(seg);
+        // queries before the first key see nothing: zeros, by the first run's block
+        if (split == 0)
+            for (int x = threadIdx.x; x < w.none * p.group * (D / 8); x += 32 * NW + 32) {
+                const int r = x / (D / 8), c = x % (D / 8), head = hk * p.group + r % p.group;
+                const int64_t t = seg.q0 + r / p.group;
+                *reinterpret_cast<uint4 *>(p.out + t * p.out_stride + (int64_t)head * D + 8 * c) = make_uint4(0u, 0u, 0u, 0u);
+                if (p.lse && c == 0) p.lse[t * p.Hq + head] = -INFINITY;
+            }
+        keys = window_keys(p, w);
+        if (first >= keys.n) return;
+        seg.q0 = w.q0;
+        seg.qn = w.qn;
+        p0 = w.p0;
+    } else {
+        if (first >= seg.kn && !(only && seg.kn == 0)) return;
+    }
+    const int n_keys = min(p.chunk, (W ? keys.n : seg.kn) - first);   // of this run
     const int n_tiles = (n_keys + kTile - 1) / kTile;
     const int n_rows = seg.qn * p.group;
 
@@ -123,7 +160,10 @@ cross_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 const int s = i % kStages;
                 if (i >= kStages && !wait(s_empty[s], (i / kStages - 1) & 1)) break;
                 const uint32_t bar = sm100::smem_addr(&s_full[s]), dst = sm100::smem_addr(ring) + s * 2 * T::BYTES;
-                const int row = seg.k0 + first + i * kTile;
+                int row = seg.k0 + first + i * kTile;
+                if constexpr (W) {
+                    if (first + i * kTile >= keys.head) row += keys.lo - keys.head;
+                }
                 sm100::mbar_arrive_expect_tx(bar, 2 * T::BYTES);
 #pragma unroll
                 for (int x = 0; x < T::N128; ++x) {
@@ -169,7 +209,12 @@ cross_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             if (!ok) break;
             unsigned char *kt = ring + s * 2 * T::BYTES, *vt = kt + T::BYTES;
             const int key0 = 16 * quarter;
-            const int live = n_keys - i * kTile - key0;       // of this warp's 16 keys
+            int live = n_keys - i * kTile - key0;             // of this warp's 16 keys
+            int kp = first + i * kTile + key0;                // W: position of the first of them
+            if constexpr (W) {
+                if (kp < keys.head) live = keys.sn - kp;
+                else kp += keys.lo - keys.head;
+            }
             if (live > 0) {
                 const uint32_t ka = sm100::smem_addr(kt), va = sm100::smem_addr(vt);
                 float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -193,6 +238,23 @@ cross_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                         *reinterpret_cast<uint4 *>(vt + T::at(key0 + live + x / (D / 8), x % (D / 8))) =
                             make_uint4(0u, 0u, 0u, 0u);
                     __syncwarp();
+                }
+                if constexpr (W) {
+                    if (seg.qn > 1) {
+                        // rows g and g + 8: keys up to `hi`, from `lo` on or before `sk`
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int hi = p0 + (row_tile * 16 + g + 8 * h) / p.group - kp;
+                            const int lo = p.window > 0 ? hi - p.window + 1 : 0, sk = p.sinks - kp;
+#pragma unroll
+                            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const int x = 8 * n + 2 * c + e;
+                                    if (x > hi || (x < lo && x >= sk)) sc[n][2 * h + e] = -INFINITY;
+                                }
+                        }
+                    }
                 }
                 float pr[2][4];
                 bool grew = false;
@@ -312,7 +374,7 @@ cross_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         if (only) {
             const int64_t tok = seg.q0 + r / p.group;
             const int head = hk * p.group + r % p.group;
-            const float inv = seg.kn > 0 ? 1.f / L[h] : 0.f;  // no key at all: 0, and lse = -inf
+            const float inv = W || seg.kn > 0 ? 1.f / L[h] : 0.f;   // no key at all: 0, and lse = -inf
             __nv_bfloat16 *dst = p.out + tok * p.out_stride + (int64_t)head * D + 2 * c;
 #pragma unroll
             for (int j = 0; j < 2 * NK; ++j)
@@ -332,7 +394,7 @@ cross_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 
 // out = sum_s 2^(e_s - E) O_s / sum_s 2^(e_s - E), e_s the log2 of run s's sum: a row by one warp, or
 // (WIDE, many runs) by the eight warps of a block, each every eighth run, added up in warp order.
-template <int D, bool WIDE>
+template <int D, bool WIDE, bool W>
 __global__ void __launch_bounds__(256)
 cross_join_kernel(const Few p)
 {
@@ -342,8 +404,15 @@ cross_join_kernel(const Few p)
     CrossSeg seg;
     grid_wait();                                              // the runs' results
     if (!load_seg(p.segs, b, seg, nullptr, false)) return;
+    int n_keys = seg.kn;
+    if constexpr (W) {                                        // (queries that see nothing are written already)
+        const WinSeg w = win_seg(seg);
+        n_keys = window_keys(p, w).n;
+        seg.q0 = w.q0;
+        seg.qn = w.qn;
+    }
     const int n_rows = seg.qn * p.Hq;                         // (token, head) rows of the sequence
-    const int runs = key_runs(seg.kn, p.chunk);
+    const int runs = key_runs(n_keys, p.chunk);
     const int x = WIDE ? (int)blockIdx.x : (int)blockIdx.x * 8 + warp;
     if (x >= n_rows) return;
     const int tok = x / p.Hq, head = x - tok * p.Hq, hk = head / p.group;
@@ -397,7 +466,7 @@ bool kv_map(CUtensorMap *m, const void *ptr, int64_t T, int H, int D, int64_t st
     return encode_tiled_map(m, ptr, 2, dims, strides, box, cols * 2);
 }
 
-template <int D, int MT>
+template <int D, int MT, bool W>
 cudaError_t launch_mt(const CrossArgs &a, const FewPlan &pl, const Few &p, cudaStream_t stream)
 {
     constexpr int rem = Tile<D>::REM > 0 ? Tile<D>::REM : 64, wide = D >= 64 ? 64 : rem;
@@ -412,25 +481,28 @@ cudaError_t launch_mt(const CrossArgs &a, const FewPlan &pl, const Few &p, cudaS
         return cudaErrorInvalidValue;
     constexpr int smem = kStages * 2 * Tile<D>::BYTES + 1024;
     static_assert(kStages * 2 * Tile<D>::BYTES >= 2 * MT * 16 * D * 4, "the joins reuse the ring");
-    auto kern = cross_few_kernel<D, MT>;
+    auto kern = cross_few_kernel<D, MT, W>;
     static DeviceOnce once;
     cudaError_t e = once.run([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
     if (e != cudaSuccess) return e;
     {
-        LaunchScope scope("cross_few", stream);
+        LaunchScope scope(W ? "window_few" : "cross_few", stream);
         e = launch_chained(kern, dim3(a.Hk, s.B, pl.n_split), 32 * kMmaWarps<MT> + 32, smem, stream, mk, mkr, mv, mvr, p);
     }
     if (e != cudaSuccess || pl.n_split == 1) return e;
     LaunchScope scope("cross_join", stream);
     const int rows = s.max_q * a.Hq;
     // with more than 16 runs a warp per row is too few loads in flight (147 runs: 37 us)
-    return pl.n_split > 16 ? launch_chained(cross_join_kernel<D, true>, dim3(rows, s.B), 256, 0, stream, p)
-                           : launch_chained(cross_join_kernel<D, false>, dim3((rows + 7) / 8, s.B), 256, 0, stream, p);
+    return pl.n_split > 16 ? launch_chained(cross_join_kernel<D, true, W>, dim3(rows, s.B), 256, 0, stream, p)
+                           : launch_chained(cross_join_kernel<D, false, W>, dim3((rows + 7) / 8, s.B), 256, 0, stream, p);
 }
 
-template <int D> cudaError_t launch_d(const CrossArgs &a, const FewPlan &pl, cudaStream_t stream)
+template <int D, bool W>
+cudaError_t launch_d(const CrossArgs &a, int window, int sinks, const FewPlan &pl, cudaStream_t stream)
 {
     Few p;
+    p.window = window;
+    p.sinks = sinks;
     p.out = static_cast<__nv_bfloat16 *>(a.out);
     p.q = static_cast<const __nv_bfloat16 *>(a.q);
     p.lse = a.lse;
@@ -449,8 +521,8 @@ template <int D> cudaError_t launch_d(const CrossArgs &a, const FewPlan &pl, cud
     p.part_o = static_cast<float *>(a.workspace);
     p.part_s = p.part_o + n * D;
     switch (pl.row_tiles) {
-        case 1: return launch_mt<D, 1>(a, pl, p, stream);
-        default: return launch_mt<D, 2>(a, pl, p, stream);
+        case 1: return launch_mt<D, 1, W>(a, pl, p, stream);
+        default: return launch_mt<D, 2, W>(a, pl, p, stream);
     }
 }
 
@@ -492,14 +564,44 @@ bool takes_few(int B, int Hq, int Hk, int D, int max_q, int max_k)
     return rows <= 16 || (rows <= 32 && (int64_t)B * max_k * Hk * D * 4 <= ((int64_t)32 << 20));
 }
 
+// Keys that the runs of a windowed call count at most: everything in one piece where no window leaves a gap behind the
+// first tokens, else those in whole tiles and what the queries of a sequence see between them.
+static int window_most(int max_q, int max_k, int window, int sinks)
+{
+    if (window == 0 || (int64_t)window + sinks >= max_k) return max_k;
+    const int64_t own = (int64_t)window + max_q - 1, head = ((int64_t)sinks + kTile - 1) / kTile * kTile;
+    const int64_t most = head + own, all = (int64_t)max_k + kTile;
+    return (int)(most < all ? most : all);
+}
+bool window_takes_few(int B, int Hq, int Hk, int D, int max_q, int max_k, int window, int sinks)
+{
+    return takes_few(B, Hq, Hk, D, max_q, window_most(max_q, max_k, window, sinks));
+}
+FewPlan window_few_plan(int B, int Hq, int Hk, int D, int max_q, int max_k, int window, int sinks)
+{
+    return few_plan(B, Hq, Hk, D, max_q, window_most(max_q, max_k, window, sinks));
+}
+
 cudaError_t launch_cross_few(const CrossArgs &a, const FewPlan &p, cudaStream_t stream)
 {
     switch (a.D) {
-        case 32: return launch_d<32>(a, p, stream);
-        case 64: return launch_d<64>(a, p, stream);
-        case 80: return launch_d<80>(a, p, stream);
-        case 96: return launch_d<96>(a, p, stream);
-        case 128: return launch_d<128>(a, p, stream);
+        case 32: return launch_d<32, false>(a, 0, 0, p, stream);
+        case 64: return launch_d<64, false>(a, 0, 0, p, stream);
+        case 80: return launch_d<80, false>(a, 0, 0, p, stream);
+        case 96: return launch_d<96, false>(a, 0, 0, p, stream);
+        case 128: return launch_d<128, false>(a, 0, 0, p, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t launch_window_few(const WinArgs &a, const FewPlan &p, cudaStream_t stream)
+{
+    switch (a.f.D) {
+        case 32: return launch_d<32, true>(a.f, a.window, a.sinks, p, stream);
+        case 64: return launch_d<64, true>(a.f, a.window, a.sinks, p, stream);
+        case 80: return launch_d<80, true>(a.f, a.window, a.sinks, p, stream);
+        case 96: return launch_d<96, true>(a.f, a.window, a.sinks, p, stream);
+        case 128: return launch_d<128, true>(a.f, a.window, a.sinks, p, stream);
         default: return cudaErrorInvalidValue;
     }
 }

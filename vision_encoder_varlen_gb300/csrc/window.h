@@ -1,0 +1,90 @@
+// Declarations shared by the translation units of a language model's own attention: a causal window over a
+// sequence's keys with its first tokens kept visible, and a prefix that several sequences share.
+#pragma once
+
+#include "cross.h"
+
+namespace vit {
+
+// Work item of the tcgen05 kernel: its 128 (split) or 256 query rows see all of the keys [f0, f0 + fn) (a sequence's
+// first tokens, or a prefix, which may be of another tensor), and of the keys [k0, k0 + kn), whose first one has
+// position `kp` in its sequence, those that the mask lets through for a query of position p: j <= p and, with a
+// window, p - j < window or j < sinks. Rows are packed as in CrossItem; token q0 has position p0.
+struct WinItem {
+    int f0, fn;
+    int k0, kn;
+    int q0, q1, head;
+    int split;
+    int slot;                     // place of the partial result, or -1: the result itself
+    int kp, p0;
+    int pad;
+};
+static_assert(sizeof(WinItem) == 48, "three 16-byte words");
+__device__ __forceinline__ int item_head(const WinItem &x) { return x.head; }
+__device__ __forceinline__ bool item_split(const WinItem &x) { return x.split != 0; }
+
+struct WinLong : CrossLong {
+    int window, sinks;            // window 0: everything before a query
+};
+
+struct WinArgs {
+    CrossArgs f;                  // the queries are the last ones of their sequence's keys
+    int window, sinks;
+    // a shared prefix: the sequences [cu_g[g], cu_g[g+1]) (all of them without cu_g) see the rows [cu_p[g], cu_p[g+1])
+    bool prefix;
+    const void *kp, *vp;          // bf16 [Tp, Hk, D]
+    int64_t kp_stride, vp_stride, Tp;
+    const int32_t *cu_g, *cu_p;
+    int G, max_p;
+};
+
+// The place of a sequence's queries among its keys. The first `none` queries lie before its first key (fewer keys than
+// queries) and see none of them; the rest, from row q0 on, have positions p0, p0 + 1, ..
+struct WinSeg {
+    int q0, qn, k0, kn, p0, none;
+};
+__device__ __forceinline__ WinSeg win_seg(const CrossSeg &x)
+{
+    WinSeg w;
+    w.none = x.qn > x.kn ? x.qn - x.kn : 0;
+    w.q0 = x.q0 + w.none;
+    w.qn = x.qn - w.none;
+    w.k0 = x.k0;
+    w.kn = x.kn;
+    w.p0 = x.kn - w.qn;
+    return w;
+}
+
+// The keys that queries of the positions [p, q] see between them: the `first` of the sequence and, behind a gap, those
+// of the positions [lo, q] (first = 0 where there is no gap).
+struct WinRange {
+    int first, lo;
+};
+__host__ __device__ inline WinRange win_range(int p, int window, int sinks)
+{
+    const int lo = window > 0 && p >= window ? p - window + 1 : 0;
+    return lo > sinks ? WinRange{sinks, lo} : WinRange{0, 0};
+}
+
+// How a call of the tcgen05 kernel is cut (a function of the sizes alone).
+struct WinPlan {
+    int lg_pack;
+    int units;                    // sequences, or groups and sequences (apart)
+    bool apart;                   // prefix and own keys are separate items, joined by row
+    int run_tiles;                // key tiles of an item at most (0: keys are not cut)
+    int runs;                     // runs of a block at most
+    int64_t max_items, max_tiles, slots;
+    size_t off_items, off_tiles, off_empty, off_units, off_part_s, off_part_o, bytes;
+};
+WinPlan win_plan(int64_t Tq, int B, int Hq, int Hk, int D, int max_q, int max_k, int window, int sinks, int G,
+                 int64_t Tp, int max_p);
+cudaError_t launch_window_tiles(const WinArgs &a, const WinPlan &p, int num_sms, cudaStream_t stream);
+cudaError_t launch_window_long(const WinArgs &a, const WinLong &cx, const WsHeader *hdr, const WinItem *items,
+                               int64_t max_items, int num_sms, cudaStream_t stream);
+
+// few query rows (cross_few.cu)
+bool window_takes_few(int B, int Hq, int Hk, int D, int max_q, int max_k, int window, int sinks);
+FewPlan window_few_plan(int B, int Hq, int Hk, int D, int max_q, int max_k, int window, int sinks);
+cudaError_t launch_window_few(const WinArgs &a, const FewPlan &p, cudaStream_t stream);
+
+}  // namespace vit

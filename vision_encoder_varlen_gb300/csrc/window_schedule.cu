@@ -1,0 +1,526 @@
+// Work list of the tcgen05 kernel in a language model's own attention, and the join of a prefix with what follows it.
+//
+// One block reads the offsets on the device (nothing returns to the host) and cuts units into items. A unit is a
+// sequence with the keys that its mask lets through, or, with a prefix, one of:
+//   - a sequence, whose items read the prefix first and then the sequence's own keys: one softmax over both;
+//   - where sequences are short (`apart`): a group's queries of all its sequences over the prefix, so that tiles are
+//     full and the prefix is read once per tile of the group instead of once per sequence, and a sequence over its own
+//     keys. Both leave partial results, which window_join_kernel adds up row by row.
+// Blocks of 256 rows, split items of 128 rows, cut key ranges and packed heads are those of cross attention (its list
+// says more). Here a block's keys depend on its place: under a causal mask the last one of a sequence has the most. So
+// units are ordered by their longest block, and a unit's blocks come last first, all heads of one after the other: long
+// items start first, and what is left at the end is short.
+#include <algorithm>
+
+#include "block_sort.cuh"
+#include "warp_mma.cuh"
+#include "window.h"
+
+namespace vit {
+namespace {
+
+constexpr int kThreads = kSortThreads;
+
+// A unit's queries (rows [q0, q0 + qn), positions from p0 on) and its keys: the prefix rows [f0, f0 + fn), and the own
+// keys from row k0 on (kn = 0: none).
+struct Unit {
+    int q0, qn, f0, fn, k0, kn, p0;
+};
+// what a unit's place in the slots is, for the join
+struct UnitSlots {
+    int q0, blocks, runs, slot;
+};
+
+struct Sched {
+    CrossSegs s;
+    int window, sinks;
+    const int32_t *cu_g, *cu_p;
+    int64_t Tp;
+    int G, max_p;
+    bool prefix, apart;
+    int Hq, lg_pack, bn, run_tiles, num_sms;
+    WsHeader *hdr;
+    WinItem *items;
+    CrossTile *tiles;
+    CrossEmpty *empty;
+    UnitSlots *units;
+    float *part_s;
+    int32_t *status;
+};
+
+__device__ __forceinline__ int group_bound(const Sched &p, int g) { return p.cu_g ? p.cu_g[g] : g == 0 ? 0 : p.s.B; }
+
+// The group's prefix: false where its rows are not in the tensor, or more than the bound.
+__device__ __forceinline__ bool load_prefix(const Sched &p, int g, int &f0, int &fn)
+{
+    const int64_t a = p.cu_p[g], b = p.cu_p[g + 1];
+    f0 = (int)a;
+    fn = (int)(b - a);
+    return a >= 0 && b >= a && b <= p.Tp && b - a <= p.max_p;
+}
+
+// Group g's error: the groups follow one another and hold every sequence, their prefixes lie in the tensor.
+__device__ __forceinline__ int group_error(const Sched &p, int g)
+{
+    const int a = group_bound(p, g), b = group_bound(p, g + 1);
+    if (b < a || (g == 0 && a != 0) || (g == p.G - 1 && b != p.s.B)) return VIT_ERR_BAD_SEQLENS;
+    int f0, fn;
+    if (load_prefix(p, g, f0, fn)) return 0;
+    return p.cu_p[g] < 0 || p.cu_p[g + 1] < p.cu_p[g] || p.cu_p[g + 1] > p.Tp ? VIT_ERR_BAD_SEQLENS
+                                                                             : VIT_ERR_SEQLEN_EXCEEDS_MAX;
+}
+
+// the group of sequence b: the last g with group_bound(g) <= b that has sequences
+__device__ __forceinline__ int group_of(const Sched &p, int b)
+{
+    int lo = 0, hi = p.G;
+    while (hi - lo > 1) {
+        const int m = (lo + hi) >> 1;
+        if (group_bound(p, m) <= b) lo = m;
+        else hi = m;
+    }
+    return lo;
+}
+
+// Unit u, and whether it can be used; `none` counts a sequence's queries that see nothing at all (its first rows).
+__device__ __forceinline__ bool load_unit(const Sched &p, int u, Unit &x, CrossEmpty &none, bool report)
+{
+    none = CrossEmpty{0, 0};
+    x = Unit{0, 0, 0, 0, 0, 0, 0};
+    if (p.apart && u < p.G) {
+        const int a = group_bound(p, u), b = group_bound(p, u + 1);
+        const bool fine = load_prefix(p, u, x.f0, x.fn);
+        if (a < 0 || b < a || b > p.s.B) return false; // (reported with the groups)
+        const int64_t q0 = p.s.cu_q[a], q1 = p.s.cu_q[b];
+        if (!fine || q0 < 0 || q1 < q0 || q1 > p.s.Tq) return false;     // (the sequences report their offsets)
+        x.q0 = (int)q0;
+        x.qn = (int)(q1 - q0);
+        return true;
+    }
+    const int b = p.apart ? u - p.G : u;
+    CrossSeg c;
+    if (!load_seg(p.s, b, c, p.status, report)) return false;
+    if (p.prefix && !p.apart) {
+        if (!load_prefix(p, group_of(p, b), x.f0, x.fn)) return false;
+    }
+    const WinSeg w = win_seg(c);
+    x.k0 = w.k0;
+    x.kn = w.kn;
+    x.q0 = w.q0;
+    x.qn = w.qn;
+    x.p0 = w.p0;
+    if (x.fn > 0) {                                    // all of them see the prefix
+        x.q0 -= w.none;
+        x.qn += w.none;
+        x.p0 -= w.none;
+    } else if (!p.apart) {
+        none = CrossEmpty{c.q0, w.none};
+    }
+    return true;
+}
+
+// What the queries [t, e) of a unit see between them, as an item says it.
+struct Span {
+    int f0, fn, lo, kn;
+    __device__ int tiles(int bn) const { return (fn + bn - 1) / bn + (kn + bn - 1) / bn; }
+};
+__device__ __forceinline__ Span span_of(const Sched &p, const Unit &u, int t, int e)
+{
+    Span s{u.f0, u.fn, 0, 0};
+    if (u.kn == 0) return s;
+    const int first = u.p0 + t, last = u.p0 + e - 1;
+    if (!p.prefix) {
+        const WinRange r = win_range(first, p.window, p.sinks);
+        s.f0 = u.k0;
+        s.fn = r.first;
+        s.lo = r.lo;
+    }
+    s.kn = max(0, last + 1 - s.lo);
+    return s;
+}
+
+__global__ void __launch_bounds__(kThreads)
+window_schedule_kernel(const Sched p)
+{
+    extern __shared__ unsigned long long s_key[];      // [NP]: longest block first, then index; later first item | index
+    __shared__ int64_t s_warp[32];
+    __shared__ int s_bad, s_used, s_total, s_tiles, s_all_split, s_more, s_empty;
+    grid_wait();
+    grid_release();
+    const int tid = threadIdx.x, n_units = p.apart ? p.G + p.s.B : p.s.B;
+    int NP = 32;
+    while (NP < n_units) NP <<= 1;
+    int *s_tile = reinterpret_cast<int *>(s_key + NP); // [NP] first tile
+    const int lg_tile = 7 - p.lg_pack;                 // tokens of a 128-row tile, log2
+    const int packs = p.Hq >> p.lg_pack;
+    auto longest = [&](const Unit &x) { return span_of(p, x, max(0, x.qn - (1 << lg_tile)), x.qn).tiles(p.bn); };
+    auto key_of = [&](bool use, const Unit &x, int i) {
+        return ((unsigned long long)(use ? 0x7fffffffu - (uint32_t)longest(x) : 0xffffffffu) << 32) | (uint32_t)i;
+    };
+    auto blocks_of = [&](const Unit &x, int lg) { return packs * (int)(((unsigned)x.qn + (1u << lg) - 1u) >> lg); };
+    auto runs_of = [&](const Unit &x) { return p.run_tiles > 0 ? max(1, (longest(x) + p.run_tiles - 1) / p.run_tiles) : 1; };
+    auto usable = [&](bool fine, const Unit &x) { return fine && x.qn > 0 && (x.fn > 0 || x.kn > 0); };
+    // two-tile blocks of the batch: few of them means split items throughout
+    auto split_all = [&](int64_t full) { return p.run_tiles > 0 || p.apart || 2 * full <= (int64_t)p.num_sms; };
+    auto unfit = [&](int u, bool fine) {               // nothing is computed at all then
+        const int b = p.apart ? u - p.G : u;
+        return (p.prefix && !fine) || (b >= 0 && p.s.cu_q[b + 1] < p.s.cu_q[b]);
+    };
+    bool wrong = false;                                // of a prefix call: then nothing is computed at all
+    if (p.prefix) {
+        for (int g = tid; g < p.G; g += kThreads) {
+            const int err = group_error(p, g);
+            if (err) report_error(p.status, err);
+            wrong |= err != 0;
+        }
+        wrong = __syncthreads_or(wrong);
+    }
+    if (n_units <= 32) {
+        // a warp: one unit per lane
+        if (tid < 32) {
+            Unit x;
+            CrossEmpty none{0, 0};
+            const bool fine = tid < n_units && load_unit(p, tid, x, none, true);
+            const bool bad = tid < n_units && unfit(tid, fine), use = usable(fine, x);
+            int64_t full = use ? blocks_of(x, lg_tile + 1) : 0;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) full += __shfl_xor_sync(0xffffffffu, full, o);
+            const bool all_split = split_all(full);
+            const int n = use ? blocks_of(x, all_split ? lg_tile : lg_tile + 1) : 0, runs = use ? runs_of(x) : 1;
+            int rank, at, tile_at;
+            warp_place(key_of(use, x, tid), n * runs, runs > 1 ? n : 0, rank, at, tile_at);
+            s_key[rank] = ((unsigned long long)at << 32) | (uint32_t)tid;
+            s_tile[rank] = tile_at;
+            const unsigned used = __ballot_sync(0xffffffffu, use), any_bad = __ballot_sync(0xffffffffu, bad);
+            const unsigned nones = __ballot_sync(0xffffffffu, fine && none.qn > 0);
+            if (fine && none.qn > 0) p.empty[__popc(nones & ((1u << tid) - 1u))] = none;
+            if (rank == 31) {                          // the last: its sums are all but its own
+                s_total = at + n * runs;
+                s_tiles = tile_at + (runs > 1 ? n : 0);
+                s_used = __popc(used);
+                s_empty = __popc(nones);
+                s_all_split = all_split;
+                s_bad = any_bad != 0;
+            }
+        }
+        __syncthreads();
+    } else {
+        if (tid == 0) s_bad = s_used = s_empty = 0;
+        __syncthreads();
+        for (int i = tid; i < NP; i += kThreads) {
+            Unit x;
+            CrossEmpty none{0, 0};
+            const bool fine = i < n_units && load_unit(p, i, x, none, true);
+            if (i < n_units && unfit(i, fine)) s_bad = 1;
+            const bool use = usable(fine, x);
+            s_key[i] = key_of(use, x, i);
+            if (use) atomicAdd(&s_used, 1);
+            if (fine && none.qn > 0) p.empty[atomicAdd(&s_empty, 1)] = none;   // (in any order)
+        }
+        __syncthreads();
+        block_sort(s_key, NP, tid);
+        const int per = (n_units + kThreads - 1) / kThreads, lo = min(tid * per, s_used), hi = min(lo + per, s_used);
+        auto unit_at = [&](int i) {
+            Unit x;
+            CrossEmpty none;
+            load_unit(p, (int)(s_key[i] & 0xffffffffu), x, none, false);
+            return x;
+        };
+        int64_t mine = 0, total_full, n_items = 0, n_tiles = 0, total, total_tiles;
+        for (int i = lo; i < hi; ++i) mine += blocks_of(unit_at(i), lg_tile + 1);
+        block_exclusive_scan(mine, s_warp, &total_full);
+        const bool all_split = split_all(total_full);
+        const int lg_block = all_split ? lg_tile : lg_tile + 1;
+        for (int i = lo; i < hi; ++i) {
+            const Unit x = unit_at(i);
+            const int n = blocks_of(x, lg_block), runs = runs_of(x);
+            n_items += (int64_t)n * runs;
+            if (runs > 1) n_tiles += n;
+        }
+        int64_t at = block_exclusive_scan(n_items, s_warp, &total);
+        int64_t tile_at = block_exclusive_scan(n_tiles, s_warp, &total_tiles);
+        for (int i = lo; i < hi; ++i) {
+            const Unit x = unit_at(i);
+            const int n = blocks_of(x, lg_block), runs = runs_of(x);
+            s_key[i] = ((unsigned long long)at << 32) | (uint32_t)(s_key[i] & 0xffffffffu);
+            s_tile[i] = (int)tile_at;
+            at += (int64_t)n * runs;
+            if (runs > 1) tile_at += n;
+        }
+        if (tid == 0) {
+            s_total = (int)total;
+            s_tiles = (int)total_tiles;
+            s_all_split = all_split;
+        }
+        __syncthreads();
+    }
+    const bool bad = wrong || s_bad != 0, all_split = s_all_split != 0;
+    const int total = bad ? 0 : s_total, lg_block = all_split ? lg_tile : lg_tile + 1;
+    // where the items end in a wave that fills at most half the SMs, its items are cut into their tiles
+    const int rest = total % p.num_sms;
+    const int whole = p.run_tiles > 0 ? 0 : !all_split && 2 * rest <= p.num_sms ? total - rest : total;
+    if (tid == 0) s_more = 0;
+    __syncthreads();
+    for (int i = tid; i < total; i += kThreads) {
+        const int at_unit = place_of(s_key, s_used, i), n = i - (int)(s_key[at_unit] >> 32);
+        const int unit = (int)(s_key[at_unit] & 0xffffffffu);
+        Unit x;
+        CrossEmpty none;
+        load_unit(p, unit, x, none, false);
+        const int nq = (int)(((unsigned)x.qn + (1u << lg_block) - 1u) >> lg_block), runs = runs_of(x);
+        const int j = n / runs, run = n - j * runs, qb = nq - 1 - j / packs, h = j % packs;
+        const int t = qb << lg_block, e = min(x.qn, t + (1 << lg_block));
+        const Span s = span_of(p, x, t, e);
+        // the block's tiles, dealt evenly to as many runs as they fill
+        const int tiles = s.tiles(p.bn), use = runs > 1 ? max(1, (tiles + p.run_tiles - 1) / p.run_tiles) : 1;
+        if (p.apart && n == 0) p.units[unit] = UnitSlots{x.q0, nq, runs, i};
+        if (run >= use) {
+            if (p.apart)
+                for (int r = 0; r < 128; ++r) p.part_s[(int64_t)i * 128 + r] = -INFINITY;
+            continue;
+        }
+        WinItem it;
+        it.q0 = x.q0 + t;
+        it.q1 = x.q0 + x.qn;
+        it.head = h << p.lg_pack;
+        it.split = all_split || x.qn - t <= (1 << lg_tile);
+        it.slot = runs > 1 || p.apart ? i : -1;
+        it.p0 = x.p0 + t;
+        it.pad = 0;
+        const int nf = (s.fn + p.bn - 1) / p.bn, a = (int)((int64_t)tiles * run / use);
+        const int b = (int)((int64_t)tiles * (run + 1) / use);
+        const int fa = min(s.fn, min(a, nf) * p.bn), fb = min(s.fn, min(b, nf) * p.bn);
+        const int ka = min(s.kn, max(0, a - nf) * p.bn), kb = min(s.kn, max(0, b - nf) * p.bn);
+        it.f0 = s.f0 + fa;
+        it.fn = fb - fa;
+        it.kp = s.lo + ka;
+        it.k0 = x.k0 + it.kp;
+        it.kn = kb - ka;
+        if (runs > 1 && run == 0 && !p.apart)
+            p.tiles[s_tile[at_unit] + j] = CrossTile{it.q0, it.q1, it.head, i, use, {0, 0, 0}};
+        if (i < whole) {
+            p.items[i] = it;
+        } else {                                       // (in any order: an item's result does not depend on its place)
+            const int halves = it.split ? 1 : 2, at = whole + atomicAdd(&s_more, halves);
+            it.split = 1;
+            p.items[at] = it;
+            if (halves == 2) {
+                it.q0 += 1 << lg_tile;
+                it.p0 += 1 << lg_tile;
+                p.items[at + 1] = it;
+            }
+        }
+    }
+    __syncthreads();
+    if (tid == 0) {
+        WsHeader *hdr = p.hdr;
+        hdr->n_long = whole + s_more;
+        hdr->n_joins = bad || p.apart ? 0 : s_tiles;
+        hdr->n_empty = bad ? 0 : s_empty;
+        hdr->n_tiny = 0;
+        hdr->bm_long = 1 << lg_block;
+        hdr->tiny_max = 0;
+        hdr->error = bad ? VIT_ERR_BAD_SEQLENS : 0;
+        hdr->long_all_split = all_split ? 1 : 0;
+        hdr->next_long = 0;
+    }
+}
+
+// A row of sequence b: its parts over the prefix and over its own keys, one warp per row,
+//   out = sum_s 2^(e_s - E) O_s / sum_s 2^(e_s - E), e_s the log2 of part s's sum.
+template <int D>
+__global__ void __launch_bounds__(256)
+window_join_kernel(const Sched p, const float *part_o, __nv_bfloat16 *out, int64_t out_stride, float *lse)
+{
+    grid_wait();
+    if (p.hdr->error != 0) return;
+    const int lane = threadIdx.x & 31, b = blockIdx.y;
+    CrossSeg c;
+    if (!load_seg(p.s, b, c, nullptr, false)) return;
+    const int g = group_of(p, b), packs = p.Hq >> p.lg_pack, lg_tile = 7 - p.lg_pack, mask = (1 << lg_tile) - 1;
+    const WinSeg w = win_seg(c);
+    // a unit without keys has no slots
+    UnitSlots own{0, 0, 0, 0}, pre{0, 0, 0, 0};
+    if (w.kn > 0) own = p.units[p.G + b];
+    if (p.cu_p[g + 1] > p.cu_p[g]) pre = p.units[g];
+    const int before = c.q0 - p.s.cu_q[group_bound(p, g)];     // rows of the group's sequences before this one
+    for (int64_t x = blockIdx.x * 8 + (threadIdx.x >> 5); x < (int64_t)c.qn * p.Hq; x += 8 * gridDim.x) {
+        const int tok = (int)(x / p.Hq), head = (int)(x - (int64_t)tok * p.Hq);
+        const int pack = head >> p.lg_pack, in_pack = head & ((1 << p.lg_pack) - 1);
+        // the first part's row of a unit's token t
+        auto first = [&](const UnitSlots &u, int t) -> int64_t {
+            const int64_t slot = u.slot + (int64_t)((u.blocks - 1 - (t >> lg_tile)) * packs + pack) * u.runs;
+            return slot * 128 + ((t & mask) << p.lg_pack) + in_pack;
+        };
+        const int own_runs = tok < w.none ? 0 : own.runs;      // the first queries may lie before the first own key
+        const int64_t own_row = first(own, tok - w.none), pre_row = first(pre, before + tok);
+        auto row = [&](int s) -> int64_t {
+            return s < pre.runs ? pre_row + (int64_t)s * 128 : own_row + (int64_t)(s - pre.runs) * 128;
+        };
+        const int runs = pre.runs + own_runs;
+        float E = -INFINITY;
+        for (int s = lane; s < runs; s += 32) E = fmaxf(E, p.part_s[row(s)]);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) E = fmaxf(E, __shfl_xor_sync(0xffffffffu, E, d));
+        const float base = E == -INFINITY ? 0.f : E;
+        float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int s = 0; s < runs; ++s) {
+            const int64_t r = row(s);
+            const float y = wmma16::ex2(p.part_s[r] - base);
+            sum += y;
+            if (lane < D / 4 && y != 0.f) {            // (a part without weight was not written)
+                const float4 v = *reinterpret_cast<const float4 *>(part_o + r * D + 4 * lane);
+                acc[0] = fmaf(y, v.x, acc[0]);
+                acc[1] = fmaf(y, v.y, acc[1]);
+                acc[2] = fmaf(y, v.z, acc[2]);
+                acc[3] = fmaf(y, v.w, acc[3]);
+            }
+        }
+        const float inv = runs > 0 ? 1.f / sum : 0.f;  // keys, but no weight: 0 * inf; no keys: 0
+        const int64_t t = (int64_t)c.q0 + tok;
+        if (lane < D / 4)
+            *reinterpret_cast<uint2 *>(out + t * out_stride + (int64_t)head * D + 4 * lane) =
+                make_uint2(wmma16::pack_bf16(acc[0] * inv, acc[1] * inv), wmma16::pack_bf16(acc[2] * inv, acc[3] * inv));
+        if (lse && lane == 0) lse[t * p.Hq + head] = (E + log2f(sum)) * 0.6931471805599453f;
+    }
+}
+
+size_t up(size_t x) { return (x + 255) / 256 * 256; }
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace
+
+WinPlan win_plan(int64_t Tq, int B, int Hq, int Hk, int D, int max_q, int max_k, int window, int sinks, int G,
+                 int64_t Tp, int max_p)
+{
+    WinPlan p;
+    p.lg_pack = cross_pack(Hq / Hk);
+    const int64_t tok = 128 >> p.lg_pack, packs = Hq >> p.lg_pack, bn = attn_long_bn(D);
+    // tiles of the sequences, and of the groups
+    const int64_t own = std::min(Tq / tok + B, (int64_t)B * cdiv(max_q, tok)), grouped = Tq / tok + G;
+    const bool prefix = G > 0 && Tp > 0;
+    // Apart where the sequences' tiles would be much emptier than the groups': otherwise a pass over both saves the
+    // partial results and their join.
+    p.apart = prefix && own > 2 * grouped;
+    p.units = p.apart ? G + B : B;
+    // key tiles of a block at most
+    const int64_t own_keys = window > 0 ? std::min<int64_t>(max_k, (int64_t)window + 2 * tok - 1) : max_k;
+    const int64_t first = prefix ? max_p : window > 0 ? std::min(sinks, max_k) : 0;
+    const int64_t own_most = cdiv(own_keys, bn), first_most = cdiv(first, bn);
+    const int64_t tiles = (p.apart ? own + grouped : own) * packs;
+    p.run_tiles = 0;
+    p.runs = 1;
+    p.max_tiles = 0;
+    // few tiles: cut their keys so that there is about one item per SM, of at least 512 keys each (a run writes and
+    // re-reads 128 * D fp32 values)
+    const int64_t least = 2 * cdiv(512, 2 * bn);
+    if (p.apart) {
+        const int64_t work = (own * own_most + grouped * first_most) * packs;
+        const int64_t run = std::max(least, cdiv(work, kDesignSms));
+        const int64_t r1 = cdiv(first_most, run), r2 = cdiv(own_most, run);
+        p.run_tiles = (int)run;
+        p.runs = (int)std::max<int64_t>(1, std::max(r1, r2));
+        p.max_items = (grouped * std::max<int64_t>(1, r1) + own * std::max<int64_t>(1, r2)) * packs;
+        p.slots = p.max_items;
+    } else {
+        const int64_t most = own_most + first_most;
+        p.max_items = tiles;
+        p.slots = 0;
+        if (2 * tiles <= kDesignSms && tiles > 0) {
+            const int64_t run = std::max(least, cdiv(most, kDesignSms / tiles)), runs = cdiv(most, run);
+            if (runs > 1) {
+                p.run_tiles = (int)run;
+                p.runs = (int)runs;
+                p.max_items = tiles * runs;
+                p.max_tiles = tiles;
+                p.slots = p.max_items;
+            }
+        }
+    }
+    p.off_items = sizeof(WsHeader);
+    p.off_tiles = up(p.off_items + sizeof(WinItem) * (size_t)p.max_items);
+    p.off_empty = up(p.off_tiles + sizeof(CrossTile) * (size_t)p.max_tiles);
+    p.off_units = up(p.off_empty + sizeof(CrossEmpty) * (size_t)B);
+    p.off_part_s = up(p.off_units + (p.apart ? sizeof(UnitSlots) * (size_t)p.units : 0));
+    p.off_part_o = up(p.off_part_s + (size_t)p.slots * 128 * sizeof(float));
+    p.bytes = p.off_part_o + (size_t)p.slots * 128 * (size_t)D * sizeof(float);
+    return p;
+}
+
+cudaError_t launch_window_tiles(const WinArgs &a, const WinPlan &pl, int num_sms, cudaStream_t stream)
+{
+    char *ws = static_cast<char *>(a.f.workspace);
+    Sched p;
+    p.s = a.f.segs;
+    p.window = a.window;
+    p.sinks = a.sinks;
+    p.cu_g = a.cu_g;
+    p.cu_p = a.cu_p;
+    p.Tp = a.Tp;
+    p.G = a.G;
+    p.max_p = a.max_p;
+    p.prefix = a.prefix;
+    p.apart = pl.apart;
+    p.Hq = a.f.Hq;
+    p.lg_pack = pl.lg_pack;
+    p.bn = attn_long_bn(a.f.D);
+    p.run_tiles = pl.run_tiles;
+    p.num_sms = num_sms;
+    p.hdr = reinterpret_cast<WsHeader *>(ws);
+    p.items = reinterpret_cast<WinItem *>(ws + pl.off_items);
+    p.tiles = reinterpret_cast<CrossTile *>(ws + pl.off_tiles);
+    p.empty = reinterpret_cast<CrossEmpty *>(ws + pl.off_empty);
+    p.units = reinterpret_cast<UnitSlots *>(ws + pl.off_units);
+    p.part_s = reinterpret_cast<float *>(ws + pl.off_part_s);
+    p.status = a.f.status;
+    int np = 32;
+    while (np < pl.units) np <<= 1;
+    constexpr size_t each = sizeof(unsigned long long) + sizeof(int);
+    static DeviceOnce once;
+    cudaError_t e = once.run([] {
+        return cudaFuncSetAttribute(window_schedule_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)each * 2 * VIT_MAX_SEGMENTS);
+    });
+    if (e != cudaSuccess) return e;
+    {
+        LaunchScope scope("window_schedule", stream);
+        e = launch_chained(window_schedule_kernel, 1, kThreads, each * np, stream, p);
+        if (e != cudaSuccess) return e;
+    }
+    WinLong cx{};
+    cx.group = a.f.Hq / a.f.Hk;
+    cx.lg_pack = pl.lg_pack;
+    cx.empty = p.empty;
+    cx.part_s = p.part_s;
+    cx.part_o = reinterpret_cast<float *>(ws + pl.off_part_o);
+    cx.window = a.window;
+    cx.sinks = a.sinks;
+    e = launch_window_long(a, cx, p.hdr, p.items, pl.max_items, num_sms, stream);
+    if (e != cudaSuccess) return e;
+    if (pl.apart) {
+        LaunchScope scope("window_join", stream);
+        // a loose bound of the lengths starts no more blocks than fill the GPU a few times over
+        const int64_t most = cdiv((int64_t)a.f.segs.max_q * a.f.Hq, 8), enough = cdiv(64 * kDesignSms, a.f.segs.B);
+        const dim3 grid((unsigned)std::min(most, enough), (unsigned)a.f.segs.B);
+        auto run = [&](auto kern) {
+            return launch_chained(kern, grid, 256, 0, stream, p, cx.part_o, static_cast<__nv_bfloat16 *>(a.f.out),
+                                  a.f.out_stride, a.f.lse);
+        };
+        switch (a.f.D) {
+            case 32: return run(window_join_kernel<32>);
+            case 64: return run(window_join_kernel<64>);
+            case 80: return run(window_join_kernel<80>);
+            case 96: return run(window_join_kernel<96>);
+            default: return run(window_join_kernel<128>);
+        }
+    }
+    if (pl.runs > 1) {
+        LongPlan join{};
+        join.max_tiles = pl.max_tiles;
+        return launch_cross_tile_join(a.f, join, cx, p.hdr, p.tiles, stream);
+    }
+    return cudaSuccess;
+}
+
+}  // namespace vit
