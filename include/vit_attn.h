@@ -609,6 +609,22 @@ vit_status_t vit_window_attn(const void *q, const void *k, const void *v, int64_
                              int sinks, float scale, void *out, int64_t out_stride, float *lse, void *workspace,
                              size_t workspace_bytes, int32_t *status_dev, vit_stream_t stream);
 
+/* Workspace bytes of vit_window_attn_bwd for these sizes (0 for invalid ones). */
+size_t vit_window_attn_bwd_workspace_size(int64_t Tq, int64_t Tk, int Hq, int Hkv, int D, int B, int max_q, int max_k,
+                                          int window, int sinks);
+
+/*
+ * Gradient of vit_window_attn: arguments, roundings and errors as for vit_cross_attn_bwd. Keys that no
+ * query sees, and queries that see no key, get 0.
+ */
+vit_status_t vit_window_attn_bwd(const void *dout, const void *q, const void *k, const void *v, const void *out,
+                                 const float *lse, int64_t Tq, int64_t Tk, int Hq, int Hkv, int D,
+                                 int64_t dout_stride, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                 int64_t out_stride, const int32_t *cu_q, const int32_t *cu_k, const int32_t *k_len,
+                                 int B, int max_q, int max_k, int window, int sinks, float scale, void *dq, void *dk,
+                                 void *dv, int64_t dq_stride, int64_t dk_stride, int64_t dv_stride, int zero_rest,
+                                 void *workspace, size_t workspace_bytes, int32_t *status_dev, vit_stream_t stream);
+
 /* Workspace bytes of vit_prefix_attn for these sizes (0 for invalid ones). */
 size_t vit_prefix_attn_workspace_size(int64_t Tq, int64_t Tp, int64_t Tk, int Hq, int Hkv, int D, int B, int G,
                                       int max_q, int max_p, int max_k);

@@ -123,6 +123,7 @@ def check(ql, kl, Hq, Hk, D, window=0, sinks=0, prefixes=None, groups=None, loos
     G, Tp = (len(prefixes), sum(prefixes)) if prefixes else (0, 0)
     max_q, max_k = (Tq, sum(kl)) if loose else (max(ql), max(kl))
     max_p = (Tp if loose else max(prefixes)) if prefixes else 0
+    window = 0 if window >= max_k else window          # it leaves nothing out
     sinks = sinks if window else 0
     p = plan(Tq, B, Hq, Hk, D, max_q, max_k, window, sinks, G, Tp, max_p)
     if prefixes is not None:

@@ -42,6 +42,8 @@ def _declare_block(L):
              [vp] * 3 + [i64] * 3 + [i32, vp, sz, vp, vp]),
             ("vit_window_attn", [vp] * 3 + [i64, i64, i32, i32, i32] + [i64] * 3 + [vp] * 3 + [i32] * 5 +
              [f32, vp, i64, vp, vp, sz, vp, vp]),
+            ("vit_window_attn_bwd", [vp] * 6 + [i64, i64, i32, i32, i32] + [i64] * 5 + [vp] * 3 + [i32] * 5 + [f32] +
+             [vp] * 3 + [i64] * 3 + [i32, vp, sz, vp, vp]),
             ("vit_prefix_attn", [vp] * 5 + [i64] * 3 + [i32] * 3 + [i64] * 5 + [vp] * 5 + [i32] * 5 +
              [f32, vp, i64, vp, vp, sz, vp, vp]),
             ("vit_norm_residual", [vp] * 7 + [i64, i32, i32] + [i64] * 5 + [f32, f32, vp]),
@@ -52,6 +54,7 @@ def _declare_block(L):
                        ("vit_cross_attn_workspace_size", [i64, i64] + [i32] * 6),
                        ("vit_cross_attn_bwd_workspace_size", [i64, i64] + [i32] * 6),
                        ("vit_window_attn_workspace_size", [i64, i64] + [i32] * 8),
+                       ("vit_window_attn_bwd_workspace_size", [i64, i64] + [i32] * 8),
                        ("vit_prefix_attn_workspace_size", [i64] * 3 + [i32] * 8),
                        ("vit_norm_residual_bwd_workspace_size", [i32])):
         fn = getattr(L, name)
@@ -710,6 +713,12 @@ def cross_attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
     """Gradient of cross_attn: from dout and the forward call's inputs and results returns (dq, dk, dv), dk and dv
     summed over the query heads that share a key head. Rows of no sequence are 0 in the tensors the call
     allocates and left as they were in dq, dk, dv buffers it is given."""
+    return _attn_bwd("vit_cross_attn_bwd", (), dout, q, k, v, out, lse, cu_q, cu_k, max_q, max_k, scale, k_len, dq, dk,
+                     dv, workspace, status, stream)
+
+
+def _attn_bwd(fn, mask, dout, q, k, v, out, lse, cu_q, cu_k, max_q, max_k, scale, k_len, dq, dk, dv, workspace, status,
+              stream):
     Tq, Hq, D = _shape3(q, "q")
     Tk, Hkv, _ = _shape3(k, "k")
     dev = _device(dout, q, k, v, out, lse, cu_q, cu_k, k_len, dq, dk, dv, workspace, status)
@@ -725,10 +734,10 @@ def cross_attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
         dq, dk, dv = (_new(q, n, _BF16, stream) for n in ((Tq, Hq, D), (Tk, Hkv, D), (Tk, Hkv, D)))
     dqs, dks, dvs = _rows3(dq, "dq", Tq, Hq, D), _rows3(dk, "dk", Tk, Hkv, D), _rows3(dv, "dv", Tk, Hkv, D)
     if workspace is None:
-        workspace = _scratch(_size("vit_cross_attn_bwd_workspace_size", Tq, Tk, Hq, Hkv, D, B, max_q, max_k), q, stream)
-    _call("vit_cross_attn_bwd", dev, stream, _addr(dout), _addr(q), _addr(k), _addr(v), _addr(out), _addr(lse), Tq,
+        workspace = _scratch(_size(fn + "_workspace_size", Tq, Tk, Hq, Hkv, D, B, max_q, max_k, *mask), q, stream)
+    _call(fn, dev, stream, _addr(dout), _addr(q), _addr(k), _addr(v), _addr(out), _addr(lse), Tq,
           Tk, Hq, Hkv, D, dos, qs, ks, vs, os_, _addr(cu_q), _addr(cu_k), _addr(k_len), B, max_q, max_k,
-          0.0 if scale is None else float(scale), _addr(dq), _addr(dk), _addr(dv), dqs, dks, dvs,
+          *mask, 0.0 if scale is None else float(scale), _addr(dq), _addr(dk), _addr(dv), dqs, dks, dvs,
           0 if given[0] else 1, _addr(workspace), _bytes(workspace), _word(status))
     if B == 0 and not given[0]:                        # the library does nothing at all without sequences
         with torch.cuda.stream(stream):
@@ -741,6 +750,12 @@ def window_attn_workspace_size(Tq: int, Tk: int, Hq: int, Hkv: int, D: int, B: i
                                window: int = 0, sinks: int = 0) -> int:
     return int(lib().vit_window_attn_workspace_size(int(Tq), int(Tk), int(Hq), int(Hkv), int(D), int(B), int(max_q),
                                                     int(max_k), int(window), int(sinks)))
+
+
+def window_attn_bwd_workspace_size(Tq: int, Tk: int, Hq: int, Hkv: int, D: int, B: int, max_q: int = 0,
+                                   max_k: int = 0, window: int = 0, sinks: int = 0) -> int:
+    return int(lib().vit_window_attn_bwd_workspace_size(int(Tq), int(Tk), int(Hq), int(Hkv), int(D), int(B),
+                                                        int(max_q), int(max_k), int(window), int(sinks)))
 
 
 def prefix_attn_workspace_size(Tq: int, Tp: int, Tk: int, Hq: int, Hkv: int, D: int, B: int, G: int, max_q: int = 0,
@@ -789,6 +804,20 @@ def window_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.T
           _addr(cu_k), _addr(k_len), B, max_q, max_k, window, sinks, 0.0 if scale is None else float(scale),
           _addr(out), os_, _addr(lse), _addr(workspace), _bytes(workspace), _word(status))
     return (out, lse) if lse is not None else out
+
+
+def window_attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                    lse: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor, max_q: int | None = None,
+                    max_k: int | None = None, window: int | None = None, sinks: int = 0, scale: float | None = None, *,
+                    k_len: torch.Tensor | None = None, dq: torch.Tensor | None = None, dk: torch.Tensor | None = None,
+                    dv: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                    status: torch.Tensor | None = None, stream=None):
+    """Gradient of window_attn: from dout and the forward call's inputs and results returns (dq, dk, dv), dk and dv
+    summed over the query heads that share a key head. Keys that no query sees and queries that see no key get 0; rows
+    of no sequence are as in cross_attn_bwd."""
+    window, sinks = _window(window, sinks)
+    return _attn_bwd("vit_window_attn_bwd", (window, sinks), dout, q, k, v, out, lse, cu_q, cu_k, max_q, max_k, scale,
+                     k_len, dq, dk, dv, workspace, status, stream)
 
 
 def prefix_attn(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Tensor, k: torch.Tensor, v: torch.Tensor,

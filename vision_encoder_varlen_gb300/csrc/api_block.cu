@@ -210,6 +210,68 @@ vit_status_t check_cross(const void *q, const void *k, const void *v, int64_t Tk
     return VIT_OK;
 }
 
+CrossArgs forward_args(const void *q, const void *k, const void *v, int64_t Tq, int64_t Tk, int Hq, int Hkv, int D,
+                       int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t *cu_q, const int32_t *cu_k,
+                       const int32_t *k_len, int B, int max_q, int max_k, float scale, void *out, int64_t out_stride,
+                       float *lse, void *workspace, int32_t *status)
+{
+    CrossArgs a{};
+    a.q = q;
+    a.k = Tk > 0 ? k : q;                       // no keys anywhere: never read, but a map needs an address
+    a.v = Tk > 0 ? v : q;
+    a.k_stride = Tk > 0 ? k_stride : (int64_t)Hkv * D;
+    a.v_stride = Tk > 0 ? v_stride : (int64_t)Hkv * D;
+    a.out = out;
+    a.lse = lse;
+    a.Hq = Hq;
+    a.Hk = Hkv;
+    a.D = D;
+    a.q_stride = q_stride;
+    a.out_stride = out_stride;
+    a.scale_log2 = (scale <= 0.f ? 1.0f / sqrtf((float)D) : scale) * 1.4426950408889634f;
+    a.segs = CrossSegs{cu_q, cu_k, k_len, B, Tq, Tk, max_q, max_k};
+    a.workspace = workspace;
+    a.status = status;
+    return a;
+}
+
+// the checks that the gradients of these share, and what they launch with
+vit_status_t check_grad(const void *dout, const void *q, const void *k, const void *v, const void *out,
+                        const float *lse, int64_t Tq, int64_t Tk, int Hq, int Hkv, int D, int64_t dout_stride,
+                        int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t out_stride, const int32_t *cu_q,
+                        const int32_t *cu_k, const int32_t *k_len, int B, int max_q, int max_k, float scale, void *dq,
+                        void *dk, void *dv, int64_t dq_stride, int64_t dk_stride, int64_t dv_stride, int zero_rest,
+                        void *workspace, int32_t *status, CrossGradArgs &a)
+{
+    // with no rows on one side nothing of it is read: the other side's address stands in for the maps
+    if (Tq == 0) {
+        q = dout = out = k;
+        q_stride = dout_stride = out_stride = (int64_t)Hq * D;
+    }
+    const vit_status_t st = check_cross(q, k, v, Tk, Hq, Hkv, D, q_stride, k_stride, v_stride, cu_q, cu_k, k_len, scale);
+    if (st != VIT_OK) return st;
+    if (!workspace || (Tq > 0 && (!dout || !out || !lse || !dq)) || (Tk > 0 && (!dk || !dv))) return VIT_ERR_NULL_POINTER;
+    const int64_t nq = (int64_t)Hq * D, nk = (int64_t)Hkv * D;
+    if (!stride_ok(dout_stride, nq) || !stride_ok(out_stride, nq) || (Tq > 0 && !stride_ok(dq_stride, nq)) ||
+        (Tk > 0 && (!stride_ok(dk_stride, nk) || !stride_ok(dv_stride, nk))))
+        return VIT_ERR_BAD_STRIDE;
+    if (!aligned16(dout) || !aligned16(out) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv) ||
+        ((uintptr_t)lse & 3u) || !aligned16(workspace))
+        return VIT_ERR_MISALIGNED;
+    a.f = forward_args(q, k, v, Tq, Tk, Hq, Hkv, D, q_stride, k_stride, v_stride, cu_q, cu_k, k_len, B, max_q, max_k,
+                       scale, const_cast<void *>(out), out_stride, const_cast<float *>(lse), workspace, status);
+    a.dout = dout;
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    a.dout_stride = dout_stride;
+    a.dq_stride = dq_stride;
+    a.dk_stride = dk_stride;
+    a.dv_stride = dv_stride;
+    a.zero_rest = zero_rest != 0;
+    return VIT_OK;
+}
+
 }  // namespace
 
 size_t vit_cross_attn_workspace_size(int64_t Tq, int64_t Tk, int Hq, int Hkv, int D, int B, int max_q, int max_k)
@@ -245,23 +307,8 @@ vit_status_t vit_cross_attn(const void *q, const void *k, const void *v, int64_t
     int sms = 0;
     st = check_device(&sms);
     if (st != VIT_OK) return st;
-    CrossArgs a{};
-    a.q = q;
-    a.k = Tk > 0 ? k : q;                       // no keys anywhere: never read, but a map needs an address
-    a.v = Tk > 0 ? v : q;
-    a.k_stride = Tk > 0 ? k_stride : q_stride;
-    a.v_stride = Tk > 0 ? v_stride : q_stride;
-    a.out = out;
-    a.lse = lse;
-    a.Hq = Hq;
-    a.Hk = Hkv;
-    a.D = D;
-    a.q_stride = q_stride;
-    a.out_stride = out_stride;
-    a.scale_log2 = (scale <= 0.f ? 1.0f / sqrtf((float)D) : scale) * 1.4426950408889634f;
-    a.segs = CrossSegs{cu_q, cu_k, k_len, B, Tq, Tk, max_q, max_k};
-    a.workspace = workspace;
-    a.status = status_dev;
+    const CrossArgs a = forward_args(q, k, v, Tq, Tk, Hq, Hkv, D, q_stride, k_stride, v_stride, cu_q, cu_k, k_len, B,
+                                     max_q, max_k, scale, out, out_stride, lse, workspace, status_dev);
     cudaStream_t s = (cudaStream_t)stream;
     if (takes_few(B, Hq, Hkv, D, max_q, max_k))
         return from_cuda(launch_cross_few(a, few_plan(B, Hq, Hkv, D, max_q, max_k), s));
@@ -302,53 +349,17 @@ vit_status_t vit_cross_attn_bwd(const void *dout, const void *q, const void *k, 
     vit_status_t st = cross_sizes(Tq, Tk, Hq, Hkv, D, B, &max_q, &max_k);
     if (st != VIT_OK) return st;
     if (B == 0 || (Tq == 0 && Tk == 0)) return VIT_OK;
-    // with no rows on one side nothing of it is read: the other side's address stands in for the maps
-    if (Tq == 0) {
-        q = dout = out = k;
-        q_stride = dout_stride = out_stride = (int64_t)Hq * D;
-    }
-    st = check_cross(q, k, v, Tk, Hq, Hkv, D, q_stride, k_stride, v_stride, cu_q, cu_k, k_len, scale);
+    CrossGradArgs a{};
+    st = check_grad(dout, q, k, v, out, lse, Tq, Tk, Hq, Hkv, D, dout_stride, q_stride, k_stride, v_stride, out_stride,
+                    cu_q, cu_k, k_len, B, max_q, max_k, scale, dq, dk, dv, dq_stride, dk_stride, dv_stride, zero_rest,
+                    workspace, status_dev, a);
     if (st != VIT_OK) return st;
-    if (!workspace || (Tq > 0 && (!dout || !out || !lse || !dq)) || (Tk > 0 && (!dk || !dv))) return VIT_ERR_NULL_POINTER;
-    const int64_t nq = (int64_t)Hq * D, nk = (int64_t)Hkv * D;
-    if (!stride_ok(dout_stride, nq) || !stride_ok(out_stride, nq) || (Tq > 0 && !stride_ok(dq_stride, nq)) ||
-        (Tk > 0 && (!stride_ok(dk_stride, nk) || !stride_ok(dv_stride, nk))))
-        return VIT_ERR_BAD_STRIDE;
-    if (!aligned16(dout) || !aligned16(out) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv) ||
-        ((uintptr_t)lse & 3u) || !aligned16(workspace))
-        return VIT_ERR_MISALIGNED;
     const size_t need = vit_cross_attn_bwd_workspace_size(Tq, Tk, Hq, Hkv, D, B, max_q, max_k);
     if (need == 0) return VIT_ERR_BAD_SHAPE;
     if (workspace_bytes < need) return VIT_ERR_WORKSPACE_TOO_SMALL;
     int sms = 0;
     st = check_device(&sms);
     if (st != VIT_OK) return st;
-    CrossGradArgs a{};
-    a.f.q = q;
-    a.f.k = Tk > 0 ? k : q;
-    a.f.v = Tk > 0 ? v : q;
-    a.f.k_stride = Tk > 0 ? k_stride : nk;
-    a.f.v_stride = Tk > 0 ? v_stride : nk;
-    a.f.out = const_cast<void *>(out);
-    a.f.lse = const_cast<float *>(lse);
-    a.f.Hq = Hq;
-    a.f.Hk = Hkv;
-    a.f.D = D;
-    a.f.q_stride = q_stride;
-    a.f.out_stride = out_stride;
-    a.f.scale_log2 = (scale <= 0.f ? 1.0f / sqrtf((float)D) : scale) * 1.4426950408889634f;
-    a.f.segs = CrossSegs{cu_q, cu_k, k_len, B, Tq, Tk, max_q, max_k};
-    a.f.workspace = workspace;
-    a.f.status = status_dev;
-    a.dout = dout;
-    a.dq = dq;
-    a.dk = dk;
-    a.dv = dv;
-    a.dout_stride = dout_stride;
-    a.dq_stride = dq_stride;
-    a.dk_stride = dk_stride;
-    a.dv_stride = dv_stride;
-    a.zero_rest = zero_rest != 0;
     return from_cuda(launch_cross_grad(a, grad_plan(Tq, Tk, B, Hq, Hkv, D, max_q, max_k), sms, (cudaStream_t)stream));
 }
 
@@ -356,38 +367,14 @@ vit_status_t vit_cross_attn_bwd(const void *dout, const void *q, const void *k, 
 
 namespace {
 
-CrossArgs forward_args(const void *q, const void *k, const void *v, int64_t Tq, int64_t Tk, int Hq, int Hkv, int D,
-                       int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t *cu_q, const int32_t *cu_k,
-                       const int32_t *k_len, int B, int max_q, int max_k, float scale, void *out, int64_t out_stride,
-                       float *lse, void *workspace, int32_t *status)
-{
-    CrossArgs a{};
-    a.q = q;
-    a.k = Tk > 0 ? k : q;                       // no keys anywhere: never read, but a map needs an address
-    a.v = Tk > 0 ? v : q;
-    a.k_stride = Tk > 0 ? k_stride : (int64_t)Hkv * D;
-    a.v_stride = Tk > 0 ? v_stride : (int64_t)Hkv * D;
-    a.out = out;
-    a.lse = lse;
-    a.Hq = Hq;
-    a.Hk = Hkv;
-    a.D = D;
-    a.q_stride = q_stride;
-    a.out_stride = out_stride;
-    a.scale_log2 = (scale <= 0.f ? 1.0f / sqrtf((float)D) : scale) * 1.4426950408889634f;
-    a.segs = CrossSegs{cu_q, cu_k, k_len, B, Tq, Tk, max_q, max_k};
-    a.workspace = workspace;
-    a.status = status;
-    return a;
-}
-
-vit_status_t window_sizes(int64_t Tq, int64_t Tk, int Hq, int Hkv, int D, int B, int *max_q, int *max_k, int window,
+vit_status_t window_sizes(int64_t Tq, int64_t Tk, int Hq, int Hkv, int D, int B, int *max_q, int *max_k, int *window,
                           int *sinks)
 {
     const vit_status_t st = cross_sizes(Tq, Tk, Hq, Hkv, D, B, max_q, max_k);
     if (st != VIT_OK) return st;
-    if (window < 0 || *sinks < 0) return VIT_ERR_BAD_ARGUMENT;
-    if (window == 0) *sinks = 0;
+    if (*window < 0 || *sinks < 0) return VIT_ERR_BAD_ARGUMENT;
+    if (*window >= *max_k) *window = 0;         // it leaves nothing out
+    if (*window == 0) *sinks = 0;
     return VIT_OK;
 }
 
@@ -398,7 +385,7 @@ constexpr int64_t kMaxItems = (int64_t)1 << 31;
 size_t vit_window_attn_workspace_size(int64_t Tq, int64_t Tk, int Hq, int Hkv, int D, int B, int max_q, int max_k,
                                       int window, int sinks)
 {
-    if (window_sizes(Tq, Tk, Hq, Hkv, D, B, &max_q, &max_k, window, &sinks) != VIT_OK) return 0;
+    if (window_sizes(Tq, Tk, Hq, Hkv, D, B, &max_q, &max_k, &window, &sinks) != VIT_OK) return 0;
     if (B == 0 || Tq == 0) return 16;
     if (window_takes_few(B, Hq, Hkv, D, max_q, max_k, window, sinks)) {
         const size_t n = window_few_plan(B, Hq, Hkv, D, max_q, max_k, window, sinks).partial_bytes;
@@ -415,7 +402,7 @@ vit_status_t vit_window_attn(const void *q, const void *k, const void *v, int64_
                              size_t workspace_bytes, int32_t *status_dev, vit_stream_t stream)
 {
     TraceRange trace("vit_window_attn");
-    vit_status_t st = window_sizes(Tq, Tk, Hq, Hkv, D, B, &max_q, &max_k, window, &sinks);
+    vit_status_t st = window_sizes(Tq, Tk, Hq, Hkv, D, B, &max_q, &max_k, &window, &sinks);
     if (st != VIT_OK) return st;
     if (B == 0 || Tq == 0) return VIT_OK;
     st = check_cross(q, k, v, Tk, Hq, Hkv, D, q_stride, k_stride, v_stride, cu_q, cu_k, k_len, scale);
@@ -438,6 +425,41 @@ vit_status_t vit_window_attn(const void *q, const void *k, const void *v, int64_
     if (window_takes_few(B, Hq, Hkv, D, max_q, max_k, window, sinks))
         return from_cuda(launch_window_few(a, window_few_plan(B, Hq, Hkv, D, max_q, max_k, window, sinks), s));
     return from_cuda(launch_window_tiles(a, win_plan(Tq, B, Hq, Hkv, D, max_q, max_k, window, sinks, 0, 0, 0), sms, s));
+}
+
+size_t vit_window_attn_bwd_workspace_size(int64_t Tq, int64_t Tk, int Hq, int Hkv, int D, int B, int max_q, int max_k,
+                                          int window, int sinks)
+{
+    if (window_sizes(Tq, Tk, Hq, Hkv, D, B, &max_q, &max_k, &window, &sinks) != VIT_OK) return 0;
+    const GradPlan p = window_grad_plan(Tq, Tk, B, Hq, Hkv, D, max_q, max_k);
+    return p.max_dq >= kMaxItems || p.max_dkv >= kMaxItems ? 0 : p.bytes;
+}
+
+vit_status_t vit_window_attn_bwd(const void *dout, const void *q, const void *k, const void *v, const void *out,
+                                 const float *lse, int64_t Tq, int64_t Tk, int Hq, int Hkv, int D,
+                                 int64_t dout_stride, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                 int64_t out_stride, const int32_t *cu_q, const int32_t *cu_k, const int32_t *k_len,
+                                 int B, int max_q, int max_k, int window, int sinks, float scale, void *dq, void *dk,
+                                 void *dv, int64_t dq_stride, int64_t dk_stride, int64_t dv_stride, int zero_rest,
+                                 void *workspace, size_t workspace_bytes, int32_t *status_dev, vit_stream_t stream)
+{
+    TraceRange trace("vit_window_attn_bwd");
+    vit_status_t st = window_sizes(Tq, Tk, Hq, Hkv, D, B, &max_q, &max_k, &window, &sinks);
+    if (st != VIT_OK) return st;
+    if (B == 0 || (Tq == 0 && Tk == 0)) return VIT_OK;
+    CrossGradArgs a{};
+    st = check_grad(dout, q, k, v, out, lse, Tq, Tk, Hq, Hkv, D, dout_stride, q_stride, k_stride, v_stride, out_stride,
+                    cu_q, cu_k, k_len, B, max_q, max_k, scale, dq, dk, dv, dq_stride, dk_stride, dv_stride, zero_rest,
+                    workspace, status_dev, a);
+    if (st != VIT_OK) return st;
+    const size_t need = vit_window_attn_bwd_workspace_size(Tq, Tk, Hq, Hkv, D, B, max_q, max_k, window, sinks);
+    if (need == 0) return VIT_ERR_BAD_SHAPE;
+    if (workspace_bytes < need) return VIT_ERR_WORKSPACE_TOO_SMALL;
+    int sms = 0;
+    st = check_device(&sms);
+    if (st != VIT_OK) return st;
+    return from_cuda(launch_window_grad(a, window_grad_plan(Tq, Tk, B, Hq, Hkv, D, max_q, max_k), window, sinks, sms,
+                                        (cudaStream_t)stream));
 }
 
 // the sizes of a call with prefixes

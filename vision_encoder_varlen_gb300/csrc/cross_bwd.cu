@@ -50,11 +50,18 @@
 // operand (of S and dP, reduced over D) and as an MN-major one (of the sums, reduced over rows).
 // Streamed rows past the sequence's end enter the sums with P = dS = 0 and are zeroed in shared memory
 // first (0 * NaN is NaN), the last 16-row step included.
+//
+// A causal window (WIN) leaves a tile only a part of the other side: a key tile the queries from its first key's position
+// on, up to the window behind its last key's or, where it holds first tokens that stay visible, to the end; a query
+// tile the first tokens and the run of keys that its rows see between them. Pairs that the mask excludes inside those
+// tiles have P = dS = 0 exactly, whatever their scores are. delta is from the scores for every row that sees 2 to 16
+// keys (the first rows of each sequence, all rows of a window of so many), made with the other statistics.
 #include <type_traits>
 
 #include "block_sort.cuh"
 #include "cross.h"
 #include "sm100.cuh"
+#include "window.h"
 
 namespace vit {
 namespace {
@@ -132,6 +139,12 @@ struct Grad {
 struct GradMaps {
     CUtensorMap x1, x2, y1, y2;
 };
+struct WinGrad : Grad {
+    const WinGradItem *win_items;
+    int window, sinks;
+};
+__device__ __forceinline__ const GradItem *items_of(const Grad &p) { return p.items; }
+__device__ __forceinline__ const WinGradItem *items_of(const WinGrad &p) { return p.win_items; }
 
 template <int D> struct GradShared {
     Bars bars;
@@ -140,10 +153,13 @@ template <int D> struct GradShared {
     alignas(16) float stat[2][2][GradCfg<D, true>::BN];    // dk, dv: [group][-lse2 | -delta][column]
 };
 
-template <int D, bool DKV>
-__device__ __forceinline__ void grad_pass(const GradMaps &tm, const Grad &p, GradShared<D> &sh)
+template <int D, bool DKV, bool WIN>
+__device__ __forceinline__ void grad_pass(const GradMaps &tm, const std::conditional_t<WIN, WinGrad, Grad> &p,
+                                          GradShared<D> &sh)
 {
     using C = GradCfg<D, DKV>;
+    using GradItem = std::conditional_t<WIN, WinGradItem, vit::GradItem>;
+    const GradItem *items = items_of(p);
     constexpr int BN = C::BN, NY = C::NY, W = C::W;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *base = reinterpret_cast<unsigned char *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -188,6 +204,17 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const Grad &p, Gra
         return (int)b - p.first_block;
     };
     auto list_length = [&] { return *static_cast<const volatile int32_t *>(p.n_items); };
+    // The block's next item. A windowed list's items shorten from first to last within a round of the blocks, so the
+    // next round goes the other way.
+    auto next_item = [&](int i) {
+        if constexpr (WIN) return i + 2 * (p.n_blocks - i % p.n_blocks) - 1;
+        else return i + p.n_blocks;
+    };
+    // tiles of the keys that a windowed query tile reads first
+    auto first_tiles = [&](const GradItem &it) -> int {
+        if constexpr (WIN && !DKV) return (it.fn + BN - 1) / BN;
+        else return 0;
+    };
 
     auto wait = [&](const uint64_t &b, uint32_t parity) -> bool {
         if (mbar_wait(bar_addr(b), parity, (const volatile int *)&s_abort, kWaitBudget)) return true;
@@ -206,6 +233,9 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const Grad &p, Gra
         if constexpr (DKV) {
             const int nt = (it.ln + y_tok - 1) / y_tok;
             return min(y_tok, it.ln - j % nt * y_tok) << p.lg_pack;
+        } else if constexpr (WIN) {
+            const int nf = first_tiles(it);
+            return min(BN, j < nf ? it.fn - j * BN : it.ln - (j - nf) * BN);
         } else {
             return min(BN, it.ln - j * BN);
         }
@@ -221,8 +251,8 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const Grad &p, Gra
             tma_prefetch_desc(&tm.y2);
             uint32_t xc = 0, yc = 0;
             bool ok = true;
-            for (int i = block(), n_items = list_length(); ok && i < n_items; i += p.n_blocks) {
-                const GradItem it = p.items[i];
+            for (int i = block(), n_items = list_length(); ok && i < n_items; i = next_item(i)) {
+                const GradItem it = items[i];
                 if (it.tiles == 0) continue;
                 const uint32_t xb = xc & 1;
                 if (xc >= 2 && !(ok = wait(bars.x_empty[xb], (xc / 2 - 1) & 1))) break;
@@ -243,8 +273,12 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const Grad &p, Gra
                         head = it.head * p.group + ((j / nt) << p.lg_pack);
                         row = it.l0 + j % nt * y_tok;
                     } else {
+                        const int nf = first_tiles(it);
                         head = it.head / p.group;
-                        row = it.l0 + j * BN;
+                        row = it.l0 + (j - nf) * BN;
+                        if constexpr (WIN) {
+                            if (j < nf) row = it.f0 + j * BN;
+                        }
                     }
                     mbar_arrive_expect_tx(bar_addr(bars.y_full[s]), 2 * C::Y_TILE);
 #pragma unroll
@@ -340,18 +374,22 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const Grad &p, Gra
             }
             return true;
         };
-        for (int i = block(), n_items = list_length(); ok && i < n_items; i += p.n_blocks) {
-            const GradItem it = p.items[i];
+        for (int i = block(), n_items = list_length(); ok && i < n_items; i = next_item(i)) {
+            const GradItem it = items[i];
             const int n = uni(it.tiles);
             if (n == 0) continue;
             // tiles follow one another inside a head pack; the last one of a pack holds `tail` rows
-            const int nt = DKV ? uni((it.ln + y_tok - 1) / y_tok) : uni((it.ln + BN - 1) / BN);
+            const int nt = DKV ? uni((it.ln + y_tok - 1) / y_tok) : WIN ? n : uni((it.ln + BN - 1) / BN);
             const int tail = uni(valid_rows(it, nt - 1)), tail_steps = (tail + 15) >> 4;
+            // (a windowed query tile's first keys may end inside a tile of their own)
+            const int nf = WIN && !DKV ? uni(first_tiles(it)) : 0;
+            const int f_tail = WIN && !DKV ? uni(nf > 0 ? valid_rows(it, nf - 1) : BN) : BN, f_steps = (f_tail + 15) >> 4;
             int pj = 0, aj = 0;                              // place in its pack of the next tile to start, to add up
             auto next_valid = [&]() {
                 const bool end = ++pj == nt;
+                const int v = end ? tail : WIN && !DKV && pj == nf ? f_tail : BN;
                 pj = end ? 0 : pj;
-                return end ? tail : BN;
+                return v;
             };
             const uint32_t xb = xc & 1, x_empty = bar_addr(bars.x_empty[0]) + 8 * xb;
             const uint64_t dx = dx0 + xb * (2 * C::X_TILE >> 4);
@@ -362,10 +400,11 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const Grad &p, Gra
             uint32_t acc = 0;
             for (int j = 0; j < n; ++j) {
                 const bool end = ++aj == nt;
+                const int steps = end ? tail_steps : WIN && !DKV && aj == nf ? f_steps : BN / 16;
                 aj = end ? 0 : aj;
                 if (!(ok = wait_warp(bars.p_full[st], ph_s))) break;
                 tc_fence_after();
-                if (leader) sums(tS, dm, end ? tail_steps : BN / 16, acc, a_yempty + 8 * s_a);
+                if (leader) sums(tS, dm, steps, acc, a_yempty + 8 * s_a);
                 if (j + 1 == n && leader) mma_commit(bar_addr(bars.acc_done));
                 __syncwarp();
                 acc = 1;
@@ -429,8 +468,8 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const Grad &p, Gra
             constexpr int PER = (BN + 31) / 32;
             uint32_t u0 = 0;
             bool ok = true;
-            for (int i = block(), n_items = list_length(); ok && i < n_items; i += p.n_blocks) {
-                const GradItem it = p.items[i];
+            for (int i = block(), n_items = list_length(); ok && i < n_items; i = next_item(i)) {
+                const GradItem it = items[i];
                 const int n = it.tiles;
                 if (n == 0) continue;
                 const int nt = (it.ln + y_tok - 1) / y_tok;
@@ -475,8 +514,8 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const Grad &p, Gra
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
         uint32_t u0 = 0, xc = 0;                              // tiles and items with tiles before this item
         bool ok = true;
-        for (int i = block(), n_items = list_length(); ok && i < n_items; i += p.n_blocks) {
-            const GradItem it = p.items[i];
+        for (int i = block(), n_items = list_length(); ok && i < n_items; i = next_item(i)) {
+            const GradItem it = items[i];
             const int n = it.tiles;
             // the row of the output that this lane holds
             int o_row, o_head;
@@ -504,6 +543,25 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const Grad &p, Gra
                     if (!(ok = wait_warp(bars.s_full[st], (u / 2) & 1))) break;
                     tc_fence_after();
                     const uint32_t tS = t_lane + C::TSTAGE + st * 2 * BN, tD = tS + BN;
+                    // WIN: what this lane sees of the tile: columns before `hi`, from `lo` on or before `sk`
+                    [[maybe_unused]] int hi = valid, lo = 0, sk = 0;
+                    if constexpr (WIN && DKV) {                // the columns of a token lie side by side
+                        const int nt = (it.ln + y_tok - 1) / y_tok;
+                        const int d = it.rp + row - (it.lp + j % nt * y_tok);     // this key against the first token
+                        lo = min(max(d, 0), BN) << p.lg_pack;
+                        if (p.window > 0 && it.rp + row >= p.sinks)
+                            hi = min(hi, min(max(d + p.window, 0), BN) << p.lg_pack);
+                    } else if constexpr (WIN) {
+                        const int nf = first_tiles(it);
+                        if (j >= nf) {
+                            const int kp = it.lp + (j - nf) * BN, d = it.rp + (row >> p.lg_pack) - kp;
+                            hi = min(hi, d + 1);
+                            if (p.window > 0) {
+                                lo = d - p.window + 1;
+                                sk = p.sinks - kp;
+                            }
+                        }
+                    }
                     if constexpr (decltype(exact)::value) {
                         // few keys, all of them in this tile: delta = sum_j p_ij dP_ij, in dq over this lane's
                         // columns, in dk, dv for each column over the lanes of the one warp that has keys (what the
@@ -591,7 +649,18 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const Grad &p, Gra
                             sr[c / 2] = pack_bf16x2(p0, p1);
                             dr[c / 2] = pack_bf16x2(g0, g1);
                         }
-                        if (valid < C0 + CN) {                    // columns past the end: exactly 0, whatever was there
+                        if constexpr (WIN) {
+                            if (__any_sync(0xffffffffu, hi < C0 + CN || lo > C0)) {
+#pragma unroll
+                                for (int c = 0; c < CN; c += 2) {
+                                    const int x = C0 + c;
+                                    const uint32_t a = x < hi && (x >= lo || x < sk) ? 0x0000ffffu : 0u;
+                                    const uint32_t b = x + 1 < hi && (x + 1 >= lo || x + 1 < sk) ? 0xffff0000u : 0u;
+                                    sr[c / 2] &= a | b;
+                                    dr[c / 2] &= a | b;
+                                }
+                            }
+                        } else if (valid < C0 + CN) {             // columns past the end: exactly 0, whatever was there
 #pragma unroll
                             for (int c = 0; c < CN; c += 2) {
                                 const int x = C0 + c;
@@ -620,8 +689,12 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const Grad &p, Gra
                 }
             };
             using std::bool_constant;
-            if (it.exact) tiles(bool_constant<true>());
-            else tiles(bool_constant<false>());
+            if constexpr (WIN) {
+                tiles(bool_constant<false>());
+            } else {
+                if (it.exact) tiles(bool_constant<true>());
+                else tiles(bool_constant<false>());
+            }
             if (!ok) break;
             u0 += n;
             // ---- the item's sums: group 0 writes dk, group 1 dv; of dq each writes half of the columns
@@ -678,9 +751,21 @@ cross_grad_kernel(const __grid_constant__ GradMaps tm_dkv, const __grid_constant
 {
     __shared__ GradShared<D> sh;
     if ((int)blockIdx.x < dkv.n_blocks)
-        grad_pass<D, true>(tm_dkv, dkv, sh);
+        grad_pass<D, true, false>(tm_dkv, dkv, sh);
     else
-        grad_pass<D, false>(tm_dq, dq, sh);
+        grad_pass<D, false, false>(tm_dq, dq, sh);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+window_grad_kernel(const __grid_constant__ GradMaps tm_dkv, const __grid_constant__ GradMaps tm_dq,
+                   const __grid_constant__ WinGrad dkv, const __grid_constant__ WinGrad dq)
+{
+    __shared__ GradShared<D> sh;
+    if ((int)blockIdx.x < dkv.n_blocks)
+        grad_pass<D, true, true>(tm_dkv, dkv, sh);
+    else
+        grad_pass<D, false, true>(tm_dq, dq, sh);
 }
 
 // ------------------------------------------------------------------ lists and statistics
@@ -688,8 +773,9 @@ cross_grad_kernel(const __grid_constant__ GradMaps tm_dkv, const __grid_constant
 // One list of work items by one block of 1024 threads: the dk, dv tiles (`keys`, ordered by query
 // count) or the dq tiles (ordered by key count), longest loop first. Tiles without a loop are listed
 // too: their gradients are 0.
+template <bool W>
 __device__ void make_list(bool keys, const CrossSegs &segs, int Hq, int Hk, int lg_pack, int bn, int32_t *counts,
-                          GradItem *items, int32_t *status)
+                          std::conditional_t<W, WinGradItem, GradItem> *items, int32_t *status, int window, int sinks)
 {
     constexpr int kThreads = kSortThreads;
     extern __shared__ unsigned long long s_key[];      // [NP] loop length descending, then index; later first item | index
@@ -760,18 +846,55 @@ __device__ void make_list(bool keys, const CrossSegs &segs, int Hq, int Hk, int 
         const int p = place_of(s_key, s_used, i), n = i - (int)(s_key[p] >> 32);
         CrossSeg x;
         load_seg(segs, (int)(s_key[p] & 0xffffffffu), x, nullptr, false);
-        const int nr = (rows_of(x) + (1 << lg_tile) - 1) >> lg_tile, h = n / nr, r = n - h * nr;
+        const int nr = (rows_of(x) + (1 << lg_tile) - 1) >> lg_tile;
         const int step = keys ? bn >> lg_pack : bn;
-        GradItem it;
-        it.r0 = (keys ? x.k0 : x.q0) + (r << lg_tile);
-        it.r1 = keys ? x.k0 + x.kn : x.q0 + x.qn;
-        it.l0 = keys ? x.q0 : x.k0;
-        it.ln = keys ? x.qn : x.kn;
-        it.head = keys ? h : h << lg_pack;
-        it.tiles = (it.ln + step - 1) / step * (keys ? Hq / Hk >> lg_pack : 1);
-        it.exact = x.kn > 1 && x.kn <= kExactKeys;     // (one key: out is v, and nothing is lost)
-        it.pad = 0;
-        items[i] = it;
+        if constexpr (W) {
+            // all heads of a tile one after the other, the longest tiles first: a sequence's first keys, its last queries
+            const int r = keys ? n / heads : nr - 1 - n / heads, h = n % heads;
+            const int p0 = x.kn - x.qn, a = r << lg_tile, e = min(rows_of(x), a + (1 << lg_tile));
+            WinGradItem it;
+            it.r0 = (keys ? x.k0 : x.q0) + a;
+            it.r1 = keys ? x.k0 + x.kn : x.q0 + x.qn;
+            it.head = keys ? h : h << lg_pack;
+            it.f0 = x.k0;
+            it.fn = 0;
+            if (keys) {                                // queries from the first key's position on
+                const int lo = max(0, a - p0);
+                const int64_t hi = window == 0 || a < sinks ? x.qn : (int64_t)e - 1 + window - p0;
+                it.rp = a;
+                it.lp = p0 + lo;
+                it.l0 = x.q0 + lo;
+                it.ln = (int)max((int64_t)0, min((int64_t)x.qn, hi) - lo);
+                it.tiles = (it.ln + step - 1) / step * (Hq / Hk >> lg_pack);
+            } else {                                   // (queries before the first key see nothing)
+                const int last = p0 + e - 1;
+                it.rp = p0 + a;
+                it.lp = 0;
+                it.ln = 0;
+                if (last >= 0) {
+                    const WinRange w = win_range(it.rp, window, sinks);
+                    it.fn = w.first;
+                    it.lp = w.lo;
+                    it.ln = last + 1 - w.lo;
+                }
+                it.l0 = x.k0 + it.lp;
+                it.tiles = (it.fn + step - 1) / step + (it.ln + step - 1) / step;
+            }
+            it.pad[0] = it.pad[1] = 0;
+            items[i] = it;
+        } else {
+            const int h = n / nr, r = n - h * nr;
+            GradItem it;
+            it.r0 = (keys ? x.k0 : x.q0) + (r << lg_tile);
+            it.r1 = keys ? x.k0 + x.kn : x.q0 + x.qn;
+            it.l0 = keys ? x.q0 : x.k0;
+            it.ln = keys ? x.qn : x.kn;
+            it.head = keys ? h : h << lg_pack;
+            it.tiles = (it.ln + step - 1) / step * (keys ? Hq / Hk >> lg_pack : 1);
+            it.exact = x.kn > 1 && x.kn <= kExactKeys;     // (one key: out is v, and nothing is lost)
+            it.pad = 0;
+            items[i] = it;
+        }
     }
 }
 
@@ -783,20 +906,52 @@ struct Prepare {
     CrossSegs segs;
     int Hq, Hk, lg_pack;
     int32_t *counts;
-    GradItem *dq, *dkv;
+    void *dq, *dkv;               // the lists
     int32_t *status;
+    // W: q, k and v for rows whose delta is from the scores
+    const __nv_bfloat16 *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    int window, sinks;
+    float scale_log2;
 };
 
-template <int D>
+// The keys that row (t, head) sees where those are 2 to kExactKeys: the first `first` of its sequence and `n` in all,
+// the others from position lo on; else n = 0.
+struct FewKeys {
+    int64_t k0;
+    int first, lo, n;
+};
+__device__ __forceinline__ FewKeys few_keys(const Prepare &p, int64_t t)
+{
+    const CrossSegs &s = p.segs;
+    FewKeys none{0, 0, 0, 0};
+    int b = 0, end = s.B;                              // the last sequence that begins at or before t (offsets that
+    while (end - b > 1) {                              // decrease lead nowhere: the call computes nothing then)
+        const int m = (b + end) >> 1;
+        if (s.cu_q[m] <= t) b = m;
+        else end = m;
+    }
+    CrossSeg x;
+    if (!load_seg(s, b, x, nullptr, false) || t < x.q0 || t >= (int64_t)x.q0 + x.qn) return none;
+    const int pos = x.kn - x.qn + (int)(t - x.q0);
+    if (pos < 1) return none;
+    const WinRange w = win_range(pos, p.window, p.sinks);
+    const int64_t n = (int64_t)w.first + pos + 1 - w.lo;
+    if (n < 2 || n > kExactKeys) return none;
+    return FewKeys{x.k0, w.first, w.lo, (int)n};
+}
+
+template <int D, bool W>
 __global__ void __launch_bounds__(kSortThreads)
 cross_grad_prepare_kernel(const Prepare p)
 {
+    using Item = std::conditional_t<W, WinGradItem, GradItem>;
     grid_wait();
     grid_release();
     if (blockIdx.x < 2) {
         const bool keys = blockIdx.x == 1;
-        make_list(keys, p.segs, p.Hq, p.Hk, p.lg_pack, keys ? GradCfg<D, true>::BN : GradCfg<D, false>::BN, p.counts,
-                  keys ? p.dkv : p.dq, p.status);
+        make_list<W>(keys, p.segs, p.Hq, p.Hk, p.lg_pack, keys ? GradCfg<D, true>::BN : GradCfg<D, false>::BN,
+                     p.counts, static_cast<Item *>(keys ? p.dkv : p.dq), p.status, p.window, p.sinks);
         return;
     }
     // D / 8 lanes per row, 16 bytes of o and do each
@@ -820,6 +975,43 @@ cross_grad_prepare_kernel(const Prepare p)
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < CH; ++i) sum += __shfl_sync(0xffffffffu, s, (g * CH + i) & 31);
+        if constexpr (W) {
+            const int64_t t = live ? r / p.Hq : 0;
+            FewKeys f{0, 0, 0, 0};
+            if (live) f = few_keys(p, t);
+            const int most = __reduce_max_sync(0xffffffffu, f.n);
+            if (most > 0) {                            // delta = sum_j p_j (do v_j), over the keys that the row sees
+                const int h = (int)(r - t * p.Hq);
+                const int64_t kv = (int64_t)(h / (p.Hq / p.Hk)) * D + 8 * c;
+                float a[8], b[8], exact = 0.f;
+                if (f.n > 0) {
+                    rope::unpack8(*reinterpret_cast<const uint4 *>(p.q + t * p.q_stride + (int64_t)h * D + 8 * c), a);
+                    rope::unpack8(*reinterpret_cast<const uint4 *>(p.dout + t * p.dout_stride + (int64_t)h * D + 8 * c), b);
+                }
+                for (int j = 0; j < most; ++j) {
+                    float x = 0.f, y = 0.f;
+                    if (j < f.n) {
+                        const int64_t row = f.k0 + (j < f.first ? j : f.lo + j - f.first);
+                        float k[8], v[8];
+                        rope::unpack8(*reinterpret_cast<const uint4 *>(p.k + row * p.k_stride + kv), k);
+                        rope::unpack8(*reinterpret_cast<const uint4 *>(p.v + row * p.v_stride + kv), v);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            x = fmaf(a[e], k[e], x);
+                            y = fmaf(b[e], v[e], y);
+                        }
+                    }
+                    float score = 0.f, dp = 0.f;
+#pragma unroll
+                    for (int i = 0; i < CH; ++i) {
+                        score += __shfl_sync(0xffffffffu, x, (g * CH + i) & 31);
+                        dp += __shfl_sync(0xffffffffu, y, (g * CH + i) & 31);
+                    }
+                    if (j < f.n) exact = fmaf(ex2(fmaf(score, p.scale_log2, -p.lse[r] * 1.4426950408889634f)), dp, exact);
+                }
+                if (f.n > 0) sum = exact;
+            }
+        }
         if (live && c == 0) p.stats[r] = make_float2(-p.lse[r] * 1.4426950408889634f, -sum);
     }
 }
@@ -871,7 +1063,9 @@ bool make_pass(const CrossGradArgs &a, const GradPlan &pl, int num_sms, GradMaps
     return true;
 }
 
-template <int D> cudaError_t launch_d(const CrossGradArgs &a, const GradPlan &pl, int num_sms, cudaStream_t stream)
+template <int D, bool W>
+cudaError_t launch_d(const CrossGradArgs &a, const GradPlan &pl, int window, int sinks, int num_sms,
+                     cudaStream_t stream)
 {
     const CrossSegs &s = a.f.segs;
     char *ws = static_cast<char *>(a.f.workspace);
@@ -889,37 +1083,55 @@ template <int D> cudaError_t launch_d(const CrossGradArgs &a, const GradPlan &pl
     r.Hk = a.f.Hk;
     r.lg_pack = pl.lg_pack;
     r.counts = reinterpret_cast<int32_t *>(ws);
-    r.dq = reinterpret_cast<GradItem *>(ws + pl.off_dq);
-    r.dkv = reinterpret_cast<GradItem *>(ws + pl.off_dkv);
+    r.dq = ws + pl.off_dq;
+    r.dkv = ws + pl.off_dkv;
     r.status = a.f.status;
+    r.q = static_cast<const __nv_bfloat16 *>(a.f.q);
+    r.k = static_cast<const __nv_bfloat16 *>(a.f.k);
+    r.v = static_cast<const __nv_bfloat16 *>(a.f.v);
+    r.q_stride = a.f.q_stride;
+    r.k_stride = a.f.k_stride;
+    r.v_stride = a.f.v_stride;
+    r.window = window;
+    r.sinks = sinks;
+    r.scale_log2 = a.f.scale_log2;
     int np = 32;
     while (np < s.B) np <<= 1;
     static DeviceOnce once_prepare;
     cudaError_t e = once_prepare.run([] {
-        return cudaFuncSetAttribute(cross_grad_prepare_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(cross_grad_prepare_kernel<D, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)sizeof(unsigned long long) * VIT_MAX_SEGMENTS);
     });
     if (e != cudaSuccess) return e;
     {
         constexpr int per = 32 * (32 / (D / 8));             // rows of a block at a time
         const int64_t want = (r.rows + per - 1) / per, cap = (int64_t)num_sms * 8;
-        LaunchScope scope("cross_grad_prepare", stream);
-        e = launch_chained(cross_grad_prepare_kernel<D>, 2 + (unsigned)(want < cap ? want : cap), kSortThreads,
+        LaunchScope scope(W ? "window_grad_prepare" : "cross_grad_prepare", stream);
+        e = launch_chained(cross_grad_prepare_kernel<D, W>, 2 + (unsigned)(want < cap ? want : cap), kSortThreads,
                            sizeof(unsigned long long) * (size_t)np, stream, r);
         if (e != cudaSuccess) return e;
     }
 
     GradMaps m_dkv, m_dq;
-    Grad dkv, dq;
+    std::conditional_t<W, WinGrad, Grad> dkv, dq;
     if (!make_pass<D, true>(a, pl, num_sms, m_dkv, dkv) || !make_pass<D, false>(a, pl, num_sms, m_dq, dq))
         return cudaErrorInvalidValue;
+    if constexpr (W) {
+        dkv.win_items = static_cast<const WinGradItem *>(r.dkv);
+        dq.win_items = static_cast<const WinGradItem *>(r.dq);
+        dkv.window = dq.window = window;
+        dkv.sinks = dq.sinks = sinks;
+    }
     dkv.first_block = 0;
     dq.first_block = dkv.n_blocks;
     const int blocks = dkv.n_blocks + dq.n_blocks;
     if (blocks == 0) return cudaSuccess;
     constexpr int a1 = GradCfg<D, true>::SMEM, a2 = GradCfg<D, false>::SMEM, smem = a1 > a2 ? a1 : a2;
     static_assert(smem + sizeof(GradShared<D>) <= 227 * 1024, "shared memory per block");
-    auto kern = cross_grad_kernel<D>;
+    auto kern = [] {
+        if constexpr (W) return window_grad_kernel<D>;
+        else return cross_grad_kernel<D>;
+    }();
     static DeviceOnce once;
     e = once.run([&] {
         cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -932,7 +1144,7 @@ template <int D> cudaError_t launch_d(const CrossGradArgs &a, const GradPlan &pl
                                                                               : cudaSuccess;
     });
     if (e != cudaSuccess) return e;
-    LaunchScope scope("cross_grad", stream);
+    LaunchScope scope(W ? "window_grad" : "cross_grad", stream);
     return launch_chained(kern, (unsigned)blocks, kThreads, smem, stream, m_dkv, m_dq, dkv, dq);
 }
 
@@ -958,14 +1170,37 @@ GradPlan grad_plan(int64_t Tq, int64_t Tk, int B, int Hq, int Hk, int D, int max
     return p;
 }
 
+// with a window: the same lists, of larger items
+GradPlan window_grad_plan(int64_t Tq, int64_t Tk, int B, int Hq, int Hk, int D, int max_q, int max_k)
+{
+    GradPlan p = grad_plan(Tq, Tk, B, Hq, Hk, D, max_q, max_k);
+    p.off_dkv = up(p.off_dq + sizeof(WinGradItem) * (size_t)p.max_dq);
+    p.off_stats = up(p.off_dkv + sizeof(WinGradItem) * (size_t)p.max_dkv);
+    p.bytes = p.off_stats + sizeof(float2) * (size_t)Tq * Hq;
+    return p;
+}
+
 cudaError_t launch_cross_grad(const CrossGradArgs &a, const GradPlan &p, int num_sms, cudaStream_t stream)
 {
     switch (a.f.D) {
-        case 32: return launch_d<32>(a, p, num_sms, stream);
-        case 64: return launch_d<64>(a, p, num_sms, stream);
-        case 80: return launch_d<80>(a, p, num_sms, stream);
-        case 96: return launch_d<96>(a, p, num_sms, stream);
-        case 128: return launch_d<128>(a, p, num_sms, stream);
+        case 32: return launch_d<32, false>(a, p, 0, 0, num_sms, stream);
+        case 64: return launch_d<64, false>(a, p, 0, 0, num_sms, stream);
+        case 80: return launch_d<80, false>(a, p, 0, 0, num_sms, stream);
+        case 96: return launch_d<96, false>(a, p, 0, 0, num_sms, stream);
+        case 128: return launch_d<128, false>(a, p, 0, 0, num_sms, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t launch_window_grad(const CrossGradArgs &a, const GradPlan &p, int window, int sinks, int num_sms,
+                               cudaStream_t stream)
+{
+    switch (a.f.D) {
+        case 32: return launch_d<32, true>(a, p, window, sinks, num_sms, stream);
+        case 64: return launch_d<64, true>(a, p, window, sinks, num_sms, stream);
+        case 80: return launch_d<80, true>(a, p, window, sinks, num_sms, stream);
+        case 96: return launch_d<96, true>(a, p, window, sinks, num_sms, stream);
+        case 128: return launch_d<128, true>(a, p, window, sinks, num_sms, stream);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -82,6 +82,22 @@ cudaError_t launch_window_tiles(const WinArgs &a, const WinPlan &p, int num_sms,
 cudaError_t launch_window_long(const WinArgs &a, const WinLong &cx, const WsHeader *hdr, const WinItem *items,
                                int64_t max_items, int num_sms, cudaStream_t stream);
 
+// Work item of a gradient pass (as GradItem, with the part of the other side that the mask leaves). dk, dv: the 128
+// keys from r0 on, the first at position rp, over the queries [l0, l0 + ln), the first at position lp. dq: the 128 / P
+// tokens from r0 on, the first at position rp, over the keys [f0, f0 + fn), which all of them see, and [l0, l0 + ln),
+// the first at position lp.
+struct WinGradItem {
+    int r0, r1, l0, ln;
+    int head, tiles;
+    int f0, fn;
+    int rp, lp;
+    int pad[2];
+};
+static_assert(sizeof(WinGradItem) == 48, "three 16-byte words");
+GradPlan window_grad_plan(int64_t Tq, int64_t Tk, int B, int Hq, int Hk, int D, int max_q, int max_k);
+cudaError_t launch_window_grad(const CrossGradArgs &a, const GradPlan &p, int window, int sinks, int num_sms,
+                               cudaStream_t stream);
+
 // few query rows (cross_few.cu)
 bool window_takes_few(int B, int Hq, int Hk, int D, int max_q, int max_k, int window, int sinks);
 FewPlan window_few_plan(int B, int Hq, int Hk, int D, int max_q, int max_k, int window, int sinks);
