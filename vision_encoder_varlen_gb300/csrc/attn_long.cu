@@ -833,22 +833,25 @@ long_body(const CUtensorMap &tm_q, const CUtensorMap &tm_qr, const CUtensorMap &
                 const bool pv_probe = p_cnt == 0 || mbar_test(bar_addr(bars.pv_done[grp]), (p_cnt - 1) & 1);
                 const int kv_valid = tile_keys(item, j);       // keys of this tile inside the segment
                 if constexpr (W) {
-                    // what this row sees of the tile: columns up to `hi`, from `lo` on or before `sk`
-                    int hi = min(kv_valid, BN) - 1, lo = 0, sk = 0;
+                    // what this row sees of the tile: columns before `hi`, from `lo` on or before `sk`
+                    int hi = min(kv_valid, BN), lo = 0, sk = 0;
                     const int nf = first_tiles(item);
                     if (j >= nf) {
                         const int kp = item.kp + (j - nf) * BN;
                         const int d = item.p0 - kp + (dj == 1 ? grp * (BM >> cx.lg_pack) : 0) + (row >> cx.lg_pack);
-                        hi = min(hi, d);
+                        hi = min(hi, d + 1);
                         if (cx.window > 0) {
                             lo = d - cx.window + 1;
                             sk = cx.sinks - kp;
                         }
                     }
-                    if (__any_sync(0xffffffffu, hi < BN - 1 || lo > 0)) {
+                    if (__any_sync(0xffffffffu, hi < BN || lo > 0)) {
+                        uint32_t seen = 0;
 #pragma unroll
-                        for (int c = 0; c < BN; ++c)
-                            if (c > hi || (c < lo && c >= sk)) sr[c] = __float_as_uint(-INFINITY);
+                        for (int c = 0; c < BN; ++c) {
+                            if (c % 32 == 0) seen = seen_bits(c, hi, lo, sk);
+                            if (!(seen & (1u << c % 32))) sr[c] = __float_as_uint(-INFINITY);
+                        }
                     }
                 } else if (kv_valid < BN) {
 #pragma unroll

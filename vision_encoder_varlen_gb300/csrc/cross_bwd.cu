@@ -615,8 +615,10 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const std::conditi
                     const uint64_t sc2 = f2_splat(p.scale_log2);
                     const uint64_t nl_row = f2_splat(st_row.x), nd_row = f2_splat(st_row.y);
                     // columns [C0, C0 + CN): P and dS go where columns already read were
-                    auto part = [&](auto c0, auto cn) {
+                    auto part = [&](auto c0, auto cn, auto masked) {
                         constexpr int C0 = decltype(c0)::value, CN = decltype(cn)::value;
+                        constexpr bool MASKED = decltype(masked)::value;
+                        [[maybe_unused]] uint32_t seen = 0;
                         uint32_t sr[CN], dr[CN];
 #pragma unroll
                         for (int c = 0; c < CN; c += 16)
@@ -646,21 +648,18 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const std::conditi
                             asm("mov.b64 %0, {%1, %2};\n" : "=l"(pp) : "f"(p0), "f"(p1));
                             float g0, g1;
                             f2_split(f2_mul(f2_add(f2_from_u32(dr[c], dr[c + 1]), d2), pp), g0, g1);
+                            if constexpr (MASKED) {           // exactly 0, whatever was there
+                                if (c % 32 == 0) seen = seen_bits(C0 + c, hi, lo, sk);
+                                const bool s0 = seen & (1u << c % 32), s1 = seen & (2u << c % 32);
+                                p0 = s0 ? p0 : 0.f;
+                                g0 = s0 ? g0 : 0.f;
+                                p1 = s1 ? p1 : 0.f;
+                                g1 = s1 ? g1 : 0.f;
+                            }
                             sr[c / 2] = pack_bf16x2(p0, p1);
                             dr[c / 2] = pack_bf16x2(g0, g1);
                         }
-                        if constexpr (WIN) {
-                            if (__any_sync(0xffffffffu, hi < C0 + CN || lo > C0)) {
-#pragma unroll
-                                for (int c = 0; c < CN; c += 2) {
-                                    const int x = C0 + c;
-                                    const uint32_t a = x < hi && (x >= lo || x < sk) ? 0x0000ffffu : 0u;
-                                    const uint32_t b = x + 1 < hi && (x + 1 >= lo || x + 1 < sk) ? 0xffff0000u : 0u;
-                                    sr[c / 2] &= a | b;
-                                    dr[c / 2] &= a | b;
-                                }
-                            }
-                        } else if (valid < C0 + CN) {             // columns past the end: exactly 0, whatever was there
+                        if (!WIN && valid < C0 + CN) {            // columns past the end: exactly 0, whatever was there
 #pragma unroll
                             for (int c = 0; c < CN; c += 2) {
                                 const int x = C0 + c;
@@ -679,9 +678,19 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const std::conditi
                             tmem_st8(tD + C0 / 2 + c, *reinterpret_cast<const uint32_t(*)[8]>(dr + c));
                     };
                     using std::integral_constant;
-                    part(integral_constant<int, 0>(), integral_constant<int, C::PART>());
-                    if constexpr (C::PART < BN)
-                        part(integral_constant<int, C::PART>(), integral_constant<int, BN - C::PART>());
+                    auto parts = [&](auto first, auto masked) {
+                        constexpr int N = decltype(first)::value;
+                        part(integral_constant<int, 0>(), first, masked);
+                        if constexpr (N < BN) part(first, integral_constant<int, BN - N>(), masked);
+                    };
+                    if constexpr (WIN) {                      // (the mask's registers do not fit beside 80 columns)
+                        if (__any_sync(0xffffffffu, hi < BN || lo > 0))
+                            parts(integral_constant<int, (BN / 2 + 15) / 16 * 16>(), std::true_type());
+                        else
+                            parts(integral_constant<int, C::PART>(), std::false_type());
+                    } else {
+                        parts(integral_constant<int, C::PART>(), std::false_type());
+                    }
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
@@ -915,20 +924,21 @@ struct Prepare {
     float scale_log2;
 };
 
-// The keys that row (t, head) sees where those are 2 to kExactKeys: the first `first` of its sequence and `n` in all,
+// The keys that a token's rows see where those are 2 to kExactKeys: the first `first` of its sequence and `n` in all,
 // the others from position lo on; else n = 0.
 struct FewKeys {
     int64_t k0;
     int first, lo, n;
 };
-__device__ __forceinline__ FewKeys few_keys(const Prepare &p, int64_t t)
+// cu_q: the list, or a copy of it in shared memory
+__device__ __forceinline__ FewKeys few_keys(const Prepare &p, const int32_t *cu_q, int64_t t)
 {
     const CrossSegs &s = p.segs;
     FewKeys none{0, 0, 0, 0};
     int b = 0, end = s.B;                              // the last sequence that begins at or before t (offsets that
     while (end - b > 1) {                              // decrease lead nowhere: the call computes nothing then)
         const int m = (b + end) >> 1;
-        if (s.cu_q[m] <= t) b = m;
+        if (cu_q[m] <= t) b = m;
         else end = m;
     }
     CrossSeg x;
@@ -939,6 +949,96 @@ __device__ __forceinline__ FewKeys few_keys(const Prepare &p, int64_t t)
     const int64_t n = (int64_t)w.first + pos + 1 - w.lo;
     if (n < 2 || n > kExactKeys) return none;
     return FewKeys{x.k0, w.first, w.lo, (int)n};
+}
+
+// The statistics of a windowed call, by the blocks from `first_block` on. A warp takes up to kHeadSteps steps of
+// 32 / (D / 8) heads of one token, so that what the token sees is looked up once for them; rows that see few keys are
+// left to a second round, two lanes per key and a warp per row (one after the other in the first round, the 16 first
+// tokens of a sequence alone took 40 us).
+constexpr int kHeadSteps = 4;
+template <int D>
+__device__ void window_stats(const Prepare &p, int first_block)
+{
+    constexpr int CH = D / 8, R = 32 / CH, HEADS = R * kHeadSteps;
+    extern __shared__ unsigned long long s_lists[];
+    const int32_t *cu_q = p.segs.cu_q;
+    if (p.segs.B <= 2 * kSortThreads) {                // (the searches' reads; the launch has room for the list)
+        int32_t *copy = reinterpret_cast<int32_t *>(s_lists);
+        for (int i = threadIdx.x; i < p.segs.B; i += kSortThreads) copy[i] = p.segs.cu_q[i];
+        __syncthreads();
+        cu_q = copy;
+    }
+    const int lane = threadIdx.x & 31;
+    const int64_t n_tokens = p.rows / p.Hq;
+    const int64_t warp = ((int64_t)(blockIdx.x - first_block) * blockDim.x + threadIdx.x) >> 5;
+    const int64_t n_warps = ((int64_t)(gridDim.x - first_block) * blockDim.x) >> 5;
+    auto load = [](const __nv_bfloat16 *x, bool live) {
+        return live ? *reinterpret_cast<const uint4 *>(x) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    auto dot = [](const uint4 &x, const uint4 &y, float s) {
+        float a[8], b[8];
+        rope::unpack8(x, a);
+        rope::unpack8(y, b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = fmaf(a[e], b[e], s);
+        return s;
+    };
+    {
+        const int g = lane / CH, c = lane % CH, per_token = (p.Hq + HEADS - 1) / HEADS;
+        for (int64_t w = warp; w < n_tokens * per_token; w += n_warps) {
+            const int64_t t = per_token == 1 ? w : w / per_token;
+            const int h0 = (int)(w - t * per_token) * HEADS + g;
+            if (few_keys(p, cu_q, t).n > 0) continue;
+            const __nv_bfloat16 *o = p.out + t * p.out_stride + 8 * c, *d = p.dout + t * p.dout_stride + 8 * c;
+#pragma unroll
+            for (int i = 0; i < kHeadSteps; ++i) {
+                const int h = h0 + R * i;
+                const bool live = g < R && h < p.Hq;
+                const float x = dot(load(o + (int64_t)h * D, live), load(d + (int64_t)h * D, live), 0.f);
+                float s = 0.f;                         // over the row's lanes
+#pragma unroll
+                for (int j = 0; j < CH; ++j) s += __shfl_sync(0xffffffffu, x, (g * CH + j) & 31);
+                const int64_t r = t * p.Hq + h;
+                if (live && c == 0) p.stats[r] = make_float2(-p.lse[r] * 1.4426950408889634f, -s);
+            }
+        }
+    }
+    // every row of a narrow window, else the first tokens of each sequence
+    const bool narrow = p.window > 0 && (int64_t)p.window + p.sinks <= kExactKeys;
+    const int64_t n_few = narrow ? p.rows : (int64_t)p.segs.B * kExactKeys * p.Hq;
+    for (int64_t w = warp; w < n_few; w += n_warps) {
+        int64_t t = w / p.Hq;
+        const int h = (int)(w - t * p.Hq);
+        if (!narrow) {
+            CrossSeg x;
+            const int b = (int)(t / kExactKeys), i = (int)(t % kExactKeys);
+            if (!load_seg(p.segs, b, x, nullptr, false)) continue;
+            const WinSeg s = win_seg(x);
+            if (i >= s.qn) continue;
+            t = (int64_t)s.q0 + i;
+        }
+        const FewKeys f = few_keys(p, cu_q, t);
+        if (f.n == 0) continue;
+        const int j = lane >> 1, part = (lane & 1) * (D / 2);
+        const bool live = j < f.n;
+        const int64_t row = f.k0 + (j < f.first ? j : f.lo + j - f.first), kv = (int64_t)(h / (p.Hq / p.Hk)) * D + part;
+        const __nv_bfloat16 *q = p.q + t * p.q_stride + (int64_t)h * D + part, *k = p.k + row * p.k_stride + kv;
+        const __nv_bfloat16 *d = p.dout + t * p.dout_stride + (int64_t)h * D + part, *v = p.v + row * p.v_stride + kv;
+        float x = 0.f, y = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 2; c += 8) {
+            x = dot(load(q + c, live), load(k + c, live), x);
+            y = dot(load(d + c, live), load(v + c, live), y);
+        }
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        y += __shfl_xor_sync(0xffffffffu, y, 1);
+        const int64_t r = t * p.Hq + h;
+        const float nl = -p.lse[r] * 1.4426950408889634f;
+        float s = live ? ex2(fmaf(x, p.scale_log2, nl)) * y : 0.f;     // delta = sum_j p_j (do v_j)
+#pragma unroll
+        for (int o = 2; o < 32; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) p.stats[r] = make_float2(nl, -s);
+    }
 }
 
 template <int D, bool W>
@@ -952,6 +1052,10 @@ cross_grad_prepare_kernel(const Prepare p)
         const bool keys = blockIdx.x == 1;
         make_list<W>(keys, p.segs, p.Hq, p.Hk, p.lg_pack, keys ? GradCfg<D, true>::BN : GradCfg<D, false>::BN,
                      p.counts, static_cast<Item *>(keys ? p.dkv : p.dq), p.status, p.window, p.sinks);
+        return;
+    }
+    if constexpr (W) {
+        window_stats<D>(p, 2);
         return;
     }
     // D / 8 lanes per row, 16 bytes of o and do each
@@ -975,43 +1079,6 @@ cross_grad_prepare_kernel(const Prepare p)
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < CH; ++i) sum += __shfl_sync(0xffffffffu, s, (g * CH + i) & 31);
-        if constexpr (W) {
-            const int64_t t = live ? r / p.Hq : 0;
-            FewKeys f{0, 0, 0, 0};
-            if (live) f = few_keys(p, t);
-            const int most = __reduce_max_sync(0xffffffffu, f.n);
-            if (most > 0) {                            // delta = sum_j p_j (do v_j), over the keys that the row sees
-                const int h = (int)(r - t * p.Hq);
-                const int64_t kv = (int64_t)(h / (p.Hq / p.Hk)) * D + 8 * c;
-                float a[8], b[8], exact = 0.f;
-                if (f.n > 0) {
-                    rope::unpack8(*reinterpret_cast<const uint4 *>(p.q + t * p.q_stride + (int64_t)h * D + 8 * c), a);
-                    rope::unpack8(*reinterpret_cast<const uint4 *>(p.dout + t * p.dout_stride + (int64_t)h * D + 8 * c), b);
-                }
-                for (int j = 0; j < most; ++j) {
-                    float x = 0.f, y = 0.f;
-                    if (j < f.n) {
-                        const int64_t row = f.k0 + (j < f.first ? j : f.lo + j - f.first);
-                        float k[8], v[8];
-                        rope::unpack8(*reinterpret_cast<const uint4 *>(p.k + row * p.k_stride + kv), k);
-                        rope::unpack8(*reinterpret_cast<const uint4 *>(p.v + row * p.v_stride + kv), v);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            x = fmaf(a[e], k[e], x);
-                            y = fmaf(b[e], v[e], y);
-                        }
-                    }
-                    float score = 0.f, dp = 0.f;
-#pragma unroll
-                    for (int i = 0; i < CH; ++i) {
-                        score += __shfl_sync(0xffffffffu, x, (g * CH + i) & 31);
-                        dp += __shfl_sync(0xffffffffu, y, (g * CH + i) & 31);
-                    }
-                    if (j < f.n) exact = fmaf(ex2(fmaf(score, p.scale_log2, -p.lse[r] * 1.4426950408889634f)), dp, exact);
-                }
-                if (f.n > 0) sum = exact;
-            }
-        }
         if (live && c == 0) p.stats[r] = make_float2(-p.lse[r] * 1.4426950408889634f, -sum);
     }
 }
@@ -1105,7 +1172,9 @@ cudaError_t launch_d(const CrossGradArgs &a, const GradPlan &pl, int window, int
     if (e != cudaSuccess) return e;
     {
         constexpr int per = 32 * (32 / (D / 8));             // rows of a block at a time
-        const int64_t want = (r.rows + per - 1) / per, cap = (int64_t)num_sms * 8;
+        constexpr int heads = kHeadSteps * (32 / (D / 8));
+        const int64_t tasks = s.Tq * ((a.f.Hq + heads - 1) / heads);
+        const int64_t want = W ? (tasks + 31) / 32 : (r.rows + per - 1) / per, cap = W ? num_sms - 2 : (int64_t)num_sms * 8;
         LaunchScope scope(W ? "window_grad_prepare" : "cross_grad_prepare", stream);
         e = launch_chained(cross_grad_prepare_kernel<D, W>, 2 + (unsigned)(want < cap ? want : cap), kSortThreads,
                            sizeof(unsigned long long) * (size_t)np, stream, r);

@@ -304,6 +304,17 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+// the bits [0, n) of a word (any n)
+__device__ __forceinline__ uint32_t bits_below(int n) {
+    uint32_t m;
+    asm("bmsk.clamp.b32 %0, 0, %1;\n" : "=r"(m) : "r"(n > 0 ? n : 0));
+    return m;
+}
+// The columns x0 .. x0 + 31 that a row sees: those before `hi`, from `lo` on or before `sk`.
+__device__ __forceinline__ uint32_t seen_bits(int x0, int hi, int lo, int sk) {
+    return bits_below(hi - x0) & (~bits_below(lo - x0) | bits_below(sk - x0));
+}
+
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));

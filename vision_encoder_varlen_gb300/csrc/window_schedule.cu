@@ -144,6 +144,7 @@ window_schedule_kernel(const Sched p)
 {
     extern __shared__ unsigned long long s_key[];      // [NP]: longest block first, then index; later first item | index
     __shared__ int64_t s_warp[32];
+    __shared__ Unit s_unit[32];                        // of up to 32 units, in their order
     __shared__ int s_bad, s_used, s_total, s_tiles, s_all_split, s_more, s_empty;
     grid_wait();
     grid_release();
@@ -191,6 +192,7 @@ window_schedule_kernel(const Sched p)
             warp_place(key_of(use, x, tid), n * runs, runs > 1 ? n : 0, rank, at, tile_at);
             s_key[rank] = ((unsigned long long)at << 32) | (uint32_t)tid;
             s_tile[rank] = tile_at;
+            s_unit[rank] = x;
             const unsigned used = __ballot_sync(0xffffffffu, use), any_bad = __ballot_sync(0xffffffffu, bad);
             const unsigned nones = __ballot_sync(0xffffffffu, fine && none.qn > 0);
             if (fine && none.qn > 0) p.empty[__popc(nones & ((1u << tid) - 1u))] = none;
@@ -266,13 +268,15 @@ window_schedule_kernel(const Sched p)
         const int unit = (int)(s_key[at_unit] & 0xffffffffu);
         Unit x;
         CrossEmpty none;
-        load_unit(p, unit, x, none, false);
+        if (n_units <= 32) x = s_unit[at_unit];
+        else load_unit(p, unit, x, none, false);
         const int nq = (int)(((unsigned)x.qn + (1u << lg_block) - 1u) >> lg_block), runs = runs_of(x);
-        const int j = n / runs, run = n - j * runs, qb = nq - 1 - j / packs, h = j % packs;
+        const int j = runs > 1 ? n / runs : n, run = n - j * runs, back = j / packs, qb = nq - 1 - back;
+        const int h = j - back * packs;
         const int t = qb << lg_block, e = min(x.qn, t + (1 << lg_block));
         const Span s = span_of(p, x, t, e);
         // the block's tiles, dealt evenly to as many runs as they fill
-        const int tiles = s.tiles(p.bn), use = runs > 1 ? max(1, (tiles + p.run_tiles - 1) / p.run_tiles) : 1;
+        const int tiles = runs > 1 ? s.tiles(p.bn) : 0, use = runs > 1 ? max(1, (tiles + p.run_tiles - 1) / p.run_tiles) : 1;
         if (p.apart && n == 0) p.units[unit] = UnitSlots{x.q0, nq, runs, i};
         if (run >= use) {
             if (p.apart)
@@ -287,10 +291,15 @@ window_schedule_kernel(const Sched p)
         it.slot = runs > 1 || p.apart ? i : -1;
         it.p0 = x.p0 + t;
         it.pad = 0;
-        const int nf = (s.fn + p.bn - 1) / p.bn, a = (int)((int64_t)tiles * run / use);
-        const int b = (int)((int64_t)tiles * (run + 1) / use);
-        const int fa = min(s.fn, min(a, nf) * p.bn), fb = min(s.fn, min(b, nf) * p.bn);
-        const int ka = min(s.kn, max(0, a - nf) * p.bn), kb = min(s.kn, max(0, b - nf) * p.bn);
+        int fa = 0, fb = s.fn, ka = 0, kb = s.kn;
+        if (use > 1) {
+            const int nf = (s.fn + p.bn - 1) / p.bn, a = (int)((int64_t)tiles * run / use);
+            const int b = (int)((int64_t)tiles * (run + 1) / use);
+            fa = min(s.fn, min(a, nf) * p.bn);
+            fb = min(s.fn, min(b, nf) * p.bn);
+            ka = min(s.kn, max(0, a - nf) * p.bn);
+            kb = min(s.kn, max(0, b - nf) * p.bn);
+        }
         it.f0 = s.f0 + fa;
         it.fn = fb - fa;
         it.kp = s.lo + ka;
