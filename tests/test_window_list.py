@@ -37,7 +37,7 @@ def plan(Tq, B, Hq, Hk, D, max_q, max_k, window, sinks, G, Tp, max_p):
     p = dict(lg=lg, apart=apart, units=(G + B if apart else B), run=0, slots=0, tiles=0)
     least = 2 * cdiv(512, 2 * bn)
     if apart:
-        p["run"] = run = max(least, cdiv((own * own_most + grouped * first_most) * packs, SMS))
+        p["run"] = run = max(least, cdiv((own * own_most + grouped * first_most) * packs, 4 * SMS))
         p["items"] = p["slots"] = (grouped * max(1, cdiv(first_most, run)) + own * max(1, cdiv(own_most, run))) * packs
     else:
         tiles, most = own * packs, own_most + first_most

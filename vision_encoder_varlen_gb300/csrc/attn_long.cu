@@ -764,6 +764,10 @@ long_body(const CUtensorMap &tm_q, const CUtensorMap &tm_qr, const CUtensorMap &
         // not yet arrived), so the next item's first P.V cannot overwrite it. Measured: 2 % faster
         // at head_dim 128, 1-6 % slower at 80 (where the epilogue is short), so only there.
         constexpr bool kDeferOut = D >= 128;
+        // W: tiles inside the mask have a copy of the code without it at head_dim 128 (prompts behind 8191 shared keys 538
+        // instead of 576 us); at 80, whose tiles are wider, one copy is as fast. More copies (for tiles that a warp does
+        // not see at all, or of few keys) cost more in instruction fetches than they save: 5 % at head_dim 128.
+        constexpr bool kTwoCopies = D >= 128;
         bool pend = false, pend_store = false;
         int pend_row = 0, pend_head = 0;
         float pend_m = 0.f, pend_l = 1.f;
@@ -815,8 +819,12 @@ long_body(const CUtensorMap &tm_q, const CUtensorMap &tm_qr, const CUtensorMap &
             // come yet (-inf less -inf is NaN; a test of it in each tile cost 3 % at head_dim 80)
             float m_run = X ? -FLT_MAX : -INFINITY, l_run = 0.f;
 
-            for (int j = dj == 2 ? grp : 0; j < n_kv && ok; j += dj) {
-                if (!(ok = wait_warp(bars.s_full[grp], p_cnt & 1))) break;
+            // key tile j; W: this row sees its columns before `hi`, from `lo` on or before `sk`
+            auto tile = [&](int j, auto masked, [[maybe_unused]] int hi, [[maybe_unused]] int lo,
+                            [[maybe_unused]] int sk) {
+                constexpr bool MASKED = decltype(masked)::value;
+                const bool edge = MASKED && (kTwoCopies || __any_sync(0xffffffffu, hi < BN || lo > 0));
+                if (!(ok = wait_warp(bars.s_full[grp], p_cnt & 1))) return;
                 tc_fence_after();
                 // S row -> registers: all loads in flight, one wait
                 uint32_t sr[BN];
@@ -831,29 +839,21 @@ long_body(const CUtensorMap &tm_q, const CUtensorMap &tm_qr, const CUtensorMap &
                 // the previous P.V of this tile has almost always finished by now: probe it
                 // without blocking, so its barrier latency overlaps the arithmetic below
                 const bool pv_probe = p_cnt == 0 || mbar_test(bar_addr(bars.pv_done[grp]), (p_cnt - 1) & 1);
-                const int kv_valid = tile_keys(item, j);       // keys of this tile inside the segment
-                if constexpr (W) {
-                    // what this row sees of the tile: columns before `hi`, from `lo` on or before `sk`
-                    int hi = min(kv_valid, BN), lo = 0, sk = 0;
-                    const int nf = first_tiles(item);
-                    if (j >= nf) {
-                        const int kp = item.kp + (j - nf) * BN;
-                        const int d = item.p0 - kp + (dj == 1 ? grp * (BM >> cx.lg_pack) : 0) + (row >> cx.lg_pack);
-                        hi = min(hi, d + 1);
-                        if (cx.window > 0) {
-                            lo = d - cx.window + 1;
-                            sk = cx.sinks - kp;
-                        }
-                    }
-                    if (__any_sync(0xffffffffu, hi < BN || lo > 0)) {
-                        uint32_t seen = 0;
+                [[maybe_unused]] const int kv_valid = W ? BN : tile_keys(item, j);   // keys of this tile inside the segment
+                if constexpr (MASKED) {
+                    // (32 columns at a time: of a tile at the mask's edge, a warp's rows agree on most)
+                    if (edge) {
 #pragma unroll
-                        for (int c = 0; c < BN; ++c) {
-                            if (c % 32 == 0) seen = seen_bits(c, hi, lo, sk);
-                            if (!(seen & (1u << c % 32))) sr[c] = __float_as_uint(-INFINITY);
+                        for (int c0 = 0; c0 < BN; c0 += 32) {
+                            constexpr uint32_t LAST = BN % 32 ? (1u << BN % 32) - 1 : 0xffffffffu;
+                            const uint32_t seen = seen_bits(c0, hi, lo, sk);
+                            if (!__all_sync(0xffffffffu, seen == (c0 + 32 > BN ? LAST : 0xffffffffu)))
+#pragma unroll
+                                for (int c = 0; c < 32; ++c)
+                                    if (c0 + c < BN && !(seen & (1u << c))) sr[c0 + c] = __float_as_uint(-INFINITY);
                         }
                     }
-                } else if (kv_valid < BN) {
+                } else if (!W && kv_valid < BN) {
 #pragma unroll
                     for (int c = 0; c < BN; ++c)
                         if (c >= kv_valid) sr[c] = __float_as_uint(-INFINITY);
@@ -897,7 +897,7 @@ long_body(const CUtensorMap &tm_q, const CUtensorMap &tm_qr, const CUtensorMap &
 
                 // this tile's P region is free, and its O holds every earlier P.V product, once
                 // the previous P.V of this tile has completed
-                if (!__all_sync(0xffffffffu, pv_probe) && !(ok = wait_warp(bars.pv_done[grp], (p_cnt - 1) & 1))) break;
+                if (!__all_sync(0xffffffffu, pv_probe) && !(ok = wait_warp(bars.pv_done[grp], (p_cnt - 1) & 1))) return;
                 tc_fence_after();
                 if (__any_sync(0xffffffffu, rescale)) {
                     const float a = rescale ? alpha : 1.f;
@@ -922,6 +922,27 @@ long_body(const CUtensorMap &tm_q, const CUtensorMap &tm_qr, const CUtensorMap &
                 // the previous item's last P.V completed before this P was stored (the wait above)
                 if constexpr (kDeferOut) {
                     if (pend) write_out();
+                }
+            };
+            for (int j = dj == 2 ? grp : 0; j < n_kv && ok; j += dj) {
+                if constexpr (W) {
+                    const int valid = min(tile_keys(item, j), BN), nf = first_tiles(item);
+                    int hi = valid, lo = 0, sk = 0;
+                    if (j >= nf) {
+                        const int kp = item.kp + (j - nf) * BN;
+                        const int d = item.p0 - kp + (dj == 1 ? grp * (BM >> cx.lg_pack) : 0) + (row >> cx.lg_pack);
+                        hi = min(hi, d + 1);
+                        if (cx.window > 0) {
+                            lo = d - cx.window + 1;
+                            sk = min(hi, cx.sinks - kp);
+                        }
+                    }
+                    if (kTwoCopies && __all_sync(0xffffffffu, hi >= BN && lo <= 0))
+                        tile(j, std::false_type(), 0, 0, 0);
+                    else
+                        tile(j, std::true_type(), hi, lo, sk);
+                } else {
+                    tile(j, std::false_type(), 0, 0, 0);
                 }
             }
             if (!ok) break;

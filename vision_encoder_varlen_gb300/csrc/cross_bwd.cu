@@ -683,11 +683,22 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const std::conditi
                         part(integral_constant<int, 0>(), first, masked);
                         if constexpr (N < BN) part(first, integral_constant<int, BN - N>(), masked);
                     };
-                    if constexpr (WIN) {                      // (the mask's registers do not fit beside 80 columns)
-                        if (__any_sync(0xffffffffu, hi < BN || lo > 0))
+                    if constexpr (WIN) {
+                        sk = min(sk, hi);
+                        if (!__any_sync(0xffffffffu, hi > 0 && (lo < hi || sk > 0))) {
+                            // none of the warp's pairs is seen: P = dS = 0, without a look at S and dP
+                            const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+                            for (int c = 0; c < BN / 2; c += 8) {
+                                if constexpr (DKV) tmem_st8(tS + c, zero);
+                                tmem_st8(tD + c, zero);
+                            }
+                        } else if (__any_sync(0xffffffffu, hi < BN || lo > 0)) {
+                            // (the mask's registers do not fit beside 80 columns)
                             parts(integral_constant<int, (BN / 2 + 15) / 16 * 16>(), std::true_type());
-                        else
+                        } else {
                             parts(integral_constant<int, C::PART>(), std::false_type());
+                        }
                     } else {
                         parts(integral_constant<int, C::PART>(), std::false_type());
                     }
@@ -952,14 +963,14 @@ __device__ __forceinline__ FewKeys few_keys(const Prepare &p, const int32_t *cu_
 }
 
 // The statistics of a windowed call, by the blocks from `first_block` on. A warp takes up to kHeadSteps steps of
-// 32 / (D / 8) heads of one token, so that what the token sees is looked up once for them; rows that see few keys are
+// 32 / (D / 16) heads of one token, 32 bytes of o and do a lane, so that what the token sees is looked up once for them; rows that see few keys are
 // left to a second round, two lanes per key and a warp per row (one after the other in the first round, the 16 first
 // tokens of a sequence alone took 40 us).
 constexpr int kHeadSteps = 4;
 template <int D>
 __device__ void window_stats(const Prepare &p, int first_block)
 {
-    constexpr int CH = D / 8, R = 32 / CH, HEADS = R * kHeadSteps;
+    constexpr int CH = D / 16, R = 32 / CH, HEADS = R * kHeadSteps;
     extern __shared__ unsigned long long s_lists[];
     const int32_t *cu_q = p.segs.cu_q;
     if (p.segs.B <= 2 * kSortThreads) {                // (the searches' reads; the launch has room for the list)
@@ -986,15 +997,18 @@ __device__ void window_stats(const Prepare &p, int first_block)
     {
         const int g = lane / CH, c = lane % CH, per_token = (p.Hq + HEADS - 1) / HEADS;
         for (int64_t w = warp; w < n_tokens * per_token; w += n_warps) {
-            const int64_t t = per_token == 1 ? w : w / per_token;
-            const int h0 = (int)(w - t * per_token) * HEADS + g;
+            const int64_t t = per_token == 1 ? w : w >> 32 ? w / per_token : (int64_t)((uint32_t)w / (uint32_t)per_token);
+            const int h0 = (int)(w - t * per_token) * HEADS;
             if (few_keys(p, cu_q, t).n > 0) continue;
-            const __nv_bfloat16 *o = p.out + t * p.out_stride + 8 * c, *d = p.dout + t * p.dout_stride + 8 * c;
+            const __nv_bfloat16 *o = p.out + t * p.out_stride + 16 * c, *d = p.dout + t * p.dout_stride + 16 * c;
 #pragma unroll
             for (int i = 0; i < kHeadSteps; ++i) {
-                const int h = h0 + R * i;
+                if (h0 + R * i >= p.Hq) break;
+                const int h = h0 + R * i + g;
                 const bool live = g < R && h < p.Hq;
-                const float x = dot(load(o + (int64_t)h * D, live), load(d + (int64_t)h * D, live), 0.f);
+                const __nv_bfloat16 *oh = o + (int64_t)h * D, *dh = d + (int64_t)h * D;
+                const uint4 o0 = load(oh, live), o1 = load(oh + 8, live), d0 = load(dh, live), d1 = load(dh + 8, live);
+                const float x = dot(o1, d1, dot(o0, d0, 0.f));
                 float s = 0.f;                         // over the row's lanes
 #pragma unroll
                 for (int j = 0; j < CH; ++j) s += __shfl_sync(0xffffffffu, x, (g * CH + j) & 31);
@@ -1172,7 +1186,7 @@ cudaError_t launch_d(const CrossGradArgs &a, const GradPlan &pl, int window, int
     if (e != cudaSuccess) return e;
     {
         constexpr int per = 32 * (32 / (D / 8));             // rows of a block at a time
-        constexpr int heads = kHeadSteps * (32 / (D / 8));
+        constexpr int heads = kHeadSteps * (32 / (D / 16));
         const int64_t tasks = s.Tq * ((a.f.Hq + heads - 1) / heads);
         const int64_t want = W ? (tasks + 31) / 32 : (r.rows + per - 1) / per, cap = W ? num_sms - 2 : (int64_t)num_sms * 8;
         LaunchScope scope(W ? "window_grad_prepare" : "cross_grad_prepare", stream);

@@ -426,7 +426,7 @@ WinPlan win_plan(int64_t Tq, int B, int Hq, int Hk, int D, int max_q, int max_k,
     const int64_t least = 2 * cdiv(512, 2 * bn);
     if (p.apart) {
         const int64_t work = (own * own_most + grouped * first_most) * packs;
-        const int64_t run = std::max(least, cdiv(work, kDesignSms));
+        const int64_t run = std::max(least, cdiv(work, 4 * kDesignSms));
         const int64_t r1 = cdiv(first_most, run), r2 = cdiv(own_most, run);
         p.run_tiles = (int)run;
         p.runs = (int)std::max<int64_t>(1, std::max(r1, r2));
