@@ -76,6 +76,7 @@ static_assert(128 * kCtrlRegs + 256 * kSoftmaxRegs <= kThreads * kLaunchRegs, "r
 constexpr int BM = 128;
 constexpr long long kWaitBudget = 4000000000ll;
 constexpr int kMaxY = 6;
+constexpr int kItemRing = 4;           // windowed lists: items the producer may take ahead of the other roles
 constexpr int kExactKeys = 16;         // sequences of 2 to so many keys have delta from the scores
 
 template <int D, bool DKV> struct GradCfg {
@@ -141,6 +142,7 @@ struct GradMaps {
 };
 struct WinGrad : Grad {
     const WinGradItem *win_items;
+    int32_t *next;                // items handed out so far beyond each block's first
     int window, sinks;
 };
 __device__ __forceinline__ const GradItem *items_of(const Grad &p) { return p.items; }
@@ -152,10 +154,14 @@ template <int D> struct GradShared {
     volatile int abort;
     alignas(16) float stat[2][2][GradCfg<D, true>::BN];    // dk, dv: [group][-lse2 | -delta][column]
 };
+template <int D> struct WinGradShared : GradShared<D> {
+    uint64_t item_full[kItemRing], item_empty[kItemRing];
+    int item[kItemRing];          // numbers of the items that the producer has taken (the list's length or more: the end)
+};
 
 template <int D, bool DKV, bool WIN>
 __device__ __forceinline__ void grad_pass(const GradMaps &tm, const std::conditional_t<WIN, WinGrad, Grad> &p,
-                                          GradShared<D> &sh)
+                                          std::conditional_t<WIN, WinGradShared<D>, GradShared<D>> &sh)
 {
     using C = GradCfg<D, DKV>;
     using GradItem = std::conditional_t<WIN, WinGradItem, vit::GradItem>;
@@ -185,6 +191,12 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const std::conditi
         mbar_init(bar_addr(bars.acc_done), 1);
         mbar_init(bar_addr(bars.acc_free), 8);
         mbar_init(bar_addr(bars.drain), 1);
+        if constexpr (WIN) {
+            for (int i = 0; i < kItemRing; ++i) {
+                mbar_init(bar_addr(sh.item_full[i]), 1);
+                mbar_init(bar_addr(sh.item_empty[i]), DKV ? 11 : 9);   // the issuer, the softmax warps, warps 2 and 3
+            }
+        }
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -204,12 +216,6 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const std::conditi
         return (int)b - p.first_block;
     };
     auto list_length = [&] { return *static_cast<const volatile int32_t *>(p.n_items); };
-    // The block's next item. A windowed list's items shorten from first to last within a round of the blocks, so the
-    // next round goes the other way.
-    auto next_item = [&](int i) {
-        if constexpr (WIN) return i + 2 * (p.n_blocks - i % p.n_blocks) - 1;
-        else return i + p.n_blocks;
-    };
     // tiles of the keys that a windowed query tile reads first
     auto first_tiles = [&](const GradItem &it) -> int {
         if constexpr (WIN && !DKV) return (it.fn + BN - 1) / BN;
@@ -227,6 +233,36 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const std::conditi
     auto wait_warp = [&](const uint64_t &b, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, wait(b, parity)) != 0;
     };
+    // The items of a block: every n_blocks-th one, or, where their lengths differ (WIN), its first one and then the next
+    // that no block has taken, which the producer takes from a counter and passes on through a ring. (Blocks of the
+    // second pass start when those of the first leave, so that with a fixed share each the sum of both counts: three
+    // texts of 1500 to 2311 tokens, 32 heads over 8 of 128, causal, 345 us.)
+    uint32_t taken = 0;                    // by this role
+    auto put = [&](int i) -> bool {        // the producer's
+        if constexpr (WIN) {
+            const uint32_t s = taken % kItemRing;
+            if (taken >= kItemRing && !wait(sh.item_empty[s], (taken / kItemRing - 1) & 1)) return false;
+            sh.item[s] = i;
+            mbar_arrive(bar_addr(sh.item_full[s]));
+            ++taken;
+        }
+        return true;
+    };
+    auto take = [&]() -> int {             // the other roles', by whole warps
+        int i = 0x7fffffff;
+        if constexpr (WIN) {
+            const uint32_t s = taken % kItemRing;
+            if (wait_warp(sh.item_full[s], (taken / kItemRing) & 1)) {
+                i = *static_cast<volatile int *>(&sh.item[s]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_addr(sh.item_empty[s]));
+                ++taken;
+            }
+        }
+        return i;
+    };
+    auto first_item = [&]() { return WIN ? take() : block(); };
+    auto next_item = [&](int i) { return WIN ? take() : i + p.n_blocks; };
     // tokens of a streamed tile; tiles of an item; streamed rows of tile j inside the sequence
     const int y_tok = DKV ? BN >> p.lg_pack : BN;
     auto valid_rows = [&](const GradItem &it, int j) -> int {
@@ -251,7 +287,14 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const std::conditi
             tma_prefetch_desc(&tm.y2);
             uint32_t xc = 0, yc = 0;
             bool ok = true;
-            for (int i = block(), n_items = list_length(); ok && i < n_items; i = next_item(i)) {
+            int after = 0;                                   // the item after this one
+            auto on = [&](int i) {
+                if constexpr (WIN) return after;
+                else return i + p.n_blocks;
+            };
+            for (int i = block(), n_items = list_length(); ok && i < n_items; i = on(i)) {
+                if (!(ok = put(i))) break;
+                if constexpr (WIN) after = p.n_blocks + atomicAdd(p.next, 1);
                 const GradItem it = items[i];
                 if (it.tiles == 0) continue;
                 const uint32_t xb = xc & 1;
@@ -289,6 +332,7 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const std::conditi
                     }
                 }
             }
+            if (ok) ok = put(0x7fffffff);
             if (!ok) {
                 // let every copy already issued land before this block's shared memory is released
                 const int never = 0;
@@ -374,7 +418,7 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const std::conditi
             }
             return true;
         };
-        for (int i = block(), n_items = list_length(); ok && i < n_items; i = next_item(i)) {
+        for (int i = first_item(), n_items = list_length(); ok && i < n_items; i = next_item(i)) {
             const GradItem it = items[i];
             const int n = uni(it.tiles);
             if (n == 0) continue;
@@ -468,7 +512,7 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const std::conditi
             constexpr int PER = (BN + 31) / 32;
             uint32_t u0 = 0;
             bool ok = true;
-            for (int i = block(), n_items = list_length(); ok && i < n_items; i = next_item(i)) {
+            for (int i = first_item(), n_items = list_length(); ok && i < n_items; i = next_item(i)) {
                 const GradItem it = items[i];
                 const int n = it.tiles;
                 if (n == 0) continue;
@@ -514,7 +558,7 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const std::conditi
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
         uint32_t u0 = 0, xc = 0;                              // tiles and items with tiles before this item
         bool ok = true;
-        for (int i = block(), n_items = list_length(); ok && i < n_items; i = next_item(i)) {
+        for (int i = first_item(), n_items = list_length(); ok && i < n_items; i = next_item(i)) {
             const GradItem it = items[i];
             const int n = it.tiles;
             // the row of the output that this lane holds
@@ -781,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 window_grad_kernel(const __grid_constant__ GradMaps tm_dkv, const __grid_constant__ GradMaps tm_dq,
                    const __grid_constant__ WinGrad dkv, const __grid_constant__ WinGrad dq)
 {
-    __shared__ GradShared<D> sh;
+    __shared__ WinGradShared<D> sh;
     if ((int)blockIdx.x < dkv.n_blocks)
         grad_pass<D, true, true>(tm_dkv, dkv, sh);
     else
@@ -862,6 +906,7 @@ __device__ void make_list(bool keys, const CrossSegs &segs, int Hq, int Hk, int 
     }
     const int total = s_bad ? 0 : s_total;
     if (tid == 0) counts[keys] = s_bad ? -1 : total;   // -1: the call is left alone altogether
+    if (W && tid == 0) counts[2 + keys] = 0;
     for (int i = tid; i < total; i += kThreads) {
         const int p = place_of(s_key, s_used, i), n = i - (int)(s_key[p] >> 32);
         CrossSeg x;
@@ -1202,6 +1247,8 @@ cudaError_t launch_d(const CrossGradArgs &a, const GradPlan &pl, int window, int
     if constexpr (W) {
         dkv.win_items = static_cast<const WinGradItem *>(r.dkv);
         dq.win_items = static_cast<const WinGradItem *>(r.dq);
+        dkv.next = r.counts + 3;
+        dq.next = r.counts + 2;
         dkv.window = dq.window = window;
         dkv.sinks = dq.sinks = sinks;
     }
@@ -1210,7 +1257,7 @@ cudaError_t launch_d(const CrossGradArgs &a, const GradPlan &pl, int window, int
     const int blocks = dkv.n_blocks + dq.n_blocks;
     if (blocks == 0) return cudaSuccess;
     constexpr int a1 = GradCfg<D, true>::SMEM, a2 = GradCfg<D, false>::SMEM, smem = a1 > a2 ? a1 : a2;
-    static_assert(smem + sizeof(GradShared<D>) <= 227 * 1024, "shared memory per block");
+    static_assert(smem + sizeof(std::conditional_t<W, WinGradShared<D>, GradShared<D>>) <= 227 * 1024, "shared memory per block");
     auto kern = [] {
         if constexpr (W) return window_grad_kernel<D>;
         else return cross_grad_kernel<D>;
