@@ -656,13 +656,13 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const std::conditi
                             st_row.y = -sum;
                         }
                     }
+                    sk = min(sk, hi);
+                    [[maybe_unused]] const bool edge = WIN && __any_sync(0xffffffffu, hi < BN || lo > 0);
                     const uint64_t sc2 = f2_splat(p.scale_log2);
                     const uint64_t nl_row = f2_splat(st_row.x), nd_row = f2_splat(st_row.y);
                     // columns [C0, C0 + CN): P and dS go where columns already read were
-                    auto part = [&](auto c0, auto cn, auto masked) {
+                    auto part = [&](auto c0, auto cn) {
                         constexpr int C0 = decltype(c0)::value, CN = decltype(cn)::value;
-                        constexpr bool MASKED = decltype(masked)::value;
-                        [[maybe_unused]] uint32_t seen = 0;
                         uint32_t sr[CN], dr[CN];
 #pragma unroll
                         for (int c = 0; c < CN; c += 16)
@@ -692,18 +692,27 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const std::conditi
                             asm("mov.b64 %0, {%1, %2};\n" : "=l"(pp) : "f"(p0), "f"(p1));
                             float g0, g1;
                             f2_split(f2_mul(f2_add(f2_from_u32(dr[c], dr[c + 1]), d2), pp), g0, g1);
-                            if constexpr (MASKED) {           // exactly 0, whatever was there
-                                if (c % 32 == 0) seen = seen_bits(C0 + c, hi, lo, sk);
-                                const bool s0 = seen & (1u << c % 32), s1 = seen & (2u << c % 32);
-                                p0 = s0 ? p0 : 0.f;
-                                g0 = s0 ? g0 : 0.f;
-                                p1 = s1 ? p1 : 0.f;
-                                g1 = s1 ? g1 : 0.f;
-                            }
                             sr[c / 2] = pack_bf16x2(p0, p1);
                             dr[c / 2] = pack_bf16x2(g0, g1);
                         }
-                        if (!WIN && valid < C0 + CN) {            // columns past the end: exactly 0, whatever was there
+                        if constexpr (WIN) {                      // what is not seen: exactly 0, whatever was there
+                            if (edge) {
+#pragma unroll
+                                for (int x = 0; x < CN; x += 32) {
+                                    constexpr uint32_t LAST = CN % 32 ? (1u << CN % 32) - 1 : 0xffffffffu;
+                                    const uint32_t seen = seen_bits(C0 + x, hi, lo, sk), all = x + 32 > CN ? LAST : 0xffffffffu;
+                                    if (!__all_sync(0xffffffffu, (seen & all) == all)) {
+#pragma unroll
+                                        for (int c = 0; c < 32; ++c)
+                                            if (x + c < CN && !(seen & (1u << c))) {
+                                                const uint32_t other = c % 2 ? 0x0000ffffu : 0xffff0000u;
+                                                sr[(x + c) / 2] &= other;
+                                                dr[(x + c) / 2] &= other;
+                                            }
+                                    }
+                                }
+                            }
+                        } else if (valid < C0 + CN) {             // columns past the end: exactly 0, whatever was there
 #pragma unroll
                             for (int c = 0; c < CN; c += 2) {
                                 const int x = C0 + c;
@@ -722,13 +731,12 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const std::conditi
                             tmem_st8(tD + C0 / 2 + c, *reinterpret_cast<const uint32_t(*)[8]>(dr + c));
                     };
                     using std::integral_constant;
-                    auto parts = [&](auto first, auto masked) {
-                        constexpr int N = decltype(first)::value;
-                        part(integral_constant<int, 0>(), first, masked);
-                        if constexpr (N < BN) part(first, integral_constant<int, BN - N>(), masked);
+                    auto parts = [&] {
+                        part(integral_constant<int, 0>(), integral_constant<int, C::PART>());
+                        if constexpr (C::PART < BN)
+                            part(integral_constant<int, C::PART>(), integral_constant<int, BN - C::PART>());
                     };
                     if constexpr (WIN) {
-                        sk = min(sk, hi);
                         if (!__any_sync(0xffffffffu, hi > 0 && (lo < hi || sk > 0))) {
                             // none of the warp's pairs is seen: P = dS = 0, without a look at S and dP
                             const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
@@ -737,14 +745,11 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const std::conditi
                                 if constexpr (DKV) tmem_st8(tS + c, zero);
                                 tmem_st8(tD + c, zero);
                             }
-                        } else if (__any_sync(0xffffffffu, hi < BN || lo > 0)) {
-                            // (the mask's registers do not fit beside 80 columns)
-                            parts(integral_constant<int, (BN / 2 + 15) / 16 * 16>(), std::true_type());
                         } else {
-                            parts(integral_constant<int, C::PART>(), std::false_type());
+                            parts();
                         }
                     } else {
-                        parts(integral_constant<int, C::PART>(), std::false_type());
+                        parts();
                     }
                     tmem_wait_st();
                     tc_fence_before();
