@@ -140,6 +140,9 @@ struct Grad {
 struct GradMaps {
     CUtensorMap x1, x2, y1, y2;
 };
+struct WinGradMaps : GradMaps {
+    CUtensorMap o1, o2;           // the outputs, in boxes of 32 rows
+};
 struct WinGrad : Grad {
     const WinGradItem *win_items;
     int32_t *next;                // items handed out so far beyond each block's first
@@ -160,7 +163,8 @@ template <int D> struct WinGradShared : GradShared<D> {
 };
 
 template <int D, bool DKV, bool WIN>
-__device__ __forceinline__ void grad_pass(const GradMaps &tm, const std::conditional_t<WIN, WinGrad, Grad> &p,
+__device__ __forceinline__ void grad_pass(const std::conditional_t<WIN, WinGradMaps, GradMaps> &tm,
+                                          const std::conditional_t<WIN, WinGrad, Grad> &p,
                                           std::conditional_t<WIN, WinGradShared<D>, GradShared<D>> &sh)
 {
     using C = GradCfg<D, DKV>;
@@ -179,7 +183,7 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const std::conditi
         s_abort = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar_addr(bars.x_full[i]), 1);
-            mbar_init(bar_addr(bars.x_empty[i]), 1);
+            mbar_init(bar_addr(bars.x_empty[i]), WIN ? 9 : 1);   // the issuer, and the softmax warps
             mbar_init(bar_addr(bars.s_full[i]), 1);
             mbar_init(bar_addr(bars.p_full[i]), 4);
             mbar_init(bar_addr(bars.stat[i]), 1);
@@ -766,40 +770,106 @@ __device__ __forceinline__ void grad_pass(const GradMaps &tm, const std::conditi
             }
             if (!ok) break;
             u0 += n;
-            // ---- the item's sums: group 0 writes dk, group 1 dv; of dq each writes half of the columns
-            constexpr int COLS = DKV ? D : D / 2;
-            const int col0 = DKV ? 0 : grp * COLS;
-            const uint32_t tA = t_lane + (DKV && grp ? C::TA2 : C::TA1) + col0;
-            __nv_bfloat16 *dst = DKV && grp ? p.out2 + (int64_t)o_row * p.out2_stride
-                                            : p.out1 + (int64_t)o_row * p.out1_stride;
-            dst += (int64_t)o_head * D + col0;
-            const float f = DKV && grp ? 1.f : p.scale;
-            if (n > 0) {
-                if (!(ok = wait_warp(bars.acc_done, xc & 1))) break;
-                ++xc;
-                tc_fence_after();
-            }
+            if constexpr (WIN) {
+                // The item's sums: group 0 writes dk, group 1 dv; of dq each writes its slabs. They go through the X tiles,
+                // which the item no longer needs (and which have the outputs' shape), and from there by TMA: a store of
+                // 16 bytes per row by every lane took 12 % of the time at a window of 1024. Tiles that the sequence ends
+                // in are written by row.
+                constexpr int HALF = (C::NS + 1) / 2;
+                auto write = [&](auto first, auto last) {
+                    constexpr int S0 = decltype(first)::value, S1 = decltype(last)::value, COLS = (S1 - S0) * W;
+                    const int which = DKV ? grp : 0;
+                    uint32_t r[COLS > 0 ? COLS : 1];
 #pragma unroll
-            for (int c = 0; c < COLS; c += 8) {
-                uint32_t r[8];
+                    for (int c = 0; c < COLS; ++c) r[c] = 0u;
+                    const uint32_t xb = xc & 1;
+                    if (n > 0) {
+                        if (!(ok = wait_warp(bars.acc_done, xc & 1))) return;
+                        ++xc;
+                        tc_fence_after();
+#pragma unroll
+                        for (int c = 0; c < COLS; c += 8)
+                            tmem_ld8(t_lane + (which ? C::TA2 : C::TA1) + S0 * W + c, *reinterpret_cast<uint32_t(*)[8]>(r + c));
+                        tmem_wait_ld();
+                        reg_fence(r);
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar_addr(bars.acc_free));
+                    }
+                    const float f = which ? 1.f : p.scale;
+                    const bool whole = n > 0 && it.r0 + (DKV ? BM : BM >> p.lg_pack) <= it.r1;
+                    unsigned char *x = base + (2 * xb + which) * C::X_TILE;
+                    __nv_bfloat16 *dst = (which ? p.out2 + (int64_t)o_row * p.out2_stride
+                                                : p.out1 + (int64_t)o_row * p.out1_stride) + (int64_t)o_head * D;
+#pragma unroll
+                    for (int c = 0; c < COLS; c += 8) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            o[e] = pack_bf16x2(__uint_as_float(r[c + 2 * e]) * f, __uint_as_float(r[c + 2 * e + 1]) * f);
+                        const uint4 v = make_uint4(o[0], o[1], o[2], o[3]);
+                        // 16-byte piece k of the row in slab s, where the swizzle puts it
+                        const int s = S0 + c / W, k = c % W / 8;
+                        const int at = C::SW == 128 ? k ^ (row & 7) : C::SW == 64 ? k ^ ((row >> 1) & 3) : k ^ ((row >> 2) & 1);
+                        if (whole) *reinterpret_cast<uint4 *>(x + s * C::X_SLAB + row * C::SW + 16 * at) = v;
+                        else if (exists) *reinterpret_cast<uint4 *>(dst + S0 * W + c) = v;
+                    }
+                    if (whole && COLS > 0) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+#pragma unroll
+                            for (int s = S0; s < S1; ++s)
+                                tma_store_3d(which ? &tm.o2 : &tm.o1, smem_addr(x + s * C::X_SLAB + 32 * quarter * C::SW),
+                                             W * s, it.head, it.r0 + (DKV ? 32 * quarter : (32 * quarter) >> p.lg_pack));
+                            bulk_commit();
+                            bulk_wait_read_all();
+                        }
+                    }
+                    if (n > 0 && lane == 0) mbar_arrive(bar_addr(bars.x_empty[xb]));
+                    __syncwarp();
+                };
+                if (DKV) write(std::integral_constant<int, 0>(), std::integral_constant<int, C::NS>());
+                else if (grp == 0) write(std::integral_constant<int, 0>(), std::integral_constant<int, HALF>());
+                else write(std::integral_constant<int, HALF>(), std::integral_constant<int, C::NS>());
+                if (!ok) break;
+                continue;
+            } else {
+                // ---- the item's sums: group 0 writes dk, group 1 dv; of dq each writes half of the columns
+                constexpr int COLS = DKV ? D : D / 2;
+                const int col0 = DKV ? 0 : grp * COLS;
+                const uint32_t tA = t_lane + (DKV && grp ? C::TA2 : C::TA1) + col0;
+                __nv_bfloat16 *dst = DKV && grp ? p.out2 + (int64_t)o_row * p.out2_stride
+                                                : p.out1 + (int64_t)o_row * p.out1_stride;
+                dst += (int64_t)o_head * D + col0;
+                const float f = DKV && grp ? 1.f : p.scale;
                 if (n > 0) {
-                    tmem_ld8(tA + c, r);
-                    tmem_wait_ld();
-                    reg_fence(r);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) r[e] = 0u;
+                    if (!(ok = wait_warp(bars.acc_done, xc & 1))) break;
+                    ++xc;
+                    tc_fence_after();
                 }
-                uint32_t o[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    o[e] = pack_bf16x2(__uint_as_float(r[2 * e]) * f, __uint_as_float(r[2 * e + 1]) * f);
-                if (exists) *reinterpret_cast<uint4 *>(dst + c) = make_uint4(o[0], o[1], o[2], o[3]);
-            }
-            if (n > 0) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_addr(bars.acc_free));
+                for (int c = 0; c < COLS; c += 8) {
+                    uint32_t r[8];
+                    if (n > 0) {
+                        tmem_ld8(tA + c, r);
+                        tmem_wait_ld();
+                        reg_fence(r);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) r[e] = 0u;
+                    }
+                    uint32_t o[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        o[e] = pack_bf16x2(__uint_as_float(r[2 * e]) * f, __uint_as_float(r[2 * e + 1]) * f);
+                    if (exists) *reinterpret_cast<uint4 *>(dst + c) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+                if (n > 0) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_addr(bars.acc_free));
+                }
             }
         }
     }
@@ -827,7 +897,7 @@ cross_grad_kernel(const __grid_constant__ GradMaps tm_dkv, const __grid_constant
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-window_grad_kernel(const __grid_constant__ GradMaps tm_dkv, const __grid_constant__ GradMaps tm_dq,
+window_grad_kernel(const __grid_constant__ WinGradMaps tm_dkv, const __grid_constant__ WinGradMaps tm_dq,
                    const __grid_constant__ WinGrad dkv, const __grid_constant__ WinGrad dq)
 {
     __shared__ WinGradShared<D> sh;
@@ -1245,11 +1315,21 @@ cudaError_t launch_d(const CrossGradArgs &a, const GradPlan &pl, int window, int
         if (e != cudaSuccess) return e;
     }
 
-    GradMaps m_dkv, m_dq;
+    std::conditional_t<W, WinGradMaps, GradMaps> m_dkv, m_dq;
     std::conditional_t<W, WinGrad, Grad> dkv, dq;
     if (!make_pass<D, true>(a, pl, num_sms, m_dkv, dkv) || !make_pass<D, false>(a, pl, num_sms, m_dq, dq))
         return cudaErrorInvalidValue;
     if constexpr (W) {
+        constexpr int cols = GradCfg<D, true>::W;
+        static_assert(cols == GradCfg<D, false>::W, "slabs of both passes");
+        // (a side without rows has no items: nothing is stored there, but a map needs an address)
+        const void *dq_at = s.Tq > 0 ? a.dq : a.dk, *dk_at = s.Tk > 0 ? a.dk : a.dq, *dv_at = s.Tk > 0 ? a.dv : a.dq;
+        const int64_t nq = (int64_t)a.f.Hq * D, nk = (int64_t)a.f.Hk * D;
+        if (!tile_map(&m_dkv.o1, dk_at, s.Tk, a.f.Hk, D, s.Tk > 0 ? a.dk_stride : nk, cols, 1, 32) ||
+            !tile_map(&m_dkv.o2, dv_at, s.Tk, a.f.Hk, D, s.Tk > 0 ? a.dv_stride : nk, cols, 1, 32) ||
+            !tile_map(&m_dq.o1, dq_at, s.Tq, a.f.Hq, D, s.Tq > 0 ? a.dq_stride : nq, cols, 1 << pl.lg_pack, 32))
+            return cudaErrorInvalidValue;
+        m_dq.o2 = m_dq.o1;
         dkv.win_items = static_cast<const WinGradItem *>(r.dkv);
         dq.win_items = static_cast<const WinGradItem *>(r.dq);
         dkv.next = r.counts + 3;

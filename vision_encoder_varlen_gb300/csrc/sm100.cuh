@@ -115,6 +115,13 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+// 3D tiled store of the box at {x, y, z} (none negative) from smem, part of the thread's next bulk group.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, uint32_t src, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];\n" ::"l"(map),
+                 "r"(x), "r"(y), "r"(z), "r"(src)
+                 : "memory");
+}
+
 // One thread of a converged warp, chosen by the hardware: unlike a test of the lane index it tells the
 // compiler that the branch is taken by a single thread, which keeps the operands of the tensor-core
 // instructions below in uniform registers.
