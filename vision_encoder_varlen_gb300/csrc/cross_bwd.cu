@@ -561,6 +561,15 @@ __device__ __forceinline__ void grad_pass(const std::conditional_t<WIN, WinGradM
         const int grp = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
         uint32_t u0 = 0, xc = 0;                              // tiles and items with tiles before this item
+        // WIN: the X buffer that this warp's store still reads, or -1; it is given back behind the warp's next tile
+        [[maybe_unused]] int pending = -1;
+        [[maybe_unused]] auto release = [&] {
+            if (pending >= 0 && lane == 0) {
+                bulk_wait_read_all();
+                mbar_arrive(bar_addr(bars.x_empty[pending]));
+            }
+            pending = -1;
+        };
         bool ok = true;
         for (int i = first_item(), n_items = list_length(); ok && i < n_items; i = next_item(i)) {
             const GradItem it = items[i];
@@ -759,6 +768,7 @@ __device__ __forceinline__ void grad_pass(const std::conditional_t<WIN, WinGradM
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar_addr(bars.p_full[st]));
+                    if constexpr (WIN) release();
                 }
             };
             using std::bool_constant;
@@ -823,12 +833,14 @@ __device__ __forceinline__ void grad_pass(const std::conditional_t<WIN, WinGradM
                                 tma_store_3d(which ? &tm.o2 : &tm.o1, smem_addr(x + s * C::X_SLAB + 32 * quarter * C::SW),
                                              W * s, it.head, it.r0 + (DKV ? 32 * quarter : (32 * quarter) >> p.lg_pack));
                             bulk_commit();
-                            bulk_wait_read_all();
                         }
+                        pending = (int)xb;
+                    } else if (n > 0 && lane == 0) {
+                        mbar_arrive(bar_addr(bars.x_empty[xb]));
                     }
-                    if (n > 0 && lane == 0) mbar_arrive(bar_addr(bars.x_empty[xb]));
                     __syncwarp();
                 };
+                release();
                 if (DKV) write(std::integral_constant<int, 0>(), std::integral_constant<int, C::NS>());
                 else if (grp == 0) write(std::integral_constant<int, 0>(), std::integral_constant<int, HALF>());
                 else write(std::integral_constant<int, HALF>(), std::integral_constant<int, C::NS>());
@@ -872,6 +884,7 @@ __device__ __forceinline__ void grad_pass(const std::conditional_t<WIN, WinGradM
                 }
             }
         }
+        if constexpr (WIN) release();                         // (the shared memory goes with the block)
     }
     tc_fence_before();
     __syncthreads();
