@@ -641,8 +641,9 @@ size_t vit_prefix_attn_workspace_size(int64_t Tq, int64_t Tp, int64_t Tk, int Hq
  *   cu_p         device int32 [G + 1], ascending; rows of no group are not read.
  *   G            1 <= G <= VIT_MAX_SEGMENTS (0 only with B = 0).
  *   max_p        bound of the prefixes' lengths, 0: Tp.
- *   The other arguments and errors are those of vit_cross_attn, but where any sequence, group or
- *   prefix is malformed nothing is computed and the outputs are left untouched.
+ *   The other arguments and errors are those of vit_cross_attn: the rows of a malformed sequence, or
+ *   of a group that is malformed or whose prefix is, are left untouched, and the others of such a
+ *   call may or may not be computed.
  */
 vit_status_t vit_prefix_attn(const void *q, const void *k_prefix, const void *v_prefix, const void *k, const void *v,
                              int64_t Tq, int64_t Tp, int64_t Tk, int Hq, int Hkv, int D, int64_t q_stride,

@@ -34,9 +34,11 @@ def plan(Tq, B, Hq, Hk, D, max_q, max_k, window, sinks, G, Tp, max_p):
     apart = prefix and own > 2 * grouped
     own_most = cdiv(min(max_k, window + 2 * tok - 1) if window else max_k, bn)
     first_most = cdiv(max_p if prefix else min(sinks, max_k) if window else 0, bn)
-    p = dict(lg=lg, apart=apart, units=(G + B if apart else B), run=0, slots=0, tiles=0)
+    own_few = apart and few(B, Hq, Hk, D, max_q, max_k, 0, 0)
+    p = dict(lg=lg, apart=apart, own_few=own_few, units=(G if own_few else G + B if apart else B), run=0, slots=0, tiles=0)
     least = 2 * cdiv(512, 2 * bn)
     if apart:
+        own = 0 if own_few else own
         p["run"] = run = max(least, cdiv((own * own_most + grouped * first_most) * packs, 4 * SMS))
         p["items"] = p["slots"] = (grouped * max(1, cdiv(first_most, run)) + own * max(1, cdiv(own_most, run))) * packs
     else:
@@ -47,8 +49,18 @@ def plan(Tq, B, Hq, Hk, D, max_q, max_k, window, sinks, G, Tp, max_p):
             if cdiv(most, run) > 1:
                 p.update(run=run, items=tiles * cdiv(most, run), tiles=tiles, slots=tiles * cdiv(most, run))
     part_s = up(up(up(up(64 + 48 * p["items"]) + 32 * p["tiles"]) + 8 * B) + (16 * p["units"] if apart else 0))
-    p["bytes"] = up(part_s + p["slots"] * 512) + p["slots"] * 512 * D
+    p["bytes"] = up(up(part_s + p["slots"] * 512) + p["slots"] * 512 * D)
+    if own_few:
+        p["bytes"] += few_bytes(B, Hq, Hk, D, max_q, max_k)
     return p
+
+
+def few_bytes(B, Hq, Hk, D, max_q, max_k):
+    """Partial results of the kernel for few rows, also where it makes one run."""
+    rows, pairs = max_q * (Hq // Hk), B * Hk
+    n = max(1, min((8 * SMS + pairs // 2) // pairs, cdiv(max_k, max(16 * rows, 128))))
+    chunk = max(64, cdiv(cdiv(max_k, n), 64) * 64)
+    return 4 * pairs * (cdiv(max_k, chunk) if max_k else 1) * rows * (D + 1)
 
 
 def few(B, Hq, Hk, D, max_q, max_k, window, sinks):
@@ -72,12 +84,12 @@ def make_list(p, ql, kl, Hq, D, window, sinks, prefixes=None, groups=None, sms=S
     bn, lg_tile, packs = tile_keys(D), 7 - p["lg"], Hq >> p["lg"]
     units, at = [], 0
     start = [sum(ql[:i]) for i in range(len(ql))]
-    if p["apart"]:
+    if p["apart"]:                                     # the groups first
         for f, m in zip(prefixes, groups):
             units.append(dict(q=(start[at] if m else 0), n=sum(ql[at:at + m]), f=f, k=0, p0=0))
             at += m
     of = [f for f, m in zip(prefixes or [], groups or []) for _ in range(m)]
-    for b, (m, n) in enumerate(zip(ql, kl)):
+    for b, (m, n) in enumerate(zip(ql, kl) if not p["own_few"] else ()):
         f = of[b] if of and not p["apart"] else 0
         none = max(0, m - n) if f == 0 else 0
         units.append(dict(q=start[b] + none, n=m - none, f=f, k=n, p0=n - m + none))
@@ -126,6 +138,9 @@ def check(ql, kl, Hq, Hk, D, window=0, sinks=0, prefixes=None, groups=None, loos
     window = 0 if window >= max_k else window          # it leaves nothing out
     sinks = sinks if window else 0
     p = plan(Tq, B, Hq, Hk, D, max_q, max_k, window, sinks, G, Tp, max_p)
+    rows, keys = max_q * (Hq // Hk), cdiv(max_p, 64) * 64 + max_k
+    if prefixes is not None and few(B, Hq, Hk, D, max_q, keys, 0, 0) and B * keys * Hk * D * 4 <= 96 << 20:
+        return                                         # each sequence reads its prefix: no list
     if prefixes is not None:
         assert vit.prefix_attn_workspace_size(Tq, Tp, sum(kl), Hq, Hk, D, B, G, max_q, max_p, max_k) == p["bytes"]
     elif not few(B, Hq, Hk, D, max_q, max_k, window, sinks):

@@ -829,8 +829,8 @@ def prefix_attn(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Tensor,
     """Attention of sequences that share prefixes: the sequences cu_group[g] .. cu_group[g + 1] (None: all of them)
     see the rows cu_prefix[g] .. cu_prefix[g + 1] of k_prefix, v_prefix [Tp, Hkv, D] and behind them their own keys
     k, v [Tk, Hkv, D] causally, as in window_attn without a window. The prefix is read once for all of a group's
-    short sequences. ``max_q``, ``max_prefix`` and ``max_k`` bound the lengths (None: Tq, Tp, Tk). A malformed list
-    leaves the whole call uncomputed; the rest is as for window_attn."""
+    short sequences. ``max_q``, ``max_prefix`` and ``max_k`` bound the lengths (None: Tq, Tp, Tk). The rest is
+    as for window_attn."""
     Tq, Hq, D = _shape3(q, "q")
     Tk, Hkv, _ = _shape3(k, "k")
     Tp = _shape3(k_prefix, "k_prefix")[0]

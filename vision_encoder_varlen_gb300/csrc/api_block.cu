@@ -423,7 +423,8 @@ vit_status_t vit_window_attn(const void *q, const void *k, const void *v, int64_
     a.sinks = sinks;
     cudaStream_t s = (cudaStream_t)stream;
     if (window_takes_few(B, Hq, Hkv, D, max_q, max_k, window, sinks))
-        return from_cuda(launch_window_few(a, window_few_plan(B, Hq, Hkv, D, max_q, max_k, window, sinks), s));
+        return from_cuda(launch_window_few(a, window_few_plan(B, Hq, Hkv, D, max_q, max_k, window, sinks), false,
+                                           workspace, s));
     return from_cuda(launch_window_tiles(a, win_plan(Tq, B, Hq, Hkv, D, max_q, max_k, window, sinks, 0, 0, 0), sms, s));
 }
 
@@ -480,6 +481,10 @@ size_t vit_prefix_attn_workspace_size(int64_t Tq, int64_t Tp, int64_t Tk, int Hq
 {
     if (prefix_sizes(Tq, Tp, Tk, Hq, Hkv, D, B, G, &max_q, &max_p, &max_k) != VIT_OK) return 0;
     if (B == 0 || Tq == 0) return 16;
+    if (prefix_takes_few(B, Hq, Hkv, D, max_q, max_k, max_p)) {
+        const size_t n = prefix_few_plan(B, Hq, Hkv, D, max_q, max_k, max_p).partial_bytes;
+        return n > 16 ? n : 16;
+    }
     const WinPlan p = win_plan(Tq, B, Hq, Hkv, D, max_q, max_k, 0, 0, G, Tp, max_p);
     return p.max_items >= kMaxItems ? 0 : p.bytes;
 }
@@ -520,11 +525,10 @@ vit_status_t vit_prefix_attn(const void *q, const void *k_prefix, const void *v_
     a.vp = Tp > 0 ? v_prefix : q;
     a.kp_stride = Tp > 0 ? kp_stride : (int64_t)Hkv * D;
     a.vp_stride = Tp > 0 ? vp_stride : (int64_t)Hkv * D;
-    a.Tp = Tp;
-    a.cu_g = cu_g;
-    a.cu_p = cu_p;
-    a.G = G;
-    a.max_p = max_p;
+    a.groups = Groups{cu_g, cu_p, Tp, G, max_p, B};
+    if (prefix_takes_few(B, Hq, Hkv, D, max_q, max_k, max_p))
+        return from_cuda(launch_window_few(a, prefix_few_plan(B, Hq, Hkv, D, max_q, max_k, max_p), false, workspace,
+                                           (cudaStream_t)stream));
     return from_cuda(launch_window_tiles(a, win_plan(Tq, B, Hq, Hkv, D, max_q, max_k, 0, 0, G, Tp, max_p), sms,
                                          (cudaStream_t)stream));
 }

@@ -1210,9 +1210,9 @@ cudaError_t launch_window_d(const WinArgs &a, const WinLong &cx, const WsHeader 
         !make_map(&mv, f.v, s.Tk, f.Hk, D, f.v_stride, C::BN, 16))
         return cudaErrorInvalidValue;
     if (a.prefix) {
-        if (!make_map(&first.k, a.kp, a.Tp, f.Hk, D, a.kp_stride, C::BN, wide) ||
-            !make_map(&first.kr, a.kp, a.Tp, f.Hk, D, a.kp_stride, C::BN, rem) ||
-            !make_map(&first.v, a.vp, a.Tp, f.Hk, D, a.vp_stride, C::BN, 16))
+        if (!make_map(&first.k, a.kp, a.groups.Tp, f.Hk, D, a.kp_stride, C::BN, wide) ||
+            !make_map(&first.kr, a.kp, a.groups.Tp, f.Hk, D, a.kp_stride, C::BN, rem) ||
+            !make_map(&first.v, a.vp, a.groups.Tp, f.Hk, D, a.vp_stride, C::BN, 16))
             return cudaErrorInvalidValue;
     } else {
         first = FirstMaps{mk, mkr, mv};

@@ -27,6 +27,8 @@
 // A causal window (W): the keys that a sequence's queries see between them are its first `sn` tokens, in tiles of
 // their own, and the run of positions from `lo` on; a run of `chunk` keys counts along both. Keys outside are not
 // loaded, and where there is more than one query each masks for itself what another one sees.
+#include <type_traits>
+
 #include "cross.h"
 #include "sm100.cuh"
 #include "warp_mma.cuh"
@@ -64,29 +66,58 @@ struct Few {
     int32_t *status;
     int chunk, n_split, rows;                 // rows: max_q * group, the partial rows of a split
     float *part_o, *part_s;                   // [B][Hk][n_split][rows][D] and [..][rows] (log2 of the run's sum)
+    bool parts;                               // W: leave the runs' partial results even where there is only one run
     int window, sinks;                        // W: as in WinLong
+    bool prefix;
+    Groups groups;
 };
 
-// The keys of a sequence as the runs count them: [0, head) are its first sn tokens padded to whole tiles, and
-// head + i is position lo + i; n in all. Without a window: its keys.
+// The keys of a sequence as the runs count them: [0, head) are the rows from f0 on, padded to whole tiles (its first sn
+// tokens, or the prefix), and head + i is position lo + i of its own; n in all. A query before the first own key sees the
+// prefix alone, or nothing (`none` of them).
 struct Keys {
-    int sn, head, lo, n;
+    int f0, sn, head, lo, n, none;
 };
-__device__ __forceinline__ Keys window_keys(const Few &p, const WinSeg &w)
+__device__ __forceinline__ Keys window_keys(const Few &p, int b, const CrossSeg &x, bool report, bool &fine)
 {
-    const WinRange r = win_range(w.p0, p.window, p.sinks);
-    const int head = (r.first + kTile - 1) / kTile * kTile;
-    return Keys{r.first, head, r.lo, w.qn > 0 ? head + w.kn - r.lo : 0};
+    const WinSeg w = win_seg(x);
+    Keys k{x.k0, 0, 0, 0, 0, w.none};
+    fine = true;
+    if (p.prefix) {
+        const int g = p.groups.of(b);
+        const int err = p.groups.bound(g) > b || p.groups.bound(g + 1) <= b ? VIT_ERR_BAD_SEQLENS : p.groups.error(g);
+        if (err) {
+            if (report) report_error(p.status, err);
+            fine = false;
+            return k;
+        }
+        p.groups.load(g, k.f0, k.sn);
+        if (k.sn > 0) k.none = 0;
+    } else {
+        const WinRange r = win_range(w.p0, p.window, p.sinks);
+        k.sn = r.first;
+        k.lo = r.lo;
+    }
+    k.head = (k.sn + kTile - 1) / kTile * kTile;
+    k.n = x.qn > k.none ? k.head + w.kn - k.lo : 0;
+    return k;
 }
 
 // Warps of a block: MT row tiles x 4 key groups.
 constexpr int kGroups = 4;
 template <int MT> constexpr int kMmaWarps = MT * kGroups;
 
+// W: the tensors of the keys that are read first
+struct FewMaps {
+    CUtensorMap k, kr, v, vr;
+};
+struct NoMaps {};
+
 template <int D, int MT, bool W>
 __global__ void __launch_bounds__(32 * kMmaWarps<MT> + 32)
 cross_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_kr,
-                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_vr, const Few p)
+                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_vr,
+                 const __grid_constant__ std::conditional_t<W, FewMaps, NoMaps> tm_f, const Few p)
 {
     using T = Tile<D>;
     constexpr int NK = D / 16, KQ = kGroups, NW = kMmaWarps<MT>;
@@ -105,24 +136,25 @@ cross_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     if (!load_seg(p.segs, b, seg, p.status, threadIdx.x == 0 && split == 0 && hk == 0)) return;
     if (seg.qn == 0) return;
     const int first = split * p.chunk;
-    const bool only = p.n_split == 1;
-    Keys keys{0, 0, 0, 0};
+    const bool only = p.n_split == 1 && !(W && p.parts);
+    Keys keys{0, 0, 0, 0, 0, 0};
     int p0 = 0;                                               // position of the first query
     if constexpr (W) {
-        const WinSeg w = win_seg(seg);
-        // queries before the first key see nothing: zeros, by the first run's block
-        if (split == 0)
-            for (int x = threadIdx.x; x < w.none * p.group * (D / 8); x += 32 * NW + 32) {
+        bool fine;
+        keys = window_keys(p, b, seg, threadIdx.x == 0 && split == 0 && hk == 0, fine);
+        if (!fine) return;
+        // queries that see nothing: zeros, by the first run's block
+        if (split == 0 && !p.parts)
+            for (int x = threadIdx.x; x < keys.none * p.group * (D / 8); x += 32 * NW + 32) {
                 const int r = x / (D / 8), c = x % (D / 8), head = hk * p.group + r % p.group;
                 const int64_t t = seg.q0 + r / p.group;
                 *reinterpret_cast<uint4 *>(p.out + t * p.out_stride + (int64_t)head * D + 8 * c) = make_uint4(0u, 0u, 0u, 0u);
                 if (p.lse && c == 0) p.lse[t * p.Hq + head] = -INFINITY;
             }
-        keys = window_keys(p, w);
         if (first >= keys.n) return;
-        seg.q0 = w.q0;
-        seg.qn = w.qn;
-        p0 = w.p0;
+        p0 = seg.kn - seg.qn + keys.none;
+        seg.q0 += keys.none;
+        seg.qn -= keys.none;
     } else {
         if (first >= seg.kn && !(only && seg.kn == 0)) return;
     }
@@ -161,18 +193,27 @@ cross_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 if (i >= kStages && !wait(s_empty[s], (i / kStages - 1) & 1)) break;
                 const uint32_t bar = sm100::smem_addr(&s_full[s]), dst = sm100::smem_addr(ring) + s * 2 * T::BYTES;
                 int row = seg.k0 + first + i * kTile;
+                const CUtensorMap *mk = &tm_k, *mkr = &tm_kr, *mv = &tm_v, *mvr = &tm_vr;
                 if constexpr (W) {
-                    if (first + i * kTile >= keys.head) row += keys.lo - keys.head;
+                    if (first + i * kTile >= keys.head) {
+                        row += keys.lo - keys.head;
+                    } else {
+                        row += keys.f0 - seg.k0;
+                        mk = &tm_f.k;
+                        mkr = &tm_f.kr;
+                        mv = &tm_f.v;
+                        mvr = &tm_f.vr;
+                    }
                 }
                 sm100::mbar_arrive_expect_tx(bar, 2 * T::BYTES);
 #pragma unroll
                 for (int x = 0; x < T::N128; ++x) {
-                    sm100::tma_load_2d(dst + x * kTile * 128, &tm_k, hk * D + 64 * x, row, bar);
-                    sm100::tma_load_2d(dst + T::BYTES + x * kTile * 128, &tm_v, hk * D + 64 * x, row, bar);
+                    sm100::tma_load_2d(dst + x * kTile * 128, mk, hk * D + 64 * x, row, bar);
+                    sm100::tma_load_2d(dst + T::BYTES + x * kTile * 128, mv, hk * D + 64 * x, row, bar);
                 }
                 if constexpr (T::REM > 0) {
-                    sm100::tma_load_2d(dst + T::N128 * kTile * 128, &tm_kr, hk * D + 64 * T::N128, row, bar);
-                    sm100::tma_load_2d(dst + T::BYTES + T::N128 * kTile * 128, &tm_vr, hk * D + 64 * T::N128, row, bar);
+                    sm100::tma_load_2d(dst + T::N128 * kTile * 128, mkr, hk * D + 64 * T::N128, row, bar);
+                    sm100::tma_load_2d(dst + T::BYTES + T::N128 * kTile * 128, mvr, hk * D + 64 * T::N128, row, bar);
                 }
             }
             // after a wait that gave up: let what was issued land before the shared memory goes
@@ -240,7 +281,7 @@ cross_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     __syncwarp();
                 }
                 if constexpr (W) {
-                    if (seg.qn > 1) {
+                    if (seg.qn > 1 && first + i * kTile >= keys.head) {
                         // rows g and g + 8: keys up to `hi`, from `lo` on or before `sk`
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
@@ -406,10 +447,12 @@ cross_join_kernel(const Few p)
     if (!load_seg(p.segs, b, seg, nullptr, false)) return;
     int n_keys = seg.kn;
     if constexpr (W) {                                        // (queries that see nothing are written already)
-        const WinSeg w = win_seg(seg);
-        n_keys = window_keys(p, w).n;
-        seg.q0 = w.q0;
-        seg.qn = w.qn;
+        bool fine;
+        const Keys keys = window_keys(p, b, seg, false, fine);
+        if (!fine) return;
+        n_keys = keys.n;
+        seg.q0 += keys.none;
+        seg.qn -= keys.none;
     }
     const int n_rows = seg.qn * p.Hq;                         // (token, head) rows of the sequence
     const int runs = key_runs(n_keys, p.chunk);
@@ -466,19 +509,29 @@ bool kv_map(CUtensorMap *m, const void *ptr, int64_t T, int H, int D, int64_t st
     return encode_tiled_map(m, ptr, 2, dims, strides, box, cols * 2);
 }
 
-template <int D, int MT, bool W>
-cudaError_t launch_mt(const CrossArgs &a, const FewPlan &pl, const Few &p, cudaStream_t stream)
+// a tensor's maps: the wide one and that of the remaining columns
+template <int D> bool kv_maps(CUtensorMap *m, CUtensorMap *mr, const void *ptr, int64_t T, int H, int64_t stride)
 {
     constexpr int rem = Tile<D>::REM > 0 ? Tile<D>::REM : 64, wide = D >= 64 ? 64 : rem;
+    if (!kv_map(m, ptr, T, H, D, stride, wide)) return false;
+    *mr = *m;
+    return rem == wide || kv_map(mr, ptr, T, H, D, stride, rem);
+}
+
+template <int D, int MT, bool W>
+cudaError_t launch_mt(const CrossArgs &a, const WinArgs *wa, const FewPlan &pl, const Few &p, cudaStream_t stream)
+{
     CUtensorMap mk, mkr, mv, mvr;
     const CrossSegs &s = a.segs;
-    if (!kv_map(&mk, a.k, s.Tk, a.Hk, D, a.k_stride, wide) || !kv_map(&mv, a.v, s.Tk, a.Hk, D, a.v_stride, wide))
+    if (!kv_maps<D>(&mk, &mkr, a.k, s.Tk, a.Hk, a.k_stride) || !kv_maps<D>(&mv, &mvr, a.v, s.Tk, a.Hk, a.v_stride))
         return cudaErrorInvalidValue;
-    mkr = mk;
-    mvr = mv;
-    if (rem != wide &&
-        (!kv_map(&mkr, a.k, s.Tk, a.Hk, D, a.k_stride, rem) || !kv_map(&mvr, a.v, s.Tk, a.Hk, D, a.v_stride, rem)))
-        return cudaErrorInvalidValue;
+    std::conditional_t<W, FewMaps, NoMaps> first;
+    if constexpr (W) {
+        first = FewMaps{mk, mkr, mv, mvr};
+        if (p.prefix && (!kv_maps<D>(&first.k, &first.kr, wa->kp, p.groups.Tp, a.Hk, wa->kp_stride) ||
+                         !kv_maps<D>(&first.v, &first.vr, wa->vp, p.groups.Tp, a.Hk, wa->vp_stride)))
+            return cudaErrorInvalidValue;
+    }
     constexpr int smem = kStages * 2 * Tile<D>::BYTES + 1024;
     static_assert(kStages * 2 * Tile<D>::BYTES >= 2 * MT * 16 * D * 4, "the joins reuse the ring");
     auto kern = cross_few_kernel<D, MT, W>;
@@ -487,9 +540,10 @@ cudaError_t launch_mt(const CrossArgs &a, const FewPlan &pl, const Few &p, cudaS
     if (e != cudaSuccess) return e;
     {
         LaunchScope scope(W ? "window_few" : "cross_few", stream);
-        e = launch_chained(kern, dim3(a.Hk, s.B, pl.n_split), 32 * kMmaWarps<MT> + 32, smem, stream, mk, mkr, mv, mvr, p);
+        e = launch_chained(kern, dim3(a.Hk, s.B, pl.n_split), 32 * kMmaWarps<MT> + 32, smem, stream, mk, mkr, mv, mvr,
+                           first, p);
     }
-    if (e != cudaSuccess || pl.n_split == 1) return e;
+    if (e != cudaSuccess || pl.n_split == 1 || p.parts) return e;
     LaunchScope scope("cross_join", stream);
     const int rows = s.max_q * a.Hq;
     // with more than 16 runs a warp per row is too few loads in flight (147 runs: 37 us)
@@ -498,11 +552,16 @@ cudaError_t launch_mt(const CrossArgs &a, const FewPlan &pl, const Few &p, cudaS
 }
 
 template <int D, bool W>
-cudaError_t launch_d(const CrossArgs &a, int window, int sinks, const FewPlan &pl, cudaStream_t stream)
+cudaError_t launch_d(const CrossArgs &a, const WinArgs *wa, const FewPlan &pl, bool parts, void *part, cudaStream_t stream)
 {
-    Few p;
-    p.window = window;
-    p.sinks = sinks;
+    Few p{};
+    if constexpr (W) {
+        p.window = wa->window;
+        p.sinks = wa->sinks;
+        p.prefix = wa->prefix && !parts;       // (else the prefix is another kernel's)
+        p.groups = wa->groups;
+    }
+    p.parts = parts;
     p.out = static_cast<__nv_bfloat16 *>(a.out);
     p.q = static_cast<const __nv_bfloat16 *>(a.q);
     p.lse = a.lse;
@@ -518,11 +577,11 @@ cudaError_t launch_d(const CrossArgs &a, int window, int sinks, const FewPlan &p
     p.n_split = pl.n_split;
     p.rows = pl.rows;
     const size_t n = (size_t)a.segs.B * a.Hk * pl.n_split * pl.rows;
-    p.part_o = static_cast<float *>(a.workspace);
+    p.part_o = static_cast<float *>(part);
     p.part_s = p.part_o + n * D;
     switch (pl.row_tiles) {
-        case 1: return launch_mt<D, 1, W>(a, pl, p, stream);
-        default: return launch_mt<D, 2, W>(a, pl, p, stream);
+        case 1: return launch_mt<D, 1, W>(a, wa, pl, p, stream);
+        default: return launch_mt<D, 2, W>(a, wa, pl, p, stream);
     }
 }
 
@@ -582,26 +641,43 @@ FewPlan window_few_plan(int B, int Hq, int Hk, int D, int max_q, int max_k, int 
     return few_plan(B, Hq, Hk, D, max_q, window_most(max_q, max_k, window, sinks));
 }
 
+// Behind prefixes: few rows where reading the prefix for each sequence anew costs less than the launches that share it.
+static int prefix_most(int max_k, int max_p)
+{
+    const int64_t most = ((int64_t)max_p + kTile - 1) / kTile * kTile + max_k;
+    return most < 0x7fff0000 ? (int)most : 0x7fff0000;
+}
+bool prefix_takes_few(int B, int Hq, int Hk, int D, int max_q, int max_k, int max_p)
+{
+    const int64_t keys = prefix_most(max_k, max_p);
+    return keys < 0x7fff0000 && takes_few(B, Hq, Hk, D, max_q, (int)keys) &&
+           B * keys * Hk * D * 4 <= ((int64_t)96 << 20);
+}
+FewPlan prefix_few_plan(int B, int Hq, int Hk, int D, int max_q, int max_k, int max_p)
+{
+    return few_plan(B, Hq, Hk, D, max_q, prefix_most(max_k, max_p));
+}
+
 cudaError_t launch_cross_few(const CrossArgs &a, const FewPlan &p, cudaStream_t stream)
 {
     switch (a.D) {
-        case 32: return launch_d<32, false>(a, 0, 0, p, stream);
-        case 64: return launch_d<64, false>(a, 0, 0, p, stream);
-        case 80: return launch_d<80, false>(a, 0, 0, p, stream);
-        case 96: return launch_d<96, false>(a, 0, 0, p, stream);
-        case 128: return launch_d<128, false>(a, 0, 0, p, stream);
+        case 32: return launch_d<32, false>(a, nullptr, p, false, a.workspace, stream);
+        case 64: return launch_d<64, false>(a, nullptr, p, false, a.workspace, stream);
+        case 80: return launch_d<80, false>(a, nullptr, p, false, a.workspace, stream);
+        case 96: return launch_d<96, false>(a, nullptr, p, false, a.workspace, stream);
+        case 128: return launch_d<128, false>(a, nullptr, p, false, a.workspace, stream);
         default: return cudaErrorInvalidValue;
     }
 }
 
-cudaError_t launch_window_few(const WinArgs &a, const FewPlan &p, cudaStream_t stream)
+cudaError_t launch_window_few(const WinArgs &a, const FewPlan &p, bool parts, void *part, cudaStream_t stream)
 {
     switch (a.f.D) {
-        case 32: return launch_d<32, true>(a.f, a.window, a.sinks, p, stream);
-        case 64: return launch_d<64, true>(a.f, a.window, a.sinks, p, stream);
-        case 80: return launch_d<80, true>(a.f, a.window, a.sinks, p, stream);
-        case 96: return launch_d<96, true>(a.f, a.window, a.sinks, p, stream);
-        case 128: return launch_d<128, true>(a.f, a.window, a.sinks, p, stream);
+        case 32: return launch_d<32, true>(a.f, &a, p, parts, part, stream);
+        case 64: return launch_d<64, true>(a.f, &a, p, parts, part, stream);
+        case 80: return launch_d<80, true>(a.f, &a, p, parts, part, stream);
+        case 96: return launch_d<96, true>(a.f, &a, p, parts, part, stream);
+        case 128: return launch_d<128, true>(a.f, &a, p, parts, part, stream);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -27,15 +27,52 @@ struct WinLong : CrossLong {
     int window, sinks;            // window 0: everything before a query
 };
 
+// Shared prefixes: the sequences [cu_g[g], cu_g[g+1]) (all of them without cu_g) see the rows [cu_p[g], cu_p[g+1]) of
+// the prefix tensors.
+struct Groups {
+    const int32_t *cu_g, *cu_p;
+    int64_t Tp;
+    int G, max_p, B;
+
+    __device__ int bound(int g) const { return cu_g ? cu_g[g] : g == 0 ? 0 : B; }
+    // the prefix of group g: false where its rows are not in the tensor, or more than the bound
+    __device__ bool load(int g, int &f0, int &fn) const
+    {
+        const int64_t a = cu_p[g], b = cu_p[g + 1];
+        f0 = (int)a;
+        fn = (int)(b - a);
+        return a >= 0 && b >= a && b <= Tp && b - a <= max_p;
+    }
+    // group g's error: the groups follow one another and hold every sequence, their prefixes lie in the tensor
+    __device__ int error(int g) const
+    {
+        const int a = bound(g), b = bound(g + 1);
+        if (a < 0 || b < a || b > B || (g == 0 && a != 0) || (g == G - 1 && b != B)) return VIT_ERR_BAD_SEQLENS;
+        int f0, fn;
+        if (load(g, f0, fn)) return 0;
+        return cu_p[g] < 0 || cu_p[g + 1] < cu_p[g] || cu_p[g + 1] > Tp ? VIT_ERR_BAD_SEQLENS
+                                                                        : VIT_ERR_SEQLEN_EXCEEDS_MAX;
+    }
+    // the group of sequence b: the last one that begins at or before it
+    __device__ int of(int b) const
+    {
+        int lo = 0, hi = G;
+        while (hi - lo > 1) {
+            const int m = (lo + hi) >> 1;
+            if (bound(m) <= b) lo = m;
+            else hi = m;
+        }
+        return lo;
+    }
+};
+
 struct WinArgs {
     CrossArgs f;                  // the queries are the last ones of their sequence's keys
     int window, sinks;
-    // a shared prefix: the sequences [cu_g[g], cu_g[g+1]) (all of them without cu_g) see the rows [cu_p[g], cu_p[g+1])
     bool prefix;
     const void *kp, *vp;          // bf16 [Tp, Hk, D]
-    int64_t kp_stride, vp_stride, Tp;
-    const int32_t *cu_g, *cu_p;
-    int G, max_p;
+    int64_t kp_stride, vp_stride;
+    Groups groups;
 };
 
 // The place of a sequence's queries among its keys. The first `none` queries lie before its first key (fewer keys than
@@ -70,7 +107,10 @@ __host__ __device__ inline WinRange win_range(int p, int window, int sinks)
 struct WinPlan {
     int lg_pack;
     int units;                    // sequences, or groups and sequences (apart)
-    bool apart;                   // prefix and own keys are separate items, joined by row
+    bool apart;                   // prefix and own keys are separate parts, joined by row
+    bool own_few;                 // apart, and the own keys' parts are made by the kernel for few query rows
+    FewPlan few;
+    size_t off_few;
     int run_tiles;                // key tiles of an item at most (0: keys are not cut)
     int runs;                     // runs of a block at most
     int64_t max_items, max_tiles, slots;
@@ -101,6 +141,10 @@ cudaError_t launch_window_grad(const CrossGradArgs &a, const GradPlan &p, int wi
 // few query rows (cross_few.cu)
 bool window_takes_few(int B, int Hq, int Hk, int D, int max_q, int max_k, int window, int sinks);
 FewPlan window_few_plan(int B, int Hq, int Hk, int D, int max_q, int max_k, int window, int sinks);
-cudaError_t launch_window_few(const WinArgs &a, const FewPlan &p, cudaStream_t stream);
+// `parts`: leave every run's partial result at `part` for another kernel to join
+cudaError_t launch_window_few(const WinArgs &a, const FewPlan &p, bool parts, void *part, cudaStream_t stream);
+// a prefix read by each of its sequences anew
+bool prefix_takes_few(int B, int Hq, int Hk, int D, int max_q, int max_k, int max_p);
+FewPlan prefix_few_plan(int B, int Hq, int Hk, int D, int max_q, int max_k, int max_p);
 
 }  // namespace vit

@@ -34,10 +34,8 @@ struct UnitSlots {
 struct Sched {
     CrossSegs s;
     int window, sinks;
-    const int32_t *cu_g, *cu_p;
-    int64_t Tp;
-    int G, max_p;
-    bool prefix, apart;
+    Groups groups;
+    bool prefix, apart, own_few;
     int Hq, lg_pack, bn, run_tiles, num_sms;
     WsHeader *hdr;
     WinItem *items;
@@ -48,48 +46,14 @@ struct Sched {
     int32_t *status;
 };
 
-__device__ __forceinline__ int group_bound(const Sched &p, int g) { return p.cu_g ? p.cu_g[g] : g == 0 ? 0 : p.s.B; }
-
-// The group's prefix: false where its rows are not in the tensor, or more than the bound.
-__device__ __forceinline__ bool load_prefix(const Sched &p, int g, int &f0, int &fn)
-{
-    const int64_t a = p.cu_p[g], b = p.cu_p[g + 1];
-    f0 = (int)a;
-    fn = (int)(b - a);
-    return a >= 0 && b >= a && b <= p.Tp && b - a <= p.max_p;
-}
-
-// Group g's error: the groups follow one another and hold every sequence, their prefixes lie in the tensor.
-__device__ __forceinline__ int group_error(const Sched &p, int g)
-{
-    const int a = group_bound(p, g), b = group_bound(p, g + 1);
-    if (b < a || (g == 0 && a != 0) || (g == p.G - 1 && b != p.s.B)) return VIT_ERR_BAD_SEQLENS;
-    int f0, fn;
-    if (load_prefix(p, g, f0, fn)) return 0;
-    return p.cu_p[g] < 0 || p.cu_p[g + 1] < p.cu_p[g] || p.cu_p[g + 1] > p.Tp ? VIT_ERR_BAD_SEQLENS
-                                                                             : VIT_ERR_SEQLEN_EXCEEDS_MAX;
-}
-
-// the group of sequence b: the last g with group_bound(g) <= b that has sequences
-__device__ __forceinline__ int group_of(const Sched &p, int b)
-{
-    int lo = 0, hi = p.G;
-    while (hi - lo > 1) {
-        const int m = (lo + hi) >> 1;
-        if (group_bound(p, m) <= b) lo = m;
-        else hi = m;
-    }
-    return lo;
-}
-
 // Unit u, and whether it can be used; `none` counts a sequence's queries that see nothing at all (its first rows).
 __device__ __forceinline__ bool load_unit(const Sched &p, int u, Unit &x, CrossEmpty &none, bool report)
 {
     none = CrossEmpty{0, 0};
     x = Unit{0, 0, 0, 0, 0, 0, 0};
-    if (p.apart && u < p.G) {
-        const int a = group_bound(p, u), b = group_bound(p, u + 1);
-        const bool fine = load_prefix(p, u, x.f0, x.fn);
+    if (p.apart && u < p.groups.G) {
+        const int a = p.groups.bound(u), b = p.groups.bound(u + 1);
+        const bool fine = p.groups.load(u, x.f0, x.fn);
         if (a < 0 || b < a || b > p.s.B) return false; // (reported with the groups)
         const int64_t q0 = p.s.cu_q[a], q1 = p.s.cu_q[b];
         if (!fine || q0 < 0 || q1 < q0 || q1 > p.s.Tq) return false;     // (the sequences report their offsets)
@@ -97,11 +61,11 @@ __device__ __forceinline__ bool load_unit(const Sched &p, int u, Unit &x, CrossE
         x.qn = (int)(q1 - q0);
         return true;
     }
-    const int b = p.apart ? u - p.G : u;
+    const int b = p.apart ? u - p.groups.G : u;
     CrossSeg c;
     if (!load_seg(p.s, b, c, p.status, report)) return false;
     if (p.prefix && !p.apart) {
-        if (!load_prefix(p, group_of(p, b), x.f0, x.fn)) return false;
+        if (!p.groups.load(p.groups.of(b), x.f0, x.fn)) return false;
     }
     const WinSeg w = win_seg(c);
     x.k0 = w.k0;
@@ -148,7 +112,7 @@ window_schedule_kernel(const Sched p)
     __shared__ int s_bad, s_used, s_total, s_tiles, s_all_split, s_more, s_empty;
     grid_wait();
     grid_release();
-    const int tid = threadIdx.x, n_units = p.apart ? p.G + p.s.B : p.s.B;
+    const int tid = threadIdx.x, n_units = p.own_few ? p.groups.G : p.apart ? p.groups.G + p.s.B : p.s.B;
     int NP = 32;
     while (NP < n_units) NP <<= 1;
     int *s_tile = reinterpret_cast<int *>(s_key + NP); // [NP] first tile
@@ -164,13 +128,13 @@ window_schedule_kernel(const Sched p)
     // two-tile blocks of the batch: few of them means split items throughout
     auto split_all = [&](int64_t full) { return p.run_tiles > 0 || p.apart || 2 * full <= (int64_t)p.num_sms; };
     auto unfit = [&](int u, bool fine) {               // nothing is computed at all then
-        const int b = p.apart ? u - p.G : u;
+        const int b = p.apart ? u - p.groups.G : u;
         return (p.prefix && !fine) || (b >= 0 && p.s.cu_q[b + 1] < p.s.cu_q[b]);
     };
     bool wrong = false;                                // of a prefix call: then nothing is computed at all
     if (p.prefix) {
-        for (int g = tid; g < p.G; g += kThreads) {
-            const int err = group_error(p, g);
+        for (int g = tid; g < p.groups.G; g += kThreads) {
+            const int err = p.groups.error(g);
             if (err) report_error(p.status, err);
             wrong |= err != 0;
         }
@@ -335,26 +299,36 @@ window_schedule_kernel(const Sched p)
     }
 }
 
+// How the own keys' parts of the kernel for few query rows lie (cross_few.cu).
+struct FewParts {
+    const float *o, *s;           // [B][Hk][n_split][rows][D] and [..][rows]
+    int Hk, group, n_split, rows, chunk;
+};
+
 // A row of sequence b: its parts over the prefix and over its own keys, one warp per row,
 //   out = sum_s 2^(e_s - E) O_s / sum_s 2^(e_s - E), e_s the log2 of part s's sum.
-template <int D>
+// FEW: the own parts are those of the kernel for few query rows.
+template <int D, bool FEW>
 __global__ void __launch_bounds__(256)
-window_join_kernel(const Sched p, const float *part_o, __nv_bfloat16 *out, int64_t out_stride, float *lse)
+window_join_kernel(const Sched p, const float *part_o, const FewParts few, __nv_bfloat16 *out, int64_t out_stride,
+                   float *lse)
 {
     grid_wait();
     if (p.hdr->error != 0) return;
     const int lane = threadIdx.x & 31, b = blockIdx.y;
     CrossSeg c;
     if (!load_seg(p.s, b, c, nullptr, false)) return;
-    const int g = group_of(p, b), packs = p.Hq >> p.lg_pack, lg_tile = 7 - p.lg_pack, mask = (1 << lg_tile) - 1;
+    const int g = p.groups.of(b), packs = p.Hq >> p.lg_pack, lg_tile = 7 - p.lg_pack, mask = (1 << lg_tile) - 1;
     const WinSeg w = win_seg(c);
     // a unit without keys has no slots
     UnitSlots own{0, 0, 0, 0}, pre{0, 0, 0, 0};
-    if (w.kn > 0) own = p.units[p.G + b];
-    if (p.cu_p[g + 1] > p.cu_p[g]) pre = p.units[g];
-    const int before = c.q0 - p.s.cu_q[group_bound(p, g)];     // rows of the group's sequences before this one
+    if (FEW) own.runs = key_runs(w.kn, few.chunk);
+    else if (w.kn > 0) own = p.units[p.groups.G + b];
+    if (p.groups.cu_p[g + 1] > p.groups.cu_p[g]) pre = p.units[g];
+    const int before = c.q0 - p.s.cu_q[p.groups.bound(g)];     // rows of the group's sequences before this one
     for (int64_t x = blockIdx.x * 8 + (threadIdx.x >> 5); x < (int64_t)c.qn * p.Hq; x += 8 * gridDim.x) {
-        const int tok = (int)(x / p.Hq), head = (int)(x - (int64_t)tok * p.Hq);
+        const int tok = (int)((uint64_t)x < 0xffffffffu ? (uint32_t)x / (uint32_t)p.Hq : x / p.Hq);
+        const int head = (int)(x - (int64_t)tok * p.Hq);
         const int pack = head >> p.lg_pack, in_pack = head & ((1 << p.lg_pack) - 1);
         // the first part's row of a unit's token t
         auto first = [&](const UnitSlots &u, int t) -> int64_t {
@@ -362,24 +336,32 @@ window_join_kernel(const Sched p, const float *part_o, __nv_bfloat16 *out, int64
             return slot * 128 + ((t & mask) << p.lg_pack) + in_pack;
         };
         const int own_runs = tok < w.none ? 0 : own.runs;      // the first queries may lie before the first own key
-        const int64_t own_row = first(own, tok - w.none), pre_row = first(pre, before + tok);
-        auto row = [&](int s) -> int64_t {
-            return s < pre.runs ? pre_row + (int64_t)s * 128 : own_row + (int64_t)(s - pre.runs) * 128;
-        };
+        const int64_t pre_row = first(pre, before + tok);
+        int64_t own_row;
+        if (FEW) {
+            const int hk = head / few.group;
+            own_row = ((int64_t)b * few.Hk + hk) * few.n_split * few.rows + (tok - w.none) * few.group + head - hk * few.group;
+        } else {
+            own_row = first(own, tok - w.none);
+        }
         const int runs = pre.runs + own_runs;
+        auto is_own = [&](int s) { return s >= pre.runs; };
+        auto row = [&](int s) -> int64_t {
+            return is_own(s) ? own_row + (int64_t)(s - pre.runs) * (FEW ? few.rows : 128) : pre_row + (int64_t)s * 128;
+        };
+        auto weight = [&](int s) { return (FEW && is_own(s) ? few.s : p.part_s)[row(s)]; };
         float E = -INFINITY;
-        for (int s = lane; s < runs; s += 32) E = fmaxf(E, p.part_s[row(s)]);
+        for (int s = lane; s < runs; s += 32) E = fmaxf(E, weight(s));
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) E = fmaxf(E, __shfl_xor_sync(0xffffffffu, E, d));
         const float base = E == -INFINITY ? 0.f : E;
         float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
         for (int s = 0; s < runs; ++s) {
-            const int64_t r = row(s);
-            const float y = wmma16::ex2(p.part_s[r] - base);
+            const float y = wmma16::ex2(weight(s) - base);
             sum += y;
             if (lane < D / 4 && y != 0.f) {            // (a part without weight was not written)
-                const float4 v = *reinterpret_cast<const float4 *>(part_o + r * D + 4 * lane);
+                const float4 v = *reinterpret_cast<const float4 *>((FEW && is_own(s) ? few.o : part_o) + row(s) * D + 4 * lane);
                 acc[0] = fmaf(y, v.x, acc[0]);
                 acc[1] = fmaf(y, v.y, acc[1]);
                 acc[2] = fmaf(y, v.z, acc[2]);
@@ -412,7 +394,8 @@ WinPlan win_plan(int64_t Tq, int B, int Hq, int Hk, int D, int max_q, int max_k,
     // Apart where the sequences' tiles would be much emptier than the groups': otherwise a pass over both saves the
     // partial results and their join.
     p.apart = prefix && own > 2 * grouped;
-    p.units = p.apart ? G + B : B;
+    p.own_few = p.apart && window_takes_few(B, Hq, Hk, D, max_q, max_k, 0, 0);
+    p.units = p.own_few ? G : p.apart ? G + B : B;
     // key tiles of a block at most
     const int64_t own_keys = window > 0 ? std::min<int64_t>(max_k, (int64_t)window + 2 * tok - 1) : max_k;
     const int64_t first = prefix ? max_p : window > 0 ? std::min(sinks, max_k) : 0;
@@ -425,12 +408,13 @@ WinPlan win_plan(int64_t Tq, int B, int Hq, int Hk, int D, int max_q, int max_k,
     // re-reads 128 * D fp32 values)
     const int64_t least = 2 * cdiv(512, 2 * bn);
     if (p.apart) {
-        const int64_t work = (own * own_most + grouped * first_most) * packs;
+        const int64_t mine = p.own_few ? 0 : own;      // tiles of the list beside the groups'
+        const int64_t work = (mine * own_most + grouped * first_most) * packs;
         const int64_t run = std::max(least, cdiv(work, 4 * kDesignSms));
-        const int64_t r1 = cdiv(first_most, run), r2 = cdiv(own_most, run);
+        const int64_t r1 = cdiv(first_most, run), r2 = p.own_few ? 0 : cdiv(own_most, run);
         p.run_tiles = (int)run;
         p.runs = (int)std::max<int64_t>(1, std::max(r1, r2));
-        p.max_items = (grouped * std::max<int64_t>(1, r1) + own * std::max<int64_t>(1, r2)) * packs;
+        p.max_items = (grouped * std::max<int64_t>(1, r1) + mine * std::max<int64_t>(1, r2)) * packs;
         p.slots = p.max_items;
     } else {
         const int64_t most = own_most + first_most;
@@ -453,7 +437,13 @@ WinPlan win_plan(int64_t Tq, int B, int Hq, int Hk, int D, int max_q, int max_k,
     p.off_units = up(p.off_empty + sizeof(CrossEmpty) * (size_t)B);
     p.off_part_s = up(p.off_units + (p.apart ? sizeof(UnitSlots) * (size_t)p.units : 0));
     p.off_part_o = up(p.off_part_s + (size_t)p.slots * 128 * sizeof(float));
-    p.bytes = p.off_part_o + (size_t)p.slots * 128 * (size_t)D * sizeof(float);
+    p.off_few = up(p.off_part_o + (size_t)p.slots * 128 * (size_t)D * sizeof(float));
+    p.few = FewPlan{};
+    p.bytes = p.off_few;
+    if (p.own_few) {
+        p.few = window_few_plan(B, Hq, Hk, D, max_q, max_k, 0, 0);
+        p.bytes += sizeof(float) * (size_t)B * Hk * p.few.n_split * p.few.rows * (D + 1);
+    }
     return p;
 }
 
@@ -464,13 +454,10 @@ cudaError_t launch_window_tiles(const WinArgs &a, const WinPlan &pl, int num_sms
     p.s = a.f.segs;
     p.window = a.window;
     p.sinks = a.sinks;
-    p.cu_g = a.cu_g;
-    p.cu_p = a.cu_p;
-    p.Tp = a.Tp;
-    p.G = a.G;
-    p.max_p = a.max_p;
+    p.groups = a.groups;
     p.prefix = a.prefix;
     p.apart = pl.apart;
+    p.own_few = pl.own_few;
     p.Hq = a.f.Hq;
     p.lg_pack = pl.lg_pack;
     p.bn = attn_long_bn(a.f.D);
@@ -508,20 +495,36 @@ cudaError_t launch_window_tiles(const WinArgs &a, const WinPlan &pl, int num_sms
     e = launch_window_long(a, cx, p.hdr, p.items, pl.max_items, num_sms, stream);
     if (e != cudaSuccess) return e;
     if (pl.apart) {
+        FewParts few{};
+        if (pl.own_few) {
+            e = launch_window_few(a, pl.few, true, ws + pl.off_few, stream);
+            if (e != cudaSuccess) return e;
+            few.Hk = a.f.Hk;
+            few.group = a.f.Hq / a.f.Hk;
+            few.n_split = pl.few.n_split;
+            few.rows = pl.few.rows;
+            few.chunk = pl.few.chunk;
+            few.o = reinterpret_cast<const float *>(ws + pl.off_few);
+            few.s = few.o + (size_t)a.f.segs.B * a.f.Hk * pl.few.n_split * pl.few.rows * a.f.D;
+        }
         LaunchScope scope("window_join", stream);
-        // a loose bound of the lengths starts no more blocks than fill the GPU a few times over
-        const int64_t most = cdiv((int64_t)a.f.segs.max_q * a.f.Hq, 8), enough = cdiv(64 * kDesignSms, a.f.segs.B);
+        // a warp per row; more blocks than fill the GPU once only cost their starts
+        const int64_t most = cdiv((int64_t)a.f.segs.max_q * a.f.Hq, 8), enough = cdiv(6 * kDesignSms, a.f.segs.B);
         const dim3 grid((unsigned)std::min(most, enough), (unsigned)a.f.segs.B);
         auto run = [&](auto kern) {
-            return launch_chained(kern, grid, 256, 0, stream, p, cx.part_o, static_cast<__nv_bfloat16 *>(a.f.out),
+            return launch_chained(kern, grid, 256, 0, stream, p, cx.part_o, few, static_cast<__nv_bfloat16 *>(a.f.out),
                                   a.f.out_stride, a.f.lse);
         };
+        auto pick = [&](auto d) {
+            constexpr int D = decltype(d)::value;
+            return pl.own_few ? run(window_join_kernel<D, true>) : run(window_join_kernel<D, false>);
+        };
         switch (a.f.D) {
-            case 32: return run(window_join_kernel<32>);
-            case 64: return run(window_join_kernel<64>);
-            case 80: return run(window_join_kernel<80>);
-            case 96: return run(window_join_kernel<96>);
-            default: return run(window_join_kernel<128>);
+            case 32: return pick(std::integral_constant<int, 32>());
+            case 64: return pick(std::integral_constant<int, 64>());
+            case 80: return pick(std::integral_constant<int, 80>());
+            case 96: return pick(std::integral_constant<int, 96>());
+            default: return pick(std::integral_constant<int, 128>());
         }
     }
     if (pl.runs > 1) {
