@@ -39,7 +39,7 @@ def plan(Tq, B, Hq, Hk, D, max_q, max_k, window, sinks, G, Tp, max_p):
     least = 2 * cdiv(512, 2 * bn)
     if apart:
         own = 0 if own_few else own
-        p["run"] = run = max(least, cdiv((own * own_most + grouped * first_most) * packs, 4 * SMS))
+        p["run"] = run = max(least, cdiv((own * own_most + grouped * first_most) * packs, 8 * SMS))
         p["items"] = p["slots"] = (grouped * max(1, cdiv(first_most, run)) + own * max(1, cdiv(own_most, run))) * packs
     else:
         tiles, most = own * packs, own_most + first_most
@@ -58,6 +58,8 @@ def plan(Tq, B, Hq, Hk, D, max_q, max_k, window, sinks, G, Tp, max_p):
 def few_bytes(B, Hq, Hk, D, max_q, max_k):
     """Partial results of the kernel for few rows, also where it makes one run."""
     rows, pairs = max_q * (Hq // Hk), B * Hk
+    if pairs >= SMS and max_k <= 2048:
+        return 4 * pairs * rows * (D + 1)
     n = max(1, min((8 * SMS + pairs // 2) // pairs, cdiv(max_k, max(16 * rows, 128))))
     chunk = max(64, cdiv(cdiv(max_k, n), 64) * 64)
     return 4 * pairs * (cdiv(max_k, chunk) if max_k else 1) * rows * (D + 1)
@@ -79,9 +81,11 @@ def span(first, last, window, sinks, prefix):
     return n, lo, max(0, last + 1 - lo)
 
 
-def make_list(p, ql, kl, Hq, D, window, sinks, prefixes=None, groups=None, sms=SMS):
-    """Items as (unit, first query, end, head, tiles, prefix or first keys [a, b), own keys [a, b), slot, two tiles)."""
+def make_list(p, ql, kl, Hq, D, window, sinks, prefixes=None, groups=None, sms=SMS, longer=0):
+    """With a prefix apart the list may take `longer` runs than the plan's. Items as (unit, first query, end, head, tiles, prefix or first keys [a, b), own keys [a, b), slot, two tiles)."""
     bn, lg_tile, packs = tile_keys(D), 7 - p["lg"], Hq >> p["lg"]
+    if p["apart"]:
+        p = dict(p, run=p["run"] + longer)
     units, at = [], 0
     start = [sum(ql[:i]) for i in range(len(ql))]
     if p["apart"]:                                     # the groups first
@@ -130,7 +134,7 @@ def make_list(p, ql, kl, Hq, D, window, sinks, prefixes=None, groups=None, sms=S
     return units, listed, len(listed) + extra, slot
 
 
-def check(ql, kl, Hq, Hk, D, window=0, sinks=0, prefixes=None, groups=None, loose=False):
+def check(ql, kl, Hq, Hk, D, window=0, sinks=0, prefixes=None, groups=None, loose=False, longer=0):
     Tq, B = sum(ql), len(ql)
     G, Tp = (len(prefixes), sum(prefixes)) if prefixes else (0, 0)
     max_q, max_k = (Tq, sum(kl)) if loose else (max(ql), max(kl))
@@ -145,7 +149,7 @@ def check(ql, kl, Hq, Hk, D, window=0, sinks=0, prefixes=None, groups=None, loos
         assert vit.prefix_attn_workspace_size(Tq, Tp, sum(kl), Hq, Hk, D, B, G, max_q, max_p, max_k) == p["bytes"]
     elif not few(B, Hq, Hk, D, max_q, max_k, window, sinks):
         assert vit.window_attn_workspace_size(Tq, sum(kl), Hq, Hk, D, B, max_q, max_k, window, sinks) == p["bytes"]
-    units, items, n_items, slots = make_list(p, ql, kl, Hq, D, window, sinks, prefixes if Tp else None, groups)
+    units, items, n_items, slots = make_list(p, ql, kl, Hq, D, window, sinks, prefixes if Tp else None, groups, longer=longer)
     assert n_items <= p["items"]
     assert (slots if p["run"] else 0) <= p["slots"]
     seen = {}
@@ -207,4 +211,4 @@ def test_prefixes():
         if B and sum(ql) and sum(kl):
             check(ql, kl, Hk * rng.choice([1, 2, 4, 8]), Hk, D,
                   prefixes=[rng.choice([0, 1, 100, 1601, 9000]) for _ in range(G)], groups=groups,
-                  loose=rng.random() < 0.3)
+                  loose=rng.random() < 0.3, longer=rng.choice([0, 1, 5, 40, 127]))

@@ -1053,10 +1053,20 @@ long_body(const CUtensorMap &tm_q, const CUtensorMap &tm_qr, const CUtensorMap &
                         x1 = fmaf(__uint_as_float(r1[2 * e + 1]), c1, x1);
                     }
                     o[e] = pack_bf16x2(x0, x1);
-                    if constexpr (X) {
+                    if constexpr (W) {
+                        r0[2 * e] = __float_as_uint(x0);
+                        r0[2 * e + 1] = __float_as_uint(x1);
+                    } else if constexpr (X) {
                         if (part && store)
                             *reinterpret_cast<float2 *>(cx.part_o + ((int64_t)item.slot * BM + row) * D + grp * HALF + c +
                                                         2 * e) = make_float2(x0, x1);
+                    }
+                }
+                if constexpr (W) {
+                    if (part && store) {
+                        uint4 *d4 = reinterpret_cast<uint4 *>(cx.part_o + ((int64_t)item.slot * BM + row) * D + grp * HALF + c);
+                        d4[0] = make_uint4(r0[0], r0[1], r0[2], r0[3]);
+                        d4[1] = make_uint4(r0[4], r0[5], r0[6], r0[7]);
                     }
                 }
                 if (store && !part) *reinterpret_cast<uint4 *>(dst + c) = make_uint4(o[0], o[1], o[2], o[3]);

@@ -20,6 +20,7 @@ namespace vit {
 namespace {
 
 constexpr int kThreads = kSortThreads;
+constexpr int kSmall = 256;            // units of a list that is made with a unit per thread
 
 // A unit's queries (rows [q0, q0 + qn), positions from p0 on) and its keys: the prefix rows [f0, f0 + fn), and the own
 // keys from row k0 on (kn = 0: none).
@@ -108,8 +109,10 @@ window_schedule_kernel(const Sched p)
 {
     extern __shared__ unsigned long long s_key[];      // [NP]: longest block first, then index; later first item | index
     __shared__ int64_t s_warp[32];
-    __shared__ Unit s_unit[32];                        // of up to 32 units, in their order
-    __shared__ int s_bad, s_used, s_total, s_tiles, s_all_split, s_more, s_empty;
+    __shared__ Unit s_unit[kSmall];                    // of up to kSmall units, in their order
+    __shared__ int s_len[kSmall], s_blocks[kSmall], s_runs[kSmall];
+    __shared__ int s_bad, s_used, s_total, s_tiles, s_all_split, s_more, s_empty, s_run;
+    __shared__ unsigned long long s_best;
     grid_wait();
     grid_release();
     const int tid = threadIdx.x, n_units = p.own_few ? p.groups.G : p.apart ? p.groups.G + p.s.B : p.s.B;
@@ -123,7 +126,8 @@ window_schedule_kernel(const Sched p)
         return ((unsigned long long)(use ? 0x7fffffffu - (uint32_t)longest(x) : 0xffffffffu) << 32) | (uint32_t)i;
     };
     auto blocks_of = [&](const Unit &x, int lg) { return packs * (int)(((unsigned)x.qn + (1u << lg) - 1u) >> lg); };
-    auto runs_of = [&](const Unit &x) { return p.run_tiles > 0 ? max(1, (longest(x) + p.run_tiles - 1) / p.run_tiles) : 1; };
+    auto runs_in = [&](int tiles, int run) { return run > 0 ? max(1, (tiles + run - 1) / run) : 1; };
+    auto runs_of = [&](const Unit &x) { return runs_in(longest(x), p.run_tiles); };
     auto usable = [&](bool fine, const Unit &x) { return fine && x.qn > 0 && (x.fn > 0 || x.kn > 0); };
     // two-tile blocks of the batch: few of them means split items throughout
     auto split_all = [&](int64_t full) { return p.run_tiles > 0 || p.apart || 2 * full <= (int64_t)p.num_sms; };
@@ -140,8 +144,14 @@ window_schedule_kernel(const Sched p)
         }
         wrong = __syncthreads_or(wrong);
     }
-    if (n_units <= 32) {
-        // a warp: one unit per lane
+    if (tid == 0) {
+        s_bad = s_used = s_empty = 0;
+        s_run = p.run_tiles;
+        s_best = ~0ull;
+    }
+    __syncthreads();
+    if (n_units <= 32 && !p.apart) {
+        // a warp: one unit per lane (1.5 us less than a thread each of the block)
         if (tid < 32) {
             Unit x;
             CrossEmpty none{0, 0};
@@ -157,6 +167,7 @@ window_schedule_kernel(const Sched p)
             s_key[rank] = ((unsigned long long)at << 32) | (uint32_t)tid;
             s_tile[rank] = tile_at;
             s_unit[rank] = x;
+            s_runs[rank] = runs;
             const unsigned used = __ballot_sync(0xffffffffu, use), any_bad = __ballot_sync(0xffffffffu, bad);
             const unsigned nones = __ballot_sync(0xffffffffu, fine && none.qn > 0);
             if (fine && none.qn > 0) p.empty[__popc(nones & ((1u << tid) - 1u))] = none;
@@ -170,9 +181,83 @@ window_schedule_kernel(const Sched p)
             }
         }
         __syncthreads();
-    } else {
-        if (tid == 0) s_bad = s_used = s_empty = 0;
+    } else if (n_units <= kSmall) {
+        // a unit per thread; its place is the number of units before it
+        Unit x;
+        CrossEmpty none{0, 0};
+        const bool fine = tid < n_units && load_unit(p, tid, x, none, true), use = usable(fine, x);
+        const int len = use ? longest(x) : 0;
+        const unsigned long long key = ((unsigned long long)(use ? 0x7fffffffu - (uint32_t)len : 0xffffffffu) << 32) | (uint32_t)tid;
+        int64_t total_full, total, total_tiles;
+        block_exclusive_scan(use ? blocks_of(x, lg_tile + 1) : 0, s_warp, &total_full);
+        const bool all_split = split_all(total_full);
+        const int blocks = use ? blocks_of(x, all_split ? lg_tile : lg_tile + 1) : 0;
+        if (tid < n_units) {
+            s_key[tid] = key;
+            s_len[tid] = len;
+            s_blocks[tid] = blocks;
+            if (unfit(tid, fine)) s_bad = 1;
+            if (use) atomicAdd(&s_used, 1);
+            if (fine && none.qn > 0) p.empty[atomicAdd(&s_empty, 1)] = none;   // (in any order)
+        }
         __syncthreads();
+        if (p.apart) {
+            // How long runs are best: an item takes a step for each two of its tiles, and about kItemSteps beside them. Of
+            // units alike (the groups alone) as many rounds as it takes, else an even share and one item more.
+            constexpr float kItemSteps = 2.5f;
+            unsigned long long best = ~0ull;
+            const int run = p.run_tiles + tid;
+            if (tid < 128) {
+                const float inv = 1.f / (float)run;
+                float items = 0.f, steps = 0.f, most = 0.f;
+                for (int u = 0; u < n_units; ++u) {
+                    const float t = (float)s_len[u], n = fmaxf(1.f, floorf((t + run - 0.5f) * inv)), b = (float)s_blocks[u];
+                    items += b * n;
+                    steps += b * t * 0.5f;
+                    if (b > 0.f) most = fmaxf(most, t / n);
+                }
+                const float share = p.own_few ? ceilf(items / p.num_sms) * (most * 0.5f + kItemSteps)
+                                              : (steps + kItemSteps * items) / p.num_sms + most * 0.5f + kItemSteps;
+                best = ((unsigned long long)__float_as_uint(share) << 32) | (uint32_t)tid;
+            }
+            if (tid < 128) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    const unsigned long long y = __shfl_xor_sync(0xffffffffu, best, o);
+                    best = y < best ? y : best;
+                }
+                if ((tid & 31) == 0) atomicMin(&s_best, best);
+            }
+            __syncthreads();
+            if (tid == 0) s_run = p.run_tiles + (int)(uint32_t)s_best;
+            __syncthreads();
+        }
+        const int runs = use ? runs_in(len, s_run) : 1;
+        int rank = 0;
+        if (tid < n_units)
+            for (int u = 0; u < n_units; ++u) rank += s_key[u] < key;
+        __syncthreads();
+        if (tid < n_units) {
+            s_unit[rank] = x;
+            s_runs[rank] = runs;
+            s_blocks[rank] = blocks;
+            s_key[rank] = (uint32_t)tid;
+        }
+        __syncthreads();
+        const int n = tid < n_units ? s_blocks[tid] : 0, r = tid < n_units ? s_runs[tid] : 1;
+        const int64_t at = block_exclusive_scan((int64_t)n * r, s_warp, &total);
+        const int64_t tile_at = block_exclusive_scan(r > 1 ? n : 0, s_warp, &total_tiles);
+        if (tid < n_units) {
+            s_key[tid] |= (unsigned long long)at << 32;
+            s_tile[tid] = (int)tile_at;
+        }
+        if (tid == 0) {
+            s_total = (int)total;
+            s_tiles = (int)total_tiles;
+            s_all_split = all_split;
+        }
+        __syncthreads();
+    } else {
         for (int i = tid; i < NP; i += kThreads) {
             Unit x;
             CrossEmpty none{0, 0};
@@ -223,8 +308,8 @@ window_schedule_kernel(const Sched p)
     const bool bad = wrong || s_bad != 0, all_split = s_all_split != 0;
     const int total = bad ? 0 : s_total, lg_block = all_split ? lg_tile : lg_tile + 1;
     // where the items end in a wave that fills at most half the SMs, its items are cut into their tiles
-    const int rest = total % p.num_sms;
-    const int whole = p.run_tiles > 0 ? 0 : !all_split && 2 * rest <= p.num_sms ? total - rest : total;
+    const int rest = total % p.num_sms, run_tiles = s_run;
+    const int whole = run_tiles > 0 ? 0 : !all_split && 2 * rest <= p.num_sms ? total - rest : total;
     if (tid == 0) s_more = 0;
     __syncthreads();
     for (int i = tid; i < total; i += kThreads) {
@@ -232,15 +317,16 @@ window_schedule_kernel(const Sched p)
         const int unit = (int)(s_key[at_unit] & 0xffffffffu);
         Unit x;
         CrossEmpty none;
-        if (n_units <= 32) x = s_unit[at_unit];
+        if (n_units <= kSmall) x = s_unit[at_unit];
         else load_unit(p, unit, x, none, false);
-        const int nq = (int)(((unsigned)x.qn + (1u << lg_block) - 1u) >> lg_block), runs = runs_of(x);
+        const int nq = (int)(((unsigned)x.qn + (1u << lg_block) - 1u) >> lg_block);
+        const int runs = n_units <= kSmall ? s_runs[at_unit] : runs_of(x);
         const int j = runs > 1 ? n / runs : n, run = n - j * runs, back = j / packs, qb = nq - 1 - back;
         const int h = j - back * packs;
         const int t = qb << lg_block, e = min(x.qn, t + (1 << lg_block));
         const Span s = span_of(p, x, t, e);
         // the block's tiles, dealt evenly to as many runs as they fill
-        const int tiles = runs > 1 ? s.tiles(p.bn) : 0, use = runs > 1 ? max(1, (tiles + p.run_tiles - 1) / p.run_tiles) : 1;
+        const int tiles = runs > 1 ? s.tiles(p.bn) : 0, use = runs > 1 ? runs_in(tiles, run_tiles) : 1;
         if (p.apart && n == 0) p.units[unit] = UnitSlots{x.q0, nq, runs, i};
         if (run >= use) {
             if (p.apart)
@@ -305,20 +391,23 @@ struct FewParts {
     int Hk, group, n_split, rows, chunk;
 };
 
-// A row of sequence b: its parts over the prefix and over its own keys, one warp per row,
-//   out = sum_s 2^(e_s - E) O_s / sum_s 2^(e_s - E), e_s the log2 of part s's sum.
-// FEW: the own parts are those of the kernel for few query rows.
+// A row of sequence b: its parts over the prefix and over its own keys,
+//   out = sum_s 2^(e_s - E) O_s / sum_s 2^(e_s - E), e_s the log2 of part s's sum,
+// D / 8 lanes per row, 32 bytes of every part a lane. FEW: the own parts are those of the kernel for few query rows.
+// Bound by latency: the offsets, then a row's weights, then its parts (1348 tokens of 16 heads of 80 in four parts, of
+// 27 MB in L2: 32 us with a warp per row, 14 us so).
 template <int D, bool FEW>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 3)
 window_join_kernel(const Sched p, const float *part_o, const FewParts few, __nv_bfloat16 *out, int64_t out_stride,
                    float *lse)
 {
     grid_wait();
-    if (p.hdr->error != 0) return;
-    const int lane = threadIdx.x & 31, b = blockIdx.y;
+    constexpr int CH = D / 8, R = 32 / CH;             // lanes of a row, rows of a warp
+    const int lane = threadIdx.x & 31, b = blockIdx.y, sub = lane / CH, c8 = lane % CH * 8;
+    const int error = p.hdr->error, g = p.groups.of(b);
     CrossSeg c;
-    if (!load_seg(p.s, b, c, nullptr, false)) return;
-    const int g = p.groups.of(b), packs = p.Hq >> p.lg_pack, lg_tile = 7 - p.lg_pack, mask = (1 << lg_tile) - 1;
+    if (!load_seg(p.s, b, c, nullptr, false) || error != 0) return;
+    const int packs = p.Hq >> p.lg_pack, lg_tile = 7 - p.lg_pack, mask = (1 << lg_tile) - 1;
     const WinSeg w = win_seg(c);
     // a unit without keys has no slots
     UnitSlots own{0, 0, 0, 0}, pre{0, 0, 0, 0};
@@ -326,8 +415,11 @@ window_join_kernel(const Sched p, const float *part_o, const FewParts few, __nv_
     else if (w.kn > 0) own = p.units[p.groups.G + b];
     if (p.groups.cu_p[g + 1] > p.groups.cu_p[g]) pre = p.units[g];
     const int before = c.q0 - p.s.cu_q[p.groups.bound(g)];     // rows of the group's sequences before this one
-    for (int64_t x = blockIdx.x * 8 + (threadIdx.x >> 5); x < (int64_t)c.qn * p.Hq; x += 8 * gridDim.x) {
-        const int tok = (int)((uint64_t)x < 0xffffffffu ? (uint32_t)x / (uint32_t)p.Hq : x / p.Hq);
+    const int64_t n_rows = (int64_t)c.qn * p.Hq;
+    for (int64_t x0 = (int64_t)(blockIdx.x * 8 + (threadIdx.x >> 5)) * R; x0 < n_rows; x0 += (int64_t)8 * R * gridDim.x) {
+        const int64_t x = x0 + sub;
+        if (sub >= R || x >= n_rows) continue;
+        const int tok = (int)(n_rows <= 0x7fffffff ? (uint32_t)x / (uint32_t)p.Hq : x / p.Hq);
         const int head = (int)(x - (int64_t)tok * p.Hq);
         const int pack = head >> p.lg_pack, in_pack = head & ((1 << p.lg_pack) - 1);
         // the first part's row of a unit's token t
@@ -335,45 +427,49 @@ window_join_kernel(const Sched p, const float *part_o, const FewParts few, __nv_
             const int64_t slot = u.slot + (int64_t)((u.blocks - 1 - (t >> lg_tile)) * packs + pack) * u.runs;
             return slot * 128 + ((t & mask) << p.lg_pack) + in_pack;
         };
-        const int own_runs = tok < w.none ? 0 : own.runs;      // the first queries may lie before the first own key
-        const int64_t pre_row = first(pre, before + tok);
-        int64_t own_row;
+        const int own_t = tok - w.none, own_runs = own_t < 0 ? 0 : own.runs;   // (the first may lie before the own keys)
+        const float *ps = p.part_s + first(pre, before + tok), *po = part_o + first(pre, before + tok) * D + c8;
+        const float *os, *oo;
+        int step = 128;                                // rows between two runs' parts of a row
         if (FEW) {
             const int hk = head / few.group;
-            own_row = ((int64_t)b * few.Hk + hk) * few.n_split * few.rows + (tok - w.none) * few.group + head - hk * few.group;
+            const int64_t row = ((int64_t)b * few.Hk + hk) * few.n_split * few.rows + own_t * few.group + head - hk * few.group;
+            os = few.s + row;
+            oo = few.o + row * D + c8;
+            step = few.rows;
         } else {
-            own_row = first(own, tok - w.none);
+            os = p.part_s + first(own, own_t);
+            oo = part_o + first(own, own_t) * D + c8;
         }
-        const int runs = pre.runs + own_runs;
-        auto is_own = [&](int s) { return s >= pre.runs; };
-        auto row = [&](int s) -> int64_t {
-            return is_own(s) ? own_row + (int64_t)(s - pre.runs) * (FEW ? few.rows : 128) : pre_row + (int64_t)s * 128;
-        };
-        auto weight = [&](int s) { return (FEW && is_own(s) ? few.s : p.part_s)[row(s)]; };
-        float E = -INFINITY;
-        for (int s = lane; s < runs; s += 32) E = fmaxf(E, weight(s));
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) E = fmaxf(E, __shfl_xor_sync(0xffffffffu, E, d));
-        const float base = E == -INFINITY ? 0.f : E;
-        float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+        float E = -INFINITY, sum = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-        for (int s = 0; s < runs; ++s) {
-            const float y = wmma16::ex2(weight(s) - base);
+        for (int s = 0; s < pre.runs; ++s) E = fmaxf(E, ps[s * 128]);
+#pragma unroll 2
+        for (int s = 0; s < own_runs; ++s) E = fmaxf(E, os[s * step]);
+        const float base = E == -INFINITY ? 0.f : E;
+        auto add = [&](float e, const float *o) {
+            const float y = wmma16::ex2(e - base);
             sum += y;
-            if (lane < D / 4 && y != 0.f) {            // (a part without weight was not written)
-                const float4 v = *reinterpret_cast<const float4 *>((FEW && is_own(s) ? few.o : part_o) + row(s) * D + 4 * lane);
-                acc[0] = fmaf(y, v.x, acc[0]);
-                acc[1] = fmaf(y, v.y, acc[1]);
-                acc[2] = fmaf(y, v.z, acc[2]);
-                acc[3] = fmaf(y, v.w, acc[3]);
-            }
-        }
-        const float inv = runs > 0 ? 1.f / sum : 0.f;  // keys, but no weight: 0 * inf; no keys: 0
+            if (y == 0.f) return;                      // (a part without weight was not written)
+            const float4 u = *reinterpret_cast<const float4 *>(o), v = *reinterpret_cast<const float4 *>(o + 4);
+            acc[0] = fmaf(y, u.x, acc[0]);
+            acc[1] = fmaf(y, u.y, acc[1]);
+            acc[2] = fmaf(y, u.z, acc[2]);
+            acc[3] = fmaf(y, u.w, acc[3]);
+            acc[4] = fmaf(y, v.x, acc[4]);
+            acc[5] = fmaf(y, v.y, acc[5]);
+            acc[6] = fmaf(y, v.z, acc[6]);
+            acc[7] = fmaf(y, v.w, acc[7]);
+        };
+#pragma unroll 2
+        for (int s = 0; s < pre.runs; ++s) add(ps[s * 128], po + (int64_t)s * 128 * D);
+        for (int s = 0; s < own_runs; ++s) add(os[s * step], oo + (int64_t)s * step * D);
+        const float inv = pre.runs + own_runs > 0 ? 1.f / sum : 0.f;   // keys, but no weight: 0 * inf; no keys: 0
         const int64_t t = (int64_t)c.q0 + tok;
-        if (lane < D / 4)
-            *reinterpret_cast<uint2 *>(out + t * out_stride + (int64_t)head * D + 4 * lane) =
-                make_uint2(wmma16::pack_bf16(acc[0] * inv, acc[1] * inv), wmma16::pack_bf16(acc[2] * inv, acc[3] * inv));
-        if (lse && lane == 0) lse[t * p.Hq + head] = (E + log2f(sum)) * 0.6931471805599453f;
+        *reinterpret_cast<uint4 *>(out + t * out_stride + (int64_t)head * D + c8) =
+            make_uint4(wmma16::pack_bf16(acc[0] * inv, acc[1] * inv), wmma16::pack_bf16(acc[2] * inv, acc[3] * inv),
+                       wmma16::pack_bf16(acc[4] * inv, acc[5] * inv), wmma16::pack_bf16(acc[6] * inv, acc[7] * inv));
+        if (lse && c8 == 0) lse[t * p.Hq + head] = (E + log2f(sum)) * 0.6931471805599453f;
     }
 }
 
@@ -410,7 +506,7 @@ WinPlan win_plan(int64_t Tq, int B, int Hq, int Hk, int D, int max_q, int max_k,
     if (p.apart) {
         const int64_t mine = p.own_few ? 0 : own;      // tiles of the list beside the groups'
         const int64_t work = (mine * own_most + grouped * first_most) * packs;
-        const int64_t run = std::max(least, cdiv(work, 4 * kDesignSms));
+        const int64_t run = std::max(least, cdiv(work, 8 * kDesignSms));   // the shortest; the list may choose longer ones
         const int64_t r1 = cdiv(first_most, run), r2 = p.own_few ? 0 : cdiv(own_most, run);
         p.run_tiles = (int)run;
         p.runs = (int)std::max<int64_t>(1, std::max(r1, r2));
@@ -442,6 +538,10 @@ WinPlan win_plan(int64_t Tq, int B, int Hq, int Hk, int D, int max_q, int max_k,
     p.bytes = p.off_few;
     if (p.own_few) {
         p.few = window_few_plan(B, Hq, Hk, D, max_q, max_k, 0, 0);
+        if ((int64_t)B * Hk >= kDesignSms && max_k <= 2048) {   // one run each: enough blocks, and short ones
+            p.few.chunk = (max_k + 63) / 64 * 64;
+            p.few.n_split = 1;
+        }
         p.bytes += sizeof(float) * (size_t)B * Hk * p.few.n_split * p.few.rows * (D + 1);
     }
     return p;
@@ -508,8 +608,9 @@ cudaError_t launch_window_tiles(const WinArgs &a, const WinPlan &pl, int num_sms
             few.s = few.o + (size_t)a.f.segs.B * a.f.Hk * pl.few.n_split * pl.few.rows * a.f.D;
         }
         LaunchScope scope("window_join", stream);
-        // a warp per row; more blocks than fill the GPU once only cost their starts
-        const int64_t most = cdiv((int64_t)a.f.segs.max_q * a.f.Hq, 8), enough = cdiv(6 * kDesignSms, a.f.segs.B);
+        // more blocks than fill the GPU once only cost their starts
+        const int64_t most = cdiv((int64_t)a.f.segs.max_q * a.f.Hq, 8 * (32 / (a.f.D / 8)));
+        const int64_t enough = cdiv(6 * kDesignSms, a.f.segs.B);
         const dim3 grid((unsigned)std::min(most, enough), (unsigned)a.f.segs.B);
         auto run = [&](auto kern) {
             return launch_chained(kern, grid, 256, 0, stream, p, cx.part_o, few, static_cast<__nv_bfloat16 *>(a.f.out),
