@@ -20,7 +20,10 @@ namespace vit {
 namespace {
 
 constexpr int kThreads = kSortThreads;
-constexpr int kSmall = 256;            // units of a list that is made with a unit per thread
+// Three ways to make the list: up to 32 units by a warp, a unit per lane; up to kSmall (and where a prefix is apart) a unit
+// per thread; more sorted by the block. Each is a kernel of its own: all in one, a list of 1864 items took 2 us longer.
+enum { kByWarp, kByThread, kSorted };
+constexpr int kSmall = 256;
 
 // A unit's queries (rows [q0, q0 + qn), positions from p0 on) and its keys: the prefix rows [f0, f0 + fn), and the own
 // keys from row k0 on (kn = 0: none).
@@ -104,13 +107,15 @@ __device__ __forceinline__ Span span_of(const Sched &p, const Unit &u, int t, in
     return s;
 }
 
+template <int MODE>
 __global__ void __launch_bounds__(kThreads)
 window_schedule_kernel(const Sched p)
 {
     extern __shared__ unsigned long long s_key[];      // [NP]: longest block first, then index; later first item | index
     __shared__ int64_t s_warp[32];
-    __shared__ Unit s_unit[kSmall];                    // of up to kSmall units, in their order
-    __shared__ int s_len[kSmall], s_blocks[kSmall], s_runs[kSmall];
+    constexpr int KEPT = MODE == kByWarp ? 32 : MODE == kByThread ? kSmall : 1;
+    __shared__ Unit s_unit[KEPT];                      // units in their order
+    __shared__ int s_runs[KEPT];
     __shared__ int s_bad, s_used, s_total, s_tiles, s_all_split, s_more, s_empty, s_run;
     __shared__ unsigned long long s_best;
     grid_wait();
@@ -144,14 +149,15 @@ window_schedule_kernel(const Sched p)
         }
         wrong = __syncthreads_or(wrong);
     }
-    if (tid == 0) {
-        s_bad = s_used = s_empty = 0;
-        s_run = p.run_tiles;
-        s_best = ~0ull;
+    if constexpr (MODE != kByWarp) {
+        if (tid == 0) {
+            s_bad = s_used = s_empty = 0;
+            s_run = p.run_tiles;
+            s_best = ~0ull;
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    if (n_units <= 32 && !p.apart) {
-        // a warp: one unit per lane (1.5 us less than a thread each of the block)
+    if constexpr (MODE == kByWarp) {
         if (tid < 32) {
             Unit x;
             CrossEmpty none{0, 0};
@@ -178,11 +184,13 @@ window_schedule_kernel(const Sched p)
                 s_empty = __popc(nones);
                 s_all_split = all_split;
                 s_bad = any_bad != 0;
+                s_run = p.run_tiles;
             }
         }
         __syncthreads();
-    } else if (n_units <= kSmall) {
-        // a unit per thread; its place is the number of units before it
+    } else if constexpr (MODE == kByThread) {
+        // a unit's place is the number of units before it
+        __shared__ int s_len[kSmall], s_blocks[kSmall];
         Unit x;
         CrossEmpty none{0, 0};
         const bool fine = tid < n_units && load_unit(p, tid, x, none, true), use = usable(fine, x);
@@ -317,10 +325,10 @@ window_schedule_kernel(const Sched p)
         const int unit = (int)(s_key[at_unit] & 0xffffffffu);
         Unit x;
         CrossEmpty none;
-        if (n_units <= kSmall) x = s_unit[at_unit];
+        if (MODE != kSorted) x = s_unit[at_unit];
         else load_unit(p, unit, x, none, false);
         const int nq = (int)(((unsigned)x.qn + (1u << lg_block) - 1u) >> lg_block);
-        const int runs = n_units <= kSmall ? s_runs[at_unit] : runs_of(x);
+        const int runs = MODE != kSorted ? s_runs[at_unit] : runs_of(x);
         const int j = runs > 1 ? n / runs : n, run = n - j * runs, back = j / packs, qb = nq - 1 - back;
         const int h = j - back * packs;
         const int t = qb << lg_block, e = min(x.qn, t + (1 << lg_block));
@@ -573,15 +581,19 @@ cudaError_t launch_window_tiles(const WinArgs &a, const WinPlan &pl, int num_sms
     int np = 32;
     while (np < pl.units) np <<= 1;
     constexpr size_t each = sizeof(unsigned long long) + sizeof(int);
+    auto sorted = window_schedule_kernel<kSorted>;
     static DeviceOnce once;
-    cudaError_t e = once.run([] {
-        return cudaFuncSetAttribute(window_schedule_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = once.run([&] {
+        return cudaFuncSetAttribute(sorted, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)each * 2 * VIT_MAX_SEGMENTS);
     });
     if (e != cudaSuccess) return e;
     {
         LaunchScope scope("window_schedule", stream);
-        e = launch_chained(window_schedule_kernel, 1, kThreads, each * np, stream, p);
+        auto kern = pl.units <= 32 && !pl.apart ? window_schedule_kernel<kByWarp>
+                    : pl.units <= kSmall        ? window_schedule_kernel<kByThread>
+                                                : sorted;
+        e = launch_chained(kern, 1, kThreads, each * np, stream, p);
         if (e != cudaSuccess) return e;
     }
     WinLong cx{};
