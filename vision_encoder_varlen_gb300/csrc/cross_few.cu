@@ -78,21 +78,14 @@ struct Few {
 struct Keys {
     int f0, sn, head, lo, n, none;
 };
-__device__ __forceinline__ Keys window_keys(const Few &p, int b, const CrossSeg &x, bool report, bool &fine)
+__device__ __forceinline__ Keys window_keys(const Few &p, int b, const CrossSeg &x, int f0, int fn)
 {
     const WinSeg w = win_seg(x);
     Keys k{x.k0, 0, 0, 0, 0, w.none};
-    fine = true;
     if (p.prefix) {
-        const int g = p.groups.of(b);
-        const int err = p.groups.bound(g) > b || p.groups.bound(g + 1) <= b ? VIT_ERR_BAD_SEQLENS : p.groups.error(g);
-        if (err) {
-            if (report) report_error(p.status, err);
-            fine = false;
-            return k;
-        }
-        p.groups.load(g, k.f0, k.sn);
-        if (k.sn > 0) k.none = 0;
+        k.f0 = f0;
+        k.sn = fn;
+        if (fn > 0) k.none = 0;
     } else {
         const WinRange r = win_range(w.p0, p.window, p.sinks);
         k.sn = r.first;
@@ -132,6 +125,14 @@ cross_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = blockIdx.z, hk = blockIdx.x, b = blockIdx.y;   // later runs last: ragged lengths leave them empty
     CrossSeg seg;
+    [[maybe_unused]] int f0 = 0, fn = 0;                      // W: the prefix
+    if constexpr (W) {
+        int g, begin, err;
+        if (p.prefix && !p.groups.find(b, lane, g, begin, f0, fn, err)) {
+            if (threadIdx.x == 0 && split == 0 && hk == 0) report_error(p.status, err);
+            return;
+        }
+    }
     // a sequence without keys is left to the join, or to split 0 where there is none
     if (!load_seg(p.segs, b, seg, p.status, threadIdx.x == 0 && split == 0 && hk == 0)) return;
     if (seg.qn == 0) return;
@@ -140,9 +141,7 @@ cross_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     Keys keys{0, 0, 0, 0, 0, 0};
     int p0 = 0;                                               // position of the first query
     if constexpr (W) {
-        bool fine;
-        keys = window_keys(p, b, seg, threadIdx.x == 0 && split == 0 && hk == 0, fine);
-        if (!fine) return;
+        keys = window_keys(p, b, seg, f0, fn);
         // queries that see nothing: zeros, by the first run's block
         if (split == 0 && !p.parts)
             for (int x = threadIdx.x; x < keys.none * p.group * (D / 8); x += 32 * NW + 32) {
@@ -436,7 +435,7 @@ cross_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 // out = sum_s 2^(e_s - E) O_s / sum_s 2^(e_s - E), e_s the log2 of run s's sum: a row by one warp, or
 // (WIDE, many runs) by the eight warps of a block, each every eighth run, added up in warp order.
 template <int D, bool WIDE, bool W>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, W ? 4 : 0)
 cross_join_kernel(const Few p)
 {
     __shared__ float s_acc[WIDE ? 8 : 1][WIDE ? D : 1], s_sum[8];
@@ -444,12 +443,15 @@ cross_join_kernel(const Few p)
     const int b = blockIdx.y;
     CrossSeg seg;
     grid_wait();                                              // the runs' results
+    [[maybe_unused]] int f0 = 0, fn = 0;
+    if constexpr (W) {
+        int g, begin, err;
+        if (p.prefix && !p.groups.find(b, lane, g, begin, f0, fn, err)) return;
+    }
     if (!load_seg(p.segs, b, seg, nullptr, false)) return;
     int n_keys = seg.kn;
     if constexpr (W) {                                        // (queries that see nothing are written already)
-        bool fine;
-        const Keys keys = window_keys(p, b, seg, false, fine);
-        if (!fine) return;
+        const Keys keys = window_keys(p, b, seg, f0, fn);
         n_keys = keys.n;
         seg.q0 += keys.none;
         seg.qn -= keys.none;
@@ -636,9 +638,23 @@ bool window_takes_few(int B, int Hq, int Hk, int D, int max_q, int max_k, int wi
 {
     return takes_few(B, Hq, Hk, D, max_q, window_most(max_q, max_k, window, sinks));
 }
+// A second round of blocks for less than half the places of the first is not begun (three single tokens behind 1601
+// shared keys: 14 runs of 24 pairs, where 304 blocks fit at head_dim 128).
+static FewPlan one_round(int B, int Hq, int Hk, int D, int max_q, int most)
+{
+    FewPlan p = few_plan(B, Hq, Hk, D, max_q, most);
+    const int64_t pairs = (int64_t)B * Hk, fit = kDesignSms * (227 * 1024 / (kStages * 4 * kTile * D + 2048));
+    if (pairs * p.n_split > fit && 2 * pairs * p.n_split < 3 * fit && pairs <= fit) {
+        const int64_t n = fit / pairs;
+        p.chunk = (int)((((int64_t)most + n - 1) / n + kTile - 1) / kTile * kTile);
+        p.n_split = (int)(((int64_t)most + p.chunk - 1) / p.chunk);
+        p.partial_bytes = p.n_split > 1 ? sizeof(float) * (size_t)pairs * p.n_split * p.rows * (D + 1) : 0;
+    }
+    return p;
+}
 FewPlan window_few_plan(int B, int Hq, int Hk, int D, int max_q, int max_k, int window, int sinks)
 {
-    return few_plan(B, Hq, Hk, D, max_q, window_most(max_q, max_k, window, sinks));
+    return one_round(B, Hq, Hk, D, max_q, window_most(max_q, max_k, window, sinks));
 }
 
 // Behind prefixes: few rows where reading the prefix for each sequence anew costs less than the launches that share it.
@@ -655,7 +671,7 @@ bool prefix_takes_few(int B, int Hq, int Hk, int D, int max_q, int max_k, int ma
 }
 FewPlan prefix_few_plan(int B, int Hq, int Hk, int D, int max_q, int max_k, int max_p)
 {
-    return few_plan(B, Hq, Hk, D, max_q, prefix_most(max_k, max_p));
+    return one_round(B, Hq, Hk, D, max_q, prefix_most(max_k, max_p));
 }
 
 cudaError_t launch_cross_few(const CrossArgs &a, const FewPlan &p, cudaStream_t stream)

@@ -43,6 +43,28 @@ struct Groups {
         fn = (int)(b - a);
         return a >= 0 && b >= a && b <= Tp && b - a <= max_p;
     }
+    // Sequence b's group g and its prefix, for a converged warp, in one round of loads for up to 31 groups: false where
+    // the group is malformed (`err`), or does not hold b.
+    __device__ bool find(int b, int lane, int &g, int &begin, int &f0, int &fn, int &err) const
+    {
+        err = 0;
+        if (G < 32) {
+            const int at = lane <= G ? bound(lane) : 0, row = lane <= G ? cu_p[lane] : 0;
+            g = 31 - __clz(__ballot_sync(0xffffffffu, lane < G && at <= b) | 1u);
+            begin = __shfl_sync(0xffffffffu, at, g);
+            const int end = __shfl_sync(0xffffffffu, at, g + 1), r1 = __shfl_sync(0xffffffffu, row, g + 1);
+            f0 = __shfl_sync(0xffffffffu, row, g);
+            fn = r1 - f0;
+            if (begin < 0 || begin > b || end <= b || end > B || f0 < 0 || r1 < f0 || r1 > Tp) err = VIT_ERR_BAD_SEQLENS;
+            else if (fn > max_p) err = VIT_ERR_SEQLEN_EXCEEDS_MAX;
+        } else {
+            g = of(b);
+            begin = bound(g);
+            load(g, f0, fn);
+            err = begin > b || bound(g + 1) <= b ? VIT_ERR_BAD_SEQLENS : error(g);
+        }
+        return err == 0;
+    }
     // group g's error: the groups follow one another and hold every sequence, their prefixes lie in the tensor
     __device__ int error(int g) const
     {

@@ -412,17 +412,19 @@ window_join_kernel(const Sched p, const float *part_o, const FewParts few, __nv_
     grid_wait();
     constexpr int CH = D / 8, R = 32 / CH;             // lanes of a row, rows of a warp
     const int lane = threadIdx.x & 31, b = blockIdx.y, sub = lane / CH, c8 = lane % CH * 8;
-    const int error = p.hdr->error, g = p.groups.of(b);
+    const int error = p.hdr->error;
+    int g, begin, f0, fn, err;
+    const bool fine = p.groups.find(b, lane, g, begin, f0, fn, err);
     CrossSeg c;
-    if (!load_seg(p.s, b, c, nullptr, false) || error != 0) return;
+    if (!load_seg(p.s, b, c, nullptr, false) || error != 0 || !fine) return;
     const int packs = p.Hq >> p.lg_pack, lg_tile = 7 - p.lg_pack, mask = (1 << lg_tile) - 1;
     const WinSeg w = win_seg(c);
     // a unit without keys has no slots
     UnitSlots own{0, 0, 0, 0}, pre{0, 0, 0, 0};
     if (FEW) own.runs = key_runs(w.kn, few.chunk);
     else if (w.kn > 0) own = p.units[p.groups.G + b];
-    if (p.groups.cu_p[g + 1] > p.groups.cu_p[g]) pre = p.units[g];
-    const int before = c.q0 - p.s.cu_q[p.groups.bound(g)];     // rows of the group's sequences before this one
+    if (fn > 0) pre = p.units[g];
+    const int before = c.q0 - p.s.cu_q[begin];         // rows of the group's sequences before this one
     const int64_t n_rows = (int64_t)c.qn * p.Hq;
     for (int64_t x0 = (int64_t)(blockIdx.x * 8 + (threadIdx.x >> 5)) * R; x0 < n_rows; x0 += (int64_t)8 * R * gridDim.x) {
         const int64_t x = x0 + sub;
