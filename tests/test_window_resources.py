@@ -16,7 +16,7 @@ def test_every_kernel_is_reported(kernels):
     for name in ("window_long_kernel", "window_grad_kernel", "window_join_kernel"):
         for D in HEAD_DIMS:
             assert any(f"{name}<{D}" in k["name"] or f"{name}<(int){D}" in k["name"] for k in kernels), (name, D)
-    assert len(of(kernels, "window_schedule_kernel")) == 3
+    assert len(of(kernels, "window_schedule_kernel")) == 6
 
 
 def test_register_counts_match_their_splits(kernels):

@@ -21,7 +21,8 @@ namespace {
 
 constexpr int kThreads = kSortThreads;
 // Three ways to make the list: up to 32 units by a warp, a unit per lane; up to kSmall (and where a prefix is apart) a unit
-// per thread; more sorted by the block. Each is a kernel of its own: all in one, a list of 1864 items took 2 us longer.
+// per thread; more sorted by the block. Each is a kernel of its own, with and without prefixes: what it takes is latency, fetching its code included (all in one,
+// a list of 1864 items took 2 us longer).
 enum { kByWarp, kByThread, kSorted };
 constexpr int kSmall = 256;
 
@@ -51,11 +52,12 @@ struct Sched {
 };
 
 // Unit u, and whether it can be used; `none` counts a sequence's queries that see nothing at all (its first rows).
+template <bool PREFIX>
 __device__ __forceinline__ bool load_unit(const Sched &p, int u, Unit &x, CrossEmpty &none, bool report)
 {
     none = CrossEmpty{0, 0};
     x = Unit{0, 0, 0, 0, 0, 0, 0};
-    if (p.apart && u < p.groups.G) {
+    if (PREFIX && p.apart && u < p.groups.G) {
         const int a = p.groups.bound(u), b = p.groups.bound(u + 1);
         const bool fine = p.groups.load(u, x.f0, x.fn);
         if (a < 0 || b < a || b > p.s.B) return false; // (reported with the groups)
@@ -65,10 +67,10 @@ __device__ __forceinline__ bool load_unit(const Sched &p, int u, Unit &x, CrossE
         x.qn = (int)(q1 - q0);
         return true;
     }
-    const int b = p.apart ? u - p.groups.G : u;
+    const int b = PREFIX && p.apart ? u - p.groups.G : u;
     CrossSeg c;
     if (!load_seg(p.s, b, c, p.status, report)) return false;
-    if (p.prefix && !p.apart) {
+    if (PREFIX && !p.apart) {
         if (!p.groups.load(p.groups.of(b), x.f0, x.fn)) return false;
     }
     const WinSeg w = win_seg(c);
@@ -77,11 +79,11 @@ __device__ __forceinline__ bool load_unit(const Sched &p, int u, Unit &x, CrossE
     x.q0 = w.q0;
     x.qn = w.qn;
     x.p0 = w.p0;
-    if (x.fn > 0) {                                    // all of them see the prefix
+    if (PREFIX && x.fn > 0) {                          // all of them see the prefix
         x.q0 -= w.none;
         x.qn += w.none;
         x.p0 -= w.none;
-    } else if (!p.apart) {
+    } else if (!PREFIX || !p.apart) {
         none = CrossEmpty{c.q0, w.none};
     }
     return true;
@@ -92,12 +94,12 @@ struct Span {
     int f0, fn, lo, kn;
     __device__ int tiles(int bn) const { return (fn + bn - 1) / bn + (kn + bn - 1) / bn; }
 };
-__device__ __forceinline__ Span span_of(const Sched &p, const Unit &u, int t, int e)
+template <bool PREFIX> __device__ __forceinline__ Span span_of(const Sched &p, const Unit &u, int t, int e)
 {
     Span s{u.f0, u.fn, 0, 0};
     if (u.kn == 0) return s;
     const int first = u.p0 + t, last = u.p0 + e - 1;
-    if (!p.prefix) {
+    if (!PREFIX) {
         const WinRange r = win_range(first, p.window, p.sinks);
         s.f0 = u.k0;
         s.fn = r.first;
@@ -107,7 +109,7 @@ __device__ __forceinline__ Span span_of(const Sched &p, const Unit &u, int t, in
     return s;
 }
 
-template <int MODE>
+template <int MODE, bool PREFIX>
 __global__ void __launch_bounds__(kThreads)
 window_schedule_kernel(const Sched p)
 {
@@ -120,13 +122,14 @@ window_schedule_kernel(const Sched p)
     __shared__ unsigned long long s_best;
     grid_wait();
     grid_release();
-    const int tid = threadIdx.x, n_units = p.own_few ? p.groups.G : p.apart ? p.groups.G + p.s.B : p.s.B;
+    const int tid = threadIdx.x, n_units = !PREFIX ? p.s.B : p.own_few ? p.groups.G : p.apart ? p.groups.G + p.s.B : p.s.B;
+    const bool apart = PREFIX && p.apart;
     int NP = 32;
     while (NP < n_units) NP <<= 1;
     int *s_tile = reinterpret_cast<int *>(s_key + NP); // [NP] first tile
     const int lg_tile = 7 - p.lg_pack;                 // tokens of a 128-row tile, log2
     const int packs = p.Hq >> p.lg_pack;
-    auto longest = [&](const Unit &x) { return span_of(p, x, max(0, x.qn - (1 << lg_tile)), x.qn).tiles(p.bn); };
+    auto longest = [&](const Unit &x) { return span_of<PREFIX>(p, x, max(0, x.qn - (1 << lg_tile)), x.qn).tiles(p.bn); };
     auto key_of = [&](bool use, const Unit &x, int i) {
         return ((unsigned long long)(use ? 0x7fffffffu - (uint32_t)longest(x) : 0xffffffffu) << 32) | (uint32_t)i;
     };
@@ -135,13 +138,13 @@ window_schedule_kernel(const Sched p)
     auto runs_of = [&](const Unit &x) { return runs_in(longest(x), p.run_tiles); };
     auto usable = [&](bool fine, const Unit &x) { return fine && x.qn > 0 && (x.fn > 0 || x.kn > 0); };
     // two-tile blocks of the batch: few of them means split items throughout
-    auto split_all = [&](int64_t full) { return p.run_tiles > 0 || p.apart || 2 * full <= (int64_t)p.num_sms; };
+    auto split_all = [&](int64_t full) { return p.run_tiles > 0 || apart || 2 * full <= (int64_t)p.num_sms; };
     auto unfit = [&](int u, bool fine) {               // nothing is computed at all then
-        const int b = p.apart ? u - p.groups.G : u;
-        return (p.prefix && !fine) || (b >= 0 && p.s.cu_q[b + 1] < p.s.cu_q[b]);
+        const int b = apart ? u - p.groups.G : u;
+        return (PREFIX && !fine) || (b >= 0 && p.s.cu_q[b + 1] < p.s.cu_q[b]);
     };
     bool wrong = false;                                // of a prefix call: then nothing is computed at all
-    if (p.prefix) {
+    if constexpr (PREFIX) {
         for (int g = tid; g < p.groups.G; g += kThreads) {
             const int err = p.groups.error(g);
             if (err) report_error(p.status, err);
@@ -161,7 +164,7 @@ window_schedule_kernel(const Sched p)
         if (tid < 32) {
             Unit x;
             CrossEmpty none{0, 0};
-            const bool fine = tid < n_units && load_unit(p, tid, x, none, true);
+            const bool fine = tid < n_units && load_unit<PREFIX>(p, tid, x, none, true);
             const bool bad = tid < n_units && unfit(tid, fine), use = usable(fine, x);
             int64_t full = use ? blocks_of(x, lg_tile + 1) : 0;
 #pragma unroll
@@ -193,7 +196,7 @@ window_schedule_kernel(const Sched p)
         __shared__ int s_len[kSmall], s_blocks[kSmall];
         Unit x;
         CrossEmpty none{0, 0};
-        const bool fine = tid < n_units && load_unit(p, tid, x, none, true), use = usable(fine, x);
+        const bool fine = tid < n_units && load_unit<PREFIX>(p, tid, x, none, true), use = usable(fine, x);
         const int len = use ? longest(x) : 0;
         const unsigned long long key = ((unsigned long long)(use ? 0x7fffffffu - (uint32_t)len : 0xffffffffu) << 32) | (uint32_t)tid;
         int64_t total_full, total, total_tiles;
@@ -209,7 +212,7 @@ window_schedule_kernel(const Sched p)
             if (fine && none.qn > 0) p.empty[atomicAdd(&s_empty, 1)] = none;   // (in any order)
         }
         __syncthreads();
-        if (p.apart) {
+        if (apart) {
             // How long runs are best: an item takes a step for each two of its tiles, and about kItemSteps beside them. Of
             // units alike (the groups alone) as many rounds as it takes, else an even share and one item more.
             constexpr float kItemSteps = 2.5f;
@@ -269,7 +272,7 @@ window_schedule_kernel(const Sched p)
         for (int i = tid; i < NP; i += kThreads) {
             Unit x;
             CrossEmpty none{0, 0};
-            const bool fine = i < n_units && load_unit(p, i, x, none, true);
+            const bool fine = i < n_units && load_unit<PREFIX>(p, i, x, none, true);
             if (i < n_units && unfit(i, fine)) s_bad = 1;
             const bool use = usable(fine, x);
             s_key[i] = key_of(use, x, i);
@@ -282,7 +285,7 @@ window_schedule_kernel(const Sched p)
         auto unit_at = [&](int i) {
             Unit x;
             CrossEmpty none;
-            load_unit(p, (int)(s_key[i] & 0xffffffffu), x, none, false);
+            load_unit<PREFIX>(p, (int)(s_key[i] & 0xffffffffu), x, none, false);
             return x;
         };
         int64_t mine = 0, total_full, n_items = 0, n_tiles = 0, total, total_tiles;
@@ -326,18 +329,18 @@ window_schedule_kernel(const Sched p)
         Unit x;
         CrossEmpty none;
         if (MODE != kSorted) x = s_unit[at_unit];
-        else load_unit(p, unit, x, none, false);
+        else load_unit<PREFIX>(p, unit, x, none, false);
         const int nq = (int)(((unsigned)x.qn + (1u << lg_block) - 1u) >> lg_block);
         const int runs = MODE != kSorted ? s_runs[at_unit] : runs_of(x);
         const int j = runs > 1 ? n / runs : n, run = n - j * runs, back = j / packs, qb = nq - 1 - back;
         const int h = j - back * packs;
         const int t = qb << lg_block, e = min(x.qn, t + (1 << lg_block));
-        const Span s = span_of(p, x, t, e);
+        const Span s = span_of<PREFIX>(p, x, t, e);
         // the block's tiles, dealt evenly to as many runs as they fill
         const int tiles = runs > 1 ? s.tiles(p.bn) : 0, use = runs > 1 ? runs_in(tiles, run_tiles) : 1;
-        if (p.apart && n == 0) p.units[unit] = UnitSlots{x.q0, nq, runs, i};
+        if (apart && n == 0) p.units[unit] = UnitSlots{x.q0, nq, runs, i};
         if (run >= use) {
-            if (p.apart)
+            if (apart)
                 for (int r = 0; r < 128; ++r) p.part_s[(int64_t)i * 128 + r] = -INFINITY;
             continue;
         }
@@ -346,7 +349,7 @@ window_schedule_kernel(const Sched p)
         it.q1 = x.q0 + x.qn;
         it.head = h << p.lg_pack;
         it.split = all_split || x.qn - t <= (1 << lg_tile);
-        it.slot = runs > 1 || p.apart ? i : -1;
+        it.slot = runs > 1 || apart ? i : -1;
         it.p0 = x.p0 + t;
         it.pad = 0;
         int fa = 0, fb = s.fn, ka = 0, kb = s.kn;
@@ -363,7 +366,7 @@ window_schedule_kernel(const Sched p)
         it.kp = s.lo + ka;
         it.k0 = x.k0 + it.kp;
         it.kn = kb - ka;
-        if (runs > 1 && run == 0 && !p.apart)
+        if (runs > 1 && run == 0 && !apart)
             p.tiles[s_tile[at_unit] + j] = CrossTile{it.q0, it.q1, it.head, i, use, {0, 0, 0}};
         if (i < whole) {
             p.items[i] = it;
@@ -382,7 +385,7 @@ window_schedule_kernel(const Sched p)
     if (tid == 0) {
         WsHeader *hdr = p.hdr;
         hdr->n_long = whole + s_more;
-        hdr->n_joins = bad || p.apart ? 0 : s_tiles;
+        hdr->n_joins = bad || apart ? 0 : s_tiles;
         hdr->n_empty = bad ? 0 : s_empty;
         hdr->n_tiny = 0;
         hdr->bm_long = 1 << lg_block;
@@ -583,19 +586,24 @@ cudaError_t launch_window_tiles(const WinArgs &a, const WinPlan &pl, int num_sms
     int np = 32;
     while (np < pl.units) np <<= 1;
     constexpr size_t each = sizeof(unsigned long long) + sizeof(int);
-    auto sorted = window_schedule_kernel<kSorted>;
+    auto kernel = [&](auto prefix) {
+        constexpr bool P = decltype(prefix)::value;
+        return pl.units <= 32 && !pl.apart ? window_schedule_kernel<kByWarp, P>
+               : pl.units <= kSmall        ? window_schedule_kernel<kByThread, P>
+                                           : window_schedule_kernel<kSorted, P>;
+    };
     static DeviceOnce once;
     cudaError_t e = once.run([&] {
-        return cudaFuncSetAttribute(sorted, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)each * 2 * VIT_MAX_SEGMENTS);
+        constexpr int most = (int)each * 2 * VIT_MAX_SEGMENTS;
+        const cudaError_t r = cudaFuncSetAttribute(window_schedule_kernel<kSorted, false>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        return r != cudaSuccess ? r : cudaFuncSetAttribute(window_schedule_kernel<kSorted, true>,
+                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     });
     if (e != cudaSuccess) return e;
     {
         LaunchScope scope("window_schedule", stream);
-        auto kern = pl.units <= 32 && !pl.apart ? window_schedule_kernel<kByWarp>
-                    : pl.units <= kSmall        ? window_schedule_kernel<kByThread>
-                                                : sorted;
-        e = launch_chained(kern, 1, kThreads, each * np, stream, p);
+        e = launch_chained(a.prefix ? kernel(std::true_type()) : kernel(std::false_type()), 1, kThreads, each * np, stream, p);
         if (e != cudaSuccess) return e;
     }
     WinLong cx{};
