@@ -191,13 +191,15 @@ MANY = [
     (20, 300, 300, 8, 8, 64, 128, 4),
     (5, 1000, 1000, 8, 2, 96, 0, 0),
     (2, 40, 70, 2, 2, 128, 3000, 500),
+    (40, 40, 40, 1, 1, 64, 0, 0),
+    (40, 40, 40, 1, 1, 64, 1500, 9),
 ]
 
 
 @pytest.mark.parametrize("B,lo,hi,Hq,Hk,D,window,sinks", MANY)
 def test_many_sequences(B, lo, hi, Hq, Hk, D, window, sinks):
     ql = torch.randint(lo, hi + 1, (B,), generator=torch.Generator().manual_seed(B)).tolist()
-    kl = [max(0, m + (7 * i) % 5 - 1) if B > 5 else m + 9000 * (B == 2) for i, m in enumerate(ql)]
+    kl = [max(0, m + (7 * i) % 5 - 1) if B > 5 and B != 40 else m + 9000 * (B == 2) + 3000 * (B == 40) for i, m in enumerate(ql)]
     q, k, v, cq, ck, _ = make(ql, kl, Hq, Hk, D)
     ref = reference(q, k, v, cq, ck, None, window, sinks)
     status = vit.new_status()
@@ -251,6 +253,46 @@ def test_views_of_one_projection(m):
     kv = torch.randn(500, 2, 2, 64, generator=g, device="cuda").bfloat16()
     got = vit.prefix_attn(q, kv[:, 0], kv[:, 1], k, v, cq, ints([100, 500]), cq, None, m, 400, m)
     check(got, None, reference(q, k, v, cq, cq, prefix=[(kv[:, 0], kv[:, 1], 100, 500)] * 3))
+
+
+@pytest.mark.parametrize("m", [1, 60])
+def test_nothing_on_a_side(m):
+    """No keys anywhere, no prefix anywhere, no queries, no sequences."""
+    q = torch.randn(2 * m, 4, 64, device="cuda").bfloat16()
+    none, cq, zero = q.new_zeros(0, 2, 64), offsets([m, m]), ints([0, 0, 0])
+    k = torch.randn(2 * m, 2, 64, device="cuda").bfloat16()
+    out, lse = vit.window_attn(q, none, none, cq, zero, m, 1, 5, 2, return_lse=True)
+    assert not out.any() and torch.isneginf(lse).all()
+    dq, dk, dv = vit.window_attn_bwd(q, q, none, none, out, lse, cq, zero, m, 1, 5, 2)
+    assert not dq.any() and dk.shape == dv.shape == none.shape
+    out, lse = vit.prefix_attn(q, none, none, none, none, cq, ints([0, 0]), zero, return_lse=True)
+    assert not out.any() and torch.isneginf(lse).all()
+    want = vit.window_attn(q, k, k, cq, cq, m, m)
+    check(vit.prefix_attn(q, none, none, k, k, cq, ints([0, 0]), cq), None, reference(q, k, k, cq, cq))
+    check(want, None, reference(q, k, k, cq, cq))
+    out, lse = vit.prefix_attn(q, k, k, none, none, cq, ints([0, 2 * m]), zero, None, m, 2 * m, 1, return_lse=True)
+    check(out, lse, reference(q, none, none, cq, zero, prefix=[(k, k, 0, 2 * m)] * 2))
+    empty = q[:0]
+    assert vit.window_attn(empty, k, k, zero, cq).shape == empty.shape
+    dq, dk, dv = vit.window_attn_bwd(empty, empty, k, k, empty, lse[:0], zero, cq, window=3)
+    assert not dk.any() and not dv.any()
+    one = ints([0])
+    dq, dk, dv = vit.window_attn_bwd(q, q, k, k, q, lse, one, one)
+    assert not dq.any() and not dk.any() and not dv.any()
+    assert vit.prefix_attn(q, k, k, k, k, one, ints([0, 0]), one).shape == q.shape
+
+
+@pytest.mark.parametrize("m,P,padded", [(1, 900, 64), (1, 30000, 64), (30, 900, 100), (400, 900, 500)])
+def test_prefix_before_a_padded_cache(m, P, padded):
+    """NaN behind the real rows of each sequence's cache, and around the prefixes."""
+    B, Hk = 6, 2
+    own = [m + 5 * b for b in range(B - 1)] + [0]
+    q, k, v, cq, ck, k_len = make([m] * B, own, 8, Hk, 80, rows=padded)
+    kp, vp = (make([P, 33], [1], Hk, Hk, 80, seed=s, gap=4)[0] for s in (1, 2))
+    cp, groups = offsets([P, 33], 4), [4, 2]
+    of = [(kp, vp, 4, 4 + P)] * 4 + [(kp, vp, 4 + P, 37 + P)] * 2
+    out, lse = vit.prefix_attn(q, kp, vp, k, v, cq, cp, ck, offsets(groups), m, P, padded, k_len=k_len, return_lse=True)
+    check(out, lse, reference(q, k, v, cq, ck, k_len, prefix=of))
 
 
 def test_windows_that_leave_nothing_out():

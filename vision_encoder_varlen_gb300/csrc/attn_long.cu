@@ -819,12 +819,13 @@ long_body(const CUtensorMap &tm_q, const CUtensorMap &tm_qr, const CUtensorMap &
             // come yet (-inf less -inf is NaN; a test of it in each tile cost 3 % at head_dim 80)
             float m_run = X ? -FLT_MAX : -INFINITY, l_run = 0.f;
 
-            // key tile j; W: this row sees its columns before `hi`, from `lo` on or before `sk`
+            // key tile j (false: a wait gave up); W: this row sees its columns before `hi`, from `lo` on or before `sk`.
+            // (Without a result, the loop's condition alone to leave by, it was 5 % slower at head_dim 80.)
             auto tile = [&](int j, auto masked, [[maybe_unused]] int hi, [[maybe_unused]] int lo,
-                            [[maybe_unused]] int sk) {
+                            [[maybe_unused]] int sk) -> bool {
                 constexpr bool MASKED = decltype(masked)::value;
                 const bool edge = MASKED && (kTwoCopies || __any_sync(0xffffffffu, hi < BN || lo > 0));
-                if (!(ok = wait_warp(bars.s_full[grp], p_cnt & 1))) return;
+                if (!(ok = wait_warp(bars.s_full[grp], p_cnt & 1))) return false;
                 tc_fence_after();
                 // S row -> registers: all loads in flight, one wait
                 uint32_t sr[BN];
@@ -897,7 +898,7 @@ long_body(const CUtensorMap &tm_q, const CUtensorMap &tm_qr, const CUtensorMap &
 
                 // this tile's P region is free, and its O holds every earlier P.V product, once
                 // the previous P.V of this tile has completed
-                if (!__all_sync(0xffffffffu, pv_probe) && !(ok = wait_warp(bars.pv_done[grp], (p_cnt - 1) & 1))) return;
+                if (!__all_sync(0xffffffffu, pv_probe) && !(ok = wait_warp(bars.pv_done[grp], (p_cnt - 1) & 1))) return false;
                 tc_fence_after();
                 if (__any_sync(0xffffffffu, rescale)) {
                     const float a = rescale ? alpha : 1.f;
@@ -923,6 +924,7 @@ long_body(const CUtensorMap &tm_q, const CUtensorMap &tm_qr, const CUtensorMap &
                 if constexpr (kDeferOut) {
                     if (pend) write_out();
                 }
+                return true;
             };
             for (int j = dj == 2 ? grp : 0; j < n_kv && ok; j += dj) {
                 if constexpr (W) {
@@ -937,12 +939,13 @@ long_body(const CUtensorMap &tm_q, const CUtensorMap &tm_qr, const CUtensorMap &
                             sk = min(hi, cx.sinks - kp);
                         }
                     }
-                    if (kTwoCopies && __all_sync(0xffffffffu, hi >= BN && lo <= 0))
-                        tile(j, std::false_type(), 0, 0, 0);
-                    else
-                        tile(j, std::true_type(), hi, lo, sk);
+                    if (kTwoCopies && __all_sync(0xffffffffu, hi >= BN && lo <= 0)) {
+                        if (!tile(j, std::false_type(), 0, 0, 0)) break;
+                    } else if (!tile(j, std::true_type(), hi, lo, sk)) {
+                        break;
+                    }
                 } else {
-                    tile(j, std::false_type(), 0, 0, 0);
+                    if (!tile(j, std::false_type(), 0, 0, 0)) break;
                 }
             }
             if (!ok) break;
