@@ -60,9 +60,15 @@ def few_bytes(B, Hq, Hk, D, max_q, max_k):
     rows, pairs = max_q * (Hq // Hk), B * Hk
     if pairs >= SMS and max_k <= 2048:
         return 4 * pairs * rows * (D + 1)
+    fit = SMS * (227 * 1024 // (3 * 256 * D + 2048))   # blocks that run at a time
     n = max(1, min((8 * SMS + pairs // 2) // pairs, cdiv(max_k, max(16 * rows, 128))))
-    chunk = max(64, cdiv(cdiv(max_k, n), 64) * 64)
-    return 4 * pairs * (cdiv(max_k, chunk) if max_k else 1) * rows * (D + 1)
+    for _ in range(2):                                 # again with fewer runs where a second round would be a small one
+        chunk = max(64, cdiv(cdiv(max_k, n), 64) * 64)
+        runs = cdiv(max_k, chunk) if max_k else 1
+        if not (pairs <= fit < pairs * runs and 2 * pairs * runs < 3 * fit):
+            break
+        n = fit // pairs
+    return 4 * pairs * runs * rows * (D + 1)
 
 
 def few(B, Hq, Hk, D, max_q, max_k, window, sinks):
