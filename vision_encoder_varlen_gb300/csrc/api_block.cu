@@ -432,7 +432,7 @@ size_t vit_window_attn_bwd_workspace_size(int64_t Tq, int64_t Tk, int Hq, int Hk
                                           int window, int sinks)
 {
     if (window_sizes(Tq, Tk, Hq, Hkv, D, B, &max_q, &max_k, &window, &sinks) != VIT_OK) return 0;
-    const GradPlan p = window_grad_plan(Tq, Tk, B, Hq, Hkv, D, max_q, max_k);
+    const WinGradPlan p = window_grad_plan(Tq, Tk, B, Hq, Hkv, D, max_q, max_k, window, sinks);
     return p.max_dq >= kMaxItems || p.max_dkv >= kMaxItems ? 0 : p.bytes;
 }
 
@@ -459,8 +459,8 @@ vit_status_t vit_window_attn_bwd(const void *dout, const void *q, const void *k,
     int sms = 0;
     st = check_device(&sms);
     if (st != VIT_OK) return st;
-    return from_cuda(launch_window_grad(a, window_grad_plan(Tq, Tk, B, Hq, Hkv, D, max_q, max_k), window, sinks, sms,
-                                        (cudaStream_t)stream));
+    return from_cuda(launch_window_grad(a, window_grad_plan(Tq, Tk, B, Hq, Hkv, D, max_q, max_k, window, sinks), window,
+                                        sinks, sms, (cudaStream_t)stream));
 }
 
 // the sizes of a call with prefixes

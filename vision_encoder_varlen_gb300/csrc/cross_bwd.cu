@@ -56,6 +56,15 @@
 // tile the first tokens and the run of keys that its rows see between them. Pairs that the mask excludes inside those
 // tiles have P = dS = 0 exactly, whatever their scores are. delta is from the scores for every row that sees 2 to 16
 // keys (the first rows of each sequence, all rows of a window of so many), made with the other statistics.
+// A key tile that holds first tokens has all queries in its loop. Where that is more than an SM's even share of the work
+// (long texts, a short window), the loop is cut into runs whose fp32 sums a last launch adds up in order: with 4 first
+// tokens the call took 56 instead of 413 us for one text of 5200 tokens, 8 heads over one of 64, window 64, 400 instead
+// of 1061 us for one of 16384, 32 over 8 of 128, window 128, and 421 instead of 1296 us for one of 32768, 16 over 4 of
+// 64, window 512.
+// Measured: four texts of 2500 to 5117 tokens, 16 heads of 80, window 1024: 381 us (0.28 of the floor with the other
+// launches); three causal texts of 1500 to 2311, 32 heads over 8 of 128: 256 us. Bound by the hand-over between the issuer
+// and the softmax groups, as without a mask: the tensor pipe is active 40 % of the time, DRAM at 1.3 TB/s.
+#include <algorithm>
 #include <type_traits>
 
 #include "block_sort.cuh"
@@ -145,6 +154,7 @@ struct WinGradMaps : GradMaps {
 };
 struct WinGrad : Grad {
     const WinGradItem *win_items;
+    float *sums;                  // of the runs of cut loops
     int32_t *next;                // items handed out so far beyond each block's first
     int window, sinks;
 };
@@ -220,6 +230,11 @@ __device__ __forceinline__ void grad_pass(const std::conditional_t<WIN, WinGradM
         return (int)b - p.first_block;
     };
     auto list_length = [&] { return *static_cast<const volatile int32_t *>(p.n_items); };
+    // the first tile of an item's loop that is its own
+    auto first_j = [&](const GradItem &it) -> int {
+        if constexpr (WIN && DKV) return it.j0;
+        else return 0;
+    };
     // tiles of the keys that a windowed query tile reads first
     auto first_tiles = [&](const GradItem &it) -> int {
         if constexpr (WIN && !DKV) return (it.fn + BN - 1) / BN;
@@ -317,8 +332,9 @@ __device__ __forceinline__ void grad_pass(const std::conditional_t<WIN, WinGradM
                     if (yc >= (uint32_t)NY && !(ok = wait(bars.y_empty[s], (yc / NY - 1) & 1))) break;
                     int head, row;
                     if constexpr (DKV) {
-                        head = it.head * p.group + ((j / nt) << p.lg_pack);
-                        row = it.l0 + j % nt * y_tok;
+                        const int jj = j + first_j(it);
+                        head = it.head * p.group + ((jj / nt) << p.lg_pack);
+                        row = it.l0 + jj % nt * y_tok;
                     } else {
                         const int nf = first_tiles(it);
                         head = it.head / p.group;
@@ -432,7 +448,7 @@ __device__ __forceinline__ void grad_pass(const std::conditional_t<WIN, WinGradM
             // (a windowed query tile's first keys may end inside a tile of their own)
             const int nf = WIN && !DKV ? uni(first_tiles(it)) : 0;
             const int f_tail = WIN && !DKV ? uni(nf > 0 ? valid_rows(it, nf - 1) : BN) : BN, f_steps = (f_tail + 15) >> 4;
-            int pj = 0, aj = 0;                              // place in its pack of the next tile to start, to add up
+            int pj = WIN && DKV ? uni(first_j(it) % nt) : 0, aj = pj;   // place in its pack of the next tile to start, to add up
             auto next_valid = [&]() {
                 const bool end = ++pj == nt;
                 const int v = end ? tail : WIN && !DKV && pj == nf ? f_tail : BN;
@@ -524,8 +540,8 @@ __device__ __forceinline__ void grad_pass(const std::conditional_t<WIN, WinGradM
                 float2 v[PER];
                 auto fetch = [&](int j) {
                     if (j >= n) return;
-                    const int valid = valid_rows(it, j), tok0 = it.l0 + j % nt * y_tok;
-                    const int head0 = it.head * p.group + ((j / nt) << p.lg_pack);
+                    const int jj = j + first_j(it), valid = valid_rows(it, jj), tok0 = it.l0 + jj % nt * y_tok;
+                    const int head0 = it.head * p.group + ((jj / nt) << p.lg_pack);
 #pragma unroll
                     for (int e = 0; e < PER; ++e) {
                         const int c = lane + 32 * e;
@@ -593,7 +609,7 @@ __device__ __forceinline__ void grad_pass(const std::conditional_t<WIN, WinGradM
             auto tiles = [&](auto exact) {
                 for (int j = (int)((u0 ^ (uint32_t)grp) & 1); j < n; j += 2) {
                     const uint32_t u = u0 + j, st = u & 1;
-                    const int valid = valid_rows(it, j);
+                    const int valid = valid_rows(it, j + first_j(it));
                     if constexpr (DKV) {
                         if (!(ok = wait_warp(bars.stat[grp], (u / 2) & 1))) break;
                     }
@@ -604,7 +620,7 @@ __device__ __forceinline__ void grad_pass(const std::conditional_t<WIN, WinGradM
                     [[maybe_unused]] int hi = valid, lo = 0, sk = 0;
                     if constexpr (WIN && DKV) {                // the columns of a token lie side by side
                         const int nt = (it.ln + y_tok - 1) / y_tok;
-                        const int d = it.rp + row - (it.lp + j % nt * y_tok);     // this key against the first token
+                        const int d = it.rp + row - (it.lp + (j + it.j0) % nt * y_tok);   // this key against the first token
                         lo = min(max(d, 0), BN) << p.lg_pack;
                         if (p.window > 0 && it.rp + row >= p.sinks)
                             hi = min(hi, min(max(d + p.window, 0), BN) << p.lg_pack);
@@ -806,6 +822,19 @@ __device__ __forceinline__ void grad_pass(const std::conditional_t<WIN, WinGradM
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar_addr(bars.acc_free));
                     }
+                    if constexpr (DKV) {
+                        if (it.slot >= 0) {                  // a run's sums, as they are
+                            float *to = p.sums + (((int64_t)it.slot * 2 + which) * BM + row) * D;
+                            if (exists) {
+#pragma unroll
+                                for (int c = 0; c < COLS; c += 4)
+                                    *reinterpret_cast<uint4 *>(to + c) = make_uint4(r[c], r[c + 1], r[c + 2], r[c + 3]);
+                            }
+                            if (lane == 0) mbar_arrive(bar_addr(bars.x_empty[xb]));
+                            __syncwarp();
+                            return;
+                        }
+                    }
                     const float f = which ? 1.f : p.scale;
                     const bool whole = n > 0 && it.r0 + (DKV ? BM : BM >> p.lg_pack) <= it.r1;
                     unsigned char *x = base + (2 * xb + which) * C::X_TILE;
@@ -927,12 +956,13 @@ window_grad_kernel(const __grid_constant__ WinGradMaps tm_dkv, const __grid_cons
 // too: their gradients are 0.
 template <bool W>
 __device__ void make_list(bool keys, const CrossSegs &segs, int Hq, int Hk, int lg_pack, int bn, int32_t *counts,
-                          std::conditional_t<W, WinGradItem, GradItem> *items, int32_t *status, int window, int sinks)
+                          std::conditional_t<W, WinGradItem, GradItem> *items, int32_t *status, int window, int sinks,
+                          int cut_over, int run_tiles, WinGradTile *cut)
 {
     constexpr int kThreads = kSortThreads;
     extern __shared__ unsigned long long s_key[];      // [NP] loop length descending, then index; later first item | index
     __shared__ int64_t s_warp[32];
-    __shared__ int s_bad, s_used, s_total;
+    __shared__ int s_bad, s_used, s_total, s_more, s_cut, s_slots;
     const int tid = threadIdx.x, B = segs.B;
     const int lg_tile = keys ? 7 : 7 - lg_pack;        // rows (tokens) of a tile, log2
     const int heads = keys ? Hk : Hq >> lg_pack;       // tiles side by side
@@ -994,7 +1024,11 @@ __device__ void make_list(bool keys, const CrossSegs &segs, int Hq, int Hk, int 
     }
     const int total = s_bad ? 0 : s_total;
     if (tid == 0) counts[keys] = s_bad ? -1 : total;   // -1: the call is left alone altogether
-    if (W && tid == 0) counts[2 + keys] = 0;
+    if (W && tid == 0) {
+        counts[2 + keys] = 0;
+        s_more = s_cut = s_slots = 0;
+    }
+    if (W) __syncthreads();
     for (int i = tid; i < total; i += kThreads) {
         const int p = place_of(s_key, s_used, i), n = i - (int)(s_key[p] >> 32);
         CrossSeg x;
@@ -1033,7 +1067,23 @@ __device__ void make_list(bool keys, const CrossSegs &segs, int Hq, int Hk, int 
                 it.l0 = x.k0 + it.lp;
                 it.tiles = (it.fn + step - 1) / step + (it.ln + step - 1) / step;
             }
-            it.pad[0] = it.pad[1] = 0;
+            it.j0 = 0;
+            it.slot = -1;
+            if (keys && cut_over > 0 && it.tiles > cut_over) {
+                // dealt evenly; its first run stands here, the others behind the list (in any order)
+                const int all = it.tiles, runs = (all + run_tiles - 1) / run_tiles;
+                const int slot = atomicAdd(&s_slots, runs), more = total + atomicAdd(&s_more, runs - 1);
+                cut[atomicAdd(&s_cut, 1)] = WinGradTile{it.r0, min(it.r0 + 128, it.r1), it.head, slot, runs, {0, 0, 0}};
+                for (int k = 1; k < runs; ++k) {
+                    it.j0 = (int)((int64_t)all * k / runs);
+                    it.tiles = (int)((int64_t)all * (k + 1) / runs) - it.j0;
+                    it.slot = slot + k;
+                    items[more + k - 1] = it;
+                }
+                it.j0 = 0;
+                it.tiles = all / runs;
+                it.slot = slot;
+            }
             items[i] = it;
         } else {
             const int h = n / nr, r = n - h * nr;
@@ -1047,6 +1097,13 @@ __device__ void make_list(bool keys, const CrossSegs &segs, int Hq, int Hk, int 
             it.exact = x.kn > 1 && x.kn <= kExactKeys;     // (one key: out is v, and nothing is lost)
             it.pad = 0;
             items[i] = it;
+        }
+    }
+    if constexpr (W) {
+        __syncthreads();
+        if (keys && tid == 0) {
+            if (!s_bad) counts[1] = total + s_more;
+            counts[4] = s_cut;
         }
     }
 }
@@ -1066,6 +1123,8 @@ struct Prepare {
     int64_t q_stride, k_stride, v_stride;
     int window, sinks;
     float scale_log2;
+    int cut_over, run_tiles;
+    WinGradTile *cut;
 };
 
 // The keys that a token's rows see where those are 2 to kExactKeys: the first `first` of its sequence and `n` in all,
@@ -1198,7 +1257,8 @@ cross_grad_prepare_kernel(const Prepare p)
     if (blockIdx.x < 2) {
         const bool keys = blockIdx.x == 1;
         make_list<W>(keys, p.segs, p.Hq, p.Hk, p.lg_pack, keys ? GradCfg<D, true>::BN : GradCfg<D, false>::BN,
-                     p.counts, static_cast<Item *>(keys ? p.dkv : p.dq), p.status, p.window, p.sinks);
+                     p.counts, static_cast<Item *>(keys ? p.dkv : p.dq), p.status, p.window, p.sinks, p.cut_over,
+                 p.run_tiles, p.cut);
         return;
     }
     if constexpr (W) {
@@ -1227,6 +1287,39 @@ cross_grad_prepare_kernel(const Prepare p)
 #pragma unroll
         for (int i = 0; i < CH; ++i) sum += __shfl_sync(0xffffffffu, s, (g * CH + i) & 31);
         if (live && c == 0) p.stats[r] = make_float2(-p.lse[r] * 1.4426950408889634f, -sum);
+    }
+}
+
+// dk and dv of the key tiles whose loops were cut: their runs' sums in order. 32 blocks of 4 rows per
+// tile: what it costs is the time of reading one run after the other.
+template <int D>
+__global__ void __launch_bounds__(256, 3)
+window_grad_join_kernel(const int32_t *counts, const WinGradTile *cut, const float *sums, float scale, __nv_bfloat16 *dk,
+                        __nv_bfloat16 *dv, int64_t dk_stride, int64_t dv_stride)
+{
+    grid_wait();
+    grid_release();
+    const int n = counts[1] < 0 ? 0 : counts[4];
+    for (int b = blockIdx.x; b < 32 * n; b += gridDim.x) {
+        const WinGradTile t = cut[b >> 5];
+        for (int x = threadIdx.x; x < 2 * 4 * (D / 4); x += 256) {
+            const int which = x / (4 * (D / 4)), r = (b & 31) * 4 + x / (D / 4) % 4, c = x % (D / 4) * 4;
+            if (t.r0 + r >= t.r1) continue;
+            const float *at = sums + (((int64_t)t.slot * 2 + which) * BM + r) * D + c;
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+            for (int k = 0; k < t.runs; ++k) {
+                const float4 v = *reinterpret_cast<const float4 *>(at + (int64_t)k * 2 * BM * D);
+                sum.x += v.x;
+                sum.y += v.y;
+                sum.z += v.z;
+                sum.w += v.w;
+            }
+            const float f = which ? 1.f : scale;
+            __nv_bfloat16 *to = (which ? dv + (int64_t)(t.r0 + r) * dv_stride : dk + (int64_t)(t.r0 + r) * dk_stride);
+            *reinterpret_cast<uint2 *>(to + (int64_t)t.head * D + c) =
+                make_uint2(pack_bf16x2(sum.x * f, sum.y * f), pack_bf16x2(sum.z * f, sum.w * f));
+        }
     }
 }
 
@@ -1278,8 +1371,8 @@ bool make_pass(const CrossGradArgs &a, const GradPlan &pl, int num_sms, GradMaps
 }
 
 template <int D, bool W>
-cudaError_t launch_d(const CrossGradArgs &a, const GradPlan &pl, int window, int sinks, int num_sms,
-                     cudaStream_t stream)
+cudaError_t launch_d(const CrossGradArgs &a, const std::conditional_t<W, WinGradPlan, GradPlan> &pl, int window,
+                     int sinks, int num_sms, cudaStream_t stream)
 {
     const CrossSegs &s = a.f.segs;
     char *ws = static_cast<char *>(a.f.workspace);
@@ -1309,6 +1402,13 @@ cudaError_t launch_d(const CrossGradArgs &a, const GradPlan &pl, int window, int
     r.window = window;
     r.sinks = sinks;
     r.scale_log2 = a.f.scale_log2;
+    r.cut_over = r.run_tiles = 0;
+    r.cut = nullptr;
+    if constexpr (W) {
+        r.cut_over = pl.cut_over;
+        r.run_tiles = pl.run_tiles;
+        r.cut = reinterpret_cast<WinGradTile *>(ws + pl.off_cut);
+    }
     int np = 32;
     while (np < s.B) np <<= 1;
     static DeviceOnce once_prepare;
@@ -1345,6 +1445,9 @@ cudaError_t launch_d(const CrossGradArgs &a, const GradPlan &pl, int window, int
         m_dq.o2 = m_dq.o1;
         dkv.win_items = static_cast<const WinGradItem *>(r.dkv);
         dq.win_items = static_cast<const WinGradItem *>(r.dq);
+        dkv.sums = dq.sums = reinterpret_cast<float *>(ws + pl.off_sums);
+        // (runs of cut loops are items as well)
+        dkv.n_blocks = dkv.n_blocks + pl.max_slots < num_sms ? dkv.n_blocks + pl.max_slots : num_sms;
         dkv.next = r.counts + 3;
         dq.next = r.counts + 2;
         dkv.window = dq.window = window;
@@ -1372,8 +1475,20 @@ cudaError_t launch_d(const CrossGradArgs &a, const GradPlan &pl, int window, int
                                                                               : cudaSuccess;
     });
     if (e != cudaSuccess) return e;
-    LaunchScope scope(W ? "window_grad" : "cross_grad", stream);
-    return launch_chained(kern, (unsigned)blocks, kThreads, smem, stream, m_dkv, m_dq, dkv, dq);
+    {
+        LaunchScope scope(W ? "window_grad" : "cross_grad", stream);
+        e = launch_chained(kern, (unsigned)blocks, kThreads, smem, stream, m_dkv, m_dq, dkv, dq);
+    }
+    if constexpr (W) {
+        if (e == cudaSuccess && pl.cut_over > 0) {
+            LaunchScope scope("window_grad_join", stream);
+            const int want = 32 * pl.max_cut;
+            e = launch_chained(window_grad_join_kernel<D>, (unsigned)(want < 4 * num_sms ? want : 4 * num_sms), 256, 0, stream,
+                               r.counts, r.cut, dkv.sums, dkv.scale, static_cast<__nv_bfloat16 *>(a.dk),
+                               static_cast<__nv_bfloat16 *>(a.dv), a.dk_stride, a.dv_stride);
+        }
+    }
+    return e;
 }
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
@@ -1398,13 +1513,42 @@ GradPlan grad_plan(int64_t Tq, int64_t Tk, int B, int Hq, int Hk, int D, int max
     return p;
 }
 
-// with a window: the same lists, of larger items
-GradPlan window_grad_plan(int64_t Tq, int64_t Tk, int B, int Hq, int Hk, int D, int max_q, int max_k)
+// With a window: the same lists, of larger items, and runs of the dk, dv pass's long loops, which are those of the key
+// tiles that hold first tokens. A loop is cut where it is longer than an SM's even share of both passes, that is two of
+// this one's (cut from one on, two texts of 8192 tokens, 16 heads, window 256 lost 5 % to the join), than a loop without
+// first tokens, and than 16 tiles; into runs of one such share (of two, one text of 32768 tokens, 4 heads, window 512
+// took 537 instead of 421 us). That comes from what the call holds and not from max_q and max_k, so that results do not
+// depend on these.
+WinGradPlan window_grad_plan(int64_t Tq, int64_t Tk, int B, int Hq, int Hk, int D, int max_q, int max_k, int window,
+                             int sinks)
 {
-    GradPlan p = grad_plan(Tq, Tk, B, Hq, Hk, D, max_q, max_k);
+    WinGradPlan p;
+    static_cast<GradPlan &>(p) = grad_plan(Tq, Tk, B, Hq, Hk, D, max_q, max_k);
+    p.cut_over = p.run_tiles = p.max_cut = p.max_slots = 0;
+    if (window > 0 && sinks > 0) {
+        const int bn = D == 32 ? GradCfg<32, true>::BN : D == 64 ? GradCfg<64, true>::BN
+                       : D == 80 ? GradCfg<80, true>::BN : D == 96 ? GradCfg<96, true>::BN : GradCfg<128, true>::BN;
+        const int64_t tok = bn >> p.lg_pack, packs = Hq / Hk >> p.lg_pack;
+        auto loop = [&](int64_t queries) { return (queries + tok - 1) / tok * packs; };
+        const int64_t some = loop(Tq < window + 127ll ? Tq : window + 127ll), firsts = (sinks + 127ll) / 128;
+        const int64_t all = (Tk / 128 + B) * Hk * some + (Tq / tok + B) * packs * Hk * firsts;
+        const int64_t share = (all + kDesignSms - 1) / kDesignSms;
+        const int64_t over = std::max({2 * share, some, (int64_t)16}), run = std::max({share, some, (int64_t)8});
+        if (loop(max_q) > over) {
+            // All loops with first tokens are no more than kDesignSms runs: fewer tiles than that have more than a run,
+            // and those have fewer than twice as many runs.
+            const int64_t tiles = (int64_t)B * Hk * firsts, runs = tiles * ((loop(max_q) + run - 1) / run);
+            p.cut_over = (int)over;
+            p.run_tiles = (int)run;
+            p.max_cut = (int)(tiles < kDesignSms ? tiles : kDesignSms);
+            p.max_slots = (int)(runs < 2 * kDesignSms ? runs : 2 * kDesignSms);
+        }
+    }
     p.off_dkv = up(p.off_dq + sizeof(WinGradItem) * (size_t)p.max_dq);
-    p.off_stats = up(p.off_dkv + sizeof(WinGradItem) * (size_t)p.max_dkv);
-    p.bytes = p.off_stats + sizeof(float2) * (size_t)Tq * Hq;
+    p.off_stats = up(p.off_dkv + sizeof(WinGradItem) * (size_t)(p.max_dkv + p.max_slots));
+    p.off_cut = up(p.off_stats + sizeof(float2) * (size_t)Tq * Hq);
+    p.off_sums = up(p.off_cut + sizeof(WinGradTile) * (size_t)p.max_cut);
+    p.bytes = p.off_sums + sizeof(float) * 2 * BM * (size_t)D * (size_t)p.max_slots;
     return p;
 }
 
@@ -1420,7 +1564,7 @@ cudaError_t launch_cross_grad(const CrossGradArgs &a, const GradPlan &p, int num
     }
 }
 
-cudaError_t launch_window_grad(const CrossGradArgs &a, const GradPlan &p, int window, int sinks, int num_sms,
+cudaError_t launch_window_grad(const CrossGradArgs &a, const WinGradPlan &p, int window, int sinks, int num_sms,
                                cudaStream_t stream)
 {
     switch (a.f.D) {

@@ -26,7 +26,11 @@
 //
 // A causal window (W): the keys that a sequence's queries see between them are its first `sn` tokens, in tiles of
 // their own, and the run of positions from `lo` on; a run of `chunk` keys counts along both. Keys outside are not
-// loaded, and where there is more than one query each masks for itself what another one sees.
+// loaded, and where there is more than one query each masks for itself what another one sees. HBM bound like the rest: 48
+// single tokens over padded caches of up to 16383 keys, window 4096, 32 heads over 8 of 128: 61 us with the join, 5.4 TB/s
+// of the visible keys (0.80 of a copy). A prefix takes the place of the first tokens where reading it for each sequence
+// is cheap: three single tokens behind 1601 shared keys 12 us in a graph, 20 with one pass for all of them, of which the
+// launches are most.
 #include <type_traits>
 
 #include "cross.h"

@@ -153,11 +153,22 @@ struct alignas(16) WinGradItem {
     int head, tiles;
     int f0, fn;
     int rp, lp;
-    int pad[2];
+    int j0;                       // dk, dv: the item's first tile where a key tile's loop is cut into runs
+    int slot;                     // place of such a run's sums, or -1: dk and dv themselves
 };
 static_assert(sizeof(WinGradItem) == 48, "three 16-byte words");
-GradPlan window_grad_plan(int64_t Tq, int64_t Tk, int B, int Hq, int Hk, int D, int max_q, int max_k);
-cudaError_t launch_window_grad(const CrossGradArgs &a, const GradPlan &p, int window, int sinks, int num_sms,
+// A key tile whose loop is cut: the join adds the slots [slot, slot + runs).
+struct WinGradTile {
+    int r0, r1, head, slot, runs, pad[3];
+};
+struct WinGradPlan : GradPlan {
+    int cut_over, run_tiles;      // a loop of more tiles than the first is cut into runs of the second at most (0: none)
+    int max_cut, max_slots;       // key tiles cut, and their runs, at most
+    size_t off_cut, off_sums;     // the sums: [slots][dk, dv][128][D] fp32
+};
+WinGradPlan window_grad_plan(int64_t Tq, int64_t Tk, int B, int Hq, int Hk, int D, int max_q, int max_k, int window,
+                             int sinks);
+cudaError_t launch_window_grad(const CrossGradArgs &a, const WinGradPlan &p, int window, int sinks, int num_sms,
                                cudaStream_t stream);
 
 // few query rows (cross_few.cu)
