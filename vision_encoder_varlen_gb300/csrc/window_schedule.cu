@@ -150,6 +150,9 @@ window_schedule_kernel(const Sched p)
             if (err) report_error(p.status, err);
             wrong |= err != 0;
         }
+        // (where sequences are no units: their rows have to lie inside their group's)
+        if (p.own_few)
+            for (int b = tid; b < p.s.B; b += kThreads) wrong |= p.s.cu_q[b + 1] < p.s.cu_q[b];
         wrong = __syncthreads_or(wrong);
     }
     if constexpr (MODE != kByWarp) {
