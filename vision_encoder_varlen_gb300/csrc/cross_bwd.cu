@@ -1258,7 +1258,7 @@ cross_grad_prepare_kernel(const Prepare p)
         const bool keys = blockIdx.x == 1;
         make_list<W>(keys, p.segs, p.Hq, p.Hk, p.lg_pack, keys ? GradCfg<D, true>::BN : GradCfg<D, false>::BN,
                      p.counts, static_cast<Item *>(keys ? p.dkv : p.dq), p.status, p.window, p.sinks, p.cut_over,
-                 p.run_tiles, p.cut);
+                     p.run_tiles, p.cut);
         return;
     }
     if constexpr (W) {
@@ -1530,7 +1530,8 @@ WinGradPlan window_grad_plan(int64_t Tq, int64_t Tk, int B, int Hq, int Hk, int 
                        : D == 80 ? GradCfg<80, true>::BN : D == 96 ? GradCfg<96, true>::BN : GradCfg<128, true>::BN;
         const int64_t tok = bn >> p.lg_pack, packs = Hq / Hk >> p.lg_pack;
         auto loop = [&](int64_t queries) { return (queries + tok - 1) / tok * packs; };
-        const int64_t some = loop(Tq < window + 127ll ? Tq : window + 127ll), firsts = (sinks + 127ll) / 128;
+        const int64_t some = loop(std::min<int64_t>(Tq, window + 127ll));
+        const int64_t firsts = (std::min<int64_t>(sinks, Tk) + 127) / 128;
         const int64_t all = (Tk / 128 + B) * Hk * some + (Tq / tok + B) * packs * Hk * firsts;
         const int64_t share = (all + kDesignSms - 1) / kDesignSms;
         const int64_t over = std::max({2 * share, some, (int64_t)16}), run = std::max({share, some, (int64_t)8});
