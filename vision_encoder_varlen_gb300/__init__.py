@@ -261,17 +261,26 @@ def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, pos_hw: torch.T
 
 
 def workspace_size(T: int, H: int, B: int, D: int) -> int:
-    return int(lib().vit_varlen_attn_workspace_size(int(T), int(H), int(B), int(D)))
+    return int(lib().vit_varlen_attn_workspace_size(int(T), *_ints(H, B, D)))
+
+
+def _c_int(x: int) -> int:
+    """x as a C int: the nearest one where x passes 32 bits, of which ctypes would keep the low ones without a word."""
+    return max(-2 ** 31, min(x, 2 ** 31 - 1))
+
+
+def _ints(*x) -> tuple:
+    return tuple(_c_int(int(v)) for v in x)
 
 
 def _max_seqlen(m) -> int:
     """The C convention: 0 = not given (the library bounds the segments by T)."""
-    return 0 if m is None else int(m)
+    return 0 if m is None else _c_int(int(m))
 
 
 def _attn_ex(q, k, v, qs, ks, vs, cu_seqlens, seq_start, seq_len, B, max_seqlen, scale, out, os_, lse, qr,
              short_max, workspace, status, stream, what):
-    opts = _AttnOptions(int(short_max))
+    opts = _AttnOptions(_c_int(int(short_max)))
     _check(lib().vit_varlen_attn_ex(_ptr(q), _ptr(k), _ptr(v), q.shape[0], q.shape[1], q.shape[2], qs, ks, vs,
                                     _ptr(cu_seqlens), _ptr(seq_start), _ptr(seq_len), B, _max_seqlen(max_seqlen),
                                     float(scale) if scale is not None else 0.0, _ptr(out), os_, _ptr(lse),
@@ -300,7 +309,7 @@ def varlen_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: t
     else:
         if num_segments is None:
             raise ValueError("num_segments is required when cu_seqlens is None")
-        B = int(num_segments)
+        B = _c_int(int(num_segments))
     if out is None:
         out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
     os_ = _tok_stride(out, "out", H, D)
@@ -348,7 +357,7 @@ def varlen_attn_fused_q(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_se
     else:
         if num_segments is None:
             raise ValueError("num_segments is required when cu_seqlens is None")
-        B = int(num_segments)
+        B = _c_int(int(num_segments))
     if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or cos_sin.shape[1] != D // 2 \
             or not cos_sin.is_contiguous():
         raise ValueError(f"cos_sin must be the contiguous float32 [max_pos, {D // 2}] table of rope_table")
@@ -530,7 +539,7 @@ MROPE_CYCLED = 1    # time, height, width in turn
 
 @functools.lru_cache(maxsize=64)
 def _three(sections: tuple):
-    return (ctypes.c_int * 3)(*sections)
+    return (ctypes.c_int * 3)(*map(_c_int, sections))
 
 
 def _mrope_args(T, D, pos_thw, inv_freq, sections, norm_w, eps, cycled, interleaved):
@@ -646,14 +655,12 @@ def _size(fn: str, *sizes) -> int:
 
 def cross_attn_workspace_size(Tq: int, Tk: int, Hq: int, Hkv: int, D: int, B: int, max_q: int = 0,
                               max_k: int = 0) -> int:
-    return int(lib().vit_cross_attn_workspace_size(int(Tq), int(Tk), int(Hq), int(Hkv), int(D), int(B), int(max_q),
-                                                   int(max_k)))
+    return int(lib().vit_cross_attn_workspace_size(int(Tq), int(Tk), *_ints(Hq, Hkv, D, B, max_q, max_k)))
 
 
 def cross_attn_bwd_workspace_size(Tq: int, Tk: int, Hq: int, Hkv: int, D: int, B: int, max_q: int = 0,
                                   max_k: int = 0) -> int:
-    return int(lib().vit_cross_attn_bwd_workspace_size(int(Tq), int(Tk), int(Hq), int(Hkv), int(D), int(B),
-                                                       int(max_q), int(max_k)))
+    return int(lib().vit_cross_attn_bwd_workspace_size(int(Tq), int(Tk), *_ints(Hq, Hkv, D, B, max_q, max_k)))
 
 
 def _cross_lists(cu_q, cu_k, k_len) -> int:
@@ -748,27 +755,29 @@ def _attn_bwd(fn, mask, dout, q, k, v, out, lse, cu_q, cu_k, max_q, max_k, scale
 
 def window_attn_workspace_size(Tq: int, Tk: int, Hq: int, Hkv: int, D: int, B: int, max_q: int = 0, max_k: int = 0,
                                window: int = 0, sinks: int = 0) -> int:
-    return int(lib().vit_window_attn_workspace_size(int(Tq), int(Tk), int(Hq), int(Hkv), int(D), int(B), int(max_q),
-                                                    int(max_k), int(window), int(sinks)))
+    return int(lib().vit_window_attn_workspace_size(int(Tq), int(Tk), *_ints(Hq, Hkv, D, B, max_q, max_k, window, sinks)))
 
 
 def window_attn_bwd_workspace_size(Tq: int, Tk: int, Hq: int, Hkv: int, D: int, B: int, max_q: int = 0,
                                    max_k: int = 0, window: int = 0, sinks: int = 0) -> int:
-    return int(lib().vit_window_attn_bwd_workspace_size(int(Tq), int(Tk), int(Hq), int(Hkv), int(D), int(B),
-                                                        int(max_q), int(max_k), int(window), int(sinks)))
+    return int(lib().vit_window_attn_bwd_workspace_size(int(Tq), int(Tk),
+                                                        *_ints(Hq, Hkv, D, B, max_q, max_k, window, sinks)))
 
 
 def prefix_attn_workspace_size(Tq: int, Tp: int, Tk: int, Hq: int, Hkv: int, D: int, B: int, G: int, max_q: int = 0,
                                max_p: int = 0, max_k: int = 0) -> int:
-    return int(lib().vit_prefix_attn_workspace_size(int(Tq), int(Tp), int(Tk), int(Hq), int(Hkv), int(D), int(B),
-                                                    int(G), int(max_q), int(max_p), int(max_k)))
+    return int(lib().vit_prefix_attn_workspace_size(int(Tq), int(Tp), int(Tk),
+                                                    *_ints(Hq, Hkv, D, B, G, max_q, max_p, max_k)))
 
 
 def _window(window, sinks):
     """The C convention: 0 = no window."""
-    if window is not None and window < 1:
+    w, s = (0 if window is None else int(window)), int(sinks)
+    if (window is not None and w != window) or s != sinks:
+        raise ValueError("window and sinks must be whole numbers")
+    if window is not None and w < 1:
         raise ValueError("window must be at least 1, or None")
-    return 0 if window is None else int(window), int(sinks)
+    return _c_int(w), _c_int(s)
 
 
 def window_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor,
