@@ -26,3 +26,40 @@ def test_no_own_keys_behind_a_prefix_read_apart(B, Hk, m):
     out, lse = vit.prefix_attn(q, kp, vp, k, v, cq, cp, ck, offsets(groups), m, 7000, 1, return_lse=True, status=status)
     assert vit.read_status(status) == 0
     check(out, lse, reference(q, k, v, cq, ck, prefix=of))
+
+
+# groups without sequences that are malformed: offsets of prefixes that decrease or leave the tensor, groups that decrease, a
+# prefix longer than its bound; few groups and many
+EMPTY = [
+    ([0, 1, 1, 2], [0, 10, 5, 20], 0, -10),
+    ([0, 1, 1, 2], [0, 10, 31, 20], 0, -10),
+    ([0, 2, 1, 2], [0, 10, 10, 20], 0, -10),
+    ([0, 1, 1, 2], [0, 5, 20, 30], 10, -11),
+    ([0, 1, 2, 2], [0, 10, 20, 31], 0, -10),
+    ([0, 0, 1, 2], [-4, 0, 10, 20], 0, -10),
+    ([0, 1] + [1] * 38 + [2], [0, 10] + [15, 12] * 19 + [20], 0, -10),
+    ([0] * 30 + [1] * 10 + [2], [0] * 29 + [10] * 5 + [25] * 7, 10, -11),
+]
+
+
+# few rows; a list of sequences; groups apart from their sequences with many rows and with few
+@pytest.mark.parametrize("ql,heads,rows", [([4, 4], 1, 30), ([600, 600], 2, 30), ([40] * 2, 16, 30), ([1, 1], 2, 30000)])
+@pytest.mark.parametrize("cg,cp,mp,code", EMPTY)
+def test_bad_groups_without_sequences_are_reported(ql, heads, rows, cg, cp, mp, code):
+    T = sum(ql)
+    q = torch.randn(T, heads, 64, device="cuda").bfloat16()
+    k, kp = (torch.randn(n, heads, 64, device="cuda").bfloat16() for n in (T, rows))
+    grow = rows // 30                                      # the offsets of thirty rows, in a prefix of `rows`
+    guard = torch.full((T + 16, heads, 64), 5.0, device="cuda", dtype=torch.bfloat16)
+    status = vit.new_status()
+    cp = [x * grow if x >= 0 else x for x in cp]
+    call = lambda g, p, m: vit.prefix_attn(q, kp, kp, k, k, offsets(ql), ints(p), offsets(ql), ints(g), max(ql), m * grow,
+                                           max(ql), out=guard[8:8 + T], status=status)
+    call(cg, cp, mp)
+    assert vit.read_status(status) == code
+    assert (guard[:8] == 5).all() and (guard[8 + T:] == 5).all()
+    status.zero_()
+    call([0] * (len(cg) - 2) + [1, 2], [0] * (len(cg) - 2) + [5 * grow, 30 * grow], 0)   # empty groups that are sound
+    assert vit.read_status(status) == 0
+    check(guard[8:8 + T], None, reference(q, k, k, offsets(ql), offsets(ql),
+                                          prefix=[(kp, kp, 0, 5 * grow), (kp, kp, 5 * grow, 30 * grow)]))

@@ -131,10 +131,11 @@ cross_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     CrossSeg seg;
     [[maybe_unused]] int f0 = 0, fn = 0;                      // W: the prefix
     if constexpr (W) {
-        int g, begin, err;
-        if (p.prefix && !p.groups.find(b, lane, g, begin, f0, fn, err)) {
-            if (threadIdx.x == 0 && split == 0 && hk == 0) report_error(p.status, err);
-            return;
+        if (p.prefix) {
+            int g, begin, err;
+            const bool fine = p.groups.find(b, lane, (split | hk | b) == 0, g, begin, f0, fn, err);
+            if (err && threadIdx.x == 0 && split == 0 && hk == 0) report_error(p.status, err);
+            if (!fine) return;
         }
     }
     // a sequence without keys is left to the join, or to split 0 where there is none
@@ -450,7 +451,7 @@ cross_join_kernel(const Few p)
     [[maybe_unused]] int f0 = 0, fn = 0;
     if constexpr (W) {
         int g, begin, err;
-        if (p.prefix && !p.groups.find(b, lane, g, begin, f0, fn, err)) return;
+        if (p.prefix && !p.groups.find(b, lane, false, g, begin, f0, fn, err)) return;
     }
     if (!load_seg(p.segs, b, seg, nullptr, false)) return;
     int n_keys = seg.kn;

@@ -44,36 +44,40 @@ struct Groups {
         return a >= 0 && b >= a && b <= Tp && b - a <= max_p;
     }
     // Sequence b's group g and its prefix, for a converged warp, in one round of loads for up to 31 groups: false where
-    // the group is malformed (`err`), or does not hold b.
-    __device__ bool find(int b, int lane, int &g, int &begin, int &f0, int &fn, int &err) const
+    // b's group is malformed, or any of up to 31. `err`: what is wrong, for one caller (`all`) also with other groups.
+    __device__ bool find(int b, int lane, bool all, int &g, int &begin, int &f0, int &fn, int &err) const
     {
-        err = 0;
+        int bad = 0;
+        bool fine = true;
         if (G < 32) {
             const int at = lane <= G ? bound(lane) : 0, row = lane <= G ? cu_p[lane] : 0;
+            const int at1 = __shfl_down_sync(0xffffffffu, at, 1), row1 = __shfl_down_sync(0xffffffffu, row, 1);
+            if (lane < G) bad = check(lane, at, at1, row, row1);
             g = 31 - __clz(__ballot_sync(0xffffffffu, lane < G && at <= b) | 1u);
             begin = __shfl_sync(0xffffffffu, at, g);
-            const int end = __shfl_sync(0xffffffffu, at, g + 1), r1 = __shfl_sync(0xffffffffu, row, g + 1);
             f0 = __shfl_sync(0xffffffffu, row, g);
-            fn = r1 - f0;
-            if (begin < 0 || begin > b || end <= b || end > B || f0 < 0 || r1 < f0 || r1 > Tp) err = VIT_ERR_BAD_SEQLENS;
-            else if (fn > max_p) err = VIT_ERR_SEQLEN_EXCEEDS_MAX;
+            fn = __shfl_sync(0xffffffffu, row1, g) - f0;
         } else {
             g = of(b);
             begin = bound(g);
             load(g, f0, fn);
-            err = begin > b || bound(g + 1) <= b ? VIT_ERR_BAD_SEQLENS : error(g);
+            bad = begin > b || bound(g + 1) <= b ? VIT_ERR_BAD_SEQLENS : error(g);
+            fine = bad == 0;
+            if (all)
+                for (int i = lane; i < G; i += 32) bad = bad ? bad : error(i);
         }
-        return err == 0;
+        const unsigned any = __ballot_sync(0xffffffffu, bad != 0);
+        err = any ? __shfl_sync(0xffffffffu, bad, __ffs(any) - 1) : 0;
+        return fine && (any == 0 || G >= 32);
     }
     // group g's error: the groups follow one another and hold every sequence, their prefixes lie in the tensor
-    __device__ int error(int g) const
+    __device__ int error(int g) const { return check(g, bound(g), bound(g + 1), cu_p[g], cu_p[g + 1]); }
+    // [a, b) its sequences, [r0, r1) its prefix's rows
+    __device__ int check(int g, int a, int b, int r0, int r1) const
     {
-        const int a = bound(g), b = bound(g + 1);
-        if (a < 0 || b < a || b > B || (g == 0 && a != 0) || (g == G - 1 && b != B)) return VIT_ERR_BAD_SEQLENS;
-        int f0, fn;
-        if (load(g, f0, fn)) return 0;
-        return cu_p[g] < 0 || cu_p[g + 1] < cu_p[g] || cu_p[g + 1] > Tp ? VIT_ERR_BAD_SEQLENS
-                                                                        : VIT_ERR_SEQLEN_EXCEEDS_MAX;
+        if (a < 0 || b < a || b > B || (g == 0 && a != 0) || (g == G - 1 && b != B) || r0 < 0 || r1 < r0 || r1 > Tp)
+            return VIT_ERR_BAD_SEQLENS;
+        return r1 - r0 > max_p ? VIT_ERR_SEQLEN_EXCEEDS_MAX : 0;
     }
     // the group of sequence b: the last one that begins at or before it
     __device__ int of(int b) const

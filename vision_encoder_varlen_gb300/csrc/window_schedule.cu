@@ -420,7 +420,7 @@ window_join_kernel(const Sched p, const float *part_o, const FewParts few, __nv_
     const int lane = threadIdx.x & 31, b = blockIdx.y, sub = lane / CH, c8 = lane % CH * 8;
     const int error = p.hdr->error;
     int g, begin, f0, fn, err;
-    const bool fine = p.groups.find(b, lane, g, begin, f0, fn, err);
+    const bool fine = p.groups.find(b, lane, false, g, begin, f0, fn, err);
     CrossSeg c;
     if (!load_seg(p.s, b, c, nullptr, false) || error != 0 || !fine) return;
     const int packs = p.Hq >> p.lg_pack, lg_tile = 7 - p.lg_pack, mask = (1 << lg_tile) - 1;
