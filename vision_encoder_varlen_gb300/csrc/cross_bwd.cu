@@ -957,7 +957,7 @@ window_grad_kernel(const __grid_constant__ WinGradMaps tm_dkv, const __grid_cons
 template <bool W>
 __device__ void make_list(bool keys, const CrossSegs &segs, int Hq, int Hk, int lg_pack, int bn, int32_t *counts,
                           std::conditional_t<W, WinGradItem, GradItem> *items, int32_t *status, int window, int sinks,
-                          int cut_over, int run_tiles, WinGradTile *cut)
+                          int cut_over, int run_tiles, int max_slots, WinGradTile *cut)
 {
     constexpr int kThreads = kSortThreads;
     extern __shared__ unsigned long long s_key[];      // [NP] loop length descending, then index; later first item | index
@@ -1072,17 +1072,20 @@ __device__ void make_list(bool keys, const CrossSegs &segs, int Hq, int Hk, int 
             if (keys && cut_over > 0 && it.tiles > cut_over) {
                 // dealt evenly; its first run stands here, the others behind the list (in any order)
                 const int all = it.tiles, runs = (all + run_tiles - 1) / run_tiles;
-                const int slot = atomicAdd(&s_slots, runs), more = total + atomicAdd(&s_more, runs - 1);
-                cut[atomicAdd(&s_cut, 1)] = WinGradTile{it.r0, min(it.r0 + 128, it.r1), it.head, slot, runs, {0, 0, 0}};
-                for (int k = 1; k < runs; ++k) {
-                    it.j0 = (int)((int64_t)all * k / runs);
-                    it.tiles = (int)((int64_t)all * (k + 1) / runs) - it.j0;
-                    it.slot = slot + k;
-                    items[more + k - 1] = it;
+                const int slot = atomicAdd(&s_slots, runs);
+                if (slot + runs <= max_slots) {        // (the plan has room for all of them)
+                    const int more = total + atomicAdd(&s_more, runs - 1);
+                    cut[atomicAdd(&s_cut, 1)] = WinGradTile{it.r0, min(it.r0 + 128, it.r1), it.head, slot, runs, {0, 0, 0}};
+                    for (int k = 1; k < runs; ++k) {
+                        it.j0 = (int)((int64_t)all * k / runs);
+                        it.tiles = (int)((int64_t)all * (k + 1) / runs) - it.j0;
+                        it.slot = slot + k;
+                        items[more + k - 1] = it;
+                    }
+                    it.j0 = 0;
+                    it.tiles = all / runs;
+                    it.slot = slot;
                 }
-                it.j0 = 0;
-                it.tiles = all / runs;
-                it.slot = slot;
             }
             items[i] = it;
         } else {
@@ -1123,7 +1126,7 @@ struct Prepare {
     int64_t q_stride, k_stride, v_stride;
     int window, sinks;
     float scale_log2;
-    int cut_over, run_tiles;
+    int cut_over, run_tiles, max_slots;
     WinGradTile *cut;
 };
 
@@ -1258,7 +1261,7 @@ cross_grad_prepare_kernel(const Prepare p)
         const bool keys = blockIdx.x == 1;
         make_list<W>(keys, p.segs, p.Hq, p.Hk, p.lg_pack, keys ? GradCfg<D, true>::BN : GradCfg<D, false>::BN,
                      p.counts, static_cast<Item *>(keys ? p.dkv : p.dq), p.status, p.window, p.sinks, p.cut_over,
-                     p.run_tiles, p.cut);
+                     p.run_tiles, p.max_slots, p.cut);
         return;
     }
     if constexpr (W) {
@@ -1402,11 +1405,12 @@ cudaError_t launch_d(const CrossGradArgs &a, const std::conditional_t<W, WinGrad
     r.window = window;
     r.sinks = sinks;
     r.scale_log2 = a.f.scale_log2;
-    r.cut_over = r.run_tiles = 0;
+    r.cut_over = r.run_tiles = r.max_slots = 0;
     r.cut = nullptr;
     if constexpr (W) {
         r.cut_over = pl.cut_over;
         r.run_tiles = pl.run_tiles;
+        r.max_slots = pl.max_slots;
         r.cut = reinterpret_cast<WinGradTile *>(ws + pl.off_cut);
     }
     int np = 32;
