@@ -10,8 +10,8 @@
 
 static void print(const vit::FewPlan &p)
 {
-    printf(" rows=%d row_tiles=%d chunk=%d n_split=%d partial_bytes=%zu", p.rows, p.row_tiles, p.chunk, p.n_split,
-           p.partial_bytes);
+    printf(" rows=%d row_tiles=%d chunk=%d n_split=%d room=%d partial_bytes=%zu", p.rows, p.row_tiles, p.chunk, p.n_split,
+           p.room, p.partial_bytes);
 }
 
 int main()

@@ -61,6 +61,7 @@ struct FewPlan {
     int row_tiles;                // 16-row tiles of a block: 1 or 2
     int chunk;                    // keys per split
     int n_split;                  // splits of the longest sequence
+    int room;                     // splits that the workspace has room for
     size_t partial_bytes;         // workspace of the partial results (0 with one split)
 };
 bool takes_few(int B, int Hq, int Hk, int D, int max_q, int max_k);   // else the tcgen05 kernel takes the call

@@ -615,7 +615,7 @@ FewPlan few_plan(int B, int Hq, int Hk, int D, int max_q, int max_k)
     if (chunk < kTile) chunk = kTile;
     n = max_k > 0 ? ((int64_t)max_k + chunk - 1) / chunk : 1;
     p.chunk = (int)chunk;
-    p.n_split = (int)n;
+    p.n_split = p.room = (int)n;
     p.partial_bytes = n > 1 ? sizeof(float) * (size_t)pairs * n * p.rows * (D + 1) : 0;
     return p;
 }
@@ -643,18 +643,28 @@ bool window_takes_few(int B, int Hq, int Hk, int D, int max_q, int max_k, int wi
 {
     return takes_few(B, Hq, Hk, D, max_q, window_most(max_q, max_k, window, sinks));
 }
-// A second round of blocks for less than half the places of the first is not begun (three single tokens behind 1601
-// shared keys: 14 runs of 24 pairs, where 304 blocks fit at head_dim 128).
+// A second round of blocks for less than half the places of the first is not begun: the places that shared memory leaves,
+// and those that registers leave to two row tiles (nine warps) from head_dim 64 on. Three single tokens behind 1601 shared
+// keys: 14 runs of 24 pairs, where 304 blocks of one row tile fit at head_dim 128. Two row tiles, 32 rows, 8 key heads: 7
+// sequences of 1100 keys at head_dim 128, 112 blocks 19.5 us in a graph, 168 27.1; 5 of 1600, 120 19.2, 160 23.0; 13 of
+// 1200 at 64, 208 19.0, 312 22.4. At head_dim 32 registers leave 4 and 3 places of 8, but counting those was slower: 20
+// of 1600, 320 blocks 25.7, 640 24.6; one row, 40 of 1000, 1280 blocks 16.4, 960 14.6.
 static FewPlan one_round(int B, int Hq, int Hk, int D, int max_q, int most)
 {
     FewPlan p = few_plan(B, Hq, Hk, D, max_q, most);
-    const int64_t pairs = (int64_t)B * Hk, fit = kDesignSms * (227 * 1024 / (kStages * 4 * kTile * D + 2048));
-    if (pairs * p.n_split > fit && 2 * pairs * p.n_split < 3 * fit && pairs <= fit) {
-        const int64_t n = fit / pairs;
-        p.chunk = (int)((((int64_t)most + n - 1) / n + kTile - 1) / kTile * kTile);
-        p.n_split = (int)(((int64_t)most + p.chunk - 1) / p.chunk);
-        p.partial_bytes = p.n_split > 1 ? sizeof(float) * (size_t)pairs * p.n_split * p.rows * (D + 1) : 0;
-    }
+    const int64_t pairs = (int64_t)B * Hk;
+    auto round = [&](int blocks) {
+        const int64_t fit = (int64_t)kDesignSms * blocks;
+        if (pairs * p.n_split > fit && 2 * pairs * p.n_split < 3 * fit && pairs <= fit) {
+            const int64_t n = fit / pairs;
+            p.chunk = (int)((((int64_t)most + n - 1) / n + kTile - 1) / kTile * kTile);
+            p.n_split = (int)(((int64_t)most + p.chunk - 1) / p.chunk);
+        }
+    };
+    round(227 * 1024 / (kStages * 4 * kTile * D + 2048));
+    p.room = p.n_split;
+    if (p.row_tiles == 2 && D >= 64) round(D <= 80 ? 2 : 1);
+    p.partial_bytes = p.room > 1 ? sizeof(float) * (size_t)pairs * p.room * p.rows * (D + 1) : 0;
     return p;
 }
 FewPlan window_few_plan(int B, int Hq, int Hk, int D, int max_q, int max_k, int window, int sinks)

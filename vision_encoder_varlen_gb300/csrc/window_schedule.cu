@@ -556,9 +556,9 @@ WinPlan win_plan(int64_t Tq, int B, int Hq, int Hk, int D, int max_q, int max_k,
         p.few = window_few_plan(B, Hq, Hk, D, max_q, max_k, 0, 0);
         if ((int64_t)B * Hk >= kDesignSms && max_k <= 2048) {   // one run each: enough blocks, and short ones
             p.few.chunk = std::max(64, (max_k + 63) / 64 * 64);
-            p.few.n_split = 1;
+            p.few.n_split = p.few.room = 1;
         }
-        p.bytes += sizeof(float) * (size_t)B * Hk * p.few.n_split * p.few.rows * (D + 1);
+        p.bytes += sizeof(float) * (size_t)B * Hk * p.few.room * p.few.rows * (D + 1);
     }
     return p;
 }
