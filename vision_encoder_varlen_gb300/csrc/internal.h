@@ -81,10 +81,12 @@ struct DeviceOnce {
 // stream still runs (as soon as every block of that one has called grid_release or ended). Every such kernel
 // calls grid_wait, in all of its threads, before it reads or writes any memory but its own, and grid_release after
 // that: the wait makes the writes of the launch before visible to the grid that waits and to no other, so a kernel
-// cannot rely on what the launch before it has waited for. Both are nothing in an ordinary launch. Waiting here
-// is the hardware's, and ends when the launch before has ended (and so all launches before that, which it has
-// waited for); that may be another call's or another library's, and what is hidden is a kernel's own start. Pointers
-// of such kernels are not `__restrict__`: a load through those could be moved before the wait.
+// that has not waited cannot rely on what the launch before it has waited for. One that has may read what earlier
+// launches wrote (a join the list of two launches before): the launch before has ended, all of its blocks after waits
+// of their own. Both are nothing in an ordinary launch. Waiting here is the hardware's, and ends when the launch before
+// has ended (and so all launches before that, which it has waited for); that may be another call's or another
+// library's, and what is hidden is a kernel's own start. Pointers of such kernels are not `__restrict__`: a load
+// through those could be moved before the wait.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 

@@ -21,8 +21,11 @@ namespace {
 
 constexpr int kThreads = kSortThreads;
 // Three ways to make the list: up to 32 units by a warp, a unit per lane; up to kSmall (and where a prefix is apart) a unit
-// per thread; more sorted by the block. Each is a kernel of its own, with and without prefixes: what it takes is latency, fetching its code included (all in one,
-// a list of 1864 items took 2 us longer).
+// per thread; more sorted by the block. Each is a kernel of its own, with and without prefixes: what it takes is latency,
+// fetching its code included (all in one, a list of 1864 items took 2 us longer). With a prefix apart the second also
+// chooses the length of runs, which the third leaves at the plan's shortest: sorted in place of a unit per thread, 254
+// questions of 20 tokens behind two prefixes of 3000, 16 heads of 80 (256 units), take 236 us in a graph instead of 218;
+// 100 of 30 behind one, 151 instead of 121.
 enum { kByWarp, kByThread, kSorted };
 constexpr int kSmall = 256;
 
@@ -40,7 +43,7 @@ struct Sched {
     CrossSegs s;
     int window, sinks;
     Groups groups;
-    bool prefix, apart, own_few;
+    bool apart, own_few;
     int Hq, lg_pack, bn, run_tiles, num_sms;
     WsHeader *hdr;
     WinItem *items;
@@ -217,7 +220,9 @@ window_schedule_kernel(const Sched p)
         __syncthreads();
         if (apart) {
             // How long runs are best: an item takes a step for each two of its tiles, and about kItemSteps beside them. Of
-            // units alike (the groups alone) as many rounds as it takes, else an even share and one item more.
+            // units alike (the groups alone) as many rounds as it takes, else an even share and one item more. (32
+            // questions of 8 to 131 tokens behind two prefixes, 16 heads of 80: 105 us in a graph at 0.5 and 1 step an
+            // item, 91 to 92 at 1.5 to 8; 64 single tokens behind four prefixes 64 to 65 at all of them.)
             constexpr float kItemSteps = 2.5f;
             unsigned long long best = ~0ull;
             const int run = p.run_tiles + tid;
@@ -504,7 +509,11 @@ WinPlan win_plan(int64_t Tq, int B, int Hq, int Hk, int D, int max_q, int max_k,
     const int64_t own = std::min(Tq / tok + B, (int64_t)B * cdiv(max_q, tok)), grouped = Tq / tok + G;
     const bool prefix = G > 0 && Tp > 0;
     // Apart where the sequences' tiles would be much emptier than the groups': otherwise a pass over both saves the
-    // partial results and their join.
+    // partial results and their join. In a graph, apart and together, 16 heads of 80, 16 sequences behind 4000 shared
+    // keys: of 32 tokens (3.2 times the tiles) 37 and 58 us, of 43 (2.7) 48 and 58, of 55 (2.3) 58 and 58, of 64 (1.8) 60
+    // and 58, of 85 (1.5) 72 and 59. Where the lines cross moves with the prefix's share of the work: 64 sequences behind
+    // 1000 keys, 32 tokens (3.8) 62 and 70, 43 (2.9) 78 and 70, 55 (2.3) 89 and 71; 8 behind 9000, 55 (2.0) 58 and 60, 85
+    // (1.3) 75 and 60.
     p.apart = prefix && own > 2 * grouped;
     p.own_few = p.apart && window_takes_few(B, Hq, Hk, D, max_q, max_k, 0, 0);
     p.units = p.own_few ? G : p.apart ? G + B : B;
@@ -554,7 +563,10 @@ WinPlan win_plan(int64_t Tq, int B, int Hq, int Hk, int D, int max_q, int max_k,
     p.bytes = p.off_few;
     if (p.own_few) {
         p.few = window_few_plan(B, Hq, Hk, D, max_q, max_k, 0, 0);
-        if ((int64_t)B * Hk >= kDesignSms && max_k <= 2048) {   // one run each: enough blocks, and short ones
+        // One run each where that is enough blocks, and short ones. In a graph, one run and several, 8 key heads of 128: 64
+        // sequences of 700 keys 68 and 74 us, of 2048 115 and 121, of 5000 221 and 226; of lengths from 20 up to 2048 82 and 82,
+        // to 3000 103 and 101; 20 sequences up to 2000 53 and 53, up to 4000 76 and 68.
+        if ((int64_t)B * Hk >= kDesignSms && max_k <= 2048) {
             p.few.chunk = std::max(64, (max_k + 63) / 64 * 64);
             p.few.n_split = p.few.room = 1;
         }
@@ -571,7 +583,6 @@ cudaError_t launch_window_tiles(const WinArgs &a, const WinPlan &pl, int num_sms
     p.window = a.window;
     p.sinks = a.sinks;
     p.groups = a.groups;
-    p.prefix = a.prefix;
     p.apart = pl.apart;
     p.own_few = pl.own_few;
     p.Hq = a.f.Hq;
