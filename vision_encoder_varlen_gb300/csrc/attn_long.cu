@@ -75,9 +75,10 @@
 // yet adds nothing, and one that never sees a key is stored as 0 with lse -inf. At head size 128 the tiles inside have a
 // loop without the masks (8191 shared keys: 538 instead of 576 us); at 80 fetching two loops costs more. Bound, as
 // without a mask, by the exchange between softmax and tensor pipe, then by the edges: 256-row tiles compute 1.1 to 1.4
-// times the visible pairs, and an item costs 3.3 us beside its tiles. Measured: prompts of 1500 to 6007 tokens over up to
-// 8191 keys, window 2048, 32 heads over 8 of 128: 393 us (1.27 PFLOP/s of visible pairs); causal ones of 700 to 4095, 16
-// heads of 80: 133 us (0.79); six prompts of 300 to 2047 behind 8191 shared keys, 32 over 8 of 128: 540 us (1.58).
+// times the visible pairs, and an item costs 3.3 us beside its tiles. Measured, back to back in a graph and as single calls
+// on new inputs: prompts of 1500 to 6007 tokens over up to 8191 keys, window 2048, 32 heads over 8 of 128: 394 and 421 us
+// (1.27 and 1.19 PFLOP/s of visible pairs); causal ones of 700 to 4095, 16 heads of 80: 131 to 134 and 137 (0.8 and 0.77);
+// six prompts of 300 to 2047 behind 8191 shared keys, 32 over 8 of 128: 545 and 592 (1.56 and 1.44).
 #include <cudaTypedefs.h>
 #include <float.h>
 

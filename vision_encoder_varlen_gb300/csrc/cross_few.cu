@@ -29,7 +29,7 @@
 // loaded, and where there is more than one query each masks for itself what another one sees. HBM bound like the rest: 48
 // single tokens over padded caches of up to 16383 keys, window 4096, 32 heads over 8 of 128: 61 us with the join, 5.4 TB/s
 // of the visible keys (0.80 of a copy). A prefix takes the place of the first tokens where reading it for each sequence
-// is cheap: three single tokens behind 1601 shared keys 12 us in a graph, 20 with one pass for all of them, of which the
+// is cheap: three single tokens behind 1601 shared keys 12 us in a graph, 27 with one pass for all of them, of which the
 // launches are most.
 #include <type_traits>
 
