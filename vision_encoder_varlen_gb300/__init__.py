@@ -822,8 +822,8 @@ def window_attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: tor
                     dv: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                     status: torch.Tensor | None = None, stream=None):
     """Gradient of window_attn: from dout and the forward call's inputs and results returns (dq, dk, dv), dk and dv
-    summed over the query heads that share a key head. Keys that no query sees and queries that see no key get 0; rows
-    of no sequence are as in cross_attn_bwd."""
+    summed over the query heads that share a key head. Keys that no query sees and queries that see no key, or one,
+    get 0; rows of no sequence are as in cross_attn_bwd."""
     window, sinks = _window(window, sinks)
     return _attn_bwd("vit_window_attn_bwd", (window, sinks), dout, q, k, v, out, lse, cu_q, cu_k, max_q, max_k, scale,
                      k_len, dq, dk, dv, workspace, status, stream)

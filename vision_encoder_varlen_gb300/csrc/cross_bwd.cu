@@ -835,7 +835,10 @@ __device__ __forceinline__ void grad_pass(const std::conditional_t<WIN, WinGradM
                             return;
                         }
                     }
-                    const float f = which ? 1.f : p.scale;
+                    // a query at position 0 sees one key, whose weight is 1 whatever its score: no dq, and no dk of a key that
+                    // no other query sees
+                    const bool alone = DKV ? it.ln == 1 && it.lp == 0 : it.rp + (row >> p.lg_pack) == 0;
+                    const float f = which ? 1.f : alone ? 0.f : p.scale;
                     const bool whole = n > 0 && it.r0 + (DKV ? BM : BM >> p.lg_pack) <= it.r1;
                     unsigned char *x = base + (2 * xb + which) * C::X_TILE;
                     __nv_bfloat16 *dst = (which ? p.out2 + (int64_t)o_row * p.out2_stride
@@ -1456,6 +1459,7 @@ cudaError_t launch_d(const CrossGradArgs &a, const std::conditional_t<W, WinGrad
         dq.next = r.counts + 2;
         dkv.window = dq.window = window;
         dkv.sinks = dq.sinks = sinks;
+        if (window == 1 && sinks == 0) dkv.scale = dq.scale = 0.f;     // every query sees one key
     }
     dkv.first_block = 0;
     dq.first_block = dkv.n_blocks;
