@@ -616,7 +616,8 @@ size_t vit_window_attn_bwd_workspace_size(int64_t Tq, int64_t Tk, int Hq, int Hk
 /*
  * Gradient of vit_window_attn: arguments, roundings and errors as for vit_cross_attn_bwd. Keys that no
  * query sees, and queries that see no key or one (whose weight is 1 whatever it is), get 0; dk of a key
- * that only such a query sees is 0. sum_d do o is from the scores for rows that see 2 to 16 keys. Values of q, k, v and dout that are not finite may reach gradients of other rows of their
+ * that only such a query sees is 0. sum_d do o is from the scores for rows that see 2 to 16 keys.
+ * Values of q, k, v and dout that are not finite may reach gradients of other rows of their
  * sequence that are computed in one tile with those (128 rows).
  */
 vit_status_t vit_window_attn_bwd(const void *dout, const void *q, const void *k, const void *v, const void *out,
