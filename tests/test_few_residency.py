@@ -1,13 +1,16 @@
 """The kernel for few query rows in a language model's own attention: how many of its blocks an SM holds, from the
 assembler's own report on the CPU, and that the library's plan begins no second round of blocks that would be a small one."""
 import math
+import os
 import random
+import subprocess
 
 import pytest
 
 import vision_encoder_varlen_gb300 as vit
-from test_ptxas_resources import kernels
+from test_ptxas_resources import _ENTRY, _demangle
 from test_window_plans import plans
+from vision_encoder_varlen_gb300 import _build
 
 SMS, HEAD_DIMS = 152, (32, 64, 80, 96, 128)
 
@@ -26,14 +29,18 @@ def places(D, row_tiles):
     return by_smem(D) if row_tiles == 1 or D < 64 else 2 if D <= 80 else 1
 
 
-def test_places_that_registers_leave(kernels):
+def test_places_that_registers_leave(tmp_path):
+    r = subprocess.run([_build._nvcc(), *_build.compile_flags(ptxas_info=True), "-c",
+                        os.path.join(_build.CSRC, "cross_few.cu"), "-o", str(tmp_path / "o")], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    report = _ENTRY.findall(r.stderr)
     found = 0
-    for k in kernels:
-        name = k["name"].replace("(int)", "").replace("(bool)1", "true")
+    for name, (_, _, _, _, regs) in zip(_demangle([x[0] for x in report]), report):
+        name = name.replace("(int)", "").replace("(bool)1", "true")
         for D in HEAD_DIMS[1:]:
             for t in (1, 2):
                 if f"cross_few_kernel<{D}, {t}, true>" in name:
-                    assert min(by_smem(D), by_registers(k["regs"], t)) == places(D, t), (k["name"], k["regs"])
+                    assert min(by_smem(D), by_registers(int(regs), t)) == places(D, t), (name, regs)
                     found += 1
     assert found == 2 * len(HEAD_DIMS[1:])
 

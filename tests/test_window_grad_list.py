@@ -61,7 +61,7 @@ def check(p, ql, kl, Hq, Hk, D, window, sinks):
 def test_lists_stay_inside_the_workspace(plans):
     rng = random.Random(11)
     calls = []
-    for i in range(4000):
+    for i in range(2000):
         D, Hk = rng.choice([32, 64, 80, 96, 128]), rng.choice([1, 1, 2, 3, 8, 16])
         Hq = Hk * rng.choice([1, 2, 3, 4, 5, 8, 16])
         B = rng.choice([1, 1, 2, 3, 9, 40, 300])
@@ -77,4 +77,4 @@ def test_lists_stay_inside_the_workspace(plans):
         window = 0 if window >= mk else window                     # as the call does before it makes its plan
         lines.append(("grad", sum(ql), sum(kl), len(ql), Hq, Hk, D, mq, mk, window, sinks if window else 0))
     used = [check(p, *c[:5], x[9], x[10]) for p, c, x in zip(plans(lines), calls, lines)]
-    assert sum(u > 0 for u in used) > 100 and max(used) > 0.4      # cut loops are among them
+    assert sum(u > 0 for u in used) > 50 and max(used) > 0.4      # cut loops are among them
